@@ -66,7 +66,9 @@ typedef struct CUstream_st* zero_stream_t;
 #define ZERO_ETIMEOUT (-5) /* reserved; a device wait that gives up records 1 in the step
                               state's error word instead */
 
-typedef enum zero_dtype { ZERO_F16 = 1, ZERO_BF16 = 2 } zero_dtype_t;
+/* The flat entry points take ZERO_F16 and ZERO_BF16; the entry points over lists of tensors
+ * also ZERO_F32 (gradients, states) and ZERO_U8 (block-scaled 8-bit states). */
+typedef enum zero_dtype { ZERO_F16 = 1, ZERO_BF16 = 2, ZERO_F32 = 3, ZERO_U8 = 4 } zero_dtype_t;
 
 #define ZERO_MAX_RANKS (1u << 20)   /* zero_partition (ledger and layout) */
 #define ZERO_MAX_KERNEL_RANKS 64u   /* device entry points: replicas summed per element */
@@ -460,6 +462,114 @@ int zero_step_static_workspace(const zero_layout_t* layout, const zero_adamw_hpa
                                zero_dtype_t dtype, const void* const* replicas, float* g,
                                float* master, float* m, float* v, uint16_t* params,
                                zero_step_state_t* st, zero_stream_t stream);
+
+/* -------------------------------------------------------------------------------------
+ * Lists of tensors: the norm and the AdamW step on a model's tensors where they lie, with
+ * no flat copy, each with its own learning-rate scale and weight decay, and with optimizer
+ * states of 32 or of 8 bits.  [ZS]: the AdamW ledger and update; [MD] sec. 1: the global
+ * norm before clipping; [ZW] sec. 4(2): a rank's shard as pieces of tensors (the pieces
+ * zero_segment_map lists are such a list).
+ *
+ * One step, on one stream:
+ *   1. zero_tensors_grad_norm  over the list (scalars into the step state)
+ *   2. zero_tensors_adamw or zero_tensors_adamw8 over the same list
+ * The list is a HOST array that each call reads before it returns; its pointers are DEVICE
+ * pointers.  Every array is contiguous and holds `elems` elements at the natural alignment
+ * of its element type (ZERO_EALIGN otherwise); tensors all of whose arrays are 16-byte
+ * aligned move in 128-bit accesses.  A tensor may be empty (its pointers are then not
+ * looked at), and so may the list.  No two arrays may overlap.  One launch covers several
+ * hundred tensors; a longer list takes more than one.
+ *
+ * 8-bit states.  A tensor's elements are cut into blocks of 256 (the last may be shorter);
+ * m and v hold one code byte per element, exps two bytes per block (m's, then v's exponent
+ * b).  b = 0 stands for a block of zeros; else the block's largest magnitude lies at or
+ * below 1.875 * 2^(b-127), b in [27, 253].  A code is a small float scaled by 2^(b-127):
+ *   m   sign, 4 exponent bits E, 3 mantissa bits M:  (1 + M/8) * 2^(E-15), or M/8 * 2^-14
+ *       for E = 0
+ *   v   5 exponent bits E, 3 mantissa bits M:        (1 + M/8) * 2^(E-31), or M/8 * 2^-30
+ *       for E = 0
+ * Arrays of zeros are the states of a fresh optimizer.  zero_tensors_adamw8 rounds each
+ * new value up or down at random so that its mean is the value itself: with beta2 = 0.999
+ * a step moves v by about 0.1%, far less than the codes' spacing of 6-12%, and rounding to
+ * nearest would leave v where it was.  A v > 0 is never stored as 0 (the update would
+ * divide by eps alone).  Magnitudes above 1.875 * 2^126, and NaN, are stored as the
+ * largest code.  The random bits are a function of `seed`, of the step state's t and of the
+ * element's place in the list, so a step repeats bit for bit:
+ *   mix(x):  x ^= x>>16; x *= 0x6A09E667; x ^= x>>15; x *= 0xBB67AE85; x ^= x>>16   (mod 2^32)
+ *   K = mix(mix(lo32(seed) + t * 0x9E3779B9) ^ hi32(seed))
+ *   G = 32 * (blocks of the list before the element's) + (element's index in its block) / 8
+ *   s_0 = mix(K + G * 0x9E3779B9);  s_j = 1664525 * s_(j-1) + 1013904223;  q = index mod 8
+ *   m's 20 random bits: s_(q+1) >> 12;  v's: s_(q+9) >> 12
+ * ------------------------------------------------------------------------------------- */
+#define ZERO_STATE8_BLOCK 256u /* elements that share an exponent byte */
+
+typedef struct zero_tensor {
+    uint64_t elems;
+    const void* grad;        /* of grad_dtype */
+    float* master;           /* fp32 parameters, updated in place */
+    void* m;                 /* optimizer state of state_dtype, updated in place */
+    void* v;
+    uint8_t* exps;           /* ZERO_U8 states: 2 * ceil(elems/256) exponent bytes */
+    uint16_t* params;        /* 16-bit parameters out, or NULL (fp32 training: master is it) */
+    uint32_t grad_dtype;     /* ZERO_F16, ZERO_BF16 or ZERO_F32 */
+    uint32_t state_dtype;    /* ZERO_F32 or ZERO_U8 (a target of zero_tensors_state8_read may
+                                also be ZERO_BF16) */
+    uint32_t params_dtype;   /* ZERO_BF16, ZERO_F16, or 0: the hyperparameters' */
+    float lr_scale;          /* this tensor's learning rate is lr * lr_scale (>= 0) */
+    float weight_decay;      /* this tensor's decoupled decay, in place of the hyperparameters' */
+    uint32_t reserved;       /* 0 */
+} zero_tensor_t;             /* 80 bytes */
+
+/* Bytes of the workspace zero_tensors_grad_norm needs for a list of n_tensors. */
+size_t zero_tensors_workspace_bytes(uint64_t n_tensors);
+
+/* zero_step_state_init for a list of tensors (no layout, no partials).
+ *   n_ranks   the gradients are sums of this many copies (1: already averaged):
+ *             inv_scale = f32(1 / (n_ranks * L)) */
+int zero_tensors_state_init(uint32_t n_ranks, float loss_scale, uint32_t dynamic,
+                            uint32_t growth_interval, zero_step_state_t* st, zero_stream_t stream);
+
+/* zero_grad_norm over a list: with g = x * st->inv_scale for every gradient element x,
+ *   norm = sqrt(sum of g^2);  overflow when any g is not finite
+ * and everything zero_grad_norm writes: clip coefficient, skip decision, t, the scaler and
+ * the bias corrections.  Reads elems, grad and grad_dtype of each tensor.
+ *   workspace   DEVICE, zero_tensors_workspace_bytes(n_tensors), 16-byte aligned; needs no
+ *               initialisation
+ * The sums are formed in a fixed order: the same list gives the same bits. */
+int zero_tensors_grad_norm(const zero_tensor_t* tensors, uint64_t n_tensors,
+                           const zero_adamw_hparams_t* hp, double* workspace,
+                           zero_step_state_t* st, zero_stream_t stream);
+
+/* AdamW over a list with fp32 states, and the cast into the 16-bit parameters.  Does
+ * nothing (on the device) when st->skip.  For every element, in fp32:
+ *   gc = c * (x * st->inv_scale_used);  m = b1*m + (1-b1)*gc;  v = b2*v + (1-b2)*(gc*gc)
+ *   p  = p*decay - step*(m / (sqrt(v)/rbc2 + eps));  params = rounded to nearest even
+ * with step = st->step_size * lr_scale and decay = f32(1 - lr * lr_scale * weight_decay).
+ * A list with lr_scale 1 and the hyperparameters' weight decay gives zero_step's bits.
+ *   hp   must equal the hp given to zero_tensors_grad_norm for this step */
+int zero_tensors_adamw(const zero_tensor_t* tensors, uint64_t n_tensors,
+                       const zero_adamw_hparams_t* hp, const zero_step_state_t* st,
+                       zero_stream_t stream);
+
+/* The same with 8-bit states: m and v are decoded, updated in fp32, used in fp32 for the
+ * parameters (with sqrt(v) * (1/rbc2) in the denominator), and stored in 8 bits again.
+ * master and params stay as in zero_tensors_adamw.
+ *   seed   of the rounding; any value, the same for a whole run */
+int zero_tensors_adamw8(const zero_tensor_t* tensors, uint64_t n_tensors,
+                        const zero_adamw_hparams_t* hp, uint64_t seed,
+                        const zero_step_state_t* st, zero_stream_t stream);
+
+/* The 8-bit states' values: for every tensor k, `to[k].m` and `to[k].v` (fp32 or bf16; both
+ * hold the values exactly) from the codes of `from[k]`.  Reads elems, m, v, exps and
+ * state_dtype; to[k].elems must equal from[k].elems. */
+int zero_tensors_state8_read(const zero_tensor_t* from, const zero_tensor_t* to,
+                             uint64_t n_tensors, zero_stream_t stream);
+
+/* fp32 states into 8 bits, each to the nearest code (half away from zero): `to[k]`'s codes
+ * and exponents from `from[k].m` and `from[k].v`; v must not be negative.  Writing what
+ * zero_tensors_state8_read gave keeps every value. */
+int zero_tensors_state8_write(const zero_tensor_t* to, const zero_tensor_t* from,
+                              uint64_t n_tensors, zero_stream_t stream);
 
 /* Text for a status code. */
 const char* zero_strerror(int status);

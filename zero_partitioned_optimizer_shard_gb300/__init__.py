@@ -17,7 +17,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libzero_shard.so")
 
 ZERO_OK, ZERO_EINVAL, ZERO_EALIGN, ZERO_ENOMEM, ZERO_ECUDA, ZERO_ETIMEOUT = 0, -1, -2, -3, -4, -5
-ZERO_F16, ZERO_BF16 = 1, 2
+ZERO_F16, ZERO_BF16, ZERO_F32, ZERO_U8 = 1, 2, 3, 4
+ZERO_STATE8_BLOCK = 256
 ZERO_MAX_KERNEL_RANKS = 64
 ZERO_TILE_ELEMS = 8192
 
@@ -61,7 +62,17 @@ class StepState(C.Structure):
     ]
 
 
-assert C.sizeof(StepState) == 128
+class Tensor(C.Structure):
+    """One tensor of a list (zero_tensor_t)."""
+    _fields_ = [
+        ("elems", C.c_uint64), ("grad", C.c_void_p), ("master", C.c_void_p), ("m", C.c_void_p),
+        ("v", C.c_void_p), ("exps", C.c_void_p), ("params", C.c_void_p),
+        ("grad_dtype", C.c_uint32), ("state_dtype", C.c_uint32), ("params_dtype", C.c_uint32),
+        ("lr_scale", C.c_float), ("weight_decay", C.c_float), ("reserved", C.c_uint32),
+    ]
+
+
+assert C.sizeof(StepState) == 128 and C.sizeof(Tensor) == 80
 STATE_BYTES = C.sizeof(StepState)
 
 _P = C.c_void_p
@@ -104,6 +115,14 @@ def _lib() -> C.CDLL:
         L.zero_step_launches.argtypes = [C.POINTER(Layout), C.c_int]
         L.zero_step_static_workspace.argtypes = [C.POINTER(Layout), C.POINTER(HParams), C.c_int,
                                                  C.POINTER(_P), _P, _P, _P, _P, _P, _P, _P]
+        L.zero_tensors_workspace_bytes.argtypes = [C.c_uint64]
+        L.zero_tensors_workspace_bytes.restype = C.c_size_t
+        L.zero_tensors_state_init.argtypes = [C.c_uint32, C.c_float, C.c_uint32, C.c_uint32, _P, _P]
+        L.zero_tensors_grad_norm.argtypes = [_P, C.c_uint64, C.POINTER(HParams), _P, _P, _P]
+        L.zero_tensors_adamw.argtypes = [_P, C.c_uint64, C.POINTER(HParams), _P, _P]
+        L.zero_tensors_adamw8.argtypes = [_P, C.c_uint64, C.POINTER(HParams), C.c_uint64, _P, _P]
+        L.zero_tensors_state8_read.argtypes = [_P, _P, C.c_uint64, _P]
+        L.zero_tensors_state8_write.argtypes = L.zero_tensors_state8_read.argtypes
         L.zero_strerror.argtypes = [C.c_int]
         L.zero_strerror.restype = C.c_char_p
         L.zero_last_cuda_error.argtypes = []
@@ -112,7 +131,9 @@ def _lib() -> C.CDLL:
                      "zero_adamw_cast_gather", "zero_adamw_cast_gather_host_state", "zero_step",
                      "zero_step_host", "zero_last_cuda_error", "zero_reduce_shard_unscale_local",
                      "zero_adamw_cast_gather_local", "zero_step_launches",
-                     "zero_step_static_workspace"):
+                     "zero_step_static_workspace", "zero_tensors_state_init",
+                     "zero_tensors_grad_norm", "zero_tensors_adamw", "zero_tensors_adamw8",
+                     "zero_tensors_state8_read", "zero_tensors_state8_write"):
             getattr(L, name).restype = C.c_int
         _L = L
     return _L
@@ -293,6 +314,141 @@ def zero_step_static_workspace(layout: Layout, hp: HParams, dtype: int, replicas
         _ptr(v), _ptr(params), _ptr(st), _stream(stream)))
 
 
+# --------------------------------------------------------------------------------------
+# lists of tensors
+# --------------------------------------------------------------------------------------
+def _dtype_code(t) -> int:
+    import torch
+    return {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32,
+            torch.uint8: ZERO_U8}.get(t.dtype, 0)
+
+
+class TensorList:
+    """A list of tensors for the zero_tensors_* calls: the C array of zero_tensor_t, built
+    once and used for as long as the tensors stay where they are.
+
+    Every argument is a sequence with one entry per tensor, or None where no call on this
+    list needs it; all are contiguous CUDA tensors of one device.  grad: fp16, bf16 or fp32;
+    master: fp32; m, v: fp32, or uint8 codes with exps, uint8 of 2*ceil(elems/256) (bf16 m
+    and v only as a target of zero_tensors_state8_read); params: bf16 or fp16, or 16-bit
+    integers, whose type is then the hyperparameters'.  lr_scale, weight_decay: one number,
+    or one per tensor.  The list keeps its tensors alive; set_grad() takes gradients that
+    have moved."""
+
+    _TYPES = {"grad": (ZERO_F16, ZERO_BF16, ZERO_F32), "master": (ZERO_F32,), "exps": (ZERO_U8,),
+              "m": (ZERO_F32, ZERO_BF16, ZERO_U8), "v": (ZERO_F32, ZERO_BF16, ZERO_U8)}
+
+    def __init__(self, grad=None, master=None, m=None, v=None, exps=None, params=None, lr_scale=1.0,
+                 weight_decay=0.0):
+        arrays = {"master": master, "m": m, "v": v, "grad": grad, "params": params, "exps": exps}
+        self.tensors = {k: list(x) for k, x in arrays.items() if x is not None}
+        if not self.tensors or list(self.tensors) == ["exps"]:
+            raise ValueError("a list of tensors needs at least one of grad, master, m, v, params")
+        first = next(iter(self.tensors.values()))
+        self.device = first[0].device if first else None
+        self.elems = [t.numel() for t in first]
+        self.array = (Tensor * max(len(first), 1))()
+        for k, x in self.tensors.items():
+            self._check(k, x)
+        if ("m" in self.tensors) != ("v" in self.tensors):
+            raise ValueError("m and v come together")
+        scales, decays = self._numbers(lr_scale), self._numbers(weight_decay)
+        for i, a in enumerate(self.array[:len(first)]):
+            a.elems, a.lr_scale, a.weight_decay = self.elems[i], scales[i], decays[i]
+            for k, x in self.tensors.items():
+                setattr(a, k, x[i].data_ptr())
+            if "grad" in self.tensors:
+                a.grad_dtype = _dtype_code(self.tensors["grad"][i])
+            if "m" in self.tensors:
+                a.state_dtype = _dtype_code(self.tensors["m"][i])
+                if a.state_dtype != _dtype_code(self.tensors["v"][i]):
+                    raise ValueError(f"m[{i}] and v[{i}] differ in type")
+            if "params" in self.tensors:
+                a.params_dtype = _dtype_code(self.tensors["params"][i])
+
+    def __len__(self) -> int:
+        return len(self.elems)
+
+    def _numbers(self, x) -> list:
+        x = list(x) if hasattr(x, "__len__") else [x] * len(self)
+        if len(x) != len(self):
+            raise ValueError("lr_scale and weight_decay: one number, or one per tensor")
+        return x
+
+    def _check(self, name: str, xs: list) -> None:
+        if len(xs) != len(self):
+            raise ValueError(f"{name} has {len(xs)} tensors, the list {len(self)}")
+        for i, (t, n) in enumerate(zip(xs, self.elems)):
+            code = _dtype_code(t)
+            want = 2 * -(-n // ZERO_STATE8_BLOCK) if name == "exps" else n
+            if t.numel() != want:
+                raise ValueError(f"{name}[{i}] has {t.numel()} elements, not {want}")
+            if not t.is_contiguous() or not t.is_cuda or t.device != self.device:
+                raise ValueError(f"{name}[{i}] is not a contiguous CUDA tensor of {self.device}")
+            if name == "params":
+                ok = code in (ZERO_F16, ZERO_BF16) or (code == 0 and str(t.dtype) in
+                                                       ("torch.int16", "torch.uint16"))
+            else:
+                ok = code in self._TYPES[name]
+            if not ok:
+                raise ValueError(f"{name}[{i}] has type {t.dtype}")
+
+    def set_grad(self, grad: Sequence) -> None:
+        """The same tensors' gradients at new addresses."""
+        grad = list(grad)
+        self._check("grad", grad)
+        self.tensors["grad"] = grad
+        for i, g in enumerate(grad):
+            self.array[i].grad, self.array[i].grad_dtype = g.data_ptr(), _dtype_code(g)
+
+
+def _same_length(a: TensorList, b: TensorList) -> int:
+    if len(a) != len(b):
+        raise ValueError(f"lists of {len(a)} and {len(b)} tensors")
+    return len(a)
+
+
+def zero_tensors_workspace_bytes(n_tensors: int) -> int:
+    return _lib().zero_tensors_workspace_bytes(n_tensors)
+
+
+def zero_tensors_state_init(n_ranks: int, loss_scale: float, dynamic: bool, growth_interval: int, st,
+                            stream=None) -> None:
+    """n_ranks: how many copies the gradients are sums of (1: already averaged)."""
+    _check("zero_tensors_state_init", _lib().zero_tensors_state_init(
+        n_ranks, loss_scale, int(bool(dynamic)), growth_interval, _ptr(st), _stream(stream)))
+
+
+def zero_tensors_grad_norm(tensors: TensorList, hp: HParams, workspace, st, stream=None) -> None:
+    """Norm, clip coefficient, skip decision and the step's scalars over the list's gradients."""
+    _check("zero_tensors_grad_norm", _lib().zero_tensors_grad_norm(
+        tensors.array, len(tensors), C.byref(hp), _ptr(workspace), _ptr(st), _stream(stream)))
+
+
+def zero_tensors_adamw(tensors: TensorList, hp: HParams, st, stream=None) -> None:
+    """AdamW over the list, fp32 states."""
+    _check("zero_tensors_adamw", _lib().zero_tensors_adamw(
+        tensors.array, len(tensors), C.byref(hp), _ptr(st), _stream(stream)))
+
+
+def zero_tensors_adamw8(tensors: TensorList, hp: HParams, seed: int, st, stream=None) -> None:
+    """AdamW over the list, 8-bit states; seed: of their stochastic rounding."""
+    _check("zero_tensors_adamw8", _lib().zero_tensors_adamw8(
+        tensors.array, len(tensors), C.byref(hp), seed, _ptr(st), _stream(stream)))
+
+
+def zero_tensors_state8_read(source: TensorList, to: TensorList, stream=None) -> None:
+    """The values of source's 8-bit states into to's fp32 or bf16 m and v."""
+    _check("zero_tensors_state8_read", _lib().zero_tensors_state8_read(
+        source.array, to.array, _same_length(source, to), _stream(stream)))
+
+
+def zero_tensors_state8_write(to: TensorList, source: TensorList, stream=None) -> None:
+    """source's fp32 m and v into to's 8-bit states, to the nearest code."""
+    _check("zero_tensors_state8_write", _lib().zero_tensors_state8_write(
+        to.array, source.array, _same_length(to, source), _stream(stream)))
+
+
 __all__ = [
     "Layout", "HParams", "StepState", "ZeroError", "hparams", "lib", "STATE_BYTES",
     "ZERO_F16", "ZERO_BF16", "Segment", "zero_partition", "zero_segment_map", "zero_workspace_bytes", "zero_step_state_init",
@@ -300,4 +456,7 @@ __all__ = [
     "zero_grad_norm", "zero_adamw_cast_gather", "zero_adamw_cast_gather_host_state", "zero_step",
     "zero_step_host", "zero_step_launches", "zero_reduce_shard_unscale_local",
     "zero_adamw_cast_gather_local", "zero_step_static_workspace",
+    "ZERO_F32", "ZERO_U8", "ZERO_STATE8_BLOCK", "Tensor", "TensorList", "zero_tensors_workspace_bytes",
+    "zero_tensors_state_init", "zero_tensors_grad_norm", "zero_tensors_adamw", "zero_tensors_adamw8",
+    "zero_tensors_state8_read", "zero_tensors_state8_write",
 ]

@@ -33,6 +33,19 @@ bool layout_ok(const zero_layout_t* L)
     return L->n_buckets == (L->psi_padded + W - 1) / W;
 }
 
+bool hparams_ok(const zero_adamw_hparams_t* hp)
+{
+    if (!hp)
+        return false;
+    const float vals[6] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay, hp->max_grad_norm};
+    for (float x : vals)
+        if (!(x == x) || x > 3.0e38f || x < -3.0e38f)
+            return false;
+    return hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f &&
+           hp->eps > 0.0f && hp->lr >= 0.0f &&
+           (hp->params_dtype == 0 || hp->params_dtype == ZERO_BF16 || hp->params_dtype == ZERO_F16);
+}
+
 namespace {
 thread_local int g_last_cuda_error = 0;
 
@@ -49,19 +62,6 @@ bool aligned16(const void* p) { return p && ((uintptr_t)p & 15u) == 0; }
 bool kernel_layout_ok(const zero_layout_t* L)
 {
     return layout_ok(L) && L->n_ranks <= ZERO_MAX_KERNEL_RANKS;
-}
-
-bool hparams_ok(const zero_adamw_hparams_t* hp)
-{
-    if (!hp)
-        return false;
-    const float vals[6] = {hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay, hp->max_grad_norm};
-    for (float x : vals)
-        if (!(x == x) || x > 3.0e38f || x < -3.0e38f)
-            return false;
-    return hp->beta1 >= 0.0f && hp->beta1 < 1.0f && hp->beta2 >= 0.0f && hp->beta2 < 1.0f &&
-           hp->eps > 0.0f && hp->lr >= 0.0f &&
-           (hp->params_dtype == 0 || hp->params_dtype == ZERO_BF16 || hp->params_dtype == ZERO_F16);
 }
 
 int reduce_window(const zero_layout_t* L, zero_dtype_t dtype, const void* const* replicas,

@@ -187,6 +187,8 @@ int sm_count();
  * or faster (2^28: 2.4%, the GPT-2-1.5B buffer: 4%); at 2^22-2^25 it cost 1-3%. */
 bool adamw_evict_first(uint64_t n, uint64_t bytes_per_elem);
 
+bool hparams_ok(const zero_adamw_hparams_t* hp);  // finite and in the documented ranges
+
 /* Make zero_last_cuda_error() report `e` on this thread. */
 void record_cuda_error(int e);
 
