@@ -349,6 +349,8 @@ class TensorList:
         self.elems = [t.numel() for t in first]
         self.array = (Tensor * max(len(first), 1))()
         for k, x in self.tensors.items():
+            self._check_length(k, x)
+        for k, x in self.tensors.items():
             self._check(k, x)
         if ("m" in self.tensors) != ("v" in self.tensors):
             raise ValueError("m and v come together")
@@ -375,9 +377,11 @@ class TensorList:
             raise ValueError("lr_scale and weight_decay: one number, or one per tensor")
         return x
 
-    def _check(self, name: str, xs: list) -> None:
+    def _check_length(self, name: str, xs: list) -> None:
         if len(xs) != len(self):
             raise ValueError(f"{name} has {len(xs)} tensors, the list {len(self)}")
+
+    def _check(self, name: str, xs: list) -> None:
         for i, (t, n) in enumerate(zip(xs, self.elems)):
             code = _dtype_code(t)
             want = 2 * -(-n // ZERO_STATE8_BLOCK) if name == "exps" else n
@@ -396,6 +400,7 @@ class TensorList:
     def set_grad(self, grad: Sequence) -> None:
         """The same tensors' gradients at new addresses."""
         grad = list(grad)
+        self._check_length("grad", grad)
         self._check("grad", grad)
         self.tensors["grad"] = grad
         for i, g in enumerate(grad):
