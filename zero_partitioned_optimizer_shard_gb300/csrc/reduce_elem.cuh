@@ -90,6 +90,13 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b)
     return d;
 }
 
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 /* s[e] += x[e] for the 8 values of one 128-bit load of a copy, in fp32 pairs. */
 template <zero_dtype_t DT>
 __device__ __forceinline__ void add8(float (&s)[8], const uint4& v)

@@ -25,14 +25,14 @@ namespace zero {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 8;                              // elements per thread and chunk
-constexpr uint32_t kTensorChunk = kThreads * kPer;   // 2048
-constexpr uint32_t kBlk = ZERO_STATE8_BLOCK;
-static_assert(kBlk == 32 * kPer, "a warp holds one block of the 8-bit states");
+constexpr int kWarps = kThreads / 32;
+constexpr int kPer = 8;                              // elements per lane and unit
+constexpr uint32_t kUnit = ZERO_STATE8_BLOCK;        // elements a warp takes at a time
+static_assert(kUnit == 32 * kPer, "a warp holds one block of the 8-bit states");
 
 constexpr uint32_t kGradMask = 3;    // the gradient's zero_dtype_t
 constexpr uint32_t kOutF16 = 4;      // 16-bit parameters are fp16
-constexpr uint32_t kAligned = 8;     // every array allows 128-bit accesses
+constexpr uint32_t kVector = 8;      // every array allows 128-bit accesses (past `head` elements)
 constexpr uint32_t kValueBF16 = 16;  // values read out as bf16
 
 /* One tensor of a launch.  The codec keeps the 32-bit arrays in x and y. */
@@ -52,46 +52,68 @@ struct Ref {
     uint64_t elems;
     float lr_scale, decay;
     uint32_t flags;
-    uint32_t group0;  // groups of 8 elements of the list before this tensor (mod 2^32)
+    union {
+        uint32_t group0;  // 8-bit states: groups of 8 elements of the list before this tensor
+        uint32_t head;    // 32-bit states: elements before the arrays' first 16-byte boundary
+    };
 };
 
-/* Tensors per launch: the parameters may be 32,764 bytes. */
-constexpr int kCap = 384;
+/* A launch's part of the list.  Kernel parameters may be 32,764 bytes; short lists take the
+ * small form, whose launch costs the host less (measured: 16 tensors, 8.4 us a call with
+ * the large form, see kSmall's callers). */
+constexpr int kSmall = 32, kLarge = 424;
 
+template <int CAP>
 struct List {
-    uint32_t n, n_chunks;
-    uint32_t begin[kCap + 1];
-    Ref t[kCap];
+    uint32_t n, n_units;
+    alignas(16) uint32_t end[CAP];  // units up to and including each tensor's, then ~0
+    Ref t[CAP];
 };
 
-struct NormArgs {
-    zero_step_state_t* st;
-    double* slots;              // one partial sum per block
-    zero_adamw_hparams_t hp;
-    uint32_t slot0, last;       // this launch's first slot; 1 in the list's last launch
-    List l;
-};
-
-struct TensorsArgs {
+template <int CAP>
+struct AdamwList {
     const zero_step_state_t* st;
     uint64_t seed;
     float beta1, beta2, eps;
-    List l;
+    List<CAP> l;
 };
-static_assert(sizeof(NormArgs) <= 32764 && sizeof(TensorsArgs) <= 32764, "kernel parameters");
+static_assert(sizeof(AdamwList<kLarge>) <= 32764, "kernel parameters");
 
-/* The tensor of chunk c: the last k with begin[k] <= c (empty tensors have no chunk). */
-__device__ __forceinline__ uint32_t tensor_of(const List& l, uint32_t c)
+/* The tensor of unit u, by the whole warp: one count of the ends at or below u, its loads
+ * all in flight at once.  They go through global addressing of the parameters: a binary
+ * search in constant memory misses its cache once per step on a launch's first unit. */
+template <int CAP>
+__device__ __forceinline__ uint32_t find_unit(const List<CAP>& l, uint32_t u)
 {
-    uint32_t lo = 0, hi = l.n;
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (l.begin[mid] <= c)
-            lo = mid;
-        else
-            hi = mid;
+    const uint4* end = reinterpret_cast<const uint4*>(l.end);
+    asm volatile("" : "+l"(end));
+    const uint32_t lane = threadIdx.x & 31, n = l.n;
+    uint32_t below = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < (uint32_t)CAP; j += 128) {
+        if (j + lane * 4 < n) {
+            const uint4 e = end[j / 4 + lane];
+            below += (e.x <= u) + (e.y <= u) + (e.z <= u) + (e.w <= u);
+        }
     }
-    return lo;
+    return __reduce_add_sync(0xffffffffu, below);
+}
+
+/* Where a warp's unit lies: its tensor and the unit's number in it. */
+struct Place {
+    uint32_t k, begin, end;  // the tensor, and the units [begin, end) it holds
+    uint32_t unit;           // the unit's number in the tensor
+};
+
+template <int CAP>
+__device__ __forceinline__ void locate(const List<CAP>& l, uint32_t u, Place& p)
+{
+    if (u < p.begin || u >= p.end) {
+        p.k = find_unit(l, u);
+        p.begin = p.k ? l.end[p.k - 1] : 0;
+        p.end = l.end[p.k];
+    }
+    p.unit = u - p.begin;
 }
 
 __device__ __forceinline__ float one_grad(const void* g, uint64_t i, uint32_t dtype)
@@ -123,19 +145,6 @@ __device__ __forceinline__ void widen8(const uint4& w, float (&x)[8])
     x[4] = lo16<DT>(w.z), x[5] = hi16<DT>(w.z), x[6] = lo16<DT>(w.w), x[7] = hi16<DT>(w.w);
 }
 
-__device__ __forceinline__ void load_grad8(const void* g, uint64_t i, uint32_t dtype, float (&x)[8])
-{
-    if (dtype == ZERO_F32) {
-        load8(static_cast<const float*>(g) + i, x);
-        return;
-    }
-    const uint4 w = ld_stream_v4(static_cast<const uint16_t*>(g) + i);
-    if (dtype == ZERO_F16)
-        widen8<ZERO_F16>(w, x);
-    else
-        widen8<ZERO_BF16>(w, x);
-}
-
 __device__ __forceinline__ void store_params8(uint16_t* p, uint32_t f16, const float (&x)[8])
 {
     uint4 o;
@@ -148,7 +157,8 @@ __device__ __forceinline__ void store_params8(uint16_t* p, uint32_t f16, const f
     __stcs(reinterpret_cast<uint4*>(p), o);
 }
 
-__device__ __forceinline__ Scalars step_scalars(const TensorsArgs& a)
+template <int CAP>
+__device__ __forceinline__ Scalars step_scalars(const AdamwList<CAP>& a)
 {
     Scalars s;
     s.c = a.st->clip_coef;
@@ -167,41 +177,157 @@ __device__ __forceinline__ Scalars step_scalars(const TensorsArgs& a)
 /* gradient norm                                                                          */
 /* ------------------------------------------------------------------------------------ */
 
-constexpr int kNormGroups = 4;                               // groups of 8 per thread in flight
-constexpr uint32_t kNormChunk = kTensorChunk * kNormGroups;  // 8192 elements
-constexpr uint32_t kNormMaxBlocks = 2048;                    // slots per launch
+constexpr int kNormLoads = 8;                // 128-bit loads in flight per thread
+constexpr uint32_t kNormPass = kThreads * kNormLoads;
+constexpr uint32_t kNormMaxBlocks = 2048;    // slots per launch
+constexpr int kNormBlocksPerSm = 4;
 
-/* A thread's sum of squares: fp32 sums of 8 squares, joined by error-free additions
- * (hi + lo), so that only a group's own 8 roundings remain; groups whose sum leaves fp32's
- * safe range (below 2^-80 or above 2^120: an infinity, a NaN, or a square that would
- * overflow or vanish) are summed in fp64 instead. */
+/* A gradient as 16-byte granules, cut at the addresses' multiples of 16 whatever the
+ * tensor's own alignment: the first and the last may be partial. */
+struct NormRef {
+    const char* base;      // the first granule's address
+    uint64_t end;          // granules of the launch up to and including this tensor's
+    uint64_t elems;
+    uint32_t dtype;
+    uint32_t skip;         // elements of the first granule before the tensor
+};
+
+constexpr int kNormCap = 1000;
+
+/* What the step's scalars are once the norm is known, formed ahead of it; in the workspace
+ * after the last launch's sums. */
+struct NormReady {
+    ScalerCand cand;
+    float step_size, rbc2;
+};
+
+struct NormArgs {
+    zero_step_state_t* st;
+    double* slots;              // one partial sum per block, then the step's scalar candidates
+    zero_adamw_hparams_t hp;
+    uint32_t slot0, last;       // this launch's first slot; 1 in the list's last launch
+    uint32_t n;
+    uint64_t quota;             // granules per block
+    NormRef t[kNormCap];
+};
+static_assert(sizeof(NormReady) <= 64, "the workspace's tail");
+static_assert(sizeof(NormArgs) <= 32764, "kernel parameters");
+
+/* A thread's sum of squares: fp32 sums of a granule's 8 (or 4) squares, joined by
+ * error-free additions (hi + lo), so that only a granule's own roundings remain (at most
+ * 6); granules whose sum leaves fp32's safe range (below 2^-80 or above 2^120: an
+ * infinity, a NaN, or a square that would overflow or vanish) are summed in fp64. */
 struct Squares {
     float hi = 0.0f, lo = 0.0f;
     double wide = 0.0;
     bool bad = false;
 
-    __device__ __forceinline__ void add(const float (&x)[8], float inv)
+    __device__ __forceinline__ void add(float s)
     {
-        float s0 = __fmul_rn(x[0], x[0]), s1 = __fmul_rn(x[1], x[1]);
-#pragma unroll
-        for (int e = 2; e < 8; e += 2) {
-            s0 = __fmaf_rn(x[e], x[e], s0);
-            s1 = __fmaf_rn(x[e + 1], x[e + 1], s1);
-        }
-        const float s = __fadd_rn(s0, s1);
-        if (s < 0x1p120f && s > 0x1p-80f && inv < 0x1p60f) {
-            const float t = __fadd_rn(hi, s);
-            const float bb = __fsub_rn(t, hi);
-            lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, bb)), __fsub_rn(s, bb)));
-            hi = t;
+        const float t = __fadd_rn(hi, s);
+        const float bb = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, bb)), __fsub_rn(s, bb)));
+        hi = t;
+    }
+
+    /* floor: 2^-80, or infinity where 1/(N*L) is so large that a finite gradient could
+     * unscale to infinity (then every granule is looked at element by element) */
+    template <uint32_t DT>
+    __device__ __forceinline__ void granule(const uint4& w, float inv, float floor)
+    {
+        if (DT == ZERO_F32) {
+            const float x0 = __uint_as_float(w.x), x1 = __uint_as_float(w.y);
+            const float x2 = __uint_as_float(w.z), x3 = __uint_as_float(w.w);
+            const float s = __fadd_rn(__fmaf_rn(x0, x0, __fmul_rn(x1, x1)),
+                                      __fmaf_rn(x2, x2, __fmul_rn(x3, x3)));
+            if (s < 0x1p120f && s > floor) {
+                add(s);
+            } else if (((w.x | w.y | w.z | w.w) & 0x7fffffffu) != 0) {
+                wide += sumsq_wide(x0, x1, x2, x3, 0.f, 0.f, 0.f, 0.f, 0xfu);
+                bad |= not_finite(__fmul_rn(x0, inv)) || not_finite(__fmul_rn(x1, inv)) ||
+                       not_finite(__fmul_rn(x2, inv)) || not_finite(__fmul_rn(x3, inv));
+            }
         } else {
-            wide += sumsq_wide(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], 0xffu);
+            constexpr zero_dtype_t D = DT == ZERO_F16 ? ZERO_F16 : ZERO_BF16;
+            float x[8];
+            widen8<D>(w, x);
+            const uint64_t a = f2(x[0], x[1]), b = f2(x[2], x[3]), c = f2(x[4], x[5]), d = f2(x[6], x[7]);
+            const uint64_t s2 = f2_add(f2_fma(a, a, f2_mul(b, b)), f2_fma(c, c, f2_mul(d, d)));
+            float s0, s1;
+            f2_split(s2, s0, s1);
+            const float s = __fadd_rn(s0, s1);
+            if (s < 0x1p120f && s > floor) {
+                add(s);
+            } else if (((w.x | w.y | w.z | w.w) & 0x7fff7fffu) != 0) {
+                wide += sumsq_wide(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], 0xffu);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                bad |= not_finite(__fmul_rn(x[e], inv));
+                for (int e = 0; e < 8; ++e)
+                    bad |= not_finite(__fmul_rn(x[e], inv));
+            }
         }
     }
 };
+
+/* A partial granule, element by element; what lies outside the tensor reads as 0. */
+__device__ __forceinline__ uint4 partial_granule(const NormRef& t, uint64_t j)
+{
+    uint32_t w[4] = {0, 0, 0, 0};
+    const uint64_t past = t.skip + t.elems;  // elements from the first granule's start to the end
+    if (t.dtype == ZERO_F32) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t i = j * 4 + e;
+            if (i >= t.skip && i < past)
+                w[e] = *reinterpret_cast<const uint32_t*>(t.base + i * 4);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t i = j * 8 + e;
+            if (i >= t.skip && i < past)
+                w[e >> 1] |= (uint32_t)ld_stream_u16(t.base + i * 2) << (16 * (e & 1));
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+/* Granule j of tensor t, whole or partial. */
+__device__ __forceinline__ uint4 any_granule(const NormRef& t, uint64_t j)
+{
+    const uint64_t n = t.dtype == ZERO_F32 ? 4 : 8;
+    if (j * n >= t.skip && (j + 1) * n <= t.skip + t.elems)
+        return ld_stream_v4(t.base + j * 16);
+    return partial_granule(t, j);
+}
+
+/* Whole passes, none of their granules partial, of one tensor. */
+template <uint32_t DT>
+__device__ __forceinline__ void norm_passes(const char* p, uint64_t passes, float inv, float floor, Squares& acc)
+{
+    p += threadIdx.x * 16;
+    for (; passes; --passes, p += kNormPass * 16) {
+        uint4 w[kNormLoads];
+#pragma unroll
+        for (int q = 0; q < kNormLoads; ++q)
+            w[q] = ld_stream_v4(p + q * kThreads * 16);
+#pragma unroll
+        for (int q = 0; q < kNormLoads; ++q)
+            acc.granule<DT>(w[q], inv, floor);
+    }
+}
+
+/* The first tensor of t[k .. upper] whose end lies past granule g. */
+__device__ __forceinline__ uint32_t norm_find(const NormArgs& a, uint64_t g, uint32_t k, uint32_t upper)
+{
+    while (k < upper) {
+        const uint32_t mid = (k + upper) / 2;
+        if (a.t[mid].end > g)
+            upper = mid;
+        else
+            k = mid + 1;
+    }
+    return k;
+}
 
 /* Adds v over the block: a fixed shuffle tree per warp, the warps in order.  Valid in
  * thread 0. */
@@ -220,47 +346,85 @@ __device__ __forceinline__ double block_sum(double v, double* warp_sum)
     return t;
 }
 
-/* Sum of squares over the list's gradients; in the last launch the block that finishes
+/* Sum of squares over the list's gradients: block b takes granules [b*quota, (b+1)*quota)
+ * of the launch, whatever tensors they lie in.  In the last launch the block that finishes
  * last adds the blocks' partial sums in order and finalises the step as zero_grad_norm. */
-__global__ void __launch_bounds__(kThreads) k_tensors_norm(const __grid_constant__ NormArgs a)
+__global__ void __launch_bounds__(kThreads, kNormBlocksPerSm) k_tensors_norm(const __grid_constant__ NormArgs a)
 {
     __shared__ double warp_sum[kThreads / 32];
     __shared__ int is_last;
     grid_dependency_wait();
     zero_step_state_t* st = a.st;
     const float inv = st->inv_scale;
+    const float floor = inv < 0x1p60f ? 0x1p-80f : __int_as_float(0x7f800000);
     Squares acc;
-    for (uint32_t c = blockIdx.x; c < a.l.n_chunks; c += gridDim.x) {
-        const uint32_t k = tensor_of(a.l, c);
-        const Ref& t = a.l.t[k];
-        const uint32_t dtype = t.flags & kGradMask;
-        const uint64_t off = (uint64_t)(c - a.l.begin[k]) * kNormChunk;
-        if ((t.flags & kAligned) && off + kNormChunk <= t.elems) {
-            float x[kNormGroups][8];
+    const uint32_t n_sum = a.last ? gridDim.x - 1 : gridDim.x;  // the last launch has one block more
+    NormReady* ready = reinterpret_cast<NormReady*>(a.slots + a.slot0 + n_sum);
+    uint64_t lo = blockIdx.x * a.quota;
+    const uint64_t total = a.n ? a.t[a.n - 1].end : 0, hi = lo + a.quota < total ? lo + a.quota : total;
+    uint32_t k = lo < hi ? norm_find(a, lo, 0, a.n - 1) : 0;
+    while (lo < hi) {
+        const NormRef& t = a.t[k];
+        const uint64_t first = k ? a.t[k - 1].end : 0;
+        // whole passes inside this tensor, past its first granule and short of its last
+        const uint64_t inner = (t.end - 1 < hi ? t.end - 1 : hi), from = lo - first;
+        if ((from || !t.skip) && lo + kNormPass <= inner) {
+            const uint64_t passes = (inner - lo) / kNormPass;
+            const char* p = t.base + from * 16;
+            if (t.dtype == ZERO_BF16)
+                norm_passes<ZERO_BF16>(p, passes, inv, floor, acc);
+            else if (t.dtype == ZERO_F16)
+                norm_passes<ZERO_F16>(p, passes, inv, floor, acc);
+            else
+                norm_passes<ZERO_F32>(p, passes, inv, floor, acc);
+            lo += passes * kNormPass;
+            continue;
+        }
+        // one pass over what follows, whichever tensors it meets: all its loads are in
+        // flight at once, however short the tensors are
+        const uint64_t stop = lo + kNormPass < hi ? lo + kNormPass : hi;
+        const uint32_t last = norm_find(a, stop - 1, k, k + kNormPass < a.n ? k + kNormPass : a.n - 1);
+        uint4 w[kNormLoads];
+        uint32_t type[kNormLoads];
 #pragma unroll
-            for (int q = 0; q < kNormGroups; ++q)
-                load_grad8(t.grad, off + q * kTensorChunk + threadIdx.x * kPer, dtype, x[q]);
-#pragma unroll
-            for (int q = 0; q < kNormGroups; ++q)
-                acc.add(x[q], inv);
-        } else {
-#pragma unroll 1
-            for (int q = 0; q < kNormGroups; ++q) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint64_t i = off + (q * 8 + e) * kThreads + threadIdx.x;
-                    x[e] = i < t.elems ? one_grad(t.grad, i, dtype) : 0.0f;
-                }
-                acc.add(x, inv);
+        for (int q = 0; q < kNormLoads; ++q) {
+            const uint64_t g = lo + q * kThreads + threadIdx.x;
+            w[q] = make_uint4(0, 0, 0, 0);
+            type[q] = 0;
+            if (g < stop) {
+                const uint32_t i = norm_find(a, g, k, last);
+                w[q] = any_granule(a.t[i], g - (i ? a.t[i - 1].end : 0));
+                type[q] = a.t[i].dtype;
             }
         }
+#pragma unroll
+        for (int q = 0; q < kNormLoads; ++q) {
+            if (type[q] == ZERO_BF16)
+                acc.granule<ZERO_BF16>(w[q], inv, floor);
+            else if (type[q] == ZERO_F16)
+                acc.granule<ZERO_F16>(w[q], inv, floor);
+            else if (type[q] == ZERO_F32)
+                acc.granule<ZERO_F32>(w[q], inv, floor);
+        }
+        lo = stop;
+        k = lo < hi ? norm_find(a, lo, last, last + 1 < a.n ? last + 1 : last) : last;
     }
     if (__any_sync(0xffffffffu, acc.bad) && (threadIdx.x & 31) == 0)
         atomicOr(&st->overflow, 1u);
-    const double part = block_sum((double)acc.hi + (double)acc.lo + acc.wide, warp_sum);
-    if (threadIdx.x == 0)
-        a.slots[a.slot0 + blockIdx.x] = part;
+    if (a.last && blockIdx.x == n_sum) {
+        // what does not need the norm, beside the sums (the fp64 powers of beta are a long
+        // chain): for either outcome of the overflow check, chosen once it is known
+        if (threadIdx.x == 0)
+            ready->cand = scaler_candidates(*st, a.hp, st->n_ranks);
+        if (threadIdx.x == 32)
+            ready->step_size = bias_step_size(a.hp, st->t + 1);
+        if (threadIdx.x == 64)
+            ready->rbc2 = bias_rbc2(a.hp, st->t + 1);
+    } else {
+        const double part = block_sum((double)acc.hi + (double)acc.lo + acc.wide, warp_sum);
+        if (threadIdx.x == 0)
+            a.slots[a.slot0 + blockIdx.x] = part;
+    }
     if (!a.last)
         return;
     // arrival, as in the norm over the flat buffer: the block's writes are ordered before
@@ -275,24 +439,27 @@ __global__ void __launch_bounds__(kThreads) k_tensors_norm(const __grid_constant
     __syncthreads();
     if (!is_last)
         return;
-    const uint32_t n_slots = a.slot0 + gridDim.x;
     double v = 0.0;
-    for (uint32_t i = threadIdx.x; i < n_slots; i += kThreads)
+    for (uint32_t i = threadIdx.x; i < a.slot0 + n_sum; i += kThreads)
         v += __ldcg(a.slots + i);
-    const double total = block_sum(v, warp_sum) * ((double)inv * (double)inv);
-    const uint32_t overflow = __ldcg(&st->overflow) != 0, next = st->t + 1;
-    __syncthreads();  // every thread has read t and the overflow flag
-    if (threadIdx.x == 32 && !overflow)
-        st->step_size = bias_step_size(a.hp, next);
-    if (threadIdx.x == 64 && !overflow)
-        st->rbc2 = bias_rbc2(a.hp, next);
-    if (threadIdx.x == 96)
-        scaler_update(st, a.hp, st->n_ranks, overflow, next);
+    const uint32_t overflow = __ldcg(&st->overflow) != 0;
+    const double sumsq = block_sum(v, warp_sum) * ((double)inv * (double)inv);
+    // block_sum's barrier: every thread has read the overflow flag
+    if (threadIdx.x == 32) {
+        const ScalerCand cand{__ldcg(&ready->cand.L_skip), __ldcg(&ready->cand.inv_skip),
+                              __ldcg(&ready->cand.L_ok), __ldcg(&ready->cand.inv_ok),
+                              __ldcg(&ready->cand.good_ok), __ldcg(&ready->cand.decay)};
+        scaler_apply(st, cand, overflow, st->t + 1);
+        if (!overflow) {
+            st->step_size = __ldcg(&ready->step_size);
+            st->rbc2 = __ldcg(&ready->rbc2);
+        }
+    }
     if (threadIdx.x == 0) {
-        const double norm = sqrt(total);
+        const double norm = sqrt(sumsq);
         const float clip = clip_coefficient(norm, overflow, a.hp.max_grad_norm);
         st->arrivals = 0;
-        st->sumsq = total;
+        st->sumsq = sumsq;
         st->norm = norm;
         st->clip_coef = clip;
         st->applied_c = overflow ? -1.0f : clip;
@@ -305,182 +472,386 @@ __global__ void __launch_bounds__(kThreads) k_tensors_norm(const __grid_constant
 /* AdamW                                                                                  */
 /* ------------------------------------------------------------------------------------ */
 
-__global__ void __launch_bounds__(kThreads) k_tensors_adamw(const __grid_constant__ TensorsArgs a)
+/* A lane's 8 gradients as they lie in memory. */
+struct RawGrad {
+    uint4 a, b;  // b: fp32 gradients only
+
+    __device__ __forceinline__ void load(const void* g, uint64_t i, uint32_t dtype)
+    {
+        if (dtype == ZERO_F32) {
+            a = ld_stream_v4(static_cast<const float*>(g) + i);
+            b = ld_stream_v4(static_cast<const float*>(g) + i + 4);
+        } else {
+            a = ld_stream_v4(static_cast<const uint16_t*>(g) + i);
+        }
+    }
+    __device__ __forceinline__ void values(uint32_t dtype, float (&x)[8]) const
+    {
+        if (dtype == ZERO_F32) {
+            x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y);
+            x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
+            x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y);
+            x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
+        } else if (dtype == ZERO_F16) {
+            widen8<ZERO_F16>(a, x);
+        } else {
+            widen8<ZERO_BF16>(a, x);
+        }
+    }
+};
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_tensors_adamw(const __grid_constant__ AdamwList<CAP> a)
 {
     grid_dependency_wait();
     if (a.st->skip)
         return;
     Scalars s = step_scalars(a);
     const float inv = a.st->inv_scale_used, step = s.step;
-    for (uint32_t c = blockIdx.x; c < a.l.n_chunks; c += gridDim.x) {
-        const uint32_t k = tensor_of(a.l, c);
-        const Ref& t = a.l.t[k];
+    const uint32_t lane = threadIdx.x & 31;
+    Place at{0, 1, 0, 0};
+    for (uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < a.l.n_units; u += gridDim.x * kWarps) {
+        locate(a.l, u, at);
+        const Ref& t = a.l.t[at.k];
         const uint32_t dtype = t.flags & kGradMask;
         float* m = static_cast<float*>(t.m);
         float* v = static_cast<float*>(t.v);
         s.step = __fmul_rn(step, t.lr_scale);
         s.decay = t.decay;
-        const uint64_t off = (uint64_t)(c - a.l.begin[k]) * kTensorChunk;
-        if ((t.flags & kAligned) && off + kTensorChunk <= t.elems) {
-            const uint64_t i = off + threadIdx.x * kPer;
-            float x8[8], p8[8], m8[8], v8[8];
-            load_grad8(t.grad, i, dtype, x8);
+        const bool vec = t.flags & kVector;
+        const uint64_t off = t.head + (uint64_t)at.unit * kUnit;
+        // consecutive elements per lane in 128-bit accesses, else lanes side by side
+        const uint64_t i = vec ? off + lane * kPer : off + lane;
+        const uint32_t stride = vec ? 1 : 32;
+        float x8[8], p8[8], m8[8], v8[8];
+        const bool whole = vec && i + kPer <= t.elems;
+        if (whole) {
+            RawGrad raw;
+            raw.load(t.grad, i, dtype);
             load8(t.master + i, p8);
             load8(m + i, m8);
             load8(v + i, v8);
+            raw.values(dtype, x8);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                adamw_one(__fmul_rn(x8[e], inv), p8[e], m8[e], v8[e], s);
+            for (int e = 0; e < 8; ++e) {
+                const uint64_t q = i + e * stride;
+                const bool in = q < t.elems;
+                x8[e] = in ? one_grad(t.grad, q, dtype) : 0.0f;
+                p8[e] = in ? __ldcs(t.master + q) : 0.0f;
+                m8[e] = in ? __ldcs(m + q) : 0.0f;
+                v8[e] = in ? __ldcs(v + q) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            adamw_one(__fmul_rn(x8[e], inv), p8[e], m8[e], v8[e], s);
+        if (whole) {
             store8(t.master + i, p8);
             store8(m + i, m8);
             store8(v + i, v8);
             if (t.params)
                 store_params8(t.params + i, t.flags & kOutF16, p8);
         } else {
-#pragma unroll 4
-            for (int e = 0; e < kPer; ++e) {
-                const uint64_t i = off + e * kThreads + threadIdx.x;
-                if (i < t.elems) {
-                    float p = t.master[i], mi = m[i], vi = v[i];
-                    adamw_one(__fmul_rn(one_grad(t.grad, i, dtype), inv), p, mi, vi, s);
-                    t.master[i] = p;
-                    m[i] = mi;
-                    v[i] = vi;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint64_t q = i + e * stride;
+                if (q < t.elems) {
+                    __stcs(t.master + q, p8[e]);
+                    __stcs(m + q, m8[e]);
+                    __stcs(v + q, v8[e]);
                     if (t.params)
-                        t.params[i] = (t.flags & kOutF16) ? pack1<true>(p) : pack1<false>(p);
+                        t.params[q] = (t.flags & kOutF16) ? pack1<true>(p8[e]) : pack1<false>(p8[e]);
                 }
             }
         }
+        if (at.unit == 0 && lane < t.head && lane < t.elems) {  // before the 16-byte boundary
+            float p = t.master[lane], mi = m[lane], vi = v[lane];
+            adamw_one(__fmul_rn(one_grad(t.grad, lane, dtype), inv), p, mi, vi, s);
+            t.master[lane] = p;
+            m[lane] = mi;
+            v[lane] = vi;
+            if (t.params)
+                t.params[lane] = (t.flags & kOutF16) ? pack1<true>(p) : pack1<false>(p);
+        }
     }
 }
 
-/* A lane's 8 codes of a block. */
-struct Codes {
-    uint32_t c[8];
+/* The largest magnitude, NaN above all. */
+__device__ __forceinline__ float max_abs(float top, float x)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
+    return r;
+}
 
-    __device__ __forceinline__ void unpack(uint2 w)
+__device__ __forceinline__ float sqrt_fast(float x)
+{
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+/* What a lane reads of its unit: 8 consecutive elements, and the block's exponents. */
+struct Pre8 {
+    RawGrad g;
+    float4 p0, p1;
+    uint2 m, v;
+    uint32_t bm, bv;
+
+    __device__ __forceinline__ void load(const Ref& t, uint32_t unit, uint32_t lane)
     {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            c[e] = w.x >> (8 * e) & 0xffu;
-            c[4 + e] = w.y >> (8 * e) & 0xffu;
-        }
-    }
-    __device__ __forceinline__ uint2 pack() const
-    {
-        return make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-                          c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+        const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
+        g.load(t.grad, i, t.flags & kGradMask);
+        p0 = __ldcs(reinterpret_cast<const float4*>(t.master + i));
+        p1 = __ldcs(reinterpret_cast<const float4*>(t.master + i) + 1);
+        m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
+        v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
+        bm = t.exps[2 * (uint64_t)unit];
+        bv = t.exps[2 * (uint64_t)unit + 1];
     }
 };
 
-/* The AdamW element update with this form's denominator: one multiplication by 1/rbc2,
- * rounded once per step, in place of a division per element. */
-__device__ __forceinline__ void moments(float gc, float& m, float& v, const Scalars& s)
+/* Four codes of a word as floats with the code's exponent in fp32's field. */
+__device__ __forceinline__ float raw_m(uint32_t w, int byte)
 {
-    m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.omb1, gc));
-    v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(s.omb2, __fmul_rn(gc, gc)));
+    const int top = (int)__byte_perm(w, 0, byte << 12 | 0x444);  // the code in bits 31..24
+    return __uint_as_float((uint32_t)(top >> 4) & 0x87f00000u);
 }
 
-__device__ __forceinline__ float updated(float p, float m, float v, float inv_rbc2, const Scalars& s)
+__device__ __forceinline__ float raw_v(uint32_t w, int byte)
 {
-    const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v), inv_rbc2), s.eps);
-    return __fsub_rn(__fmul_rn(p, s.decay), __fmul_rn(s.step, __fdiv_rn(m, denom)));
+    return __uint_as_float(__byte_perm(w, 0, byte << 12 | 0x444) >> 4);
 }
 
-__global__ void __launch_bounds__(kThreads) k_tensors_adamw8(const __grid_constant__ TensorsArgs a)
+/* Four codes, each in its word's top byte, as one word. */
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+/* The block exponents up to which one multiplication by a power of two stands for the two
+ * of the definition (their product is a normal float both ways). */
+constexpr uint32_t kPlainM = 141, kPlainV = 157;
+
+struct Step8 {
+    float inv, c, step, decay, b1, b2, omb1, omb2, eps, rbc2;
+    uint32_t key;
+    bool exact;  // eps too small for the fast reciprocal
+};
+
+/* One block of 256 elements, 8 per lane: moments, parameters, new codes and exponents.
+ *   x p                  gradients; parameters, updated
+ *   ym yv                the codes as floats (raw_m, raw_v)
+ *   bm bv                the exponents, replaced
+ *   cm cv                the new codes, each in its word's top byte
+ *   rm rv                random words; their top 20 bits round
+ * The moments are fp32 operations each rounded as written (the codes follow from them bit
+ * for bit): decoding needs no instruction of its own, since b1 * (y * 2^k) = y * (b1 * 2^k)
+ * exactly.  The parameter's square root, division and sums use the fast forms (within 2
+ * ulp): the rounding of p itself is larger than what they add to the update. */
+__device__ __forceinline__ void block8(const float (&x)[8], float (&p)[8], float (&ym)[8], float (&yv)[8],
+                                       uint32_t& bm, uint32_t& bv, const uint32_t (&rm)[8],
+                                       const uint32_t (&rv)[8], uint32_t (&cm)[8], uint32_t (&cv)[8],
+                                       const Step8& s)
+{
+    float fm = bm ? __uint_as_float((bm + 112u) << 23) : 0.0f;
+    float fv = bv ? __uint_as_float((bv + 96u) << 23) : 0.0f;
+    if (bm > kPlainM || bv > kPlainV) {  // the whole warp: far above any gradient met in earnest
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ym[e] = __fmul_rn(ym[e], 0x1p112f);
+            yv[e] = __fmul_rn(yv[e], 0x1p96f);
+        }
+        fm = exp_scale(bm);
+        fv = exp_scale(bv);
+    }
+    fm = __fmul_rn(s.b1, fm);
+    fv = __fmul_rn(s.b2, fv);
+    const uint64_t inv2 = f2(s.inv, s.inv), c2 = f2(s.c, s.c), fm2 = f2(fm, fm), fv2 = f2(fv, fv);
+    const uint64_t o1 = f2(s.omb1, s.omb1), o2 = f2(s.omb2, s.omb2);
+    float m[8], v[8], top_m = 0.0f, top_v = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const uint64_t gc = f2_mul(c2, f2_mul(f2(x[e], x[e + 1]), inv2));
+        const uint64_t m2 = f2_add(f2_mul(f2(ym[e], ym[e + 1]), fm2), f2_mul(o1, gc));
+        const uint64_t v2 = f2_add(f2_mul(f2(yv[e], yv[e + 1]), fv2), f2_mul(o2, f2_mul(gc, gc)));
+        f2_split(m2, m[e], m[e + 1]);
+        f2_split(v2, v[e], v[e + 1]);
+        top_m = max_abs(max_abs(top_m, m[e]), m[e + 1]);
+        top_v = max_abs(max_abs(top_v, v[e]), v[e + 1]);
+    }
+    bm = block_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m) & 0x7fffffffu));
+    bv = block_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v) & 0x7fffffffu));
+    if (bm <= kPlainM && bv <= kPlainV && !s.exact) {
+        const uint64_t um = f2(__uint_as_float((142u - bm) << 23), __uint_as_float((142u - bm) << 23));
+        const uint64_t uv = f2(__uint_as_float((158u - bv) << 23), __uint_as_float((158u - bv) << 23));
+        // sqrt(v) = sqrt(v * 2^24) * 2^-12: no subnormal v reaches the fast square root
+        const float r = __fmul_rn(__fdiv_rn(1.0f, s.rbc2), 0x1p-12f);
+        const uint64_t up = f2(0x1p24f, 0x1p24f), r2 = f2(r, r), eps2 = f2(s.eps, s.eps);
+        const uint64_t decay2 = f2(s.decay, s.decay), step2 = f2(-s.step, -s.step);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const uint64_t m2 = f2(m[e], m[e + 1]), v2 = f2(v[e], v[e + 1]);
+            float v0, v1, d0, d1, y0, y1;
+            f2_split(f2_mul(v2, up), v0, v1);
+            f2_split(f2_fma(f2(sqrt_fast(v0), sqrt_fast(v1)), r2, eps2), d0, d1);
+            const uint64_t q = f2_mul(f2_mul(m2, step2), f2(rcp_fast(d0), rcp_fast(d1)));
+            f2_split(f2_fma(f2(p[e], p[e + 1]), decay2, q), p[e], p[e + 1]);
+            f2_split(f2_mul(m2, um), y0, y1);
+            // sign and magnitude: adding to the bits adds to the magnitude
+            const uint32_t t0 = __float_as_uint(y0) + (rm[e] >> 12), t1 = __float_as_uint(y1) + (rm[e + 1] >> 12);
+            cm[e] = (t0 << 4 & 0x7fffffffu) | (t0 & 0x80000000u);
+            cm[e + 1] = (t1 << 4 & 0x7fffffffu) | (t1 & 0x80000000u);
+            f2_split(f2_mul(v2, uv), y0, y1);
+            uint32_t w0 = __float_as_uint(y0) + (rv[e] >> 12), w1 = __float_as_uint(y1) + (rv[e + 1] >> 12);
+            if (v[e] != 0.0f)
+                w0 = max(w0, 1u << 20);
+            if (v[e + 1] != 0.0f)
+                w1 = max(w1, 1u << 20);
+            cv[e] = w0 << 4;
+            cv[e + 1] = w1 << 4;
+        }
+    } else {
+        const float inv_rbc2 = __fdiv_rn(1.0f, s.rbc2), um = exp_unscale(bm), uv = exp_unscale(bv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v[e]), inv_rbc2), s.eps);
+            p[e] = __fsub_rn(__fmul_rn(p[e], s.decay), __fmul_rn(s.step, __fdiv_rn(m[e], denom)));
+            cm[e] = encode_m(m[e], um, rm[e] >> 12) << 24;
+            cv[e] = encode_v(v[e], uv, rv[e] >> 12) << 24;
+        }
+    }
+}
+
+__device__ __forceinline__ bool whole_unit(const Ref& t, uint32_t unit)
+{
+    return (t.flags & kVector) && ((uint64_t)unit + 1) * kUnit <= t.elems;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_constant__ AdamwList<CAP> a)
 {
     grid_dependency_wait();
-    if (a.st->skip)
+    const zero_step_state_t* st = a.st;
+    if (st->skip)
         return;
-    Scalars s = step_scalars(a);
-    const float inv = a.st->inv_scale_used, step = s.step, inv_rbc2 = __fdiv_rn(1.0f, s.rbc2);
-    const uint32_t key = step_key(a.seed, a.st->t);
-    const uint32_t lane = threadIdx.x & 31;
-    // the generator's outputs for this lane's elements where lanes lie side by side
-    Jump jm = jump(1), jv = jump(9);
-    for (uint32_t q = 0; q < (lane & 7); ++q) {
-        jm.add = jm.add * kLcgMul + kLcgAdd, jm.mul *= kLcgMul;
-        jv.add = jv.add * kLcgMul + kLcgAdd, jv.mul *= kLcgMul;
-    }
-    for (uint32_t c = blockIdx.x; c < a.l.n_chunks; c += gridDim.x) {
-        const uint32_t k = tensor_of(a.l, c);
+    Step8 s;
+    s.inv = st->inv_scale_used;
+    s.c = st->clip_coef;
+    s.b1 = a.beta1;
+    s.b2 = a.beta2;
+    s.omb1 = __fsub_rn(1.0f, a.beta1);
+    s.omb2 = __fsub_rn(1.0f, a.beta2);
+    s.eps = a.eps;
+    s.rbc2 = st->rbc2;
+    s.key = step_key(a.seed, st->t);
+    s.exact = a.eps < 0x1p-100f;
+    const float step = st->step_size;
+    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps, n = a.l.n_units;
+    uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (u >= n)
+        return;
+    Place at{0, 1, 0, 0};
+    Pre8 pre;
+    locate(a.l, u, at);
+    if (whole_unit(a.l.t[at.k], at.unit))
+        pre.load(a.l.t[at.k], at.unit, lane);
+    for (;;) {
+        const uint32_t k = at.k, unit = at.unit;
+        const Pre8 cur = pre;
+        u += stride;
+        const bool more = u < n;
+        if (more) {  // the next unit's loads go out before this one's arithmetic
+            locate(a.l, u, at);
+            if (whole_unit(a.l.t[at.k], at.unit))
+                pre.load(a.l.t[at.k], at.unit, lane);
+        }
         const Ref& t = a.l.t[k];
+        s.step = __fmul_rn(step, t.lr_scale);
+        s.decay = t.decay;
         const uint32_t dtype = t.flags & kGradMask;
         uint8_t* m = static_cast<uint8_t*>(t.m);
         uint8_t* v = static_cast<uint8_t*>(t.v);
-        s.step = __fmul_rn(step, t.lr_scale);
-        s.decay = t.decay;
-        const uint64_t blk = (uint64_t)(c - a.l.begin[k]) * (kTensorChunk / kBlk) + (threadIdx.x >> 5);
-        const uint64_t off = blk * kBlk;
-        if (off >= t.elems)
-            continue;  // a whole warp past the tensor's last block
-        const bool vec = (t.flags & kAligned) && off + kBlk <= t.elems;
-        // element e of this lane: consecutive in 128-bit accesses, else lanes side by side
-        const uint64_t i0 = vec ? off + lane * kPer : off + lane;
-        const uint64_t left = i0 < t.elems ? t.elems - i0 : 0;
-        float x8[8], p8[8], m8[8], v8[8];
-        Codes cm, cv;
-        if (vec) {
-            load_grad8(t.grad, i0, dtype, x8);
-            load8(t.master + i0, p8);
-            cm.unpack(__ldcs(reinterpret_cast<const uint2*>(m + i0)));
-            cv.unpack(__ldcs(reinterpret_cast<const uint2*>(v + i0)));
+        const bool whole = whole_unit(t, unit);
+        // lane L's seed is that of the block's group L
+        const uint32_t seed = mix32(s.key + (t.group0 + unit * 32 + lane) * kGolden);
+        uint32_t bm, bv, rm[8], rv[8], cm[8], cv[8];
+        float x[8], p[8], ym[8], yv[8];
+        if (whole) {
+            cur.g.values(dtype, x);
+            p[0] = cur.p0.x, p[1] = cur.p0.y, p[2] = cur.p0.z, p[3] = cur.p0.w;
+            p[4] = cur.p1.x, p[5] = cur.p1.y, p[6] = cur.p1.z, p[7] = cur.p1.w;
+            bm = cur.bm;
+            bv = cur.bv;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ym[e] = raw_m(e < 4 ? cur.m.x : cur.m.y, e & 3);
+                yv[e] = raw_v(e < 4 ? cur.v.x : cur.v.y, e & 3);
+                const Jump jm = jump(e + 1), jv = jump(e + 9);
+                rm[e] = seed * jm.mul + jm.add;
+                rv[e] = seed * jv.mul + jv.add;
+            }
         } else {
+            // lanes side by side: element e of a lane lies in group 4e + lane/8, place lane%8
+            const uint64_t i = (uint64_t)unit * kUnit + lane;
+            bm = t.exps[2 * (uint64_t)unit];
+            bv = t.exps[2 * (uint64_t)unit + 1];
+            Jump jm = jump(1), jv = jump(9);
+            for (uint32_t q = 0; q < (lane & 7); ++q) {
+                jm.add = jm.add * kLcgMul + kLcgAdd, jm.mul *= kLcgMul;
+                jv.add = jv.add * kLcgMul + kLcgAdd, jv.mul *= kLcgMul;
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const bool in = e * 32u < left;
-                x8[e] = in ? one_grad(t.grad, i0 + e * 32, dtype) : 0.0f;
-                p8[e] = in ? t.master[i0 + e * 32] : 0.0f;
-                cm.c[e] = in ? m[i0 + e * 32] : 0u;
-                cv.c[e] = in ? v[i0 + e * 32] : 0u;
+                const uint64_t q = i + e * 32;
+                const bool in = q < t.elems;
+                x[e] = in ? one_grad(t.grad, q, dtype) : 0.0f;
+                p[e] = in ? __ldcs(t.master + q) : 0.0f;
+                ym[e] = in ? raw_m(m[q], 0) : 0.0f;
+                yv[e] = in ? raw_v(v[q], 0) : 0.0f;
+                const uint32_t s0 = __shfl_sync(0xffffffffu, seed, e * 4 + (lane >> 3));
+                rm[e] = s0 * jm.mul + jm.add;
+                rv[e] = s0 * jv.mul + jv.add;
             }
         }
-        const float scale_m = exp_scale(t.exps[2 * blk]), scale_v = exp_scale(t.exps[2 * blk + 1]);
-        uint32_t top_m = 0, top_v = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            m8[e] = decode_m(cm.c[e], scale_m);
-            v8[e] = decode_v(cv.c[e], scale_v);
-            moments(__fmul_rn(s.c, __fmul_rn(x8[e], inv)), m8[e], v8[e], s);
-            p8[e] = updated(p8[e], m8[e], v8[e], inv_rbc2, s);
-            top_m = max(top_m, __float_as_uint(m8[e]) & 0x7fffffffu);
-            top_v = max(top_v, __float_as_uint(v8[e]) & 0x7fffffffu);
-        }
-        const uint32_t bm = block_exponent(__reduce_max_sync(0xffffffffu, top_m));
-        const uint32_t bv = block_exponent(__reduce_max_sync(0xffffffffu, top_v));
-        const float unscale_m = exp_unscale(bm), unscale_v = exp_unscale(bv);
-        const uint32_t group = t.group0 + (uint32_t)blk * 32;
-        if (vec) {
-            const uint32_t s0 = mix32(key + (group + lane) * kGolden);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const Jump a1 = jump(e + 1), a9 = jump(e + 9);
-                cm.c[e] = encode_m(m8[e], unscale_m, (s0 * a1.mul + a1.add) >> 12);
-                cv.c[e] = encode_v(v8[e], unscale_v, (s0 * a9.mul + a9.add) >> 12);
-            }
-            store8(t.master + i0, p8);
+        block8(x, p, ym, yv, bm, bv, rm, rv, cm, cv, s);
+        if (whole) {
+            const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
+            store8(t.master + i, p);
             if (t.params)
-                store_params8(t.params + i0, t.flags & kOutF16, p8);
-            __stcs(reinterpret_cast<uint2*>(m + i0), cm.pack());
-            __stcs(reinterpret_cast<uint2*>(v + i0), cv.pack());
+                store_params8(t.params + i, t.flags & kOutF16, p);
+            __stcs(reinterpret_cast<uint2*>(m + i),
+                   make_uint2(top_bytes(cm[0], cm[1], cm[2], cm[3]), top_bytes(cm[4], cm[5], cm[6], cm[7])));
+            __stcs(reinterpret_cast<uint2*>(v + i),
+                   make_uint2(top_bytes(cv[0], cv[1], cv[2], cv[3]), top_bytes(cv[4], cv[5], cv[6], cv[7])));
         } else {
+            const uint64_t i = (uint64_t)unit * kUnit + lane;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t s0 = mix32(key + (group + e * 4 + (lane >> 3)) * kGolden);
-                if (e * 32u < left) {
-                    const uint64_t i = i0 + e * 32;
-                    m[i] = (uint8_t)encode_m(m8[e], unscale_m, (s0 * jm.mul + jm.add) >> 12);
-                    v[i] = (uint8_t)encode_v(v8[e], unscale_v, (s0 * jv.mul + jv.add) >> 12);
-                    t.master[i] = p8[e];
+                const uint64_t q = i + e * 32;
+                if (q < t.elems) {
+                    m[q] = (uint8_t)(cm[e] >> 24);
+                    v[q] = (uint8_t)(cv[e] >> 24);
+                    __stcs(t.master + q, p[e]);
                     if (t.params)
-                        t.params[i] = (t.flags & kOutF16) ? pack1<true>(p8[e]) : pack1<false>(p8[e]);
+                        t.params[q] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
                 }
             }
         }
         if (lane == 0) {
-            t.exps[2 * blk] = (uint8_t)bm;
-            t.exps[2 * blk + 1] = (uint8_t)bv;
+            t.exps[2 * (uint64_t)unit] = (uint8_t)bm;
+            t.exps[2 * (uint64_t)unit + 1] = (uint8_t)bv;
         }
+        if (!more)
+            break;
     }
 }
 
@@ -488,104 +859,141 @@ __global__ void __launch_bounds__(kThreads) k_tensors_adamw8(const __grid_consta
 /* 8-bit states to values and back                                                        */
 /* ------------------------------------------------------------------------------------ */
 
-template <bool WRITE>
-__global__ void __launch_bounds__(kThreads) k_tensors_state8(const __grid_constant__ List l)
+/* A unit of the codec, lanes side by side. */
+template <bool WRITE, int CAP>
+__device__ __forceinline__ void codec_by_element(const List<CAP>& l, uint32_t k, uint32_t unit)
+{
+    const Ref& t = l.t[k];
+    const uint32_t lane = threadIdx.x & 31;
+    uint8_t* m = static_cast<uint8_t*>(t.m);
+    uint8_t* v = static_cast<uint8_t*>(t.v);
+    uint8_t* b = t.exps + 2 * (uint64_t)unit;
+    const uint64_t i = (uint64_t)unit * kUnit + lane;
+    if (WRITE) {
+        float xm[8], xv[8];
+        uint32_t top_m = 0, top_v = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t q = i + e * 32;
+            xm[e] = q < t.elems ? __ldcs(static_cast<const float*>(t.x) + q) : 0.0f;
+            xv[e] = q < t.elems ? __ldcs(static_cast<const float*>(t.y) + q) : 0.0f;
+            top_m = max(top_m, __float_as_uint(xm[e]) & 0x7fffffffu);
+            top_v = max(top_v, __float_as_uint(xv[e]) & 0x7fffffffu);
+        }
+        const uint32_t bm = block_exponent(__reduce_max_sync(0xffffffffu, top_m));
+        const uint32_t bv = block_exponent(__reduce_max_sync(0xffffffffu, top_v));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t q = i + e * 32;
+            if (q < t.elems) {
+                m[q] = (uint8_t)encode_m(xm[e], exp_unscale(bm), kNearest);
+                v[q] = (uint8_t)encode_v(xv[e], exp_unscale(bv), kNearest);
+            }
+        }
+        if (lane == 0) {
+            b[0] = (uint8_t)bm;
+            b[1] = (uint8_t)bv;
+        }
+    } else {
+        const float scale_m = exp_scale(b[0]), scale_v = exp_scale(b[1]);
+        uint32_t cm[8], cv[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t q = i + e * 32;
+            cm[e] = q < t.elems ? m[q] : 0u;
+            cv[e] = q < t.elems ? v[q] : 0u;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint64_t q = i + e * 32;
+            if (q >= t.elems)
+                continue;
+            const float xm = decode_m(cm[e], scale_m), xv = decode_v(cv[e], scale_v);
+            if (t.flags & kValueBF16) {
+                static_cast<uint16_t*>(t.x)[q] = pack1<false>(xm);
+                static_cast<uint16_t*>(t.y)[q] = pack1<false>(xv);
+            } else {
+                static_cast<float*>(t.x)[q] = xm;
+                static_cast<float*>(t.y)[q] = xv;
+            }
+        }
+    }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_state8_read(const __grid_constant__ List<CAP> l)
 {
     grid_dependency_wait();
-    const uint32_t lane = threadIdx.x & 31;
-    for (uint32_t c = blockIdx.x; c < l.n_chunks; c += gridDim.x) {
-        const uint32_t k = tensor_of(l, c);
-        const Ref& t = l.t[k];
-        uint8_t* m = static_cast<uint8_t*>(t.m);
-        uint8_t* v = static_cast<uint8_t*>(t.v);
-        const uint64_t blk = (uint64_t)(c - l.begin[k]) * (kTensorChunk / kBlk) + (threadIdx.x >> 5);
-        const uint64_t off = blk * kBlk;
-        if (off >= t.elems)
+    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
+    Place at{0, 1, 0, 0};
+    for (uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < l.n_units; u += stride) {
+        locate(l, u, at);
+        const Ref& t = l.t[at.k];
+        if (!whole_unit(t, at.unit)) {
+            codec_by_element<false>(l, at.k, at.unit);
             continue;
-        const bool vec = (t.flags & kAligned) && off + kBlk <= t.elems;
-        const uint64_t i0 = vec ? off + lane * kPer : off + lane;
-        const uint64_t left = i0 < t.elems ? t.elems - i0 : 0;
-        float m8[8], v8[8];
-        Codes cm, cv;
-        if (WRITE) {
-            const float* xm = static_cast<const float*>(t.x);
-            const float* xv = static_cast<const float*>(t.y);
-            if (vec) {
-                load8(xm + i0, m8);
-                load8(xv + i0, v8);
-            } else {
+        }
+        const uint64_t i = (uint64_t)at.unit * kUnit + lane * kPer;
+        const uint2 cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
+        const uint2 cv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
+        const uint8_t* b = t.exps + 2 * (uint64_t)at.unit;
+        const float scale_m = exp_scale(b[0]), scale_v = exp_scale(b[1]);
+        float xm[8], xv[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    m8[e] = e * 32u < left ? xm[i0 + e * 32] : 0.0f;
-                    v8[e] = e * 32u < left ? xv[i0 + e * 32] : 0.0f;
-                }
-            }
-            uint32_t top_m = 0, top_v = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                top_m = max(top_m, __float_as_uint(m8[e]) & 0x7fffffffu);
-                top_v = max(top_v, __float_as_uint(v8[e]) & 0x7fffffffu);
-            }
-            const uint32_t bm = block_exponent(__reduce_max_sync(0xffffffffu, top_m));
-            const uint32_t bv = block_exponent(__reduce_max_sync(0xffffffffu, top_v));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                cm.c[e] = encode_m(m8[e], exp_unscale(bm), kNearest);
-                cv.c[e] = encode_v(v8[e], exp_unscale(bv), kNearest);
-            }
-            if (vec) {
-                __stcs(reinterpret_cast<uint2*>(m + i0), cm.pack());
-                __stcs(reinterpret_cast<uint2*>(v + i0), cv.pack());
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e * 32u < left) {
-                        m[i0 + e * 32] = (uint8_t)cm.c[e];
-                        v[i0 + e * 32] = (uint8_t)cv.c[e];
-                    }
-            }
-            if (lane == 0) {
-                t.exps[2 * blk] = (uint8_t)bm;
-                t.exps[2 * blk + 1] = (uint8_t)bv;
-            }
+        for (int e = 0; e < 8; ++e) {
+            xm[e] = __fmul_rn(__fmul_rn(raw_m(e < 4 ? cm.x : cm.y, e & 3), 0x1p112f), scale_m);
+            xv[e] = __fmul_rn(__fmul_rn(raw_v(e < 4 ? cv.x : cv.y, e & 3), 0x1p96f), scale_v);
+        }
+        if (t.flags & kValueBF16) {
+            store_params8(static_cast<uint16_t*>(t.x) + i, 0, xm);
+            store_params8(static_cast<uint16_t*>(t.y) + i, 0, xv);
         } else {
-            if (vec) {
-                cm.unpack(__ldcs(reinterpret_cast<const uint2*>(m + i0)));
-                cv.unpack(__ldcs(reinterpret_cast<const uint2*>(v + i0)));
-            } else {
+            store8(static_cast<float*>(t.x) + i, xm);
+            store8(static_cast<float*>(t.y) + i, xv);
+        }
+    }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) k_state8_write(const __grid_constant__ List<CAP> l)
+{
+    grid_dependency_wait();
+    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
+    Place at{0, 1, 0, 0};
+    for (uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < l.n_units; u += stride) {
+        locate(l, u, at);
+        const Ref& t = l.t[at.k];
+        if (!whole_unit(t, at.unit)) {
+            codec_by_element<true>(l, at.k, at.unit);
+            continue;
+        }
+        const uint64_t i = (uint64_t)at.unit * kUnit + lane * kPer;
+        float xm[8], xv[8];
+        load8(static_cast<const float*>(t.x) + i, xm);
+        load8(static_cast<const float*>(t.y) + i, xv);
+        uint32_t top_m = 0, top_v = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    cm.c[e] = e * 32u < left ? m[i0 + e * 32] : 0u;
-                    cv.c[e] = e * 32u < left ? v[i0 + e * 32] : 0u;
-                }
-            }
-            const float scale_m = exp_scale(t.exps[2 * blk]), scale_v = exp_scale(t.exps[2 * blk + 1]);
+        for (int e = 0; e < 8; ++e) {
+            top_m = max(top_m, __float_as_uint(xm[e]) & 0x7fffffffu);
+            top_v = max(top_v, __float_as_uint(xv[e]) & 0x7fffffffu);
+        }
+        const uint32_t bm = block_exponent(__reduce_max_sync(0xffffffffu, top_m));
+        const uint32_t bv = block_exponent(__reduce_max_sync(0xffffffffu, top_v));
+        const float um = exp_unscale(bm), uv = exp_unscale(bv);
+        uint32_t cm[8], cv[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                m8[e] = decode_m(cm.c[e], scale_m);
-                v8[e] = decode_v(cv.c[e], scale_v);
-            }
-            const bool bf16 = t.flags & kValueBF16;
-            if (vec && bf16) {
-                store_params8(static_cast<uint16_t*>(t.x) + i0, 0, m8);
-                store_params8(static_cast<uint16_t*>(t.y) + i0, 0, v8);
-            } else if (vec) {
-                store8(static_cast<float*>(t.x) + i0, m8);
-                store8(static_cast<float*>(t.y) + i0, v8);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e * 32u < left) {
-                        const uint64_t i = i0 + e * 32;
-                        if (bf16) {
-                            static_cast<uint16_t*>(t.x)[i] = pack1<false>(m8[e]);
-                            static_cast<uint16_t*>(t.y)[i] = pack1<false>(v8[e]);
-                        } else {
-                            static_cast<float*>(t.x)[i] = m8[e];
-                            static_cast<float*>(t.y)[i] = v8[e];
-                        }
-                    }
-            }
+        for (int e = 0; e < 8; ++e) {
+            cm[e] = encode_m(xm[e], um, kNearest) << 24;
+            cv[e] = encode_v(xv[e], uv, kNearest) << 24;
+        }
+        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i),
+               make_uint2(top_bytes(cm[0], cm[1], cm[2], cm[3]), top_bytes(cm[4], cm[5], cm[6], cm[7])));
+        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i),
+               make_uint2(top_bytes(cv[0], cv[1], cv[2], cv[3]), top_bytes(cv[4], cv[5], cv[6], cv[7])));
+        if (lane == 0) {
+            uint8_t* b = t.exps + 2 * (uint64_t)at.unit;
+            b[0] = (uint8_t)bm;
+            b[1] = (uint8_t)bv;
         }
     }
 }
@@ -605,7 +1013,7 @@ int check_tensor(const zero_tensor_t& t, const zero_tensor_t* other, Op op)
 {
     if (t.elems == 0)
         return other && other->elems != 0 ? ZERO_EINVAL : ZERO_OK;
-    if (t.elems > (1ull << 42))
+    if (t.elems > (1ull << 39))
         return ZERO_EINVAL;
     const bool codec = op == Op::kRead || op == Op::kWrite;
     const bool adamw = op == Op::kAdamw || op == Op::kAdamw8;
@@ -644,41 +1052,51 @@ int check_tensor(const zero_tensor_t& t, const zero_tensor_t* other, Op op)
     return ZERO_OK;
 }
 
-/* Every array of the operator allows 128-bit accesses of 8 elements. */
-bool vector_ok(const zero_tensor_t& t, const zero_tensor_t* other, Op op)
+/* Every array of the operator allows 128-bit accesses of 8 elements from element h on. */
+bool vector_from(const zero_tensor_t& t, const zero_tensor_t* other, Op op, uint32_t h)
 {
-    switch (op) {
-    case Op::kNorm: return at(t.grad, 16);
-    case Op::kAdamw:
-        return at(t.grad, 16) && at(t.master, 16) && at(t.m, 16) && at(t.v, 16) && at(t.params, 16);
-    case Op::kAdamw8:
-        return at(t.grad, 16) && at(t.master, 16) && at(t.m, 8) && at(t.v, 8) && at(t.params, 16);
-    default: return at(t.m, 8) && at(t.v, 8) && at(other->m, 16) && at(other->v, 16);
+    auto ok = [h](const void* p, uintptr_t size, uintptr_t align) {
+        return !p || (((uintptr_t)p + h * size) & (align - 1)) == 0;
+    };
+    if (op == Op::kRead || op == Op::kWrite) {
+        const uintptr_t size = other->state_dtype == ZERO_BF16 ? 2 : 4;
+        return ok(t.m, 1, 8) && ok(t.v, 1, 8) && ok(other->m, size, 16) && ok(other->v, size, 16);
     }
+    const bool rest = ok(t.grad, t.grad_dtype == ZERO_F32 ? 4 : 2, 16) && ok(t.master, 4, 16) && ok(t.params, 2, 16);
+    return op == Op::kAdamw ? rest && ok(t.m, 4, 16) && ok(t.v, 4, 16) : rest && ok(t.m, 1, 8) && ok(t.v, 1, 8);
 }
 
 /* Fills `l` with tensors from index `next` on, as many as fit; returns the next index. */
-uint64_t fill(List& l, const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
+uint64_t fill(List<kLarge>& l, const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
               uint64_t next, Op op, const zero_adamw_hparams_t* hp, uint32_t& group0)
 {
-    const uint64_t chunk = op == Op::kNorm ? kNormChunk : kTensorChunk;
-    uint64_t chunks = 0;
+    uint64_t units = 0;
     l.n = 0;
-    l.begin[0] = 0;
-    for (; next < n && l.n < (uint32_t)kCap; ++next) {
+    for (; next < n && l.n < (uint32_t)kLarge; ++next) {
         const zero_tensor_t& t = tensors[next];
         const zero_tensor_t* other = others ? others + next : nullptr;
         if (t.elems == 0)
             continue;
-        const uint64_t c = (t.elems + chunk - 1) / chunk;
-        if (chunks + c > 0xffffffffull - (1u << 20))
-            break;  // chunk counters are 32-bit; check_tensor bounds one tensor's chunks
+        // 32-bit states: an offset that all arrays share (pieces of flat buffers) is stepped
+        // over; 8-bit states: their blocks start at element 0
+        uint32_t head = 0;
+        if (op == Op::kAdamw)
+            while (head < 8 && !vector_from(t, other, op, head))
+                ++head;
+        const bool vec = head < 8 && vector_from(t, other, op, head);
+        if (!vec)
+            head = 0;
+        const uint64_t body = t.elems > head ? t.elems - head : 1;
+        const uint64_t c = (body + kUnit - 1) / kUnit;
+        if (units + c > 0xf0000000ull)
+            break;  // unit counters are 32-bit; check_tensor bounds one tensor's units
         Ref& r = l.t[l.n];
         memset(&r, 0, sizeof r);
         r.elems = t.elems;
         r.m = t.m;
         r.v = t.v;
         r.exps = t.exps;
+        r.flags = vec ? kVector : 0;
         if (other) {
             r.x = other->m;
             r.y = other->v;
@@ -689,22 +1107,62 @@ uint64_t fill(List& l, const zero_tensor_t* tensors, const zero_tensor_t* others
             r.master = t.master;
             r.params = t.params;
             r.flags |= t.grad_dtype;
-        }
-        if (hp) {
             r.lr_scale = t.lr_scale;
             r.decay = (float)(1.0 - (double)hp->lr * (double)t.lr_scale * (double)t.weight_decay);
             if ((t.params_dtype ? t.params_dtype : hp->params_dtype) == ZERO_F16)
                 r.flags |= kOutF16;
         }
-        if (vector_ok(t, other, op))
-            r.flags |= kAligned;
-        r.group0 = group0;
-        group0 += (uint32_t)((t.elems + kBlk - 1) / kBlk) * 32u;
-        chunks += c;
-        l.begin[++l.n] = (uint32_t)chunks;
+        if (op == Op::kAdamw)
+            r.head = head;
+        else
+            r.group0 = group0;
+        group0 += (uint32_t)((t.elems + kUnit - 1) / kUnit) * 32u;
+        units += c;
+        l.end[l.n++] = (uint32_t)units;
     }
-    l.n_chunks = (uint32_t)chunks;
+    for (uint32_t k = l.n; k < (uint32_t)kLarge && k % 4; ++k)
+        l.end[k] = ~0u;  // read with the last tensors', never at or below a unit's number
+    l.n_units = (uint32_t)units;
     return next;
+}
+
+/* The same list in the small form. */
+void shrink(const List<kLarge>& from, List<kSmall>& to)
+{
+    to.n = from.n;
+    to.n_units = from.n_units;
+    memcpy(to.end, from.end, sizeof to.end);
+    memcpy(to.t, from.t, from.n * sizeof(Ref));
+}
+
+/* The same for the norm. */
+uint64_t fill_norm(NormArgs& a, const zero_tensor_t* tensors, uint64_t n, uint64_t next)
+{
+    uint64_t end = 0;
+    a.n = 0;
+    for (; next < n && a.n < (uint32_t)kNormCap; ++next) {
+        const zero_tensor_t& t = tensors[next];
+        if (t.elems == 0)
+            continue;
+        const uint32_t size = t.grad_dtype == ZERO_F32 ? 4 : 2;
+        NormRef& r = a.t[a.n++];
+        const uintptr_t off = (uintptr_t)t.grad & 15u;
+        r.base = static_cast<const char*>(t.grad) - off;
+        r.skip = (uint32_t)(off / size);
+        r.elems = t.elems;
+        r.dtype = t.grad_dtype;
+        end += (r.skip + t.elems + 16 / size - 1) / (16 / size);
+        r.end = end;
+    }
+    return next;
+}
+
+int status_of(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return ZERO_OK;
+    record_cuda_error((int)e);
+    return ZERO_ECUDA;
 }
 
 int check_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n, Op op)
@@ -723,8 +1181,10 @@ int check_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64
     return align;
 }
 
-template <typename K>
-unsigned blocks_for(K kernel, uint64_t chunks, std::atomic<int> (&per_sm)[64])
+/* A launch over `units` units, a warp each, on at most as many blocks as fit at once. */
+template <typename Args>
+int launch_units(void (*kernel)(Args), std::atomic<int> (&per_sm)[64], uint32_t units, cudaStream_t s,
+                 const Args& a)
 {
     int dev = 0;
     cudaGetDevice(&dev);
@@ -735,56 +1195,62 @@ unsigned blocks_for(K kernel, uint64_t chunks, std::atomic<int> (&per_sm)[64])
         occ = o > 0 ? o : 1;
         per_sm[dev & 63].store(occ, std::memory_order_relaxed);
     }
-    const uint64_t cap = (uint64_t)sm_count() * (uint64_t)occ;
-    return (unsigned)(chunks < cap ? chunks : cap);
-}
-
-int status_of(cudaError_t e)
-{
-    if (e == cudaSuccess)
-        return ZERO_OK;
-    record_cuda_error((int)e);
-    return ZERO_ECUDA;
+    const uint64_t want = ((uint64_t)units + kWarps - 1) / kWarps, cap = (uint64_t)sm_count() * (uint64_t)occ;
+    return status_of(launch_pdl(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kThreads), 0, s, a));
 }
 
 int run_adamw(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparams_t* hp, uint64_t seed,
               const zero_step_state_t* st, cudaStream_t s, Op op)
 {
-    static std::atomic<int> occ[64], occ8[64];
-    TensorsArgs a;
-    a.st = st;
-    a.seed = seed;
-    a.beta1 = hp->beta1;
-    a.beta2 = hp->beta2;
-    a.eps = hp->eps;
+    static std::atomic<int> occ[4][64];
+    AdamwList<kLarge> a;
+    AdamwList<kSmall> b;
+    a.st = b.st = st;
+    a.seed = b.seed = seed;
+    a.beta1 = b.beta1 = hp->beta1;
+    a.beta2 = b.beta2 = hp->beta2;
+    a.eps = b.eps = hp->eps;
     uint32_t group0 = 0;
     for (uint64_t next = 0; next < n;) {
         next = fill(a.l, tensors, nullptr, n, next, op, hp, group0);
-        if (a.l.n_chunks == 0)
+        if (a.l.n == 0)
             continue;
-        const auto kernel = op == Op::kAdamw ? k_tensors_adamw : k_tensors_adamw8;
-        const unsigned grid = blocks_for(kernel, a.l.n_chunks, op == Op::kAdamw ? occ : occ8);
-        const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, s, a);
-        if (e != cudaSuccess)
-            return status_of(e);
+        int rc;
+        if (a.l.n <= (uint32_t)kSmall) {
+            shrink(a.l, b.l);
+            rc = op == Op::kAdamw ? launch_units(k_tensors_adamw<kSmall>, occ[0], b.l.n_units, s, b)
+                                  : launch_units(k_tensors_adamw8<kSmall>, occ[1], b.l.n_units, s, b);
+        } else {
+            rc = op == Op::kAdamw ? launch_units(k_tensors_adamw<kLarge>, occ[2], a.l.n_units, s, a)
+                                  : launch_units(k_tensors_adamw8<kLarge>, occ[3], a.l.n_units, s, a);
+        }
+        if (rc != ZERO_OK)
+            return rc;
     }
     return ZERO_OK;
 }
 
 int run_codec(const zero_tensor_t* t8, const zero_tensor_t* t32, uint64_t n, cudaStream_t s, Op op)
 {
-    static std::atomic<int> occ_r[64], occ_w[64];
-    List l;
+    static std::atomic<int> occ[4][64];
+    List<kLarge> a;
+    List<kSmall> b;
     uint32_t group0 = 0;
     for (uint64_t next = 0; next < n;) {
-        next = fill(l, t8, t32, n, next, op, nullptr, group0);
-        if (l.n_chunks == 0)
+        next = fill(a, t8, t32, n, next, op, nullptr, group0);
+        if (a.n == 0)
             continue;
-        const auto kernel = op == Op::kRead ? k_tensors_state8<false> : k_tensors_state8<true>;
-        const unsigned grid = blocks_for(kernel, l.n_chunks, op == Op::kRead ? occ_r : occ_w);
-        const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, s, l);
-        if (e != cudaSuccess)
-            return status_of(e);
+        int rc;
+        if (a.n <= (uint32_t)kSmall) {
+            shrink(a, b);
+            rc = op == Op::kRead ? launch_units(k_state8_read<kSmall>, occ[0], b.n_units, s, b)
+                                 : launch_units(k_state8_write<kSmall>, occ[1], b.n_units, s, b);
+        } else {
+            rc = op == Op::kRead ? launch_units(k_state8_read<kLarge>, occ[2], a.n_units, s, a)
+                                 : launch_units(k_state8_write<kLarge>, occ[3], a.n_units, s, a);
+        }
+        if (rc != ZERO_OK)
+            return rc;
     }
     return ZERO_OK;
 }
@@ -796,8 +1262,8 @@ using namespace zero;
 
 extern "C" size_t zero_tensors_workspace_bytes(uint64_t n_tensors)
 {
-    const uint64_t launches = n_tensors / kCap + 1;
-    return (size_t)(launches * kNormMaxBlocks * sizeof(double));
+    const uint64_t launches = n_tensors / kNormCap + 1;
+    return (size_t)(launches * kNormMaxBlocks * sizeof(double) + 64);
 }
 
 extern "C" int zero_tensors_state_init(uint32_t n_ranks, float loss_scale, uint32_t dynamic,
@@ -830,20 +1296,23 @@ extern "C" int zero_tensors_grad_norm(const zero_tensor_t* tensors, uint64_t n_t
         return ZERO_EINVAL;
     if (rc != ZERO_OK || !at(workspace, 16) || !at(st, 16))
         return ZERO_EALIGN;
-    static std::atomic<int> occ[64];
     NormArgs a;
     a.st = st;
     a.slots = workspace;
     a.hp = *hp;
     a.slot0 = 0;
-    uint32_t group0 = 0;
+    const uint64_t cap = (uint64_t)sm_count() * kNormBlocksPerSm;
     uint64_t next = 0;
     do {
-        next = fill(a.l, tensors, nullptr, n_tensors, next, Op::kNorm, nullptr, group0);
+        next = fill_norm(a, tensors, n_tensors, next);
         a.last = next == n_tensors;
-        unsigned grid = blocks_for(k_tensors_norm, a.l.n_chunks, occ);
-        grid = grid < 1 ? 1 : grid > kNormMaxBlocks ? kNormMaxBlocks : grid;
-        const cudaError_t e = launch_pdl(k_tensors_norm, dim3(grid), dim3(kThreads), 0,
+        // equal shares, in whole passes of a block's loads; short lists one load per thread
+        const uint64_t total = a.n ? a.t[a.n - 1].end : 0;
+        const uint64_t blocks = cap < kNormMaxBlocks ? cap : kNormMaxBlocks;
+        const uint64_t pass = total <= blocks * kNormPass ? kThreads : kNormPass;
+        a.quota = ((total + blocks - 1) / blocks + pass - 1) / pass * pass;
+        const unsigned grid = total ? (unsigned)((total + a.quota - 1) / a.quota) : 0u;
+        const cudaError_t e = launch_pdl(k_tensors_norm, dim3(grid + a.last), dim3(kThreads), 0,
                                          (cudaStream_t)stream, a);
         if (e != cudaSuccess)
             return status_of(e);
