@@ -642,25 +642,53 @@ __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c
 constexpr uint32_t kPlainM = 141, kPlainV = 157;
 
 struct Step8 {
-    float inv, c, step, decay, b1, b2, omb1, omb2, eps, rbc2;
+    float inv, c, step, decay, b1, b2, omb1, omb2, eps, inv_rbc2;
     uint32_t key;
     bool exact;  // eps too small for the fast reciprocal
 };
 
+/* The random words of a lane's element e, their top 20 bits to round with: consecutive
+ * elements of the lane's own group ... */
+struct RandomInGroup {
+    uint32_t seed;
+
+    __device__ __forceinline__ uint32_t m(int e) const { return seed * jump(e + 1).mul + jump(e + 1).add; }
+    __device__ __forceinline__ uint32_t v(int e) const { return seed * jump(e + 9).mul + jump(e + 9).add; }
+};
+
+/* ... or, lanes side by side, element e in group 4e + lane/8 (whose seed lane 4e + lane/8
+ * holds) at place lane%8. */
+struct RandomAcross {
+    uint32_t seed[8];
+    Jump jm, jv;
+
+    __device__ __forceinline__ RandomAcross(uint32_t own, uint32_t lane) : jm(jump(1)), jv(jump(9))
+    {
+        for (uint32_t q = 0; q < (lane & 7); ++q) {
+            jm.add = jm.add * kLcgMul + kLcgAdd, jm.mul *= kLcgMul;
+            jv.add = jv.add * kLcgMul + kLcgAdd, jv.mul *= kLcgMul;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            seed[e] = __shfl_sync(0xffffffffu, own, e * 4 + (lane >> 3));
+    }
+    __device__ __forceinline__ uint32_t m(int e) const { return seed[e] * jm.mul + jm.add; }
+    __device__ __forceinline__ uint32_t v(int e) const { return seed[e] * jv.mul + jv.add; }
+};
+
 /* One block of 256 elements, 8 per lane: moments, parameters, new codes and exponents.
- *   x p                  gradients; parameters, updated
- *   ym yv                the codes as floats (raw_m, raw_v)
- *   bm bv                the exponents, replaced
- *   cm cv                the new codes, each in its word's top byte
- *   rm rv                random words; their top 20 bits round
+ *   x p        gradients; parameters, updated
+ *   ym yv      the codes as floats (raw_m, raw_v)
+ *   bm bv      the exponents, replaced
+ *   cm cv      the new codes, element e in byte e
  * The moments are fp32 operations each rounded as written (the codes follow from them bit
  * for bit): decoding needs no instruction of its own, since b1 * (y * 2^k) = y * (b1 * 2^k)
  * exactly.  The parameter's square root, division and sums use the fast forms (within 2
  * ulp): the rounding of p itself is larger than what they add to the update. */
+template <typename Random>
 __device__ __forceinline__ void block8(const float (&x)[8], float (&p)[8], float (&ym)[8], float (&yv)[8],
-                                       uint32_t& bm, uint32_t& bv, const uint32_t (&rm)[8],
-                                       const uint32_t (&rv)[8], uint32_t (&cm)[8], uint32_t (&cv)[8],
-                                       const Step8& s)
+                                       uint32_t& bm, uint32_t& bv, const Random& random, uint2& cm,
+                                       uint2& cv, const Step8& s)
 {
     float fm = bm ? __uint_as_float((bm + 112u) << 23) : 0.0f;
     float fv = bv ? __uint_as_float((bv + 96u) << 23) : 0.0f;
@@ -690,45 +718,62 @@ __device__ __forceinline__ void block8(const float (&x)[8], float (&p)[8], float
     }
     bm = block_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(top_m) & 0x7fffffffu));
     bv = block_exponent(__reduce_max_sync(0xffffffffu, __float_as_uint(top_v) & 0x7fffffffu));
+    uint32_t word_m[2], word_v[2];
     if (bm <= kPlainM && bv <= kPlainV && !s.exact) {
         const uint64_t um = f2(__uint_as_float((142u - bm) << 23), __uint_as_float((142u - bm) << 23));
         const uint64_t uv = f2(__uint_as_float((158u - bv) << 23), __uint_as_float((158u - bv) << 23));
         // sqrt(v) = sqrt(v * 2^24) * 2^-12: no subnormal v reaches the fast square root
-        const float r = __fmul_rn(__fdiv_rn(1.0f, s.rbc2), 0x1p-12f);
+        const float r = __fmul_rn(s.inv_rbc2, 0x1p-12f);
         const uint64_t up = f2(0x1p24f, 0x1p24f), r2 = f2(r, r), eps2 = f2(s.eps, s.eps);
         const uint64_t decay2 = f2(s.decay, s.decay), step2 = f2(-s.step, -s.step);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            const uint64_t m2 = f2(m[e], m[e + 1]), v2 = f2(v[e], v[e + 1]);
-            float v0, v1, d0, d1, y0, y1;
-            f2_split(f2_mul(v2, up), v0, v1);
-            f2_split(f2_fma(f2(sqrt_fast(v0), sqrt_fast(v1)), r2, eps2), d0, d1);
-            const uint64_t q = f2_mul(f2_mul(m2, step2), f2(rcp_fast(d0), rcp_fast(d1)));
-            f2_split(f2_fma(f2(p[e], p[e + 1]), decay2, q), p[e], p[e + 1]);
-            f2_split(f2_mul(m2, um), y0, y1);
-            // sign and magnitude: adding to the bits adds to the magnitude
-            const uint32_t t0 = __float_as_uint(y0) + (rm[e] >> 12), t1 = __float_as_uint(y1) + (rm[e + 1] >> 12);
-            cm[e] = (t0 << 4 & 0x7fffffffu) | (t0 & 0x80000000u);
-            cm[e + 1] = (t1 << 4 & 0x7fffffffu) | (t1 & 0x80000000u);
-            f2_split(f2_mul(v2, uv), y0, y1);
-            uint32_t w0 = __float_as_uint(y0) + (rv[e] >> 12), w1 = __float_as_uint(y1) + (rv[e + 1] >> 12);
-            if (v[e] != 0.0f)
-                w0 = max(w0, 1u << 20);
-            if (v[e + 1] != 0.0f)
-                w1 = max(w1, 1u << 20);
-            cv[e] = w0 << 4;
-            cv[e + 1] = w1 << 4;
+        for (int h = 0; h < 2; ++h) {
+            uint32_t code_m[4], code_v[4];  // in the words' top bytes
+#pragma unroll
+            for (int o = 0; o < 4; o += 2) {
+                const int e = 4 * h + o;
+                const uint64_t m2 = f2(m[e], m[e + 1]), v2 = f2(v[e], v[e + 1]);
+                float v0, v1, d0, d1, y0, y1;
+                f2_split(f2_mul(v2, up), v0, v1);
+                f2_split(f2_fma(f2(sqrt_fast(v0), sqrt_fast(v1)), r2, eps2), d0, d1);
+                const uint64_t q = f2_mul(f2_mul(m2, step2), f2(rcp_fast(d0), rcp_fast(d1)));
+                f2_split(f2_fma(f2(p[e], p[e + 1]), decay2, q), p[e], p[e + 1]);
+                f2_split(f2_mul(m2, um), y0, y1);
+                // sign and magnitude: adding to the bits adds to the magnitude
+                const uint32_t t0 = __float_as_uint(y0) + (random.m(e) >> 12);
+                const uint32_t t1 = __float_as_uint(y1) + (random.m(e + 1) >> 12);
+                code_m[o] = (t0 << 4 & 0x7fffffffu) | (t0 & 0x80000000u);
+                code_m[o + 1] = (t1 << 4 & 0x7fffffffu) | (t1 & 0x80000000u);
+                f2_split(f2_mul(v2, uv), y0, y1);
+                uint32_t w0 = __float_as_uint(y0) + (random.v(e) >> 12);
+                uint32_t w1 = __float_as_uint(y1) + (random.v(e + 1) >> 12);
+                if (v[e] != 0.0f)
+                    w0 = max(w0, 1u << 20);
+                if (v[e + 1] != 0.0f)
+                    w1 = max(w1, 1u << 20);
+                code_v[o] = w0 << 4;
+                code_v[o + 1] = w1 << 4;
+            }
+            word_m[h] = top_bytes(code_m[0], code_m[1], code_m[2], code_m[3]);
+            word_v[h] = top_bytes(code_v[0], code_v[1], code_v[2], code_v[3]);
         }
     } else {
-        const float inv_rbc2 = __fdiv_rn(1.0f, s.rbc2), um = exp_unscale(bm), uv = exp_unscale(bv);
+        const float um = exp_unscale(bm), uv = exp_unscale(bv);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v[e]), inv_rbc2), s.eps);
-            p[e] = __fsub_rn(__fmul_rn(p[e], s.decay), __fmul_rn(s.step, __fdiv_rn(m[e], denom)));
-            cm[e] = encode_m(m[e], um, rm[e] >> 12) << 24;
-            cv[e] = encode_v(v[e], uv, rv[e] >> 12) << 24;
+        for (int h = 0; h < 2; ++h) {
+            word_m[h] = word_v[h] = 0;
+#pragma unroll
+            for (int o = 0; o < 4; ++o) {
+                const int e = 4 * h + o;
+                const float denom = __fadd_rn(__fmul_rn(__fsqrt_rn(v[e]), s.inv_rbc2), s.eps);
+                p[e] = __fsub_rn(__fmul_rn(p[e], s.decay), __fmul_rn(s.step, __fdiv_rn(m[e], denom)));
+                word_m[h] |= encode_m(m[e], um, random.m(e) >> 12) << (8 * o);
+                word_v[h] |= encode_v(v[e], uv, random.v(e) >> 12) << (8 * o);
+            }
         }
     }
+    cm = make_uint2(word_m[0], word_m[1]);
+    cv = make_uint2(word_v[0], word_v[1]);
 }
 
 __device__ __forceinline__ bool whole_unit(const Ref& t, uint32_t unit)
@@ -751,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_con
     s.omb1 = __fsub_rn(1.0f, a.beta1);
     s.omb2 = __fsub_rn(1.0f, a.beta2);
     s.eps = a.eps;
-    s.rbc2 = st->rbc2;
+    s.inv_rbc2 = __fdiv_rn(1.0f, st->rbc2);
     s.key = step_key(a.seed, st->t);
     s.exact = a.eps < 0x1p-100f;
     const float step = st->step_size;
@@ -783,9 +828,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_con
         const bool whole = whole_unit(t, unit);
         // lane L's seed is that of the block's group L
         const uint32_t seed = mix32(s.key + (t.group0 + unit * 32 + lane) * kGolden);
-        uint32_t bm, bv, rm[8], rv[8], cm[8], cv[8];
+        uint32_t bm, bv;
+        uint2 cm, cv;
         float x[8], p[8], ym[8], yv[8];
         if (whole) {
+            const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
             cur.g.values(dtype, x);
             p[0] = cur.p0.x, p[1] = cur.p0.y, p[2] = cur.p0.z, p[3] = cur.p0.w;
             p[4] = cur.p1.x, p[5] = cur.p1.y, p[6] = cur.p1.z, p[7] = cur.p1.w;
@@ -795,20 +842,17 @@ __global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_con
             for (int e = 0; e < 8; ++e) {
                 ym[e] = raw_m(e < 4 ? cur.m.x : cur.m.y, e & 3);
                 yv[e] = raw_v(e < 4 ? cur.v.x : cur.v.y, e & 3);
-                const Jump jm = jump(e + 1), jv = jump(e + 9);
-                rm[e] = seed * jm.mul + jm.add;
-                rv[e] = seed * jv.mul + jv.add;
             }
+            block8(x, p, ym, yv, bm, bv, RandomInGroup{seed}, cm, cv, s);
+            store8(t.master + i, p);
+            if (t.params)
+                store_params8(t.params + i, t.flags & kOutF16, p);
+            __stcs(reinterpret_cast<uint2*>(m + i), cm);
+            __stcs(reinterpret_cast<uint2*>(v + i), cv);
         } else {
-            // lanes side by side: element e of a lane lies in group 4e + lane/8, place lane%8
             const uint64_t i = (uint64_t)unit * kUnit + lane;
             bm = t.exps[2 * (uint64_t)unit];
             bv = t.exps[2 * (uint64_t)unit + 1];
-            Jump jm = jump(1), jv = jump(9);
-            for (uint32_t q = 0; q < (lane & 7); ++q) {
-                jm.add = jm.add * kLcgMul + kLcgAdd, jm.mul *= kLcgMul;
-                jv.add = jv.add * kLcgMul + kLcgAdd, jv.mul *= kLcgMul;
-            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint64_t q = i + e * 32;
@@ -817,29 +861,14 @@ __global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_con
                 p[e] = in ? __ldcs(t.master + q) : 0.0f;
                 ym[e] = in ? raw_m(m[q], 0) : 0.0f;
                 yv[e] = in ? raw_v(v[q], 0) : 0.0f;
-                const uint32_t s0 = __shfl_sync(0xffffffffu, seed, e * 4 + (lane >> 3));
-                rm[e] = s0 * jm.mul + jm.add;
-                rv[e] = s0 * jv.mul + jv.add;
             }
-        }
-        block8(x, p, ym, yv, bm, bv, rm, rv, cm, cv, s);
-        if (whole) {
-            const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
-            store8(t.master + i, p);
-            if (t.params)
-                store_params8(t.params + i, t.flags & kOutF16, p);
-            __stcs(reinterpret_cast<uint2*>(m + i),
-                   make_uint2(top_bytes(cm[0], cm[1], cm[2], cm[3]), top_bytes(cm[4], cm[5], cm[6], cm[7])));
-            __stcs(reinterpret_cast<uint2*>(v + i),
-                   make_uint2(top_bytes(cv[0], cv[1], cv[2], cv[3]), top_bytes(cv[4], cv[5], cv[6], cv[7])));
-        } else {
-            const uint64_t i = (uint64_t)unit * kUnit + lane;
+            block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint64_t q = i + e * 32;
                 if (q < t.elems) {
-                    m[q] = (uint8_t)(cm[e] >> 24);
-                    v[q] = (uint8_t)(cv[e] >> 24);
+                    m[q] = (uint8_t)((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
+                    v[q] = (uint8_t)((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
                     __stcs(t.master + q, p[e]);
                     if (t.params)
                         t.params[q] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
