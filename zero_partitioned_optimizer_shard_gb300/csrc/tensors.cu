@@ -124,18 +124,20 @@ __device__ __forceinline__ float one_grad(const void* g, uint64_t i, uint32_t dt
     return dtype == ZERO_F16 ? one16<ZERO_F16>(b) : one16<ZERO_BF16>(b);
 }
 
+/* 8 consecutive floats in one 256-bit access (32-byte aligned): with two of 128 bits each
+ * would touch every 32-byte sector of the warp's kilobyte and write it half. */
 __device__ __forceinline__ void load8(const float* p, float (&x)[8])
 {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    asm volatile("ld.global.L1::no_allocate.L2::evict_first.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p));
 }
 
 __device__ __forceinline__ void store8(float* p, const float (&x)[8])
 {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    asm volatile("st.global.L1::no_allocate.L2::evict_first.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
 }
 
 template <zero_dtype_t DT>
@@ -474,28 +476,30 @@ __global__ void __launch_bounds__(kThreads, kNormBlocksPerSm) k_tensors_norm(con
 
 /* A lane's 8 gradients as they lie in memory. */
 struct RawGrad {
-    uint4 a, b;  // b: fp32 gradients only
+    float w[8];  // 16-bit gradients: the first four words
 
     __device__ __forceinline__ void load(const void* g, uint64_t i, uint32_t dtype)
     {
         if (dtype == ZERO_F32) {
-            a = ld_stream_v4(static_cast<const float*>(g) + i);
-            b = ld_stream_v4(static_cast<const float*>(g) + i + 4);
+            load8(static_cast<const float*>(g) + i, w);
         } else {
-            a = ld_stream_v4(static_cast<const uint16_t*>(g) + i);
+            const uint4 a = ld_stream_v4(static_cast<const uint16_t*>(g) + i);
+            w[0] = __uint_as_float(a.x), w[1] = __uint_as_float(a.y);
+            w[2] = __uint_as_float(a.z), w[3] = __uint_as_float(a.w);
         }
     }
     __device__ __forceinline__ void values(uint32_t dtype, float (&x)[8]) const
     {
-        if (dtype == ZERO_F32) {
-            x[0] = __uint_as_float(a.x), x[1] = __uint_as_float(a.y);
-            x[2] = __uint_as_float(a.z), x[3] = __uint_as_float(a.w);
-            x[4] = __uint_as_float(b.x), x[5] = __uint_as_float(b.y);
-            x[6] = __uint_as_float(b.z), x[7] = __uint_as_float(b.w);
-        } else if (dtype == ZERO_F16) {
+        const uint4 a = make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]),
+                                   __float_as_uint(w[3]));
+        if (dtype == ZERO_F16) {
             widen8<ZERO_F16>(a, x);
-        } else {
+        } else if (dtype == ZERO_BF16) {
             widen8<ZERO_BF16>(a, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = w[e];
         }
     }
 };
@@ -602,7 +606,7 @@ __device__ __forceinline__ float rcp_fast(float x)
 /* What a lane reads of its unit: 8 consecutive elements, and the block's exponents. */
 struct Pre8 {
     RawGrad g;
-    float4 p0, p1;
+    float p[8];
     uint2 m, v;
     uint32_t bm, bv;
 
@@ -610,8 +614,7 @@ struct Pre8 {
     {
         const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
         g.load(t.grad, i, t.flags & kGradMask);
-        p0 = __ldcs(reinterpret_cast<const float4*>(t.master + i));
-        p1 = __ldcs(reinterpret_cast<const float4*>(t.master + i) + 1);
+        load8(t.master + i, p);
         m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
         v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
         bm = t.exps[2 * (uint64_t)unit];
@@ -834,12 +837,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_con
         if (whole) {
             const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
             cur.g.values(dtype, x);
-            p[0] = cur.p0.x, p[1] = cur.p0.y, p[2] = cur.p0.z, p[3] = cur.p0.w;
-            p[4] = cur.p1.x, p[5] = cur.p1.y, p[6] = cur.p1.z, p[7] = cur.p1.w;
             bm = cur.bm;
             bv = cur.bv;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
+                p[e] = cur.p[e];
                 ym[e] = raw_m(e < 4 ? cur.m.x : cur.m.y, e & 3);
                 yv[e] = raw_v(e < 4 ? cur.v.x : cur.v.y, e & 3);
             }
@@ -1081,7 +1083,8 @@ int check_tensor(const zero_tensor_t& t, const zero_tensor_t* other, Op op)
     return ZERO_OK;
 }
 
-/* Every array of the operator allows 128-bit accesses of 8 elements from element h on. */
+/* Every array of the operator allows one access per 8 elements from element h on: fp32 at
+ * 32 bytes, 16-bit arrays at 16, codes at 8. */
 bool vector_from(const zero_tensor_t& t, const zero_tensor_t* other, Op op, uint32_t h)
 {
     auto ok = [h](const void* p, uintptr_t size, uintptr_t align) {
@@ -1089,10 +1092,11 @@ bool vector_from(const zero_tensor_t& t, const zero_tensor_t* other, Op op, uint
     };
     if (op == Op::kRead || op == Op::kWrite) {
         const uintptr_t size = other->state_dtype == ZERO_BF16 ? 2 : 4;
-        return ok(t.m, 1, 8) && ok(t.v, 1, 8) && ok(other->m, size, 16) && ok(other->v, size, 16);
+        return ok(t.m, 1, 8) && ok(t.v, 1, 8) && ok(other->m, size, size * 8) && ok(other->v, size, size * 8);
     }
-    const bool rest = ok(t.grad, t.grad_dtype == ZERO_F32 ? 4 : 2, 16) && ok(t.master, 4, 16) && ok(t.params, 2, 16);
-    return op == Op::kAdamw ? rest && ok(t.m, 4, 16) && ok(t.v, 4, 16) : rest && ok(t.m, 1, 8) && ok(t.v, 1, 8);
+    const uintptr_t size = t.grad_dtype == ZERO_F32 ? 4 : 2;
+    const bool rest = ok(t.grad, size, size * 8) && ok(t.master, 4, 32) && ok(t.params, 2, 16);
+    return op == Op::kAdamw ? rest && ok(t.m, 4, 32) && ok(t.v, 4, 32) : rest && ok(t.m, 1, 8) && ok(t.v, 1, 8);
 }
 
 /* Fills `l` with tensors from index `next` on, as many as fit; returns the next index. */
