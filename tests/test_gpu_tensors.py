@@ -502,6 +502,67 @@ def test_adamw8_repeats_and_its_seed_and_step_matter():
 
 
 # ------------------------------------------------------------------------------------------
+# lists long enough for the staged form
+# ------------------------------------------------------------------------------------------
+LONG = EDGES + [2_200_003, 4095, 4097, 8200, 12_288, 1]
+
+
+@pytest.mark.parametrize("shifts", [(0,), (1,), (3, 0, 8, 5)])
+@pytest.mark.parametrize("grads", [("bf16",), ("f16",), ("f32", "bf16", "f16")])
+@pytest.mark.parametrize("state", ["f32", "u8"])
+def test_adamw_on_long_lists(state, grads, shifts):
+    """The same checks, over two calls, on a list of 2.3 million elements."""
+    c = Case(LONG, grads, shifts, state, ("bf16", "f16"), (1.0, 0.5, 0.0), (0.01, 0.0))
+    c.set(**STEP)
+    for seed in (1, 2):
+        before = c.arrays()
+        if state == "u8":
+            z.zero_tensors_adamw8(c.list, c.hp, seed, c.st)
+            c.arena.check()
+            check8(c, before, STEP, seed)
+        else:
+            z.zero_tensors_adamw(c.list, c.hp, c.st)
+            c.arena.check()
+            after = c.arrays()
+            for k in range(len(LONG)):
+                m1, v1, p1, tm, tv, tp = expected(c, before, k, c.hp, STEP, before["m"][k], before["v"][k])
+                assert np.all(np.abs(after["m"][k] - m1) <= tm) and np.all(np.abs(after["v"][k] - v1) <= tv)
+                assert np.all(np.abs(after["master"][k] - p1) <= tp)
+                rounded = torch.from_numpy(after["master"][k]).to(c.params[k].dtype).float().numpy()
+                assert np.array_equal(after["params"][k], rounded)
+        s = c.state()
+        assert (s.adamw_next_chunk, s.adamw_done, s.error) == (0, 0, 0)
+
+
+@pytest.mark.parametrize("state", ["f32", "u8"])
+def test_long_lists_of_several_launches(state):
+    """900 tensors, 3 million elements: the blocks and the queue go on over the launches; a
+    skipped step leaves everything."""
+    sizes = [1 + (k * 7919) % 6700 for k in range(900)]
+    c = Case(sizes, ("f32", "bf16"), (0, 0, 1), state)
+    c.set(**STEP)
+    before = c.arrays()
+    call = z.zero_tensors_adamw if state == "f32" else lambda *a: z.zero_tensors_adamw8(a[0], a[1], 99, a[2])
+    c.set(skip=1)
+    call(c.list, c.hp, c.st)
+    for k, xs in c.arrays().items():
+        assert all(np.array_equal(a, b) for a, b in zip(xs, before[k])), k
+    c.set(skip=0)
+    call(c.list, c.hp, c.st)
+    c.arena.check()
+    if state == "u8":
+        check8(c, before, STEP, 99)
+    else:
+        after = c.arrays()
+        for k in range(len(sizes)):
+            m1, v1, p1, tm, tv, tp = expected(c, before, k, c.hp, STEP, before["m"][k], before["v"][k])
+            assert np.all(np.abs(after["m"][k] - m1) <= tm) and np.all(np.abs(after["v"][k] - v1) <= tv)
+            assert np.all(np.abs(after["master"][k] - p1) <= tp)
+    s = c.state()
+    assert (s.adamw_next_chunk, s.adamw_done, s.error) == (0, 0, 0)
+
+
+# ------------------------------------------------------------------------------------------
 # the 8-bit states read and written
 # ------------------------------------------------------------------------------------------
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

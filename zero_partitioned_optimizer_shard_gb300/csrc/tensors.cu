@@ -712,10 +712,17 @@ __device__ __forceinline__ void block8(const float (&x)[8], float (&p)[8], float
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         const uint64_t gc = f2_mul(c2, f2_mul(f2(x[e], x[e + 1]), inv2));
-        const uint64_t m2 = f2_add(f2_mul(f2(ym[e], ym[e + 1]), fm2), f2_mul(o1, gc));
-        const uint64_t v2 = f2_add(f2_mul(f2(yv[e], yv[e + 1]), fv2), f2_mul(o2, f2_mul(gc, gc)));
-        f2_split(m2, m[e], m[e + 1]);
-        f2_split(v2, v[e], v[e + 1]);
+        // the sums are scalar: a paired sum of paired products came out contracted (one
+        // product unrounded), 1 ulp off the definition where a code's boundary showed it
+        float a0, a1, b0, b1;
+        f2_split(f2_mul(f2(ym[e], ym[e + 1]), fm2), a0, a1);
+        f2_split(f2_mul(o1, gc), b0, b1);
+        m[e] = __fadd_rn(a0, b0);
+        m[e + 1] = __fadd_rn(a1, b1);
+        f2_split(f2_mul(f2(yv[e], yv[e + 1]), fv2), a0, a1);
+        f2_split(f2_mul(o2, f2_mul(gc, gc)), b0, b1);
+        v[e] = __fadd_rn(a0, b0);
+        v[e + 1] = __fadd_rn(a1, b1);
         top_m = max_abs(max_abs(top_m, m[e]), m[e + 1]);
         top_v = max_abs(max_abs(top_v, v[e]), v[e + 1]);
     }
@@ -883,6 +890,337 @@ __global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_con
         }
         if (!more)
             break;
+    }
+}
+
+/* ------------------------------------------------------------------------------------ */
+/* AdamW on long lists: staged through shared memory                                      */
+/* ------------------------------------------------------------------------------------ */
+
+/* One block per SM: a producer warp fills a ring of stages with the bulk-copy engine, 16
+ * consumer warps take a 256-element unit each from every stage, release it as soon as its
+ * values are in registers, and store their results straight to global memory.  A stage is
+ * a chunk of at most 4096 elements of one tensor. */
+constexpr int kRingWarps = 16;
+constexpr int kRingThreads = (kRingWarps + 1) * 32;
+constexpr uint32_t kRingChunk = kRingWarps * kUnit;
+constexpr uint32_t kNoTensor = ~0u;
+
+/* A stage's slots (each 128 bytes longer than a chunk's data: an array that does not start
+ * on 16 bytes keeps its offset from the boundary below). */
+template <bool S8>
+struct Ring {
+    static constexpr uint32_t kWide = kRingChunk * 4 + 128, kState = kRingChunk * (S8 ? 1 : 4) + 128;
+    static constexpr uint32_t kGrad = 0, kMaster = kWide, kM = 2 * kWide, kV = kM + kState, kExps = kV + kState;
+    static constexpr uint32_t kBytes = kExps + (S8 ? 256 : 0);
+    static constexpr int kStages = S8 ? 5 : 3;
+    static constexpr uint32_t kSmem = kBytes * kStages;
+};
+static_assert(Ring<false>::kSmem <= 220 * 1024 && Ring<true>::kSmem <= 220 * 1024, "shared memory");
+
+struct StageInfo {
+    uint32_t k, chunk;  // the tensor (kNoTensor: the queue is empty) and the chunk's number in it
+};
+
+/* The producer warp's copy of bytes [at, at + len) of an array of `bytes` bytes into a
+ * slot, at the same offset from a 16-byte boundary.  Whole 16-byte granules go by bulk
+ * copy, over the chunk's ends where the array goes on there; the granules that the array's
+ * own ends cut are filled byte by byte, so nothing outside the array is read.  Returns the
+ * bulk copy's span in lo, hi (for expect_tx, before bulk()). */
+struct SlotCopy {
+    const char* from;
+    uint32_t dst, len;
+
+    __device__ __forceinline__ SlotCopy(const void* base, uint64_t bytes, uint64_t at, uint32_t n, char* slot,
+                                        uint32_t lane)
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(base), first = a + at, end = first + n;
+        const uintptr_t origin = first & ~(uintptr_t)15;
+        uintptr_t lo = origin, hi = (end + 15) & ~(uintptr_t)15;
+        if (lo < a || hi > a + bytes) {
+            const uintptr_t stop = a + bytes < end ? a + bytes : end;
+            if (lo < a)
+                lo += 16;
+            if (hi > a + bytes)
+                hi -= 16;
+            if (hi < lo)
+                hi = lo;  // one granule cut at both ends: all of it byte by byte
+            // at most 15 bytes before lo and 15 from hi on (16 to `stop` when lo == hi)
+            const uintptr_t x = lane < 16 ? first + lane : hi + (lane - 16);
+            if (lane < 16 ? x < lo && x < stop : x < stop)
+                slot[x - origin] = *reinterpret_cast<const char*>(x);
+        }
+        from = reinterpret_cast<const char*>(lo);
+        dst = smem_addr(slot) + (uint32_t)(lo - origin);
+        len = (uint32_t)(hi - lo);
+    }
+    __device__ __forceinline__ void bulk(uint32_t bar) const
+    {
+        if (len)
+            bulk_load<true>(dst, from, len, bar);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ const char* in_slot(const char* slot, const T* base, uint64_t at)
+{
+    return slot + (((uintptr_t)base + at) & 15u);
+}
+
+template <bool S8, int CAP>
+__global__ void __launch_bounds__(kRingThreads, 1) k_tensors_ring(const __grid_constant__ AdamwList<CAP> a)
+{
+    using R = Ring<S8>;
+    extern __shared__ __align__(128) char stages[];
+    __shared__ __align__(8) uint64_t full[R::kStages], empty[R::kStages];
+    __shared__ StageInfo info[R::kStages];
+    grid_dependency_wait();
+    zero_step_state_t* st = const_cast<zero_step_state_t*>(a.st);
+    if (st->skip)
+        return;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < R::kStages; ++k) {
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[k])));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[k])), "n"(kRingWarps));
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (warp == kRingWarps) {  // the producer
+        unsigned long long* queue = reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk);
+        unsigned long long next = 0;
+        if (lane == 0)
+            next = atomicAdd(queue, 1ull);
+        Place at{0, 1, 0, 0};
+        uint32_t issued = 0, live = R::kStages - 1;  // stages before `issued` that may be unread
+        for (;; ++issued) {
+            const uint32_t k = issued % R::kStages;
+            if (issued >= (uint32_t)R::kStages &&
+                !wait_parity_bounded(smem_addr(&empty[k]), (issued / R::kStages - 1) & 1)) {
+                if (lane == 0)
+                    atomicOr(&st->error, 1u);
+                live = R::kStages;
+                break;
+            }
+            const unsigned long long c = __shfl_sync(0xffffffffu, next, 0);
+            const uint32_t bar = smem_addr(&full[k]);
+            if (c >= a.l.n_units) {
+                if (lane == 0) {
+                    info[k].k = kNoTensor;
+                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+                }
+                break;
+            }
+            if (lane == 0)
+                next = atomicAdd(queue, 1ull);  // one ahead: its latency stays off the ring's path
+            locate(a.l, (uint32_t)c, at);
+            const Ref& t = a.l.t[at.k];
+            char* s = stages + k * R::kBytes;
+            const uint64_t first = (uint64_t)at.unit * kRingChunk;
+            const uint32_t n = t.elems - first < kRingChunk ? (uint32_t)(t.elems - first) : kRingChunk;
+            const uint32_t gs = (t.flags & kGradMask) == ZERO_F32 ? 4 : 2, ss = S8 ? 1 : 4;
+            const SlotCopy g(t.grad, t.elems * gs, first * gs, n * gs, s + R::kGrad, lane);
+            const SlotCopy p(t.master, t.elems * 4, first * 4, n * 4, s + R::kMaster, lane);
+            const SlotCopy m(t.m, t.elems * ss, first * ss, n * ss, s + R::kM, lane);
+            const SlotCopy v(t.v, t.elems * ss, first * ss, n * ss, s + R::kV, lane);
+            uint32_t bytes = g.len + p.len + m.len + v.len;
+            SlotCopy b = m;
+            if (S8) {
+                b = SlotCopy(t.exps, (t.elems + kUnit - 1) / kUnit * 2, first / kUnit * 2, (n + kUnit - 1) / kUnit * 2,
+                             s + R::kExps, lane);
+                bytes += b.len;
+            }
+            // the bytes the lanes wrote come before the arrival, and before any later bulk
+            // copy into the same slot
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                info[k] = StageInfo{at.k, at.unit};
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+                g.bulk(bar);
+                p.bulk(bar);
+                m.bulk(bar);
+                v.bulk(bar);
+                if (S8)
+                    b.bulk(bar);
+            }
+        }
+        // every copy has landed before the block may end (a consumer that gave up leaves
+        // stages unread)
+        for (uint32_t i = issued > live ? issued - live : 0; i < issued; ++i)
+            wait_parity_bounded(smem_addr(&full[i % R::kStages]), (i / R::kStages) & 1);
+        if (lane == 0) {  // the queue back to 0 for the next launch, by the last block
+            __threadfence();
+            if (atomicAdd(&st->adamw_done, 1u) == gridDim.x - 1) {
+                __threadfence();
+                atomicExch(queue, 0ull);
+                atomicExch(&st->adamw_done, 0u);
+            }
+        }
+        return;
+    }
+
+    Step8 s8;
+    Scalars s = step_scalars(a);
+    const float inv = st->inv_scale_used, step = s.step;
+    if (S8) {
+        s8.inv = inv;
+        s8.c = s.c;
+        s8.b1 = s.b1;
+        s8.b2 = s.b2;
+        s8.omb1 = s.omb1;
+        s8.omb2 = s.omb2;
+        s8.eps = s.eps;
+        s8.inv_rbc2 = __fdiv_rn(1.0f, s.rbc2);
+        s8.key = step_key(a.seed, st->t);
+        s8.exact = a.eps < 0x1p-100f;
+    }
+    for (uint32_t i = 0;; ++i) {
+        const uint32_t q = i % R::kStages, bar = smem_addr(&empty[q]);
+        if (!wait_parity_bounded(smem_addr(&full[q]), (i / R::kStages) & 1)) {
+            if (lane == 0)
+                atomicOr(&st->error, 1u);
+            return;
+        }
+        const StageInfo where = info[q];
+        if (where.k == kNoTensor)
+            return;
+        const Ref& t = a.l.t[where.k];
+        const char* slot = stages + q * R::kBytes;
+        const uint64_t first = (uint64_t)where.chunk * kRingChunk;  // the stage's first element
+        const uint64_t off = first + warp * kUnit;                  // this warp's
+        auto release = [&] {
+            __syncwarp();
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+        };
+        if (off >= t.elems) {
+            release();
+            continue;
+        }
+        const uint32_t dtype = t.flags & kGradMask, gs = dtype == ZERO_F32 ? 4 : 2;
+        const bool whole = (t.flags & kVector) && off + kUnit <= t.elems;
+        // this lane's elements: 8 consecutive ones, or one of every 32
+        const uint32_t e0 = warp * kUnit + (whole ? lane * kPer : lane), apart = whole ? 1 : 32;
+        const char* g = in_slot(slot + R::kGrad, static_cast<const char*>(t.grad), first * gs) + e0 * gs;
+        const float* pm = reinterpret_cast<const float*>(in_slot(slot + R::kMaster, t.master, first * 4)) + e0;
+        float x[8], p[8];
+        auto read = [&](const float* from, float (&to)[8]) {
+            if (whole) {
+                const float4 lo = reinterpret_cast<const float4*>(from)[0], hi = reinterpret_cast<const float4*>(from)[1];
+                to[0] = lo.x, to[1] = lo.y, to[2] = lo.z, to[3] = lo.w;
+                to[4] = hi.x, to[5] = hi.y, to[6] = hi.z, to[7] = hi.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    to[e] = from[e * 32];
+            }
+        };
+        if (dtype == ZERO_F32) {
+            read(reinterpret_cast<const float*>(g), x);
+        } else if (whole) {
+            const uint4 w = *reinterpret_cast<const uint4*>(g);
+            if (dtype == ZERO_F16)
+                widen8<ZERO_F16>(w, x);
+            else
+                widen8<ZERO_BF16>(w, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint16_t w = reinterpret_cast<const uint16_t*>(g)[e * 32];
+                x[e] = dtype == ZERO_F16 ? one16<ZERO_F16>(w) : one16<ZERO_BF16>(w);
+            }
+        }
+        read(pm, p);
+        const uint64_t at = first + e0;  // this lane's first element
+        if (S8) {
+            s8.step = __fmul_rn(step, t.lr_scale);
+            s8.decay = t.decay;
+            const char* cm_at = in_slot(slot + R::kM, static_cast<const char*>(t.m), first) + e0;
+            const char* cv_at = in_slot(slot + R::kV, static_cast<const char*>(t.v), first) + e0;
+            const uint8_t* b = reinterpret_cast<const uint8_t*>(
+                                   in_slot(slot + R::kExps, t.exps, first / kUnit * 2)) + 2 * warp;
+            uint32_t bm = b[0], bv = b[1];
+            float ym[8], yv[8];
+            const uint32_t unit = (uint32_t)(off / kUnit);
+            const uint32_t seed = mix32(s8.key + (t.group0 + unit * 32 + lane) * kGolden);
+            uint2 cm, cv;
+            uint8_t* m = static_cast<uint8_t*>(t.m) + at;
+            uint8_t* v = static_cast<uint8_t*>(t.v) + at;
+            if (whole) {
+                cm = *reinterpret_cast<const uint2*>(cm_at);
+                cv = *reinterpret_cast<const uint2*>(cv_at);
+                release();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ym[e] = raw_m(e < 4 ? cm.x : cm.y, e & 3);
+                    yv[e] = raw_v(e < 4 ? cv.x : cv.y, e & 3);
+                }
+                block8(x, p, ym, yv, bm, bv, RandomInGroup{seed}, cm, cv, s8);
+                __stcs(reinterpret_cast<uint2*>(m), cm);
+                __stcs(reinterpret_cast<uint2*>(v), cv);
+            } else {
+                // what lies past the tensor's end must not count in the block's exponents
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = at + e * 32 < t.elems;
+                    x[e] = in ? x[e] : 0.0f;
+                    p[e] = in ? p[e] : 0.0f;
+                    ym[e] = in ? raw_m((uint8_t)cm_at[e * 32], 0) : 0.0f;
+                    yv[e] = in ? raw_v((uint8_t)cv_at[e * 32], 0) : 0.0f;
+                }
+                release();
+                block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (at + e * 32 < t.elems) {
+                        m[e * 32] = (uint8_t)((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
+                        v[e * 32] = (uint8_t)((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
+                    }
+            }
+            if (lane == 0) {
+                t.exps[off / kUnit * 2] = (uint8_t)bm;
+                t.exps[off / kUnit * 2 + 1] = (uint8_t)bv;
+            }
+        } else {
+            float mm[8], vv[8];
+            read(reinterpret_cast<const float*>(in_slot(slot + R::kM, static_cast<const char*>(t.m), first * 4)) + e0, mm);
+            read(reinterpret_cast<const float*>(in_slot(slot + R::kV, static_cast<const char*>(t.v), first * 4)) + e0, vv);
+            release();
+            s.step = __fmul_rn(step, t.lr_scale);
+            s.decay = t.decay;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                adamw_one(__fmul_rn(x[e], inv), p[e], mm[e], vv[e], s);
+            float* m = static_cast<float*>(t.m) + at;
+            float* v = static_cast<float*>(t.v) + at;
+            if (whole) {
+                store8(m, mm);
+                store8(v, vv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (at + e * 32 < t.elems) {
+                        __stcs(m + e * 32, mm[e]);
+                        __stcs(v + e * 32, vv[e]);
+                    }
+            }
+        }
+        if (whole) {
+            store8(t.master + at, p);
+            if (t.params)
+                store_params8(t.params + at, t.flags & kOutF16, p);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e * apart < t.elems) {
+                    __stcs(t.master + at + e * 32, p[e]);
+                    if (t.params)
+                        t.params[at + e * 32] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
+                }
+        }
     }
 }
 
@@ -1101,7 +1439,7 @@ bool vector_from(const zero_tensor_t& t, const zero_tensor_t* other, Op op, uint
 
 /* Fills `l` with tensors from index `next` on, as many as fit; returns the next index. */
 uint64_t fill(List<kLarge>& l, const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
-              uint64_t next, Op op, const zero_adamw_hparams_t* hp, uint32_t& group0)
+              uint64_t next, Op op, const zero_adamw_hparams_t* hp, uint32_t& group0, uint32_t unit = kUnit)
 {
     uint64_t units = 0;
     l.n = 0;
@@ -1113,14 +1451,14 @@ uint64_t fill(List<kLarge>& l, const zero_tensor_t* tensors, const zero_tensor_t
         // 32-bit states: an offset that all arrays share (pieces of flat buffers) is stepped
         // over; 8-bit states: their blocks start at element 0
         uint32_t head = 0;
-        if (op == Op::kAdamw)
+        if (op == Op::kAdamw && unit == kUnit)
             while (head < 8 && !vector_from(t, other, op, head))
                 ++head;
         const bool vec = head < 8 && vector_from(t, other, op, head);
         if (!vec)
             head = 0;
         const uint64_t body = t.elems > head ? t.elems - head : 1;
-        const uint64_t c = (body + kUnit - 1) / kUnit;
+        const uint64_t c = (body + unit - 1) / unit;
         if (units + c > 0xf0000000ull)
             break;  // unit counters are 32-bit; check_tensor bounds one tensor's units
         Ref& r = l.t[l.n];
@@ -1232,10 +1570,41 @@ int launch_units(void (*kernel)(Args), std::atomic<int> (&per_sm)[64], uint32_t 
     return status_of(launch_pdl(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kThreads), 0, s, a));
 }
 
+/* The staged form: one block per SM. */
+template <typename Args>
+int launch_ring(void (*kernel)(Args), std::atomic<bool> (&configured)[64], uint32_t smem, uint32_t chunks,
+                cudaStream_t s, const Args& a)
+{
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (!configured[dev & 63].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return status_of(e);
+        configured[dev & 63].store(true, std::memory_order_relaxed);
+    }
+    const uint32_t cap = (uint32_t)sm_count();
+    return status_of(launch_pdl(kernel, dim3(chunks < cap ? chunks : cap), dim3(kRingThreads), smem, s, a));
+}
+
+template <int CAP>
+int launch_adamw_list(const AdamwList<CAP>& a, Op op, bool ring, cudaStream_t s)
+{
+    static std::atomic<int> occ[2][64];  // per device; a race only repeats the set-up
+    static std::atomic<bool> configured[2][64];
+    const bool s8 = op == Op::kAdamw8;
+    if (ring)
+        return s8 ? launch_ring(k_tensors_ring<true, CAP>, configured[1], Ring<true>::kSmem, a.l.n_units, s, a)
+                  : launch_ring(k_tensors_ring<false, CAP>, configured[0], Ring<false>::kSmem, a.l.n_units, s, a);
+    return s8 ? launch_units(k_tensors_adamw8<CAP>, occ[1], a.l.n_units, s, a)
+              : launch_units(k_tensors_adamw<CAP>, occ[0], a.l.n_units, s, a);
+}
+
+constexpr uint64_t kRingElems = 1u << 21;
+
 int run_adamw(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparams_t* hp, uint64_t seed,
               const zero_step_state_t* st, cudaStream_t s, Op op)
 {
-    static std::atomic<int> occ[4][64];
     AdamwList<kLarge> a;
     AdamwList<kSmall> b;
     a.st = b.st = st;
@@ -1243,19 +1612,21 @@ int run_adamw(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparams
     a.beta1 = b.beta1 = hp->beta1;
     a.beta2 = b.beta2 = hp->beta2;
     a.eps = b.eps = hp->eps;
+    uint64_t total = 0;
+    for (uint64_t k = 0; k < n; ++k)
+        total += tensors[k].elems;
+    const bool ring = total >= kRingElems;
     uint32_t group0 = 0;
     for (uint64_t next = 0; next < n;) {
-        next = fill(a.l, tensors, nullptr, n, next, op, hp, group0);
+        next = fill(a.l, tensors, nullptr, n, next, op, hp, group0, ring ? kRingChunk : kUnit);
         if (a.l.n == 0)
             continue;
         int rc;
         if (a.l.n <= (uint32_t)kSmall) {
             shrink(a.l, b.l);
-            rc = op == Op::kAdamw ? launch_units(k_tensors_adamw<kSmall>, occ[0], b.l.n_units, s, b)
-                                  : launch_units(k_tensors_adamw8<kSmall>, occ[1], b.l.n_units, s, b);
+            rc = launch_adamw_list(b, op, ring, s);
         } else {
-            rc = op == Op::kAdamw ? launch_units(k_tensors_adamw<kLarge>, occ[2], a.l.n_units, s, a)
-                                  : launch_units(k_tensors_adamw8<kLarge>, occ[3], a.l.n_units, s, a);
+            rc = launch_adamw_list(a, op, ring, s);
         }
         if (rc != ZERO_OK)
             return rc;
