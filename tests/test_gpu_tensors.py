@@ -565,20 +565,21 @@ def test_long_lists_of_several_launches(state):
 # ------------------------------------------------------------------------------------------
 # the 8-bit states read and written
 # ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("sizes", [EDGES, LONG], ids=["short", "long"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("shifts", [(0,), (1,), (3, 0, 8, 5)])
-def test_write_and_read(shifts, dtype):
-    c = Case(EDGES, state="u8", shifts=shifts)
+def test_write_and_read(shifts, dtype, sizes):
+    c = Case(sizes, state="u8", shifts=shifts)
     a = Arena()
     src = [[a.put(rand(n, 40 + k, 1e-3 * 10.0 ** (k % 7 - 3), square=sq), shifts[k % len(shifts)])
-            for k, n in enumerate(EDGES)] for sq in (False, True)]
-    out = [[a.put(torch.zeros(n, dtype=dtype), shifts[k % len(shifts)]) for k, n in enumerate(EDGES)] for _ in "mv"]
+            for k, n in enumerate(sizes)] for sq in (False, True)]
+    out = [[a.put(torch.zeros(n, dtype=dtype), shifts[k % len(shifts)]) for k, n in enumerate(sizes)] for _ in "mv"]
     z.zero_tensors_state8_write(c.list, z.TensorList(m=src[0], v=src[1]))
     z.zero_tensors_state8_read(c.list, z.TensorList(m=out[0], v=out[1]))
     c.arena.check()
     a.check()
     got = c.arrays()
-    for k, n in enumerate(EDGES):
+    for k, n in enumerate(sizes):
         for name, x, y, col in (("m", src[0][k], out[0][k], 0), ("v", src[1][k], out[1][k], 1)):
             x, y = host(x), host(y)
             codes, b = S.encode(x, name, S.NEAREST)

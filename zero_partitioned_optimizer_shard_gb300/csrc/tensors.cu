@@ -24,6 +24,8 @@
 namespace zero {
 namespace {
 
+enum class Op { kNorm, kAdamw, kAdamw8, kRead, kWrite };
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 8;                              // elements per lane and unit
@@ -71,13 +73,13 @@ struct List {
 };
 
 template <int CAP>
-struct AdamwList {
+struct ListArgs {
     const zero_step_state_t* st;
     uint64_t seed;
     float beta1, beta2, eps;
     List<CAP> l;
 };
-static_assert(sizeof(AdamwList<kLarge>) <= 32764, "kernel parameters");
+static_assert(sizeof(ListArgs<kLarge>) <= 32764, "kernel parameters");
 
 /* The tensor of unit u, by the whole warp: one count of the ends at or below u, its loads
  * all in flight at once.  They go through global addressing of the parameters: a binary
@@ -160,7 +162,7 @@ __device__ __forceinline__ void store_params8(uint16_t* p, uint32_t f16, const f
 }
 
 template <int CAP>
-__device__ __forceinline__ Scalars step_scalars(const AdamwList<CAP>& a)
+__device__ __forceinline__ Scalars step_scalars(const ListArgs<CAP>& a)
 {
     Scalars s;
     s.c = a.st->clip_coef;
@@ -505,16 +507,19 @@ struct RawGrad {
 };
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads) k_tensors_adamw(const __grid_constant__ AdamwList<CAP> a)
+__global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_constant__ ListArgs<CAP> a)
 {
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    Place at{0, 1, 0, 0};
+    if (u < a.l.n_units)
+        locate(a.l, u, at);  // the parameters are this launch's own: no need to wait
     grid_dependency_wait();
-    if (a.st->skip)
-        return;
+    grid_launch_dependents();
+    const bool skip = a.st->skip;
     Scalars s = step_scalars(a);
     const float inv = a.st->inv_scale_used, step = s.step;
-    const uint32_t lane = threadIdx.x & 31;
-    Place at{0, 1, 0, 0};
-    for (uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < a.l.n_units; u += gridDim.x * kWarps) {
+    for (; u < a.l.n_units; u += gridDim.x * kWarps) {
         locate(a.l, u, at);
         const Ref& t = a.l.t[at.k];
         const uint32_t dtype = t.flags & kGradMask;
@@ -547,6 +552,8 @@ __global__ void __launch_bounds__(kThreads) k_tensors_adamw(const __grid_constan
                 v8[e] = in ? __ldcs(v + q) : 0.0f;
             }
         }
+        if (skip)  // only now: the loads need not wait for the state's
+            return;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             adamw_one(__fmul_rn(x8[e], inv), p8[e], m8[e], v8[e], s);
@@ -602,25 +609,6 @@ __device__ __forceinline__ float rcp_fast(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-
-/* What a lane reads of its unit: 8 consecutive elements, and the block's exponents. */
-struct Pre8 {
-    RawGrad g;
-    float p[8];
-    uint2 m, v;
-    uint32_t bm, bv;
-
-    __device__ __forceinline__ void load(const Ref& t, uint32_t unit, uint32_t lane)
-    {
-        const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
-        g.load(t.grad, i, t.flags & kGradMask);
-        load8(t.master + i, p);
-        m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
-        v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
-        bm = t.exps[2 * (uint64_t)unit];
-        bv = t.exps[2 * (uint64_t)unit + 1];
-    }
-};
 
 /* Four codes of a word as floats with the code's exponent in fp32's field. */
 __device__ __forceinline__ float raw_m(uint32_t w, int byte)
@@ -792,15 +780,14 @@ __device__ __forceinline__ bool whole_unit(const Ref& t, uint32_t unit)
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_constant__ AdamwList<CAP> a)
+__device__ __forceinline__ Step8 step8(const ListArgs<CAP>& a)
 {
-    grid_dependency_wait();
     const zero_step_state_t* st = a.st;
-    if (st->skip)
-        return;
     Step8 s;
     s.inv = st->inv_scale_used;
     s.c = st->clip_coef;
+    s.step = st->step_size;
+    s.decay = 1.0f;
     s.b1 = a.beta1;
     s.b2 = a.beta2;
     s.omb1 = __fsub_rn(1.0f, a.beta1);
@@ -809,92 +796,219 @@ __global__ void __launch_bounds__(kThreads, 3) k_tensors_adamw8(const __grid_con
     s.inv_rbc2 = __fdiv_rn(1.0f, st->rbc2);
     s.key = step_key(a.seed, st->t);
     s.exact = a.eps < 0x1p-100f;
-    const float step = st->step_size;
-    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps, n = a.l.n_units;
+    return s;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw8(const __grid_constant__ ListArgs<CAP> a)
+{
+    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
     uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (u >= n)
-        return;
     Place at{0, 1, 0, 0};
-    Pre8 pre;
-    locate(a.l, u, at);
-    if (whole_unit(a.l.t[at.k], at.unit))
-        pre.load(a.l.t[at.k], at.unit, lane);
-    for (;;) {
-        const uint32_t k = at.k, unit = at.unit;
-        const Pre8 cur = pre;
-        u += stride;
-        const bool more = u < n;
-        if (more) {  // the next unit's loads go out before this one's arithmetic
-            locate(a.l, u, at);
-            if (whole_unit(a.l.t[at.k], at.unit))
-                pre.load(a.l.t[at.k], at.unit, lane);
-        }
-        const Ref& t = a.l.t[k];
+    if (u < a.l.n_units)
+        locate(a.l, u, at);  // the parameters are this launch's own: no need to wait
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const bool skip = a.st->skip;
+    Step8 s = step8(a);
+    const float step = s.step;
+    for (; u < a.l.n_units; u += stride) {
+        locate(a.l, u, at);
+        const Ref& t = a.l.t[at.k];
+        const uint32_t dtype = t.flags & kGradMask, unit = at.unit;
         s.step = __fmul_rn(step, t.lr_scale);
         s.decay = t.decay;
-        const uint32_t dtype = t.flags & kGradMask;
-        uint8_t* m = static_cast<uint8_t*>(t.m);
-        uint8_t* v = static_cast<uint8_t*>(t.v);
         const bool whole = whole_unit(t, unit);
+        // consecutive elements per lane, else lanes side by side
+        const uint64_t i = (uint64_t)unit * kUnit + (whole ? lane * kPer : lane);
+        uint8_t* m = static_cast<uint8_t*>(t.m) + i;
+        uint8_t* v = static_cast<uint8_t*>(t.v) + i;
+        uint8_t* exps = t.exps + 2 * (uint64_t)unit;
+        uint32_t bm = exps[0], bv = exps[1];
         // lane L's seed is that of the block's group L
         const uint32_t seed = mix32(s.key + (t.group0 + unit * 32 + lane) * kGolden);
-        uint32_t bm, bv;
         uint2 cm, cv;
         float x[8], p[8], ym[8], yv[8];
         if (whole) {
-            const uint64_t i = (uint64_t)unit * kUnit + lane * kPer;
-            cur.g.values(dtype, x);
-            bm = cur.bm;
-            bv = cur.bv;
+            RawGrad raw;
+            raw.load(t.grad, i, dtype);
+            load8(t.master + i, p);
+            cm = __ldcs(reinterpret_cast<const uint2*>(m));
+            cv = __ldcs(reinterpret_cast<const uint2*>(v));
+            raw.values(dtype, x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                p[e] = cur.p[e];
-                ym[e] = raw_m(e < 4 ? cur.m.x : cur.m.y, e & 3);
-                yv[e] = raw_v(e < 4 ? cur.v.x : cur.v.y, e & 3);
+                ym[e] = raw_m(e < 4 ? cm.x : cm.y, e & 3);
+                yv[e] = raw_v(e < 4 ? cv.x : cv.y, e & 3);
             }
+            if (skip)
+                return;
             block8(x, p, ym, yv, bm, bv, RandomInGroup{seed}, cm, cv, s);
             store8(t.master + i, p);
             if (t.params)
                 store_params8(t.params + i, t.flags & kOutF16, p);
-            __stcs(reinterpret_cast<uint2*>(m + i), cm);
-            __stcs(reinterpret_cast<uint2*>(v + i), cv);
+            __stcs(reinterpret_cast<uint2*>(m), cm);
+            __stcs(reinterpret_cast<uint2*>(v), cv);
         } else {
-            const uint64_t i = (uint64_t)unit * kUnit + lane;
-            bm = t.exps[2 * (uint64_t)unit];
-            bv = t.exps[2 * (uint64_t)unit + 1];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint64_t q = i + e * 32;
-                const bool in = q < t.elems;
-                x[e] = in ? one_grad(t.grad, q, dtype) : 0.0f;
-                p[e] = in ? __ldcs(t.master + q) : 0.0f;
-                ym[e] = in ? raw_m(m[q], 0) : 0.0f;
-                yv[e] = in ? raw_v(v[q], 0) : 0.0f;
+                const bool in = i + e * 32 < t.elems;
+                x[e] = in ? one_grad(t.grad, i + e * 32, dtype) : 0.0f;
+                p[e] = in ? __ldcs(t.master + i + e * 32) : 0.0f;
+                ym[e] = in ? raw_m(m[e * 32], 0) : 0.0f;
+                yv[e] = in ? raw_v(v[e * 32], 0) : 0.0f;
             }
+            if (skip)
+                return;
             block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint64_t q = i + e * 32;
-                if (q < t.elems) {
-                    m[q] = (uint8_t)((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
-                    v[q] = (uint8_t)((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
-                    __stcs(t.master + q, p[e]);
+                if (i + e * 32 < t.elems) {
+                    m[e * 32] = (uint8_t)((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
+                    v[e * 32] = (uint8_t)((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
+                    __stcs(t.master + i + e * 32, p[e]);
                     if (t.params)
-                        t.params[q] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
+                        t.params[i + e * 32] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
                 }
             }
         }
         if (lane == 0) {
-            t.exps[2 * (uint64_t)unit] = (uint8_t)bm;
-            t.exps[2 * (uint64_t)unit + 1] = (uint8_t)bv;
+            exps[0] = (uint8_t)bm;
+            exps[1] = (uint8_t)bv;
         }
-        if (!more)
-            break;
     }
 }
 
 /* ------------------------------------------------------------------------------------ */
-/* AdamW on long lists: staged through shared memory                                      */
+/* 8-bit states to values and back                                                        */
+/* ------------------------------------------------------------------------------------ */
+
+/* Codes as floats (raw_m, raw_v) to their values. */
+__device__ __forceinline__ void scale_values(float (&m)[8], float (&v)[8], float scale_m, float scale_v)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        m[e] = __fmul_rn(__fmul_rn(m[e], 0x1p112f), scale_m);
+        v[e] = __fmul_rn(__fmul_rn(v[e], 0x1p96f), scale_v);
+    }
+}
+
+/* A block's values, 8 per lane, to their nearest codes; the exponents (m's, v's). */
+__device__ __forceinline__ uint2 nearest_codes(const float (&m)[8], const float (&v)[8], uint2& cm, uint2& cv)
+{
+    uint32_t top_m = 0, top_v = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        top_m = max(top_m, __float_as_uint(m[e]) & 0x7fffffffu);
+        top_v = max(top_v, __float_as_uint(v[e]) & 0x7fffffffu);
+    }
+    const uint32_t bm = block_exponent(__reduce_max_sync(0xffffffffu, top_m));
+    const uint32_t bv = block_exponent(__reduce_max_sync(0xffffffffu, top_v));
+    const float um = exp_unscale(bm), uv = exp_unscale(bv);
+    uint32_t wm[2] = {0, 0}, wv[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        wm[e / 4] |= encode_m(m[e], um, kNearest) << (8 * (e & 3));
+        wv[e / 4] |= encode_v(v[e], uv, kNearest) << (8 * (e & 3));
+    }
+    cm = make_uint2(wm[0], wm[1]);
+    cv = make_uint2(wv[0], wv[1]);
+    return make_uint2(bm, bv);
+}
+
+/* Short lists: a warp per unit, straight from global memory. */
+template <Op OP, int CAP>
+__global__ void __launch_bounds__(kThreads, 4) k_tensors_codec(const __grid_constant__ ListArgs<CAP> a)
+{
+    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
+    uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    Place place{0, 1, 0, 0};
+    if (u < a.l.n_units)
+        locate(a.l, u, place);  // the parameters are this launch's own: no need to wait
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (; u < a.l.n_units; u += stride) {
+        locate(a.l, u, place);
+        const Ref& t = a.l.t[place.k];
+        const bool whole = whole_unit(t, place.unit);
+        const uint64_t at = (uint64_t)place.unit * kUnit + (whole ? lane * kPer : lane);
+        uint8_t* exps = t.exps + 2 * (uint64_t)place.unit;
+        uint8_t* cm = static_cast<uint8_t*>(t.m) + at;
+        uint8_t* cv = static_cast<uint8_t*>(t.v) + at;
+        float m[8], v[8];
+        if (OP == Op::kRead) {
+            if (whole) {
+                const uint2 wm = __ldcs(reinterpret_cast<const uint2*>(cm)), wv = __ldcs(reinterpret_cast<const uint2*>(cv));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    m[e] = raw_m(e < 4 ? wm.x : wm.y, e & 3);
+                    v[e] = raw_v(e < 4 ? wv.x : wv.y, e & 3);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = at + e * 32 < t.elems;
+                    m[e] = in ? raw_m(cm[e * 32], 0) : 0.0f;
+                    v[e] = in ? raw_v(cv[e * 32], 0) : 0.0f;
+                }
+            }
+            scale_values(m, v, exp_scale(exps[0]), exp_scale(exps[1]));
+            const bool bf16 = t.flags & kValueBF16;
+            if (whole && bf16) {
+                store_params8(static_cast<uint16_t*>(t.x) + at, 0, m);
+                store_params8(static_cast<uint16_t*>(t.y) + at, 0, v);
+            } else if (whole) {
+                store8(static_cast<float*>(t.x) + at, m);
+                store8(static_cast<float*>(t.y) + at, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint64_t q = at + e * 32;
+                    if (q < t.elems && bf16) {
+                        static_cast<uint16_t*>(t.x)[q] = pack1<false>(m[e]);
+                        static_cast<uint16_t*>(t.y)[q] = pack1<false>(v[e]);
+                    } else if (q < t.elems) {
+                        static_cast<float*>(t.x)[q] = m[e];
+                        static_cast<float*>(t.y)[q] = v[e];
+                    }
+                }
+            }
+        } else {
+            const float* xm = static_cast<const float*>(t.x) + at;
+            const float* xv = static_cast<const float*>(t.y) + at;
+            if (whole) {
+                load8(xm, m);
+                load8(xv, v);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    m[e] = at + e * 32 < t.elems ? __ldcs(xm + e * 32) : 0.0f;
+                    v[e] = at + e * 32 < t.elems ? __ldcs(xv + e * 32) : 0.0f;
+                }
+            }
+            uint2 wm, wv;
+            const uint2 b = nearest_codes(m, v, wm, wv);
+            if (whole) {
+                __stcs(reinterpret_cast<uint2*>(cm), wm);
+                __stcs(reinterpret_cast<uint2*>(cv), wv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (at + e * 32 < t.elems) {
+                        cm[e * 32] = (uint8_t)((e < 4 ? wm.x : wm.y) >> (8 * (e & 3)));
+                        cv[e * 32] = (uint8_t)((e < 4 ? wv.x : wv.y) >> (8 * (e & 3)));
+                    }
+            }
+            if (lane == 0) {
+                exps[0] = (uint8_t)b.x;
+                exps[1] = (uint8_t)b.y;
+            }
+        }
+    }
+}
+
+/* ------------------------------------------------------------------------------------ */
+/* long lists: staged through shared memory                                               */
 /* ------------------------------------------------------------------------------------ */
 
 /* One block per SM: a producer warp fills a ring of stages with the bulk-copy engine, 16
@@ -906,17 +1020,20 @@ constexpr int kRingThreads = (kRingWarps + 1) * 32;
 constexpr uint32_t kRingChunk = kRingWarps * kUnit;
 constexpr uint32_t kNoTensor = ~0u;
 
-/* A stage's slots (each 128 bytes longer than a chunk's data: an array that does not start
- * on 16 bytes keeps its offset from the boundary below). */
-template <bool S8>
+/* What a stage holds, by operator: up to five arrays' parts of the chunk, each in a slot
+ * 128 bytes longer than its data (an array that does not start on 16 bytes keeps its
+ * offset from the boundary below).  As many stages as shared memory takes, 16 at most. */
+template <Op OP>
 struct Ring {
-    static constexpr uint32_t kWide = kRingChunk * 4 + 128, kState = kRingChunk * (S8 ? 1 : 4) + 128;
-    static constexpr uint32_t kGrad = 0, kMaster = kWide, kM = 2 * kWide, kV = kM + kState, kExps = kV + kState;
-    static constexpr uint32_t kBytes = kExps + (S8 ? 256 : 0);
-    static constexpr int kStages = S8 ? 5 : 3;
-    static constexpr uint32_t kSmem = kBytes * kStages;
+    static constexpr bool kStep = OP == Op::kAdamw || OP == Op::kAdamw8;
+    static constexpr uint32_t kWide = kRingChunk * 4 + 128, kState = (OP == Op::kAdamw8 || OP == Op::kRead ? 1 : 4) * kRingChunk + 128;
+    static constexpr uint32_t kGrad = 0, kMaster = kWide;          // AdamW only
+    static constexpr uint32_t kM = kStep ? 2 * kWide : 0, kV = kM + kState;
+    static constexpr uint32_t kExps = kV + kState;                 // codes read, only
+    static constexpr uint32_t kBytes = kExps + (OP == Op::kAdamw8 || OP == Op::kRead ? 256 : 0);
+    static constexpr uint32_t kFit = 216 * 1024 / kBytes;
+    static constexpr uint32_t kStages = kFit < 16 ? kFit : 16, kSmem = kBytes * kStages;
 };
-static_assert(Ring<false>::kSmem <= 220 * 1024 && Ring<true>::kSmem <= 220 * 1024, "shared memory");
 
 struct StageInfo {
     uint32_t k, chunk;  // the tensor (kNoTensor: the queue is empty) and the chunk's number in it
@@ -961,25 +1078,212 @@ struct SlotCopy {
     }
 };
 
-template <typename T>
-__device__ __forceinline__ const char* in_slot(const char* slot, const T* base, uint64_t at)
+/* Fills the stages until the list's chunks are used up.  The steps take them from a queue
+ * in the step state, one at a time, so that the chunks in flight stay together at the
+ * front of the list however the blocks' speeds differ; the codec, which has no step state,
+ * takes every gridDim.x-th. */
+template <Op OP, int CAP>
+__device__ __forceinline__ void produce(const ListArgs<CAP>& a, char* stages, uint64_t* full, uint64_t* empty,
+                                        StageInfo* info)
 {
-    return slot + (((uintptr_t)base + at) & 15u);
+    using R = Ring<OP>;
+    const uint32_t lane = threadIdx.x & 31;
+    zero_step_state_t* st = const_cast<zero_step_state_t*>(a.st);
+    unsigned long long next = blockIdx.x;
+    if (R::kStep && lane == 0)
+        next = atomicAdd(reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk), 1ull);
+    Place at{0, 1, 0, 0};
+    uint32_t issued = 0, live = R::kStages - 1;  // stages before `issued` that may be unread
+    for (;; ++issued) {
+        const uint32_t k = issued % R::kStages;
+        if (issued >= R::kStages && !wait_parity_bounded(smem_addr(&empty[k]), (issued / R::kStages - 1) & 1)) {
+            if (lane == 0 && st)
+                atomicOr(&st->error, 1u);
+            live = R::kStages;
+            break;
+        }
+        const unsigned long long c = __shfl_sync(0xffffffffu, next, 0);
+        const uint32_t bar = smem_addr(&full[k]);
+        if (c >= a.l.n_units) {
+            if (lane == 0) {
+                info[k].k = kNoTensor;
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+            }
+            break;
+        }
+        if (!R::kStep)
+            next = c + gridDim.x;
+        else if (lane == 0)  // one ahead: its latency stays off the ring's path
+            next = atomicAdd(reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk), 1ull);
+        locate(a.l, (uint32_t)c, at);
+        const Ref& t = a.l.t[at.k];
+        char* s = stages + k * R::kBytes;
+        const uint64_t first = (uint64_t)at.unit * kRingChunk;
+        const uint32_t n = t.elems - first < kRingChunk ? (uint32_t)(t.elems - first) : kRingChunk;
+        auto copy = [&](const void* base, uint32_t size, uint32_t slot) {
+            return SlotCopy(base, t.elems * size, first * size, n * size, s + slot, lane);
+        };
+        constexpr uint32_t kSize = OP == Op::kAdamw8 || OP == Op::kRead ? 1 : 4;
+        const SlotCopy m = copy(OP == Op::kWrite ? t.x : t.m, kSize, R::kM);
+        const SlotCopy v = copy(OP == Op::kWrite ? t.y : t.v, kSize, R::kV);
+        SlotCopy g = m, p = m, b = m;
+        uint32_t bytes = m.len + v.len;
+        if (R::kStep) {
+            g = copy(t.grad, (t.flags & kGradMask) == ZERO_F32 ? 4 : 2, R::kGrad);
+            p = copy(t.master, 4, R::kMaster);
+            bytes += g.len + p.len;
+        }
+        if (kSize == 1) {
+            b = SlotCopy(t.exps, (t.elems + kUnit - 1) / kUnit * 2, first / kUnit * 2, (n + kUnit - 1) / kUnit * 2,
+                         s + R::kExps, lane);
+            bytes += b.len;
+        }
+        // the bytes the lanes wrote come before the arrival, and before any later bulk copy
+        // into the same slot
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            info[k] = StageInfo{at.k, at.unit};
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+            m.bulk(bar);
+            v.bulk(bar);
+            if (R::kStep) {
+                g.bulk(bar);
+                p.bulk(bar);
+            }
+            if (kSize == 1)
+                b.bulk(bar);
+        }
+    }
+    // every copy has landed before the block may end (a consumer that gave up leaves stages
+    // unread)
+    for (uint32_t i = issued > live ? issued - live : 0; i < issued; ++i)
+        wait_parity_bounded(smem_addr(&full[i % R::kStages]), (i / R::kStages) & 1);
+    if (R::kStep && lane == 0) {  // the queue back to 0 for the next launch, by the last block
+        __threadfence();
+        if (atomicAdd(&st->adamw_done, 1u) == gridDim.x - 1) {
+            __threadfence();
+            atomicExch(reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk), 0ull);
+            atomicExch(&st->adamw_done, 0u);
+        }
+    }
 }
 
-template <bool S8, int CAP>
-__global__ void __launch_bounds__(kRingThreads, 1) k_tensors_ring(const __grid_constant__ AdamwList<CAP> a)
+/* A warp's unit of a stage: where it lies, and its lanes' elements: 8 consecutive ones
+ * where every array allows it, else one of every 32. */
+struct InStage {
+    const char* slot;
+    uint64_t first, at;  // the stage's and this lane's first element in the tensor
+    uint32_t e0;         // at - first
+    bool whole;
+
+    template <typename T>
+    __device__ __forceinline__ const T* in(uint32_t array, const void* base) const
+    {
+        return reinterpret_cast<const T*>(slot + array + (((uintptr_t)base + first * sizeof(T)) & 15u)) + e0;
+    }
+    __device__ __forceinline__ void floats(uint32_t array, const void* base, float (&to)[8]) const
+    {
+        const float* from = in<float>(array, base);
+        if (whole) {
+            const float4 lo = reinterpret_cast<const float4*>(from)[0], hi = reinterpret_cast<const float4*>(from)[1];
+            to[0] = lo.x, to[1] = lo.y, to[2] = lo.z, to[3] = lo.w;
+            to[4] = hi.x, to[5] = hi.y, to[6] = hi.z, to[7] = hi.w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                to[e] = from[e * 32];
+        }
+    }
+    __device__ __forceinline__ void grads(uint32_t array, const void* base, uint32_t dtype, float (&to)[8]) const
+    {
+        if (dtype == ZERO_F32) {
+            floats(array, base, to);
+            return;
+        }
+        const uint16_t* from = in<uint16_t>(array, base);
+        if (whole) {
+            const uint4 w = *reinterpret_cast<const uint4*>(from);
+            if (dtype == ZERO_F16)
+                widen8<ZERO_F16>(w, to);
+            else
+                widen8<ZERO_BF16>(w, to);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                to[e] = dtype == ZERO_F16 ? one16<ZERO_F16>(from[e * 32]) : one16<ZERO_BF16>(from[e * 32]);
+        }
+    }
+    /* The codes of m and v as floats; 0 past the tensor's end, so that what lies there does
+     * not count in the block's exponents. */
+    __device__ __forceinline__ void codes(uint32_t m, uint32_t v, const Ref& t, float (&ym)[8], float (&yv)[8]) const
+    {
+        const uint8_t* cm = in<uint8_t>(m, t.m);
+        const uint8_t* cv = in<uint8_t>(v, t.v);
+        if (whole) {
+            const uint2 wm = *reinterpret_cast<const uint2*>(cm), wv = *reinterpret_cast<const uint2*>(cv);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ym[e] = raw_m(e < 4 ? wm.x : wm.y, e & 3);
+                yv[e] = raw_v(e < 4 ? wv.x : wv.y, e & 3);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool inside = at + e * 32 < t.elems;
+                ym[e] = inside ? raw_m(cm[e * 32], 0) : 0.0f;
+                yv[e] = inside ? raw_v(cv[e * 32], 0) : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void put(float* to, const Ref& t, const float (&x)[8]) const
+    {
+        if (whole) {
+            store8(to + at, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e * 32 < t.elems)
+                    __stcs(to + at + e * 32, x[e]);
+        }
+    }
+    __device__ __forceinline__ void put16(uint16_t* to, const Ref& t, bool f16, const float (&x)[8]) const
+    {
+        if (whole) {
+            store_params8(to + at, f16, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e * 32 < t.elems)
+                    to[at + e * 32] = f16 ? pack1<true>(x[e]) : pack1<false>(x[e]);
+        }
+    }
+    __device__ __forceinline__ void put_codes(void* to, const Ref& t, uint2 c) const
+    {
+        uint8_t* p = static_cast<uint8_t*>(to) + at;
+        if (whole) {
+            __stcs(reinterpret_cast<uint2*>(p), c);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e * 32 < t.elems)
+                    p[e * 32] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+        }
+    }
+};
+
+template <Op OP, int CAP>
+__global__ void __launch_bounds__(kRingThreads, 1) k_tensors_ring(const __grid_constant__ ListArgs<CAP> a)
 {
-    using R = Ring<S8>;
+    using R = Ring<OP>;
     extern __shared__ __align__(128) char stages[];
     __shared__ __align__(8) uint64_t full[R::kStages], empty[R::kStages];
     __shared__ StageInfo info[R::kStages];
     grid_dependency_wait();
-    zero_step_state_t* st = const_cast<zero_step_state_t*>(a.st);
-    if (st->skip)
+    if (R::kStep && a.st->skip)
         return;
     if (threadIdx.x == 0) {
-        for (int k = 0; k < R::kStages; ++k) {
+        for (uint32_t k = 0; k < R::kStages; ++k) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[k])));
             asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[k])), "n"(kRingWarps));
         }
@@ -987,382 +1291,128 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_tensors_ring(const __grid_c
     }
     __syncthreads();
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-    if (warp == kRingWarps) {  // the producer
-        unsigned long long* queue = reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk);
-        unsigned long long next = 0;
-        if (lane == 0)
-            next = atomicAdd(queue, 1ull);
-        Place at{0, 1, 0, 0};
-        uint32_t issued = 0, live = R::kStages - 1;  // stages before `issued` that may be unread
-        for (;; ++issued) {
-            const uint32_t k = issued % R::kStages;
-            if (issued >= (uint32_t)R::kStages &&
-                !wait_parity_bounded(smem_addr(&empty[k]), (issued / R::kStages - 1) & 1)) {
-                if (lane == 0)
-                    atomicOr(&st->error, 1u);
-                live = R::kStages;
-                break;
-            }
-            const unsigned long long c = __shfl_sync(0xffffffffu, next, 0);
-            const uint32_t bar = smem_addr(&full[k]);
-            if (c >= a.l.n_units) {
-                if (lane == 0) {
-                    info[k].k = kNoTensor;
-                    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-                }
-                break;
-            }
-            if (lane == 0)
-                next = atomicAdd(queue, 1ull);  // one ahead: its latency stays off the ring's path
-            locate(a.l, (uint32_t)c, at);
-            const Ref& t = a.l.t[at.k];
-            char* s = stages + k * R::kBytes;
-            const uint64_t first = (uint64_t)at.unit * kRingChunk;
-            const uint32_t n = t.elems - first < kRingChunk ? (uint32_t)(t.elems - first) : kRingChunk;
-            const uint32_t gs = (t.flags & kGradMask) == ZERO_F32 ? 4 : 2, ss = S8 ? 1 : 4;
-            const SlotCopy g(t.grad, t.elems * gs, first * gs, n * gs, s + R::kGrad, lane);
-            const SlotCopy p(t.master, t.elems * 4, first * 4, n * 4, s + R::kMaster, lane);
-            const SlotCopy m(t.m, t.elems * ss, first * ss, n * ss, s + R::kM, lane);
-            const SlotCopy v(t.v, t.elems * ss, first * ss, n * ss, s + R::kV, lane);
-            uint32_t bytes = g.len + p.len + m.len + v.len;
-            SlotCopy b = m;
-            if (S8) {
-                b = SlotCopy(t.exps, (t.elems + kUnit - 1) / kUnit * 2, first / kUnit * 2, (n + kUnit - 1) / kUnit * 2,
-                             s + R::kExps, lane);
-                bytes += b.len;
-            }
-            // the bytes the lanes wrote come before the arrival, and before any later bulk
-            // copy into the same slot
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                info[k] = StageInfo{at.k, at.unit};
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-                g.bulk(bar);
-                p.bulk(bar);
-                m.bulk(bar);
-                v.bulk(bar);
-                if (S8)
-                    b.bulk(bar);
-            }
-        }
-        // every copy has landed before the block may end (a consumer that gave up leaves
-        // stages unread)
-        for (uint32_t i = issued > live ? issued - live : 0; i < issued; ++i)
-            wait_parity_bounded(smem_addr(&full[i % R::kStages]), (i / R::kStages) & 1);
-        if (lane == 0) {  // the queue back to 0 for the next launch, by the last block
-            __threadfence();
-            if (atomicAdd(&st->adamw_done, 1u) == gridDim.x - 1) {
-                __threadfence();
-                atomicExch(queue, 0ull);
-                atomicExch(&st->adamw_done, 0u);
-            }
-        }
+    if (warp == kRingWarps) {
+        produce<OP>(a, stages, full, empty, info);
         return;
     }
-
+    Scalars s;
     Step8 s8;
-    Scalars s = step_scalars(a);
-    const float inv = st->inv_scale_used, step = s.step;
-    if (S8) {
-        s8.inv = inv;
-        s8.c = s.c;
-        s8.b1 = s.b1;
-        s8.b2 = s.b2;
-        s8.omb1 = s.omb1;
-        s8.omb2 = s.omb2;
-        s8.eps = s.eps;
-        s8.inv_rbc2 = __fdiv_rn(1.0f, s.rbc2);
-        s8.key = step_key(a.seed, st->t);
-        s8.exact = a.eps < 0x1p-100f;
+    float inv = 1.0f, step = 0.0f;
+    if (OP == Op::kAdamw) {
+        s = step_scalars(a);
+        inv = a.st->inv_scale_used;
+        step = s.step;
+    } else if (OP == Op::kAdamw8) {
+        s8 = step8(a);
+        step = s8.step;
     }
     for (uint32_t i = 0;; ++i) {
         const uint32_t q = i % R::kStages, bar = smem_addr(&empty[q]);
         if (!wait_parity_bounded(smem_addr(&full[q]), (i / R::kStages) & 1)) {
-            if (lane == 0)
-                atomicOr(&st->error, 1u);
+            if (R::kStep && lane == 0)
+                atomicOr(&const_cast<zero_step_state_t*>(a.st)->error, 1u);
             return;
         }
         const StageInfo where = info[q];
         if (where.k == kNoTensor)
             return;
-        const Ref& t = a.l.t[where.k];
-        const char* slot = stages + q * R::kBytes;
-        const uint64_t first = (uint64_t)where.chunk * kRingChunk;  // the stage's first element
-        const uint64_t off = first + warp * kUnit;                  // this warp's
-        auto release = [&] {
+        auto release = [&] {  // this warp has what it needs of the stage
             __syncwarp();
             if (lane == 0)
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
         };
+        const Ref& t = a.l.t[where.k];
+        const uint64_t first = (uint64_t)where.chunk * kRingChunk, off = first + warp * kUnit;
         if (off >= t.elems) {
             release();
             continue;
         }
-        const uint32_t dtype = t.flags & kGradMask, gs = dtype == ZERO_F32 ? 4 : 2;
-        const bool whole = (t.flags & kVector) && off + kUnit <= t.elems;
-        // this lane's elements: 8 consecutive ones, or one of every 32
-        const uint32_t e0 = warp * kUnit + (whole ? lane * kPer : lane), apart = whole ? 1 : 32;
-        const char* g = in_slot(slot + R::kGrad, static_cast<const char*>(t.grad), first * gs) + e0 * gs;
-        const float* pm = reinterpret_cast<const float*>(in_slot(slot + R::kMaster, t.master, first * 4)) + e0;
-        float x[8], p[8];
-        auto read = [&](const float* from, float (&to)[8]) {
-            if (whole) {
-                const float4 lo = reinterpret_cast<const float4*>(from)[0], hi = reinterpret_cast<const float4*>(from)[1];
-                to[0] = lo.x, to[1] = lo.y, to[2] = lo.z, to[3] = lo.w;
-                to[4] = hi.x, to[5] = hi.y, to[6] = hi.z, to[7] = hi.w;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    to[e] = from[e * 32];
-            }
-        };
-        if (dtype == ZERO_F32) {
-            read(reinterpret_cast<const float*>(g), x);
-        } else if (whole) {
-            const uint4 w = *reinterpret_cast<const uint4*>(g);
-            if (dtype == ZERO_F16)
-                widen8<ZERO_F16>(w, x);
-            else
-                widen8<ZERO_BF16>(w, x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint16_t w = reinterpret_cast<const uint16_t*>(g)[e * 32];
-                x[e] = dtype == ZERO_F16 ? one16<ZERO_F16>(w) : one16<ZERO_BF16>(w);
-            }
-        }
-        read(pm, p);
-        const uint64_t at = first + e0;  // this lane's first element
-        if (S8) {
-            s8.step = __fmul_rn(step, t.lr_scale);
-            s8.decay = t.decay;
-            const char* cm_at = in_slot(slot + R::kM, static_cast<const char*>(t.m), first) + e0;
-            const char* cv_at = in_slot(slot + R::kV, static_cast<const char*>(t.v), first) + e0;
-            const uint8_t* b = reinterpret_cast<const uint8_t*>(
-                                   in_slot(slot + R::kExps, t.exps, first / kUnit * 2)) + 2 * warp;
-            uint32_t bm = b[0], bv = b[1];
-            float ym[8], yv[8];
-            const uint32_t unit = (uint32_t)(off / kUnit);
-            const uint32_t seed = mix32(s8.key + (t.group0 + unit * 32 + lane) * kGolden);
-            uint2 cm, cv;
-            uint8_t* m = static_cast<uint8_t*>(t.m) + at;
-            uint8_t* v = static_cast<uint8_t*>(t.v) + at;
-            if (whole) {
-                cm = *reinterpret_cast<const uint2*>(cm_at);
-                cv = *reinterpret_cast<const uint2*>(cv_at);
-                release();
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ym[e] = raw_m(e < 4 ? cm.x : cm.y, e & 3);
-                    yv[e] = raw_v(e < 4 ? cv.x : cv.y, e & 3);
-                }
-                block8(x, p, ym, yv, bm, bv, RandomInGroup{seed}, cm, cv, s8);
-                __stcs(reinterpret_cast<uint2*>(m), cm);
-                __stcs(reinterpret_cast<uint2*>(v), cv);
-            } else {
-                // what lies past the tensor's end must not count in the block's exponents
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const bool in = at + e * 32 < t.elems;
-                    x[e] = in ? x[e] : 0.0f;
-                    p[e] = in ? p[e] : 0.0f;
-                    ym[e] = in ? raw_m((uint8_t)cm_at[e * 32], 0) : 0.0f;
-                    yv[e] = in ? raw_v((uint8_t)cv_at[e * 32], 0) : 0.0f;
-                }
-                release();
-                block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s8);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (at + e * 32 < t.elems) {
-                        m[e * 32] = (uint8_t)((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
-                        v[e * 32] = (uint8_t)((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
-                    }
-            }
-            if (lane == 0) {
-                t.exps[off / kUnit * 2] = (uint8_t)bm;
-                t.exps[off / kUnit * 2 + 1] = (uint8_t)bv;
-            }
-        } else {
-            float mm[8], vv[8];
-            read(reinterpret_cast<const float*>(in_slot(slot + R::kM, static_cast<const char*>(t.m), first * 4)) + e0, mm);
-            read(reinterpret_cast<const float*>(in_slot(slot + R::kV, static_cast<const char*>(t.v), first * 4)) + e0, vv);
+        InStage u;
+        u.slot = stages + q * R::kBytes;
+        u.first = first;
+        u.whole = (t.flags & kVector) && off + kUnit <= t.elems;
+        u.e0 = warp * kUnit + (u.whole ? lane * kPer : lane);
+        u.at = first + u.e0;
+        uint8_t* exps = t.exps + off / kUnit * 2;
+        const uint8_t* b = reinterpret_cast<const uint8_t*>(u.slot + R::kExps + (((uintptr_t)t.exps + first / kUnit * 2) & 15u)) + 2 * warp;
+        if (OP == Op::kAdamw) {
+            float x[8], p[8], m[8], v[8];
+            u.grads(R::kGrad, t.grad, t.flags & kGradMask, x);
+            u.floats(R::kMaster, t.master, p);
+            u.floats(R::kM, t.m, m);
+            u.floats(R::kV, t.v, v);
             release();
             s.step = __fmul_rn(step, t.lr_scale);
             s.decay = t.decay;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                adamw_one(__fmul_rn(x[e], inv), p[e], mm[e], vv[e], s);
-            float* m = static_cast<float*>(t.m) + at;
-            float* v = static_cast<float*>(t.v) + at;
-            if (whole) {
-                store8(m, mm);
-                store8(v, vv);
+                adamw_one(__fmul_rn(x[e], inv), p[e], m[e], v[e], s);
+            u.put(static_cast<float*>(t.m), t, m);
+            u.put(static_cast<float*>(t.v), t, v);
+            u.put(t.master, t, p);
+            if (t.params)
+                u.put16(t.params, t, t.flags & kOutF16, p);
+        } else if (OP == Op::kAdamw8) {
+            float x[8], p[8], ym[8], yv[8];
+            u.grads(R::kGrad, t.grad, t.flags & kGradMask, x);
+            u.floats(R::kMaster, t.master, p);
+            u.codes(R::kM, R::kV, t, ym, yv);
+            uint32_t bm = b[0], bv = b[1];
+            release();
+            s8.step = __fmul_rn(step, t.lr_scale);
+            s8.decay = t.decay;
+            const uint32_t seed = mix32(s8.key + (t.group0 + (uint32_t)(off / kPer) + lane) * kGolden);
+            uint2 cm, cv;
+            if (u.whole) {
+                block8(x, p, ym, yv, bm, bv, RandomInGroup{seed}, cm, cv, s8);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (at + e * 32 < t.elems) {
-                        __stcs(m + e * 32, mm[e]);
-                        __stcs(v + e * 32, vv[e]);
-                    }
+                    x[e] = u.at + e * 32 < t.elems ? x[e] : 0.0f;
+                block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s8);
             }
-        }
-        if (whole) {
-            store8(t.master + at, p);
+            u.put_codes(t.m, t, cm);
+            u.put_codes(t.v, t, cv);
+            u.put(t.master, t, p);
             if (t.params)
-                store_params8(t.params + at, t.flags & kOutF16, p);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (at + e * apart < t.elems) {
-                    __stcs(t.master + at + e * 32, p[e]);
-                    if (t.params)
-                        t.params[at + e * 32] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
-                }
-        }
-    }
-}
-
-/* ------------------------------------------------------------------------------------ */
-/* 8-bit states to values and back                                                        */
-/* ------------------------------------------------------------------------------------ */
-
-/* A unit of the codec, lanes side by side. */
-template <bool WRITE, int CAP>
-__device__ __forceinline__ void codec_by_element(const List<CAP>& l, uint32_t k, uint32_t unit)
-{
-    const Ref& t = l.t[k];
-    const uint32_t lane = threadIdx.x & 31;
-    uint8_t* m = static_cast<uint8_t*>(t.m);
-    uint8_t* v = static_cast<uint8_t*>(t.v);
-    uint8_t* b = t.exps + 2 * (uint64_t)unit;
-    const uint64_t i = (uint64_t)unit * kUnit + lane;
-    if (WRITE) {
-        float xm[8], xv[8];
-        uint32_t top_m = 0, top_v = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint64_t q = i + e * 32;
-            xm[e] = q < t.elems ? __ldcs(static_cast<const float*>(t.x) + q) : 0.0f;
-            xv[e] = q < t.elems ? __ldcs(static_cast<const float*>(t.y) + q) : 0.0f;
-            top_m = max(top_m, __float_as_uint(xm[e]) & 0x7fffffffu);
-            top_v = max(top_v, __float_as_uint(xv[e]) & 0x7fffffffu);
-        }
-        const uint32_t bm = block_exponent(__reduce_max_sync(0xffffffffu, top_m));
-        const uint32_t bv = block_exponent(__reduce_max_sync(0xffffffffu, top_v));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint64_t q = i + e * 32;
-            if (q < t.elems) {
-                m[q] = (uint8_t)encode_m(xm[e], exp_unscale(bm), kNearest);
-                v[q] = (uint8_t)encode_v(xv[e], exp_unscale(bv), kNearest);
+                u.put16(t.params, t, t.flags & kOutF16, p);
+            if (lane == 0) {
+                exps[0] = (uint8_t)bm;
+                exps[1] = (uint8_t)bv;
             }
-        }
-        if (lane == 0) {
-            b[0] = (uint8_t)bm;
-            b[1] = (uint8_t)bv;
-        }
-    } else {
-        const float scale_m = exp_scale(b[0]), scale_v = exp_scale(b[1]);
-        uint32_t cm[8], cv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint64_t q = i + e * 32;
-            cm[e] = q < t.elems ? m[q] : 0u;
-            cv[e] = q < t.elems ? v[q] : 0u;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint64_t q = i + e * 32;
-            if (q >= t.elems)
-                continue;
-            const float xm = decode_m(cm[e], scale_m), xv = decode_v(cv[e], scale_v);
+        } else if (OP == Op::kRead) {
+            float m[8], v[8];
+            u.codes(R::kM, R::kV, t, m, v);
+            const float scale_m = exp_scale(b[0]), scale_v = exp_scale(b[1]);
+            release();
+            scale_values(m, v, scale_m, scale_v);
             if (t.flags & kValueBF16) {
-                static_cast<uint16_t*>(t.x)[q] = pack1<false>(xm);
-                static_cast<uint16_t*>(t.y)[q] = pack1<false>(xv);
+                u.put16(static_cast<uint16_t*>(t.x), t, false, m);
+                u.put16(static_cast<uint16_t*>(t.y), t, false, v);
             } else {
-                static_cast<float*>(t.x)[q] = xm;
-                static_cast<float*>(t.y)[q] = xv;
+                u.put(static_cast<float*>(t.x), t, m);
+                u.put(static_cast<float*>(t.y), t, v);
             }
-        }
-    }
-}
-
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) k_state8_read(const __grid_constant__ List<CAP> l)
-{
-    grid_dependency_wait();
-    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
-    Place at{0, 1, 0, 0};
-    for (uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < l.n_units; u += stride) {
-        locate(l, u, at);
-        const Ref& t = l.t[at.k];
-        if (!whole_unit(t, at.unit)) {
-            codec_by_element<false>(l, at.k, at.unit);
-            continue;
-        }
-        const uint64_t i = (uint64_t)at.unit * kUnit + lane * kPer;
-        const uint2 cm = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.m) + i));
-        const uint2 cv = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(t.v) + i));
-        const uint8_t* b = t.exps + 2 * (uint64_t)at.unit;
-        const float scale_m = exp_scale(b[0]), scale_v = exp_scale(b[1]);
-        float xm[8], xv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            xm[e] = __fmul_rn(__fmul_rn(raw_m(e < 4 ? cm.x : cm.y, e & 3), 0x1p112f), scale_m);
-            xv[e] = __fmul_rn(__fmul_rn(raw_v(e < 4 ? cv.x : cv.y, e & 3), 0x1p96f), scale_v);
-        }
-        if (t.flags & kValueBF16) {
-            store_params8(static_cast<uint16_t*>(t.x) + i, 0, xm);
-            store_params8(static_cast<uint16_t*>(t.y) + i, 0, xv);
         } else {
-            store8(static_cast<float*>(t.x) + i, xm);
-            store8(static_cast<float*>(t.y) + i, xv);
-        }
-    }
-}
-
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) k_state8_write(const __grid_constant__ List<CAP> l)
-{
-    grid_dependency_wait();
-    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
-    Place at{0, 1, 0, 0};
-    for (uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5); u < l.n_units; u += stride) {
-        locate(l, u, at);
-        const Ref& t = l.t[at.k];
-        if (!whole_unit(t, at.unit)) {
-            codec_by_element<true>(l, at.k, at.unit);
-            continue;
-        }
-        const uint64_t i = (uint64_t)at.unit * kUnit + lane * kPer;
-        float xm[8], xv[8];
-        load8(static_cast<const float*>(t.x) + i, xm);
-        load8(static_cast<const float*>(t.y) + i, xv);
-        uint32_t top_m = 0, top_v = 0;
+            float m[8], v[8];
+            u.floats(R::kM, t.x, m);
+            u.floats(R::kV, t.y, v);
+            release();
+            if (!u.whole) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            top_m = max(top_m, __float_as_uint(xm[e]) & 0x7fffffffu);
-            top_v = max(top_v, __float_as_uint(xv[e]) & 0x7fffffffu);
-        }
-        const uint32_t bm = block_exponent(__reduce_max_sync(0xffffffffu, top_m));
-        const uint32_t bv = block_exponent(__reduce_max_sync(0xffffffffu, top_v));
-        const float um = exp_unscale(bm), uv = exp_unscale(bv);
-        uint32_t cm[8], cv[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            cm[e] = encode_m(xm[e], um, kNearest) << 24;
-            cv[e] = encode_v(xv[e], uv, kNearest) << 24;
-        }
-        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.m) + i),
-               make_uint2(top_bytes(cm[0], cm[1], cm[2], cm[3]), top_bytes(cm[4], cm[5], cm[6], cm[7])));
-        __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(t.v) + i),
-               make_uint2(top_bytes(cv[0], cv[1], cv[2], cv[3]), top_bytes(cv[4], cv[5], cv[6], cv[7])));
-        if (lane == 0) {
-            uint8_t* b = t.exps + 2 * (uint64_t)at.unit;
-            b[0] = (uint8_t)bm;
-            b[1] = (uint8_t)bv;
+                for (int e = 0; e < 8; ++e) {
+                    m[e] = u.at + e * 32 < t.elems ? m[e] : 0.0f;
+                    v[e] = u.at + e * 32 < t.elems ? v[e] : 0.0f;
+                }
+            }
+            uint2 cm, cv;
+            const uint2 top = nearest_codes(m, v, cm, cv);
+            u.put_codes(t.m, t, cm);
+            u.put_codes(t.v, t, cv);
+            if (lane == 0) {
+                exps[0] = (uint8_t)top.x;
+                exps[1] = (uint8_t)top.y;
+            }
         }
     }
 }
@@ -1370,8 +1420,6 @@ __global__ void __launch_bounds__(kThreads) k_state8_write(const __grid_constant
 /* ------------------------------------------------------------------------------------ */
 /* host side                                                                              */
 /* ------------------------------------------------------------------------------------ */
-
-enum class Op { kNorm, kAdamw, kAdamw8, kRead, kWrite };
 
 bool finite_f(float x) { return x == x && x <= 3.4e38f && x >= -3.4e38f; }
 
@@ -1587,71 +1635,54 @@ int launch_ring(void (*kernel)(Args), std::atomic<bool> (&configured)[64], uint3
     return status_of(launch_pdl(kernel, dim3(chunks < cap ? chunks : cap), dim3(kRingThreads), smem, s, a));
 }
 
-template <int CAP>
-int launch_adamw_list(const AdamwList<CAP>& a, Op op, bool ring, cudaStream_t s)
+template <Op OP, int CAP>
+int launch_list(void (*direct)(ListArgs<CAP>), const ListArgs<CAP>& a, bool ring, cudaStream_t s)
 {
-    static std::atomic<int> occ[2][64];  // per device; a race only repeats the set-up
-    static std::atomic<bool> configured[2][64];
-    const bool s8 = op == Op::kAdamw8;
+    static std::atomic<int> occ[64];  // per device; a race only repeats the set-up
+    static std::atomic<bool> configured[64];
     if (ring)
-        return s8 ? launch_ring(k_tensors_ring<true, CAP>, configured[1], Ring<true>::kSmem, a.l.n_units, s, a)
-                  : launch_ring(k_tensors_ring<false, CAP>, configured[0], Ring<false>::kSmem, a.l.n_units, s, a);
-    return s8 ? launch_units(k_tensors_adamw8<CAP>, occ[1], a.l.n_units, s, a)
-              : launch_units(k_tensors_adamw<CAP>, occ[0], a.l.n_units, s, a);
+        return launch_ring(k_tensors_ring<OP, CAP>, configured, Ring<OP>::kSmem, a.l.n_units, s, a);
+    return launch_units(direct, occ, a.l.n_units, s, a);
+}
+
+template <int CAP>
+int launch_op(const ListArgs<CAP>& a, Op op, bool ring, cudaStream_t s)
+{
+    switch (op) {
+    case Op::kAdamw: return launch_list<Op::kAdamw>(k_tensors_adamw<CAP>, a, ring, s);
+    case Op::kAdamw8: return launch_list<Op::kAdamw8>(k_tensors_adamw8<CAP>, a, ring, s);
+    case Op::kRead: return launch_list<Op::kRead>(k_tensors_codec<Op::kRead, CAP>, a, ring, s);
+    default: return launch_list<Op::kWrite>(k_tensors_codec<Op::kWrite, CAP>, a, ring, s);
+    }
 }
 
 constexpr uint64_t kRingElems = 1u << 21;
 
-int run_adamw(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparams_t* hp, uint64_t seed,
-              const zero_step_state_t* st, cudaStream_t s, Op op)
+int run_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
+             const zero_adamw_hparams_t* hp, uint64_t seed, const zero_step_state_t* st, cudaStream_t s, Op op)
 {
-    AdamwList<kLarge> a;
-    AdamwList<kSmall> b;
+    ListArgs<kLarge> a;
+    ListArgs<kSmall> b;
     a.st = b.st = st;
     a.seed = b.seed = seed;
-    a.beta1 = b.beta1 = hp->beta1;
-    a.beta2 = b.beta2 = hp->beta2;
-    a.eps = b.eps = hp->eps;
+    a.beta1 = b.beta1 = hp ? hp->beta1 : 0.0f;
+    a.beta2 = b.beta2 = hp ? hp->beta2 : 0.0f;
+    a.eps = b.eps = hp ? hp->eps : 0.0f;
     uint64_t total = 0;
     for (uint64_t k = 0; k < n; ++k)
         total += tensors[k].elems;
     const bool ring = total >= kRingElems;
     uint32_t group0 = 0;
     for (uint64_t next = 0; next < n;) {
-        next = fill(a.l, tensors, nullptr, n, next, op, hp, group0, ring ? kRingChunk : kUnit);
+        next = fill(a.l, tensors, others, n, next, op, hp, group0, ring ? kRingChunk : kUnit);
         if (a.l.n == 0)
             continue;
         int rc;
         if (a.l.n <= (uint32_t)kSmall) {
             shrink(a.l, b.l);
-            rc = launch_adamw_list(b, op, ring, s);
+            rc = launch_op(b, op, ring, s);
         } else {
-            rc = launch_adamw_list(a, op, ring, s);
-        }
-        if (rc != ZERO_OK)
-            return rc;
-    }
-    return ZERO_OK;
-}
-
-int run_codec(const zero_tensor_t* t8, const zero_tensor_t* t32, uint64_t n, cudaStream_t s, Op op)
-{
-    static std::atomic<int> occ[4][64];
-    List<kLarge> a;
-    List<kSmall> b;
-    uint32_t group0 = 0;
-    for (uint64_t next = 0; next < n;) {
-        next = fill(a, t8, t32, n, next, op, nullptr, group0);
-        if (a.n == 0)
-            continue;
-        int rc;
-        if (a.n <= (uint32_t)kSmall) {
-            shrink(a, b);
-            rc = op == Op::kRead ? launch_units(k_state8_read<kSmall>, occ[0], b.n_units, s, b)
-                                 : launch_units(k_state8_write<kSmall>, occ[1], b.n_units, s, b);
-        } else {
-            rc = op == Op::kRead ? launch_units(k_state8_read<kLarge>, occ[2], a.n_units, s, a)
-                                 : launch_units(k_state8_write<kLarge>, occ[3], a.n_units, s, a);
+            rc = launch_op(a, op, ring, s);
         }
         if (rc != ZERO_OK)
             return rc;
@@ -1735,7 +1766,7 @@ extern "C" int zero_tensors_adamw(const zero_tensor_t* tensors, uint64_t n_tenso
         return ZERO_EINVAL;
     if (rc != ZERO_OK || !at(st, 16))
         return ZERO_EALIGN;
-    return run_adamw(tensors, n_tensors, hp, 0, st, (cudaStream_t)stream, Op::kAdamw);
+    return run_list(tensors, nullptr, n_tensors, hp, 0, st, (cudaStream_t)stream, Op::kAdamw);
 }
 
 extern "C" int zero_tensors_adamw8(const zero_tensor_t* tensors, uint64_t n_tensors,
@@ -1748,7 +1779,7 @@ extern "C" int zero_tensors_adamw8(const zero_tensor_t* tensors, uint64_t n_tens
         return ZERO_EINVAL;
     if (rc != ZERO_OK || !at(st, 16))
         return ZERO_EALIGN;
-    return run_adamw(tensors, n_tensors, hp, seed, st, (cudaStream_t)stream, Op::kAdamw8);
+    return run_list(tensors, nullptr, n_tensors, hp, seed, st, (cudaStream_t)stream, Op::kAdamw8);
 }
 
 extern "C" int zero_tensors_state8_read(const zero_tensor_t* from, const zero_tensor_t* to,
@@ -1756,7 +1787,7 @@ extern "C" int zero_tensors_state8_read(const zero_tensor_t* from, const zero_te
 {
     const NvtxRange range("zero_tensors_state8_read");
     const int rc = check_list(from, to, n_tensors, Op::kRead);
-    return rc != ZERO_OK ? rc : run_codec(from, to, n_tensors, (cudaStream_t)stream, Op::kRead);
+    return rc != ZERO_OK ? rc : run_list(from, to, n_tensors, nullptr, 0, nullptr, (cudaStream_t)stream, Op::kRead);
 }
 
 extern "C" int zero_tensors_state8_write(const zero_tensor_t* to, const zero_tensor_t* from,
@@ -1764,5 +1795,5 @@ extern "C" int zero_tensors_state8_write(const zero_tensor_t* to, const zero_ten
 {
     const NvtxRange range("zero_tensors_state8_write");
     const int rc = check_list(to, from, n_tensors, Op::kWrite);
-    return rc != ZERO_OK ? rc : run_codec(to, from, n_tensors, (cudaStream_t)stream, Op::kWrite);
+    return rc != ZERO_OK ? rc : run_list(to, from, n_tensors, nullptr, 0, nullptr, (cudaStream_t)stream, Op::kWrite);
 }
