@@ -622,6 +622,12 @@ __device__ __forceinline__ float raw_v(uint32_t w, int byte)
     return __uint_as_float(__byte_perm(w, 0, byte << 12 | 0x444) >> 4);
 }
 
+/* The code of a float from raw_m's or raw_v's scale, rounded with r, in the top byte. */
+__device__ __forceinline__ uint32_t top_code(float y, uint32_t r)
+{
+    return __float_as_uint(y) * 16u + (r >> 8);
+}
+
 /* Four codes, each in its word's top byte, as one word. */
 __device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
@@ -737,20 +743,17 @@ __device__ __forceinline__ void block8(const float (&x)[8], float (&p)[8], float
                 const uint64_t q = f2_mul(f2_mul(m2, step2), f2(rcp_fast(d0), rcp_fast(d1)));
                 f2_split(f2_fma(f2(p[e], p[e + 1]), decay2, q), p[e], p[e + 1]);
                 f2_split(f2_mul(m2, um), y0, y1);
-                // sign and magnitude: adding to the bits adds to the magnitude
-                const uint32_t t0 = __float_as_uint(y0) + (random.m(e) >> 12);
-                const uint32_t t1 = __float_as_uint(y1) + (random.m(e + 1) >> 12);
-                code_m[o] = (t0 << 4 & 0x7fffffffu) | (t0 & 0x80000000u);
-                code_m[o + 1] = (t1 << 4 & 0x7fffffffu) | (t1 & 0x80000000u);
+                // the bits times 16 put the code into the top byte (m's sign falls out); four
+                // more random bits below the 20 change no carry, since all else there is 0
+                code_m[o] = top_code(y0, random.m(e)) & 0x7fffffffu | __float_as_uint(y0) & 0x80000000u;
+                code_m[o + 1] = top_code(y1, random.m(e + 1)) & 0x7fffffffu | __float_as_uint(y1) & 0x80000000u;
                 f2_split(f2_mul(v2, uv), y0, y1);
-                uint32_t w0 = __float_as_uint(y0) + (random.v(e) >> 12);
-                uint32_t w1 = __float_as_uint(y1) + (random.v(e + 1) >> 12);
+                code_v[o] = top_code(y0, random.v(e));
+                code_v[o + 1] = top_code(y1, random.v(e + 1));
                 if (v[e] != 0.0f)
-                    w0 = max(w0, 1u << 20);
+                    code_v[o] = max(code_v[o], 1u << 24);
                 if (v[e + 1] != 0.0f)
-                    w1 = max(w1, 1u << 20);
-                code_v[o] = w0 << 4;
-                code_v[o + 1] = w1 << 4;
+                    code_v[o + 1] = max(code_v[o + 1], 1u << 24);
             }
             word_m[h] = top_bytes(code_m[0], code_m[1], code_m[2], code_m[3]);
             word_v[h] = top_bytes(code_v[0], code_v[1], code_v[2], code_v[3]);
@@ -883,16 +886,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw8(const __grid_con
 /* 8-bit states to values and back                                                        */
 /* ------------------------------------------------------------------------------------ */
 
-/* Codes as floats (raw_m, raw_v) to their values. */
-__device__ __forceinline__ void scale_values(float (&m)[8], float (&v)[8], float scale_m, float scale_v)
-{
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        m[e] = __fmul_rn(__fmul_rn(m[e], 0x1p112f), scale_m);
-        v[e] = __fmul_rn(__fmul_rn(v[e], 0x1p96f), scale_v);
-    }
-}
-
 /* A block's values, 8 per lane, to their nearest codes; the exponents (m's, v's). */
 __device__ __forceinline__ uint2 nearest_codes(const float (&m)[8], const float (&v)[8], uint2& cm, uint2& cv)
 {
@@ -916,9 +909,10 @@ __device__ __forceinline__ uint2 nearest_codes(const float (&m)[8], const float 
     return make_uint2(bm, bv);
 }
 
-/* Short lists: a warp per unit, straight from global memory. */
-template <Op OP, int CAP>
-__global__ void __launch_bounds__(kThreads, 4) k_tensors_codec(const __grid_constant__ ListArgs<CAP> a)
+/* A warp per unit, straight from global memory, as many warps as fit: there is little
+ * arithmetic to hide and twice to four times as much to write as to read. */
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 8) k_state8_read(const __grid_constant__ ListArgs<CAP> a)
 {
     const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
     uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -930,114 +924,148 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_codec(const __grid_cons
     for (; u < a.l.n_units; u += stride) {
         locate(a.l, u, place);
         const Ref& t = a.l.t[place.k];
-        const bool whole = whole_unit(t, place.unit);
+        const bool whole = whole_unit(t, place.unit), bf16 = t.flags & kValueBF16;
         const uint64_t at = (uint64_t)place.unit * kUnit + (whole ? lane * kPer : lane);
-        uint8_t* exps = t.exps + 2 * (uint64_t)place.unit;
-        uint8_t* cm = static_cast<uint8_t*>(t.m) + at;
-        uint8_t* cv = static_cast<uint8_t*>(t.v) + at;
-        float m[8], v[8];
-        if (OP == Op::kRead) {
-            if (whole) {
-                const uint2 wm = __ldcs(reinterpret_cast<const uint2*>(cm)), wv = __ldcs(reinterpret_cast<const uint2*>(cv));
+        const uint8_t* exps = t.exps + 2 * (uint64_t)place.unit;
+        const uint8_t* cm = static_cast<const uint8_t*>(t.m) + at;
+        const uint8_t* cv = static_cast<const uint8_t*>(t.v) + at;
+        const float scale_m = exp_scale(exps[0]), scale_v = exp_scale(exps[1]);
+        auto value_m = [&](float y) { return __fmul_rn(__fmul_rn(y, 0x1p112f), scale_m); };
+        auto value_v = [&](float y) { return __fmul_rn(__fmul_rn(y, 0x1p96f), scale_v); };
+        if (whole) {
+            const uint2 wm = __ldcs(reinterpret_cast<const uint2*>(cm)), wv = __ldcs(reinterpret_cast<const uint2*>(cv));
+            float m[8], v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    m[e] = raw_m(e < 4 ? wm.x : wm.y, e & 3);
-                    v[e] = raw_v(e < 4 ? wv.x : wv.y, e & 3);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const bool in = at + e * 32 < t.elems;
-                    m[e] = in ? raw_m(cm[e * 32], 0) : 0.0f;
-                    v[e] = in ? raw_v(cv[e * 32], 0) : 0.0f;
-                }
+            for (int e = 0; e < 8; ++e) {
+                m[e] = value_m(raw_m(e < 4 ? wm.x : wm.y, e & 3));
+                v[e] = value_v(raw_v(e < 4 ? wv.x : wv.y, e & 3));
             }
-            scale_values(m, v, exp_scale(exps[0]), exp_scale(exps[1]));
-            const bool bf16 = t.flags & kValueBF16;
-            if (whole && bf16) {
+            if (bf16) {
                 store_params8(static_cast<uint16_t*>(t.x) + at, 0, m);
                 store_params8(static_cast<uint16_t*>(t.y) + at, 0, v);
-            } else if (whole) {
+            } else {
                 store8(static_cast<float*>(t.x) + at, m);
                 store8(static_cast<float*>(t.y) + at, v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint64_t q = at + e * 32;
-                    if (q < t.elems && bf16) {
-                        static_cast<uint16_t*>(t.x)[q] = pack1<false>(m[e]);
-                        static_cast<uint16_t*>(t.y)[q] = pack1<false>(v[e]);
-                    } else if (q < t.elems) {
-                        static_cast<float*>(t.x)[q] = m[e];
-                        static_cast<float*>(t.y)[q] = v[e];
-                    }
-                }
             }
         } else {
-            const float* xm = static_cast<const float*>(t.x) + at;
-            const float* xv = static_cast<const float*>(t.y) + at;
-            if (whole) {
-                load8(xm, m);
-                load8(xv, v);
-            } else {
+            uint32_t c[8];  // m's code, v's above it
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    m[e] = at + e * 32 < t.elems ? __ldcs(xm + e * 32) : 0.0f;
-                    v[e] = at + e * 32 < t.elems ? __ldcs(xv + e * 32) : 0.0f;
+            for (int e = 0; e < 8; ++e)
+                c[e] = at + e * 32 < t.elems ? cm[e * 32] | cv[e * 32] << 8 : 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint64_t q = at + e * 32;
+                if (q >= t.elems)
+                    continue;
+                const float m = value_m(raw_m(c[e], 0)), v = value_v(raw_v(c[e], 1));
+                if (bf16) {
+                    static_cast<uint16_t*>(t.x)[q] = pack1<false>(m);
+                    static_cast<uint16_t*>(t.y)[q] = pack1<false>(v);
+                } else {
+                    static_cast<float*>(t.x)[q] = m;
+                    static_cast<float*>(t.y)[q] = v;
                 }
-            }
-            uint2 wm, wv;
-            const uint2 b = nearest_codes(m, v, wm, wv);
-            if (whole) {
-                __stcs(reinterpret_cast<uint2*>(cm), wm);
-                __stcs(reinterpret_cast<uint2*>(cv), wv);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (at + e * 32 < t.elems) {
-                        cm[e * 32] = (uint8_t)((e < 4 ? wm.x : wm.y) >> (8 * (e & 3)));
-                        cv[e * 32] = (uint8_t)((e < 4 ? wv.x : wv.y) >> (8 * (e & 3)));
-                    }
-            }
-            if (lane == 0) {
-                exps[0] = (uint8_t)b.x;
-                exps[1] = (uint8_t)b.y;
             }
         }
     }
 }
 
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 6) k_state8_write(const __grid_constant__ ListArgs<CAP> a)
+{
+    const uint32_t lane = threadIdx.x & 31, stride = gridDim.x * kWarps;
+    uint32_t u = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    Place place{0, 1, 0, 0};
+    if (u < a.l.n_units)
+        locate(a.l, u, place);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (; u < a.l.n_units; u += stride) {
+        locate(a.l, u, place);
+        const Ref& t = a.l.t[place.k];
+        const bool whole = whole_unit(t, place.unit);
+        const uint64_t at = (uint64_t)place.unit * kUnit + (whole ? lane * kPer : lane);
+        const float* xm = static_cast<const float*>(t.x) + at;
+        const float* xv = static_cast<const float*>(t.y) + at;
+        uint8_t* cm = static_cast<uint8_t*>(t.m) + at;
+        uint8_t* cv = static_cast<uint8_t*>(t.v) + at;
+        float m[8], v[8];
+        if (whole) {
+            load8(xm, m);
+            load8(xv, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                m[e] = at + e * 32 < t.elems ? __ldcs(xm + e * 32) : 0.0f;
+                v[e] = at + e * 32 < t.elems ? __ldcs(xv + e * 32) : 0.0f;
+            }
+        }
+        uint2 wm, wv;
+        const uint2 b = nearest_codes(m, v, wm, wv);
+        if (whole) {
+            __stcs(reinterpret_cast<uint2*>(cm), wm);
+            __stcs(reinterpret_cast<uint2*>(cv), wv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e * 32 < t.elems) {
+                    cm[e * 32] = (uint8_t)((e < 4 ? wm.x : wm.y) >> (8 * (e & 3)));
+                    cv[e * 32] = (uint8_t)((e < 4 ? wv.x : wv.y) >> (8 * (e & 3)));
+                }
+        }
+        if (lane == 0) {
+            t.exps[2 * (uint64_t)place.unit] = (uint8_t)b.x;
+            t.exps[2 * (uint64_t)place.unit + 1] = (uint8_t)b.y;
+        }
+    }
+}
+
 /* ------------------------------------------------------------------------------------ */
-/* long lists: staged through shared memory                                               */
+/* AdamW on long lists: staged through shared memory                                      */
 /* ------------------------------------------------------------------------------------ */
 
-/* One block per SM: a producer warp fills a ring of stages with the bulk-copy engine, 16
+/* One block per SM: a producer warp fills a ring of stages with the bulk-copy engine, the
  * consumer warps take a 256-element unit each from every stage, release it as soon as its
  * values are in registers, and store their results straight to global memory.  A stage is
- * a chunk of at most 4096 elements of one tensor. */
-constexpr int kRingWarps = 16;
-constexpr int kRingThreads = (kRingWarps + 1) * 32;
-constexpr uint32_t kRingChunk = kRingWarps * kUnit;
-constexpr uint32_t kNoTensor = ~0u;
-
-/* What a stage holds, by operator: up to five arrays' parts of the chunk, each in a slot
- * 128 bytes longer than its data (an array that does not start on 16 bytes keeps its
- * offset from the boundary below).  As many stages as shared memory takes, 16 at most. */
-template <Op OP>
+ * a chunk of one tensor, a unit for each consumer warp; its slots are 128 bytes longer than
+ * a chunk's data: an array that does not start on 16 bytes keeps its offset from the
+ * boundary below. */
+template <bool S8>
 struct Ring {
-    static constexpr bool kStep = OP == Op::kAdamw || OP == Op::kAdamw8;
-    static constexpr uint32_t kWide = kRingChunk * 4 + 128, kState = (OP == Op::kAdamw8 || OP == Op::kRead ? 1 : 4) * kRingChunk + 128;
-    static constexpr uint32_t kGrad = 0, kMaster = kWide;          // AdamW only
-    static constexpr uint32_t kM = kStep ? 2 * kWide : 0, kV = kM + kState;
-    static constexpr uint32_t kExps = kV + kState;                 // codes read, only
-    static constexpr uint32_t kBytes = kExps + (OP == Op::kAdamw8 || OP == Op::kRead ? 256 : 0);
-    static constexpr uint32_t kFit = 216 * 1024 / kBytes;
-    static constexpr uint32_t kStages = kFit < 16 ? kFit : 16, kSmem = kBytes * kStages;
+    static constexpr int kWarps = S8 ? 23 : 16, kThreads = (kWarps + 1) * 32;
+    static constexpr uint32_t kChunk = kWarps * kUnit;
+    static constexpr uint32_t kWide = kChunk * 4 + 128, kState = kChunk * (S8 ? 1 : 4) + 128;
+    static constexpr uint32_t kGrad = 0, kMaster = kWide, kM = 2 * kWide, kV = kM + kState, kExps = kV + kState;
+    static constexpr uint32_t kBytes = kExps + (S8 ? 256 : 0);
+    static constexpr uint32_t kStages = 3, kSmem = kBytes * kStages;
+};
+static_assert(Ring<false>::kSmem <= 220 * 1024 && Ring<true>::kSmem <= 220 * 1024, "shared memory");
+
+/* What the producer tells the consumers of a stage, so that each warp need not work it out:
+ * arrays at the chunk's first element. */
+struct alignas(16) StageInfo {
+    uint32_t n;      // elements; 0: the queue is empty
+    uint32_t flags;  // the tensor's
+    float lr_scale, decay;
+    uint32_t group;  // 8-bit states: the chunk's first group of 8 elements
+    uint32_t grad, master, m, v, exps;  // in the stage
+    float* out_master;
+    char* out_m;
+    char* out_v;
+    uint8_t* out_exps;
+    uint16_t* out_params;  // or null
 };
 
-struct StageInfo {
-    uint32_t k, chunk;  // the tensor (kNoTensor: the queue is empty) and the chunk's number in it
-};
+/* Phase `parity` of a stage's barrier; the clock is read only where the first try fails. */
+__device__ __forceinline__ bool stage_wait(const uint64_t& bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(smem_addr(&bar)), "r"(parity)
+                 : "memory");
+    return ok || wait_parity_bounded(smem_addr(&bar), parity);
+}
 
 /* The producer warp's copy of bytes [at, at + len) of an array of `bytes` bytes into a
  * slot, at the same offset from a 16-byte boundary.  Whole 16-byte granules go by bulk
@@ -1047,6 +1075,7 @@ struct StageInfo {
 struct SlotCopy {
     const char* from;
     uint32_t dst, len;
+    uint32_t offset;  // the first byte's place in the slot
 
     __device__ __forceinline__ SlotCopy(const void* base, uint64_t bytes, uint64_t at, uint32_t n, char* slot,
                                         uint32_t lane)
@@ -1068,6 +1097,7 @@ struct SlotCopy {
                 slot[x - origin] = *reinterpret_cast<const char*>(x);
         }
         from = reinterpret_cast<const char*>(lo);
+        offset = (uint32_t)(first - origin);
         dst = smem_addr(slot) + (uint32_t)(lo - origin);
         len = (uint32_t)(hi - lo);
     }
@@ -1078,26 +1108,26 @@ struct SlotCopy {
     }
 };
 
-/* Fills the stages until the list's chunks are used up.  The steps take them from a queue
- * in the step state, one at a time, so that the chunks in flight stay together at the
- * front of the list however the blocks' speeds differ; the codec, which has no step state,
- * takes every gridDim.x-th. */
-template <Op OP, int CAP>
+/* Fills the stages until the list's chunks are used up: one at a time from a queue in the
+ * step state, so that the chunks in flight stay together at the front of the list however
+ * the blocks' speeds differ. */
+template <bool S8, int CAP>
 __device__ __forceinline__ void produce(const ListArgs<CAP>& a, char* stages, uint64_t* full, uint64_t* empty,
                                         StageInfo* info)
 {
-    using R = Ring<OP>;
+    using R = Ring<S8>;
     const uint32_t lane = threadIdx.x & 31;
     zero_step_state_t* st = const_cast<zero_step_state_t*>(a.st);
-    unsigned long long next = blockIdx.x;
-    if (R::kStep && lane == 0)
-        next = atomicAdd(reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk), 1ull);
+    unsigned long long* queue = reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk);
+    unsigned long long next = 0;
+    if (lane == 0)
+        next = atomicAdd(queue, 1ull);
     Place at{0, 1, 0, 0};
     uint32_t issued = 0, live = R::kStages - 1;  // stages before `issued` that may be unread
     for (;; ++issued) {
         const uint32_t k = issued % R::kStages;
-        if (issued >= R::kStages && !wait_parity_bounded(smem_addr(&empty[k]), (issued / R::kStages - 1) & 1)) {
-            if (lane == 0 && st)
+        if (issued >= R::kStages && !stage_wait(empty[k], (issued / R::kStages - 1) & 1)) {
+            if (lane == 0)
                 atomicOr(&st->error, 1u);
             live = R::kStages;
             break;
@@ -1106,34 +1136,28 @@ __device__ __forceinline__ void produce(const ListArgs<CAP>& a, char* stages, ui
         const uint32_t bar = smem_addr(&full[k]);
         if (c >= a.l.n_units) {
             if (lane == 0) {
-                info[k].k = kNoTensor;
+                info[k].n = 0;
                 asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
             }
             break;
         }
-        if (!R::kStep)
-            next = c + gridDim.x;
-        else if (lane == 0)  // one ahead: its latency stays off the ring's path
-            next = atomicAdd(reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk), 1ull);
+        if (lane == 0)  // one ahead: its latency stays off the ring's path
+            next = atomicAdd(queue, 1ull);
         locate(a.l, (uint32_t)c, at);
         const Ref& t = a.l.t[at.k];
         char* s = stages + k * R::kBytes;
-        const uint64_t first = (uint64_t)at.unit * kRingChunk;
-        const uint32_t n = t.elems - first < kRingChunk ? (uint32_t)(t.elems - first) : kRingChunk;
+        const uint64_t first = (uint64_t)at.unit * R::kChunk;
+        const uint32_t n = t.elems - first < R::kChunk ? (uint32_t)(t.elems - first) : R::kChunk;
         auto copy = [&](const void* base, uint32_t size, uint32_t slot) {
             return SlotCopy(base, t.elems * size, first * size, n * size, s + slot, lane);
         };
-        constexpr uint32_t kSize = OP == Op::kAdamw8 || OP == Op::kRead ? 1 : 4;
-        const SlotCopy m = copy(OP == Op::kWrite ? t.x : t.m, kSize, R::kM);
-        const SlotCopy v = copy(OP == Op::kWrite ? t.y : t.v, kSize, R::kV);
-        SlotCopy g = m, p = m, b = m;
-        uint32_t bytes = m.len + v.len;
-        if (R::kStep) {
-            g = copy(t.grad, (t.flags & kGradMask) == ZERO_F32 ? 4 : 2, R::kGrad);
-            p = copy(t.master, 4, R::kMaster);
-            bytes += g.len + p.len;
-        }
-        if (kSize == 1) {
+        const SlotCopy g = copy(t.grad, (t.flags & kGradMask) == ZERO_F32 ? 4 : 2, R::kGrad);
+        const SlotCopy p = copy(t.master, 4, R::kMaster);
+        const SlotCopy m = copy(t.m, S8 ? 1 : 4, R::kM);
+        const SlotCopy v = copy(t.v, S8 ? 1 : 4, R::kV);
+        SlotCopy b = m;
+        uint32_t bytes = g.len + p.len + m.len + v.len;
+        if (S8) {
             b = SlotCopy(t.exps, (t.elems + kUnit - 1) / kUnit * 2, first / kUnit * 2, (n + kUnit - 1) / kUnit * 2,
                          s + R::kExps, lane);
             bytes += b.len;
@@ -1143,15 +1167,28 @@ __device__ __forceinline__ void produce(const ListArgs<CAP>& a, char* stages, ui
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
-            info[k] = StageInfo{at.k, at.unit};
+            StageInfo& w = info[k];
+            w.n = n;
+            w.flags = t.flags;
+            w.lr_scale = t.lr_scale;
+            w.decay = t.decay;
+            w.group = t.group0 + (uint32_t)(first / kPer);
+            w.grad = R::kGrad + g.offset;
+            w.master = R::kMaster + p.offset;
+            w.m = R::kM + m.offset;
+            w.v = R::kV + v.offset;
+            w.exps = S8 ? R::kExps + b.offset : 0;
+            w.out_master = t.master + first;
+            w.out_m = static_cast<char*>(t.m) + first * (S8 ? 1 : 4);
+            w.out_v = static_cast<char*>(t.v) + first * (S8 ? 1 : 4);
+            w.out_exps = S8 ? t.exps + first / kUnit * 2 : nullptr;
+            w.out_params = t.params ? t.params + first : nullptr;
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+            g.bulk(bar);
+            p.bulk(bar);
             m.bulk(bar);
             v.bulk(bar);
-            if (R::kStep) {
-                g.bulk(bar);
-                p.bulk(bar);
-            }
-            if (kSize == 1)
+            if (S8)
                 b.bulk(bar);
         }
     }
@@ -1159,49 +1196,45 @@ __device__ __forceinline__ void produce(const ListArgs<CAP>& a, char* stages, ui
     // unread)
     for (uint32_t i = issued > live ? issued - live : 0; i < issued; ++i)
         wait_parity_bounded(smem_addr(&full[i % R::kStages]), (i / R::kStages) & 1);
-    if (R::kStep && lane == 0) {  // the queue back to 0 for the next launch, by the last block
+    if (lane == 0) {  // the queue back to 0 for the next launch, by the last block
         __threadfence();
         if (atomicAdd(&st->adamw_done, 1u) == gridDim.x - 1) {
             __threadfence();
-            atomicExch(reinterpret_cast<unsigned long long*>(&st->adamw_next_chunk), 0ull);
+            atomicExch(queue, 0ull);
             atomicExch(&st->adamw_done, 0u);
         }
     }
 }
 
-/* A warp's unit of a stage: where it lies, and its lanes' elements: 8 consecutive ones
- * where every array allows it, else one of every 32. */
+/* A lane's elements of a stage: 8 consecutive ones where every array allows it and the
+ * warp's unit is whole, else one of every 32. */
 struct InStage {
     const char* slot;
-    uint64_t first, at;  // the stage's and this lane's first element in the tensor
-    uint32_t e0;         // at - first
+    uint32_t e0, n;  // the first of them; the stage's elements
     bool whole;
 
-    template <typename T>
-    __device__ __forceinline__ const T* in(uint32_t array, const void* base) const
+    __device__ __forceinline__ bool in(int e) const { return e0 + e * 32 < n; }
+
+    __device__ __forceinline__ void floats(uint32_t array, float (&to)[8]) const
     {
-        return reinterpret_cast<const T*>(slot + array + (((uintptr_t)base + first * sizeof(T)) & 15u)) + e0;
-    }
-    __device__ __forceinline__ void floats(uint32_t array, const void* base, float (&to)[8]) const
-    {
-        const float* from = in<float>(array, base);
+        const float* from = reinterpret_cast<const float*>(slot + array) + e0;
         if (whole) {
             const float4 lo = reinterpret_cast<const float4*>(from)[0], hi = reinterpret_cast<const float4*>(from)[1];
             to[0] = lo.x, to[1] = lo.y, to[2] = lo.z, to[3] = lo.w;
             to[4] = hi.x, to[5] = hi.y, to[6] = hi.z, to[7] = hi.w;
-        } else {
+        } else {  // past n: what the slot holds there, never stored
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 to[e] = from[e * 32];
         }
     }
-    __device__ __forceinline__ void grads(uint32_t array, const void* base, uint32_t dtype, float (&to)[8]) const
+    __device__ __forceinline__ void grads(uint32_t array, uint32_t dtype, float (&to)[8]) const
     {
         if (dtype == ZERO_F32) {
-            floats(array, base, to);
+            floats(array, to);
             return;
         }
-        const uint16_t* from = in<uint16_t>(array, base);
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(slot + array) + e0;
         if (whole) {
             const uint4 w = *reinterpret_cast<const uint4*>(from);
             if (dtype == ZERO_F16)
@@ -1214,12 +1247,12 @@ struct InStage {
                 to[e] = dtype == ZERO_F16 ? one16<ZERO_F16>(from[e * 32]) : one16<ZERO_BF16>(from[e * 32]);
         }
     }
-    /* The codes of m and v as floats; 0 past the tensor's end, so that what lies there does
-     * not count in the block's exponents. */
-    __device__ __forceinline__ void codes(uint32_t m, uint32_t v, const Ref& t, float (&ym)[8], float (&yv)[8]) const
+    /* The codes of m and v as floats; 0 past n, so that what lies there does not count in
+     * the block's exponents. */
+    __device__ __forceinline__ void codes(uint32_t m, uint32_t v, float (&ym)[8], float (&yv)[8]) const
     {
-        const uint8_t* cm = in<uint8_t>(m, t.m);
-        const uint8_t* cv = in<uint8_t>(v, t.v);
+        const uint8_t* cm = reinterpret_cast<const uint8_t*>(slot + m) + e0;
+        const uint8_t* cv = reinterpret_cast<const uint8_t*>(slot + v) + e0;
         if (whole) {
             const uint2 wm = *reinterpret_cast<const uint2*>(cm), wv = *reinterpret_cast<const uint2*>(cv);
 #pragma unroll
@@ -1230,190 +1263,148 @@ struct InStage {
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const bool inside = at + e * 32 < t.elems;
-                ym[e] = inside ? raw_m(cm[e * 32], 0) : 0.0f;
-                yv[e] = inside ? raw_v(cv[e * 32], 0) : 0.0f;
+                ym[e] = in(e) ? raw_m(cm[e * 32], 0) : 0.0f;
+                yv[e] = in(e) ? raw_v(cv[e * 32], 0) : 0.0f;
             }
         }
     }
-    __device__ __forceinline__ void put(float* to, const Ref& t, const float (&x)[8]) const
+    __device__ __forceinline__ void put(void* to, const float (&x)[8]) const
     {
+        float* p = static_cast<float*>(to) + e0;
         if (whole) {
-            store8(to + at, x);
+            store8(p, x);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (at + e * 32 < t.elems)
-                    __stcs(to + at + e * 32, x[e]);
+                if (in(e))
+                    __stcs(p + e * 32, x[e]);
         }
     }
-    __device__ __forceinline__ void put16(uint16_t* to, const Ref& t, bool f16, const float (&x)[8]) const
+    __device__ __forceinline__ void put_params(uint16_t* to, bool f16, const float (&x)[8]) const
     {
         if (whole) {
-            store_params8(to + at, f16, x);
+            store_params8(to + e0, f16, x);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (at + e * 32 < t.elems)
-                    to[at + e * 32] = f16 ? pack1<true>(x[e]) : pack1<false>(x[e]);
+                if (in(e))
+                    to[e0 + e * 32] = f16 ? pack1<true>(x[e]) : pack1<false>(x[e]);
         }
     }
-    __device__ __forceinline__ void put_codes(void* to, const Ref& t, uint2 c) const
+    __device__ __forceinline__ void put_codes(char* to, uint2 c) const
     {
-        uint8_t* p = static_cast<uint8_t*>(to) + at;
         if (whole) {
-            __stcs(reinterpret_cast<uint2*>(p), c);
+            __stcs(reinterpret_cast<uint2*>(to + e0), c);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (at + e * 32 < t.elems)
-                    p[e * 32] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+                if (in(e))
+                    to[e0 + e * 32] = (char)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
         }
     }
 };
 
-template <Op OP, int CAP>
-__global__ void __launch_bounds__(kRingThreads, 1) k_tensors_ring(const __grid_constant__ ListArgs<CAP> a)
+template <bool S8, int CAP>
+__global__ void __launch_bounds__(Ring<S8>::kThreads, 1) k_tensors_ring(const __grid_constant__ ListArgs<CAP> a)
 {
-    using R = Ring<OP>;
+    using R = Ring<S8>;
     extern __shared__ __align__(128) char stages[];
     __shared__ __align__(8) uint64_t full[R::kStages], empty[R::kStages];
     __shared__ StageInfo info[R::kStages];
     grid_dependency_wait();
-    if (R::kStep && a.st->skip)
+    if (a.st->skip)
         return;
     if (threadIdx.x == 0) {
         for (uint32_t k = 0; k < R::kStages; ++k) {
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[k])));
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[k])), "n"(kRingWarps));
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty[k])), "n"(R::kWarps));
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == kRingWarps) {
-        produce<OP>(a, stages, full, empty, info);
+    if (warp == R::kWarps) {
+        produce<S8>(a, stages, full, empty, info);
         return;
     }
     Scalars s;
     Step8 s8;
     float inv = 1.0f, step = 0.0f;
-    if (OP == Op::kAdamw) {
+    if (S8) {
+        s8 = step8(a);
+        step = s8.step;
+    } else {
         s = step_scalars(a);
         inv = a.st->inv_scale_used;
         step = s.step;
-    } else if (OP == Op::kAdamw8) {
-        s8 = step8(a);
-        step = s8.step;
     }
     for (uint32_t i = 0;; ++i) {
-        const uint32_t q = i % R::kStages, bar = smem_addr(&empty[q]);
-        if (!wait_parity_bounded(smem_addr(&full[q]), (i / R::kStages) & 1)) {
-            if (R::kStep && lane == 0)
+        const uint32_t q = i % R::kStages;
+        if (!stage_wait(full[q], (i / R::kStages) & 1)) {
+            if (lane == 0)
                 atomicOr(&const_cast<zero_step_state_t*>(a.st)->error, 1u);
             return;
         }
-        const StageInfo where = info[q];
-        if (where.k == kNoTensor)
+        const StageInfo t = info[q];
+        if (t.n == 0)
             return;
         auto release = [&] {  // this warp has what it needs of the stage
             __syncwarp();
             if (lane == 0)
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty[q])) : "memory");
         };
-        const Ref& t = a.l.t[where.k];
-        const uint64_t first = (uint64_t)where.chunk * kRingChunk, off = first + warp * kUnit;
-        if (off >= t.elems) {
+        if (warp * kUnit >= t.n) {
             release();
             continue;
         }
         InStage u;
         u.slot = stages + q * R::kBytes;
-        u.first = first;
-        u.whole = (t.flags & kVector) && off + kUnit <= t.elems;
+        u.n = t.n;
+        u.whole = (t.flags & kVector) && (warp + 1) * kUnit <= t.n;
         u.e0 = warp * kUnit + (u.whole ? lane * kPer : lane);
-        u.at = first + u.e0;
-        uint8_t* exps = t.exps + off / kUnit * 2;
-        const uint8_t* b = reinterpret_cast<const uint8_t*>(u.slot + R::kExps + (((uintptr_t)t.exps + first / kUnit * 2) & 15u)) + 2 * warp;
-        if (OP == Op::kAdamw) {
-            float x[8], p[8], m[8], v[8];
-            u.grads(R::kGrad, t.grad, t.flags & kGradMask, x);
-            u.floats(R::kMaster, t.master, p);
-            u.floats(R::kM, t.m, m);
-            u.floats(R::kV, t.v, v);
-            release();
-            s.step = __fmul_rn(step, t.lr_scale);
-            s.decay = t.decay;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                adamw_one(__fmul_rn(x[e], inv), p[e], m[e], v[e], s);
-            u.put(static_cast<float*>(t.m), t, m);
-            u.put(static_cast<float*>(t.v), t, v);
-            u.put(t.master, t, p);
-            if (t.params)
-                u.put16(t.params, t, t.flags & kOutF16, p);
-        } else if (OP == Op::kAdamw8) {
-            float x[8], p[8], ym[8], yv[8];
-            u.grads(R::kGrad, t.grad, t.flags & kGradMask, x);
-            u.floats(R::kMaster, t.master, p);
-            u.codes(R::kM, R::kV, t, ym, yv);
+        float x[8], p[8];
+        u.grads(t.grad, t.flags & kGradMask, x);
+        u.floats(t.master, p);
+        if (S8) {
+            const uint8_t* b = reinterpret_cast<const uint8_t*>(u.slot + t.exps) + 2 * warp;
+            float ym[8], yv[8];
+            u.codes(t.m, t.v, ym, yv);
             uint32_t bm = b[0], bv = b[1];
             release();
             s8.step = __fmul_rn(step, t.lr_scale);
             s8.decay = t.decay;
-            const uint32_t seed = mix32(s8.key + (t.group0 + (uint32_t)(off / kPer) + lane) * kGolden);
+            const uint32_t seed = mix32(s8.key + (t.group + warp * 32 + lane) * kGolden);
             uint2 cm, cv;
             if (u.whole) {
                 block8(x, p, ym, yv, bm, bv, RandomInGroup{seed}, cm, cv, s8);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    x[e] = u.at + e * 32 < t.elems ? x[e] : 0.0f;
+                    x[e] = u.in(e) ? x[e] : 0.0f;
                 block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s8);
             }
-            u.put_codes(t.m, t, cm);
-            u.put_codes(t.v, t, cv);
-            u.put(t.master, t, p);
-            if (t.params)
-                u.put16(t.params, t, t.flags & kOutF16, p);
+            u.put_codes(t.out_m, cm);
+            u.put_codes(t.out_v, cv);
             if (lane == 0) {
-                exps[0] = (uint8_t)bm;
-                exps[1] = (uint8_t)bv;
-            }
-        } else if (OP == Op::kRead) {
-            float m[8], v[8];
-            u.codes(R::kM, R::kV, t, m, v);
-            const float scale_m = exp_scale(b[0]), scale_v = exp_scale(b[1]);
-            release();
-            scale_values(m, v, scale_m, scale_v);
-            if (t.flags & kValueBF16) {
-                u.put16(static_cast<uint16_t*>(t.x), t, false, m);
-                u.put16(static_cast<uint16_t*>(t.y), t, false, v);
-            } else {
-                u.put(static_cast<float*>(t.x), t, m);
-                u.put(static_cast<float*>(t.y), t, v);
+                t.out_exps[2 * warp] = (uint8_t)bm;
+                t.out_exps[2 * warp + 1] = (uint8_t)bv;
             }
         } else {
             float m[8], v[8];
-            u.floats(R::kM, t.x, m);
-            u.floats(R::kV, t.y, v);
+            u.floats(t.m, m);
+            u.floats(t.v, v);
             release();
-            if (!u.whole) {
+            s.step = __fmul_rn(step, t.lr_scale);
+            s.decay = t.decay;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    m[e] = u.at + e * 32 < t.elems ? m[e] : 0.0f;
-                    v[e] = u.at + e * 32 < t.elems ? v[e] : 0.0f;
-                }
-            }
-            uint2 cm, cv;
-            const uint2 top = nearest_codes(m, v, cm, cv);
-            u.put_codes(t.m, t, cm);
-            u.put_codes(t.v, t, cv);
-            if (lane == 0) {
-                exps[0] = (uint8_t)top.x;
-                exps[1] = (uint8_t)top.y;
-            }
+            for (int e = 0; e < 8; ++e)
+                adamw_one(__fmul_rn(x[e], inv), p[e], m[e], v[e], s);
+            u.put(t.out_m, m);
+            u.put(t.out_v, v);
         }
+        u.put(t.out_master, p);
+        if (t.out_params)
+            u.put_params(t.out_params, t.flags & kOutF16, p);
     }
 }
 
@@ -1619,44 +1610,44 @@ int launch_units(void (*kernel)(Args), std::atomic<int> (&per_sm)[64], uint32_t 
 }
 
 /* The staged form: one block per SM. */
-template <typename Args>
-int launch_ring(void (*kernel)(Args), std::atomic<bool> (&configured)[64], uint32_t smem, uint32_t chunks,
-                cudaStream_t s, const Args& a)
+template <bool S8, int CAP>
+int launch_ring(const ListArgs<CAP>& a, cudaStream_t s)
 {
+    static std::atomic<bool> configured[64];  // per device; a race only repeats the set-up
     int dev = 0;
     cudaGetDevice(&dev);
     if (!configured[dev & 63].load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(k_tensors_ring<S8, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)Ring<S8>::kSmem);
         if (e != cudaSuccess)
             return status_of(e);
         configured[dev & 63].store(true, std::memory_order_relaxed);
     }
-    const uint32_t cap = (uint32_t)sm_count();
-    return status_of(launch_pdl(kernel, dim3(chunks < cap ? chunks : cap), dim3(kRingThreads), smem, s, a));
+    const uint32_t cap = (uint32_t)sm_count(), want = a.l.n_units;
+    return status_of(launch_pdl(k_tensors_ring<S8, CAP>, dim3(want < cap ? want : cap), dim3(Ring<S8>::kThreads),
+                                Ring<S8>::kSmem, s, a));
 }
 
-template <Op OP, int CAP>
-int launch_list(void (*direct)(ListArgs<CAP>), const ListArgs<CAP>& a, bool ring, cudaStream_t s)
-{
-    static std::atomic<int> occ[64];  // per device; a race only repeats the set-up
-    static std::atomic<bool> configured[64];
-    if (ring)
-        return launch_ring(k_tensors_ring<OP, CAP>, configured, Ring<OP>::kSmem, a.l.n_units, s, a);
-    return launch_units(direct, occ, a.l.n_units, s, a);
-}
-
+/* One launch of an operator over its part of the list. */
 template <int CAP>
 int launch_op(const ListArgs<CAP>& a, Op op, bool ring, cudaStream_t s)
 {
+    static std::atomic<int> occ[4][64];  // per device; a race only repeats the set-up
+    const uint32_t n = a.l.n_units;
     switch (op) {
-    case Op::kAdamw: return launch_list<Op::kAdamw>(k_tensors_adamw<CAP>, a, ring, s);
-    case Op::kAdamw8: return launch_list<Op::kAdamw8>(k_tensors_adamw8<CAP>, a, ring, s);
-    case Op::kRead: return launch_list<Op::kRead>(k_tensors_codec<Op::kRead, CAP>, a, ring, s);
-    default: return launch_list<Op::kWrite>(k_tensors_codec<Op::kWrite, CAP>, a, ring, s);
+    case Op::kAdamw:
+        return ring ? launch_ring<false>(a, s) : launch_units(k_tensors_adamw<CAP>, occ[0], n, s, a);
+    case Op::kAdamw8:
+        return ring ? launch_ring<true>(a, s) : launch_units(k_tensors_adamw8<CAP>, occ[1], n, s, a);
+    case Op::kRead: return launch_units(k_state8_read<CAP>, occ[2], n, s, a);
+    default: return launch_units(k_state8_write<CAP>, occ[3], n, s, a);
     }
 }
 
-constexpr uint64_t kRingElems = 1u << 21;
+/* Lists of this many elements take the staged kernel.  Measured, direct against staged, us a
+ * launch (32-bit states; 8-bit): 2^20 elements 5.3 / 8.9 (4.2 / 7.1), 2^22 21.8 / 22.7
+ * (14.8 / 15.1), 2^23 41.0 / 39.7 (25.9 / 24.7), 2^24 78.7 / 73.0 (51.0 / 43.8). */
+constexpr uint64_t kRingElems = 3ull << 21;
 
 int run_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
              const zero_adamw_hparams_t* hp, uint64_t seed, const zero_step_state_t* st, cudaStream_t s, Op op)
@@ -1671,10 +1662,11 @@ int run_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t
     uint64_t total = 0;
     for (uint64_t k = 0; k < n; ++k)
         total += tensors[k].elems;
-    const bool ring = total >= kRingElems;
+    const bool ring = total >= kRingElems && (op == Op::kAdamw || op == Op::kAdamw8);
+    const uint32_t unit = !ring ? kUnit : op == Op::kAdamw ? Ring<false>::kChunk : Ring<true>::kChunk;
     uint32_t group0 = 0;
     for (uint64_t next = 0; next < n;) {
-        next = fill(a.l, tensors, others, n, next, op, hp, group0, ring ? kRingChunk : kUnit);
+        next = fill(a.l, tensors, others, n, next, op, hp, group0, unit);
         if (a.l.n == 0)
             continue;
         int rc;
