@@ -318,10 +318,16 @@ def zero_step_static_workspace(layout: Layout, hp: HParams, dtype: int, replicas
 # --------------------------------------------------------------------------------------
 # lists of tensors
 # --------------------------------------------------------------------------------------
-def _dtype_code(t) -> int:
-    import torch
-    return {torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32,
-            torch.uint8: ZERO_U8}.get(t.dtype, 0)
+_CODES = {}
+
+
+def _dtype_codes() -> dict:
+    """torch dtypes to zero_dtype_t; 16-bit integers to 0 (parameters' bit patterns)."""
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32,
+                       torch.uint8: ZERO_U8, torch.int16: 0, torch.uint16: 0})
+    return _CODES
 
 
 class TensorList:
@@ -337,7 +343,8 @@ class TensorList:
     have moved."""
 
     _TYPES = {"grad": (ZERO_F16, ZERO_BF16, ZERO_F32), "master": (ZERO_F32,), "exps": (ZERO_U8,),
-              "m": (ZERO_F32, ZERO_BF16, ZERO_U8), "v": (ZERO_F32, ZERO_BF16, ZERO_U8)}
+              "m": (ZERO_F32, ZERO_BF16, ZERO_U8), "v": (ZERO_F32, ZERO_BF16, ZERO_U8),
+              "params": (ZERO_F16, ZERO_BF16, 0)}
 
     def __init__(self, grad=None, master=None, m=None, v=None, exps=None, params=None, lr_scale=1.0,
                  weight_decay=0.0):
@@ -345,29 +352,28 @@ class TensorList:
         self.tensors = {k: list(x) for k, x in arrays.items() if x is not None}
         if not self.tensors or list(self.tensors) == ["exps"]:
             raise ValueError("a list of tensors needs at least one of grad, master, m, v, params")
-        first = next(iter(self.tensors.values()))
-        self.device = first[0].device if first else None
-        self.elems = [t.numel() for t in first]
-        self.array = (Tensor * max(len(first), 1))()
-        for k, x in self.tensors.items():
-            self._check_length(k, x)
-        for k, x in self.tensors.items():
-            self._check(k, x)
         if ("m" in self.tensors) != ("v" in self.tensors):
             raise ValueError("m and v come together")
-        scales, decays = self._numbers(lr_scale), self._numbers(weight_decay)
-        for i, a in enumerate(self.array[:len(first)]):
-            a.elems, a.lr_scale, a.weight_decay = self.elems[i], scales[i], decays[i]
-            for k, x in self.tensors.items():
-                setattr(a, k, x[i].data_ptr())
-            if "grad" in self.tensors:
-                a.grad_dtype = _dtype_code(self.tensors["grad"][i])
-            if "m" in self.tensors:
-                a.state_dtype = _dtype_code(self.tensors["m"][i])
-                if a.state_dtype != _dtype_code(self.tensors["v"][i]):
-                    raise ValueError(f"m[{i}] and v[{i}] differ in type")
-            if "params" in self.tensors:
-                a.params_dtype = _dtype_code(self.tensors["params"][i])
+        first = next(iter(self.tensors.values()))
+        self.elems = [t.numel() for t in first]
+        self.device = first[0].get_device() if first else -1
+        n = len(first)
+        for k, x in self.tensors.items():
+            if len(x) != n:
+                raise ValueError(f"{k} has {len(x)} tensors, the list {n}")
+        codes = {k: self._check(k, x) for k, x in self.tensors.items()}
+        if codes.get("m") != codes.get("v"):
+            i = next(i for i, (a, b) in enumerate(zip(codes["m"], codes["v"])) if a != b)
+            raise ValueError(f"m[{i}] and v[{i}] differ in type")
+        none = [None] * n
+        ptr = {k: [t.data_ptr() for t in x] for k, x in self.tensors.items()}
+        zeros = [0] * n
+        self.array = (Tensor * max(n, 1))()
+        for i, row in enumerate(zip(
+                self.elems, *(ptr.get(k, none) for k in ("grad", "master", "m", "v", "exps", "params")),
+                *(codes.get(k, zeros) for k in ("grad", "m", "params")), self._numbers(lr_scale),
+                self._numbers(weight_decay))):
+            self.array[i] = row
 
     def __len__(self) -> int:
         return len(self.elems)
@@ -378,34 +384,30 @@ class TensorList:
             raise ValueError("lr_scale and weight_decay: one number, or one per tensor")
         return x
 
-    def _check_length(self, name: str, xs: list) -> None:
-        if len(xs) != len(self):
-            raise ValueError(f"{name} has {len(xs)} tensors, the list {len(self)}")
-
-    def _check(self, name: str, xs: list) -> None:
+    def _check(self, name: str, xs: list) -> list:
+        """The tensors' type codes, once every one of them is what the kernels take."""
+        known, types, device, codes = _dtype_codes(), self._TYPES[name], self.device, []
         for i, (t, n) in enumerate(zip(xs, self.elems)):
-            code = _dtype_code(t)
             want = 2 * -(-n // ZERO_STATE8_BLOCK) if name == "exps" else n
             if t.numel() != want:
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements, not {want}")
-            if not t.is_contiguous() or not t.is_cuda or t.device != self.device:
-                raise ValueError(f"{name}[{i}] is not a contiguous CUDA tensor of {self.device}")
-            if name == "params":
-                ok = code in (ZERO_F16, ZERO_BF16) or (code == 0 and str(t.dtype) in
-                                                       ("torch.int16", "torch.uint16"))
-            else:
-                ok = code in self._TYPES[name]
-            if not ok:
+            if not t.is_contiguous() or not t.is_cuda or t.get_device() != device:
+                raise ValueError(f"{name}[{i}] is not a contiguous CUDA tensor of the list's device")
+            code = known.get(t.dtype, -1)
+            if code not in types:
                 raise ValueError(f"{name}[{i}] has type {t.dtype}")
+            codes.append(code)
+        return codes
 
     def set_grad(self, grad: Sequence) -> None:
         """The same tensors' gradients at new addresses."""
         grad = list(grad)
-        self._check_length("grad", grad)
-        self._check("grad", grad)
+        if len(grad) != len(self):
+            raise ValueError(f"grad has {len(grad)} tensors, the list {len(self)}")
+        codes = self._check("grad", grad)
         self.tensors["grad"] = grad
-        for i, g in enumerate(grad):
-            self.array[i].grad, self.array[i].grad_dtype = g.data_ptr(), _dtype_code(g)
+        for a, g, code in zip(self.array, grad, codes):
+            a.grad, a.grad_dtype = g.data_ptr(), code
 
 
 def _same_length(a: TensorList, b: TensorList) -> int:

@@ -205,6 +205,7 @@ struct NormReady {
     float step_size, rbc2;
 };
 
+template <int CAP>
 struct NormArgs {
     zero_step_state_t* st;
     double* slots;              // one partial sum per block, then the step's scalar candidates
@@ -212,10 +213,10 @@ struct NormArgs {
     uint32_t slot0, last;       // this launch's first slot; 1 in the list's last launch
     uint32_t n;
     uint64_t quota;             // granules per block
-    NormRef t[kNormCap];
+    NormRef t[CAP];
 };
 static_assert(sizeof(NormReady) <= 64, "the workspace's tail");
-static_assert(sizeof(NormArgs) <= 32764, "kernel parameters");
+static_assert(sizeof(NormArgs<kNormCap>) <= 32764, "kernel parameters");
 
 /* A thread's sum of squares: fp32 sums of a granule's 8 (or 4) squares, joined by
  * error-free additions (hi + lo), so that only a granule's own roundings remain (at most
@@ -321,7 +322,8 @@ __device__ __forceinline__ void norm_passes(const char* p, uint64_t passes, floa
 }
 
 /* The first tensor of t[k .. upper] whose end lies past granule g. */
-__device__ __forceinline__ uint32_t norm_find(const NormArgs& a, uint64_t g, uint32_t k, uint32_t upper)
+template <int CAP>
+__device__ __forceinline__ uint32_t norm_find(const NormArgs<CAP>& a, uint64_t g, uint32_t k, uint32_t upper)
 {
     while (k < upper) {
         const uint32_t mid = (k + upper) / 2;
@@ -353,20 +355,23 @@ __device__ __forceinline__ double block_sum(double v, double* warp_sum)
 /* Sum of squares over the list's gradients: block b takes granules [b*quota, (b+1)*quota)
  * of the launch, whatever tensors they lie in.  In the last launch the block that finishes
  * last adds the blocks' partial sums in order and finalises the step as zero_grad_norm. */
-__global__ void __launch_bounds__(kThreads, kNormBlocksPerSm) k_tensors_norm(const __grid_constant__ NormArgs a)
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kNormBlocksPerSm) k_tensors_norm(const __grid_constant__ NormArgs<CAP> a)
 {
     __shared__ double warp_sum[kThreads / 32];
     __shared__ int is_last;
+    // this block's share, from the parameters alone, before the wait for what came before
+    const uint32_t n_sum = a.last ? gridDim.x - 1 : gridDim.x;  // the last launch has one block more
+    uint64_t lo = blockIdx.x * a.quota;
+    const uint64_t total = a.n ? a.t[a.n - 1].end : 0, hi = lo + a.quota < total ? lo + a.quota : total;
+    uint32_t k = lo < hi ? norm_find(a, lo, 0, a.n - 1) : 0;
     grid_dependency_wait();
+    grid_launch_dependents();
     zero_step_state_t* st = a.st;
     const float inv = st->inv_scale;
     const float floor = inv < 0x1p60f ? 0x1p-80f : __int_as_float(0x7f800000);
     Squares acc;
-    const uint32_t n_sum = a.last ? gridDim.x - 1 : gridDim.x;  // the last launch has one block more
     NormReady* ready = reinterpret_cast<NormReady*>(a.slots + a.slot0 + n_sum);
-    uint64_t lo = blockIdx.x * a.quota;
-    const uint64_t total = a.n ? a.t[a.n - 1].end : 0, hi = lo + a.quota < total ? lo + a.quota : total;
-    uint32_t k = lo < hi ? norm_find(a, lo, 0, a.n - 1) : 0;
     while (lo < hi) {
         const NormRef& t = a.t[k];
         const uint64_t first = k ? a.t[k - 1].end : 0;
@@ -1416,122 +1421,142 @@ bool finite_f(float x) { return x == x && x <= 3.4e38f && x >= -3.4e38f; }
 
 bool at(const void* p, uintptr_t align) { return ((uintptr_t)p & (align - 1)) == 0; }
 
+constexpr bool is_adamw(Op op) { return op == Op::kAdamw || op == Op::kAdamw8; }
+constexpr bool is_codec(Op op) { return op == Op::kRead || op == Op::kWrite; }
+
 /* What an operator needs of tensor t (and, for the codec, of its 32-bit partner). */
-int check_tensor(const zero_tensor_t& t, const zero_tensor_t* other, Op op)
+template <Op OP>
+int check_tensor(const zero_tensor_t& t, const zero_tensor_t* other)
 {
     if (t.elems == 0)
         return other && other->elems != 0 ? ZERO_EINVAL : ZERO_OK;
     if (t.elems > (1ull << 39))
         return ZERO_EINVAL;
-    const bool codec = op == Op::kRead || op == Op::kWrite;
-    const bool adamw = op == Op::kAdamw || op == Op::kAdamw8;
-    if (!codec) {
+    bool aligned = true;
+    if (!is_codec(OP)) {
         if (!t.grad || (t.grad_dtype != ZERO_F16 && t.grad_dtype != ZERO_BF16 && t.grad_dtype != ZERO_F32))
             return ZERO_EINVAL;
-        if (!at(t.grad, t.grad_dtype == ZERO_F32 ? 4 : 2))
-            return ZERO_EALIGN;
+        aligned &= at(t.grad, t.grad_dtype == ZERO_F32 ? 4 : 2);
     }
-    if (adamw) {
-        if (!t.master || !t.m || !t.v)
-            return ZERO_EINVAL;
-        if (t.params_dtype != 0 && t.params_dtype != ZERO_BF16 && t.params_dtype != ZERO_F16)
+    if (is_adamw(OP)) {
+        if (!t.master || (t.params_dtype != 0 && t.params_dtype != ZERO_BF16 && t.params_dtype != ZERO_F16))
             return ZERO_EINVAL;
         if (!finite_f(t.lr_scale) || t.lr_scale < 0.0f || !finite_f(t.weight_decay))
             return ZERO_EINVAL;
-        if (!at(t.master, 4) || !at(t.params, 2))
-            return ZERO_EALIGN;
+        aligned &= at(t.master, 4) && at(t.params, 2);
     }
-    if (op == Op::kAdamw) {
+    if (OP != Op::kNorm && (!t.m || !t.v))
+        return ZERO_EINVAL;
+    if (OP == Op::kAdamw) {
         if (t.state_dtype != ZERO_F32)
             return ZERO_EINVAL;
-        if (!at(t.m, 4) || !at(t.v, 4))
-            return ZERO_EALIGN;
+        aligned &= at(t.m, 4) && at(t.v, 4);
     }
-    if (op == Op::kAdamw8 || codec)
-        if (t.state_dtype != ZERO_U8 || !t.m || !t.v || !t.exps)
-            return ZERO_EINVAL;
-    if (codec) {
-        const bool bf16 = op == Op::kRead && other->state_dtype == ZERO_BF16;
+    if ((OP == Op::kAdamw8 || is_codec(OP)) && (t.state_dtype != ZERO_U8 || !t.exps))
+        return ZERO_EINVAL;
+    if (is_codec(OP)) {
+        const bool bf16 = OP == Op::kRead && other->state_dtype == ZERO_BF16;
         if (other->elems != t.elems || !other->m || !other->v || (other->state_dtype != ZERO_F32 && !bf16))
             return ZERO_EINVAL;
-        if (!at(other->m, bf16 ? 2 : 4) || !at(other->v, bf16 ? 2 : 4))
-            return ZERO_EALIGN;
+        aligned &= at(other->m, bf16 ? 2 : 4) && at(other->v, bf16 ? 2 : 4);
     }
-    return ZERO_OK;
+    return aligned ? ZERO_OK : ZERO_EALIGN;
+}
+
+/* The whole list, and its number of elements. */
+template <Op OP>
+int check_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n, uint64_t& total)
+{
+    total = 0;
+    if (n > (1ull << 31) || (n && (!tensors || (is_codec(OP) && !others))))
+        return ZERO_EINVAL;
+    int align = ZERO_OK;
+    for (uint64_t k = 0; k < n; ++k) {
+        const int rc = check_tensor<OP>(tensors[k], is_codec(OP) ? others + k : nullptr);
+        if (rc == ZERO_EINVAL)
+            return rc;
+        if (rc != ZERO_OK)
+            align = rc;
+        total += tensors[k].elems;
+    }
+    return align;
 }
 
 /* Every array of the operator allows one access per 8 elements from element h on: fp32 at
  * 32 bytes, 16-bit arrays at 16, codes at 8. */
-bool vector_from(const zero_tensor_t& t, const zero_tensor_t* other, Op op, uint32_t h)
+template <Op OP>
+bool vector_from(const zero_tensor_t& t, const zero_tensor_t* other, uint32_t h)
 {
-    auto ok = [h](const void* p, uintptr_t size, uintptr_t align) {
-        return !p || (((uintptr_t)p + h * size) & (align - 1)) == 0;
-    };
-    if (op == Op::kRead || op == Op::kWrite) {
+    // the bits of the addresses below their alignment, as multiples of 8 elements
+    auto off = [h](const void* p, uintptr_t size) { return ((uintptr_t)p + h * size) & (8 * size - 1); };
+    if (is_codec(OP)) {
         const uintptr_t size = other->state_dtype == ZERO_BF16 ? 2 : 4;
-        return ok(t.m, 1, 8) && ok(t.v, 1, 8) && ok(other->m, size, size * 8) && ok(other->v, size, size * 8);
+        return (off(t.m, 1) | off(t.v, 1) | off(other->m, size) | off(other->v, size)) == 0;
     }
-    const uintptr_t size = t.grad_dtype == ZERO_F32 ? 4 : 2;
-    const bool rest = ok(t.grad, size, size * 8) && ok(t.master, 4, 32) && ok(t.params, 2, 16);
-    return op == Op::kAdamw ? rest && ok(t.m, 4, 32) && ok(t.v, 4, 32) : rest && ok(t.m, 1, 8) && ok(t.v, 1, 8);
+    const uintptr_t size = OP == Op::kAdamw8 ? 1 : 4;
+    return (off(t.grad, t.grad_dtype == ZERO_F32 ? 4 : 2) | off(t.master, 4) | off(t.m, size) | off(t.v, size) |
+            (t.params ? off(t.params, 2) : 0)) == 0;
 }
 
-/* Fills `l` with tensors from index `next` on, as many as fit; returns the next index. */
+/* Fills `l` with tensors from index `next` on, as many as fit, in units of UNIT elements;
+ * returns the next index. */
+template <Op OP, uint32_t UNIT>
 uint64_t fill(List<kLarge>& l, const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
-              uint64_t next, Op op, const zero_adamw_hparams_t* hp, uint32_t& group0, uint32_t unit = kUnit)
+              uint64_t next, const zero_adamw_hparams_t* hp, uint32_t& group0)
 {
     uint64_t units = 0;
-    l.n = 0;
-    for (; next < n && l.n < (uint32_t)kLarge; ++next) {
+    uint32_t filled = 0;
+    for (; next < n && filled < (uint32_t)kLarge; ++next) {
         const zero_tensor_t& t = tensors[next];
-        const zero_tensor_t* other = others ? others + next : nullptr;
+        const zero_tensor_t* other = is_codec(OP) ? others + next : nullptr;
         if (t.elems == 0)
             continue;
-        // 32-bit states: an offset that all arrays share (pieces of flat buffers) is stepped
-        // over; 8-bit states: their blocks start at element 0
+        // 32-bit states, straight from global memory: an offset that all arrays share
+        // (pieces of flat buffers) is stepped over; 8-bit blocks start at element 0
+        bool vec = vector_from<OP>(t, other, 0);
         uint32_t head = 0;
-        if (op == Op::kAdamw && unit == kUnit)
-            while (head < 8 && !vector_from(t, other, op, head))
-                ++head;
-        const bool vec = head < 8 && vector_from(t, other, op, head);
-        if (!vec)
-            head = 0;
+        if (OP == Op::kAdamw && UNIT == kUnit && !vec) {
+            for (uint32_t h = 1; h < 8 && !vec; ++h)
+                if (vector_from<OP>(t, other, h)) {
+                    vec = true;
+                    head = h;
+                }
+        }
         const uint64_t body = t.elems > head ? t.elems - head : 1;
-        const uint64_t c = (body + unit - 1) / unit;
+        const uint64_t c = (body + UNIT - 1) / UNIT;
         if (units + c > 0xf0000000ull)
             break;  // unit counters are 32-bit; check_tensor bounds one tensor's units
-        Ref& r = l.t[l.n];
-        memset(&r, 0, sizeof r);
-        r.elems = t.elems;
+        Ref& r = l.t[filled];
         r.m = t.m;
         r.v = t.v;
         r.exps = t.exps;
-        r.flags = vec ? kVector : 0;
-        if (other) {
+        r.elems = t.elems;
+        uint32_t flags = vec ? kVector : 0;
+        if (is_codec(OP)) {
             r.x = other->m;
             r.y = other->v;
-            if (other->state_dtype == ZERO_BF16)
-                r.flags |= kValueBF16;
+            flags |= other->state_dtype == ZERO_BF16 ? kValueBF16 : 0;
         } else {
             r.grad = t.grad;
             r.master = t.master;
             r.params = t.params;
-            r.flags |= t.grad_dtype;
             r.lr_scale = t.lr_scale;
             r.decay = (float)(1.0 - (double)hp->lr * (double)t.lr_scale * (double)t.weight_decay);
-            if ((t.params_dtype ? t.params_dtype : hp->params_dtype) == ZERO_F16)
-                r.flags |= kOutF16;
+            flags |= t.grad_dtype;
+            flags |= (t.params_dtype ? t.params_dtype : hp->params_dtype) == ZERO_F16 ? kOutF16 : 0;
         }
-        if (op == Op::kAdamw)
+        r.flags = flags;
+        if (OP == Op::kAdamw)
             r.head = head;
         else
             r.group0 = group0;
         group0 += (uint32_t)((t.elems + kUnit - 1) / kUnit) * 32u;
         units += c;
-        l.end[l.n++] = (uint32_t)units;
+        l.end[filled++] = (uint32_t)units;
     }
-    for (uint32_t k = l.n; k < (uint32_t)kLarge && k % 4; ++k)
+    for (uint32_t k = filled; k < (uint32_t)kLarge && k % 4; ++k)
         l.end[k] = ~0u;  // read with the last tensors', never at or below a unit's number
+    l.n = filled;
     l.n_units = (uint32_t)units;
     return next;
 }
@@ -1545,50 +1570,12 @@ void shrink(const List<kLarge>& from, List<kSmall>& to)
     memcpy(to.t, from.t, from.n * sizeof(Ref));
 }
 
-/* The same for the norm. */
-uint64_t fill_norm(NormArgs& a, const zero_tensor_t* tensors, uint64_t n, uint64_t next)
-{
-    uint64_t end = 0;
-    a.n = 0;
-    for (; next < n && a.n < (uint32_t)kNormCap; ++next) {
-        const zero_tensor_t& t = tensors[next];
-        if (t.elems == 0)
-            continue;
-        const uint32_t size = t.grad_dtype == ZERO_F32 ? 4 : 2;
-        NormRef& r = a.t[a.n++];
-        const uintptr_t off = (uintptr_t)t.grad & 15u;
-        r.base = static_cast<const char*>(t.grad) - off;
-        r.skip = (uint32_t)(off / size);
-        r.elems = t.elems;
-        r.dtype = t.grad_dtype;
-        end += (r.skip + t.elems + 16 / size - 1) / (16 / size);
-        r.end = end;
-    }
-    return next;
-}
-
 int status_of(cudaError_t e)
 {
     if (e == cudaSuccess)
         return ZERO_OK;
     record_cuda_error((int)e);
     return ZERO_ECUDA;
-}
-
-int check_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n, Op op)
-{
-    const bool codec = op == Op::kRead || op == Op::kWrite;
-    if (n > (1ull << 31) || (n && (!tensors || (codec && !others))))
-        return ZERO_EINVAL;
-    int align = ZERO_OK;
-    for (uint64_t k = 0; k < n; ++k) {
-        const int rc = check_tensor(tensors[k], codec ? others + k : nullptr, op);
-        if (rc == ZERO_EINVAL)
-            return rc;
-        if (rc != ZERO_OK)
-            align = rc;
-    }
-    return align;
 }
 
 /* A launch over `units` units, a warp each, on at most as many blocks as fit at once. */
@@ -1629,19 +1616,55 @@ int launch_ring(const ListArgs<CAP>& a, cudaStream_t s)
 }
 
 /* One launch of an operator over its part of the list. */
-template <int CAP>
-int launch_op(const ListArgs<CAP>& a, Op op, bool ring, cudaStream_t s)
+template <Op OP, bool RING, int CAP>
+int launch_op(const ListArgs<CAP>& a, cudaStream_t s)
 {
-    static std::atomic<int> occ[4][64];  // per device; a race only repeats the set-up
-    const uint32_t n = a.l.n_units;
-    switch (op) {
-    case Op::kAdamw:
-        return ring ? launch_ring<false>(a, s) : launch_units(k_tensors_adamw<CAP>, occ[0], n, s, a);
-    case Op::kAdamw8:
-        return ring ? launch_ring<true>(a, s) : launch_units(k_tensors_adamw8<CAP>, occ[1], n, s, a);
-    case Op::kRead: return launch_units(k_state8_read<CAP>, occ[2], n, s, a);
-    default: return launch_units(k_state8_write<CAP>, occ[3], n, s, a);
+    static std::atomic<int> occ[64];  // per device; a race only repeats the set-up
+    if constexpr (RING)
+        return launch_ring<OP == Op::kAdamw8>(a, s);
+    else if constexpr (OP == Op::kAdamw)
+        return launch_units(k_tensors_adamw<CAP>, occ, a.l.n_units, s, a);
+    else if constexpr (OP == Op::kAdamw8)
+        return launch_units(k_tensors_adamw8<CAP>, occ, a.l.n_units, s, a);
+    else if constexpr (OP == Op::kRead)
+        return launch_units(k_state8_read<CAP>, occ, a.l.n_units, s, a);
+    else
+        return launch_units(k_state8_write<CAP>, occ, a.l.n_units, s, a);
+}
+
+template <Op OP, bool RING>
+int run_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
+             const zero_adamw_hparams_t* hp, uint64_t seed, const zero_step_state_t* st, cudaStream_t s)
+{
+    constexpr uint32_t kElems = !RING ? kUnit : Ring<OP == Op::kAdamw8>::kChunk;
+    ListArgs<kLarge> a;
+    a.st = st;
+    a.seed = seed;
+    a.beta1 = hp ? hp->beta1 : 0.0f;
+    a.beta2 = hp ? hp->beta2 : 0.0f;
+    a.eps = hp ? hp->eps : 0.0f;
+    uint32_t group0 = 0;
+    for (uint64_t next = 0; next < n;) {
+        next = fill<OP, kElems>(a.l, tensors, others, n, next, hp, group0);
+        if (a.l.n == 0)
+            continue;
+        int rc;
+        if (a.l.n <= (uint32_t)kSmall) {
+            ListArgs<kSmall> b;
+            b.st = a.st;
+            b.seed = a.seed;
+            b.beta1 = a.beta1;
+            b.beta2 = a.beta2;
+            b.eps = a.eps;
+            shrink(a.l, b.l);
+            rc = launch_op<OP, RING>(b, s);
+        } else {
+            rc = launch_op<OP, RING>(a, s);
+        }
+        if (rc != ZERO_OK)
+            return rc;
     }
+    return ZERO_OK;
 }
 
 /* Lists of this many elements take the staged kernel.  Measured, direct against staged, us a
@@ -1649,36 +1672,76 @@ int launch_op(const ListArgs<CAP>& a, Op op, bool ring, cudaStream_t s)
  * (14.8 / 15.1), 2^23 41.0 / 39.7 (25.9 / 24.7), 2^24 78.7 / 73.0 (51.0 / 43.8). */
 constexpr uint64_t kRingElems = 3ull << 21;
 
-int run_list(const zero_tensor_t* tensors, const zero_tensor_t* others, uint64_t n,
-             const zero_adamw_hparams_t* hp, uint64_t seed, const zero_step_state_t* st, cudaStream_t s, Op op)
+template <Op OP>
+int adamw_list(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparams_t* hp, uint64_t seed,
+               const zero_step_state_t* st, cudaStream_t s)
 {
-    ListArgs<kLarge> a;
-    ListArgs<kSmall> b;
-    a.st = b.st = st;
-    a.seed = b.seed = seed;
-    a.beta1 = b.beta1 = hp ? hp->beta1 : 0.0f;
-    a.beta2 = b.beta2 = hp ? hp->beta2 : 0.0f;
-    a.eps = b.eps = hp ? hp->eps : 0.0f;
-    uint64_t total = 0;
-    for (uint64_t k = 0; k < n; ++k)
-        total += tensors[k].elems;
-    const bool ring = total >= kRingElems && (op == Op::kAdamw || op == Op::kAdamw8);
-    const uint32_t unit = !ring ? kUnit : op == Op::kAdamw ? Ring<false>::kChunk : Ring<true>::kChunk;
-    uint32_t group0 = 0;
-    for (uint64_t next = 0; next < n;) {
-        next = fill(a.l, tensors, others, n, next, op, hp, group0, unit);
-        if (a.l.n == 0)
+    uint64_t total;
+    const int rc = check_list<OP>(tensors, nullptr, n, total);
+    if (rc == ZERO_EINVAL || !hparams_ok(hp) || !st)
+        return ZERO_EINVAL;
+    if (rc != ZERO_OK || !at(st, 16))
+        return ZERO_EALIGN;
+    return total >= kRingElems ? run_list<OP, true>(tensors, nullptr, n, hp, seed, st, s)
+                               : run_list<OP, false>(tensors, nullptr, n, hp, seed, st, s);
+}
+
+template <Op OP>
+int codec_list(const zero_tensor_t* t8, const zero_tensor_t* t32, uint64_t n, cudaStream_t s)
+{
+    uint64_t total;
+    const int rc = check_list<OP>(t8, t32, n, total);
+    return rc != ZERO_OK ? rc : run_list<OP, false>(t8, t32, n, nullptr, 0, nullptr, s);
+}
+
+/* The norm's launches: a list in its parameters' form, then equal shares for the blocks. */
+template <int CAP>
+uint64_t fill_norm(NormArgs<CAP>& a, const zero_tensor_t* tensors, uint64_t n, uint64_t next)
+{
+    uint64_t end = 0;
+    uint32_t filled = 0;
+    for (; next < n && filled < (uint32_t)CAP; ++next) {
+        const zero_tensor_t& t = tensors[next];
+        if (t.elems == 0)
             continue;
-        int rc;
-        if (a.l.n <= (uint32_t)kSmall) {
-            shrink(a.l, b.l);
-            rc = launch_op(b, op, ring, s);
-        } else {
-            rc = launch_op(a, op, ring, s);
-        }
-        if (rc != ZERO_OK)
-            return rc;
+        const uint32_t shift = t.grad_dtype == ZERO_F32 ? 2 : 1;  // log2 of the element's size
+        NormRef& r = a.t[filled++];
+        const uintptr_t off = (uintptr_t)t.grad & 15u;
+        r.base = static_cast<const char*>(t.grad) - off;
+        r.skip = (uint32_t)(off >> shift);
+        r.elems = t.elems;
+        r.dtype = t.grad_dtype;
+        end += (((r.skip + t.elems) << shift) + 15) >> 4;
+        r.end = end;
     }
+    a.n = filled;
+    return next;
+}
+
+template <int CAP>
+int run_norm(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparams_t* hp, double* workspace,
+             zero_step_state_t* st, cudaStream_t s)
+{
+    NormArgs<CAP> a;
+    a.st = st;
+    a.slots = workspace;
+    a.hp = *hp;
+    a.slot0 = 0;
+    const uint64_t cap = (uint64_t)sm_count() * kNormBlocksPerSm, blocks = cap < kNormMaxBlocks ? cap : kNormMaxBlocks;
+    uint64_t next = 0;
+    do {
+        next = fill_norm(a, tensors, n, next);
+        a.last = next == n;
+        // equal shares, in whole passes of a block's loads; short lists one load per thread
+        const uint64_t total = a.n ? a.t[a.n - 1].end : 0;
+        const uint64_t pass = total <= blocks * kNormPass ? kThreads : kNormPass;
+        a.quota = ((total + blocks - 1) / blocks + pass - 1) / pass * pass;
+        const unsigned grid = total ? (unsigned)((total + a.quota - 1) / a.quota) : 0u;
+        const cudaError_t e = launch_pdl(k_tensors_norm<CAP>, dim3(grid + a.last), dim3(kThreads), 0, s, a);
+        if (e != cudaSuccess)
+            return status_of(e);
+        a.slot0 += grid;
+    } while (next < n);
     return ZERO_OK;
 }
 
@@ -1718,34 +1781,15 @@ extern "C" int zero_tensors_grad_norm(const zero_tensor_t* tensors, uint64_t n_t
                                       zero_step_state_t* st, zero_stream_t stream)
 {
     const NvtxRange range("zero_tensors_grad_norm");
-    const int rc = check_list(tensors, nullptr, n_tensors, Op::kNorm);
+    uint64_t total;
+    const int rc = check_list<Op::kNorm>(tensors, nullptr, n_tensors, total);
     if (rc == ZERO_EINVAL || !hparams_ok(hp) || !workspace || !st)
         return ZERO_EINVAL;
     if (rc != ZERO_OK || !at(workspace, 16) || !at(st, 16))
         return ZERO_EALIGN;
-    NormArgs a;
-    a.st = st;
-    a.slots = workspace;
-    a.hp = *hp;
-    a.slot0 = 0;
-    const uint64_t cap = (uint64_t)sm_count() * kNormBlocksPerSm;
-    uint64_t next = 0;
-    do {
-        next = fill_norm(a, tensors, n_tensors, next);
-        a.last = next == n_tensors;
-        // equal shares, in whole passes of a block's loads; short lists one load per thread
-        const uint64_t total = a.n ? a.t[a.n - 1].end : 0;
-        const uint64_t blocks = cap < kNormMaxBlocks ? cap : kNormMaxBlocks;
-        const uint64_t pass = total <= blocks * kNormPass ? kThreads : kNormPass;
-        a.quota = ((total + blocks - 1) / blocks + pass - 1) / pass * pass;
-        const unsigned grid = total ? (unsigned)((total + a.quota - 1) / a.quota) : 0u;
-        const cudaError_t e = launch_pdl(k_tensors_norm, dim3(grid + a.last), dim3(kThreads), 0,
-                                         (cudaStream_t)stream, a);
-        if (e != cudaSuccess)
-            return status_of(e);
-        a.slot0 += grid;
-    } while (next < n_tensors);
-    return ZERO_OK;
+    return n_tensors <= (uint64_t)kSmall
+               ? run_norm<kSmall>(tensors, n_tensors, hp, workspace, st, (cudaStream_t)stream)
+               : run_norm<kNormCap>(tensors, n_tensors, hp, workspace, st, (cudaStream_t)stream);
 }
 
 extern "C" int zero_tensors_adamw(const zero_tensor_t* tensors, uint64_t n_tensors,
@@ -1753,12 +1797,7 @@ extern "C" int zero_tensors_adamw(const zero_tensor_t* tensors, uint64_t n_tenso
                                   zero_stream_t stream)
 {
     const NvtxRange range("zero_tensors_adamw");
-    const int rc = check_list(tensors, nullptr, n_tensors, Op::kAdamw);
-    if (rc == ZERO_EINVAL || !hparams_ok(hp) || !st)
-        return ZERO_EINVAL;
-    if (rc != ZERO_OK || !at(st, 16))
-        return ZERO_EALIGN;
-    return run_list(tensors, nullptr, n_tensors, hp, 0, st, (cudaStream_t)stream, Op::kAdamw);
+    return adamw_list<Op::kAdamw>(tensors, n_tensors, hp, 0, st, (cudaStream_t)stream);
 }
 
 extern "C" int zero_tensors_adamw8(const zero_tensor_t* tensors, uint64_t n_tensors,
@@ -1766,26 +1805,19 @@ extern "C" int zero_tensors_adamw8(const zero_tensor_t* tensors, uint64_t n_tens
                                    const zero_step_state_t* st, zero_stream_t stream)
 {
     const NvtxRange range("zero_tensors_adamw8");
-    const int rc = check_list(tensors, nullptr, n_tensors, Op::kAdamw8);
-    if (rc == ZERO_EINVAL || !hparams_ok(hp) || !st)
-        return ZERO_EINVAL;
-    if (rc != ZERO_OK || !at(st, 16))
-        return ZERO_EALIGN;
-    return run_list(tensors, nullptr, n_tensors, hp, seed, st, (cudaStream_t)stream, Op::kAdamw8);
+    return adamw_list<Op::kAdamw8>(tensors, n_tensors, hp, seed, st, (cudaStream_t)stream);
 }
 
 extern "C" int zero_tensors_state8_read(const zero_tensor_t* from, const zero_tensor_t* to,
                                         uint64_t n_tensors, zero_stream_t stream)
 {
     const NvtxRange range("zero_tensors_state8_read");
-    const int rc = check_list(from, to, n_tensors, Op::kRead);
-    return rc != ZERO_OK ? rc : run_list(from, to, n_tensors, nullptr, 0, nullptr, (cudaStream_t)stream, Op::kRead);
+    return codec_list<Op::kRead>(from, to, n_tensors, (cudaStream_t)stream);
 }
 
 extern "C" int zero_tensors_state8_write(const zero_tensor_t* to, const zero_tensor_t* from,
                                          uint64_t n_tensors, zero_stream_t stream)
 {
     const NvtxRange range("zero_tensors_state8_write");
-    const int rc = check_list(to, from, n_tensors, Op::kWrite);
-    return rc != ZERO_OK ? rc : run_list(to, from, n_tensors, nullptr, 0, nullptr, (cudaStream_t)stream, Op::kWrite);
+    return codec_list<Op::kWrite>(to, from, n_tensors, (cudaStream_t)stream);
 }
