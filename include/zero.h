@@ -475,8 +475,9 @@ int zero_step_static_workspace(const zero_layout_t* layout, const zero_adamw_hpa
  *   2. zero_tensors_adamw or zero_tensors_adamw8 over the same list
  * The list is a HOST array that each call reads before it returns; its pointers are DEVICE
  * pointers.  Every array is contiguous and holds `elems` elements at the natural alignment
- * of its element type (ZERO_EALIGN otherwise); tensors all of whose arrays are 16-byte
- * aligned move in 128-bit accesses.  A tensor may be empty (its pointers are then not
+ * of its element type (ZERO_EALIGN otherwise); tensors whose fp32 arrays are 32-byte, 16-bit
+ * arrays 16-byte and code arrays 8-byte aligned move in one access per 8 elements, others
+ * element by element.  A tensor may be empty (its pointers are then not
  * looked at), and so may the list.  No two arrays may overlap.  One launch covers several
  * hundred tensors; a longer list takes more than one.
  *

@@ -7,6 +7,9 @@ round at most 9 times, so its square is within 9u and the norm within 4.5u < 3e-
 5 roundings of terms below |b1 m| + |(1-b1) gc|, v 8 of positive terms; the parameter adds
 3 roundings of p and at most 12 of the update (the divisions and the square root may be
 within 2 ulp), besides m's own error over the denominator."""
+import ctypes as C
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -561,6 +564,44 @@ def test_long_lists_of_several_launches(state):
             assert np.all(np.abs(after["master"][k] - p1) <= tp)
     s = c.state()
     assert (s.adamw_next_chunk, s.adamw_done, s.error) == (0, 0, 0)
+
+
+@pytest.mark.parametrize("state", ["f32", "u8"])
+def test_a_wait_that_runs_out_reports_an_error(hooked, state):
+    """With one chunk's copies withheld (test build only) the staged kernel gives up after
+    ~2 s, records 1 in the error word, puts the queue back and ends; the GPU stays usable."""
+    sizes = [6_500_017, 300]
+    c = Case(sizes, state=state)
+    c.set(**STEP)
+    hooked.zero_test_withhold_tensors_chunk.argtypes = [C.c_ulonglong]
+    hooked.zero_tensors_adamw.argtypes = z.lib().zero_tensors_adamw.argtypes
+    hooked.zero_tensors_adamw8.argtypes = z.lib().zero_tensors_adamw8.argtypes
+    stream = torch.cuda.current_stream().cuda_stream
+    assert hooked.zero_test_withhold_tensors_chunk(200) == 0
+    t0 = time.time()
+    if state == "u8":
+        rc = hooked.zero_tensors_adamw8(c.list.array, 2, C.byref(c.hp), 1, c.st.data_ptr(), stream)
+    else:
+        rc = hooked.zero_tensors_adamw(c.list.array, 2, C.byref(c.hp), c.st.data_ptr(), stream)
+    assert rc == 0
+    torch.cuda.synchronize()  # completes: the waits gave up, no fault
+    waited = time.time() - t0
+    assert hooked.zero_test_withhold_tensors_chunk(~0 & 0xFFFFFFFFFFFFFFFF) == 0
+    s = c.state()
+    assert (s.error, s.adamw_next_chunk, s.adamw_done) == (1, 0, 0) and 1.0 < waited < 60.0
+    c.arena.check()
+    # the context is still good: the product library's step on fresh buffers
+    c = Case(sizes, state=state)
+    c.set(**STEP)
+    before = c.arrays()
+    if state == "u8":
+        z.zero_tensors_adamw8(c.list, c.hp, 1, c.st)
+        check8(c, before, STEP, 1)
+    else:
+        z.zero_tensors_adamw(c.list, c.hp, c.st)
+        p1, tp = expected(c, before, 0, c.hp, STEP, before["m"][0], before["v"][0])[2::3]
+        assert np.all(np.abs(c.arrays()["master"][0] - p1) <= tp)
+    c.arena.check()
 
 
 # ------------------------------------------------------------------------------------------

@@ -635,7 +635,7 @@ extern "C" const char* zero_strerror(int status)
     switch (status) {
     case ZERO_OK: return "ok";
     case ZERO_EINVAL: return "invalid argument";
-    case ZERO_EALIGN: return "pointer or window not aligned (16-byte pointers, window start a multiple of 8)";
+    case ZERO_EALIGN: return "pointer or window not aligned (16-byte pointers, window start a multiple of 8, a list's arrays at their element size)";
     case ZERO_ENOMEM: return "caller-provided buffer too small";
     case ZERO_ECUDA: return "CUDA launch or copy failed";
     case ZERO_ETIMEOUT: return "bounded device wait timed out";

@@ -95,5 +95,17 @@ __device__ __forceinline__ uint32_t encode_v(float x, float unscale, uint32_t r)
     return max(min((__float_as_uint(y) + r) >> 20, 255u), x != 0.0f ? 1u : 0u);
 }
 
+/* Four codes of a word as floats with the code's exponent in fp32's field. */
+__device__ __forceinline__ float raw_m(uint32_t w, int byte)
+{
+    const int top = (int)__byte_perm(w, 0, byte << 12 | 0x444);  // the code in bits 31..24
+    return __uint_as_float((uint32_t)(top >> 4) & 0x87f00000u);
+}
+
+__device__ __forceinline__ float raw_v(uint32_t w, int byte)
+{
+    return __uint_as_float(__byte_perm(w, 0, byte << 12 | 0x444) >> 4);
+}
+
 }  // namespace
 }  // namespace zero
