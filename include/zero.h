@@ -505,7 +505,7 @@ int zero_step_static_workspace(const zero_layout_t* layout, const zero_adamw_hpa
 #define ZERO_STATE8_BLOCK 256u /* elements that share an exponent byte */
 
 typedef struct zero_tensor {
-    uint64_t elems;
+    uint64_t elems;          /* at most 2^39 */
     const void* grad;        /* of grad_dtype */
     float* master;           /* fp32 parameters, updated in place */
     void* m;                 /* optimizer state of state_dtype, updated in place */

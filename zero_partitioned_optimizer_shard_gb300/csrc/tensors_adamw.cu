@@ -36,6 +36,11 @@ __device__ __forceinline__ Scalars step_scalars(const ListArgs<CAP>& a)
     s.eps = a.eps;
     return s;
 }
+
+/* ------------------------------------------------------------------------------------ */
+/* short lists: straight from global memory                                               */
+/* ------------------------------------------------------------------------------------ */
+
 /* A lane's 8 gradients as they lie in memory. */
 struct RawGrad {
     float w[8];  // 16-bit gradients: the first four words
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
         s.decay = t.decay;
         const bool vec = t.flags & kVector;
         const uint64_t off = t.head + (uint64_t)at.unit * kUnit;
-        // consecutive elements per lane in 128-bit accesses, else lanes side by side
+        // 8 consecutive elements per lane, one access an array; else lanes side by side
         const uint64_t i = vec ? off + lane * kPer : off + lane;
         const uint32_t stride = vec ? 1 : 32;
         float x8[8], p8[8], m8[8], v8[8];
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
                 }
             }
         }
-        if (at.unit == 0 && lane < t.head && lane < t.elems) {  // before the 16-byte boundary
+        if (at.unit == 0 && lane < t.head && lane < t.elems) {  // before the common boundary
             float p = t.master[lane], mi = m[lane], vi = v[lane];
             adamw_one(__fmul_rn(one_grad(t.grad, lane, dtype), inv), p, mi, vi, s);
             t.master[lane] = p;

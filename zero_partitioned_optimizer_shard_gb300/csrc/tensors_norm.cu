@@ -5,15 +5,16 @@
  *
  * norm = sqrt(sum of (x * inv)^2) over every gradient element x.  Nothing but a read of the
  * gradients, 2 or 4 bytes an element, so it is bound by HBM: GPT-2 1.5B's 580 bf16
- * gradients (3.1 GB) take 464 us, 100% of the measured copy peak (6,669 GB/s).  What that
- * took:
+ * gradients (3.1 GB) take 450 us, 104% of the measured copy peak (6,669 GB/s); a short list
+ * takes 7 us, most of it the blocks' arrival and the fp64 chain behind it.  What that took:
  *   - each gradient is a run of 16-byte granules at the addresses' own multiples of 16, so
  *     every tensor moves in 128-bit loads whatever its alignment and only a first and a
  *     last granule can be partial (a sum does not care which lane holds what);
  *   - every block takes an equal share of the launch's granules, across tensor boundaries
  *     (chunks of 8192 elements handed out in turn, each looked up anew: 1,068 us);
- *   - 8 loads in flight per thread; a pass that crosses tensors looks each granule's tensor
- *     up on its own, so a run of short tensors costs one memory latency and not one each;
+ *   - 8 loads in flight per thread in 3 blocks per SM (4 blocks: 464 us, with spills; 16
+ *     loads in 2 blocks: 456); a pass that crosses tensors looks each granule's tensor up on
+ *     its own, so a run of short tensors costs one memory latency and not one each;
  *   - squares in fp32, two at a time, in sums of 8; the sums joined by error-free additions;
  *     fp64 only per block and for values whose squares fp32 cannot hold.
  */
@@ -26,7 +27,7 @@ namespace {
 constexpr int kNormLoads = 8;                // 128-bit loads in flight per thread
 constexpr uint32_t kNormPass = kThreads * kNormLoads;
 constexpr uint32_t kNormMaxBlocks = 2048;    // slots per launch
-constexpr int kNormBlocksPerSm = 4;
+constexpr int kNormBlocksPerSm = 3;
 
 /* A gradient as 16-byte granules, cut at the addresses' multiples of 16 whatever the
  * tensor's own alignment: the first and the last may be partial. */
@@ -177,8 +178,8 @@ __device__ __forceinline__ uint32_t norm_find(const NormArgs<CAP>& a, uint64_t g
     return k;
 }
 
-/* Adds v over the block: a fixed shuffle tree per warp, the warps in order.  Valid in
- * thread 0. */
+/* Adds v over the block in a fixed order: a shuffle tree per warp, then one over the warps'
+ * sums.  Valid in warp 0. */
 __device__ __forceinline__ double block_sum(double v, double* warp_sum)
 {
 #pragma unroll
@@ -187,11 +188,13 @@ __device__ __forceinline__ double block_sum(double v, double* warp_sum)
     if ((threadIdx.x & 31) == 0)
         warp_sum[threadIdx.x >> 5] = v;
     __syncthreads();
-    double t = 0.0;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < kThreads / 32; ++w)
-            t += warp_sum[w];
-    return t;
+    if (threadIdx.x < 32) {
+        v = threadIdx.x < kWarps ? warp_sum[threadIdx.x] : 0.0;
+#pragma unroll
+        for (int o = kWarps / 2; o > 0; o >>= 1)
+            v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
 }
 
 /* Sum of squares over the list's gradients: block b takes granules [b*quota, (b+1)*quota)
@@ -278,14 +281,14 @@ __global__ void __launch_bounds__(kThreads, kNormBlocksPerSm) k_tensors_norm(con
     }
     if (!a.last)
         return;
-    // arrival, as in the norm over the flat buffer: the block's writes are ordered before
-    // the count by the barrier and one fence of thread 0
-    __syncthreads();
+    // arrival: thread 0 has written the block's sum itself, and block_sum's barrier came
+    // after every thread's overflow flag (the scalar block has a barrier of its own)
+    if (blockIdx.x == n_sum)
+        __syncthreads();
     if (threadIdx.x == 0) {
-        asm volatile("fence.acq_rel.gpu;" ::: "memory");
-        is_last = atomicAdd(&st->arrivals, 1u) == gridDim.x - 1;
-        if (is_last)
-            asm volatile("fence.acq_rel.gpu;" ::: "memory");
+        uint32_t before;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(&st->arrivals) : "memory");
+        is_last = before == gridDim.x - 1;
     }
     __syncthreads();
     if (!is_last)
