@@ -539,10 +539,10 @@ def test_adamw_on_long_lists(state, grads, shifts):
 
 @pytest.mark.parametrize("state", ["f32", "u8"])
 def test_long_lists_of_several_launches(state):
-    """900 tensors, 6.7 million elements: the blocks and the queue go on over the launches; a
-    skipped step leaves everything."""
-    sizes = [1 + (k * 7919) % 14_900 for k in range(900)]
-    assert sum(sizes) > 3 << 21
+    """430 tensors, 14 million elements, in the staged form: the blocks and the queue go on
+    over the launches; a skipped step leaves everything."""
+    sizes = [1 + (k * 7919) % 300 for k in range(424)] + [7_000_001, 2, 4096, 7_100_003, 300, 5889]
+    assert sum(sizes) >= len(sizes) << 15
     c = Case(sizes, ("f32", "bf16"), (0, 0, 1), state)
     c.set(**STEP)
     before = c.arrays()
@@ -664,6 +664,34 @@ def test_norm_past_32_bit_offsets():
     z.zero_tensors_grad_norm(z.TensorList(grad=[g]), z.hparams(), work, st)
     assert z.zero_step_state_read(st).sumsq == 91.0
     del g
+    torch.cuda.empty_cache()
+
+
+def test_adamw_past_32_bit_offsets():
+    """2^31 + 300 elements: 8 GB arrays, element and byte offsets past 32 bits."""
+    n = (1 << 31) + 300
+    near = [0, (1 << 30) - 128, (1 << 31) - 128]
+    grad = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    master, m, v = (torch.zeros(n, device="cuda") for _ in "pmv")
+    for k, i in enumerate(near):
+        grad[i:i + 256] = (k + 1) * 1e-3
+        master[i:i + 256] = 0.1 * (k + 1)
+    grad[n - 1] = master[n - 1] = 1.0
+    st = torch.empty(z.STATE_BYTES, dtype=torch.uint8, device="cuda")
+    z.zero_tensors_state_init(1, 1.0, False, 0, st)
+    s = z.zero_step_state_read(st)
+    for k, x in dict(STEP, inv_scale_used=1.0, clip_coef=1.0).items():
+        setattr(s, k, x)
+    z.zero_step_state_write(st, s)
+    z.zero_tensors_adamw(z.TensorList(grad=[grad], master=[master], m=[m], v=[v], weight_decay=0.01), z.hparams(), st)
+    for k, i in enumerate(near + [n - 1]):
+        g, p = grad[i].double().item(), 0.1 * (k + 1) if i < n - 1 else 1.0
+        want = p * (1 - 1e-5) - 2.3e-3 * 0.1 * g / (np.sqrt(0.001) * g / 0.41 + 1e-8)
+        got = master[i:min(n, i + 256)]
+        assert torch.allclose(got, torch.full_like(got, want), rtol=1e-5), i
+        assert torch.allclose(m[i:min(n, i + 256)], torch.full_like(got, 0.1 * g), rtol=1e-5)
+    assert int((master != 0).sum()) == int((m != 0).sum()) == int((v != 0).sum()) == 3 * 256 + 1
+    del grad, master, m, v, got
     torch.cuda.empty_cache()
 
 

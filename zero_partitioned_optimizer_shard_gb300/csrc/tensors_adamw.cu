@@ -847,10 +847,15 @@ int launch_ring(const ListArgs<CAP>& a, cudaStream_t s)
                                 Ring<S8>::kSmem, s, a));
 }
 
-/* Lists of this many elements take the staged kernel.  Measured, direct against staged, us a
- * launch (32-bit states; 8-bit): 2^20 elements 5.3 / 8.9 (4.2 / 7.1), 2^22 21.8 / 22.7
- * (14.8 / 15.1), 2^23 41.0 / 39.7 (25.9 / 24.7), 2^24 78.7 / 73.0 (51.0 / 43.8). */
-constexpr uint64_t kRingElems = 3ull << 21;
+/* Lists of this many elements, and this many per tensor on average, take the staged kernel.
+ * Measured, us a call, direct / staged, 32-bit states (8-bit states):
+ *   4 tensors     2^20 elements 5.3 / 8.9 (4.2 / 7.1), 2^22 21.8 / 22.7 (14.8 / 15.1),
+ *                 2^23 41.0 / 39.7 (25.9 / 24.7), 2^24 78.7 / 73.0 (51.0 / 43.8)
+ *   2^25 elements in tensors of 8,192: 173 / 185 (122 / 151), of 16,384: 172 / 166
+ *                 (111 / 109), of 65,536: 159 / 147 (106 / 94)
+ *   2^23 elements in tensors of 1,024: 91 / 166 (64 / 182): a short tensor leaves most of a
+ *                 stage empty */
+constexpr uint64_t kRingElems = 3ull << 21, kRingTensor = 1ull << 15;
 
 /* One launch of the direct form. */
 template <Op OP, int CAP>
@@ -871,7 +876,7 @@ int adamw_list(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparam
         return ZERO_EINVAL;
     if (rc != ZERO_OK || !at(st, 16))
         return ZERO_EALIGN;
-    if (total >= kRingElems)
+    if (total >= kRingElems && total >= n * kRingTensor)
         return run_list<OP, Ring<kS8>::kChunk>(tensors, nullptr, n, hp, seed, st,
                                                [s](const auto& a) { return launch_ring<kS8>(a, s); });
     return run_list<OP, kUnit>(tensors, nullptr, n, hp, seed, st,
