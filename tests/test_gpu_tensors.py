@@ -347,6 +347,32 @@ def test_whole_step_as_a_user_runs_it():
     graphed.arena.check()
 
 
+@pytest.mark.parametrize("state", ["f32", "u8"])
+def test_tensors_dense_in_another_order(state):
+    """A channels-last weight and a transposed one, every array in that order: the same update
+    as on the elements in memory order."""
+    c = Case([4 * 6 * 5 * 7, 60 * 33], ("f32",), state=state)
+    c.set(**STEP)
+    before = c.arrays()
+
+    def shaped(xs):
+        return [xs[0].view(4, 5, 7, 6).permute(0, 3, 1, 2), xs[1].view(60, 33).t()]
+
+    kw = dict(exps=c.exps) if state == "u8" else {}
+    lst = z.TensorList(grad=shaped(c.grad), master=shaped(c.master), m=shaped(c.m), v=shaped(c.v),
+                       params=shaped(c.params), weight_decay=0.01, **kw)
+    assert not lst.tensors["grad"][0].is_contiguous() and not lst.tensors["m"][1].is_contiguous()
+    if state == "u8":
+        z.zero_tensors_adamw8(lst, c.hp, 4, c.st)
+        check8(c, before, STEP, 4)
+    else:
+        z.zero_tensors_adamw(lst, c.hp, c.st)
+        for k in range(2):
+            p1, tp = expected(c, before, k, c.hp, STEP, before["m"][k], before["v"][k])[2::3]
+            assert np.all(np.abs(c.arrays()["master"][k] - p1) <= tp)
+    c.arena.check()
+
+
 def test_params_may_be_absent_and_integers():
     c = Case([3000, 77])
     c.set(**STEP)
@@ -740,11 +766,13 @@ def test_adamw8_and_read_past_32_bit_offsets():
 def test_lists_refuse_what_the_kernels_cannot_take():
     x = torch.zeros(64, device="cuda")
     u = torch.zeros(64, dtype=torch.uint8, device="cuda")
-    for kw, match in ((dict(grad=[x[::2]]), "contiguous"), (dict(grad=[x.double()]), "type"),
+    square = torch.zeros(8, 8, device="cuda")
+    for kw, match in ((dict(grad=[x[::2]]), "contiguous"), (dict(grad=[square.t()], master=[square]), "order"),
+                      (dict(grad=[square], master=[square.t()]), "order"), (dict(grad=[x.double()]), "type"),
                       (dict(master=[x.half()]), "type"), (dict(grad=[x], master=[x[:63]]), "elements"),
                       (dict(m=[u], v=[x]), "differ"), (dict(m=[x]), "together"),
                       (dict(m=[u], v=[u], exps=[u]), "elements"), (dict(grad=[x], lr_scale=[1.0, 2.0]), "one per tensor"),
-                      (dict(grad=[x], params=[x]), "type"), (dict(grad=[x.cpu()], master=[x]), "contiguous CUDA")):
+                      (dict(grad=[x], params=[x]), "type"), (dict(grad=[x.cpu()], master=[x]), "CUDA")):
         with pytest.raises(ValueError, match=match):
             z.TensorList(**kw)
     lst = z.TensorList(grad=[x], master=[x], m=[x], v=[x])

@@ -335,8 +335,9 @@ class TensorList:
     once and used for as long as the tensors stay where they are.
 
     Every argument is a sequence with one entry per tensor, or None where no call on this
-    list needs it; all are contiguous CUDA tensors of one device.  grad: fp16, bf16 or fp32;
-    master: fp32; m, v: fp32, or uint8 codes with exps, uint8 of 2*ceil(elems/256) (bf16 m
+    list needs it; all are CUDA tensors of one device.  A tensor's arrays are contiguous, or
+    dense in one and the same other order (channels last, a transposed weight).  grad: fp16,
+    bf16 or fp32; master: fp32; m, v: fp32, or uint8 codes with exps, uint8 of 2*ceil(elems/256) (bf16 m
     and v only as a target of zero_tensors_state8_read); params: bf16 or fp16, or 16-bit
     integers, whose type is then the hyperparameters'.  lr_scale, weight_decay: one number,
     or one per tensor.  The list keeps its tensors alive; set_grad() takes gradients that
@@ -391,23 +392,54 @@ class TensorList:
             want = 2 * -(-n // ZERO_STATE8_BLOCK) if name == "exps" else n
             if t.numel() != want:
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements, not {want}")
-            if not t.is_contiguous() or not t.is_cuda or t.get_device() != device:
-                raise ValueError(f"{name}[{i}] is not a contiguous CUDA tensor of the list's device")
+            if not t.is_cuda or t.get_device() != device:
+                raise ValueError(f"{name}[{i}] is not a CUDA tensor of the list's device")
+            if not t.is_contiguous():
+                self._check_order(name, i, t)
             code = known.get(t.dtype, -1)
             if code not in types:
                 raise ValueError(f"{name}[{i}] has type {t.dtype}")
             codes.append(code)
         return codes
 
+    def _check_order(self, name: str, i: int, t) -> None:
+        """A tensor that is not contiguous: dense, and every array of it in the same order."""
+        n = 1
+        for size, stride in sorted(zip(t.shape, t.stride()), key=lambda x: x[1]):
+            if size > 1 and stride != n:
+                raise ValueError(f"{name}[{i}] is not contiguous, nor dense in another order")
+            n *= size
+        for k, xs in self.tensors.items():
+            if k != "exps" and (name == "exps" or xs[i].shape != t.shape or xs[i].stride() != t.stride()):
+                raise ValueError(f"{name}[{i}] and {k}[{i}] differ in order")
+
     def set_grad(self, grad: Sequence) -> None:
         """The same tensors' gradients at new addresses."""
         grad = list(grad)
         if len(grad) != len(self):
             raise ValueError(f"grad has {len(grad)} tensors, the list {len(self)}")
-        codes = self._check("grad", grad)
+        old = self.tensors.get("grad")
         self.tensors["grad"] = grad
+        try:
+            codes = self._check("grad", grad)
+        except ValueError:
+            self.tensors["grad"] = old
+            if old is None:
+                del self.tensors["grad"]
+            raise
         for a, g, code in zip(self.array, grad, codes):
             a.grad, a.grad_dtype = g.data_ptr(), code
+
+
+def _list_stream(tensors: TensorList, stream) -> int | None:
+    """The stream of a call on a list: by default the current one, of the list's device."""
+    if stream is None:
+        import torch
+        current = torch.cuda.current_device()
+        if tensors.device not in (current, -1):
+            raise ValueError(f"the list is on device {tensors.device}, the current device is {current}")
+        return torch._C._cuda_getCurrentRawStream(current)
+    return _stream(stream)
 
 
 def _same_length(a: TensorList, b: TensorList) -> int:
@@ -430,31 +462,32 @@ def zero_tensors_state_init(n_ranks: int, loss_scale: float, dynamic: bool, grow
 def zero_tensors_grad_norm(tensors: TensorList, hp: HParams, workspace, st, stream=None) -> None:
     """Norm, clip coefficient, skip decision and the step's scalars over the list's gradients."""
     _check("zero_tensors_grad_norm", _lib().zero_tensors_grad_norm(
-        tensors.array, len(tensors), C.byref(hp), _ptr(workspace), _ptr(st), _stream(stream)))
+        tensors.array, len(tensors), C.byref(hp), _ptr(workspace), _ptr(st),
+        _list_stream(tensors, stream)))
 
 
 def zero_tensors_adamw(tensors: TensorList, hp: HParams, st, stream=None) -> None:
     """AdamW over the list, fp32 states."""
     _check("zero_tensors_adamw", _lib().zero_tensors_adamw(
-        tensors.array, len(tensors), C.byref(hp), _ptr(st), _stream(stream)))
+        tensors.array, len(tensors), C.byref(hp), _ptr(st), _list_stream(tensors, stream)))
 
 
 def zero_tensors_adamw8(tensors: TensorList, hp: HParams, seed: int, st, stream=None) -> None:
     """AdamW over the list, 8-bit states; seed: of their stochastic rounding."""
     _check("zero_tensors_adamw8", _lib().zero_tensors_adamw8(
-        tensors.array, len(tensors), C.byref(hp), seed, _ptr(st), _stream(stream)))
+        tensors.array, len(tensors), C.byref(hp), seed, _ptr(st), _list_stream(tensors, stream)))
 
 
 def zero_tensors_state8_read(source: TensorList, to: TensorList, stream=None) -> None:
     """The values of source's 8-bit states into to's fp32 or bf16 m and v."""
     _check("zero_tensors_state8_read", _lib().zero_tensors_state8_read(
-        source.array, to.array, _same_length(source, to), _stream(stream)))
+        source.array, to.array, _same_length(source, to), _list_stream(source, stream)))
 
 
 def zero_tensors_state8_write(to: TensorList, source: TensorList, stream=None) -> None:
     """source's fp32 m and v into to's 8-bit states, to the nearest code."""
     _check("zero_tensors_state8_write", _lib().zero_tensors_state8_write(
-        to.array, source.array, _same_length(to, source), _stream(stream)))
+        to.array, source.array, _same_length(to, source), _list_stream(to, stream)))
 
 
 __all__ = [

@@ -71,17 +71,6 @@ __device__ __forceinline__ uint32_t block_exponent(uint32_t top)
 __device__ __forceinline__ float exp_scale(uint32_t b) { return __uint_as_float(b << 23); }
 __device__ __forceinline__ float exp_unscale(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
-__device__ __forceinline__ float decode_m(uint32_t code, float scale)
-{
-    const float y = __fmul_rn(__fmul_rn(__uint_as_float((code & 0x7fu) << 20), 0x1p112f), scale);
-    return __uint_as_float(__float_as_uint(y) | (code & 0x80u) << 24);
-}
-
-__device__ __forceinline__ float decode_v(uint32_t code, float scale)
-{
-    return __fmul_rn(__fmul_rn(__uint_as_float(code << 20), 0x1p96f), scale);
-}
-
 __device__ __forceinline__ uint32_t encode_m(float x, float unscale, uint32_t r)
 {
     const float y = __fmul_rn(__fmul_rn(fabsf(x), unscale), 0x1p-112f);
@@ -95,7 +84,8 @@ __device__ __forceinline__ uint32_t encode_v(float x, float unscale, uint32_t r)
     return max(min((__float_as_uint(y) + r) >> 20, 255u), x != 0.0f ? 1u : 0u);
 }
 
-/* Four codes of a word as floats with the code's exponent in fp32's field. */
+/* One of a word's four codes as a float with the code's exponent in fp32's field: times
+ * 2^112 (m) or 2^96 (v) and the block's 2^(b-127) it is the value. */
 __device__ __forceinline__ float raw_m(uint32_t w, int byte)
 {
     const int top = (int)__byte_perm(w, 0, byte << 12 | 0x444);  // the code in bits 31..24
