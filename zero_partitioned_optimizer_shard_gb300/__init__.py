@@ -431,21 +431,28 @@ class TensorList:
             a.grad, a.grad_dtype = g.data_ptr(), code
 
 
+_TORCH_C = None
+
+
 def _list_stream(tensors: TensorList, stream) -> int | None:
     """The stream of a call on a list: by default the current one, of the list's device."""
-    if stream is None:
+    global _TORCH_C
+    if stream is not None:
+        return _stream(stream)
+    if _TORCH_C is None:
         import torch
-        current = torch.cuda.current_device()
-        if tensors.device not in (current, -1):
-            raise ValueError(f"the list is on device {tensors.device}, the current device is {current}")
-        return torch._C._cuda_getCurrentRawStream(current)
-    return _stream(stream)
+        torch.cuda.current_device()  # CUDA is initialised from here on
+        _TORCH_C = torch._C
+    current = _TORCH_C._cuda_getDevice()
+    if tensors.device not in (current, -1):
+        raise ValueError(f"the list is on device {tensors.device}, the current device is {current}")
+    return _TORCH_C._cuda_getCurrentRawStream(current)
 
 
 def _same_length(a: TensorList, b: TensorList) -> int:
-    if len(a) != len(b):
+    if len(a.elems) != len(b.elems):
         raise ValueError(f"lists of {len(a)} and {len(b)} tensors")
-    return len(a)
+    return len(a.elems)
 
 
 def zero_tensors_workspace_bytes(n_tensors: int) -> int:
@@ -461,33 +468,42 @@ def zero_tensors_state_init(n_ranks: int, loss_scale: float, dynamic: bool, grow
 
 def zero_tensors_grad_norm(tensors: TensorList, hp: HParams, workspace, st, stream=None) -> None:
     """Norm, clip coefficient, skip decision and the step's scalars over the list's gradients."""
-    _check("zero_tensors_grad_norm", _lib().zero_tensors_grad_norm(
-        tensors.array, len(tensors), C.byref(hp), _ptr(workspace), _ptr(st),
-        _list_stream(tensors, stream)))
+    status = _lib().zero_tensors_grad_norm(tensors.array, len(tensors.elems), C.byref(hp), _ptr(workspace),
+                                           _ptr(st), _list_stream(tensors, stream))
+    if status:
+        _check("zero_tensors_grad_norm", status)
 
 
 def zero_tensors_adamw(tensors: TensorList, hp: HParams, st, stream=None) -> None:
     """AdamW over the list, fp32 states."""
-    _check("zero_tensors_adamw", _lib().zero_tensors_adamw(
-        tensors.array, len(tensors), C.byref(hp), _ptr(st), _list_stream(tensors, stream)))
+    status = _lib().zero_tensors_adamw(tensors.array, len(tensors.elems), C.byref(hp), _ptr(st),
+                                       _list_stream(tensors, stream))
+    if status:
+        _check("zero_tensors_adamw", status)
 
 
 def zero_tensors_adamw8(tensors: TensorList, hp: HParams, seed: int, st, stream=None) -> None:
     """AdamW over the list, 8-bit states; seed: of their stochastic rounding."""
-    _check("zero_tensors_adamw8", _lib().zero_tensors_adamw8(
-        tensors.array, len(tensors), C.byref(hp), seed, _ptr(st), _list_stream(tensors, stream)))
+    status = _lib().zero_tensors_adamw8(tensors.array, len(tensors.elems), C.byref(hp), seed, _ptr(st),
+                                        _list_stream(tensors, stream))
+    if status:
+        _check("zero_tensors_adamw8", status)
 
 
 def zero_tensors_state8_read(source: TensorList, to: TensorList, stream=None) -> None:
     """The values of source's 8-bit states into to's fp32 or bf16 m and v."""
-    _check("zero_tensors_state8_read", _lib().zero_tensors_state8_read(
-        source.array, to.array, _same_length(source, to), _list_stream(source, stream)))
+    status = _lib().zero_tensors_state8_read(source.array, to.array, _same_length(source, to),
+                                             _list_stream(source, stream))
+    if status:
+        _check("zero_tensors_state8_read", status)
 
 
 def zero_tensors_state8_write(to: TensorList, source: TensorList, stream=None) -> None:
     """source's fp32 m and v into to's 8-bit states, to the nearest code."""
-    _check("zero_tensors_state8_write", _lib().zero_tensors_state8_write(
-        to.array, source.array, _same_length(to, source), _list_stream(to, stream)))
+    status = _lib().zero_tensors_state8_write(to.array, source.array, _same_length(to, source),
+                                              _list_stream(to, stream))
+    if status:
+        _check("zero_tensors_state8_write", status)
 
 
 __all__ = [
