@@ -9,8 +9,8 @@
  * Both are bound by HBM: 28 bytes an element with 32-bit states and bf16 gradients, 16 with
  * 8-bit states.  Two forms of each:
  *   direct   a warp per 256-element unit, straight from and to global memory.  For short
- *            lists, where one memory latency is all there is: 16 tensors of 2,048 elements
- *            take 2.6 us, 386 tensors with a million elements 5.4.
+ *            lists, where a memory latency or two is all there is: 16,384 elements take 2.7
+ *            us (8-bit states 2.4), a million 5.2 (4.2).
  *   staged   one block per SM; a producer warp bulk-copies chunks into a ring in shared
  *            memory, consumer warps compute (k_tensors_ring).  For long lists: GPT-2
  *            1.5B's 580 tensors take 6,160 us with 32-bit states (106% of the measured copy
@@ -97,16 +97,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
         // 8 consecutive elements per lane, one access an array; else lanes side by side
         const uint64_t i = vec ? off + lane * kPer : off + lane;
         const uint32_t stride = vec ? 1 : 32;
-        float x8[8], p8[8], m8[8], v8[8];
+        float x8[8] = {}, p8[8] = {}, m8[8] = {}, v8[8] = {};
+        RawGrad raw;
         const bool whole = vec && i + kPer <= t.elems;
         if (whole) {
-            RawGrad raw;
             raw.load(t.grad, i, dtype);
             load8(t.master + i, p8);
             load8(m + i, m8);
             load8(v + i, v8);
-            raw.values(dtype, x8);
-        } else {
+        } else if (i < t.elems) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint64_t q = i + e * stride;
@@ -117,6 +116,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
                 v8[e] = in ? __ldcs(v + q) : 0.0f;
             }
         }
+        if (whole)  // only here: inside the branch above they would wait for its loads
+            raw.values(dtype, x8);
         if (skip)  // only now: the loads need not wait for the state's
             return;
 #pragma unroll
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
             store8(v + i, v8);
             if (t.params)
                 store_params8(t.params + i, t.flags & kOutF16, p8);
-        } else {
+        } else if (i < t.elems) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint64_t q = i + e * stride;
