@@ -315,15 +315,20 @@ def test_adamw_gives_the_flat_steps_bits(psi, dtype):
                 assert torch.equal(have[:psi].view(bits), want.view(bits)), (name, k)
 
 
-def test_whole_step_as_a_user_runs_it():
-    """Norm, then AdamW, for a list longer than one launch, on a stream of its own, captured
-    into a graph and replayed; the eager run gives the same bits."""
-    sizes = [40 + 13 * (k % 11) for k in range(450)]
-    eager, graphed = Case(sizes, ("bf16", "f32"), (0, 1)), Case(sizes, ("bf16", "f32"), (0, 1))
+@pytest.mark.parametrize("state", ["f32", "u8"])
+@pytest.mark.parametrize("sizes", [[40 + 13 * (k % 11) for k in range(450)], [6_900_000, 300, 77]],
+                         ids=["450 tensors", "staged"])
+def test_whole_step_as_a_user_runs_it(sizes, state):
+    """Norm, then AdamW, for a list longer than one launch and for one in the staged form, on a
+    stream of its own, captured into a graph and replayed; the eager run gives the same bits."""
+    eager, graphed = (Case(sizes, ("bf16", "f32"), (0, 1), state) for _ in range(2))
 
     def step(c):
         z.zero_tensors_grad_norm(c.list, c.hp, c.work, c.st)
-        z.zero_tensors_adamw(c.list, c.hp, c.st)
+        if state == "u8":
+            z.zero_tensors_adamw8(c.list, c.hp, 6, c.st)
+        else:
+            z.zero_tensors_adamw(c.list, c.hp, c.st)
 
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -331,7 +336,7 @@ def test_whole_step_as_a_user_runs_it():
         for _ in range(4):
             step(eager)
     torch.cuda.current_stream().wait_stream(side)
-    warm = Case(sizes, ("bf16", "f32"), (0, 1))
+    warm = Case(sizes, ("bf16", "f32"), (0, 1), state)
     step(warm)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
@@ -470,7 +475,25 @@ def test_adamw8_values_at_the_ends_of_the_range(shift):
                 assert np.array_equal(after[name][0], want), (name, np.flatnonzero(after[name][0] != want)[:5])
         assert np.all(after["v"][0][v1 > 0] > 0)
         assert np.all(after["m"][0][:256] == 0) and np.all(after["exps"][0][:2] == 0)
+        fits = np.isfinite(v1)      # else the denominator is infinite in fp32, and the update 0
+        with np.errstate(over="ignore"):
+            _, _, p1, _, _, tp = expected(c, before, 0, c.hp, sc, m, v)
+        assert np.all(np.abs(after["master"][0] - p1)[fits] <= tp[fits])
         assert np.all(np.isfinite(after["master"][0]))
+
+
+@pytest.mark.parametrize("eps", [1e-8, 1e-30, 1e-35, 1e-40])
+def test_adamw8_with_a_small_eps(eps):
+    """An eps down to fp32's subnormals, with gradients and states of zero among the others."""
+    c = Case([5000, 300], ("f32",), (0, 1), "u8")
+    c.hp = z.hparams(eps=eps)
+    c.set(**STEP)
+    for x in (*c.grad, *c.m, *c.v):
+        x[::3] = 0
+    before = c.arrays()
+    z.zero_tensors_adamw8(c.list, c.hp, 8, c.st)
+    c.arena.check()
+    check8(c, before, STEP, 8)
 
 
 def test_adamw8_follows_the_32_bit_moments():
