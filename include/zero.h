@@ -546,7 +546,8 @@ int zero_tensors_grad_norm(const zero_tensor_t* tensors, uint64_t n_tensors,
  *   gc = c * (x * st->inv_scale_used);  m = b1*m + (1-b1)*gc;  v = b2*v + (1-b2)*(gc*gc)
  *   p  = p*decay - step*(m / (sqrt(v)/rbc2 + eps));  params = rounded to nearest even
  * with step = st->step_size * lr_scale and decay = f32(1 - lr * lr_scale * weight_decay).
- * A list with lr_scale 1 and the hyperparameters' weight decay gives zero_step's bits.
+ * With lr_scale 1 and the hyperparameters' weight decay, zero_adamw_cast_gather's bits for
+ * the same gradient and step state.
  *   hp   must equal the hp given to zero_tensors_grad_norm for this step */
 int zero_tensors_adamw(const zero_tensor_t* tensors, uint64_t n_tensors,
                        const zero_adamw_hparams_t* hp, const zero_step_state_t* st,

@@ -329,6 +329,26 @@ inline int status_of(cudaError_t e)
     return ZERO_ECUDA;
 }
 
+/* launch_pdl for a kernel whose one argument is large: handed over where it lies (a call by
+ * value would copy the 32 KB once more). */
+template <typename Args>
+cudaError_t launch_args(void (*kernel)(Args), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
+                        const Args& a)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    void* args[1] = {const_cast<Args*>(&a)};
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kernel), args);
+}
+
 /* A launch over `units` units, a warp each, on at most as many blocks as fit at once. */
 template <typename Args>
 int launch_units(void (*kernel)(Args), std::atomic<int> (&per_sm)[64], uint32_t units, cudaStream_t s,
@@ -344,7 +364,7 @@ int launch_units(void (*kernel)(Args), std::atomic<int> (&per_sm)[64], uint32_t 
         per_sm[dev & 63].store(occ, std::memory_order_relaxed);
     }
     const uint64_t want = ((uint64_t)units + kWarps - 1) / kWarps, cap = (uint64_t)sm_count() * (uint64_t)occ;
-    return status_of(launch_pdl(kernel, dim3((unsigned)(want < cap ? want : cap)), dim3(kThreads), 0, s, a));
+    return status_of(launch_args(kernel, (unsigned)(want < cap ? want : cap), kThreads, 0, s, a));
 }
 
 /* Runs an operator over the list, in units of UNIT elements and in as many launches as it

@@ -844,8 +844,8 @@ int launch_ring(const ListArgs<CAP>& a, cudaStream_t s)
         configured[dev & 63].store(true, std::memory_order_relaxed);
     }
     const uint32_t cap = (uint32_t)sm_count(), want = a.l.n_units;
-    return status_of(launch_pdl(k_tensors_ring<S8, CAP>, dim3(want < cap ? want : cap), dim3(Ring<S8>::kThreads),
-                                Ring<S8>::kSmem, s, a));
+    return status_of(launch_args(k_tensors_ring<S8, CAP>, want < cap ? want : cap, Ring<S8>::kThreads,
+                                 Ring<S8>::kSmem, s, a));
 }
 
 /* Lists of this many elements, and this many per tensor on average, take the staged kernel.

@@ -365,7 +365,7 @@ int run_norm(const zero_tensor_t* tensors, uint64_t n, const zero_adamw_hparams_
         const uint64_t pass = total <= blocks * kNormPass ? kThreads : kNormPass;
         a.quota = ((total + blocks - 1) / blocks + pass - 1) / pass * pass;
         const unsigned grid = total ? (unsigned)((total + a.quota - 1) / a.quota) : 0u;
-        const cudaError_t e = launch_pdl(k_tensors_norm<CAP>, dim3(grid + a.last), dim3(kThreads), 0, s, a);
+        const cudaError_t e = launch_args(k_tensors_norm<CAP>, grid + a.last, kThreads, 0, s, a);
         if (e != cudaSuccess)
             return status_of(e);
         a.slot0 += grid;
