@@ -315,6 +315,46 @@ def test_adamw_gives_the_flat_steps_bits(psi, dtype):
                 assert torch.equal(have[:psi].view(bits), want.view(bits)), (name, k)
 
 
+@pytest.mark.parametrize("eps,lr", [(1e-8, 1e-3), (1e-30, 1e-3), (1e-8, 1e30), (1e-12, 0.0)])
+@pytest.mark.parametrize("n", [300_000, 6_400_000])
+def test_adamw_gives_the_flat_steps_bits_on_any_values(n, eps, lr):
+    """zero_adamw_cast_gather's bits where division and square root have their special cases:
+    zeros of both signs, subnormals, every exponent, infinities and NaN in each operand."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    u = lambda: torch.rand(n, device="cuda", generator=gen)  # noqa: E731
+
+    def values(special, lo=-149.0, hi=60.0, signed=True):
+        x = torch.exp2(u() * (hi - lo) + lo) * (1 + u())
+        if signed:
+            x = torch.where(u() < 0.5, -x, x)
+        pick = torch.tensor(special, device="cuda")
+        return torch.where(u() < 0.4, pick[(u() * len(special)).long().clamp(max=len(special) - 1)], x)
+
+    inf, nan = float("inf"), float("nan")
+    g = values([0.0, -0.0, 1e-4, -1e-3, 1e-30, 1e-45], -149, 40)
+    m = values([0.0, -0.0, 1e-40, -1.4e-45, 1e-34, nan, inf], -149, 40)
+    v = values([0.0, 1e-44, 1e-38, 1e-31, 1e-8, inf, nan], -149, 60, signed=False)
+    p = values([0.0, -0.0, 0.02, -0.02, 1e-42, 1e-13, 2.0 ** -40, nan], -149, 20)
+    lay = z.zero_partition(n, 1)
+    hp = z.hparams(eps=eps, lr=lr)
+    st = torch.empty(z.STATE_BYTES, dtype=torch.uint8, device="cuda")
+    z.zero_tensors_state_init(1, 1.0, False, 0, st)
+    s = z.zero_step_state_read(st)
+    s.t, s.clip_coef, s.inv_scale_used, s.step_size, s.rbc2, s.decay = 7, 0.731, 1.0, lr * 2, 0.41, 1.0 - lr * 0.01 if lr < 1 else 0.5
+    z.zero_step_state_write(st, s)
+    flat = [x.clone() for x in (p, m, v)]
+    out = torch.zeros(lay.psi_padded, dtype=torch.bfloat16, device="cuda")
+    assert lay.psi_padded == n
+    z.zero_adamw_cast_gather(lay, hp, g, *flat, out, st)
+    params = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    wd = 0.01 if lr < 1 else 0.5 / lr
+    z.zero_tensors_adamw(z.TensorList(grad=[g], master=[p], m=[m], v=[v], params=[params], weight_decay=wd), hp, st)
+    for name, a, b in (("master", p, flat[0]), ("m", m, flat[1]), ("v", v, flat[2])):
+        same = (a.view(torch.int32) == b.view(torch.int32)) | (a.isnan() & b.isnan())
+        assert bool(same.all()), (name, int((~same).sum()), [(x[~same][:3].tolist()) for x in (a, b, m, v, p, g)])
+    assert bool(((params.view(torch.int16) == out[:n].view(torch.int16)) | (params.isnan() & out[:n].isnan())).all())
+
+
 @pytest.mark.parametrize("state", ["f32", "u8"])
 @pytest.mark.parametrize("sizes", [[40 + 13 * (k % 11) for k in range(450)], [6_900_000, 300, 77]],
                          ids=["450 tensors", "staged"])
