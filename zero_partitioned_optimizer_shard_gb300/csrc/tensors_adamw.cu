@@ -37,34 +37,62 @@ __device__ __forceinline__ Scalars step_scalars(const ListArgs<CAP>& a)
     return s;
 }
 
-/* adamw_one (adamw_elem.cuh), bit for bit, without the slow ways of fp32 division and square
- * root.  Those are taken for zeros and for operands near fp32's lower end, which is what the
- * rows of an embedding that saw no token hold: m = v = 0, or an m that has decayed into the
- * subnormals.  With half of the elements so, GPT-2-sized lists ran at 63% of the copy peak
- * in place of 106% (400 million elements: 2,665 us; now 1,581).
+/* A parameter's update from its new moments, as adamw_one (adamw_elem.cuh) has it, bit for
+ * bit.  ANY: without the slow ways of fp32 division and square root, which are taken for
+ * zeros and for operands near fp32's lower end.  That is what the rows of an embedding that
+ * saw no token hold: m = v = 0, or an m that has decayed into the subnormals; with half of
+ * 400 million elements so, the plain form took 2,665 us in place of 1,579, this one 1,573.
  *   sqrt(v)        below 2^-100: sqrt(v * 2^64) * 2^-32, both factors exact and no result
  *                  subnormal; for v = 0 any operand, and 0 put in its place after the division
  *   step * (m / d) r = m where m = 0 (the same signed zero); and where |m| < tiny and
  *                  |p| >= 2^-40: tiny is 2^-110 where step <= 2^40 eps, so that the true
  *                  value lies below 2^-70, under a quarter of p's last place, as does m: p - r
  *                  is p either way.  The division gets 1 for m there. */
-__device__ __forceinline__ void adamw_even(float g, float& p, float& m, float& v, const Scalars& s, float tiny)
+template <bool ANY>
+__device__ __forceinline__ float new_param(float p, float m, float v, const Scalars& s, float tiny)
 {
-    const float gc = __fmul_rn(s.c, g);
-    m = __fadd_rn(__fmul_rn(s.b1, m), __fmul_rn(s.omb1, gc));
-    v = __fadd_rn(__fmul_rn(s.b2, v), __fmul_rn(s.omb2, __fmul_rn(gc, gc)));
+    p = __fmul_rn(p, s.decay);
+    if (!ANY) {
+        const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v), s.rbc2), s.eps);
+        return __fsub_rn(p, __fmul_rn(s.step, __fdiv_rn(m, denom)));
+    }
     const bool small = v < 0x1p-100f;
     const float root = __fmul_rn(__fsqrt_rn(small ? fmaxf(__fmul_rn(v, 0x1p64f), 0x1p-90f) : v),
                                  small ? 0x1p-32f : 1.0f);
     const float quotient = __fdiv_rn(root, s.rbc2);
     const float denom = __fadd_rn(v == 0.0f ? 0.0f : quotient, s.eps);
-    p = __fmul_rn(p, s.decay);
     const bool same = (m == 0.0f || (fabsf(m) < tiny && fabsf(p) >= 0x1p-40f)) && v >= 0.0f;
     const float r = __fmul_rn(s.step, __fdiv_rn(same ? 1.0f : m, denom));
-    p = __fsub_rn(p, same ? m : r);
+    return __fsub_rn(p, same ? m : r);
 }
 
-/* Below this |m| the update leaves a parameter of 2^-40 or more as it is (adamw_even). */
+/* The AdamW update of a lane's N elements with gradients x * inv: the moments, and the
+ * parameters in the form that the whole warp's values allow (ANY costs 13 instructions an
+ * element more: 4% on misaligned pieces). */
+template <int N>
+__device__ __forceinline__ void adamw_list_elems(const float (&x)[N], float inv, float (&p)[N], float (&m)[N],
+                                                 float (&v)[N], const Scalars& s, float tiny)
+{
+    float low = 1.0f;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float gc = __fmul_rn(s.c, __fmul_rn(x[e], inv));
+        m[e] = __fadd_rn(__fmul_rn(s.b1, m[e]), __fmul_rn(s.omb1, gc));
+        v[e] = __fadd_rn(__fmul_rn(s.b2, v[e]), __fmul_rn(s.omb2, __fmul_rn(gc, gc)));
+        low = fminf(low, fminf(fabsf(m[e]), v[e]));
+    }
+    if (__any_sync(0xffffffffu, low < 0x1p-100f)) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            p[e] = new_param<true>(p[e], m[e], v[e], s, tiny);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            p[e] = new_param<false>(p[e], m[e], v[e], s, tiny);
+    }
+}
+
+/* Below this |m| the update leaves a parameter of 2^-40 or more as it is (new_param). */
 __device__ __forceinline__ float tiny_moment(float step, float eps)
 {
     return step <= __fmul_rn(eps, 0x1p40f) ? 0x1p-110f : 0.0f;
@@ -131,7 +159,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
         // 8 consecutive elements per lane, one access an array; else lanes side by side
         const uint64_t i = vec ? off + lane * kPer : off + lane;
         const uint32_t stride = vec ? 1 : 32;
-        float x8[8] = {}, p8[8] = {}, m8[8] = {}, v8[8] = {};
+        float x8[8], p8[8], m8[8], v8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // what lanes past the end compute with: ordinary values
+            x8[e] = p8[e] = m8[e] = v8[e] = 1.0f;
         RawGrad raw;
         const bool whole = vec && i + kPer <= t.elems;
         if (whole) {
@@ -144,19 +175,17 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
             for (int e = 0; e < 8; ++e) {
                 const uint64_t q = i + e * stride;
                 const bool in = q < t.elems;
-                x8[e] = in ? one_grad(t.grad, q, dtype) : 0.0f;
-                p8[e] = in ? __ldcs(t.master + q) : 0.0f;
-                m8[e] = in ? __ldcs(m + q) : 0.0f;
-                v8[e] = in ? __ldcs(v + q) : 0.0f;
+                x8[e] = in ? one_grad(t.grad, q, dtype) : 1.0f;
+                p8[e] = in ? __ldcs(t.master + q) : 1.0f;
+                m8[e] = in ? __ldcs(m + q) : 1.0f;
+                v8[e] = in ? __ldcs(v + q) : 1.0f;
             }
         }
         if (whole)  // only here: inside the branch above they would wait for its loads
             raw.values(dtype, x8);
         if (skip)  // only now: the loads need not wait for the state's
             return;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            adamw_even(__fmul_rn(x8[e], inv), p8[e], m8[e], v8[e], s, tiny);
+        adamw_list_elems(x8, inv, p8, m8, v8, s, tiny);
         if (whole) {
             store8(t.master + i, p8);
             store8(m + i, m8);
@@ -176,14 +205,18 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
                 }
             }
         }
-        if (at.unit == 0 && lane < t.head && lane < t.elems) {  // before the common boundary
-            float p = t.master[lane], mi = m[lane], vi = v[lane];
-            adamw_even(__fmul_rn(one_grad(t.grad, lane, dtype), inv), p, mi, vi, s, tiny);
-            t.master[lane] = p;
-            m[lane] = mi;
-            v[lane] = vi;
-            if (t.params)
-                t.params[lane] = (t.flags & kOutF16) ? pack1<true>(p) : pack1<false>(p);
+        if (at.unit == 0 && t.head) {  // before the common boundary: an element each
+            const bool in = lane < t.head && lane < t.elems;
+            float x1[1] = {in ? one_grad(t.grad, lane, dtype) : 1.0f}, p1[1] = {in ? t.master[lane] : 1.0f};
+            float m1[1] = {in ? m[lane] : 1.0f}, v1[1] = {in ? v[lane] : 1.0f};
+            adamw_list_elems(x1, inv, p1, m1, v1, s, tiny);
+            if (in) {
+                t.master[lane] = p1[0];
+                m[lane] = m1[0];
+                v[lane] = v1[0];
+                if (t.params)
+                    t.params[lane] = (t.flags & kOutF16) ? pack1<true>(p1[0]) : pack1<false>(p1[0]);
+            }
         }
     }
 }
@@ -852,9 +885,7 @@ __global__ void __launch_bounds__(Ring<S8>::kThreads, 1) k_tensors_ring(const __
             s.step = __fmul_rn(step, t.lr_scale);
             s.decay = t.decay;
             const float tiny = tiny_moment(s.step, s.eps);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                adamw_even(__fmul_rn(x[e], inv), p[e], m[e], v[e], s, tiny);
+            adamw_list_elems(x, inv, p, m, v, s, tiny);
             u.put(t.out_m, m);
             u.put(t.out_v, v);
         }
