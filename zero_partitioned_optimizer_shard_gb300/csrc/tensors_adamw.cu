@@ -437,57 +437,69 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw8(const __grid_con
         const uint32_t dtype = t.flags & kGradMask, unit = at.unit;
         s.step = __fmul_rn(step, t.lr_scale);
         s.decay = t.decay;
-        const bool whole = whole_unit(t, unit);
-        // consecutive elements per lane, else lanes side by side
-        const uint64_t i = (uint64_t)unit * kUnit + (whole ? lane * kPer : lane);
+        const bool vec = t.flags & kVector;
+        // 8 consecutive elements per lane, one access an array; else lanes side by side
+        const uint64_t i = (uint64_t)unit * kUnit + (vec ? lane * kPer : lane);
+        const uint32_t apart = vec ? 1 : 32;
+        const bool full = vec && i + kPer <= t.elems;
         uint8_t* m = static_cast<uint8_t*>(t.m) + i;
         uint8_t* v = static_cast<uint8_t*>(t.v) + i;
         uint8_t* exps = t.exps + 2 * (uint64_t)unit;
         uint32_t bm = exps[0], bv = exps[1];
-        // lane L's seed is that of the block's group L
-        const uint32_t seed = mix32(s.key + (t.group0 + unit * 32 + lane) * kGolden);
-        uint2 cm, cv;
+        uint2 cm = make_uint2(0, 0), cv = cm;
         float x[8], p[8], ym[8], yv[8];
-        if (whole) {
-            RawGrad raw;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // past the end: zeros do not count in the exponents
+            x[e] = p[e] = 0.0f;
+        RawGrad raw;
+        if (full) {
             raw.load(t.grad, i, dtype);
             load8(t.master + i, p);
             cm = __ldcs(reinterpret_cast<const uint2*>(m));
             cv = __ldcs(reinterpret_cast<const uint2*>(v));
-            raw.values(dtype, x);
+        } else if (i < t.elems) {
+            uint32_t am[8], av[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                ym[e] = raw_m(e < 4 ? cm.x : cm.y, e & 3);
-                yv[e] = raw_v(e < 4 ? cv.x : cv.y, e & 3);
+                const bool in = i + e * apart < t.elems;
+                x[e] = in ? one_grad(t.grad, i + e * apart, dtype) : 0.0f;
+                p[e] = in ? __ldcs(t.master + i + e * apart) : 0.0f;
+                am[e] = in ? m[e * apart] : 0u;
+                av[e] = in ? v[e * apart] : 0u;
             }
-            if (skip)
-                return;
+            cm = make_uint2(am[0] | am[1] << 8 | am[2] << 16 | am[3] << 24, am[4] | am[5] << 8 | am[6] << 16 | am[7] << 24);
+            cv = make_uint2(av[0] | av[1] << 8 | av[2] << 16 | av[3] << 24, av[4] | av[5] << 8 | av[6] << 16 | av[7] << 24);
+        }
+        if (full)  // only here: inside the branch above they would wait for its loads
+            raw.values(dtype, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ym[e] = raw_m(e < 4 ? cm.x : cm.y, e & 3);
+            yv[e] = raw_v(e < 4 ? cv.x : cv.y, e & 3);
+        }
+        if (skip)
+            return;
+        // lane L's seed is that of the block's group L
+        const uint32_t seed = mix32(s.key + (t.group0 + unit * 32 + lane) * kGolden);
+        if (vec)
             block8(x, p, ym, yv, bm, bv, RandomInGroup{seed}, cm, cv, s);
+        else
+            block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s);
+        if (full) {
             store8(t.master + i, p);
             if (t.params)
                 store_params8(t.params + i, t.flags & kOutF16, p);
             __stcs(reinterpret_cast<uint2*>(m), cm);
             __stcs(reinterpret_cast<uint2*>(v), cv);
-        } else {
+        } else if (i < t.elems) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const bool in = i + e * 32 < t.elems;
-                x[e] = in ? one_grad(t.grad, i + e * 32, dtype) : 0.0f;
-                p[e] = in ? __ldcs(t.master + i + e * 32) : 0.0f;
-                ym[e] = in ? raw_m(m[e * 32], 0) : 0.0f;
-                yv[e] = in ? raw_v(v[e * 32], 0) : 0.0f;
-            }
-            if (skip)
-                return;
-            block8(x, p, ym, yv, bm, bv, RandomAcross(seed, lane), cm, cv, s);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (i + e * 32 < t.elems) {
-                    m[e * 32] = (uint8_t)((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
-                    v[e * 32] = (uint8_t)((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
-                    __stcs(t.master + i + e * 32, p[e]);
+                if (i + e * apart < t.elems) {
+                    m[e * apart] = (uint8_t)((e < 4 ? cm.x : cm.y) >> (8 * (e & 3)));
+                    v[e * apart] = (uint8_t)((e < 4 ? cv.x : cv.y) >> (8 * (e & 3)));
+                    __stcs(t.master + i + e * apart, p[e]);
                     if (t.params)
-                        t.params[i + e * 32] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
+                        t.params[i + e * apart] = (t.flags & kOutF16) ? pack1<true>(p[e]) : pack1<false>(p[e]);
                 }
             }
         }
