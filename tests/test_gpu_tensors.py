@@ -192,7 +192,7 @@ def test_one_nonfinite_gradient_skips_the_step(value, dtype):
             assert all(np.array_equal(a, b) for a, b in zip(xs, before[k])), k
 
 
-@pytest.mark.parametrize("scale", [1e-42, 1e-30, 1e-22, 1e19, 1e30, 3e38])
+@pytest.mark.parametrize("scale", [1e-42, 1e-30, 1e-22, 2e-19, 1e-18, 3e-18, 1e-15, 1e17, 1e18, 1e19, 1e30, 3e38])
 @pytest.mark.parametrize("shift", [0, 1])
 def test_norm_of_extreme_magnitudes(scale, shift):
     """Squares outside fp32's range, whole or only in one group."""

@@ -5,15 +5,15 @@
  *
  * norm = sqrt(sum of (x * inv)^2) over every gradient element x.  Nothing but a read of the
  * gradients, 2 or 4 bytes an element, so it is bound by HBM: GPT-2 1.5B's 580 bf16
- * gradients (3.1 GB) take 450 us, 104% of the measured copy peak (6,669 GB/s); a short list
+ * gradients (3.1 GB) take 440 us, 106% of the measured copy peak (6,669 GB/s); a short list
  * takes 7 us, most of it the blocks' arrival and the fp64 chain behind it.  What that took:
  *   - each gradient is a run of 16-byte granules at the addresses' own multiples of 16, so
  *     every tensor moves in 128-bit loads whatever its alignment and only a first and a
  *     last granule can be partial (a sum does not care which lane holds what);
  *   - every block takes an equal share of the launch's granules, across tensor boundaries
  *     (chunks of 8192 elements handed out in turn, each looked up anew: 1,068 us);
- *   - 8 loads in flight per thread in 3 blocks per SM (4 blocks: 464 us, with spills; 16
- *     loads in 2 blocks: 456); a pass that crosses tensors looks each granule's tensor up on
+ *   - 8 loads in flight per thread in 3 blocks per SM (450 us when
+ *     first measured so; 4 blocks 464, with spills; 16 loads in 2 blocks 456); a pass that crosses tensors looks each granule's tensor up on
  *     its own, so a run of short tensors costs one memory latency and not one each;
  *   - squares in fp32, two at a time, in sums of 8; the sums joined by error-free additions;
  *     fp64 only per block and for values whose squares fp32 cannot hold.
@@ -63,8 +63,9 @@ static_assert(sizeof(NormArgs<kNormCap>) <= 32764, "kernel parameters");
 
 /* A thread's sum of squares: fp32 sums of a granule's 8 (or 4) squares, joined by
  * error-free additions (hi + lo), so that only a granule's own roundings remain (at most
- * 6); granules whose sum leaves fp32's safe range (below 2^-80 or above 2^120: an
- * infinity, a NaN, or a square that would overflow or vanish) are summed in fp64. */
+ * 6).  Granules whose sum leaves fp32's safe range are summed in fp64: below 2^-120, where
+ * what underflows could reach 2^-27 of it, or above 2^120, which an infinity, a NaN and a
+ * square that overflows exceed too. */
 struct Squares {
     float hi = 0.0f, lo = 0.0f;
     double wide = 0.0;
@@ -78,7 +79,7 @@ struct Squares {
         hi = t;
     }
 
-    /* floor: 2^-80, or infinity where 1/(N*L) is so large that a finite gradient could
+    /* floor: 2^-120, or infinity where 1/(N*L) is so large that a finite gradient could
      * unscale to infinity (then every granule is looked at element by element) */
     template <uint32_t DT>
     __device__ __forceinline__ void granule(const uint4& w, float inv, float floor)
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, kNormBlocksPerSm) k_tensors_norm(con
     grid_launch_dependents();
     zero_step_state_t* st = a.st;
     const float inv = st->inv_scale;
-    const float floor = inv < 0x1p60f ? 0x1p-80f : __int_as_float(0x7f800000);
+    const float floor = inv < 0x1p60f ? 0x1p-120f : __int_as_float(0x7f800000);
     Squares acc;
     NormReady* ready = reinterpret_cast<NormReady*>(a.slots + a.slot0 + n_sum);
     while (lo < hi) {
