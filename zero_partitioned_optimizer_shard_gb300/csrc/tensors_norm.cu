@@ -12,9 +12,10 @@
  *     last granule can be partial (a sum does not care which lane holds what);
  *   - every block takes an equal share of the launch's granules, across tensor boundaries
  *     (chunks of 8192 elements handed out in turn, each looked up anew: 1,068 us);
- *   - 8 loads in flight per thread in 3 blocks per SM (450 us when
- *     first measured so; 4 blocks 464, with spills; 16 loads in 2 blocks 456); a pass that crosses tensors looks each granule's tensor up on
- *     its own, so a run of short tensors costs one memory latency and not one each;
+ *   - 8 loads in flight per thread in 3 blocks per SM (4 blocks 464 us, with spills; 16
+ *     loads in 2 blocks 456);
+ *   - a pass that crosses tensors looks each granule's tensor up on its own, so a run of
+ *     short tensors costs one memory latency and not one each;
  *   - squares in fp32, two at a time, in sums of 8; the sums joined by error-free additions;
  *     fp64 only per block and for values whose squares fp32 cannot hold.
  */
