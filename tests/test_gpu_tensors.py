@@ -69,10 +69,12 @@ class Case:
     """A list with every array guarded; per-tensor gradient types and shifts cycle."""
 
     def __init__(self, sizes, grads=("bf16",), shifts=(0,), state="f32", params=("bf16",), scales=(1.0,),
-                 decays=(0.01,), seed=1, sigma=1e-3):
+                 decays=(0.01,), seed=1, sigma=1e-3, apart=False):
+        """apart: every array of a tensor at an offset of its own, drawn from `shifts`."""
         self.arena, self.sizes = Arena(), list(sizes)
         pick = lambda xs, k: xs[k % len(xs)]  # noqa: E731
-        put = self.arena.put
+        draw = np.random.RandomState(seed)
+        put = lambda x, sh: self.arena.put(x, int(draw.choice(shifts)) if apart else sh)  # noqa: E731
         self.scales = [pick(scales, k) for k in range(len(self.sizes))]
         self.decays = [pick(decays, k) for k in range(len(self.sizes))]
         self.grad, self.master, self.m, self.v, self.exps, self.params = [], [], [], [], [], []
@@ -266,6 +268,66 @@ def test_adamw_over_edges(grads, shifts):
         rounded = torch.from_numpy(after["master"][k]).to(c.params[k].dtype).float().numpy()
         assert np.array_equal(after["params"][k], rounded)
     assert c.state().adamw_next_chunk == 0 and c.state().adamw_done == 0
+
+
+@pytest.mark.parametrize("state", ["f32", "u8"])
+@pytest.mark.parametrize("seed", [3, 4, 5, 6])
+def test_every_array_at_an_offset_of_its_own(state, seed):
+    """Random sizes, types and offsets, in the direct and in the staged form."""
+    draw = np.random.RandomState(seed)
+    sizes = [int(np.exp(draw.uniform(0, np.log(40_000)))) for _ in range(40)]
+    if seed % 2:
+        sizes[7] = 6_400_000 + int(draw.randint(9000))
+    c = Case(sizes, ("f32", "bf16", "f16"), (0, 0, 1, 2, 3, 4, 5, 7, 8, 16), state, ("bf16", "f16"),
+             (1.0, 0.5, 0.0, 2.0), (0.01, 0.0, 0.1), seed, apart=True)
+    c.set(**STEP)
+    s = c.norm()
+    want = np.sqrt(sum(np.sum(host(g).astype(np.float64) ** 2) for g in c.grad))
+    assert abs(s.norm - want) <= 3e-7 * want
+    c.set(**STEP)
+    before = c.arrays()
+    if state == "u8":
+        z.zero_tensors_adamw8(c.list, c.hp, seed, c.st)
+        c.arena.check()
+        check8(c, before, STEP, seed)
+        return
+    z.zero_tensors_adamw(c.list, c.hp, c.st)
+    c.arena.check()
+    after = c.arrays()
+    for k in range(len(sizes)):
+        m1, v1, p1, tm, tv, tp = expected(c, before, k, c.hp, STEP, before["m"][k], before["v"][k])
+        assert np.all(np.abs(after["m"][k] - m1) <= tm) and np.all(np.abs(after["v"][k] - v1) <= tv)
+        assert np.all(np.abs(after["master"][k] - p1) <= tp)
+        assert np.array_equal(after["params"][k], torch.from_numpy(after["master"][k]).to(c.params[k].dtype).float().numpy())
+
+
+def test_the_pieces_of_the_ranks_shards():
+    """The pieces that zero_segment_map lists for each rank, every rank's state in its own
+    shard, the gradients in the model's tensors: the same bits as the whole tensors at once."""
+    sizes = [50_003, 77, 4801, 0, 12_288, 1, 30_000]
+    psi, ranks = sum(sizes), 4
+    lay = z.zero_partition(psi, ranks, 2)
+    grads = [rand(n, 20 + k, 1e-3, torch.bfloat16).cuda() for k, n in enumerate(sizes)]
+    flat = {"master": rand(lay.psi_padded, 1, 0.02).cuda(), "m": rand(lay.psi_padded, 2, 1e-3).cuda(),
+            "v": rand(lay.psi_padded, 3, 1e-3, square=True).cuda()}
+    decay = [0.1 if n > 5000 else 0.0 for n in sizes]
+    c = Case([1])
+    c.set(**STEP)
+    cuts = np.cumsum([0, *sizes])
+    whole = {k: x.clone() for k, x in flat.items()}
+    z.zero_tensors_adamw(z.TensorList(grad=grads, weight_decay=decay, **{
+        k: [x[a:b] for a, b in zip(cuts, cuts[1:])] for k, x in whole.items()}), c.hp, c.st)
+    shards = [{k: x[r * lay.shard:(r + 1) * lay.shard].clone() for k, x in flat.items()} for r in range(ranks)]
+    for r in range(ranks):
+        mine = [s for s in z.zero_segment_map(lay, sizes) if s.rank == r]
+        lst = z.TensorList(
+            grad=[grads[s.tensor][s.tensor_offset:s.tensor_offset + s.count] for s in mine],
+            weight_decay=[decay[s.tensor] for s in mine],
+            **{k: [x[s.shard_offset:s.shard_offset + s.count] for s in mine] for k, x in shards[r].items()})
+        z.zero_tensors_adamw(lst, c.hp, c.st)
+    for k, x in whole.items():
+        got = torch.cat([s[k] for s in shards])
+        assert torch.equal(got.view(torch.int32), x.view(torch.int32)), k
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
