@@ -554,7 +554,8 @@ int zero_tensors_adamw(const zero_tensor_t* tensors, uint64_t n_tensors,
                        zero_stream_t stream);
 
 /* The same with 8-bit states: m and v are decoded, updated in fp32, used in fp32 for the
- * parameters (with sqrt(v) * (1/rbc2) in the denominator), and stored in 8 bits again.
+ * parameters (with sqrt(v) * (1/rbc2) in the denominator; the square root and the quotient
+ * are within 2 ulp), and stored in 8 bits again.
  * master and params stay as in zero_tensors_adamw.
  *   seed   of the rounding; any value, the same for a whole run */
 int zero_tensors_adamw8(const zero_tensor_t* tensors, uint64_t n_tensors,

@@ -341,7 +341,7 @@ class TensorList:
     and v only as a target of zero_tensors_state8_read); params: bf16 or fp16, or 16-bit
     integers, whose type is then the hyperparameters'.  lr_scale, weight_decay: one number,
     or one per tensor.  The list keeps its tensors alive; set_grad() takes gradients that
-    have moved."""
+    have moved.  The calls write the tensors in place, past autograd."""
 
     _TYPES = {"grad": (ZERO_F16, ZERO_BF16, ZERO_F32), "master": (ZERO_F32,), "exps": (ZERO_U8,),
               "m": (ZERO_F32, ZERO_BF16, ZERO_U8), "v": (ZERO_F32, ZERO_BF16, ZERO_U8),
