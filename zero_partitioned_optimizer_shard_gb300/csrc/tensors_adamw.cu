@@ -13,8 +13,8 @@
  *            us (8-bit states 2.4), a million 5.2 (4.2).
  *   staged   one block per SM; a producer warp bulk-copies chunks into a ring in shared
  *            memory, consumer warps compute (k_tensors_ring).  For long lists: GPT-2
- *            1.5B's 580 tensors take 6,160 us with 32-bit states (106% of the measured copy
- *            peak; the direct form 6,929) and 3,554 us with 8-bit states (105%; 4,122).
+ *            1.5B's 580 tensors take 6,147 us with 32-bit states (106% of the measured copy
+ *            peak; the direct form 6,929) and 3,546 us with 8-bit states (105%; 4,122).
  */
 #include "tensors.cuh"
 
