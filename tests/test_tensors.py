@@ -2,6 +2,8 @@
 refusals (every call here is invalid or empty, so nothing reaches the device), and the 8-bit
 form's definition on the host: unbiased rounding, round trips, the generator's quality."""
 import ctypes as C
+import os
+import re
 
 import numpy as np
 import pytest
@@ -135,6 +137,21 @@ def test_tensor_list_refusals():
     with pytest.raises(ValueError, match="the list 1"):
         z.TensorList(master=[f], grad=[f, f])
     assert len(z.TensorList(grad=[])) == 0
+
+
+def test_loads_of_the_list_kernels_stay_behind_their_waits():
+    """The kernels over lists know their first addresses before they wait for the launch
+    before them.  A load that the compiler may move (an asm that is not volatile, an intrinsic
+    that may be one) or that the hardware may take through the read-only path is not theirs:
+    it could read what that launch has yet to write."""
+    names = ("tensors.cuh", "tensors_norm.cu", "tensors_adamw.cu", "tensors_codec.cu")
+    for name in names:
+        with open(os.path.join(_build.CSRC, name)) as f:
+            code = re.sub(r"/\*.*?\*/|//[^\n]*", "", f.read(), flags=re.S)
+        assert not re.findall(r"\b(?:ld_stream_\w+|__ld\w+)\s*\(", code), name
+        loads = re.findall(r"\basm\b(\s+volatile)?\s*\(\s*\"[^\"]*\bld\.global([\w.:]*)", code)
+        assert all(volatile and ".nc" not in kind for volatile, kind in loads), (name, loads)
+        assert loads or name in ("tensors_adamw.cu", "tensors_codec.cu")
 
 
 # ------------------------------------------------------------------------------------------

@@ -116,11 +116,46 @@ __device__ __forceinline__ void locate(const List<CAP>& l, uint32_t u, Place& p)
     p.unit = u - p.begin;
 }
 
+/* Loads of what an earlier launch may have written.  A kernel over a list works out its
+ * first addresses before grid_dependency_wait(): volatile keeps these loads behind the wait
+ * (and the norm's behind its arrival), in the order written.  They do not take the read-only
+ * path (.nc): its promise, that nothing writes while the kernel runs, does not hold for a
+ * kernel that starts before its predecessor ends. */
+__device__ __forceinline__ uint4 ld_list_v4(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint2 ld_list_v2(const void* p)
+{
+    uint2 v;
+    asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint16_t ld_list_u16(const void* p)
+{
+    unsigned short v;
+    asm volatile("ld.global.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float ld_list_f32(const float* p)
+{
+    float v;
+    asm volatile("ld.global.cs.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ float one_grad(const void* g, uint64_t i, uint32_t dtype)
 {
     if (dtype == ZERO_F32)
-        return __ldcs(static_cast<const float*>(g) + i);
-    const uint16_t b = ld_stream_u16(static_cast<const uint16_t*>(g) + i);
+        return ld_list_f32(static_cast<const float*>(g) + i);
+    const uint16_t b = ld_list_u16(static_cast<const uint16_t*>(g) + i);
     return dtype == ZERO_F16 ? one16<ZERO_F16>(b) : one16<ZERO_BF16>(b);
 }
 

@@ -111,7 +111,7 @@ struct RawGrad {
         if (dtype == ZERO_F32) {
             load8(static_cast<const float*>(g) + i, w);
         } else {
-            const uint4 a = ld_stream_v4(static_cast<const uint16_t*>(g) + i);
+            const uint4 a = ld_list_v4(static_cast<const uint16_t*>(g) + i);
             w[0] = __uint_as_float(a.x), w[1] = __uint_as_float(a.y);
             w[2] = __uint_as_float(a.z), w[3] = __uint_as_float(a.w);
         }
@@ -176,9 +176,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw(const __grid_cons
                 const uint64_t q = i + e * stride;
                 const bool in = q < t.elems;
                 x8[e] = in ? one_grad(t.grad, q, dtype) : 1.0f;
-                p8[e] = in ? __ldcs(t.master + q) : 1.0f;
-                m8[e] = in ? __ldcs(m + q) : 1.0f;
-                v8[e] = in ? __ldcs(v + q) : 1.0f;
+                p8[e] = in ? ld_list_f32(t.master + q) : 1.0f;
+                m8[e] = in ? ld_list_f32(m + q) : 1.0f;
+                v8[e] = in ? ld_list_f32(v + q) : 1.0f;
             }
         }
         if (whole)  // only here: inside the branch above they would wait for its loads
@@ -455,15 +455,15 @@ __global__ void __launch_bounds__(kThreads, 4) k_tensors_adamw8(const __grid_con
         if (full) {
             raw.load(t.grad, i, dtype);
             load8(t.master + i, p);
-            cm = __ldcs(reinterpret_cast<const uint2*>(m));
-            cv = __ldcs(reinterpret_cast<const uint2*>(v));
+            cm = ld_list_v2(m);
+            cv = ld_list_v2(v);
         } else if (i < t.elems) {
             uint32_t am[8], av[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const bool in = i + e * apart < t.elems;
                 x[e] = in ? one_grad(t.grad, i + e * apart, dtype) : 0.0f;
-                p[e] = in ? __ldcs(t.master + i + e * apart) : 0.0f;
+                p[e] = in ? ld_list_f32(t.master + i + e * apart) : 0.0f;
                 am[e] = in ? m[e * apart] : 0u;
                 av[e] = in ? v[e * apart] : 0u;
             }

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads, 8) k_state8_read(const __grid_consta
         auto value_m = [&](float y) { return __fmul_rn(__fmul_rn(y, 0x1p112f), scale_m); };
         auto value_v = [&](float y) { return __fmul_rn(__fmul_rn(y, 0x1p96f), scale_v); };
         if (whole) {
-            const uint2 wm = __ldcs(reinterpret_cast<const uint2*>(cm)), wv = __ldcs(reinterpret_cast<const uint2*>(cv));
+            const uint2 wm = ld_list_v2(cm), wv = ld_list_v2(cv);
             float m[8], v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -123,8 +123,8 @@ __global__ void __launch_bounds__(kThreads, 6) k_state8_write(const __grid_const
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                m[e] = at + e * 32 < t.elems ? __ldcs(xm + e * 32) : 0.0f;
-                v[e] = at + e * 32 < t.elems ? __ldcs(xv + e * 32) : 0.0f;
+                m[e] = at + e * 32 < t.elems ? ld_list_f32(xm + e * 32) : 0.0f;
+                v[e] = at + e * 32 < t.elems ? ld_list_f32(xv + e * 32) : 0.0f;
             }
         }
         uint2 wm, wv;

@@ -135,7 +135,7 @@ __device__ __forceinline__ uint4 partial_granule(const NormRef& t, uint64_t j)
         for (int e = 0; e < 8; ++e) {
             const uint64_t i = j * 8 + e;
             if (i >= t.skip && i < past)
-                w[e >> 1] |= (uint32_t)ld_stream_u16(t.base + i * 2) << (16 * (e & 1));
+                w[e >> 1] |= (uint32_t)ld_list_u16(t.base + i * 2) << (16 * (e & 1));
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -146,7 +146,7 @@ __device__ __forceinline__ uint4 any_granule(const NormRef& t, uint64_t j)
 {
     const uint64_t n = t.dtype == ZERO_F32 ? 4 : 8;
     if (j * n >= t.skip && (j + 1) * n <= t.skip + t.elems)
-        return ld_stream_v4(t.base + j * 16);
+        return ld_list_v4(t.base + j * 16);
     return partial_granule(t, j);
 }
 
@@ -159,7 +159,7 @@ __device__ __forceinline__ void norm_passes(const char* p, uint64_t passes, floa
         uint4 w[kNormLoads];
 #pragma unroll
         for (int q = 0; q < kNormLoads; ++q)
-            w[q] = ld_stream_v4(p + q * kThreads * 16);
+            w[q] = ld_list_v4(p + q * kThreads * 16);
 #pragma unroll
         for (int q = 0; q < kNormLoads; ++q)
             acc.granule<DT>(w[q], inv, floor);
@@ -178,6 +178,26 @@ __device__ __forceinline__ uint32_t norm_find(const NormArgs<CAP>& a, uint64_t g
             k = mid + 1;
     }
     return k;
+}
+
+/* What other blocks of this launch have written, read past L1 after their arrival. */
+__device__ __forceinline__ uint32_t ld_other(const uint32_t* p)
+{
+    uint32_t x;
+    asm volatile("ld.global.cg.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+    return x;
+}
+
+__device__ __forceinline__ float ld_other(const float* p)
+{
+    return __uint_as_float(ld_other(reinterpret_cast<const uint32_t*>(p)));
+}
+
+__device__ __forceinline__ double ld_other(const double* p)
+{
+    double x;
+    asm volatile("ld.global.cg.f64 %0, [%1];" : "=d"(x) : "l"(p) : "memory");
+    return x;
 }
 
 /* Adds v over the block in a fixed order: a shuffle tree per warp, then one over the warps'
@@ -297,18 +317,18 @@ __global__ void __launch_bounds__(kThreads, kNormBlocksPerSm) k_tensors_norm(con
         return;
     double v = 0.0;
     for (uint32_t i = threadIdx.x; i < a.slot0 + n_sum; i += kThreads)
-        v += __ldcg(a.slots + i);
-    const uint32_t overflow = __ldcg(&st->overflow) != 0;
+        v += ld_other(a.slots + i);
+    const uint32_t overflow = ld_other(&st->overflow) != 0;
     const double sumsq = block_sum(v, warp_sum) * ((double)inv * (double)inv);
     // block_sum's barrier: every thread has read the overflow flag
     if (threadIdx.x == 32) {
-        const ScalerCand cand{__ldcg(&ready->cand.L_skip), __ldcg(&ready->cand.inv_skip),
-                              __ldcg(&ready->cand.L_ok), __ldcg(&ready->cand.inv_ok),
-                              __ldcg(&ready->cand.good_ok), __ldcg(&ready->cand.decay)};
+        const ScalerCand cand{ld_other(&ready->cand.L_skip), ld_other(&ready->cand.inv_skip),
+                              ld_other(&ready->cand.L_ok), ld_other(&ready->cand.inv_ok),
+                              ld_other(&ready->cand.good_ok), ld_other(&ready->cand.decay)};
         scaler_apply(st, cand, overflow, st->t + 1);
         if (!overflow) {
-            st->step_size = __ldcg(&ready->step_size);
-            st->rbc2 = __ldcg(&ready->rbc2);
+            st->step_size = ld_other(&ready->step_size);
+            st->rbc2 = ld_other(&ready->rbc2);
         }
     }
     if (threadIdx.x == 0) {

@@ -92,9 +92,11 @@ struct InitArgs {
 
 /* Programmatic dependent launch (Hopper/Blackwell): the kernel may be launched while the
  * preceding kernel in the stream is still finishing, so the launch itself overlaps that
- * kernel's tail.  Every kernel launched this way executes grid_dependency_wait() as its
- * first instruction, which returns once the preceding grid has completed and its memory
- * is visible: nothing runs early, so stream order holds whatever the preceding kernel is. */
+ * kernel's tail.  Every kernel launched this way executes grid_dependency_wait() before it
+ * touches memory that another launch may have written (the kernels over lists look their
+ * first unit up in their own parameters ahead of it); it returns once the preceding grid
+ * has completed and its memory is visible, so stream order holds whatever the preceding
+ * kernel is. */
 __device__ __forceinline__ void grid_dependency_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
