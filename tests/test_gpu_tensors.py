@@ -210,6 +210,23 @@ def test_norm_of_extreme_magnitudes(scale, shift):
     assert abs(c.norm().norm - float(np.float32(scale))) <= 3e-7 * scale
 
 
+@pytest.mark.parametrize("grads,n,value", [(("bf16",), 300_000_000, 4e17), (("f32",), 130_000_000, 5.7e17),
+                                           (("bf16", "f32"), 160_000_000, 4e17)])
+def test_norm_of_long_lists_of_large_gradients(grads, n, value):
+    """Finite gradients whose squares fp32 can hold one granule at a time, but not a whole
+    share's sum of them (over 256 granules a thread): the norm is finite, the clip bites."""
+    xs = [torch.full((n,), value, dtype=GRAD[d], device="cuda") for d in grads]
+    st = torch.empty(z.STATE_BYTES, dtype=torch.uint8, device="cuda")
+    work = torch.empty(z.zero_tensors_workspace_bytes(len(xs)), dtype=torch.uint8, device="cuda")
+    z.zero_tensors_state_init(1, 1.0, False, 0, st)
+    z.zero_tensors_grad_norm(z.TensorList(grad=xs), z.hparams(), work, st)
+    s = z.zero_step_state_read(st)
+    want = np.sqrt(sum(n * float(x[0].double()) ** 2 for x in xs))
+    assert (s.skip, s.t, s.n_skipped) == (0, 1, 0)
+    assert abs(s.norm - want) <= 3e-7 * want
+    assert s.clip_coef == np.float32(1.0 / (s.norm + 1e-6)) and s.applied_c == s.clip_coef
+
+
 def test_norm_of_zero_and_of_a_gradient_that_unscaling_overflows():
     c = Case([5000, 3], ("f32",))
     c.grad[0].zero_()

@@ -65,8 +65,9 @@ static_assert(sizeof(NormArgs<kNormCap>) <= 32764, "kernel parameters");
 /* A thread's sum of squares: fp32 sums of a granule's 8 (or 4) squares, joined by
  * error-free additions (hi + lo), so that only a granule's own roundings remain (at most
  * 6).  Granules whose sum leaves fp32's safe range are summed in fp64: below 2^-120, where
- * what underflows could reach 2^-27 of it, or above 2^120, which an infinity, a NaN and a
- * square that overflows exceed too. */
+ * what underflows could reach 2^-27 of it, or from 2^100 up, which an infinity, a NaN and a
+ * square that overflows exceed too.  Below that hi stays finite over 2^27 granules and more;
+ * a thread's share of gradients that fill the GPU's memory is 2^18. */
 struct Squares {
     float hi = 0.0f, lo = 0.0f;
     double wide = 0.0;
@@ -90,7 +91,7 @@ struct Squares {
             const float x2 = __uint_as_float(w.z), x3 = __uint_as_float(w.w);
             const float s = __fadd_rn(__fmaf_rn(x0, x0, __fmul_rn(x1, x1)),
                                       __fmaf_rn(x2, x2, __fmul_rn(x3, x3)));
-            if (s < 0x1p120f && s > floor) {
+            if (s < 0x1p100f && s > floor) {
                 add(s);
             } else if (((w.x | w.y | w.z | w.w) & 0x7fffffffu) != 0) {
                 wide += sumsq_wide(x0, x1, x2, x3, 0.f, 0.f, 0.f, 0.f, 0xfu);
@@ -106,7 +107,7 @@ struct Squares {
             float s0, s1;
             f2_split(s2, s0, s1);
             const float s = __fadd_rn(s0, s1);
-            if (s < 0x1p120f && s > floor) {
+            if (s < 0x1p100f && s > floor) {
                 add(s);
             } else if (((w.x | w.y | w.z | w.w) & 0x7fff7fffu) != 0) {
                 wide += sumsq_wide(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], 0xffu);
