@@ -434,6 +434,37 @@ def test_adamw_gives_the_flat_steps_bits_on_any_values(n, eps, lr):
     assert bool(((params.view(torch.int16) == out[:n].view(torch.int16)) | (params.isnan() & out[:n].isnan())).all())
 
 
+@pytest.mark.parametrize("n", [300_000, 6_400_000])
+def test_adamw_shows_a_negative_second_moment(n):
+    """A v that has gone negative (a damaged state) gives NaN, as zero_adamw_cast_gather does,
+    and no finite update, however small it is and whatever lies beside it."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    u = lambda: torch.rand(n, device="cuda", generator=gen)  # noqa: E731
+    g = torch.where(u() < 0.5, 0.0, 1e-4 * (u() - 0.5))
+    m, p = 1e-3 * (u() - 0.5), 0.02 * (u() - 0.5)
+    m[u() < 0.3] = 0.0
+    v = torch.exp2(-149 + 150 * u())
+    v = torch.where(u() < 0.3, -v, torch.where(u() < 0.3, 0.0, v))
+    lay, hp = z.zero_partition(n, 1), z.hparams()
+    assert lay.psi_padded == n
+    st = torch.empty(z.STATE_BYTES, dtype=torch.uint8, device="cuda")
+    z.zero_tensors_state_init(1, 1.0, False, 0, st)
+    s = z.zero_step_state_read(st)
+    s.t, s.clip_coef, s.inv_scale_used, s.step_size, s.rbc2 = 7, 0.731, 1.0, 2e-3, 0.41
+    s.decay = 1.0 - float(np.float32(hp.lr)) * float(np.float32(0.01))
+    z.zero_step_state_write(st, s)
+    flat = [x.clone() for x in (p, m, v)]
+    out = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    z.zero_adamw_cast_gather(lay, hp, g, *flat, out, st)
+    params = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    z.zero_tensors_adamw(z.TensorList(grad=[g], master=[p], m=[m], v=[v], params=[params], weight_decay=0.01), hp, st)
+    assert int((flat[2] < 0).sum()) > n // 10
+    assert bool(params[flat[2] < 0].isnan().all()) and bool(p[flat[2] < 0].isnan().all())
+    for name, a, b in (("master", p, flat[0]), ("m", m, flat[1]), ("v", v, flat[2])):
+        same = (a.view(torch.int32) == b.view(torch.int32)) | (a.isnan() & b.isnan())
+        assert bool(same.all()), (name, int((~same).sum()))
+
+
 @pytest.mark.parametrize("state", ["f32", "u8"])
 @pytest.mark.parametrize("sizes", [[40 + 13 * (k % 11) for k in range(450)], [6_900_000, 300, 77]],
                          ids=["450 tensors", "staged"])

@@ -43,7 +43,8 @@ __device__ __forceinline__ Scalars step_scalars(const ListArgs<CAP>& a)
  * saw no token hold: m = v = 0, or an m that has decayed into the subnormals; with half of
  * 400 million elements so, the plain form took 2,665 us in place of 1,579, this one 1,573.
  *   sqrt(v)        below 2^-100: sqrt(v * 2^64) * 2^-32, both factors exact and no result
- *                  subnormal; for v = 0 any operand, and 0 put in its place after the division
+ *                  subnormal; for v = 0 any operand, and 0 put in its place after the division;
+ *                  a v < 0 gives NaN either way
  *   step * (m / d) r = m where m = 0 (the same signed zero); and where |m| < tiny and
  *                  |p| >= 2^-40: tiny is 2^-110 where step <= 2^40 eps, so that the true
  *                  value lies below 2^-70, under a quarter of p's last place, as does m: p - r
@@ -56,9 +57,9 @@ __device__ __forceinline__ float new_param(float p, float m, float v, const Scal
         const float denom = __fadd_rn(__fdiv_rn(__fsqrt_rn(v), s.rbc2), s.eps);
         return __fsub_rn(p, __fmul_rn(s.step, __fdiv_rn(m, denom)));
     }
-    const bool small = v < 0x1p-100f;
-    const float root = __fmul_rn(__fsqrt_rn(small ? fmaxf(__fmul_rn(v, 0x1p64f), 0x1p-90f) : v),
-                                 small ? 0x1p-32f : 1.0f);
+    const bool small = fabsf(v) < 0x1p-100f;
+    const float up = small ? __fmul_rn(v, 0x1p64f) : v;
+    const float root = __fmul_rn(__fsqrt_rn(v == 0.0f ? 1.0f : up), small ? 0x1p-32f : 1.0f);
     const float quotient = __fdiv_rn(root, s.rbc2);
     const float denom = __fadd_rn(v == 0.0f ? 0.0f : quotient, s.eps);
     const bool same = (m == 0.0f || (fabsf(m) < tiny && fabsf(p) >= 0x1p-40f)) && v >= 0.0f;
