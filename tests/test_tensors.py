@@ -154,6 +154,47 @@ def test_loads_of_the_list_kernels_stay_behind_their_waits():
         assert loads or name in ("tensors_adamw.cu", "tensors_codec.cu")
 
 
+class OnGpu(torch.Tensor):
+    """A host tensor that passes for one of device 0: lists are built, nothing is launched."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
+def on_gpu(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+
+def weight(order, dtype=torch.float32):
+    """A 4-dimensional weight of 4 x 3 x 5 x 2, contiguous or dense in another order."""
+    return on_gpu(4, 5, 2, 3, dtype=dtype).permute(0, 3, 1, 2) if order == "channels last" else on_gpu(4, 3, 5, 2, dtype=dtype)
+
+
+@pytest.mark.parametrize("order,other", [("contiguous", "channels last"), ("channels last", "contiguous")])
+@pytest.mark.parametrize("first_grad", [False, True])
+@pytest.mark.parametrize("state", [torch.float32, torch.uint8])
+def test_set_grad_refuses_gradients_in_another_order(order, other, first_grad, state):
+    """As the constructor does: element i of the gradient is then not element i of the master.
+    The list stays as it was, the tensors it keeps alive included."""
+    arrays = dict(master=[on_gpu(7), weight(order)], m=[on_gpu(7, dtype=state), weight(order, state)],
+                  v=[on_gpu(7, dtype=state), weight(order, state)])
+    if state == torch.uint8:
+        arrays["exps"] = [on_gpu(2, dtype=state), on_gpu(2, dtype=state)]
+    kw = dict(grad=[on_gpu(7), weight(order)]) if first_grad else {}
+    with pytest.raises(ValueError, match="differ in order"):
+        z.TensorList(grad=[on_gpu(7), weight(other)], **arrays)
+    lst = z.TensorList(**arrays, **kw)
+    before, kept = bytes(lst.array), lst.tensors.get("grad")
+    with pytest.raises(ValueError, match="differ in order"):
+        lst.set_grad([on_gpu(7), weight(other)])
+    assert bytes(lst.array) == before and lst.tensors.get("grad") is kept
+    moved = [on_gpu(7, dtype=torch.bfloat16), weight(order, torch.bfloat16)]
+    lst.set_grad(moved)
+    assert [a.grad for a in lst.array] == [g.data_ptr() for g in moved]
+    assert [a.grad_dtype for a in lst.array] == [z.ZERO_BF16] * 2 and lst.tensors["grad"] == moved
+
+
 # ------------------------------------------------------------------------------------------
 # the 8-bit form on the host
 # ------------------------------------------------------------------------------------------

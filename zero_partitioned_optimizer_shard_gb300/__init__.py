@@ -358,6 +358,7 @@ class TensorList:
         first = next(iter(self.tensors.values()))
         self.elems = [t.numel() for t in first]
         self.device = first[0].get_device() if first else -1
+        self._other_order = set()  # where the arrays besides the gradient are not contiguous
         n = len(first)
         for k, x in self.tensors.items():
             if len(x) != n:
@@ -394,8 +395,10 @@ class TensorList:
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements, not {want}")
             if not t.is_cuda or t.get_device() != device:
                 raise ValueError(f"{name}[{i}] is not a CUDA tensor of the list's device")
-            if not t.is_contiguous():
+            if (i in self._other_order and name != "exps") or not t.is_contiguous():
                 self._check_order(name, i, t)
+                if name != "grad":
+                    self._other_order.add(i)
             code = known.get(t.dtype, -1)
             if code not in types:
                 raise ValueError(f"{name}[{i}] has type {t.dtype}")
@@ -403,7 +406,8 @@ class TensorList:
         return codes
 
     def _check_order(self, name: str, i: int, t) -> None:
-        """A tensor that is not contiguous: dense, and every array of it in the same order."""
+        """A tensor some array of which is not contiguous: dense, and every array of it in the
+        same order."""
         n = 1
         for size, stride in sorted(zip(t.shape, t.stride()), key=lambda x: x[1]):
             if size > 1 and stride != n:
@@ -414,7 +418,7 @@ class TensorList:
                 raise ValueError(f"{name}[{i}] and {k}[{i}] differ in order")
 
     def set_grad(self, grad: Sequence) -> None:
-        """The same tensors' gradients at new addresses."""
+        """The same tensors' gradients at new addresses, in the order of the other arrays."""
         grad = list(grad)
         if len(grad) != len(self):
             raise ValueError(f"grad has {len(grad)} tensors, the list {len(self)}")
