@@ -195,6 +195,17 @@ def test_set_grad_refuses_gradients_in_another_order(order, other, first_grad, s
     assert [a.grad_dtype for a in lst.array] == [z.ZERO_BF16] * 2 and lst.tensors["grad"] == moved
 
 
+def test_set_grad_keeps_the_old_gradients_whatever_the_new_ones_lack():
+    """A gradient that is None (a parameter that took no part) raises; the list still holds the
+    tensors that its addresses point to."""
+    lst = z.TensorList(grad=[on_gpu(8), on_gpu(9)], master=[on_gpu(8), on_gpu(9)])
+    kept, before = lst.tensors["grad"], bytes(lst.array)
+    for bad in ([on_gpu(8), None], [on_gpu(8), on_gpu(8)], [on_gpu(8)], [on_gpu(8), on_gpu(9, dtype=torch.float64)]):
+        with pytest.raises((ValueError, AttributeError)):
+            lst.set_grad(bad)
+        assert lst.tensors["grad"] is kept and bytes(lst.array) == before
+
+
 # ------------------------------------------------------------------------------------------
 # the 8-bit form on the host
 # ------------------------------------------------------------------------------------------

@@ -426,7 +426,7 @@ class TensorList:
         self.tensors["grad"] = grad
         try:
             codes = self._check("grad", grad)
-        except ValueError:
+        except BaseException:  # the addresses in use stay those of tensors that are kept
             self.tensors["grad"] = old
             if old is None:
                 del self.tensors["grad"]
