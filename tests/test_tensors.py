@@ -206,6 +206,17 @@ def test_set_grad_keeps_the_old_gradients_whatever_the_new_ones_lack():
         assert lst.tensors["grad"] is kept and bytes(lst.array) == before
 
 
+def test_dimensions_of_one_element_do_not_count_as_an_order():
+    """The strides of such dimensions say nothing of where the elements lie."""
+    a = on_gpu(4, 1, 5, 2).permute(0, 3, 1, 2)          # 4 x 2 x 1 x 5
+    b = torch.as_strided(a, a.shape, (10, 1, 77, 2)).as_subclass(OnGpu)
+    assert not a.is_contiguous() and a.stride() != b.stride()
+    lst = z.TensorList(grad=[a], master=[b])
+    lst.set_grad([b])
+    with pytest.raises(ValueError, match="differ in order"):
+        lst.set_grad([on_gpu(4, 2, 1, 5)])
+
+
 # ------------------------------------------------------------------------------------------
 # the 8-bit form on the host
 # ------------------------------------------------------------------------------------------

@@ -330,6 +330,11 @@ def _dtype_codes() -> dict:
     return _CODES
 
 
+def _order(t) -> tuple:
+    """Where a tensor's elements lie: a dimension of one element has no say in it."""
+    return t.shape, [s for n, s in zip(t.shape, t.stride()) if n > 1]
+
+
 class TensorList:
     """A list of tensors for the zero_tensors_* calls: the C array of zero_tensor_t, built
     once and used for as long as the tensors stay where they are.
@@ -414,7 +419,7 @@ class TensorList:
                 raise ValueError(f"{name}[{i}] is not contiguous, nor dense in another order")
             n *= size
         for k, xs in self.tensors.items():
-            if k != "exps" and (name == "exps" or xs[i].shape != t.shape or xs[i].stride() != t.stride()):
+            if k != "exps" and (name == "exps" or _order(xs[i]) != _order(t)):
                 raise ValueError(f"{name}[{i}] and {k}[{i}] differ in order")
 
     def set_grad(self, grad: Sequence) -> None:
