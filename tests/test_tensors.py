@@ -217,6 +217,29 @@ def test_dimensions_of_one_element_do_not_count_as_an_order():
         lst.set_grad([on_gpu(4, 2, 1, 5)])
 
 
+@pytest.mark.parametrize("call", ["zero_tensors_state8_read", "zero_tensors_state8_write"])
+@pytest.mark.parametrize("order,other", [("contiguous", "channels last"), ("channels last", "contiguous"),
+                                         ("channels last", "flat")])
+def test_codec_refuses_lists_in_different_orders(monkeypatch, call, order, other):
+    """The two lists of a state8 call lie alike, tensor by tensor; nothing reaches the library
+    otherwise."""
+    calls = []
+    monkeypatch.setattr(z, "_lib", lambda: type("L", (), {call: staticmethod(lambda *a: calls.append(a) or 0)}))
+    def flat(kind, dtype):
+        return on_gpu(120, dtype=dtype) if kind == "flat" else weight(kind, dtype)
+
+    def lists(a, b):
+        code = dict(m=[on_gpu(7, dtype=torch.uint8), flat(a, torch.uint8)], exps=[on_gpu(2, dtype=torch.uint8)] * 2)
+        return (z.TensorList(v=code["m"], **code), z.TensorList(**{k: [on_gpu(7), flat(b, torch.float32)] for k in "mv"}))
+
+    for a, b in ((order, other), (other, order)):
+        with pytest.raises(ValueError, match="differ in order"):
+            getattr(z, call)(*lists(a, b), stream=0)
+    assert not calls
+    getattr(z, call)(*lists(order, order), stream=0)
+    assert len(calls) == 1
+
+
 # ------------------------------------------------------------------------------------------
 # the 8-bit form on the host
 # ------------------------------------------------------------------------------------------

@@ -458,9 +458,13 @@ def _list_stream(tensors: TensorList, stream) -> int | None:
     return _TORCH_C._cuda_getCurrentRawStream(current)
 
 
-def _same_length(a: TensorList, b: TensorList) -> int:
+def _alike(a: TensorList, b: TensorList) -> int:
+    """The length of two lists whose states lie alike."""
     if len(a.elems) != len(b.elems):
         raise ValueError(f"lists of {len(a)} and {len(b)} tensors")
+    for i in a._other_order | b._other_order:
+        if "m" in a.tensors and "m" in b.tensors and _order(a.tensors["m"][i]) != _order(b.tensors["m"][i]):
+            raise ValueError(f"the lists' m[{i}] differ in order")
     return len(a.elems)
 
 
@@ -500,16 +504,18 @@ def zero_tensors_adamw8(tensors: TensorList, hp: HParams, seed: int, st, stream=
 
 
 def zero_tensors_state8_read(source: TensorList, to: TensorList, stream=None) -> None:
-    """The values of source's 8-bit states into to's fp32 or bf16 m and v."""
-    status = _lib().zero_tensors_state8_read(source.array, to.array, _same_length(source, to),
+    """The values of source's 8-bit states into to's fp32 or bf16 m and v, which lie in the
+    same order."""
+    status = _lib().zero_tensors_state8_read(source.array, to.array, _alike(source, to),
                                              _list_stream(source, stream))
     if status:
         _check("zero_tensors_state8_read", status)
 
 
 def zero_tensors_state8_write(to: TensorList, source: TensorList, stream=None) -> None:
-    """source's fp32 m and v into to's 8-bit states, to the nearest code."""
-    status = _lib().zero_tensors_state8_write(to.array, source.array, _same_length(to, source),
+    """source's fp32 m and v into to's 8-bit states, to the nearest code; both lie in the same
+    order."""
+    status = _lib().zero_tensors_state8_write(to.array, source.array, _alike(to, source),
                                               _list_stream(to, stream))
     if status:
         _check("zero_tensors_state8_write", status)
