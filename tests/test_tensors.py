@@ -240,6 +240,21 @@ def test_codec_refuses_lists_in_different_orders(monkeypatch, call, order, other
     assert len(calls) == 1
 
 
+def test_codec_refuses_lists_of_two_devices(monkeypatch):
+    class Second(OnGpu):
+        def get_device(self):
+            return 1
+
+    calls = []
+    monkeypatch.setattr(z, "_lib", lambda: type("L", (), {"zero_tensors_state8_read": staticmethod(lambda *a: calls.append(a) or 0)}))
+    code = [on_gpu(7, dtype=torch.uint8)]
+    source = z.TensorList(m=code, v=code, exps=[on_gpu(2, dtype=torch.uint8)])
+    there = [torch.zeros(7).as_subclass(Second)]
+    with pytest.raises(ValueError, match="devices"):
+        z.zero_tensors_state8_read(source, z.TensorList(m=there, v=there), stream=0)
+    assert not calls
+
+
 # ------------------------------------------------------------------------------------------
 # the 8-bit form on the host
 # ------------------------------------------------------------------------------------------

@@ -462,6 +462,8 @@ def _alike(a: TensorList, b: TensorList) -> int:
     """The length of two lists whose states lie alike."""
     if len(a.elems) != len(b.elems):
         raise ValueError(f"lists of {len(a)} and {len(b)} tensors")
+    if a.device != b.device:
+        raise ValueError(f"lists of devices {a.device} and {b.device}")
     for i in a._other_order | b._other_order:
         if "m" in a.tensors and "m" in b.tensors and _order(a.tensors["m"][i]) != _order(b.tensors["m"][i]):
             raise ValueError(f"the lists' m[{i}] differ in order")
