@@ -255,6 +255,31 @@ def test_codec_refuses_lists_of_two_devices(monkeypatch):
     assert not calls
 
 
+@pytest.mark.parametrize("n", [0, 1, 40, 999, 1000, 2500])
+def test_a_workspace_that_is_too_small_is_refused(lib, monkeypatch, n):
+    """Before the library is called: the norm's kernels write the workspace without knowing
+    its size, which grows with the list."""
+    calls = []
+
+    class Library:
+        zero_tensors_grad_norm = staticmethod(lambda *a: calls.append(a) or 0)
+
+        def __getattr__(self, name):
+            return getattr(lib, name)
+
+    monkeypatch.setattr(z, "_lib", lambda: Library())
+    tensors, hp, st = z.TensorList(grad=[on_gpu(3)] * n), z.hparams(), on_gpu(128, dtype=torch.uint8)
+    need = z.zero_tensors_workspace_bytes(n)
+    for small in (on_gpu(need - 1, dtype=torch.uint8), on_gpu(need // 8 - 1, dtype=torch.float64),
+                  on_gpu(0, dtype=torch.uint8)):
+        with pytest.raises(z.ZeroError) as e:
+            z.zero_tensors_grad_norm(tensors, hp, small, st, stream=0)
+        assert e.value.status == z.ZERO_ENOMEM and not calls
+    for enough in (on_gpu(need, dtype=torch.uint8), on_gpu(need // 8, dtype=torch.float64), A):
+        z.zero_tensors_grad_norm(tensors, hp, enough, st, stream=0)
+    assert len(calls) == 3
+
+
 # ------------------------------------------------------------------------------------------
 # the 8-bit form on the host
 # ------------------------------------------------------------------------------------------

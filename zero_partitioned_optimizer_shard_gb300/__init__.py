@@ -363,6 +363,7 @@ class TensorList:
         first = next(iter(self.tensors.values()))
         self.elems = [t.numel() for t in first]
         self.device = first[0].get_device() if first else -1
+        self._work_bytes = None    # zero_tensors_workspace_bytes, once a norm needs it
         self._other_order = set()  # where the arrays besides the gradient are not contiguous
         n = len(first)
         for k, x in self.tensors.items():
@@ -482,7 +483,14 @@ def zero_tensors_state_init(n_ranks: int, loss_scale: float, dynamic: bool, grow
 
 
 def zero_tensors_grad_norm(tensors: TensorList, hp: HParams, workspace, st, stream=None) -> None:
-    """Norm, clip coefficient, skip decision and the step's scalars over the list's gradients."""
+    """Norm, clip coefficient, skip decision and the step's scalars over the list's gradients.
+    workspace: of zero_tensors_workspace_bytes(len(tensors)) bytes; a tensor that is smaller is
+    refused (ZERO_ENOMEM), the size behind a plain address is the caller's word."""
+    need = tensors._work_bytes
+    if need is None:
+        need = tensors._work_bytes = zero_tensors_workspace_bytes(len(tensors.elems))
+    if getattr(workspace, "nbytes", need) < need:
+        raise ZeroError("zero_tensors_grad_norm", ZERO_ENOMEM)
     status = _lib().zero_tensors_grad_norm(tensors.array, len(tensors.elems), C.byref(hp), _ptr(workspace),
                                            _ptr(st), _list_stream(tensors, stream))
     if status:
