@@ -280,6 +280,24 @@ def test_a_workspace_that_is_too_small_is_refused(lib, monkeypatch, n):
     assert len(calls) == 3
 
 
+@pytest.mark.parametrize("call", ["zero_tensors_adamw", "zero_tensors_adamw8"])
+def test_a_list_without_a_decay_takes_the_hyperparameters(monkeypatch, call):
+    """A list that names no weight decay trains with that of the call's hyperparameters, and
+    follows it; a list that names one, zero among them, keeps its own."""
+    seen = []
+    monkeypatch.setattr(z, "_lib", lambda: type("L", (), {call: staticmethod(
+        lambda array, n, *a: seen.append([array[i].weight_decay for i in range(n)]) or 0)}))
+    arrays = dict(master=[on_gpu(3), on_gpu(4)])
+    plain, zero, own = z.TensorList(**arrays), z.TensorList(weight_decay=0.0, **arrays), z.TensorList(weight_decay=[0.5, 0.0], **arrays)
+    args = (7,) if call.endswith("8") else ()
+    want = []
+    for decay in (0.125, 0.125, 0.25, 0.0):
+        for lst, w in ((plain, [decay] * 2), (zero, [0.0] * 2), (own, [0.5, 0.0])):
+            getattr(z, call)(lst, z.hparams(weight_decay=decay), *args, A, stream=0)
+            want.append(w)
+    assert seen == want
+
+
 # ------------------------------------------------------------------------------------------
 # the 8-bit form on the host
 # ------------------------------------------------------------------------------------------

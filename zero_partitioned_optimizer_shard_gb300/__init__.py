@@ -342,18 +342,19 @@ class TensorList:
     Every argument is a sequence with one entry per tensor, or None where no call on this
     list needs it; all are CUDA tensors of one device.  A tensor's arrays are contiguous, or
     dense in one and the same other order (channels last, a transposed weight).  grad: fp16,
-    bf16 or fp32; master: fp32; m, v: fp32, or uint8 codes with exps, uint8 of 2*ceil(elems/256) (bf16 m
-    and v only as a target of zero_tensors_state8_read); params: bf16 or fp16, or 16-bit
-    integers, whose type is then the hyperparameters'.  lr_scale, weight_decay: one number,
-    or one per tensor.  The list keeps its tensors alive; set_grad() takes gradients that
-    have moved.  The calls write the tensors in place, past autograd."""
+    bf16 or fp32; master: fp32; m, v: fp32, or uint8 codes with exps, uint8 of
+    2*ceil(elems/256) (bf16 m and v only as a target of zero_tensors_state8_read); params:
+    bf16 or fp16, or 16-bit integers, whose type is then the hyperparameters'.  lr_scale,
+    weight_decay: one number, or one per tensor; without a weight_decay each call takes its
+    hyperparameters'.  The list keeps its tensors alive; set_grad() takes gradients that have
+    moved.  The calls write the tensors in place, past autograd."""
 
     _TYPES = {"grad": (ZERO_F16, ZERO_BF16, ZERO_F32), "master": (ZERO_F32,), "exps": (ZERO_U8,),
               "m": (ZERO_F32, ZERO_BF16, ZERO_U8), "v": (ZERO_F32, ZERO_BF16, ZERO_U8),
               "params": (ZERO_F16, ZERO_BF16, 0)}
 
     def __init__(self, grad=None, master=None, m=None, v=None, exps=None, params=None, lr_scale=1.0,
-                 weight_decay=0.0):
+                 weight_decay=None):
         arrays = {"master": master, "m": m, "v": v, "grad": grad, "params": params, "exps": exps}
         self.tensors = {k: list(x) for k, x in arrays.items() if x is not None}
         if not self.tensors or list(self.tensors) == ["exps"]:
@@ -373,6 +374,8 @@ class TensorList:
         if codes.get("m") != codes.get("v"):
             i = next(i for i, (a, b) in enumerate(zip(codes["m"], codes["v"])) if a != b)
             raise ValueError(f"m[{i}] and v[{i}] differ in type")
+        # the decay that the array holds where it is the hyperparameters', else None
+        self._hp_decay = 0.0 if weight_decay is None else None
         none = [None] * n
         ptr = {k: [t.data_ptr() for t in x] for k, x in self.tensors.items()}
         zeros = [0] * n
@@ -380,11 +383,16 @@ class TensorList:
         for i, row in enumerate(zip(
                 self.elems, *(ptr.get(k, none) for k in ("grad", "master", "m", "v", "exps", "params")),
                 *(codes.get(k, zeros) for k in ("grad", "m", "params")), self._numbers(lr_scale),
-                self._numbers(weight_decay))):
+                self._numbers(0.0 if weight_decay is None else weight_decay))):
             self.array[i] = row
 
     def __len__(self) -> int:
         return len(self.elems)
+
+    def _take_decay(self, decay: float) -> None:
+        self._hp_decay = decay
+        for a in self.array:
+            a.weight_decay = decay
 
     def _numbers(self, x) -> list:
         x = list(x) if hasattr(x, "__len__") else [x] * len(self)
@@ -499,6 +507,8 @@ def zero_tensors_grad_norm(tensors: TensorList, hp: HParams, workspace, st, stre
 
 def zero_tensors_adamw(tensors: TensorList, hp: HParams, st, stream=None) -> None:
     """AdamW over the list, fp32 states."""
+    if tensors._hp_decay is not None and tensors._hp_decay != hp.weight_decay:
+        tensors._take_decay(hp.weight_decay)
     status = _lib().zero_tensors_adamw(tensors.array, len(tensors.elems), C.byref(hp), _ptr(st),
                                        _list_stream(tensors, stream))
     if status:
@@ -507,6 +517,8 @@ def zero_tensors_adamw(tensors: TensorList, hp: HParams, st, stream=None) -> Non
 
 def zero_tensors_adamw8(tensors: TensorList, hp: HParams, seed: int, st, stream=None) -> None:
     """AdamW over the list, 8-bit states; seed: of their stochastic rounding."""
+    if tensors._hp_decay is not None and tensors._hp_decay != hp.weight_decay:
+        tensors._take_decay(hp.weight_decay)
     status = _lib().zero_tensors_adamw8(tensors.array, len(tensors.elems), C.byref(hp), seed, _ptr(st),
                                         _list_stream(tensors, stream))
     if status:
