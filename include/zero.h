@@ -473,6 +473,13 @@ int zero_step_static_workspace(const zero_layout_t* layout, const zero_adamw_hpa
  * One step, on one stream:
  *   1. zero_tensors_grad_norm  over the list (scalars into the step state)
  *   2. zero_tensors_adamw or zero_tensors_adamw8 over the same list
+ * A step state serves one stream at a time: AdamW hands out a long list's work through the
+ * state's internal counters (adamw_next_chunk, adamw_done), although it takes it as const.
+ * Two lists under one state on two streams would each skip part of their elements; give
+ * each a copy of the state (its 128 bytes, taken after the norm).
+ * The norm and the overflow check are those of the list given.  A rank whose list is its own
+ * shard gets its shard's norm: clipping by the norm over all ranks takes the step state of
+ * zero_grad_norm over the partials that the ranks have exchanged.
  * The list is a HOST array that each call reads before it returns; its pointers are DEVICE
  * pointers.  Every array is contiguous and holds `elems` elements at the natural alignment
  * of its element type (ZERO_EALIGN otherwise); tensors whose fp32 arrays are 32-byte, 16-bit

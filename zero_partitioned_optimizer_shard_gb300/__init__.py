@@ -347,7 +347,8 @@ class TensorList:
     bf16 or fp16, or 16-bit integers, whose type is then the hyperparameters'.  lr_scale,
     weight_decay: one number, or one per tensor; without a weight_decay each call takes its
     hyperparameters'.  The list keeps its tensors alive; set_grad() takes gradients that have
-    moved.  The calls write the tensors in place, past autograd."""
+    moved.  The calls write the tensors in place, past autograd, and one step state serves one
+    stream at a time."""
 
     _TYPES = {"grad": (ZERO_F16, ZERO_BF16, ZERO_F32), "master": (ZERO_F32,), "exps": (ZERO_U8,),
               "m": (ZERO_F32, ZERO_BF16, ZERO_U8), "v": (ZERO_F32, ZERO_BF16, ZERO_U8),
@@ -491,7 +492,8 @@ def zero_tensors_state_init(n_ranks: int, loss_scale: float, dynamic: bool, grow
 
 
 def zero_tensors_grad_norm(tensors: TensorList, hp: HParams, workspace, st, stream=None) -> None:
-    """Norm, clip coefficient, skip decision and the step's scalars over the list's gradients.
+    """Norm, clip coefficient, skip decision and the step's scalars over the list's gradients
+    (of this list alone: a rank's shard has its own norm, not the run's).
     workspace: of zero_tensors_workspace_bytes(len(tensors)) bytes; a tensor that is smaller is
     refused (ZERO_ENOMEM), the size behind a plain address is the caller's word."""
     need = tensors._work_bytes
