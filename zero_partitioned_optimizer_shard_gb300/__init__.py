@@ -404,16 +404,17 @@ class TensorList:
     def _check(self, name: str, xs: list) -> list:
         """The tensors' type codes, once every one of them is what the kernels take."""
         known, types, device, codes = _dtype_codes(), self._TYPES[name], self.device, []
+        other = self._other_order if name != "exps" else set()  # exps have an order of their own
         for i, (t, n) in enumerate(zip(xs, self.elems)):
             want = 2 * -(-n // ZERO_STATE8_BLOCK) if name == "exps" else n
             if t.numel() != want:
                 raise ValueError(f"{name}[{i}] has {t.numel()} elements, not {want}")
             if not t.is_cuda or t.get_device() != device:
                 raise ValueError(f"{name}[{i}] is not a CUDA tensor of the list's device")
-            if (i in self._other_order and name != "exps") or not t.is_contiguous():
+            if not t.is_contiguous() or (other and i in other):
                 self._check_order(name, i, t)
                 if name != "grad":
-                    self._other_order.add(i)
+                    other.add(i)
             code = known.get(t.dtype, -1)
             if code not in types:
                 raise ValueError(f"{name}[{i}] has type {t.dtype}")
@@ -474,9 +475,10 @@ def _alike(a: TensorList, b: TensorList) -> int:
         raise ValueError(f"lists of {len(a)} and {len(b)} tensors")
     if a.device != b.device:
         raise ValueError(f"lists of devices {a.device} and {b.device}")
-    for i in a._other_order | b._other_order:
-        if "m" in a.tensors and "m" in b.tensors and _order(a.tensors["m"][i]) != _order(b.tensors["m"][i]):
-            raise ValueError(f"the lists' m[{i}] differ in order")
+    if a._other_order or b._other_order:
+        for i in a._other_order | b._other_order:
+            if "m" in a.tensors and "m" in b.tensors and _order(a.tensors["m"][i]) != _order(b.tensors["m"][i]):
+                raise ValueError(f"the lists' m[{i}] differ in order")
     return len(a.elems)
 
 
