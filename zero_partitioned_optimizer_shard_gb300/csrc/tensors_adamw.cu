@@ -9,11 +9,11 @@
  * Both are bound by HBM: 28 bytes an element with 32-bit states and bf16 gradients, 16 with
  * 8-bit states.  Two forms of each:
  *   direct   a warp per 256-element unit, straight from and to global memory.  For short
- *            lists, where a memory latency or two is all there is: 16,384 elements take 2.7
- *            us (8-bit states 2.4), a million 5.2 (4.2).
+ *            lists, where a memory latency or two is all there is: 16,384 elements take 2.8
+ *            us (8-bit states 2.4), a million 5.1 (4.2).
  *   staged   one block per SM; a producer warp bulk-copies chunks into a ring in shared
  *            memory, consumer warps compute (k_tensors_ring).  For long lists: GPT-2
- *            1.5B's 580 tensors take 6,147 us with 32-bit states (106% of the measured copy
+ *            1.5B's 580 tensors take 6,146 us with 32-bit states (106% of the measured copy
  *            peak; the direct form 6,929) and 3,546 us with 8-bit states (105%; 4,122).
  */
 #include "tensors.cuh"
@@ -41,7 +41,8 @@ __device__ __forceinline__ Scalars step_scalars(const ListArgs<CAP>& a)
  * bit.  ANY: without the slow ways of fp32 division and square root, which are taken for
  * zeros and for operands near fp32's lower end.  That is what the rows of an embedding that
  * saw no token hold: m = v = 0, or an m that has decayed into the subnormals; with half of
- * 400 million elements so, the plain form took 2,665 us in place of 1,579, this one 1,573.
+ * 400 million elements so, the plain form took 2,665 us; this one takes 1,582, as long as
+ * other values do.
  *   sqrt(v)        below 2^-100: sqrt(v * 2^64) * 2^-32, both factors exact and no result
  *                  subnormal; for v = 0 any operand, and 0 put in its place after the division;
  *                  a v < 0 gives NaN either way
@@ -932,11 +933,11 @@ int launch_ring(const ListArgs<CAP>& a, cudaStream_t s)
 
 /* Lists of this many elements, and this many per tensor on average, take the staged kernel.
  * Measured, us a call, direct / staged, 32-bit states (8-bit states):
- *   4 tensors     2^20 elements 5.3 / 8.9 (4.2 / 7.1), 2^22 21.8 / 22.7 (14.8 / 15.1),
- *                 2^23 41.0 / 39.7 (25.9 / 24.7), 2^24 78.7 / 73.0 (51.0 / 43.8)
- *   2^25 elements in tensors of 8,192: 173 / 185 (122 / 151), of 16,384: 172 / 166
- *                 (111 / 109), of 65,536: 159 / 147 (106 / 94)
- *   2^23 elements in tensors of 1,024: 91 / 166 (64 / 182): a short tensor leaves most of a
+ *   4 tensors     2^20 elements 5.1 / 9.1 (4.2 / 7.1), 2^22 21.8 / 23.1 (14.8 / 15.0),
+ *                 2^23 41.2 / 40.4 (25.7 / 25.1), 2^24 79.6 / 73.5 (50.1 / 44.4)
+ *   2^25 elements in tensors of 8,192: 172 / 193 (124 / 152), of 16,384: 169 / 168
+ *                 (110 / 109), of 65,536: 158 / 149 (106 / 92)
+ *   2^23 elements in tensors of 1,024: 89 / 165 (65 / 183): a short tensor leaves most of a
  *                 stage empty */
 constexpr uint64_t kRingElems = 3ull << 21, kRingTensor = 1ull << 15;
 

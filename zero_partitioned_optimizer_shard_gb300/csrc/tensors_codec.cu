@@ -5,9 +5,9 @@
  * A warp per 256-element unit, which is a block of the 8-bit form: 8 elements per lane, the
  * block's largest magnitude by one warp reduction.  Bound by HBM: reading moves 1 + 1 bytes
  * in and 2 + 2 (bf16) or 4 + 4 out per element, writing 4 + 4 in and 1 + 1 out.  GPT-2
- * 1.5B's states read as bf16 in 1,459 us (96% of the measured copy peak), 80 million
- * elements written in 121 us (99%).  The staged form of the AdamW kernels gained nothing
- * here (read 1,761 us, written 120): what reading needs is many warps with stores in
+ * 1.5B's states read as bf16 in 1,460 us (96% of the measured copy peak), as fp32 in 2,633
+ * (89%); 80 million elements written in 121 us (99%).  The staged form of the AdamW kernels gained nothing
+ * here (read 1,760 us, written 120): what reading needs is many warps with stores in
  * flight (32 registers, 64 warps per SM; with 40 and 48 warps 1,572 us).
  */
 #include "tensors.cuh"
