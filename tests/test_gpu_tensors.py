@@ -646,6 +646,28 @@ def test_adamw8_with_a_small_eps(eps):
     check8(c, before, STEP, 8)
 
 
+@pytest.mark.parametrize("eps", [1e-8, 1e-20, 1e-29])
+@pytest.mark.parametrize("n", [3000, 6_300_000])
+def test_adamw8_updates_from_gradients_near_the_smallest(n, eps):
+    """Moments of 1e-37 over a small eps: the update is an ordinary number (1e-11 for the
+    smallest eps) and as precise as any other, though step * m is subnormal."""
+    c = Case([n], ("f32",), (0,), "u8")
+    for x in (c.m[0], c.v[0], c.exps[0], c.master[0]):
+        x.zero_()
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    c.grad[0].copy_((1 + 3 * torch.rand(n, device="cuda", generator=gen)) * 1e-36)
+    c.hp = z.hparams(eps=eps)
+    c.set(**STEP)
+    before = c.arrays()
+    z.zero_tensors_adamw8(c.list, c.hp, 5, c.st)
+    c.arena.check()
+    zeros = np.zeros(n, np.float32)
+    _, _, p1, _, _, tp = expected(c, before, 0, c.hp, STEP, zeros, zeros)
+    got = c.arrays()["master"][0]
+    assert np.all(np.abs(got - p1) <= tp), np.max(np.abs(got / p1 - 1))
+    assert np.all(np.abs(p1) > 20 * tp)     # the tolerance says something of the update
+
+
 def test_adamw8_follows_the_32_bit_moments():
     """Over 300 steps with gradients whose size drops by 10 after the first 100, v's mean
     follows the 32-bit run's (rounding to nearest would hold it where it was), and the

@@ -14,7 +14,7 @@
  *   staged   one block per SM; a producer warp bulk-copies chunks into a ring in shared
  *            memory, consumer warps compute (k_tensors_ring).  For long lists: GPT-2
  *            1.5B's 580 tensors take 6,146 us with 32-bit states (106% of the measured copy
- *            peak; the direct form 6,929) and 3,546 us with 8-bit states (105%; 4,122).
+ *            peak; the direct form 6,929) and 3,552 us with 8-bit states (105%; 4,122).
  */
 #include "tensors.cuh"
 
@@ -363,7 +363,8 @@ __device__ __forceinline__ void block8(const float (&x)[8], float (&p)[8], float
                 float v0, v1, d0, d1, y0, y1;
                 f2_split(f2_mul(v2, up), v0, v1);
                 f2_split(f2_fma(f2(sqrt_fast(v0), sqrt_fast(v1)), r2, eps2), d0, d1);
-                const uint64_t q = f2_mul(f2_mul(m2, step2), f2(rcp_fast(d0), rcp_fast(d1)));
+                // the quotient first: step * m would lose bits among the subnormals
+                const uint64_t q = f2_mul(f2_mul(m2, f2(rcp_fast(d0), rcp_fast(d1))), step2);
                 f2_split(f2_fma(f2(p[e], p[e + 1]), decay2, q), p[e], p[e + 1]);
                 f2_split(f2_mul(m2, um), y0, y1);
                 // the bits times 16 put the code into the top byte (m's sign falls out); four
