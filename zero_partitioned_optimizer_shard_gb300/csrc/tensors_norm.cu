@@ -5,8 +5,9 @@
  *
  * norm = sqrt(sum of (x * inv)^2) over every gradient element x.  Nothing but a read of the
  * gradients, 2 or 4 bytes an element, so it is bound by HBM: GPT-2 1.5B's 580 bf16
- * gradients (3.1 GB) take 450 us, 104% of the measured copy peak (6,669 GB/s); a short list
- * takes 7 us, most of it the blocks' arrival and the fp64 chain behind it.  What that took:
+ * gradients (3.1 GB) take 440 to 450 us, by the card, 104-106% of the measured copy peak
+ * (6,669 GB/s); a short list takes 7 us, most of it the blocks' arrival and the fp64 chain
+ * behind it.  What that took:
  *   - each gradient is a run of 16-byte granules at the addresses' own multiples of 16, so
  *     every tensor moves in 128-bit loads whatever its alignment and only a first and a
  *     last granule can be partial (a sum does not care which lane holds what);
