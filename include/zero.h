@@ -33,7 +33,8 @@
  * Conventions for every function below:
  *   - Ownership: the caller allocates and frees every buffer.  No function allocates or
  *     frees device memory; zero_step_host creates and destroys four CUDA events.
- *   - Device pointers must be 16-byte aligned (ZERO_EALIGN otherwise).
+ *   - Device pointers must be 16-byte aligned (ZERO_EALIGN otherwise) where an entry point
+ *     does not say otherwise.
  *   - Asynchrony: device work is enqueued on the caller's stream and the call returns
  *     without waiting, except zero_step_state_read / zero_step_state_write, which wait.
  *   - Errors: arguments are validated on the host before anything is enqueued; a
@@ -580,6 +581,116 @@ int zero_tensors_state8_read(const zero_tensor_t* from, const zero_tensor_t* to,
  * zero_tensors_state8_read gave keeps every value. */
 int zero_tensors_state8_write(const zero_tensor_t* to, const zero_tensor_t* from,
                               uint64_t n_tensors, zero_stream_t stream);
+
+/* -------------------------------------------------------------------------------------
+ * Beside a model's matrix products: layer norm, token embedding and the softmax cross entropy
+ * of a large vocabulary, forward and backward.  These are where the gradients of a model's
+ * vectors and of its embedding and head come from; zero_tensors_grad_norm and
+ * zero_tensors_adamw read them where they are written, and the loss's gradient takes the
+ * step state's loss scale on the device.  [ZW] sec. 2(1): the gradients and the activations
+ * of a training step; [ZO] stage-2 flow: forward, backward, then the step.
+ *
+ * Rows of activations (x, y, dy, dx, out, dout, hidden, dhidden) are `dim` elements each, the
+ * next row `*_stride` elements further (at least dim, at most 2^32; any value for a single
+ * row).  Weights, tables and their gradients are contiguous.  Every pointer has the natural
+ * alignment of its element type (ZERO_EALIGN otherwise) unless said otherwise; rows on 16-byte
+ * boundaries with dim % 8 == 0 move in 128-bit accesses, others element by element.
+ * dtype: ZERO_F16, ZERO_BF16 or (not the head) ZERO_F32.  Sums, statistics and all
+ * arithmetic are fp32; 16-bit outputs are rounded once, to nearest even.
+ * grad_dtype, of weights' gradients: dtype or ZERO_F32.  accumulate = 1 adds to what they hold
+ * (an earlier micro-batch; the other end of a tied embedding), 0 overwrites all of them.
+ * Outputs must not overlap inputs or each other (ZERO_EINVAL).  A workspace needs no
+ * initialisation, keeps nothing from one call for the next, and serves one call at a time:
+ * calls (or captured graphs) that share one run one after another.
+ * No call adds in an order that varies: the same call gives the same bits.
+ * ------------------------------------------------------------------------------------- */
+
+/* Layer norm.  Per row: mean = sum(x)/dim, rstd = 1/sqrt(sum((x - mean)^2)/dim + eps),
+ * y = (x - mean) * rstd * weight + bias.
+ *   rows          at most 2^30
+ *   dim           1 .. 16384
+ *   weight, bias  param_dtype (dtype or ZERO_F32); bias may be NULL (0)
+ *   eps           >= 0
+ *   mean, rstd    fp32 per row, for the backward pass; each may be NULL */
+int zero_layernorm(zero_dtype_t dtype, uint64_t rows, uint32_t dim, const void* x, uint64_t x_stride,
+                   const void* weight, const void* bias, zero_dtype_t param_dtype, float eps, void* y,
+                   uint64_t y_stride, float* mean, float* rstd, zero_stream_t stream);
+
+/* Bytes of zero_layernorm_backward's workspace; 0 for sizes that it refuses. */
+size_t zero_layernorm_workspace_bytes(uint64_t rows, uint32_t dim);
+
+/* Its gradients.  With xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum(g)/dim - xh * sum(g * xh)/dim)
+ *   dweight (+)= sum over rows of dy * xh;  dbias (+)= sum over rows of dy
+ *   mean, rstd      as zero_layernorm wrote them
+ *   dweight, dbias  grad_dtype, dim elements; each may be NULL (not wanted)
+ *   workspace       DEVICE, zero_layernorm_workspace_bytes(rows, dim), 16-byte aligned
+ * Without rows dweight and dbias are 0 (or left as they are, accumulate). */
+int zero_layernorm_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, const void* x, uint64_t x_stride,
+                            const void* weight, zero_dtype_t param_dtype, const float* mean, const float* rstd,
+                            const void* dy, uint64_t dy_stride, void* dx, uint64_t dx_stride, void* dweight,
+                            void* dbias, zero_dtype_t grad_dtype, uint32_t accumulate, void* workspace,
+                            zero_stream_t stream);
+
+/* Embedding: out[t] = scale * table[tokens[t]]; a row of zeros where the id lies outside
+ * [0, vocab) (padding).
+ *   n_tokens     at most 2^28
+ *   dim          1 .. 65536;  vocab  1 .. 2^30
+ *   tokens       int32 or int64 ids (token_bytes 4 or 8), contiguous
+ *   table        dtype, [vocab][dim] */
+int zero_embedding(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim, uint32_t vocab, const void* tokens,
+                   uint32_t token_bytes, const void* table, float scale, void* out, uint64_t out_stride,
+                   zero_stream_t stream);
+
+/* Bytes of zero_embedding_backward's workspace; 0 for sizes that it refuses. */
+size_t zero_embedding_workspace_bytes(uint64_t n_tokens, uint32_t dim, uint32_t vocab);
+
+/* Its gradient: dtable[v] (+)= scale * (sum over the places t with tokens[t] = v of dout[t]),
+ * in the order of the places.  Ids outside [0, vocab) have none.  With accumulate the rows of
+ * tokens that do not occur are not touched; without, they are written 0.
+ *   dtable      grad_dtype, [vocab][dim]
+ *   workspace   DEVICE, zero_embedding_workspace_bytes(...), 16-byte aligned */
+int zero_embedding_backward(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim, uint32_t vocab, const void* tokens,
+                            uint32_t token_bytes, const void* dout, uint64_t dout_stride, float scale, void* dtable,
+                            zero_dtype_t grad_dtype, uint32_t accumulate, void* workspace, zero_stream_t stream);
+
+/* Bytes of the head's workspace, forward or backward; 0 for sizes that they refuse. */
+size_t zero_head_workspace_bytes(uint64_t rows, uint32_t dim, uint32_t vocab);
+
+/* Softmax cross entropy of the logits l[t][v] = sum over k of hidden[t][k] * weight[v][k], which
+ * are never kept:
+ *   lse[t] = log(sum over v of exp(l[t][v]));  loss[t] = lse[t] - l[t][targets[t]]
+ * A token whose target lies outside [0, vocab) (e.g. -100) has none: loss = lse = 0, whatever its
+ * hidden row holds.
+ *   dtype      ZERO_BF16 or ZERO_F16
+ *   rows       at most 2^24;  dim  1 .. 65536;  vocab  1 .. 2^24
+ *   weight     dtype, [vocab][dim]; 16-byte aligned when dim % 8 == 0
+ *   targets    int32 or int64 (target_bytes 4 or 8), contiguous
+ *   loss, lse  fp32 per token
+ *   workspace  DEVICE, zero_head_workspace_bytes(...), 256-byte aligned
+ * Should a bounded wait inside give up, the workspace's second 32-bit word is 1 and the losses
+ * are NaN. */
+int zero_head_loss(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t vocab, const void* hidden,
+                   uint64_t hidden_stride, const void* weight, const void* targets, uint32_t target_bytes, float* loss,
+                   float* lse, void* workspace, zero_stream_t stream);
+
+/* Its gradients.  With f[t] = scale * row_scale[t] * st->loss_scale:
+ *   D[t][v]   = f[t] * (exp(l[t][v] - lse[t]) - (v == targets[t]))
+ *   dhidden   = D . weight  (0 for tokens without a target);  dweight (+)= D^T . hidden
+ * D is formed a piece of the vocabulary at a time and rounded to dtype before the two products
+ * (fp16: scaled by a power of two so that the largest |f| lies just below 2^15; tokens whose
+ * |f| is less than 2^-14 of the largest lose digits).
+ *   lse         as zero_head_loss wrote it
+ *   scale       e.g. 1 / tokens, for the gradient of a mean
+ *   row_scale   fp32 per token (what arrives at loss[t]), or NULL: 1
+ *   st          the step state whose loss_scale the gradients get, or NULL: 1.  A bounded wait
+ *               that gives up puts 1 into its error word (and the workspace's second word)
+ *   dhidden     dtype, or NULL (not wanted);  dweight  grad_dtype, or NULL (not wanted) */
+int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t vocab, const void* hidden,
+                            uint64_t hidden_stride, const void* weight, const void* targets, uint32_t target_bytes,
+                            const float* lse, float scale, const float* row_scale, zero_step_state_t* st,
+                            void* dhidden, uint64_t dhidden_stride, void* dweight, zero_dtype_t grad_dtype,
+                            uint32_t accumulate, void* workspace, zero_stream_t stream);
 
 /* Text for a status code. */
 const char* zero_strerror(int status);

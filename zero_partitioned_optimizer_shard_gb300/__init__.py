@@ -123,6 +123,21 @@ def _lib() -> C.CDLL:
         L.zero_tensors_adamw8.argtypes = [_P, C.c_uint64, C.POINTER(HParams), C.c_uint64, _P, _P]
         L.zero_tensors_state8_read.argtypes = [_P, _P, C.c_uint64, _P]
         L.zero_tensors_state8_write.argtypes = L.zero_tensors_state8_read.argtypes
+        u32, u64, f32 = C.c_uint32, C.c_uint64, C.c_float
+        L.zero_layernorm.argtypes = [C.c_int, u64, u32, _P, u64, _P, _P, C.c_int, f32, _P, u64, _P, _P, _P]
+        L.zero_layernorm_workspace_bytes.argtypes = [u64, u32]
+        L.zero_layernorm_backward.argtypes = [C.c_int, u64, u32, _P, u64, _P, C.c_int, _P, _P, _P, u64, _P, u64,
+                                              _P, _P, C.c_int, u32, _P, _P]
+        L.zero_embedding.argtypes = [C.c_int, u64, u32, u32, _P, u32, _P, f32, _P, u64, _P]
+        L.zero_embedding_workspace_bytes.argtypes = [u64, u32, u32]
+        L.zero_embedding_backward.argtypes = [C.c_int, u64, u32, u32, _P, u32, _P, u64, f32, _P, C.c_int, u32, _P,
+                                              _P]
+        L.zero_head_workspace_bytes.argtypes = [u64, u32, u32]
+        L.zero_head_loss.argtypes = [C.c_int, u64, u32, u32, _P, u64, _P, _P, u32, _P, _P, _P, _P]
+        L.zero_head_loss_backward.argtypes = [C.c_int, u64, u32, u32, _P, u64, _P, _P, u32, _P, f32, _P, _P, _P, u64,
+                                              _P, C.c_int, u32, _P, _P]
+        for name in ("layernorm", "embedding", "head"):
+            getattr(L, f"zero_{name}_workspace_bytes").restype = C.c_size_t
         L.zero_strerror.argtypes = [C.c_int]
         L.zero_strerror.restype = C.c_char_p
         L.zero_last_cuda_error.argtypes = []
@@ -133,7 +148,9 @@ def _lib() -> C.CDLL:
                      "zero_adamw_cast_gather_local", "zero_step_launches",
                      "zero_step_static_workspace", "zero_tensors_state_init",
                      "zero_tensors_grad_norm", "zero_tensors_adamw", "zero_tensors_adamw8",
-                     "zero_tensors_state8_read", "zero_tensors_state8_write"):
+                     "zero_tensors_state8_read", "zero_tensors_state8_write", "zero_layernorm",
+                     "zero_layernorm_backward", "zero_embedding", "zero_embedding_backward", "zero_head_loss",
+                     "zero_head_loss_backward"):
             getattr(L, name).restype = C.c_int
         _L = L
     return _L
@@ -547,6 +564,242 @@ def zero_tensors_state8_write(to: TensorList, source: TensorList, stream=None) -
         _check("zero_tensors_state8_write", status)
 
 
+# --------------------------------------------------------------------------------------
+# beside the matrix products
+# --------------------------------------------------------------------------------------
+_FLOATS = (ZERO_F16, ZERO_BF16, ZERO_F32)
+
+
+class _Operands:
+    """The tensors of one call, checked as they are named: CUDA tensors of one device, which is
+    the current one."""
+
+    def __init__(self):
+        self.device = None
+
+    def take(self, name: str, t, types=None) -> int:
+        """The tensor's type code."""
+        device = t.get_device()
+        if self.device is None:
+            import torch
+            if device < 0:
+                raise ValueError(f"{name} is not a CUDA tensor")
+            current = torch.cuda.current_device()
+            if device != current:
+                raise ValueError(f"{name} is on device {device}, the current device is {current}")
+            self.device = device
+        elif device != self.device:
+            raise ValueError(f"{name} is not on device {self.device}")
+        code = _dtype_codes().get(t.dtype, -1)
+        if types is not None and code not in types:
+            raise ValueError(f"{name} has type {t.dtype}")
+        return code
+
+    def rows(self, name: str, t, dim: int, types) -> tuple:
+        """Type code, number of rows and their stride: the last dimension holds a row, the
+        others count rows at one distance from each other."""
+        code = self.take(name, t, types)
+        if t.dim() == 0 or t.shape[-1] != dim:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not rows of {dim}")
+        if t.is_contiguous():
+            return code, t.numel() // dim, dim
+        n, stride = 1, 0
+        if dim > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}'s rows are not contiguous")
+        for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if size == 1:
+                continue
+            if stride and step != n * stride:
+                raise ValueError(f"{name}'s rows are not at one distance from each other")
+            stride = stride or step
+            n *= size
+        if stride < dim and n > 1:
+            raise ValueError(f"{name}'s rows overlap")
+        return code, n, stride or dim
+
+    def whole(self, name: str, t, shape: tuple, types) -> int:
+        """The type code of a contiguous tensor of the given shape."""
+        code = self.take(name, t, types)
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}" if tuple(t.shape) != shape
+                             else f"{name} is not contiguous")
+        return code
+
+    def per_row(self, name: str, t, n: int) -> None:
+        """fp32, one number per row, in any shape."""
+        self.take(name, t, (ZERO_F32,))
+        if t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} has {t.numel()} elements, not {n}" if t.numel() != n
+                             else f"{name} is not contiguous")
+
+    def ids(self, name: str, t, n: int | None = None) -> tuple:
+        """How many ids, and their bytes: int32 or int64."""
+        self.take(name, t)
+        size = {"torch.int32": 4, "torch.int64": 8}.get(str(t.dtype))
+        if size is None:
+            raise ValueError(f"{name} has type {t.dtype}, not int32 or int64")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+        return t.numel(), size
+
+    def work(self, fn: str, t, need: int) -> int:
+        """A workspace's address: a tensor that is smaller than needed is refused, the size
+        behind a plain address is the caller's word."""
+        if not isinstance(t, int):
+            self.take("workspace", t)
+            if not t.is_contiguous():
+                raise ValueError("workspace is not contiguous")
+            if t.nbytes < need:
+                raise ZeroError(fn, ZERO_ENOMEM)
+        return _ptr(t)
+
+
+def zero_layernorm_workspace_bytes(rows: int, dim: int) -> int:
+    return _lib().zero_layernorm_workspace_bytes(rows, dim)
+
+
+def zero_layernorm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """y = (x - mean) * rstd * weight + bias over x's last dimension.  x, y: fp16, bf16 or fp32;
+    weight, bias (or None): x's type or fp32; mean, rstd: fp32 per row, kept for the backward
+    pass, or None."""
+    o, dim = _Operands(), weight.numel()
+    code, n, xs = o.rows("x", x, dim, _FLOATS)
+    param = o.whole("weight", weight, (dim,), (code, ZERO_F32))
+    if bias is not None:
+        o.whole("bias", bias, (dim,), (param,))
+    _, ny, ys = o.rows("y", y, dim, (code,))
+    if ny != n:
+        raise ValueError(f"x has {n} rows, y {ny}")
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            o.per_row(name, t, n)
+    _check("zero_layernorm", _lib().zero_layernorm(
+        code, n, dim, _ptr(x), xs, _ptr(weight), _ptr(bias), param, eps, _ptr(y), ys, _ptr(mean), _ptr(rstd),
+        _stream(stream)))
+
+
+def zero_layernorm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, workspace, accumulate: bool = False,
+                            stream=None) -> None:
+    """The gradients of zero_layernorm.  dy, dx: x's type; dweight, dbias: x's type or fp32, either
+    may be None; accumulate: they are added to.  workspace: of
+    zero_layernorm_workspace_bytes(rows, dim) bytes."""
+    o, dim = _Operands(), weight.numel()
+    code, n, xs = o.rows("x", x, dim, _FLOATS)
+    param = o.whole("weight", weight, (dim,), (code, ZERO_F32))
+    _, nd, ds = o.rows("dy", dy, dim, (code,))
+    _, ng, gs = o.rows("dx", dx, dim, (code,))
+    if nd != n or ng != n:
+        raise ValueError(f"x has {n} rows, dy {nd}, dx {ng}")
+    o.per_row("mean", mean, n)
+    o.per_row("rstd", rstd, n)
+    grad = code
+    if dweight is not None:
+        grad = o.whole("dweight", dweight, (dim,), (code, ZERO_F32))
+    if dbias is not None:
+        grad = o.whole("dbias", dbias, (dim,), (code, ZERO_F32) if dweight is None else (grad,))
+    f, fn = _lib().zero_layernorm_backward, "zero_layernorm_backward"
+    _check(fn, f(code, n, dim, _ptr(x), xs, _ptr(weight), param, _ptr(mean), _ptr(rstd), _ptr(dy), ds, _ptr(dx), gs,
+                 _ptr(dweight), _ptr(dbias), grad, int(bool(accumulate)),
+                 o.work(fn, workspace, zero_layernorm_workspace_bytes(n, dim)), _stream(stream)))
+
+
+def zero_embedding_workspace_bytes(n_tokens: int, dim: int, vocab: int) -> int:
+    return _lib().zero_embedding_workspace_bytes(n_tokens, dim, vocab)
+
+
+def zero_embedding(tokens, table, out, scale: float = 1.0, stream=None) -> None:
+    """out[t] = scale * table[tokens[t]], zeros for ids outside the table.  tokens: int32 or int64;
+    table [vocab, dim] and out [..., dim]: fp16, bf16 or fp32, alike."""
+    o = _Operands()
+    n, size = o.ids("tokens", tokens)
+    if table.dim() != 2:
+        raise ValueError(f"table has shape {tuple(table.shape)}")
+    vocab, dim = table.shape
+    code = o.whole("table", table, (vocab, dim), _FLOATS)
+    _, no, stride = o.rows("out", out, dim, (code,))
+    if no != n:
+        raise ValueError(f"{n} tokens, out has {no} rows")
+    _check("zero_embedding", _lib().zero_embedding(code, n, dim, vocab, _ptr(tokens), size, _ptr(table), scale, _ptr(out),
+                                                   stride, _stream(stream)))
+
+
+def zero_embedding_backward(tokens, dout, dtable, workspace, scale: float = 1.0, accumulate: bool = False,
+                            stream=None) -> None:
+    """The table's gradient: each row the sum of dout over its tokens' places, times scale.
+    dtable: dout's type or fp32; accumulate: it is added to (rows without a token are not
+    touched), else all of it is written.  workspace: of
+    zero_embedding_workspace_bytes(n_tokens, dim, vocab) bytes."""
+    o = _Operands()
+    n, size = o.ids("tokens", tokens)
+    if dtable.dim() != 2:
+        raise ValueError(f"dtable has shape {tuple(dtable.shape)}")
+    vocab, dim = dtable.shape
+    code, nd, stride = o.rows("dout", dout, dim, _FLOATS)
+    if nd != n:
+        raise ValueError(f"{n} tokens, dout has {nd} rows")
+    grad = o.whole("dtable", dtable, (vocab, dim), (code, ZERO_F32))
+    f, fn = _lib().zero_embedding_backward, "zero_embedding_backward"
+    _check(fn, f(code, n, dim, vocab, _ptr(tokens), size, _ptr(dout), stride, scale, _ptr(dtable), grad,
+                 int(bool(accumulate)), o.work(fn, workspace, zero_embedding_workspace_bytes(n, dim, vocab)),
+                 _stream(stream)))
+
+
+def zero_head_workspace_bytes(rows: int, dim: int, vocab: int) -> int:
+    return _lib().zero_head_workspace_bytes(rows, dim, vocab)
+
+
+def _head(o: _Operands, hidden, weight, targets) -> tuple:
+    """What both of the head's calls check: (type code, rows, dim, vocab), row stride, bytes per
+    target."""
+    if weight.dim() != 2:
+        raise ValueError(f"weight has shape {tuple(weight.shape)}")
+    vocab, dim = weight.shape
+    code, n, stride = o.rows("hidden", hidden, dim, (ZERO_F16, ZERO_BF16))
+    o.whole("weight", weight, (vocab, dim), (code,))
+    return (code, n, dim, vocab), stride, o.ids("targets", targets, n)[1]
+
+
+def zero_head_loss(hidden, weight, targets, loss, lse, workspace, stream=None) -> None:
+    """The cross entropy of every token and its logits' log-sum-exp, from hidden [..., dim] and
+    weight [vocab, dim] (fp16 or bf16); the logits are never kept.  Tokens whose target lies outside
+    [0, vocab) get 0.  workspace: of zero_head_workspace_bytes(rows, dim, vocab) bytes."""
+    o, fn = _Operands(), "zero_head_loss"
+    sizes, stride, width = _head(o, hidden, weight, targets)
+    o.per_row("loss", loss, sizes[1])
+    o.per_row("lse", lse, sizes[1])
+    _check(fn, _lib().zero_head_loss(*sizes, _ptr(hidden), stride, _ptr(weight), _ptr(targets), width, _ptr(loss),
+                                     _ptr(lse), o.work(fn, workspace, zero_head_workspace_bytes(*sizes[1:])),
+                                     _stream(stream)))
+
+
+def zero_head_loss_backward(hidden, weight, targets, lse, dhidden, dweight, workspace, scale: float = 1.0,
+                            row_scale=None, st=None, accumulate: bool = False, stream=None) -> None:
+    """The gradients of sum over tokens of scale * row_scale * loss, times the loss scale that the
+    step state st holds (None: 1).  dhidden: hidden's type, or None; dweight: that or fp32, or
+    None; accumulate: dweight is added to."""
+    o, fn = _Operands(), "zero_head_loss_backward"
+    sizes, stride, width = _head(o, hidden, weight, targets)
+    code, n, dim, vocab = sizes
+    o.per_row("lse", lse, n)
+    if row_scale is not None:
+        o.per_row("row_scale", row_scale, n)
+    hs, grad = dim, code
+    if dhidden is not None:
+        _, nh, hs = o.rows("dhidden", dhidden, dim, (code,))
+        if nh != n:
+            raise ValueError(f"hidden has {n} rows, dhidden {nh}")
+    if dweight is not None:
+        grad = o.whole("dweight", dweight, (vocab, dim), (code, ZERO_F32))
+    if st is not None and not isinstance(st, int):
+        o.take("st", st)
+    f = _lib().zero_head_loss_backward
+    _check(fn, f(*sizes, _ptr(hidden), stride, _ptr(weight), _ptr(targets), width, _ptr(lse), scale, _ptr(row_scale),
+                 _ptr(st), _ptr(dhidden), hs, _ptr(dweight), grad, int(bool(accumulate)),
+                 o.work(fn, workspace, zero_head_workspace_bytes(*sizes[1:])), _stream(stream)))
+
+
 __all__ = [
     "Layout", "HParams", "StepState", "ZeroError", "hparams", "lib", "STATE_BYTES",
     "ZERO_F16", "ZERO_BF16", "Segment", "zero_partition", "zero_segment_map", "zero_workspace_bytes", "zero_step_state_init",
@@ -557,4 +810,7 @@ __all__ = [
     "ZERO_F32", "ZERO_U8", "ZERO_STATE8_BLOCK", "Tensor", "TensorList", "zero_tensors_workspace_bytes",
     "zero_tensors_state_init", "zero_tensors_grad_norm", "zero_tensors_adamw", "zero_tensors_adamw8",
     "zero_tensors_state8_read", "zero_tensors_state8_write",
+    "zero_layernorm", "zero_layernorm_backward", "zero_layernorm_workspace_bytes", "zero_embedding",
+    "zero_embedding_backward", "zero_embedding_workspace_bytes", "zero_head_loss", "zero_head_loss_backward",
+    "zero_head_workspace_bytes",
 ]

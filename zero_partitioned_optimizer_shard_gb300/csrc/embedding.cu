@@ -1,0 +1,573 @@
+/*
+ * embedding.cu -- rows of a table by token id, with a scale, and the table's gradient summed
+ * over the tokens in a fixed order.
+ *
+ * Forward: out[t] = scale * table[token[t]].
+ * Backward: dtable[v] (+)= scale * (sum over the places t with token[t] = v, ascending, of
+ * dout[t]).  The places are sorted by token (stable), cut into chunks of a fixed number of
+ * sorted places, and each chunk's tokens are summed in fp32 by one block; a token whose
+ * places lie in several chunks leaves one partial sum per chunk, which a second kernel adds
+ * in the order of the chunks.  No atomics on values: the same call gives the same bits.
+ * Ids outside [0, vocab) sort behind all others and are dropped.
+ */
+#include "rows.cuh"
+
+namespace zero {
+namespace {
+
+constexpr uint32_t kMaxDim = 65536;
+constexpr uint32_t kPlaces = 16;      // sorted places per chunk
+constexpr uint32_t kSortThreads = 1024;
+constexpr uint32_t kItems = 8;        // per thread and tile of the sort
+constexpr uint32_t kTile = kSortThreads * kItems;
+constexpr uint32_t kBins = 256;       // 8 bits of the key per pass
+constexpr uint32_t kSortWarps = kSortThreads / 32;
+
+struct Tokens {
+    const void* p;
+    uint32_t wide;  // 64-bit ids
+    uint32_t vocab;
+
+    /* The id at place t, or vocab where there is none. */
+    __device__ __forceinline__ uint32_t at(uint32_t t) const
+    {
+        if (wide) {
+            const uint64_t v = (uint64_t) * (static_cast<const volatile long long*>(p) + t);
+            return v < vocab ? (uint32_t)v : vocab;
+        }
+        const uint32_t v = (uint32_t) * (static_cast<const volatile int*>(p) + t);
+        return v < vocab ? v : vocab;
+    }
+};
+
+/* ------------------------------------------------------------------------------------ */
+/* forward                                                                                */
+/* ------------------------------------------------------------------------------------ */
+struct LookupArgs {
+    Tokens tokens;
+    const void* table;
+    void* out;
+    uint64_t out_stride;
+    uint32_t n, d, pieces;  // pieces of a row: 32 chunks of 8 elements, a warp's
+    float scale;
+};
+
+/* A warp takes a piece of a row; W pieces in flight at a time. */
+template <zero_dtype_t DT, bool VEC>
+__global__ void __launch_bounds__(256) k_embedding(const LookupArgs a)
+{
+    using T = typename Elem<DT>::T;
+    constexpr int W = 4;
+    grid_dependency_wait();
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t total = (uint64_t)a.n * a.pieces;
+    const uint64_t first = ((uint64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5)) * W;
+    uint32_t row[W], at[W], id[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const uint64_t u = first + i;
+        row[i] = (uint32_t)(u / a.pieces);
+        at[i] = (uint32_t)(u - (uint64_t)row[i] * a.pieces);
+        id[i] = u < total ? a.tokens.at(row[i]) : 0xffffffffu;
+    }
+    typename Elem<DT>::Raw x[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        x[i] = load_chunk<DT, VEC>(static_cast<const T*>(a.table) + (uint64_t)id[i] * a.d,
+                                   id[i] < a.tokens.vocab ? a.d : 0, at[i], lane, 32);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        if (id[i] == 0xffffffffu)
+            return;
+        float v[8];
+        widen<DT>(x[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // rows without a token: 0, whatever the scale
+            v[j] = id[i] < a.tokens.vocab ? __fmul_rn(v[j], a.scale) : 0.0f;
+        store_chunk<DT, VEC>(static_cast<T*>(a.out) + row[i] * a.out_stride, a.d, at[i], lane, 32, v);
+    }
+}
+
+/* ------------------------------------------------------------------------------------ */
+/* the sort: least significant digit first, 8 bits a pass, stable                         */
+/* ------------------------------------------------------------------------------------ */
+struct RankSmem {
+    uint32_t of_warp[kSortWarps][kBins];  // counts, then offsets, of each warp's keys
+    uint32_t base[kBins];                 // keys of the tile below each digit
+    uint32_t warp_total[8];
+};
+
+/* Each thread's kItems keys (a warp's are 32 * kItems neighbours, taken 32 at a time) get
+ * their rank among the tile's keys of the same digit, in the keys' order; base[] becomes the
+ * number of the tile's keys with a smaller digit and count the tile's keys of digit
+ * threadIdx.x. */
+__device__ __forceinline__ void rank_tile(RankSmem& sm, const uint32_t (&key)[kItems], uint32_t shift,
+                                          uint32_t (&rank)[kItems], uint32_t& count)
+{
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (uint32_t b = lane; b < kBins; b += 32)
+        sm.of_warp[warp][b] = 0;
+    __syncwarp();
+#pragma unroll
+    for (uint32_t i = 0; i < kItems; ++i) {
+        const uint32_t digit = key[i] >> shift & (kBins - 1);
+        const uint32_t peers = __match_any_sync(0xffffffffu, digit);
+        const uint32_t below = __popc(peers & ((1u << lane) - 1));
+        const uint32_t before = sm.of_warp[warp][digit];
+        __syncwarp();
+        if (below == 0)
+            sm.of_warp[warp][digit] = before + __popc(peers);
+        __syncwarp();
+        rank[i] = before + below;
+    }
+    __syncthreads();
+    count = 0;
+    if (threadIdx.x < kBins) {
+#pragma unroll 8
+        for (uint32_t w = 0; w < kSortWarps; ++w) {
+            const uint32_t c = sm.of_warp[w][threadIdx.x];
+            sm.of_warp[w][threadIdx.x] = count;
+            count += c;
+        }
+        uint32_t sum = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane >= (uint32_t)o ? up : 0;
+        }
+        if (lane == 31)
+            sm.warp_total[warp] = sum;
+        sm.base[threadIdx.x] = sum - count;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBins) {
+        uint32_t more = 0;
+        for (uint32_t w = 0; w < warp; ++w)
+            more += sm.warp_total[w];
+        sm.base[threadIdx.x] += more;
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < kItems; ++i)
+        rank[i] += sm.of_warp[warp][key[i] >> shift & (kBins - 1)];
+}
+
+/* The place in its tile of item i of the calling thread. */
+__device__ __forceinline__ uint32_t item_at(uint32_t i)
+{
+    return (threadIdx.x >> 5) * 32 * kItems + i * 32 + (threadIdx.x & 31);
+}
+
+struct SortArgs {
+    Tokens tokens;
+    uint2* from;       // (token, place), or null: the caller's ids, place = index
+    uint2* to;
+    uint32_t* hist;    // [kBins][tiles]
+    uint32_t n, tiles, shift;
+};
+
+__device__ __forceinline__ uint2 sort_item(const SortArgs& a, uint32_t i)
+{
+    if (i >= a.n)
+        return make_uint2(0xffffffffu, 0);
+    return a.from ? a.from[i] : make_uint2(a.tokens.at(i), i);
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_sort_count(const SortArgs a)
+{
+    __shared__ uint32_t count[kBins];
+    grid_dependency_wait();
+    if (threadIdx.x < kBins)
+        count[threadIdx.x] = 0;
+    __syncthreads();
+    for (uint32_t i = 0; i < kItems; ++i) {
+        const uint32_t at = blockIdx.x * kTile + item_at(i);
+        if (at < a.n)
+            atomicAdd(&count[sort_item(a, at).x >> a.shift & (kBins - 1)], 1u);
+    }
+    __syncthreads();
+    if (threadIdx.x < kBins)
+        a.hist[threadIdx.x * a.tiles + blockIdx.x] = count[threadIdx.x];
+}
+
+/* Exclusive sums of the histogram (digit major), in place, by one block. */
+__global__ void __launch_bounds__(kSortThreads) k_sort_scan(uint32_t* hist, uint32_t n)
+{
+    __shared__ uint32_t total[kSortWarps];
+    grid_dependency_wait();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t carry = 0;
+    for (uint32_t at = 0; at < n; at += kSortThreads) {
+        const uint32_t i = at + threadIdx.x;
+        const uint32_t x = i < n ? hist[i] : 0;
+        uint32_t sum = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane >= (uint32_t)o ? up : 0;
+        }
+        if (lane == 31)
+            total[warp] = sum;
+        __syncthreads();
+        uint32_t more = carry, all = carry;
+        for (uint32_t w = 0; w < kSortWarps; ++w) {
+            more += w < warp ? total[w] : 0;
+            all += total[w];
+        }
+        if (i < n)
+            hist[i] = more + sum - x;
+        carry = all;
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const SortArgs a)
+{
+    extern __shared__ uint4 smem[];
+    RankSmem& sm = *reinterpret_cast<RankSmem*>(smem);
+    grid_dependency_wait();
+    uint32_t key[kItems], place[kItems], rank[kItems], count;
+#pragma unroll
+    for (uint32_t i = 0; i < kItems; ++i) {
+        const uint2 x = sort_item(a, blockIdx.x * kTile + item_at(i));
+        key[i] = x.x;
+        place[i] = x.y;
+    }
+    rank_tile(sm, key, a.shift, rank, count);
+#pragma unroll
+    for (uint32_t i = 0; i < kItems; ++i)
+        if (blockIdx.x * kTile + item_at(i) < a.n)
+            a.to[a.hist[(key[i] >> a.shift & (kBins - 1)) * a.tiles + blockIdx.x] + rank[i]] =
+                make_uint2(key[i], place[i]);
+}
+
+/* ------------------------------------------------------------------------------------ */
+/* backward: the sums                                                                     */
+/* ------------------------------------------------------------------------------------ */
+struct GradArgs {
+    const uint2* sorted;  // (token, place)
+    uint32_t* last;       // [vocab]: the last sorted place of each token that occurs
+    const void* dout;
+    float* head;          // [chunks][d]: sums of the token that continues from an earlier chunk
+    float* tail;          // [chunks][d]: sums of the token that starts here and goes on
+    void* dtable;
+    uint64_t dout_stride;
+    uint32_t n, d, vocab;
+    uint32_t accumulate;
+    float scale;
+};
+
+/* One row's piece of the gradient, with the scale, added to what is there if so asked. */
+template <zero_dtype_t GT, bool VEC>
+__device__ __forceinline__ void put_grad(const GradArgs& a, uint32_t token, uint32_t i, uint32_t k, uint32_t n,
+                                         const float (&s)[8])
+{
+    using G = typename Elem<GT>::T;
+    G* row = static_cast<G*>(a.dtable) + (uint64_t)token * a.d;
+    float v[8];
+    if (a.accumulate)
+        widen<GT>(load_chunk<GT, VEC>(row, a.d, i, k, n), v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = a.accumulate ? __fmaf_rn(s[j], a.scale, v[j]) : __fmul_rn(s[j], a.scale);
+    store_chunk<GT, VEC>(row, a.d, i, k, n, v);
+}
+
+template <zero_dtype_t DT, zero_dtype_t GT, bool VEC>
+__global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
+{
+    using T = typename Elem<DT>::T;
+    __shared__ uint2 item[kPlaces + 2];  // the chunk's, between its neighbours
+    grid_dependency_wait();
+    const uint32_t chunk = blockIdx.x, lo = chunk * kPlaces;
+    const uint32_t len = a.n - lo < kPlaces ? a.n - lo : kPlaces;
+    if (threadIdx.x < kPlaces + 2) {
+        const uint32_t i = lo + threadIdx.x;  // of sorted place i - 1
+        item[threadIdx.x] = i >= 1 && i <= a.n ? a.sorted[i - 1] : make_uint2(0xffffffffu, 0);
+    }
+    __syncthreads();
+    if (blockIdx.y == 0 && threadIdx.x >= 1 && threadIdx.x <= len) {
+        const uint32_t k = threadIdx.x, token = item[k].x;
+        if (token < a.vocab && item[k + 1].x != token)
+            a.last[token] = lo + k - 1;
+    }
+    const uint32_t n = blockDim.x, piece = blockIdx.y, k = threadIdx.x;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    bool from_before = item[0].x == item[1].x;
+    for (uint32_t at = 0; at < len; at += 8) {
+        typename Elem<DT>::Raw x[8];
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q) {
+            const uint2 it = item[1 + (at + q < len ? at + q : 0)];
+            x[q] = load_chunk<DT, VEC>(static_cast<const T*>(a.dout) + it.y * a.dout_stride,
+                                       at + q < len && it.x < a.vocab ? a.d : 0, piece, k, n);
+        }
+#pragma unroll
+        for (uint32_t q = 0; q < 8; ++q) {
+            if (at + q >= len)
+                break;
+            const uint32_t token = item[1 + at + q].x;
+            if (token >= a.vocab)
+                return;  // no token from here on
+            float v[8];
+            widen<DT>(x[q], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s[j] = __fadd_rn(s[j], v[j]);
+            const bool ends = item[2 + at + q].x != token;
+            if (!ends && at + q + 1 < len)
+                continue;
+            if (from_before)
+                store_chunk<ZERO_F32, VEC>(a.head + (uint64_t)chunk * a.d, a.d, piece, k, n, s);
+            else if (ends)
+                put_grad<GT, VEC>(a, token, piece, k, n, s);
+            else
+                store_chunk<ZERO_F32, VEC>(a.tail + (uint64_t)chunk * a.d, a.d, piece, k, n, s);
+            from_before = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s[j] = 0.0f;
+        }
+    }
+}
+
+/* Tokens over several chunks: their partial sums in the order of the chunks.  A block looks
+ * at one chunk's last token; 8 warps sum a run of the partials each, over 32 places of the
+ * row's piece. */
+template <zero_dtype_t GT, bool VEC>
+__global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a)
+{
+    __shared__ float part[8][8][33];
+    grid_dependency_wait();
+    const uint32_t chunk = blockIdx.x, end = (chunk + 1) * kPlaces;
+    if (end >= a.n)
+        return;
+    const uint32_t token = a.sorted[end - 1].x;
+    if (token >= a.vocab || a.sorted[end].x != token)
+        return;
+    if (end > kPlaces && a.sorted[end - kPlaces - 1].x == token)
+        return;  // it does not start here
+    const uint32_t chunks = a.last[token] / kPlaces - chunk;  // with a partial in head[]
+    const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5, piece = blockIdx.y;
+    const uint32_t each = (chunks + 7) / 8, lo = run * each, hi = lo + each < chunks ? lo + each : chunks;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    if (run == 0)
+        widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(a.tail + (uint64_t)chunk * a.d, a.d, piece, lane, 32), s);
+#pragma unroll 4
+    for (uint32_t c = lo; c < hi; ++c) {
+        float v[8];
+        widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(a.head + (uint64_t)(chunk + 1 + c) * a.d, a.d, piece, lane, 32), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s[j] = __fadd_rn(s[j], v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        part[run][j][lane] = s[j];
+    __syncthreads();
+    if (run)
+        return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int r = 1; r < 8; ++r)
+            s[j] = __fadd_rn(s[j], part[r][j][lane]);
+    put_grad<GT, VEC>(a, token, piece, lane, 32, s);
+}
+
+__global__ void __launch_bounds__(512) k_zero_fill(uint4* p, uint64_t n16, uint8_t* tail, uint32_t bytes)
+{
+    grid_dependency_wait();
+    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += (uint64_t)gridDim.x * blockDim.x)
+        p[i] = make_uint4(0, 0, 0, 0);
+    if (blockIdx.x == 0 && threadIdx.x < bytes)
+        tail[threadIdx.x] = 0;
+}
+
+/* ------------------------------------------------------------------------------------ */
+/* host side                                                                              */
+/* ------------------------------------------------------------------------------------ */
+struct Workspace {
+    uint64_t sorted[2], hist, last, head, tail, bytes;
+};
+
+uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
+
+Workspace layout(uint64_t n, uint32_t d, uint32_t vocab)
+{
+    Workspace w;
+    const uint64_t tiles = (n + kTile - 1) / kTile, chunks = (n + kPlaces - 1) / kPlaces;
+    uint64_t at = 0;
+    auto take = [&](uint64_t bytes) {
+        const uint64_t p = at;
+        at += up16(bytes);
+        return p;
+    };
+    w.sorted[0] = take(n * 8);
+    w.sorted[1] = take(n * 8);
+    w.hist = take((uint64_t)kBins * tiles * 4);
+    w.last = take((uint64_t)vocab * 4);
+    w.head = take(chunks * d * 4);
+    w.tail = take(chunks * d * 4);
+    w.bytes = at ? at : 16;
+    return w;
+}
+
+bool sizes_ok(uint64_t n, uint32_t d, uint32_t vocab)
+{
+    return n <= (1ull << 28) && d >= 1 && d <= kMaxDim && vocab >= 1 && vocab <= (1u << 30);
+}
+
+template <zero_dtype_t DT>
+cudaError_t lookup(const LookupArgs& a, bool vec, cudaStream_t s)
+{
+    const uint64_t warps = ((uint64_t)a.n * a.pieces + 3) / 4;
+    const dim3 grid((unsigned)((warps + 7) / 8));
+    return vec ? launch_pdl(k_embedding<DT, true>, grid, dim3(256), 0, s, a)
+               : launch_pdl(k_embedding<DT, false>, grid, dim3(256), 0, s, a);
+}
+
+template <zero_dtype_t DT, zero_dtype_t GT, bool VEC>
+cudaError_t sums(const GradArgs& a, cudaStream_t s)
+{
+    const uint32_t chunks = (a.n + kPlaces - 1) / kPlaces, eights = (a.d + 7) / 8;
+    const uint32_t threads = eights < 256 ? (eights + 31) / 32 * 32 : 256;
+    cudaError_t e = launch_pdl(k_embedding_sum<DT, GT, VEC>, dim3(chunks, (eights + threads - 1) / threads),
+                               dim3(threads), 0, s, a);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(k_embedding_join<GT, VEC>, dim3(chunks, (eights + 31) / 32), dim3(256), 0, s, a);
+}
+
+template <zero_dtype_t DT, zero_dtype_t GT>
+cudaError_t sums(const GradArgs& a, bool vec, cudaStream_t s)
+{
+    return vec ? sums<DT, GT, true>(a, s) : sums<DT, GT, false>(a, s);
+}
+
+cudaError_t sort_tokens(const Tokens& tokens, uint32_t n, uint2* buf[2], uint32_t* hist, const uint2*& sorted,
+                        cudaStream_t s)
+{
+    uint32_t bits = 1;
+    while (bits < 32 && tokens.vocab >> bits)
+        ++bits;  // of the largest key, vocab itself
+    const uint32_t tiles = (n + kTile - 1) / kTile;
+    cudaError_t e = cudaFuncSetAttribute(k_sort_scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(RankSmem));
+    SortArgs a{tokens, nullptr, buf[0], hist, n, tiles, 0};
+    for (uint32_t turn = 0; a.shift < bits && e == cudaSuccess; a.shift += 8, ++turn) {
+        a.to = buf[turn & 1];
+        e = launch_pdl(k_sort_count, dim3(tiles), dim3(kSortThreads), 0, s, a);
+        if (e == cudaSuccess)
+            e = launch_pdl(k_sort_scan, dim3(1), dim3(kSortThreads), 0, s, hist, tiles * kBins);
+        if (e == cudaSuccess)
+            e = launch_pdl(k_sort_scatter, dim3(tiles), dim3(kSortThreads), sizeof(RankSmem), s, a);
+        a.from = a.to;
+    }
+    sorted = a.from;
+    return e;
+}
+
+cudaError_t zero_fill(void* p, uint64_t bytes, cudaStream_t s)
+{
+    if (!aligned_to(p, 16))
+        return cudaMemsetAsync(p, 0, bytes, s);
+    const uint64_t n16 = bytes / 16;
+    const uint64_t want = (n16 + 511) / 512, cap = (uint64_t)sm_count() * 4;
+    return launch_pdl(k_zero_fill, dim3((unsigned)(want < cap ? (want ? want : 1) : cap)), dim3(512), 0, s,
+                      static_cast<uint4*>(p), n16, static_cast<uint8_t*>(p) + n16 * 16, (uint32_t)(bytes % 16));
+}
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" {
+
+int zero_embedding(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim, uint32_t vocab, const void* tokens,
+                   uint32_t token_bytes, const void* table, float scale, void* out, uint64_t out_stride,
+                   zero_stream_t stream)
+{
+    NvtxRange range("zero_embedding");
+    if (!float_dtype(dtype) || !sizes_ok(n_tokens, dim, vocab) || (token_bytes != 4 && token_bytes != 8) ||
+        !(scale >= -3.0e38f && scale <= 3.0e38f))
+        return ZERO_EINVAL;
+    if (n_tokens == 0)
+        return ZERO_OK;
+    if (!tokens || !table || !out || (n_tokens > 1 && out_stride < dim) || out_stride > (1ull << 32))
+        return ZERO_EINVAL;
+    const size_t e = dtype_size(dtype);
+    if (!aligned_to(tokens, token_bytes) || !aligned_to(table, e) || !aligned_to(out, e))
+        return ZERO_EALIGN;
+    const uint64_t no = span(n_tokens, out_stride, dim, dtype);
+    if (overlap(out, no, table, (uint64_t)vocab * dim * e) || overlap(out, no, tokens, n_tokens * token_bytes))
+        return ZERO_EINVAL;
+    const LookupArgs a{{tokens, token_bytes == 8, vocab}, table, out, out_stride, (uint32_t)n_tokens, dim,
+                       (dim + 255) / 256, scale};
+    const bool vec = rows_vec(table, dim, dim, dtype) && rows_vec(out, out_stride, dim, dtype);
+    return rows_status(dtype == ZERO_BF16  ? lookup<ZERO_BF16>(a, vec, stream)
+                       : dtype == ZERO_F16 ? lookup<ZERO_F16>(a, vec, stream)
+                                           : lookup<ZERO_F32>(a, vec, stream));
+}
+
+size_t zero_embedding_workspace_bytes(uint64_t n_tokens, uint32_t dim, uint32_t vocab)
+{
+    return sizes_ok(n_tokens, dim, vocab) ? (size_t)layout(n_tokens, dim, vocab).bytes : 0;
+}
+
+int zero_embedding_backward(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim, uint32_t vocab, const void* tokens,
+                            uint32_t token_bytes, const void* dout, uint64_t dout_stride, float scale, void* dtable,
+                            zero_dtype_t grad_dtype, uint32_t accumulate, void* workspace, zero_stream_t stream)
+{
+    NvtxRange range("zero_embedding_backward");
+    if (!float_dtype(dtype) || (grad_dtype != dtype && grad_dtype != ZERO_F32) || accumulate > 1 ||
+        !sizes_ok(n_tokens, dim, vocab) || (token_bytes != 4 && token_bytes != 8) ||
+        !(scale >= -3.0e38f && scale <= 3.0e38f) || !dtable || !workspace)
+        return ZERO_EINVAL;
+    if (n_tokens && (!tokens || !dout || (n_tokens > 1 && dout_stride < dim) || dout_stride > (1ull << 32)))
+        return ZERO_EINVAL;
+    if (!aligned_to(tokens, token_bytes) || !aligned_to(dout, dtype_size(dtype)) ||
+        !aligned_to(dtable, dtype_size(grad_dtype)) || !aligned_to(workspace, 16))
+        return ZERO_EALIGN;
+    const Workspace w = layout(n_tokens, dim, vocab);
+    const uint64_t nt = (uint64_t)vocab * dim * dtype_size(grad_dtype), no = span(n_tokens, dout_stride, dim, dtype);
+    if (overlap(dtable, nt, dout, no) || overlap(dtable, nt, tokens, n_tokens * token_bytes) ||
+        overlap(workspace, w.bytes, dout, no) || overlap(workspace, w.bytes, tokens, n_tokens * token_bytes) ||
+        overlap(workspace, w.bytes, dtable, nt))
+        return ZERO_EINVAL;
+    if (!accumulate) {
+        const int rc = rows_status(zero_fill(dtable, nt, stream));
+        if (rc != ZERO_OK)
+            return rc;
+    }
+    if (n_tokens == 0)
+        return ZERO_OK;
+    char* base = static_cast<char*>(workspace);
+    uint2* buf[2] = {reinterpret_cast<uint2*>(base + w.sorted[0]), reinterpret_cast<uint2*>(base + w.sorted[1])};
+    const uint2* sorted = nullptr;
+    int rc = rows_status(sort_tokens({tokens, token_bytes == 8, vocab}, (uint32_t)n_tokens, buf,
+                                     reinterpret_cast<uint32_t*>(base + w.hist), sorted, stream));
+    if (rc != ZERO_OK)
+        return rc;
+    const GradArgs a{sorted,
+                     reinterpret_cast<uint32_t*>(base + w.last),
+                     dout,
+                     reinterpret_cast<float*>(base + w.head),
+                     reinterpret_cast<float*>(base + w.tail),
+                     dtable,
+                     dout_stride,
+                     (uint32_t)n_tokens,
+                     dim,
+                     vocab,
+                     accumulate,
+                     scale};
+    const bool vec = rows_vec(dout, dout_stride, dim, dtype) && rows_vec(dtable, dim, dim, grad_dtype);
+    if (grad_dtype == ZERO_F32)
+        return rows_status(dtype == ZERO_BF16  ? sums<ZERO_BF16, ZERO_F32>(a, vec, stream)
+                           : dtype == ZERO_F16 ? sums<ZERO_F16, ZERO_F32>(a, vec, stream)
+                                               : sums<ZERO_F32, ZERO_F32>(a, vec, stream));
+    return rows_status(dtype == ZERO_BF16 ? sums<ZERO_BF16, ZERO_BF16>(a, vec, stream)
+                                          : sums<ZERO_F16, ZERO_F16>(a, vec, stream));
+}
+
+}  // extern "C"

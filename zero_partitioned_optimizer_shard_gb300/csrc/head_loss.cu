@@ -1,0 +1,1070 @@
+/*
+ * head_loss.cu -- softmax cross entropy of logits = hidden . weight^T over a large vocabulary,
+ * with its gradients; the logits are never kept.
+ *
+ * With l = hidden . weight^T (n tokens by V), f_t = scale * row_scale[t] * loss scale:
+ *   lse_t  = log(sum over v of exp(l_tv)),  loss_t = lse_t - l_t,target
+ *   D_tv   = f_t * (exp(l_tv - lse_t) - [v = target_t])
+ *   dhidden = D . weight,  dweight (+)= D^T . hidden
+ * Forward: one product whose epilogue leaves, per token and tile of 128 logits, their maximum
+ * and the sum of exponentials below it; a second kernel joins them.  Backward: pieces of the
+ * vocabulary.  A piece's logits are formed again, D goes to 16 bits into the workspace, and two
+ * products take it from there: dhidden summed in fp32 over the pieces, dweight's rows of the
+ * piece whole.  One product more than keeping the logits would need, against n * V * 4 bytes.
+ *
+ * Tokens without a target are dropped first: the tokens that have one are listed, and unless
+ * that is all of them their hidden rows are gathered, so such a token costs nothing and
+ * whatever its row holds reaches no sum.
+ *
+ * D's 16 bits: the products take operands of hidden's type.  bf16 has fp32's range; for fp16 D
+ * is scaled by a power of two so that the largest |f_t| lies just below 2^15: softmax values
+ * down to 2^-29 of it stay normal numbers.  Each D is rounded once, relative error 2^-9 (bf16)
+ * or 2^-12, of the size of the one rounding of the 16-bit gradients themselves.
+ */
+#include "tcgen05.cuh"
+
+#include <mutex>
+
+namespace zero {
+namespace {
+
+constexpr uint32_t kTileM = 128, kTileN = 256, kBlockK = 64;
+constexpr uint32_t kRing = 4;
+constexpr uint32_t kStageBytes = (kTileM + kTileN) * kBlockK * 2;
+constexpr uint32_t kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;
+constexpr uint32_t kSmem = kRing * kStageBytes + 1024;  // and to a 1,024-byte boundary
+constexpr uint32_t kSms = 152;  // of a GB300: sizes the workspace and the splits
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+/* Head of the workspace. */
+struct Header {
+    uint32_t valid;  // tokens that have a target
+    uint32_t error;  // 1: a bounded wait gave up
+    float post;      // the gradients' factor beside D (fp16: a power of two; bf16: 1)
+    uint32_t pad[61];
+};
+static_assert(sizeof(Header) == 256, "the workspace's head");
+
+enum Mode { kStats, kD, kDhidden, kDweight };
+
+struct ProductArgs {
+    CUtensorMap hidden;    // the caller's rows, or (where they cannot be used as they lie) the gathered ones
+    CUtensorMap gathered;  // the rows of the tokens that have a target
+    CUtensorMap weight;
+    CUtensorMap d;         // D's piece
+    Header* head;
+    uint32_t* state_error;  // the step state's error word, or null
+    const int* target;      // [valid]
+    const float* factor;    // [valid]
+    const float* lse;       // [valid]
+    float* target_logit;    // [valid]
+    float2* stats;          // [valid][2 * column tiles]
+    uint16_t* dd;           // D: [rows][d_stride]
+    float* sums;            // dhidden: [splits][rows_pad][dim8]; dweight: [splits][piece][dim8]
+    void* dweight;          // one split: written in place
+    uint32_t rows;          // of the call, with or without a target
+    uint32_t rows_pad, dim, dim8, vocab;
+    uint32_t v0, cols;      // the piece: columns [v0, v0 + cols) of the vocabulary
+    uint32_t d_stride;
+    uint32_t tile_n;        // dhidden, dweight: columns of a tile
+    uint32_t splits;        // of the sum over the piece (dhidden) or the tokens (dweight)
+    uint32_t group;         // row tiles that share a run through the columns
+    uint32_t first_piece;   // sums start here
+    uint32_t grad_dtype, accumulate, vec;
+};
+
+struct Tile {
+    uint32_t m, n;      // first row and column
+    uint32_t k0, k1;    // blocks of 64 along the sum
+    uint32_t split, nt;
+};
+
+/* The extents of a launch's tiles, known once the number of tokens with a target is. */
+template <Mode MODE>
+struct Tiles {
+    uint32_t mt, nt, blocks, splits, group, tile_n, total;
+
+    __device__ Tiles(const ProductArgs& a, uint32_t valid)
+    {
+        const uint32_t m = MODE == kDweight ? a.cols : valid;
+        const uint32_t k = MODE == kDweight ? valid : MODE == kDhidden ? a.cols : a.dim;
+        const uint32_t n = MODE == kStats || MODE == kD ? a.cols : a.dim;
+        tile_n = MODE == kStats || MODE == kD ? kTileN : a.tile_n;
+        mt = (m + kTileM - 1) / kTileM;
+        nt = (n + tile_n - 1) / tile_n;
+        blocks = (k + kBlockK - 1) / kBlockK;
+        splits = MODE == kStats || MODE == kD ? 1 : a.splits;
+        group = a.group;
+        total = mt * nt * splits;
+    }
+
+    __device__ __forceinline__ Tile at(uint32_t t) const
+    {
+        Tile r;
+        uint32_t m, n;
+        r.split = t / (mt * nt);
+        t -= r.split * mt * nt;
+        if (MODE == kStats || MODE == kD) {
+            // a group's rows of hidden stay in L2 while the columns pass once
+            const uint32_t g = t / (group * nt), first = g * group, in = mt - first < group ? mt - first : group;
+            t -= g * group * nt;
+            n = t / in;
+            m = first + t - n * in;
+        } else {
+            m = t / nt;  // D's tile is read once for all its columns
+            n = t - m * nt;
+        }
+        r.m = m * kTileM;
+        r.n = n * tile_n;
+        r.nt = n;
+        r.k0 = (uint32_t)((uint64_t)blocks * r.split / splits);
+        r.k1 = (uint32_t)((uint64_t)blocks * (r.split + 1) / splits);
+        return r;
+    }
+};
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));  // within 2 ulp, far below the 16 bits it ends in
+    return y;
+}
+
+struct Shared {
+    uint64_t full[kRing], empty[kRing], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem, gave_up;
+};
+
+/* The part of a tile that one warp of the epilogue has: 32 rows, 128 of the columns (half). */
+struct Part {
+    uint32_t acc;   // tensor memory address
+    uint32_t row;   // this thread's row
+    uint32_t half;
+    bool empty;     // no block along the sum: zeros
+};
+
+__device__ __forceinline__ void load_part(const Part& p, uint32_t c, float (&x)[32])
+{
+    if (p.empty) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            x[j] = 0.0f;
+    } else {
+        tmem_load32(p.acc + c, x);
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ void stats_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid)
+{
+    const int target = p.row < valid ? a.target[p.row] : -1;
+    float top = __int_as_float(0xff800000), sum = 0.0f;
+#pragma unroll 1
+    for (uint32_t c = 0; c < kTileN / 2; c += 32) {
+        const uint32_t col = t.n + p.half * (kTileN / 2) + c;
+        float x[32];
+        load_part(p, c, x);
+        if (col + 32 > a.vocab) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                x[j] = col + j < a.vocab ? x[j] : __int_as_float(0xff800000);
+        }
+        const uint32_t off = (uint32_t)target - col;
+        if (off < 32) {
+            float v = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v = off == (uint32_t)j ? x[j] : v;
+            a.target_logit[p.row] = v;
+        }
+        float m = top;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            m = fmaxf(m, x[j]);
+        // a row of -inf so far: any reference will do, exp gives 0
+        const float ref = m == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(m, kLog2e);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            s[j & 3] = __fadd_rn(s[j & 3], exp2_approx(__fmaf_rn(x[j], kLog2e, -ref)));
+        sum = __fmaf_rn(sum, exp2_approx(__fmaf_rn(top, kLog2e, -ref)),
+                        __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])));
+        top = m;
+    }
+    if (p.row < valid) {
+        const uint32_t tiles = 2 * ((a.cols + kTileN - 1) / kTileN);
+        a.stats[(uint64_t)p.row * tiles + 2 * t.nt + p.half] = make_float2(top, sum);
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ void d_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid)
+{
+    const bool in = p.row < valid;
+    const int target = in ? a.target[p.row] - (int)a.v0 : -1;
+    const float f = in ? a.factor[p.row] : 0.0f;
+    const float lse = in ? __fmul_rn(a.lse[p.row], kLog2e) : 0.0f;
+    uint16_t* out = a.dd + (uint64_t)p.row * a.d_stride;
+#pragma unroll 1
+    for (uint32_t c = 0; c < kTileN / 2; c += 32) {
+        const uint32_t col = t.n + p.half * (kTileN / 2) + c;
+        float x[32];
+        load_part(p, c, x);
+        const uint32_t off = (uint32_t)target - col;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            float e = exp2_approx(__fmaf_rn(x[j], kLog2e, -lse));
+            if (off == (uint32_t)j)
+                e = __fsub_rn(e, 1.0f);
+            x[j] = in && col + j < a.cols ? __fmul_rn(f, e) : 0.0f;
+        }
+        uint4* to = reinterpret_cast<uint4*>(out + col);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            to[q] = make_uint4(pack2<F16>(x[8 * q], x[8 * q + 1]), pack2<F16>(x[8 * q + 2], x[8 * q + 3]),
+                               pack2<F16>(x[8 * q + 4], x[8 * q + 5]), pack2<F16>(x[8 * q + 6], x[8 * q + 7]));
+    }
+}
+
+/* 32 columns of a row of the weight's gradient. */
+template <zero_dtype_t GT>
+__device__ __forceinline__ void put_columns(typename Elem<GT>::T* row, uint32_t col, uint32_t dim, float post,
+                                            bool accumulate, bool vec, const float (&x)[32])
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t c = col + 8 * q;
+        float v[8];
+        if (vec) {
+            if (c >= dim)
+                return;
+            if (accumulate)
+                widen<GT>(load_chunk<GT, true>(row + c, 8, 0, 0, 1), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = accumulate ? __fmaf_rn(x[8 * q + j], post, v[j]) : __fmul_rn(x[8 * q + j], post);
+            store_chunk<GT, true>(row + c, 8, 0, 0, 1, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (c + j < dim) {
+                    const float y = x[8 * q + j];
+                    row[c + j] = from_f32<GT>(accumulate ? __fmaf_rn(y, post, to_f32<GT>(row[c + j])) : __fmul_rn(y, post));
+                }
+            }
+        }
+    }
+}
+
+/* Sums in fp32, or (one split of dweight) the gradient itself. */
+template <Mode MODE, bool F16>
+__device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid)
+{
+    const uint32_t rows = MODE == kDhidden ? valid : a.cols;
+    const bool add = MODE == kDhidden && !a.first_piece;
+    const float post = a.head->post;
+#pragma unroll 1
+    for (uint32_t c = 0; c < kTileN / 2; c += 32) {
+        const uint32_t in = p.half * (kTileN / 2) + c, col = t.n + in;
+        if (in >= a.tile_n)
+            break;  // the same for the whole warp
+        float x[32];
+        load_part(p, c, x);
+        if (p.row >= rows)
+            continue;
+        // tile_n is a multiple of 16: the other half of the 32 may be the next tile's
+        const uint32_t end = t.n + a.tile_n < a.dim ? t.n + a.tile_n : a.dim;
+        if (MODE == kDweight && a.splits == 1) {
+            const uint64_t row = a.v0 + p.row;
+            if (a.grad_dtype == ZERO_F32)
+                put_columns<ZERO_F32>(static_cast<float*>(a.dweight) + row * a.dim, col, end, post, a.accumulate, a.vec, x);
+            else
+                put_columns<F16 ? ZERO_F16 : ZERO_BF16>(static_cast<uint16_t*>(a.dweight) + row * a.dim, col, end, post,
+                                                        a.accumulate, a.vec, x);
+            continue;
+        }
+        const uint32_t height = MODE == kDhidden ? a.rows_pad : a.d_stride;
+        float* to = a.sums + ((uint64_t)t.split * height + p.row) * a.dim8;
+        const uint32_t end8 = t.n + a.tile_n < a.dim8 ? t.n + a.tile_n : a.dim8;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            if (col + 4 * q >= end8)
+                break;
+            float4* at = reinterpret_cast<float4*>(to + col + 4 * q);
+            float4 v = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            if (add) {
+                const float4 o = *at;
+                v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
+            }
+            *at = v;
+        }
+    }
+}
+
+/* One product over all its tiles: a block per SM takes tiles in turn.  Warp 0 copies operands
+ * in, warp 1 issues the matrix instructions (one thread each), warps 4 to 11 take finished
+ * accumulators out while the next tile's are formed in the other half of tensor memory. */
+template <Mode MODE, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_constant__ ProductArgs a)
+{
+    constexpr bool kAmn = MODE == kDweight, kBmn = MODE == kDhidden || MODE == kDweight;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared sh;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t stages = (smem_addr(raw) + 1023) / 1024 * 1024;
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < kRing; ++s) {
+            bar_init(smem_addr(&sh.full[s]), 1);
+            bar_init(smem_addr(&sh.empty[s]), 1);
+        }
+        for (uint32_t b = 0; b < 2; ++b) {
+            bar_init(smem_addr(&sh.acc_full[b]), 1);
+            bar_init(smem_addr(&sh.acc_empty[b]), kEpilogueWarps);
+        }
+        bar_init(smem_addr(&sh.drain), 1);
+        sh.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2)
+        tmem_alloc(smem_addr(&sh.tmem), 512);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile uint32_t* gave_up = &sh.gave_up;
+    grid_dependency_wait();
+    const uint32_t valid = *const_cast<const volatile uint32_t*>(&a.head->valid);
+    const Tiles<MODE> tiles(a, valid);
+
+    if (warp == 0 && lane == 0) {
+        // what earlier kernels wrote through the generic proxy, for the TMA's reads
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        const CUtensorMap* hidden = valid == a.rows ? &a.hidden : &a.gathered;
+        const CUtensorMap* ma = MODE == kStats || MODE == kD ? hidden : &a.d;
+        const CUtensorMap* mb = MODE == kDweight ? hidden : &a.weight;
+        const uint32_t boxes_b = (tiles.tile_n + 63) / 64, bytes = (2 + boxes_b) * kBoxBytes;
+        const uint32_t b0 = MODE == kDweight ? 0 : a.v0;  // weight's rows of the piece
+        uint32_t issued = 0;
+        bool ok = true;
+        for (uint32_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+            const Tile t = tiles.at(i);
+            for (uint32_t k = t.k0; k < t.k1; ++k, ++issued) {
+                const uint32_t s = issued % kRing, turn = issued / kRing;
+                if (turn && !bar_wait(smem_addr(&sh.empty[s]), (turn - 1) & 1, gave_up)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = smem_addr(&sh.full[s]), to = stages + s * kStageBytes, kk = k * kBlockK;
+                bar_expect(bar, bytes);
+                for (uint32_t j = 0; j < 2; ++j) {
+                    const uint32_t r = t.m + 64 * j;
+                    tma_box(to + j * kBoxBytes, ma, (int)(kAmn ? r : kk), (int)(kAmn ? kk : r), bar);
+                }
+                for (uint32_t j = 0; j < boxes_b; ++j) {
+                    const uint32_t r = t.n + 64 * j;
+                    tma_box(to + (2 + j) * kBoxBytes, mb, (int)(kBmn ? r : kk), (int)(kBmn ? b0 + kk : b0 + r), bar);
+                }
+            }
+        }
+        if (!ok) {  // copies still in flight land before the block's shared memory goes
+            uint32_t none = 0;
+            for (uint32_t q = issued > kRing ? issued - kRing : 0; q < issued; ++q)
+                bar_wait(smem_addr(&sh.full[q % kRing]), (q / kRing) & 1, &none);
+        }
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t idesc = instr_desc(F16, kAmn, kBmn, kTileM, tiles.tile_n);
+        uint32_t used = 0, buf = 0;
+        bool ok = true;
+        for (uint32_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+            const Tile t = tiles.at(i);
+            if (t.k0 >= t.k1)
+                continue;
+            const uint32_t b = buf & 1, turn = buf >> 1;
+            if (turn && !bar_wait(smem_addr(&sh.acc_empty[b]), (turn - 1) & 1, gave_up)) {
+                ok = false;
+                break;
+            }
+            tmem_fence_after();
+            for (uint32_t k = t.k0; k < t.k1; ++k, ++used) {
+                const uint32_t s = used % kRing;
+                if (!bar_wait(smem_addr(&sh.full[s]), (used / kRing) & 1, gave_up)) {
+                    ok = false;
+                    break;
+                }
+                tmem_fence_after();
+                const uint32_t at = stages + s * kStageBytes;
+                const uint64_t da = operand_desc(at, kAmn), db = operand_desc(at + 2 * kBoxBytes, kBmn);
+#pragma unroll
+                for (uint32_t q = 0; q < kBlockK / 16; ++q)
+                    mma_16(tmem + b * kTileN, da + q * k_step(kAmn), db + q * k_step(kBmn), idesc, k > t.k0 || q > 0);
+                mma_commit(smem_addr(&sh.empty[s]));
+            }
+            if (ok)
+                mma_commit(smem_addr(&sh.acc_full[b]));
+            ++buf;
+        }
+        if (!ok) {  // matrix instructions in flight finish before tensor memory goes
+            uint32_t none = 0;
+            mma_commit(smem_addr(&sh.drain));
+            bar_wait(smem_addr(&sh.drain), 0, &none);
+        }
+    } else if (warp >= 4) {
+        const uint32_t quarter = warp & 3;
+        uint32_t buf = 0;
+        for (uint32_t i = blockIdx.x; i < tiles.total; i += gridDim.x) {
+            const Tile t = tiles.at(i);
+            Part p;
+            p.half = (warp - 4) / 4;
+            p.row = t.m + quarter * 32 + lane;
+            p.empty = t.k0 >= t.k1;
+            const uint32_t b = buf & 1, turn = buf >> 1;
+            p.acc = tmem + (quarter * 32 << 16) + b * kTileN + p.half * (kTileN / 2);
+            if (!p.empty) {
+                if (!__all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_full[b]), turn & 1, gave_up)))
+                    break;
+                tmem_fence_after();
+            }
+            if (MODE == kStats)
+                stats_epilogue<F16>(a, t, p, valid);
+            else if (MODE == kD)
+                d_epilogue<F16>(a, t, p, valid);
+            else
+                sum_epilogue<MODE, F16>(a, t, p, valid);
+            if (!p.empty) {
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(smem_addr(&sh.acc_empty[b]));
+                ++buf;
+            }
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 2)
+        tmem_free(tmem, 512);
+    if (threadIdx.x == 0 && sh.gave_up) {
+        a.head->error = 1;
+        if (a.state_error)
+            *a.state_error = 1;
+    }
+}
+
+/* ------------------------------------------------------------------------------------ */
+/* before and after the products                                                          */
+/* ------------------------------------------------------------------------------------ */
+struct ListArgs {
+    const void* targets;
+    uint32_t wide, rows, rows_pad, vocab;
+    Header* head;
+    uint32_t* token;       // [valid]: the token in its place
+    int* target;           // [valid]
+    float* loss;           // forward: of tokens without a target, 0
+    float* lse;
+    const float* lse_in;   // backward
+    float* lse_out;        // [valid]
+    float* factor;         // [valid]
+    const float* row_scale;
+    const zero_step_state_t* st;
+    float scale;
+    uint32_t backward, f16;
+};
+
+__device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_t vocab, uint32_t t)
+{
+    if (wide) {
+        const long long v = *(static_cast<const volatile long long*>(p) + t);
+        return v >= 0 && v < (long long)vocab ? (int)v : -1;
+    }
+    const int v = *(static_cast<const volatile int*>(p) + t);
+    return v >= 0 && v < (int)vocab ? v : -1;
+}
+
+/* The tokens that have a target, in order, by one block: each warp counts its run of tokens,
+ * then writes them behind the earlier warps'. */
+__global__ void __launch_bounds__(1024) k_head_list(const ListArgs a)
+{
+    __shared__ uint32_t count[32];
+    __shared__ float most[32];
+    grid_dependency_wait();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t each = (a.rows + 1023) / 1024 * 32, lo = warp * each;
+    const uint32_t hi = lo + each < a.rows ? lo + each : a.rows;
+    const float common = a.backward ? __fmul_rn(a.scale, a.st ? *const_cast<const volatile float*>(&a.st->loss_scale) : 1.0f) : 0.0f;
+    uint32_t n = 0;
+    float top = 0.0f;
+#pragma unroll 4
+    for (uint32_t t = lo + lane; t < hi; t += 32) {
+        const bool there = head_target(a.targets, a.wide, a.vocab, t) >= 0;
+        n += there;
+        if (a.f16 && a.backward && there)
+            top = fmaxf(top, fabsf(a.row_scale ? __fmul_rn(common, a.row_scale[t]) : common));
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) {
+        count[warp] = n;
+        most[warp] = top;
+    }
+    __syncthreads();
+    uint32_t at = 0, all = 0;
+    for (uint32_t w = 0; w < 32; ++w) {
+        at += w < warp ? count[w] : 0;
+        all += count[w];
+        top = fmaxf(top, most[w]);
+    }
+    // 2^e with the largest |f| / 2^e in [2^14, 2^15); what is 0 or not finite stays as it is
+    float post = 1.0f;
+    if (a.f16 && a.backward && top > 0.0f && top <= 3.0e38f)
+        post = scalbnf(1.0f, max(ilogbf(top) - 14, -126));
+    const float back = __fdiv_rn(1.0f, post);
+    if (threadIdx.x == 0) {
+        a.head->valid = all;
+        a.head->error = 0;
+        a.head->post = post;
+    }
+#pragma unroll 2
+    for (uint32_t t = lo + lane; t - lane < hi; t += 32) {
+        const int target = t < hi ? head_target(a.targets, a.wide, a.vocab, t) : -1;
+        const uint32_t mask = __ballot_sync(0xffffffffu, target >= 0);
+        const uint32_t r = at + __popc(mask & ((1u << lane) - 1));
+        at += __popc(mask);
+        if (target >= 0) {
+            a.token[r] = t;
+            a.target[r] = target;
+            if (a.backward) {
+                a.lse_out[r] = a.lse_in[t];
+                a.factor[r] = __fmul_rn(a.row_scale ? __fmul_rn(common, a.row_scale[t]) : common, back);
+            }
+        } else if (t < hi && !a.backward) {
+            a.loss[t] = 0.0f;
+            a.lse[t] = 0.0f;
+        }
+    }
+}
+
+struct GatherArgs {
+    const void* targets;
+    uint32_t wide, rows, vocab, dim, dim8, direct;  // direct: hidden can be used as it lies
+    const Header* head;
+    const uint32_t* token;
+    const uint16_t* hidden;
+    uint64_t hidden_stride;
+    uint16_t* gathered;   // [rows_pad][dim8]
+    uint16_t* dhidden;    // backward: rows of tokens without a target are written 0
+    uint64_t dhidden_stride;
+};
+
+/* Rows of the tokens that have a target next to each other, then zeros up to a multiple of
+ * 128 rows; nothing where every token has one and hidden can be used as it lies. */
+__global__ void __launch_bounds__(256) k_head_gather(const GatherArgs a)
+{
+    grid_dependency_wait();
+    const uint32_t valid = a.head->valid, lane = threadIdx.x & 31;
+    const uint32_t warps = gridDim.x * (blockDim.x / 32), first = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
+    if (a.dhidden && valid != a.rows) {
+        for (uint32_t t = first; t < a.rows; t += warps) {
+            if (head_target(a.targets, a.wide, a.vocab, t) >= 0)
+                continue;
+            uint16_t* row = a.dhidden + t * a.dhidden_stride;
+            for (uint32_t c = lane; c < a.dim; c += 32)
+                row[c] = 0;
+        }
+    }
+    if (valid == a.rows && a.direct)
+        return;
+    const bool vec = a.dim % 8 == 0 && a.hidden_stride % 8 == 0 && ((uintptr_t)a.hidden & 15) == 0;
+    const uint32_t end = (valid + kTileM - 1) / kTileM * kTileM;
+    for (uint32_t r = first; r < end; r += warps) {
+        const uint16_t* from = a.hidden + (r < valid ? a.token[r] * a.hidden_stride : 0);
+        uint16_t* to = a.gathered + (uint64_t)r * a.dim8;
+        if (vec) {
+            for (uint32_t c = lane; c < a.dim / 8; c += 32)
+                reinterpret_cast<uint4*>(to)[c] = r < valid ? ld_v4(from + c * 8) : make_uint4(0, 0, 0, 0);
+        } else {
+            for (uint32_t c = lane; c < a.dim8; c += 32)
+                to[c] = r < valid && c < a.dim ? from[c] : (uint16_t)0;
+        }
+    }
+}
+
+/* Rows of odd length at a pitch that the TMA takes. */
+__global__ void __launch_bounds__(256) k_head_pad(const uint16_t* from, uint16_t* to, uint32_t rows, uint32_t dim,
+                                                  uint32_t dim8)
+{
+    grid_dependency_wait();
+    const uint32_t lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
+    for (uint32_t r = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps)
+        for (uint32_t c = lane; c < dim8; c += 32)
+            to[(uint64_t)r * dim8 + c] = c < dim ? from[(uint64_t)r * dim + c] : (uint16_t)0;
+}
+
+struct LossArgs {
+    const Header* head;
+    const uint32_t* token;
+    const float2* stats;
+    const float* target_logit;
+    float* loss;
+    float* lse;
+    uint32_t tiles;
+};
+
+/* The tiles' statistics of a token, a warp per token. */
+__global__ void __launch_bounds__(256) k_head_loss(const LossArgs a)
+{
+    grid_dependency_wait();
+    const uint32_t valid = a.head->valid, lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
+    for (uint32_t r = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < valid; r += warps) {
+        const float2* s = a.stats + (uint64_t)r * a.tiles;
+        float top = __int_as_float(0xff800000), sum = 0.0f;
+        for (uint32_t i = lane; i < a.tiles; i += 32) {
+            const float2 x = s[i];
+            const float m = fmaxf(top, x.x), ref = m == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(m, kLog2e);
+            sum = __fadd_rn(__fmul_rn(sum, exp2f(__fmaf_rn(top, kLog2e, -ref))),
+                            __fmul_rn(x.y, exp2f(__fmaf_rn(x.x, kLog2e, -ref))));
+            top = m;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const float ot = __shfl_xor_sync(0xffffffffu, top, o), os = __shfl_xor_sync(0xffffffffu, sum, o);
+            const float m = fmaxf(top, ot), ref = m == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(m, kLog2e);
+            sum = __fadd_rn(__fmul_rn(sum, exp2f(__fmaf_rn(top, kLog2e, -ref))),
+                            __fmul_rn(os, exp2f(__fmaf_rn(ot, kLog2e, -ref))));
+            top = m;
+        }
+        if (lane == 0) {
+            // sum is relative to 2^(top * log2e): the same product as in the exponents
+            const float ref = top == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(top, kLog2e);
+            const float lse = a.head->error ? __int_as_float(0x7fc00000)
+                                            : __fmul_rn(__fadd_rn(log2f(sum), ref), kLn2);
+            a.lse[a.token[r]] = lse;
+            a.loss[a.token[r]] = __fsub_rn(lse, a.target_logit[r]);
+        }
+    }
+}
+
+struct JoinArgs {
+    const Header* head;
+    const float* sums;
+    const uint32_t* token;  // dhidden: row r goes to token[r]; dweight: null, row r to v0 + r
+    void* out;
+    uint64_t out_stride, split_stride;
+    uint32_t rows, v0, dim, dim8, splits, accumulate;
+};
+
+/* The splits' sums in order, times the common factor, rounded once. */
+template <zero_dtype_t GT, bool VEC>
+__global__ void __launch_bounds__(256) k_head_join(const JoinArgs a)
+{
+    using G = typename Elem<GT>::T;
+    grid_dependency_wait();
+    const uint32_t rows = a.token ? a.head->valid : a.rows, lane = threadIdx.x & 31;
+    const float post = a.head->post;
+    const uint32_t pieces = (a.dim + 255) / 256;
+    const uint64_t warps = (uint64_t)gridDim.x * (blockDim.x / 32), total = (uint64_t)rows * pieces;
+    for (uint64_t u = (uint64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); u < total; u += warps) {
+        const uint32_t r = (uint32_t)(u / pieces), piece = (uint32_t)(u - (uint64_t)r * pieces);
+        G* row = static_cast<G*>(a.out) + (a.token ? a.token[r] : a.v0 + r) * a.out_stride;
+        const float* from = a.sums + (uint64_t)r * a.dim8;
+        float s[8], v[8];
+        widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(from, a.dim, piece, lane, 32), s);
+        for (uint32_t k = 1; k < a.splits; ++k) {
+            widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(from + k * a.split_stride, a.dim, piece, lane, 32), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s[j] = __fadd_rn(s[j], v[j]);
+        }
+        if (a.accumulate)
+            widen<GT>(load_chunk<GT, VEC>(row, a.dim, piece, lane, 32), v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s[j] = a.accumulate ? __fmaf_rn(s[j], post, v[j]) : __fmul_rn(s[j], post);
+        store_chunk<GT, VEC>(row, a.dim, piece, lane, 32, s);
+    }
+}
+
+/* ------------------------------------------------------------------------------------ */
+/* host side                                                                              */
+/* ------------------------------------------------------------------------------------ */
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+/* The driver's encoder, through the runtime (the library does not link libcuda). */
+EncodeTiled encoder()
+{
+    static EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+bool tensor_map(CUtensorMap* map, const void* p, bool f16, uint64_t cols, uint64_t rows, uint64_t stride)
+{
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride * 2};
+    const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+    return encoder() &&
+           encoder()(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                     const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
+
+/* How a call is cut, and where its parts lie in the workspace. */
+struct Plan {
+    uint32_t rows_pad, dim8, piece, pieces, tile_n, splits_h, splits_w;
+    uint64_t token, target, factor, lse, logit, gathered, weight, stats, d, sums_h, sums_w, bytes;
+};
+
+Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
+{
+    Plan p;
+    p.rows_pad = (uint32_t)up(rows ? rows : 1, kTileM);
+    p.dim8 = (uint32_t)up(dim, 8);
+    const uint64_t vp = up(vocab, kTileN);
+    // D of a piece: 64 million elements (128 MB, about the L2) or 8,192 columns, whichever is more
+    uint64_t piece = up((64ull << 20) / p.rows_pad, kTileN);
+    piece = piece < 8192 ? 8192 : piece;
+    p.pieces = (uint32_t)((vp + piece - 1) / piece);
+    p.piece = (uint32_t)up((vp + p.pieces - 1) / p.pieces, kTileN);
+    p.pieces = (uint32_t)((vp + p.piece - 1) / p.piece);
+    const uint32_t nt = (dim + kTileN - 1) / kTileN;
+    p.tile_n = (uint32_t)up((dim + nt - 1) / nt, 16);
+    // few tiles: the sum is split so that the SMs have work, 8 blocks of 64 at least to a split
+    auto splits = [](uint64_t tiles, uint64_t k) {
+        const uint64_t want = tiles >= kSms ? 1 : kSms / tiles, most = k / (8 * kBlockK);
+        return (uint32_t)(want < most ? want : most > 0 ? most : 1);
+    };
+    p.splits_h = splits((uint64_t)p.rows_pad / kTileM * nt, p.piece);
+    p.splits_w = splits((uint64_t)p.piece / kTileM * nt, p.rows_pad);
+    uint64_t at = sizeof(Header);
+    auto take = [&](uint64_t bytes) {
+        const uint64_t q = at;
+        at += up(bytes, 256);
+        return q;
+    };
+    p.token = take(4ull * p.rows_pad);
+    p.target = take(4ull * p.rows_pad);
+    p.factor = take(4ull * p.rows_pad);
+    p.lse = take(4ull * p.rows_pad);
+    p.logit = take(4ull * p.rows_pad);
+    p.gathered = take(2ull * p.rows_pad * p.dim8);
+    p.weight = take(dim % 8 ? 2ull * vocab * p.dim8 : 0);
+    const uint64_t shared = at;
+    p.stats = take(8ull * p.rows_pad * (vp / 128));
+    const uint64_t forward = at;
+    at = shared;
+    p.d = take(2ull * p.rows_pad * p.piece);
+    p.sums_h = take(4ull * p.splits_h * p.rows_pad * p.dim8);
+    p.sums_w = take(p.splits_w > 1 ? 4ull * p.splits_w * p.piece * p.dim8 : 0);
+    p.bytes = at > forward ? at : forward;
+    return p;
+}
+
+bool sizes_ok(uint64_t rows, uint32_t dim, uint32_t vocab)
+{
+    return rows <= (1ull << 24) && dim >= 1 && dim <= 65536 && vocab >= 1 && vocab <= (1u << 24);
+}
+
+struct Call {
+    zero_dtype_t dtype;
+    uint64_t rows;
+    uint32_t dim, vocab;
+    const void* hidden;
+    uint64_t hidden_stride;
+    const void* weight;
+    const void* targets;
+    uint32_t target_bytes;
+    char* work;
+    cudaStream_t stream;
+};
+
+int check_call(const Call& c, uint64_t bytes)
+{
+    if ((c.dtype != ZERO_BF16 && c.dtype != ZERO_F16) || !sizes_ok(c.rows, c.dim, c.vocab) ||
+        (c.target_bytes != 4 && c.target_bytes != 8) || !c.weight || !c.work)
+        return ZERO_EINVAL;
+    if (c.rows && (!c.hidden || !c.targets || (c.rows > 1 && c.hidden_stride < c.dim) || c.hidden_stride > (1ull << 32)))
+        return ZERO_EINVAL;
+    if (!aligned_to(c.hidden, 2) || !aligned_to(c.weight, c.dim % 8 ? 2 : 16) ||
+        !aligned_to(c.targets, c.target_bytes) || !aligned_to(c.work, 256))
+        return ZERO_EALIGN;
+    if (overlap(c.work, bytes, c.hidden, span(c.rows, c.hidden_stride, c.dim, c.dtype)) ||
+        overlap(c.work, bytes, c.weight, 2ull * c.vocab * c.dim) ||
+        overlap(c.work, bytes, c.targets, c.rows * c.target_bytes))
+        return ZERO_EINVAL;
+    return ZERO_OK;
+}
+
+unsigned warps_grid(uint64_t warps)
+{
+    const uint64_t want = (warps + 7) / 8, cap = (uint64_t)sm_count() * 8;
+    return (unsigned)(want < cap ? (want ? want : 1) : cap);
+}
+
+/* Lists and gathers the tokens, pads weight's rows where they need it, and fills what the
+ * products of the call share. */
+int prologue(const Call& c, const Plan& p, ListArgs l, void* dhidden, uint64_t dhidden_stride, ProductArgs& a)
+{
+    const bool f16 = c.dtype == ZERO_F16;
+    Header* head = reinterpret_cast<Header*>(c.work);
+    l.targets = c.targets;
+    l.wide = c.target_bytes == 8;
+    l.rows = (uint32_t)c.rows;
+    l.rows_pad = p.rows_pad;
+    l.vocab = c.vocab;
+    l.head = head;
+    l.token = reinterpret_cast<uint32_t*>(c.work + p.token);
+    l.target = reinterpret_cast<int*>(c.work + p.target);
+    l.lse_out = reinterpret_cast<float*>(c.work + p.lse);
+    l.factor = reinterpret_cast<float*>(c.work + p.factor);
+    l.f16 = f16;
+    const bool direct = c.dim % 8 == 0 && c.hidden_stride % 8 == 0 && aligned_to(c.hidden, 16);
+    uint16_t* gathered = reinterpret_cast<uint16_t*>(c.work + p.gathered);
+    const void* weight = c.dim % 8 ? c.work + p.weight : c.weight;
+    memset(&a, 0, sizeof a);
+    const uint64_t stride = c.rows > 1 ? c.hidden_stride : p.dim8;
+    if (!tensor_map(&a.gathered, gathered, f16, c.dim, p.rows_pad, p.dim8) ||
+        !tensor_map(&a.weight, weight, f16, c.dim, c.vocab, p.dim8) ||
+        !tensor_map(&a.d, c.work + p.d, f16, p.piece, p.rows_pad, p.piece) ||
+        (direct && c.rows && !tensor_map(&a.hidden, c.hidden, f16, c.dim, c.rows, stride))) {
+        record_cuda_error((int)cudaErrorInvalidValue);
+        return ZERO_ECUDA;
+    }
+    if (!direct || !c.rows)
+        a.hidden = a.gathered;
+    a.head = head;
+    a.target = l.target;
+    a.factor = l.factor;
+    a.lse = l.lse_out;
+    a.target_logit = reinterpret_cast<float*>(c.work + p.logit);
+    a.stats = reinterpret_cast<float2*>(c.work + p.stats);
+    a.dd = reinterpret_cast<uint16_t*>(c.work + p.d);
+    a.rows = (uint32_t)c.rows;
+    a.rows_pad = p.rows_pad;
+    a.dim = c.dim;
+    a.dim8 = p.dim8;
+    a.vocab = c.vocab;
+    a.d_stride = p.piece;
+    a.tile_n = p.tile_n;
+    a.splits = 1;
+    // row tiles whose hidden rows (32 MB) stay in L2 while weight passes by
+    const uint64_t group = (32ull << 20) / (kTileM * 2ull * p.dim8);
+    a.group = (uint32_t)(group ? group : 1);
+    cudaError_t e = launch_pdl(k_head_list, dim3(1), dim3(1024), 0, c.stream, l);
+    const GatherArgs g{c.targets,
+                       l.wide,
+                       l.rows,
+                       c.vocab,
+                       c.dim,
+                       p.dim8,
+                       direct,
+                       head,
+                       l.token,
+                       static_cast<const uint16_t*>(c.hidden),
+                       c.hidden_stride,
+                       gathered,
+                       static_cast<uint16_t*>(dhidden),
+                       dhidden_stride};
+    if (e == cudaSuccess)
+        e = launch_pdl(k_head_gather, dim3(warps_grid(p.rows_pad)), dim3(256), 0, c.stream, g);
+    if (e == cudaSuccess && c.dim % 8)
+        e = launch_pdl(k_head_pad, dim3(warps_grid(c.vocab)), dim3(256), 0, c.stream,
+                       static_cast<const uint16_t*>(c.weight), reinterpret_cast<uint16_t*>(c.work + p.weight), c.vocab,
+                       c.dim, p.dim8);
+    return rows_status(e);
+}
+
+template <Mode MODE>
+cudaError_t product(const ProductArgs& a, bool f16, uint64_t tiles, cudaStream_t s)
+{
+    auto* kernel = f16 ? k_head_product<MODE, true> : k_head_product<MODE, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t sms = (uint64_t)sm_count();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <zero_dtype_t GT>
+cudaError_t join(const JoinArgs& j, uint64_t rows, bool vec, cudaStream_t s)
+{
+    const unsigned grid = warps_grid(rows * ((j.dim + 255) / 256));
+    return vec ? launch_pdl(k_head_join<GT, true>, dim3(grid), dim3(256), 0, s, j)
+               : launch_pdl(k_head_join<GT, false>, dim3(grid), dim3(256), 0, s, j);
+}
+
+cudaError_t join(const JoinArgs& j, uint64_t rows, zero_dtype_t t, bool vec, cudaStream_t s)
+{
+    return t == ZERO_F32   ? join<ZERO_F32>(j, rows, vec, s)
+           : t == ZERO_F16 ? join<ZERO_F16>(j, rows, vec, s)
+                           : join<ZERO_BF16>(j, rows, vec, s);
+}
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" {
+
+size_t zero_head_workspace_bytes(uint64_t rows, uint32_t dim, uint32_t vocab)
+{
+    return sizes_ok(rows, dim, vocab) ? (size_t)make_plan(rows, dim, vocab).bytes : 0;
+}
+
+int zero_head_loss(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t vocab, const void* hidden,
+                   uint64_t hidden_stride, const void* weight, const void* targets, uint32_t target_bytes, float* loss,
+                   float* lse, void* workspace, zero_stream_t stream)
+{
+    NvtxRange range("zero_head_loss");
+    const Call c{dtype,  rows,    dim,          vocab,  hidden, hidden_stride,
+                 weight, targets, target_bytes, static_cast<char*>(workspace), stream};
+    const uint64_t bytes = zero_head_workspace_bytes(rows, dim, vocab);
+    int rc = check_call(c, bytes);
+    if (rc == ZERO_EINVAL || (rows && (!loss || !lse)))
+        return ZERO_EINVAL;
+    if (rc != ZERO_OK || !aligned_to(loss, 4) || !aligned_to(lse, 4))
+        return ZERO_EALIGN;
+    const uint64_t nh = span(rows, hidden_stride, dim, dtype), nv = 2ull * vocab * dim, nt = rows * target_bytes;
+    for (const float* out : {loss, lse})
+        if (overlap(out, rows * 4, hidden, nh) || overlap(out, rows * 4, weight, nv) ||
+            overlap(out, rows * 4, targets, nt) || overlap(out, rows * 4, workspace, bytes))
+            return ZERO_EINVAL;
+    if (overlap(loss, rows * 4, lse, rows * 4))
+        return ZERO_EINVAL;
+    if (rows == 0)
+        return ZERO_OK;
+    const Plan p = make_plan(rows, dim, vocab);
+    ListArgs l = {};
+    l.loss = loss;
+    l.lse = lse;
+    ProductArgs a;
+    rc = prologue(c, p, l, nullptr, 0, a);
+    if (rc != ZERO_OK)
+        return rc;
+    a.cols = vocab;
+    const uint32_t tiles = (vocab + kTileN - 1) / kTileN;
+    cudaError_t e = product<kStats>(a, dtype == ZERO_F16, (uint64_t)p.rows_pad / kTileM * tiles, stream);
+    if (e != cudaSuccess)
+        return rows_status(e);
+    const LossArgs j{a.head, reinterpret_cast<const uint32_t*>(c.work + p.token), a.stats, a.target_logit, loss, lse, 2 * tiles};
+    return rows_status(launch_pdl(k_head_loss, dim3(warps_grid(rows)), dim3(256), 0, stream, j));
+}
+
+int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t vocab, const void* hidden,
+                            uint64_t hidden_stride, const void* weight, const void* targets, uint32_t target_bytes,
+                            const float* lse, float scale, const float* row_scale, zero_step_state_t* st,
+                            void* dhidden, uint64_t dhidden_stride, void* dweight, zero_dtype_t grad_dtype,
+                            uint32_t accumulate, void* workspace, zero_stream_t stream)
+{
+    NvtxRange range("zero_head_loss_backward");
+    const Call c{dtype,  rows,    dim,          vocab,  hidden, hidden_stride,
+                 weight, targets, target_bytes, static_cast<char*>(workspace), stream};
+    const uint64_t bytes = zero_head_workspace_bytes(rows, dim, vocab);
+    int rc = check_call(c, bytes);
+    if (rc == ZERO_EINVAL || (rows && !lse) || (!dhidden && !dweight) || accumulate > 1 ||
+        (dweight && grad_dtype != dtype && grad_dtype != ZERO_F32) || !(scale >= -3.0e38f && scale <= 3.0e38f) ||
+        (dhidden && ((rows > 1 && dhidden_stride < dim) || dhidden_stride > (1ull << 32))))
+        return ZERO_EINVAL;
+    const size_t g = dtype_size(grad_dtype);
+    if (rc != ZERO_OK || !aligned_to(lse, 4) || !aligned_to(row_scale, 4) || !aligned_to(st, 16) ||
+        !aligned_to(dhidden, 2) || !aligned_to(dweight, g))
+        return ZERO_EALIGN;
+    const uint64_t nh = span(rows, hidden_stride, dim, dtype), nv = 2ull * vocab * dim, nt = rows * target_bytes,
+                   nd = span(rows, dhidden_stride, dim, dtype), nw = (uint64_t)vocab * dim * g;
+    const struct {
+        const void* p;
+        uint64_t n;
+    } in[] = {{hidden, nh}, {weight, nv}, {targets, nt}, {lse, rows * 4}, {row_scale, rows * 4}, {st, sizeof *st},
+              {workspace, bytes}},
+      out[] = {{dhidden, nd}, {dweight, nw}};
+    for (const auto& o : out)
+        for (const auto& i : in)
+            if (overlap(o.p, o.n, i.p, i.n))
+                return ZERO_EINVAL;
+    if (overlap(dhidden, nd, dweight, nw) || overlap(workspace, bytes, lse, rows * 4) ||
+        overlap(workspace, bytes, row_scale, rows * 4) || overlap(workspace, bytes, st, sizeof *st))
+        return ZERO_EINVAL;
+    if (rows == 0 && (!dweight || accumulate))
+        return ZERO_OK;
+    const bool f16 = dtype == ZERO_F16;
+    const Plan p = make_plan(rows, dim, vocab);
+    ListArgs l = {};
+    l.lse_in = lse;
+    l.row_scale = row_scale;
+    l.st = st;
+    l.scale = scale;
+    l.backward = 1;
+    ProductArgs a;
+    rc = prologue(c, p, l, dhidden, dhidden_stride, a);
+    if (rc != ZERO_OK)
+        return rc;
+    a.state_error = st ? &st->error : nullptr;
+    a.dweight = dweight;
+    a.grad_dtype = (uint32_t)grad_dtype;
+    a.accumulate = accumulate;
+    a.vec = dweight && rows_vec(dweight, dim, dim, grad_dtype);
+    const uint64_t mt = p.rows_pad / kTileM, nd_tiles = (dim + p.tile_n - 1) / p.tile_n;
+    cudaError_t e = cudaSuccess;
+    for (uint32_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += p.piece) {
+        a.v0 = v0;
+        a.cols = vocab - v0 < p.piece ? vocab - v0 : p.piece;
+        a.first_piece = v0 == 0;
+        e = product<kD>(a, f16, mt * ((a.cols + kTileN - 1) / kTileN), stream);
+        if (e == cudaSuccess && dhidden) {
+            a.splits = p.splits_h;
+            a.sums = reinterpret_cast<float*>(c.work + p.sums_h);
+            e = product<kDhidden>(a, f16, mt * nd_tiles * a.splits, stream);
+        }
+        if (e == cudaSuccess && dweight) {
+            a.splits = p.splits_w;
+            a.sums = reinterpret_cast<float*>(c.work + p.sums_w);
+            e = product<kDweight>(a, f16, (a.cols + kTileM - 1) / kTileM * nd_tiles * a.splits, stream);
+            if (e == cudaSuccess && p.splits_w > 1) {
+                const JoinArgs j{a.head, a.sums, nullptr, dweight, dim, (uint64_t)p.piece * p.dim8, a.cols, v0, dim,
+                                 p.dim8, p.splits_w, accumulate};
+                e = join(j, a.cols, grad_dtype, a.vec, stream);
+            }
+        }
+    }
+    if (e == cudaSuccess && dhidden && rows) {
+        const JoinArgs j{a.head,
+                         reinterpret_cast<const float*>(c.work + p.sums_h),
+                         reinterpret_cast<const uint32_t*>(c.work + p.token),
+                         dhidden,
+                         dhidden_stride,
+                         (uint64_t)p.rows_pad * p.dim8,
+                         (uint32_t)rows,
+                         0,
+                         dim,
+                         p.dim8,
+                         p.splits_h,
+                         0};
+        e = join(j, rows, dtype, rows_vec(dhidden, dhidden_stride, dim, dtype), stream);
+    }
+    return rows_status(e);
+}
+
+}  // extern "C"

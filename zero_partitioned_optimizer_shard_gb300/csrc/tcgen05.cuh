@@ -1,0 +1,139 @@
+/*
+ * tcgen05.cuh -- the matrix unit of sm_103a as head_loss.cu uses it: shared-memory operand
+ * tiles brought in by TMA, accumulators in tensor memory, mbarriers with bounded waits.
+ *
+ * Operands are 16-bit tiles under the 128-byte swizzle, cut into boxes of 64 rows of 128
+ * bytes (8 KB, one TMA copy each):
+ *   K-major   a box is 64 rows of the operand by 64 of K; 8-row groups lie 1,024 bytes apart,
+ *             a step of 16 along K is 32 bytes
+ *   MN-major  a box is 64 of K by 64 of the operand's rows: each K row holds 64 neighbours.
+ *             The next 64 lie a box further, the next 8 of K 1,024 bytes, a step of 16 along
+ *             K 2,048 bytes
+ */
+#pragma once
+
+#include "rows.cuh"
+
+#include <cuda.h>
+
+namespace zero {
+namespace {
+
+constexpr uint32_t kBoxBytes = 8192;
+
+__device__ __forceinline__ uint64_t operand_desc(uint32_t smem, bool mn_major)
+{
+    const uint64_t lead = mn_major ? kBoxBytes / 16 : 1;
+    return (uint64_t)((smem & 0x3ffff) >> 4) | lead << 16 | (uint64_t)(1024 / 16) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+/* Bytes / 16 from one step of 16 along K to the next. */
+__host__ __device__ constexpr uint32_t k_step(bool mn_major) { return mn_major ? 128 : 2; }
+
+/* fp32 accumulation of an M x N tile; A and B both bf16 or both fp16. */
+__device__ __forceinline__ uint32_t instr_desc(bool f16, bool a_mn, bool b_mn, uint32_t m, uint32_t n)
+{
+    const uint32_t type = f16 ? 0 : 1;
+    return 1u << 4 | type << 7 | type << 10 | (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16 | (n / 8) << 17 |
+           (m / 16) << 24;
+}
+
+__device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "r"(accumulate)
+                 : "memory");
+}
+
+/* Arrives on the mbarrier once every MMA issued so far by this thread has finished. */
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns));
+}
+
+/* 32 columns of the warp's 32 accumulator rows: thread l gets row l. */
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32])
+{
+    uint32_t r[32];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+                   "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+                   "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+                   "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
+/* One box at (x: the contiguous dimension, y: the rows); what lies outside the tensor is 0.
+ * x is a multiple of 8 elements. */
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+/* A wait of at most ~2 s, cut short where another thread of the block has given up. */
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up)
+{
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t ok;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(ok)
+                     : "r"(bar), "r"(parity)
+                     : "memory");
+        if (ok)
+            return true;
+        if (*gave_up)
+            return false;
+        if (clock64() - t0 > 4000000000LL) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+}
+
+/* A row-major tensor of 16-bit elements for boxes of 64 x 64.  False where the driver refuses
+ * it (the address, the stride and the extents are checked by the callers). */
+bool tensor_map(CUtensorMap* map, const void* p, bool f16, uint64_t cols, uint64_t rows, uint64_t stride);
+
+}  // namespace
+}  // namespace zero
