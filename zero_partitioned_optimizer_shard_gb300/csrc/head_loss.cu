@@ -28,11 +28,15 @@
 namespace zero {
 namespace {
 
-constexpr uint32_t kTileM = 128, kTileN = 256, kBlockK = 64;
-constexpr uint32_t kRing = 4;
-constexpr uint32_t kStageBytes = (kTileM + kTileN) * kBlockK * 2;
+constexpr uint32_t kTileM = 256, kTileN = 256, kBlockK = 64;
+constexpr uint32_t kRows = kTileM / 2;  // of a block of the pair
+constexpr uint32_t kRing = 6;
+constexpr uint32_t kStageBytes = 4 * kBoxBytes;  // 128 rows of A and half of B's, by 64
+constexpr uint32_t kSumBlocks = 16;     // logits: blocks of 64 that the matrix unit sums by itself
 constexpr uint32_t kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;
-constexpr uint32_t kSmem = kRing * kStageBytes + 1024;  // and to a 1,024-byte boundary
+constexpr uint32_t kOutBytes = 4096;    // of an epilogue warp: 32 rows of 128 bytes
+constexpr uint32_t kSmem = kRing * kStageBytes + kEpilogueWarps * kOutBytes + 1024;  // and to a 1,024-byte boundary
+static_assert(kSmem <= 226 * 1024, "beside the barriers, of 227 KB");
 constexpr uint32_t kSms = 152;  // of a GB300: sizes the workspace and the splits
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -52,6 +56,7 @@ struct ProductArgs {
     CUtensorMap gathered;  // the rows of the tokens that have a target
     CUtensorMap weight;
     CUtensorMap d;         // D's piece
+    CUtensorMap out;       // what the launch writes: D's piece, or the sums, or dweight
     Header* head;
     uint32_t* state_error;  // the step state's error word, or null
     const int* target;      // [valid]
@@ -59,14 +64,11 @@ struct ProductArgs {
     const float* lse;       // [valid]
     float* target_logit;    // [valid]
     float2* stats;          // [valid][2 * column tiles]
-    uint16_t* dd;           // D: [rows][d_stride]
-    float* sums;            // dhidden: [splits][rows_pad][dim8]; dweight: [splits][piece][dim8]
-    void* dweight;          // one split: written in place
+    void* dweight;          // where it is added to, or lies as the TMA does not take it; else null
     uint32_t rows;          // of the call, with or without a target
     uint32_t rows_pad, dim, dim8, vocab;
     uint32_t v0, cols;      // the piece: columns [v0, v0 + cols) of the vocabulary
-    uint32_t d_stride;
-    uint32_t tile_n;        // dhidden, dweight: columns of a tile
+    uint32_t piece;
     uint32_t splits;        // of the sum over the piece (dhidden) or the tokens (dweight)
     uint32_t group;         // row tiles that share a run through the columns
     uint32_t first_piece;   // sums start here
@@ -74,24 +76,24 @@ struct ProductArgs {
 };
 
 struct Tile {
-    uint32_t m, n;      // first row and column
-    uint32_t k0, k1;    // blocks of 64 along the sum
+    uint32_t m, n, width;  // first row and column, columns
+    uint32_t k0, k1;       // blocks of 64 along the sum
     uint32_t split, nt;
 };
 
 /* The extents of a launch's tiles, known once the number of tokens with a target is. */
 template <Mode MODE>
 struct Tiles {
-    uint32_t mt, nt, blocks, splits, group, tile_n, total;
+    uint32_t mt, nt, units, blocks, splits, group, total;
 
     __device__ Tiles(const ProductArgs& a, uint32_t valid)
     {
         const uint32_t m = MODE == kDweight ? a.cols : valid;
         const uint32_t k = MODE == kDweight ? valid : MODE == kDhidden ? a.cols : a.dim;
         const uint32_t n = MODE == kStats || MODE == kD ? a.cols : a.dim;
-        tile_n = MODE == kStats || MODE == kD ? kTileN : a.tile_n;
         mt = (m + kTileM - 1) / kTileM;
-        nt = (n + tile_n - 1) / tile_n;
+        units = (n + 31) / 32;
+        nt = (n + kTileN - 1) / kTileN;
         blocks = (k + kBlockK - 1) / kBlockK;
         splits = MODE == kStats || MODE == kD ? 1 : a.splits;
         group = a.group;
@@ -115,7 +117,13 @@ struct Tiles {
             n = t - m * nt;
         }
         r.m = m * kTileM;
-        r.n = n * tile_n;
+        if (MODE == kStats || MODE == kD) {
+            r.n = n * kTileN;
+            r.width = kTileN;
+        } else {  // dim in equal tiles, to a multiple of 32
+            r.n = units * n / nt * 32;
+            r.width = units * (n + 1) / nt * 32 - r.n;
+        }
         r.nt = n;
         r.k0 = (uint32_t)((uint64_t)blocks * r.split / splits);
         r.k1 = (uint32_t)((uint64_t)blocks * (r.split + 1) / splits);
@@ -140,6 +148,7 @@ struct Part {
     uint32_t acc;   // tensor memory address
     uint32_t row;   // this thread's row
     uint32_t half;
+    uint32_t stage, lane;
     bool empty;     // no block along the sum: zeros
 };
 
@@ -154,46 +163,48 @@ __device__ __forceinline__ void load_part(const Part& p, uint32_t c, float (&x)[
     }
 }
 
-template <bool F16>
-__device__ __forceinline__ void stats_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid)
+/* x: the row's 128 logits of the tile. */
+__device__ __forceinline__ void stats_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid,
+                                               float (&x)[4][32])
 {
+    const float none = __int_as_float(0xff800000);
     const int target = p.row < valid ? a.target[p.row] : -1;
-    float top = __int_as_float(0xff800000), sum = 0.0f;
-#pragma unroll 1
-    for (uint32_t c = 0; c < kTileN / 2; c += 32) {
-        const uint32_t col = t.n + p.half * (kTileN / 2) + c;
-        float x[32];
-        load_part(p, c, x);
-        if (col + 32 > a.vocab) {
+    const uint32_t col = t.n + p.half * (kTileN / 2);
+    if (col + kTileN / 2 > a.vocab) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                x[j] = col + j < a.vocab ? x[j] : __int_as_float(0xff800000);
-        }
-        const uint32_t off = (uint32_t)target - col;
-        if (off < 32) {
-            float v = 0.0f;
+        for (uint32_t q = 0; q < 4; ++q)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                v = off == (uint32_t)j ? x[j] : v;
-            a.target_logit[p.row] = v;
-        }
-        float m = top;
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            m = fmaxf(m, x[j]);
-        // a row of -inf so far: any reference will do, exp gives 0
-        const float ref = m == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(m, kLog2e);
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            s[j & 3] = __fadd_rn(s[j & 3], exp2_approx(__fmaf_rn(x[j], kLog2e, -ref)));
-        sum = __fmaf_rn(sum, exp2_approx(__fmaf_rn(top, kLog2e, -ref)),
-                        __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])));
-        top = m;
+            for (uint32_t j = 0; j < 32; ++j)
+                x[q][j] = col + 32 * q + j < a.vocab ? x[q][j] : none;
     }
+    const uint32_t off = (uint32_t)target - col;
+    if (off < kTileN / 2) {
+        float v = 0.0f;
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q)
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j)
+                v = off == 32 * q + j ? x[q][j] : v;
+        a.target_logit[p.row] = v;
+    }
+    float top[4] = {none, none, none, none}, s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q)
+#pragma unroll
+        for (uint32_t j = 0; j < 32; ++j)
+            top[j & 3] = fmaxf(top[j & 3], x[q][j]);
+    const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    // a row of -inf: any reference will do, exp gives 0
+    const float ref = m == none ? 0.0f : __fmul_rn(m, kLog2e);
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q)
+#pragma unroll
+        for (uint32_t j = 0; j < 32; ++j)
+            s[j & 3] = __fadd_rn(s[j & 3], exp2_approx(__fmaf_rn(x[q][j], kLog2e, -ref)));
     if (p.row < valid) {
         const uint32_t tiles = 2 * ((a.cols + kTileN - 1) / kTileN);
-        a.stats[(uint64_t)p.row * tiles + 2 * t.nt + p.half] = make_float2(top, sum);
+        a.stats[(uint64_t)p.row * tiles + 2 * t.nt + p.half] =
+            make_float2(m, __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])));
     }
 }
 
@@ -204,25 +215,34 @@ __device__ __forceinline__ void d_epilogue(const ProductArgs& a, const Tile& t, 
     const int target = in ? a.target[p.row] - (int)a.v0 : -1;
     const float f = in ? a.factor[p.row] : 0.0f;
     const float lse = in ? __fmul_rn(a.lse[p.row], kLog2e) : 0.0f;
-    uint16_t* out = a.dd + (uint64_t)p.row * a.d_stride;
 #pragma unroll 1
-    for (uint32_t c = 0; c < kTileN / 2; c += 32) {
-        const uint32_t col = t.n + p.half * (kTileN / 2) + c;
-        float x[32];
-        load_part(p, c, x);
-        const uint32_t off = (uint32_t)target - col;
+    for (uint32_t c = 0; c < kTileN / 2; c += 64) {
+        const uint32_t col = t.n + p.half * (kTileN / 2) + c, off = (uint32_t)target - col;
+        uint4 v[8];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            float e = exp2_approx(__fmaf_rn(x[j], kLog2e, -lse));
-            if (off == (uint32_t)j)
-                e = __fsub_rn(e, 1.0f);
-            x[j] = in && col + j < a.cols ? __fmul_rn(f, e) : 0.0f;
+        for (uint32_t h = 0; h < 2; ++h) {
+            float x[32];
+            tmem_load32(p.acc + c + 32 * h, x);
+#pragma unroll
+            for (uint32_t j = 0; j < 32; ++j) {
+                float e = exp2_approx(__fmaf_rn(x[j], kLog2e, -lse));
+                if (off == 32 * h + j)
+                    e = __fsub_rn(e, 1.0f);
+                x[j] = in ? __fmul_rn(f, e) : 0.0f;
+            }
+            if (col + 64 > a.cols) {  // behind the vocabulary
+#pragma unroll
+                for (uint32_t j = 0; j < 32; ++j)
+                    x[j] = col + 32 * h + j < a.cols ? x[j] : 0.0f;
+            }
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q)
+                v[4 * h + q] = make_uint4(pack2<F16>(x[8 * q], x[8 * q + 1]), pack2<F16>(x[8 * q + 2], x[8 * q + 3]),
+                                          pack2<F16>(x[8 * q + 4], x[8 * q + 5]), pack2<F16>(x[8 * q + 6], x[8 * q + 7]));
         }
-        uint4* to = reinterpret_cast<uint4*>(out + col);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            to[q] = make_uint4(pack2<F16>(x[8 * q], x[8 * q + 1]), pack2<F16>(x[8 * q + 2], x[8 * q + 3]),
-                               pack2<F16>(x[8 * q + 4], x[8 * q + 5]), pack2<F16>(x[8 * q + 6], x[8 * q + 7]));
+        stage_wait(p.lane);
+        stage_row<128>(p.stage, p.lane, v);
+        stage_send(p.stage, p.lane, &a.out, col, p.row - p.lane, false);
     }
 }
 
@@ -256,61 +276,74 @@ __device__ __forceinline__ void put_columns(typename Elem<GT>::T* row, uint32_t 
     }
 }
 
-/* Sums in fp32, or (one split of dweight) the gradient itself. */
+/* Sums in fp32 (of a piece after the first: added in L2, one launch after another), or dweight's
+ * rows of the piece. */
 template <Mode MODE, bool F16>
-__device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid)
+__device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p)
 {
-    const uint32_t rows = MODE == kDhidden ? valid : a.cols;
-    const bool add = MODE == kDhidden && !a.first_piece;
-    const float post = a.head->post;
+    const float post = MODE == kDweight && a.splits == 1 ? a.head->post : 1.0f;
+    const uint32_t row0 = p.row - p.lane;
 #pragma unroll 1
     for (uint32_t c = 0; c < kTileN / 2; c += 32) {
-        const uint32_t in = p.half * (kTileN / 2) + c, col = t.n + in;
-        if (in >= a.tile_n)
+        const uint32_t at = p.half * (kTileN / 2) + c, col = t.n + at;
+        if (at >= t.width || col >= a.dim)
             break;  // the same for the whole warp
         float x[32];
         load_part(p, c, x);
-        if (p.row >= rows)
-            continue;
-        // tile_n is a multiple of 16: the other half of the 32 may be the next tile's
-        const uint32_t end = t.n + a.tile_n < a.dim ? t.n + a.tile_n : a.dim;
-        if (MODE == kDweight && a.splits == 1) {
+        if (MODE == kDweight && a.dweight) {
             const uint64_t row = a.v0 + p.row;
+            if (p.row >= a.cols)
+                continue;
             if (a.grad_dtype == ZERO_F32)
-                put_columns<ZERO_F32>(static_cast<float*>(a.dweight) + row * a.dim, col, end, post, a.accumulate, a.vec, x);
+                put_columns<ZERO_F32>(static_cast<float*>(a.dweight) + row * a.dim, col, a.dim, post, a.accumulate, a.vec, x);
             else
-                put_columns<F16 ? ZERO_F16 : ZERO_BF16>(static_cast<uint16_t*>(a.dweight) + row * a.dim, col, end, post,
+                put_columns<F16 ? ZERO_F16 : ZERO_BF16>(static_cast<uint16_t*>(a.dweight) + row * a.dim, col, a.dim, post,
                                                         a.accumulate, a.vec, x);
             continue;
         }
-        const uint32_t height = MODE == kDhidden ? a.rows_pad : a.d_stride;
-        float* to = a.sums + ((uint64_t)t.split * height + p.row) * a.dim8;
-        const uint32_t end8 = t.n + a.tile_n < a.dim8 ? t.n + a.tile_n : a.dim8;
+        if (row0 >= (MODE == kDhidden ? a.rows_pad : a.cols))
+            break;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (col + 4 * q >= end8)
-                break;
-            float4* at = reinterpret_cast<float4*>(to + col + 4 * q);
-            float4 v = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-            if (add) {
-                const float4 o = *at;
-                v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
-            }
-            *at = v;
+        for (uint32_t j = 0; j < 32; ++j)
+            x[j] = __fmul_rn(x[j], post);
+        stage_wait(p.lane);
+        if (MODE == kDweight && a.splits == 1 && a.grad_dtype != ZERO_F32) {
+            uint4 v[4];
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q)
+                v[q] = make_uint4(pack2<F16>(x[8 * q], x[8 * q + 1]), pack2<F16>(x[8 * q + 2], x[8 * q + 3]),
+                                  pack2<F16>(x[8 * q + 4], x[8 * q + 5]), pack2<F16>(x[8 * q + 6], x[8 * q + 7]));
+            stage_row<64>(p.stage, p.lane, v);
+        } else {
+            uint4 v[8];
+#pragma unroll
+            for (uint32_t q = 0; q < 8; ++q)
+                v[q] = make_uint4(__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]), __float_as_uint(x[4 * q + 2]),
+                                  __float_as_uint(x[4 * q + 3]));
+            stage_row<128>(p.stage, p.lane, v);
         }
+        const uint32_t first = MODE == kDhidden ? t.split * a.rows_pad : a.splits == 1 ? a.v0 : t.split * a.piece;
+        stage_send(p.stage, p.lane, &a.out, col, first + row0, MODE == kDhidden && !a.first_piece);
     }
 }
 
-/* One product over all its tiles: a block per SM takes tiles in turn.  Warp 0 copies operands
- * in, warp 1 issues the matrix instructions (one thread each), warps 4 to 11 take finished
- * accumulators out while the next tile's are formed in the other half of tensor memory. */
+/* One product over all its tiles: a pair of blocks on every two SMs takes tiles of 256 x 256 in
+ * turn.  Warp 0 copies operands in, warp 1 of the pair's first block issues the matrix
+ * instructions (one elected lane each), warps 4 to 11 take finished accumulators out while the next
+ * tile's are formed in the other half of tensor memory.
+ *
+ * The matrix unit cuts its fp32 sums off instead of rounding them, always toward 0: 256 steps
+ * for a logit of 4,096 terms left the loss 1.5e-5 too small.  The losses therefore take a
+ * logit in parts of 1,024 terms, added up in registers (measured: 4e-6 there, at no cost in
+ * time).  The gradients' sums end in 16 bits and go without. */
 template <Mode MODE, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_constant__ ProductArgs a)
 {
     constexpr bool kAmn = MODE == kDweight, kBmn = MODE == kDhidden || MODE == kDweight;
+    constexpr uint32_t kPart = MODE == kStats ? kSumBlocks : ~0u;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = block_of_pair();
     const uint32_t stages = (smem_addr(raw) + 1023) / 1024 * 1024;
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < kRing; ++s) {
@@ -319,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
         }
         for (uint32_t b = 0; b < 2; ++b) {
             bar_init(smem_addr(&sh.acc_full[b]), 1);
-            bar_init(smem_addr(&sh.acc_empty[b]), kEpilogueWarps);
+            bar_init(smem_addr(&sh.acc_empty[b]), 2 * kEpilogueWarps);
         }
         bar_init(smem_addr(&sh.drain), 1);
         sh.gave_up = 0;
@@ -329,118 +362,172 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
         tmem_alloc(smem_addr(&sh.tmem), 512);
     tmem_fence_before();
     __syncthreads();
+    pair_sync();
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
     volatile uint32_t* gave_up = &sh.gave_up;
     grid_dependency_wait();
     const uint32_t valid = *const_cast<const volatile uint32_t*>(&a.head->valid);
     const Tiles<MODE> tiles(a, valid);
+    const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // what earlier kernels wrote through the generic proxy, for the TMA's reads
         asm volatile("fence.proxy.async.global;" ::: "memory");
         const CUtensorMap* hidden = valid == a.rows ? &a.hidden : &a.gathered;
         const CUtensorMap* ma = MODE == kStats || MODE == kD ? hidden : &a.d;
         const CUtensorMap* mb = MODE == kDweight ? hidden : &a.weight;
-        const uint32_t boxes_b = (tiles.tile_n + 63) / 64, bytes = (2 + boxes_b) * kBoxBytes;
         const uint32_t b0 = MODE == kDweight ? 0 : a.v0;  // weight's rows of the piece
         uint32_t issued = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+        for (uint32_t i = first; ok && i < tiles.total; i += step) {
             const Tile t = tiles.at(i);
+            const uint32_t m = t.m + rank * kRows, n = t.n + rank * (t.width / 2), boxes = (t.width / 2 + 63) / 64;
             for (uint32_t k = t.k0; k < t.k1; ++k, ++issued) {
                 const uint32_t s = issued % kRing, turn = issued / kRing;
-                if (turn && !bar_wait(smem_addr(&sh.empty[s]), (turn - 1) & 1, gave_up)) {
+                if (turn && !warp_wait(smem_addr(&sh.empty[s]), (turn - 1) & 1, gave_up)) {
                     ok = false;
                     break;
                 }
-                const uint32_t bar = smem_addr(&sh.full[s]), to = stages + s * kStageBytes, kk = k * kBlockK;
-                bar_expect(bar, bytes);
-                for (uint32_t j = 0; j < 2; ++j) {
-                    const uint32_t r = t.m + 64 * j;
-                    tma_box(to + j * kBoxBytes, ma, (int)(kAmn ? r : kk), (int)(kAmn ? kk : r), bar);
+                // both blocks' copies count on the first one's barrier
+                const uint32_t bar = of_first(smem_addr(&sh.full[s])), to = stages + s * kStageBytes, kk = k * kBlockK;
+                if (elect_one()) {
+                    if (rank == 0)
+                        bar_expect(smem_addr(&sh.full[s]), 2 * (2 + boxes) * kBoxBytes);
+                    for (uint32_t j = 0; j < 2; ++j) {
+                        const uint32_t r = m + 64 * j;
+                        tma_box(to + j * kBoxBytes, ma, (int)(kAmn ? r : kk), (int)(kAmn ? kk : r), bar);
+                    }
+                    for (uint32_t j = 0; j < boxes; ++j) {
+                        const uint32_t r = n + 64 * j;
+                        tma_box(to + (2 + j) * kBoxBytes, mb, (int)(kBmn ? r : kk), (int)(kBmn ? b0 + kk : b0 + r), bar);
+                    }
                 }
-                for (uint32_t j = 0; j < boxes_b; ++j) {
-                    const uint32_t r = t.n + 64 * j;
-                    tma_box(to + (2 + j) * kBoxBytes, mb, (int)(kBmn ? r : kk), (int)(kBmn ? b0 + kk : b0 + r), bar);
-                }
+                __syncwarp();
             }
         }
         if (!ok) {  // copies still in flight land before the block's shared memory goes
             uint32_t none = 0;
-            for (uint32_t q = issued > kRing ? issued - kRing : 0; q < issued; ++q)
-                bar_wait(smem_addr(&sh.full[q % kRing]), (q / kRing) & 1, &none);
+            if (rank == 0) {
+                for (uint32_t q = issued > kRing ? issued - kRing : 0; q < issued; ++q)
+                    bar_wait(smem_addr(&sh.full[q % kRing]), (q / kRing) & 1, &none);
+            } else {
+                for (const long long t0 = clock64(); clock64() - t0 < 100000000LL;) {
+                }
+            }
         }
-    } else if (warp == 1 && lane == 0) {
-        const uint32_t idesc = instr_desc(F16, kAmn, kBmn, kTileM, tiles.tile_n);
+    } else if (warp == 1 && rank == 0) {
         uint32_t used = 0, buf = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < tiles.total; i += gridDim.x) {
+        for (uint32_t i = first; ok && i < tiles.total; i += step) {
             const Tile t = tiles.at(i);
-            if (t.k0 >= t.k1)
-                continue;
-            const uint32_t b = buf & 1, turn = buf >> 1;
-            if (turn && !bar_wait(smem_addr(&sh.acc_empty[b]), (turn - 1) & 1, gave_up)) {
-                ok = false;
-                break;
-            }
-            tmem_fence_after();
-            for (uint32_t k = t.k0; k < t.k1; ++k, ++used) {
-                const uint32_t s = used % kRing;
-                if (!bar_wait(smem_addr(&sh.full[s]), (used / kRing) & 1, gave_up)) {
+            const uint32_t idesc = instr_desc(F16, kAmn, kBmn, kTileM, t.width);
+            for (uint32_t k = t.k0; ok && k < t.k1; ++buf) {
+                const uint32_t b = buf & 1, turn = buf >> 1, begin = k, end = t.k1 - k > kPart ? k + kPart : t.k1;
+                if (turn && !warp_wait(smem_addr(&sh.acc_empty[b]), (turn - 1) & 1, gave_up)) {
                     ok = false;
                     break;
                 }
                 tmem_fence_after();
-                const uint32_t at = stages + s * kStageBytes;
-                const uint64_t da = operand_desc(at, kAmn), db = operand_desc(at + 2 * kBoxBytes, kBmn);
+                for (; k < end; ++k, ++used) {
+                    const uint32_t s = used % kRing;
+                    if (!warp_wait(smem_addr(&sh.full[s]), (used / kRing) & 1, gave_up)) {
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after();
+                    const uint32_t at = stages + s * kStageBytes;
+                    const uint64_t da = operand_desc(at, kAmn), db = operand_desc(at + 2 * kBoxBytes, kBmn);
+                    if (elect_one()) {
 #pragma unroll
-                for (uint32_t q = 0; q < kBlockK / 16; ++q)
-                    mma_16(tmem + b * kTileN, da + q * k_step(kAmn), db + q * k_step(kBmn), idesc, k > t.k0 || q > 0);
-                mma_commit(smem_addr(&sh.empty[s]));
+                        for (uint32_t q = 0; q < kBlockK / 16; ++q)
+                            mma_pair(tmem + b * kTileN, da + q * k_step(kAmn), db + q * k_step(kBmn), idesc,
+                                     k > begin || q > 0);
+                        mma_commit(smem_addr(&sh.empty[s]));
+                    }
+                    __syncwarp();
+                }
+                if (ok && elect_one())
+                    mma_commit(smem_addr(&sh.acc_full[b]));
+                __syncwarp();
             }
-            if (ok)
-                mma_commit(smem_addr(&sh.acc_full[b]));
-            ++buf;
         }
         if (!ok) {  // matrix instructions in flight finish before tensor memory goes
             uint32_t none = 0;
-            mma_commit(smem_addr(&sh.drain));
+            if (elect_one())
+                mma_commit(smem_addr(&sh.drain));
+            __syncwarp();
             bar_wait(smem_addr(&sh.drain), 0, &none);
         }
     } else if (warp >= 4) {
         const uint32_t quarter = warp & 3;
         uint32_t buf = 0;
-        for (uint32_t i = blockIdx.x; i < tiles.total; i += gridDim.x) {
-            const Tile t = tiles.at(i);
-            Part p;
-            p.half = (warp - 4) / 4;
-            p.row = t.m + quarter * 32 + lane;
-            p.empty = t.k0 >= t.k1;
-            const uint32_t b = buf & 1, turn = buf >> 1;
+        bool ok = true;
+        Part p;
+        p.half = (warp - 4) / 4;
+        p.lane = lane;
+        p.stage = stages + kRing * kStageBytes + (warp - 4) * kOutBytes;
+        auto acquire = [&] {
+            const uint32_t b = buf & 1;
             p.acc = tmem + (quarter * 32 << 16) + b * kTileN + p.half * (kTileN / 2);
-            if (!p.empty) {
-                if (!__all_sync(0xffffffffu, bar_wait(smem_addr(&sh.acc_full[b]), turn & 1, gave_up)))
+            ok = warp_wait(smem_addr(&sh.acc_full[b]), (buf >> 1) & 1, gave_up);
+            tmem_fence_after();
+        };
+        auto release = [&] {
+            tmem_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(of_first(smem_addr(&sh.acc_empty[buf & 1])));
+            ++buf;
+        };
+        for (uint32_t i = first; i < tiles.total; i += step) {
+            const Tile t = tiles.at(i);
+            p.row = t.m + rank * kRows + quarter * 32 + lane;
+            p.empty = t.k0 >= t.k1;
+            if constexpr (MODE == kStats) {
+                float x[4][32];
+                for (uint32_t k = t.k0; k < t.k1; k += kPart) {
+                    acquire();
+                    if (!ok)
+                        break;
+#pragma unroll
+                    for (uint32_t q = 0; q < 4; ++q) {
+                        if (k == t.k0) {
+                            tmem_load32(p.acc + 32 * q, x[q]);
+                        } else {
+                            float y[32];
+                            tmem_load32(p.acc + 32 * q, y);
+#pragma unroll
+                            for (uint32_t j = 0; j < 32; ++j)
+                                x[q][j] = __fadd_rn(x[q][j], y[j]);
+                        }
+                    }
+                    release();
+                }
+                if (!ok)
                     break;
-                tmem_fence_after();
-            }
-            if (MODE == kStats)
-                stats_epilogue<F16>(a, t, p, valid);
-            else if (MODE == kD)
-                d_epilogue<F16>(a, t, p, valid);
-            else
-                sum_epilogue<MODE, F16>(a, t, p, valid);
-            if (!p.empty) {
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(smem_addr(&sh.acc_empty[b]));
-                ++buf;
+                stats_epilogue(a, t, p, valid, x);
+            } else {
+                if (!p.empty) {
+                    acquire();
+                    if (!ok)
+                        break;
+                }
+                if constexpr (MODE == kD)
+                    d_epilogue<F16>(a, t, p, valid);
+                else
+                    sum_epilogue<MODE, F16>(a, t, p);
+                if (!p.empty)
+                    release();
             }
         }
+        if (lane == 0)  // what is on its way out has left shared memory, and is written
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    __syncwarp();
     tmem_fence_before();
     __syncthreads();
+    pair_sync();  // neither block's memory goes while the other may still reach it
     tmem_fence_after();
     if (warp == 2)
         tmem_free(tmem, 512);
@@ -708,22 +795,31 @@ EncodeTiled encoder()
     return f;
 }
 
-bool tensor_map(CUtensorMap* map, const void* p, bool f16, uint64_t cols, uint64_t rows, uint64_t stride)
+bool tensor_map(CUtensorMap* map, const void* p, zero_dtype_t t, uint64_t cols, uint64_t rows, uint64_t stride,
+                uint32_t box_cols, uint32_t box_rows)
 {
-    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride * 2};
-    const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride * dtype_size(t)};
+    const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
+    const CUtensorMapDataType type = t == ZERO_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : t == ZERO_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     return encoder() &&
-           encoder()(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                     const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+           encoder()(map, type, 2, const_cast<void*>(p), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     box_cols * dtype_size(t) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int map_refused()
+{
+    record_cuda_error((int)cudaErrorInvalidValue);
+    return ZERO_ECUDA;
 }
 
 uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
 /* How a call is cut, and where its parts lie in the workspace. */
 struct Plan {
-    uint32_t rows_pad, dim8, piece, pieces, tile_n, splits_h, splits_w;
+    uint32_t rows_pad, dim8, piece, splits_h, splits_w;
     uint64_t token, target, factor, lse, logit, gathered, weight, stats, d, sums_h, sums_w, bytes;
 };
 
@@ -732,18 +828,26 @@ Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
     Plan p;
     p.rows_pad = (uint32_t)up(rows ? rows : 1, kTileM);
     p.dim8 = (uint32_t)up(dim, 8);
-    const uint64_t vp = up(vocab, kTileN);
-    // D of a piece: 64 million elements (128 MB, about the L2) or 8,192 columns, whichever is more
-    uint64_t piece = up((64ull << 20) / p.rows_pad, kTileN);
-    piece = piece < 8192 ? 8192 : piece;
-    p.pieces = (uint32_t)((vp + piece - 1) / piece);
-    p.piece = (uint32_t)up((vp + p.pieces - 1) / p.pieces, kTileN);
-    p.pieces = (uint32_t)((vp + p.piece - 1) / p.piece);
-    const uint32_t nt = (dim + kTileN - 1) / kTileN;
-    p.tile_n = (uint32_t)up((dim + nt - 1) / nt, 16);
+    const uint64_t vp = up(vocab, kTileN), tiles = vp / kTileN, nt = (dim + kTileN - 1) / kTileN;
+    // D of a piece: 64 million elements (128 MB, about the L2) or 8,192 columns, whichever is more.
+    // Within a factor of two above that, the width whose dweight tiles leave the fewest SMs idle
+    // over all pieces (GPT-2 1.5B's head at 8,192 tokens: 32 tiles of 256 take 19 turns of the
+    // 76 pairs of SMs, 7 equal pieces of 29 took 21)
+    uint64_t least = up((64ull << 20) / p.rows_pad, kTileN) / kTileN;
+    least = least < 32 ? 32 : least;
+    uint64_t best = ~0ull, width = tiles;
+    for (uint64_t w = least; w <= 2 * least && w < tiles; ++w) {
+        auto turns = [&](uint64_t n) { return (n * nt + kSms / 2 - 1) / (kSms / 2); };
+        const uint64_t all = tiles / w * turns(w) + turns(tiles % w);
+        if (all < best) {
+            best = all;
+            width = w;
+        }
+    }
+    p.piece = (uint32_t)(width * kTileN);
     // few tiles: the sum is split so that the SMs have work, 8 blocks of 64 at least to a split
     auto splits = [](uint64_t tiles, uint64_t k) {
-        const uint64_t want = tiles >= kSms ? 1 : kSms / tiles, most = k / (8 * kBlockK);
+        const uint64_t want = tiles >= kSms / 2 ? 1 : kSms / 2 / tiles, most = k / (8 * kBlockK);
         return (uint32_t)(want < most ? want : most > 0 ? most : 1);
     };
     p.splits_h = splits((uint64_t)p.rows_pad / kTileM * nt, p.piece);
@@ -835,13 +939,11 @@ int prologue(const Call& c, const Plan& p, ListArgs l, void* dhidden, uint64_t d
     const void* weight = c.dim % 8 ? c.work + p.weight : c.weight;
     memset(&a, 0, sizeof a);
     const uint64_t stride = c.rows > 1 ? c.hidden_stride : p.dim8;
-    if (!tensor_map(&a.gathered, gathered, f16, c.dim, p.rows_pad, p.dim8) ||
-        !tensor_map(&a.weight, weight, f16, c.dim, c.vocab, p.dim8) ||
-        !tensor_map(&a.d, c.work + p.d, f16, p.piece, p.rows_pad, p.piece) ||
-        (direct && c.rows && !tensor_map(&a.hidden, c.hidden, f16, c.dim, c.rows, stride))) {
-        record_cuda_error((int)cudaErrorInvalidValue);
-        return ZERO_ECUDA;
-    }
+    if (!tensor_map(&a.gathered, gathered, c.dtype, c.dim, p.rows_pad, p.dim8, 64, 64) ||
+        !tensor_map(&a.weight, weight, c.dtype, c.dim, c.vocab, p.dim8, 64, 64) ||
+        (l.backward && !tensor_map(&a.d, c.work + p.d, c.dtype, p.piece, p.rows_pad, p.piece, 64, 64)) ||
+        (direct && c.rows && !tensor_map(&a.hidden, c.hidden, c.dtype, c.dim, c.rows, stride, 64, 64)))
+        return map_refused();
     if (!direct || !c.rows)
         a.hidden = a.gathered;
     a.head = head;
@@ -850,14 +952,12 @@ int prologue(const Call& c, const Plan& p, ListArgs l, void* dhidden, uint64_t d
     a.lse = l.lse_out;
     a.target_logit = reinterpret_cast<float*>(c.work + p.logit);
     a.stats = reinterpret_cast<float2*>(c.work + p.stats);
-    a.dd = reinterpret_cast<uint16_t*>(c.work + p.d);
     a.rows = (uint32_t)c.rows;
     a.rows_pad = p.rows_pad;
     a.dim = c.dim;
     a.dim8 = p.dim8;
     a.vocab = c.vocab;
-    a.d_stride = p.piece;
-    a.tile_n = p.tile_n;
+    a.piece = p.piece;
     a.splits = 1;
     // row tiles whose hidden rows (32 MB) stay in L2 while weight passes by
     const uint64_t group = (32ull << 20) / (kTileM * 2ull * p.dim8);
@@ -893,17 +993,20 @@ cudaError_t product(const ProductArgs& a, bool f16, uint64_t tiles, cudaStream_t
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess)
         return e;
-    const uint64_t sms = (uint64_t)sm_count();
+    const uint64_t pairs = (uint64_t)sm_count() / 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles < sms ? tiles : sms));
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 2;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -1022,28 +1125,40 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     if (rc != ZERO_OK)
         return rc;
     a.state_error = st ? &st->error : nullptr;
-    a.dweight = dweight;
     a.grad_dtype = (uint32_t)grad_dtype;
     a.accumulate = accumulate;
     a.vec = dweight && rows_vec(dweight, dim, dim, grad_dtype);
-    const uint64_t mt = p.rows_pad / kTileM, nd_tiles = (dim + p.tile_n - 1) / p.tile_n;
+    // dweight leaves by bulk copies unless it is added to or its rows lie off the 16-byte grid
+    const bool whole = p.splits_w == 1 && dweight;
+    if (whole && (accumulate || !a.vec))
+        a.dweight = dweight;
+    CUtensorMap out_d, out_h, out_w;
+    float *sums_h = reinterpret_cast<float*>(c.work + p.sums_h), *sums_w = reinterpret_cast<float*>(c.work + p.sums_w);
+    if (!tensor_map(&out_d, c.work + p.d, dtype, p.piece, p.rows_pad, p.piece, 64, 32) ||
+        !tensor_map(&out_h, sums_h, ZERO_F32, p.dim8, (uint64_t)p.splits_h * p.rows_pad, p.dim8, 32, 32) ||
+        (whole && !a.dweight && !tensor_map(&out_w, dweight, grad_dtype, dim, vocab, dim, 32, 32)) ||
+        (dweight && !whole &&
+         !tensor_map(&out_w, sums_w, ZERO_F32, p.dim8, (uint64_t)p.splits_w * p.piece, p.dim8, 32, 32)))
+        return map_refused();
+    const uint64_t mt = p.rows_pad / kTileM, nd_tiles = (dim + kTileN - 1) / kTileN;
     cudaError_t e = cudaSuccess;
     for (uint32_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += p.piece) {
         a.v0 = v0;
         a.cols = vocab - v0 < p.piece ? vocab - v0 : p.piece;
         a.first_piece = v0 == 0;
+        a.out = out_d;
         e = product<kD>(a, f16, mt * ((a.cols + kTileN - 1) / kTileN), stream);
         if (e == cudaSuccess && dhidden) {
             a.splits = p.splits_h;
-            a.sums = reinterpret_cast<float*>(c.work + p.sums_h);
+            a.out = out_h;
             e = product<kDhidden>(a, f16, mt * nd_tiles * a.splits, stream);
         }
         if (e == cudaSuccess && dweight) {
             a.splits = p.splits_w;
-            a.sums = reinterpret_cast<float*>(c.work + p.sums_w);
+            a.out = out_w;
             e = product<kDweight>(a, f16, (a.cols + kTileM - 1) / kTileM * nd_tiles * a.splits, stream);
             if (e == cudaSuccess && p.splits_w > 1) {
-                const JoinArgs j{a.head, a.sums, nullptr, dweight, dim, (uint64_t)p.piece * p.dim8, a.cols, v0, dim,
+                const JoinArgs j{a.head, sums_w, nullptr, dweight, dim, (uint64_t)p.piece * p.dim8, a.cols, v0, dim,
                                  p.dim8, p.splits_w, accumulate};
                 e = join(j, a.cols, grad_dtype, a.vec, stream);
             }
@@ -1051,7 +1166,7 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     }
     if (e == cudaSuccess && dhidden && rows) {
         const JoinArgs j{a.head,
-                         reinterpret_cast<const float*>(c.work + p.sums_h),
+                         sums_h,
                          reinterpret_cast<const uint32_t*>(c.work + p.token),
                          dhidden,
                          dhidden_stride,

@@ -1,6 +1,7 @@
 /*
- * tcgen05.cuh -- the matrix unit of sm_103a as head_loss.cu uses it: shared-memory operand
- * tiles brought in by TMA, accumulators in tensor memory, mbarriers with bounded waits.
+ * tcgen05.cuh -- the matrix unit of sm_103a as head_loss.cu uses it: a pair of blocks on two SMs
+ * works on one tile, shared-memory operand tiles brought in by TMA, accumulators in tensor
+ * memory, mbarriers with bounded waits.
  *
  * Operands are 16-bit tiles under the 128-byte swizzle, cut into boxes of 64 rows of 128
  * bytes (8 KB, one TMA copy each):
@@ -38,18 +39,23 @@ __device__ __forceinline__ uint32_t instr_desc(bool f16, bool a_mn, bool b_mn, u
            (m / 16) << 24;
 }
 
-__device__ __forceinline__ void mma_16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+/* One 256 x N x 16 step by the pair of blocks: each holds its 128 rows of A and of D and half of
+ * B's rows, at the same shared and tensor memory addresses; the first block issues. */
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
                  "r"(accumulate)
                  : "memory");
 }
 
-/* Arrives on the mbarrier once every MMA issued so far by this thread has finished. */
+/* Arrives on the mbarrier at this address in both blocks once every MMA issued so far by this
+ * thread has finished. */
 __device__ __forceinline__ void mma_commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -57,14 +63,14 @@ __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence
 
 __device__ __forceinline__ void tmem_alloc(uint32_t smem, uint32_t columns)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem), "r"(columns)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem), "r"(columns)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 
 __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns));
 }
 
 /* 32 columns of the warp's 32 accumulator rows: thread l gets row l. */
@@ -87,12 +93,82 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32])
 }
 
 /* One box at (x: the contiguous dimension, y: the rows); what lies outside the tensor is 0.
- * x is a multiple of 8 elements. */
+ * x is a multiple of 8 elements.  bar: of either block of the pair. */
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
                  : "memory");
+}
+
+/* A warp's finished columns on their way out: written row by row (thread l: row l) under the
+ * swizzle of a tensor map whose box is 32 rows of kBytes, then one bulk copy, which what lies
+ * outside the tensor is cut from.  The lane that issues it also waits before the next one. */
+template <uint32_t kBytes>
+__device__ __forceinline__ void stage_row(uint32_t smem, uint32_t lane, const uint4 (&v)[kBytes / 16])
+{
+    static_assert(kBytes == 128 || kBytes == 64, "the swizzle of 128 or of 64 bytes");
+    const uint32_t turn = kBytes == 128 ? lane & 7 : lane >> 1 & 3;
+#pragma unroll
+    for (uint32_t q = 0; q < kBytes / 16; ++q)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(smem + lane * kBytes + ((q ^ turn) << 4)),
+                     "r"(v[q].x), "r"(v[q].y), "r"(v[q].z), "r"(v[q].w)
+                     : "memory");
+}
+
+__device__ __forceinline__ void stage_wait(uint32_t lane)
+{
+    if (lane == 0)
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+}
+
+__device__ __forceinline__ void stage_send(uint32_t smem, uint32_t lane, const CUtensorMap* map, uint32_t x, uint32_t y,
+                                           bool add)
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        if (add)
+            asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                         "r"(x), "r"(y), "r"(smem)
+                         : "memory");
+        else
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                         "r"(x), "r"(y), "r"(smem)
+                         : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+}
+
+/* A shared address of this block as the pair's first block has it. */
+__device__ __forceinline__ uint32_t of_first(uint32_t addr)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(0));
+    return r;
+}
+
+/* True in one lane of the (converged) warp: the compiler then knows that what the lane issues
+ * has the warp's uniform operands, which a test of the lane's number does not tell it. */
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p;
+}
+
+__device__ __forceinline__ uint32_t block_of_pair()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void pair_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n"
+                 "barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
@@ -100,9 +176,10 @@ __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count)
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
 }
 
+/* On a barrier of either block (of_first). */
 __device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
@@ -110,18 +187,20 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
-/* A wait of at most ~2 s, cut short where another thread of the block has given up. */
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up)
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok;
+}
+
+__device__ __noinline__ bool bar_wait_bounded(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up)
 {
     const long long t0 = clock64();
-    while (true) {
-        uint32_t ok;
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                     : "=r"(ok)
-                     : "r"(bar), "r"(parity)
-                     : "memory");
-        if (ok)
-            return true;
+    while (!bar_done(bar, parity)) {
         if (*gave_up)
             return false;
         if (clock64() - t0 > 4000000000LL) {
@@ -129,11 +208,26 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
             return false;
         }
     }
+    return true;
 }
 
-/* A row-major tensor of 16-bit elements for boxes of 64 x 64.  False where the driver refuses
- * it (the address, the stride and the extents are checked by the callers). */
-bool tensor_map(CUtensorMap* map, const void* p, bool f16, uint64_t cols, uint64_t rows, uint64_t stride);
+/* A wait of at most ~2 s, cut short where another thread of the block has given up. */
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up)
+{
+    return bar_done(bar, parity) || bar_wait_bounded(bar, parity, gave_up);
+}
+
+/* The same by a whole warp, with one answer. */
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile uint32_t* gave_up)
+{
+    return __all_sync(0xffffffffu, bar_wait(bar, parity, gave_up));
+}
+
+/* A row-major tensor of elements of type t, for boxes of box_cols (64 or 128 bytes, the swizzle)
+ * by box_rows.  False where the driver refuses it (the address, the stride and the extents are
+ * checked by the callers). */
+bool tensor_map(CUtensorMap* map, const void* p, zero_dtype_t t, uint64_t cols, uint64_t rows, uint64_t stride,
+                uint32_t box_cols, uint32_t box_rows);
 
 }  // namespace
 }  // namespace zero
