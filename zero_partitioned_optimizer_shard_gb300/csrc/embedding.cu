@@ -241,6 +241,69 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const SortArgs a)
                 make_uint2(key[i], place[i]);
 }
 
+struct Fill {
+    uint4* p;
+    uint64_t n16;
+    uint8_t* tail;
+    uint32_t tail_bytes;
+};
+
+__device__ __forceinline__ void zero_fill(const Fill& f, uint32_t block, uint32_t blocks)
+{
+    for (uint64_t i = (uint64_t)block * blockDim.x + threadIdx.x; i < f.n16; i += (uint64_t)blocks * blockDim.x)
+        f.p[i] = make_uint4(0, 0, 0, 0);
+    if (block == 0 && threadIdx.x < f.tail_bytes)
+        f.tail[threadIdx.x] = 0;
+}
+
+__global__ void __launch_bounds__(512) k_zero_fill(const Fill f)
+{
+    grid_dependency_wait();
+    zero_fill(f, blockIdx.x, gridDim.x);
+}
+
+struct SmallSmem {
+    RankSmem rank;
+    uint2 item[kTile];
+};
+
+/* All passes over at most one tile of tokens, by block 0, while the other blocks write the
+ * table's zeros (sorting 8,192 tokens takes less time than 161 MB of zeros). */
+__global__ void __launch_bounds__(kSortThreads) k_sort_small(const SortArgs a, const uint32_t bits, const Fill f)
+{
+    extern __shared__ uint4 smem[];
+    SmallSmem& sm = *reinterpret_cast<SmallSmem*>(smem);
+    grid_dependency_wait();
+    if (blockIdx.x) {
+        zero_fill(f, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    uint32_t key[kItems], place[kItems], rank[kItems], count;
+#pragma unroll
+    for (uint32_t i = 0; i < kItems; ++i) {
+        const uint2 x = sort_item(a, item_at(i));
+        key[i] = x.x;
+        place[i] = x.y;
+    }
+    for (uint32_t shift = 0; shift < bits; shift += 8) {
+        rank_tile(sm.rank, key, shift, rank, count);
+#pragma unroll
+        for (uint32_t i = 0; i < kItems; ++i)
+            sm.item[sm.rank.base[key[i] >> shift & (kBins - 1)] + rank[i]] = make_uint2(key[i], place[i]);
+        __syncthreads();
+#pragma unroll
+        for (uint32_t i = 0; i < kItems; ++i) {
+            const uint2 x = sm.item[item_at(i)];
+            key[i] = x.x;
+            place[i] = x.y;
+        }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kItems; ++i)
+        if (item_at(i) < a.n)
+            a.to[item_at(i)] = make_uint2(key[i], place[i]);
+}
+
 /* ------------------------------------------------------------------------------------ */
 /* backward: the sums                                                                     */
 /* ------------------------------------------------------------------------------------ */
@@ -331,57 +394,57 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
     }
 }
 
-/* Tokens over several chunks: their partial sums in the order of the chunks.  A block looks
- * at one chunk's last token; 8 warps sum a run of the partials each, over 32 places of the
- * row's piece. */
+/* Tokens over several chunks: their partial sums in the order of the chunks.  A block looks at
+ * the last tokens of 8 chunks; for each that starts in its chunk and goes on, 8 warps sum a run
+ * of the partials each, over 32 places of the row's piece. */
 template <zero_dtype_t GT, bool VEC>
 __global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a)
 {
     __shared__ float part[8][8][33];
+    __shared__ uint32_t owner[8];  // the token, or none
     grid_dependency_wait();
-    const uint32_t chunk = blockIdx.x, end = (chunk + 1) * kPlaces;
-    if (end >= a.n)
-        return;
-    const uint32_t token = a.sorted[end - 1].x;
-    if (token >= a.vocab || a.sorted[end].x != token)
-        return;
-    if (end > kPlaces && a.sorted[end - kPlaces - 1].x == token)
-        return;  // it does not start here
-    const uint32_t chunks = a.last[token] / kPlaces - chunk;  // with a partial in head[]
     const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5, piece = blockIdx.y;
-    const uint32_t each = (chunks + 7) / 8, lo = run * each, hi = lo + each < chunks ? lo + each : chunks;
-    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (run == 0)
-        widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(a.tail + (uint64_t)chunk * a.d, a.d, piece, lane, 32), s);
+    if (lane == 0) {
+        const uint32_t end = (blockIdx.x * 8 + run + 1) * kPlaces;
+        uint32_t token = 0xffffffffu;
+        if (end < a.n) {
+            const uint32_t before = end > kPlaces ? a.sorted[end - kPlaces - 1].x : 0xffffffffu;
+            const uint32_t last = a.sorted[end - 1].x, next = a.sorted[end].x;
+            token = last < a.vocab && next == last && before != last ? last : token;
+        }
+        owner[run] = token;
+    }
+    __syncthreads();
+    for (uint32_t o = 0; o < 8; ++o) {
+        const uint32_t token = owner[o], chunk = blockIdx.x * 8 + o;
+        if (token == 0xffffffffu)
+            continue;
+        const uint32_t chunks = a.last[token] / kPlaces - chunk;  // with a partial in head[]
+        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (run == 0)
+            widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(a.tail + (uint64_t)chunk * a.d, a.d, piece, lane, 32), s);
 #pragma unroll 4
-    for (uint32_t c = lo; c < hi; ++c) {
-        float v[8];
-        widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(a.head + (uint64_t)(chunk + 1 + c) * a.d, a.d, piece, lane, 32), v);
+        for (uint32_t c = run; c < chunks; c += 8) {
+            float v[8];
+            widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(a.head + (uint64_t)(chunk + 1 + c) * a.d, a.d, piece, lane, 32), v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s[j] = __fadd_rn(s[j], v[j]);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            s[j] = __fadd_rn(s[j], v[j]);
+            part[run][j][lane] = s[j];
+        __syncthreads();
+        if (run == 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    s[j] = __fadd_rn(s[j], part[r][j][lane]);
+            put_grad<GT, VEC>(a, token, piece, lane, 32, s);
+        }
+        __syncthreads();
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        part[run][j][lane] = s[j];
-    __syncthreads();
-    if (run)
-        return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int r = 1; r < 8; ++r)
-            s[j] = __fadd_rn(s[j], part[r][j][lane]);
-    put_grad<GT, VEC>(a, token, piece, lane, 32, s);
-}
-
-__global__ void __launch_bounds__(512) k_zero_fill(uint4* p, uint64_t n16, uint8_t* tail, uint32_t bytes)
-{
-    grid_dependency_wait();
-    for (uint64_t i = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n16; i += (uint64_t)gridDim.x * blockDim.x)
-        p[i] = make_uint4(0, 0, 0, 0);
-    if (blockIdx.x == 0 && threadIdx.x < bytes)
-        tail[threadIdx.x] = 0;
 }
 
 /* ------------------------------------------------------------------------------------ */
@@ -436,7 +499,7 @@ cudaError_t sums(const GradArgs& a, cudaStream_t s)
                                dim3(threads), 0, s, a);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(k_embedding_join<GT, VEC>, dim3(chunks, (eights + 31) / 32), dim3(256), 0, s, a);
+    return launch_pdl(k_embedding_join<GT, VEC>, dim3((chunks + 7) / 8, (eights + 31) / 32), dim3(256), 0, s, a);
 }
 
 template <zero_dtype_t DT, zero_dtype_t GT>
@@ -445,16 +508,43 @@ cudaError_t sums(const GradArgs& a, bool vec, cudaStream_t s)
     return vec ? sums<DT, GT, true>(a, s) : sums<DT, GT, false>(a, s);
 }
 
-cudaError_t sort_tokens(const Tokens& tokens, uint32_t n, uint2* buf[2], uint32_t* hist, const uint2*& sorted,
-                        cudaStream_t s)
+Fill fill_of(void* p, uint64_t bytes)
+{
+    const uint64_t n16 = aligned_to(p, 16) ? bytes / 16 : 0;
+    return {static_cast<uint4*>(p), n16, static_cast<uint8_t*>(p) + n16 * 16, (uint32_t)(bytes - n16 * 16)};
+}
+
+/* Zeros over the table's gradient (bytes of it, 0: none) and the tokens' places in order. */
+cudaError_t fill_and_sort(const Tokens& tokens, uint32_t n, void* table, uint64_t bytes, uint2* buf[2], uint32_t* hist,
+                          const uint2*& sorted, cudaStream_t s)
 {
     uint32_t bits = 1;
     while (bits < 32 && tokens.vocab >> bits)
         ++bits;  // of the largest key, vocab itself
     const uint32_t tiles = (n + kTile - 1) / kTile;
-    cudaError_t e = cudaFuncSetAttribute(k_sort_scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(RankSmem));
+    cudaError_t e = cudaSuccess;
+    if (bytes && !aligned_to(table, 16)) {
+        e = cudaMemsetAsync(table, 0, bytes, s);
+        if (e != cudaSuccess)
+            return e;
+        bytes = 0;
+    }
+    const Fill f = fill_of(table, bytes);
+    const uint64_t want = (f.n16 + 4095) / 4096, cap = (uint64_t)sm_count() * 2 - 1;
+    const unsigned fillers = bytes ? (unsigned)(want < cap ? (want ? want : 1) : cap) : 0;
     SortArgs a{tokens, nullptr, buf[0], hist, n, tiles, 0};
-    for (uint32_t turn = 0; a.shift < bits && e == cudaSuccess; a.shift += 8, ++turn) {
+    if (tiles == 1) {
+        e = cudaFuncSetAttribute(k_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SmallSmem));
+        sorted = buf[0];
+        return e != cudaSuccess ? e
+                                : launch_pdl(k_sort_small, dim3(1 + fillers), dim3(kSortThreads), sizeof(SmallSmem), s, a,
+                                             bits, f);
+    }
+    if (fillers)
+        e = launch_pdl(k_zero_fill, dim3(fillers * 2), dim3(512), 0, s, f);
+    if (tiles && e == cudaSuccess)
+        e = cudaFuncSetAttribute(k_sort_scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(RankSmem));
+    for (uint32_t turn = 0; tiles && a.shift < bits && e == cudaSuccess; a.shift += 8, ++turn) {
         a.to = buf[turn & 1];
         e = launch_pdl(k_sort_count, dim3(tiles), dim3(kSortThreads), 0, s, a);
         if (e == cudaSuccess)
@@ -465,16 +555,6 @@ cudaError_t sort_tokens(const Tokens& tokens, uint32_t n, uint2* buf[2], uint32_
     }
     sorted = a.from;
     return e;
-}
-
-cudaError_t zero_fill(void* p, uint64_t bytes, cudaStream_t s)
-{
-    if (!aligned_to(p, 16))
-        return cudaMemsetAsync(p, 0, bytes, s);
-    const uint64_t n16 = bytes / 16;
-    const uint64_t want = (n16 + 511) / 512, cap = (uint64_t)sm_count() * 4;
-    return launch_pdl(k_zero_fill, dim3((unsigned)(want < cap ? (want ? want : 1) : cap)), dim3(512), 0, s,
-                      static_cast<uint4*>(p), n16, static_cast<uint8_t*>(p) + n16 * 16, (uint32_t)(bytes % 16));
 }
 
 }  // namespace
@@ -535,19 +615,13 @@ int zero_embedding_backward(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim,
         overlap(workspace, w.bytes, dout, no) || overlap(workspace, w.bytes, tokens, n_tokens * token_bytes) ||
         overlap(workspace, w.bytes, dtable, nt))
         return ZERO_EINVAL;
-    if (!accumulate) {
-        const int rc = rows_status(zero_fill(dtable, nt, stream));
-        if (rc != ZERO_OK)
-            return rc;
-    }
-    if (n_tokens == 0)
-        return ZERO_OK;
     char* base = static_cast<char*>(workspace);
     uint2* buf[2] = {reinterpret_cast<uint2*>(base + w.sorted[0]), reinterpret_cast<uint2*>(base + w.sorted[1])};
     const uint2* sorted = nullptr;
-    int rc = rows_status(sort_tokens({tokens, token_bytes == 8, vocab}, (uint32_t)n_tokens, buf,
-                                     reinterpret_cast<uint32_t*>(base + w.hist), sorted, stream));
-    if (rc != ZERO_OK)
+    const int rc = rows_status(fill_and_sort({tokens, token_bytes == 8, vocab}, (uint32_t)n_tokens, dtable,
+                                             accumulate ? 0 : nt, buf, reinterpret_cast<uint32_t*>(base + w.hist), sorted,
+                                             stream));
+    if (rc != ZERO_OK || n_tokens == 0)
         return rc;
     const GradArgs a{sorted,
                      reinterpret_cast<uint32_t*>(base + w.last),

@@ -17,6 +17,8 @@ namespace {
 
 constexpr uint32_t kMaxDim = 16384;
 constexpr uint32_t kMaxParts = 608;  // blocks of the backward pass: 4 on each of 152 SMs
+constexpr uint32_t kRing = 4;        // stages of a ring, at most
+constexpr uint32_t kRingWarps = 8;   // forward: warps per block, each with a ring of its own
 
 struct ForwardArgs {
     const void* x;
@@ -43,66 +45,143 @@ __device__ __forceinline__ float row_sum(float x, float* slots, uint32_t n)
     return warp_sum(lane < n / 32 ? slots[lane] : 0.0f);
 }
 
-/* One row per n threads: a warp (blockDim.y rows per block) or the whole block. */
+/* One row of n threads from its chunks: the statistics, and y. */
 template <zero_dtype_t DT, zero_dtype_t PT, int NV, bool VEC>
-__global__ void __launch_bounds__(512) k_layernorm(const ForwardArgs a)
+__device__ __forceinline__ void norm_row(const ForwardArgs& a, uint32_t row, const typename Elem<DT>::Raw (&raw)[NV],
+                                         float (&slots)[2][32], uint32_t k, uint32_t n)
 {
     using T = typename Elem<DT>::T;
     using P = typename Elem<PT>::T;
+    const uint32_t d = a.d;
+    uint64_t s = 0;  // a pair of zeros
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        uint64_t v[4];
+        widen2<DT>(raw[i], v);
+        s = f2_add(s, f2_add(f2_add(v[0], v[1]), f2_add(v[2], v[3])));
+    }
+    const float mean = __fdiv_rn(row_sum(f2_sum(s), slots[0], n), (float)d);
+    const uint64_t mean2 = f2(mean, mean);
+    s = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        uint64_t v[4];
+        widen2<DT>(raw[i], v);
+        if (VEC && elem_of<VEC>(i, 0, k, n) >= d)
+            continue;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint64_t c = f2_sub(v[q], mean2);
+            if constexpr (!VEC) {
+                float c0, c1;
+                f2_split(c, c0, c1);
+                c = f2(elem_of<VEC>(i, 2 * q, k, n) < d ? c0 : 0.0f, elem_of<VEC>(i, 2 * q + 1, k, n) < d ? c1 : 0.0f);
+            }
+            s = f2_fma(c, c, s);
+        }
+    }
+    const float var = __fdiv_rn(row_sum(f2_sum(s), slots[1], n), (float)d);
+    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+    if (k == 0 && a.mean)
+        a.mean[row] = mean;
+    if (k == 0 && a.rstd)
+        a.rstd[row] = rstd;
+    const uint64_t rstd2 = f2(rstd, rstd);
+    T* y = static_cast<T*>(a.y) + (uint64_t)row * a.y_stride;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        uint64_t v[4], w[4], b[4] = {0, 0, 0, 0};
+        widen2<DT>(raw[i], v);
+        widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), d, i, k, n), w);
+        if (a.bias)
+            widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), d, i, k, n), b);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            v[q] = f2_fma(f2_mul(f2_sub(v[q], mean2), rstd2), w[q], b[q]);
+        float out[8];
+        split4(v, out);
+        store_chunk<DT, VEC>(y, d, i, k, n, out);
+    }
+}
+
+/* One row per n threads: a warp (blockDim.y rows per block) or the whole block. */
+template <zero_dtype_t DT, zero_dtype_t PT, int NV, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
+{
+    using T = typename Elem<DT>::T;
     __shared__ float slots[2][32];
     grid_dependency_wait();
-    const uint32_t n = blockDim.x, k = threadIdx.x, d = a.d;
-    const uint32_t row = blockIdx.x * blockDim.y + threadIdx.y;
+    const uint32_t n = blockDim.x, k = threadIdx.x, row = blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= a.rows)
         return;
     const T* x = static_cast<const T*>(a.x) + (uint64_t)row * a.x_stride;
     typename Elem<DT>::Raw raw[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        raw[i] = load_chunk<DT, VEC>(x, d, i, k, n);
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float v[8];
-        widen<DT>(raw[i], v);
-        s = __fadd_rn(s, __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3])),
-                                   __fadd_rn(__fadd_rn(v[4], v[5]), __fadd_rn(v[6], v[7]))));
+        raw[i] = load_chunk<DT, VEC>(x, a.d, i, k, n);
+    norm_row<DT, PT, NV, VEC>(a, row, raw, slots, k, n);
+}
+
+/* A warp per row, many rows to a warp: lane 0 bulk-copies the warp's next rows into a ring of
+ * its own, so that they are on their way while one is worked on. */
+template <zero_dtype_t DT, zero_dtype_t PT, int NV>
+__global__ void __launch_bounds__(32 * kRingWarps) k_layernorm_staged(const ForwardArgs a, const uint32_t stages)
+{
+    using T = typename Elem<DT>::T;
+    extern __shared__ uint4 rings[];
+    __shared__ uint64_t full[kRingWarps][kRing];
+    __shared__ float slots[2][32];  // not used by single warps
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, d = a.d, row_bytes = d * sizeof(T);
+    if (lane == 0) {
+        for (uint32_t q = 0; q < stages; ++q)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[warp][q])));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    const float mean = __fdiv_rn(row_sum(s, slots[0], n), (float)d);
-    s = 0.0f;
+    __syncwarp();
+    grid_dependency_wait();
+    const uint4* ring = rings + (uint64_t)warp * stages * row_bytes / 16;
+    const uint64_t first = blockIdx.x * kRingWarps + warp, step = gridDim.x * kRingWarps;
+    auto fetch = [&](uint32_t turn) {
+        const uint64_t row = first + turn * step;
+        if (row >= a.rows)
+            return;
+        const uint32_t q = turn % stages, bar = smem_addr(&full[warp][q]);
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(row_bytes) : "memory");
+        bulk_load<false>(smem_addr(ring) + q * row_bytes, static_cast<const T*>(a.x) + row * a.x_stride, row_bytes, bar);
+    };
+    if (lane == 0)
+        for (uint32_t q = 0; q < stages; ++q)
+            fetch(q);
+    uint32_t turn = 0;
+    for (uint64_t row = first; row < a.rows; row += step, ++turn) {
+        const uint32_t q = turn % stages;
+        const bool ok = __all_sync(0xffffffffu, wait_parity_bounded(smem_addr(&full[warp][q]), turn / stages & 1));
+        const uint4* at = ring + q * row_bytes / 16;
+        typename Elem<DT>::Raw raw[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float v[8];
-        widen<DT>(raw[i], v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float c = elem_of<VEC>(i, j, k, n) < d ? __fsub_rn(v[j], mean) : 0.0f;
-            s = __fmaf_rn(c, c, s);
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t c = i * 32 + lane;
+            raw[i] = {};
+            if (c * 8 < d) {
+                if constexpr (DT == ZERO_F32)
+                    raw[i].a = as_f4(at[2 * c]), raw[i].b = as_f4(at[2 * c + 1]);
+                else
+                    raw[i].v = at[c];
+            }
         }
-    }
-    const float var = __fdiv_rn(row_sum(s, slots[1], n), (float)d);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
-    if (k == 0 && a.mean)
-        a.mean[row] = mean;
-    if (k == 0 && a.rstd)
-        a.rstd[row] = rstd;
-    T* y = static_cast<T*>(a.y) + (uint64_t)row * a.y_stride;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        float v[8], w[8], b[8];
-        widen<DT>(raw[i], v);
-        widen<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), d, i, k, n), w);
-        if (a.bias) {
-            widen<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), d, i, k, n), b);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                b[j] = 0.0f;
+        __syncwarp();  // the stage has been read
+        if (!ok) {     // a copy did not arrive within 2 s: this row and the warp's later ones tell, as NaN
+            if (lane == 0)
+                for (uint32_t t = turn; t < turn + stages && first + t * step < a.rows; ++t)
+                    wait_parity_bounded(smem_addr(&full[warp][t % stages]), t / stages & 1);
+            for (; row < a.rows; row += step)
+                for (uint32_t c = lane; c < d; c += 32)
+                    static_cast<T*>(a.y)[row * a.y_stride + c] = from_f32<DT>(__int_as_float(0x7fc00000));
+            return;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            v[j] = __fmaf_rn(__fmul_rn(__fsub_rn(v[j], mean), rstd), w[j], b[j]);
-        store_chunk<DT, VEC>(y, d, i, k, n, v);
+        if (lane == 0)
+            fetch(turn + stages);
+        norm_row<DT, PT, NV, true>(a, (uint32_t)row, raw, slots, lane, 32);
     }
 }
 
@@ -118,33 +197,117 @@ struct BackwardArgs {
     uint32_t rows, d;
 };
 
-/* R rows at a time per block; a thread keeps its columns' sums over the block's rows. */
-template <zero_dtype_t DT, zero_dtype_t PT, int NV, int R, bool VEC>
-__global__ void __launch_bounds__(1024) k_layernorm_backward(const BackwardArgs a)
+/* What a thread keeps over all its block's rows: the weights of its columns, and their sums; in
+ * pairs of neighbours. */
+template <int NV>
+struct Columns {
+    uint64_t w[NV][4], dw[NV][4], db[NV][4];
+
+    template <zero_dtype_t PT, bool VEC>
+    __device__ __forceinline__ void begin(const BackwardArgs& a, uint32_t k, uint32_t n)
+    {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            widen2<PT>(load_chunk<PT, VEC>(static_cast<const typename Elem<PT>::T*>(a.weight), a.d, i, k, n), w[i]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                dw[i][q] = db[i][q] = 0;
+        }
+    }
+
+    /* A chunk of a row into the columns' sums and the row's two, of g and of g * xh, which stay.
+     * Past the row's end dy is 0; xh is finite there where the row's statistics are. */
+    template <zero_dtype_t DT>
+    __device__ __forceinline__ void add(int i, const typename Elem<DT>::Raw& x, const typename Elem<DT>::Raw& dy,
+                                        float mean, float rstd, uint64_t (&xh)[4], uint64_t (&g)[4], uint64_t& sg,
+                                        uint64_t& sx)
+    {
+        const uint64_t mean2 = f2(mean, mean), rstd2 = f2(rstd, rstd);
+        widen2<DT>(x, xh);
+        widen2<DT>(dy, g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            xh[q] = f2_mul(f2_sub(xh[q], mean2), rstd2);
+            dw[i][q] = f2_fma(g[q], xh[q], dw[i][q]);
+            db[i][q] = f2_add(db[i][q], g[q]);
+            g[q] = f2_mul(g[q], w[i][q]);
+            sg = f2_add(sg, g[q]);
+            sx = f2_fma(g[q], xh[q], sx);
+        }
+    }
+
+    template <bool VEC>
+    __device__ __forceinline__ void end(const BackwardArgs& a, uint32_t k, uint32_t n) const
+    {
+        float* mine = a.parts + (uint64_t)blockIdx.x * 2 * a.d;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float v[8];
+            split4(dw[i], v);
+            store_chunk<ZERO_F32, VEC>(mine, a.d, i, k, n, v);
+            split4(db[i], v);
+            store_chunk<ZERO_F32, VEC>(mine + a.d, a.d, i, k, n, v);
+        }
+    }
+};
+
+/* A chunk's dx = rstd * (g - c1 - xh * c2), from the row's two sums over d. */
+template <zero_dtype_t DT, bool VEC>
+__device__ __forceinline__ void put_dx(int i, typename Elem<DT>::T* dx, uint32_t d, uint32_t k, uint32_t n,
+                                       const uint64_t (&xh)[4], const uint64_t (&g)[4], float rstd, float c1, float c2)
+{
+    const uint64_t rstd2 = f2(rstd, rstd), less1 = f2(c1, c1), less2 = f2(-c2, -c2);
+    uint64_t v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        v[q] = f2_mul(rstd2, f2_fma(xh[q], less2, f2_sub(g[q], less1)));
+    float out[8];
+    split4(v, out);
+    store_chunk<DT, VEC>(dx, d, i, k, n, out);
+}
+
+/* Sums of N values over the block; slots are of this turn, so one barrier is enough. */
+template <int N>
+__device__ __forceinline__ void block_sums(float (&s)[N], float (&slots)[N][32], uint32_t n)
+{
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        s[q] = warp_sum(s[q]);
+    if (n == 32)
+        return;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) {
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+            slots[q][warp] = s[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+        s[q] = warp_sum(lane < n / 32 ? slots[q][lane] : 0.0f);
+}
+
+/* R rows at a time per block, straight from global memory: rows that the bulk copies do not
+ * take, and the longest. */
+template <zero_dtype_t DT, zero_dtype_t PT, int NV, int R, bool VEC, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs a)
 {
     using T = typename Elem<DT>::T;
-    using P = typename Elem<PT>::T;
     __shared__ float slots[2][2 * R][32];
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint32_t n = blockDim.x, k = threadIdx.x, d = a.d, warp = k >> 5, lane = k & 31;
-    float w[NV][8], dw[NV][8], db[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        widen<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), d, i, k, n), w[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            dw[i][j] = db[i][j] = 0.0f;
-    }
+    const uint32_t n = blockDim.x, k = threadIdx.x, d = a.d;
+    Columns<NV> c;
+    c.template begin<PT, VEC>(a, k, n);
     const float inv_d = __fdiv_rn(1.0f, (float)d);
     uint32_t turn = 0;
     for (uint32_t row0 = blockIdx.x * R; row0 < a.rows; row0 += gridDim.x * R, turn ^= 1) {
         typename Elem<DT>::Raw x[R][NV], dy[R][NV];
-        float mean[R], rstd[R];
+        uint64_t xh[R][NV][4], g[R][NV][4];
+        float mean[R], rstd[R], s[2 * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint32_t row = row0 + r;
-            const uint32_t len = row < a.rows ? d : 0;
+            const uint32_t row = row0 + r, len = row < a.rows ? d : 0;
             mean[r] = len ? a.mean[row] : 0.0f;
             rstd[r] = len ? a.rstd[row] : 0.0f;
 #pragma unroll
@@ -153,68 +316,132 @@ __global__ void __launch_bounds__(1024) k_layernorm_backward(const BackwardArgs 
                 dy[r][i] = load_chunk<DT, VEC>(static_cast<const T*>(a.dy) + (uint64_t)row * a.dy_stride, len, i, k, n);
             }
         }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint64_t sg = 0, sx = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                c.template add<DT>(i, x[r][i], dy[r][i], mean[r], rstd[r], xh[r][i], g[r][i], sg, sx);
+            s[2 * r] = f2_sum(sg);
+            s[2 * r + 1] = f2_sum(sx);
+        }
+        block_sums(s, slots[turn], n);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row0 + r >= a.rows)
+                break;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                put_dx<DT, VEC>(i, static_cast<T*>(a.dx) + (uint64_t)(row0 + r) * a.dx_stride, d, k, n, xh[r][i], g[r][i],
+                                rstd[r], __fmul_rn(s[2 * r], inv_d), __fmul_rn(s[2 * r + 1], inv_d));
+        }
+    }
+    c.template end<VEC>(a, k, n);
+}
+
+/* The same through a ring of stages of R rows of x and dy, bulk-copied ahead by thread 0: the
+ * rows of the next turns are on their way while one is worked on, without registers. */
+template <zero_dtype_t DT, zero_dtype_t PT, int R, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_layernorm_backward_staged(const BackwardArgs a, const uint32_t stages)
+{
+    using T = typename Elem<DT>::T;
+    extern __shared__ uint4 ring[];
+    __shared__ float slots[2][2 * R][32];
+    __shared__ uint64_t full[kRing];
+    const uint32_t n = blockDim.x, k = threadIdx.x, d = a.d, row_bytes = d * sizeof(T);
+    if (k == 0) {
+        for (uint32_t q = 0; q < stages; ++q)
+            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[q])));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    auto fetch = [&](uint32_t turn) {
+        const uint64_t row0 = ((uint64_t)turn * gridDim.x + blockIdx.x) * R;
+        if (row0 >= a.rows)
+            return;
+        const uint32_t rows = a.rows - row0 < R ? (uint32_t)(a.rows - row0) : R, q = turn % stages;
+        const uint32_t bar = smem_addr(&full[q]), to = smem_addr(ring) + q * 2 * R * row_bytes;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(2 * rows * row_bytes)
+                     : "memory");
+        for (uint32_t r = 0; r < rows; ++r) {
+            bulk_load<false>(to + 2 * r * row_bytes, static_cast<const T*>(a.x) + (row0 + r) * a.x_stride, row_bytes, bar);
+            bulk_load<false>(to + (2 * r + 1) * row_bytes, static_cast<const T*>(a.dy) + (row0 + r) * a.dy_stride,
+                             row_bytes, bar);
+        }
+    };
+    if (k == 0)
+        for (uint32_t q = 0; q < stages; ++q)
+            fetch(q);
+    Columns<1> c;
+    c.template begin<PT, true>(a, k, n);
+    const float inv_d = __fdiv_rn(1.0f, (float)d);
+    const bool in = k * 8 < d;
+    float mean[R], rstd[R];
+    auto statistics = [&](uint64_t row0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] = row0 + r < a.rows ? a.mean[row0 + r] : 0.0f;
+            rstd[r] = row0 + r < a.rows ? a.rstd[row0 + r] : 0.0f;
+        }
+    };
+    statistics((uint64_t)blockIdx.x * R);
+    bool gave_up = false;
+    uint32_t turn = 0;
+    for (uint64_t row0 = (uint64_t)blockIdx.x * R; row0 < a.rows; row0 += (uint64_t)gridDim.x * R, ++turn) {
+        const uint32_t q = turn % stages;
+        const bool ok = wait_parity_bounded(smem_addr(&full[q]), turn / stages & 1);
+        const uint4* stage = ring + (uint64_t)q * 2 * R * row_bytes / 16;
+        uint64_t xh[R][4], g[R][4];
         float s[2 * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            s[2 * r] = s[2 * r + 1] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float xv[8], dv[8];
-                widen<DT>(x[r][i], xv);
-                widen<DT>(dy[r][i], dv);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    // places past the row's end hold dy = 0, and xh must not make a NaN of it
-                    const bool in = VEC ? (i * n + k) * 8 < d : elem_of<VEC>(i, j, k, n) < d;
-                    const float xh = in ? __fmul_rn(__fsub_rn(xv[j], mean[r]), rstd[r]) : 0.0f;
-                    const float g = __fmul_rn(dv[j], w[i][j]);
-                    s[2 * r] = __fadd_rn(s[2 * r], g);
-                    s[2 * r + 1] = __fmaf_rn(g, xh, s[2 * r + 1]);
-                    dw[i][j] = __fmaf_rn(dv[j], xh, dw[i][j]);
-                    db[i][j] = __fadd_rn(db[i][j], dv[j]);
+            typename Elem<DT>::Raw x = {}, dy = {};
+            if (in && row0 + r < a.rows) {
+                const uint4 *px = stage + 2 * r * row_bytes / 16, *py = px + row_bytes / 16;
+                if constexpr (DT == ZERO_F32) {
+                    x.a = as_f4(px[2 * k]), x.b = as_f4(px[2 * k + 1]);
+                    dy.a = as_f4(py[2 * k]), dy.b = as_f4(py[2 * k + 1]);
+                } else {
+                    x.v = px[k];
+                    dy.v = py[k];
                 }
             }
+            uint64_t sg = 0, sx = 0;
+            c.template add<DT>(0, x, dy, mean[r], rstd[r], xh[r], g[r], sg, sx);
+            s[2 * r] = f2_sum(sg);
+            s[2 * r + 1] = f2_sum(sx);
         }
+        float rs[R];
 #pragma unroll
-        for (int q = 0; q < 2 * R; ++q)
-            s[q] = warp_sum(s[q]);
-        if (n > 32) {
-            if (lane == 0) {
-#pragma unroll
-                for (int q = 0; q < 2 * R; ++q)
-                    slots[turn][q][warp] = s[q];
-            }
-            __syncthreads();  // the other set of slots is written next: one barrier a turn
-#pragma unroll
-            for (int q = 0; q < 2 * R; ++q)
-                s[q] = warp_sum(lane < n / 32 ? slots[turn][q][lane] : 0.0f);
+        for (int r = 0; r < R; ++r)
+            rs[r] = rstd[r];
+        statistics(row0 + (uint64_t)gridDim.x * R);  // of the next turn
+        if (__syncthreads_or(!ok)) {                 // and: this stage has been read by everyone
+            gave_up = true;
+            break;
         }
+        if (k == 0)
+            fetch(turn + stages);
+        block_sums(s, slots[turn & 1], n);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const uint32_t row = row0 + r;
-            if (row >= a.rows)
+            if (row0 + r >= a.rows)
                 break;
-            const float c1 = __fmul_rn(s[2 * r], inv_d), c2 = __fmul_rn(s[2 * r + 1], inv_d);
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                float xv[8], dv[8];
-                widen<DT>(x[r][i], xv);
-                widen<DT>(dy[r][i], dv);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float xh = __fmul_rn(__fsub_rn(xv[j], mean[r]), rstd[r]);
-                    xv[j] = __fmul_rn(rstd[r], __fmaf_rn(-xh, c2, __fsub_rn(__fmul_rn(dv[j], w[i][j]), c1)));
-                }
-                store_chunk<DT, VEC>(static_cast<T*>(a.dx) + (uint64_t)row * a.dx_stride, d, i, k, n, xv);
-            }
+            put_dx<DT, true>(0, static_cast<T*>(a.dx) + (row0 + r) * a.dx_stride, d, k, n, xh[r], g[r], rs[r],
+                             __fmul_rn(s[2 * r], inv_d), __fmul_rn(s[2 * r + 1], inv_d));
         }
     }
-    float* mine = a.parts + (uint64_t)blockIdx.x * 2 * d;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        store_chunk<ZERO_F32, VEC>(mine, d, i, k, n, dw[i]);
-        store_chunk<ZERO_F32, VEC>(mine + d, d, i, k, n, db[i]);
+    if (gave_up) {  // a copy did not arrive within 2 s: the weights' gradients tell, as NaN
+        if (k == 0)
+            for (uint32_t t = turn; t < turn + stages; ++t)  // the others are let land
+                if (((uint64_t)t * gridDim.x + blockIdx.x) * R < a.rows)
+                    wait_parity_bounded(smem_addr(&full[t % stages]), t / stages & 1);
+        __syncthreads();
+        c.dw[0][0] = c.db[0][0] = f2(__int_as_float(0x7fc00000), 0.0f);
     }
+    c.template end<true>(a, k, n);
 }
 
 struct JoinArgs {
@@ -225,29 +452,27 @@ struct JoinArgs {
     uint32_t dtype, accumulate;
 };
 
-/* The blocks' sums of one column, in the order of the blocks: 32 columns by 8 runs of parts
- * per block. */
-__global__ void __launch_bounds__(256) k_layernorm_join(const JoinArgs a)
+/* The blocks' sums of one column: 32 columns by 32 runs of parts per block, in a fixed order. */
+__global__ void __launch_bounds__(1024) k_layernorm_join(const JoinArgs a)
 {
-    __shared__ float part[8][33];
+    __shared__ float part[32][33];
     grid_dependency_wait();
     const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5;
-    const uint32_t col = blockIdx.x * 32 + lane, n = 2 * a.d;
+    uint32_t col = blockIdx.x * 32 + lane;
+    const uint32_t n = 2 * a.d;
     float s = 0.0f;
     if (col < n) {
-        const uint32_t each = (a.n_parts + 7) / 8, lo = run * each;
-        const uint32_t hi = lo + each < a.n_parts ? lo + each : a.n_parts;
-#pragma unroll 8
-        for (uint32_t p = lo; p < hi; ++p)
+#pragma unroll 10
+        for (uint32_t p = run; p < a.n_parts; p += 32)
             s = __fadd_rn(s, a.parts[(uint64_t)p * n + col]);
     }
     part[run][lane] = s;
     __syncthreads();
-    if (run || col >= n)
+    // a warp per column now: its 32 runs
+    s = warp_sum(part[lane][run]);
+    col = blockIdx.x * 32 + run;
+    if (lane || col >= n)
         return;
-#pragma unroll
-    for (int r = 1; r < 8; ++r)
-        s = __fadd_rn(s, part[r][lane]);
     void* out = col < a.d ? a.dweight : a.dbias;
     if (!out)
         return;
@@ -264,42 +489,101 @@ __global__ void __launch_bounds__(256) k_layernorm_join(const JoinArgs a)
     }
 }
 
+/* Blocks of a kernel that fit on the current device at once. */
+template <typename K>
+cudaError_t resident(K kernel, uint32_t threads, size_t smem, uint32_t& blocks)
+{
+    int per_sm = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)threads, smem);
+    blocks = (uint32_t)(sm_count() * (per_sm > 0 ? per_sm : 1));
+    return e;
+}
+
 template <zero_dtype_t DT, zero_dtype_t PT, bool VEC>
 cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
 {
     // a warp per row up to 2,048 elements (no barrier), then 128 and 512 threads
     const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 256 ? 32 : chunks <= 1024 ? 128 : 512;
     const uint32_t per = (chunks + n - 1) / n, rows = n == 32 ? 4 : 1;
-    const dim3 grid((a.rows + rows - 1) / rows), block(n, rows);
-    if (per <= 1)
-        return launch_pdl(k_layernorm<DT, PT, 1, VEC>, grid, block, 0, s, a);
-    if (per <= 2)
-        return launch_pdl(k_layernorm<DT, PT, 2, VEC>, grid, block, 0, s, a);
-    if (per <= 4)
-        return launch_pdl(k_layernorm<DT, PT, 4, VEC>, grid, block, 0, s, a);
-    return launch_pdl(k_layernorm<DT, PT, 8, VEC>, grid, block, 0, s, a);
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((a.rows + rows - 1) / rows), dim3(n, rows), 0, s, a);
+    };
+    if constexpr (VEC) {
+        if (n == 32) {
+            const uint32_t row_bytes = a.d * (uint32_t)sizeof(typename Elem<DT>::T);
+            uint32_t stages = 16384 / row_bytes;
+            stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
+            const size_t smem = (size_t)kRingWarps * stages * row_bytes;
+            auto staged = [&](auto kernel, bool& taken) {
+                uint32_t fit = 0;
+                cudaError_t e =
+                    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (e == cudaSuccess)
+                    e = resident(kernel, 32 * kRingWarps, smem, fit);
+                taken = e == cudaSuccess && a.rows > fit * kRingWarps;  // several rows to a warp
+                return taken ? launch_pdl(kernel, dim3(fit), dim3(32 * kRingWarps), smem, s, a, stages) : e;
+            };
+            bool taken = false;
+            const cudaError_t e = per <= 1   ? staged(k_layernorm_staged<DT, PT, 1>, taken)
+                                  : per <= 2 ? staged(k_layernorm_staged<DT, PT, 2>, taken)
+                                  : per <= 4 ? staged(k_layernorm_staged<DT, PT, 4>, taken)
+                                             : staged(k_layernorm_staged<DT, PT, 8>, taken);
+            if (taken || e != cudaSuccess)
+                return e;
+        }
+    }
+    if (n == 512)
+        return per <= 2 ? go(k_layernorm<DT, PT, 2, VEC, 512>) : go(k_layernorm<DT, PT, 4, VEC, 512>);
+    return per <= 1   ? go(k_layernorm<DT, PT, 1, VEC, 128>)
+           : per <= 2 ? go(k_layernorm<DT, PT, 2, VEC, 128>)
+           : per <= 4 ? go(k_layernorm<DT, PT, 4, VEC, 128>)
+                      : go(k_layernorm<DT, PT, 8, VEC, 128>);
 }
 
 template <zero_dtype_t DT, zero_dtype_t PT, bool VEC>
 cudaError_t backward(const BackwardArgs& a, uint32_t& parts, cudaStream_t s)
 {
-    constexpr int R = DT == ZERO_F32 ? 2 : 4;
     const uint32_t chunks = (a.d + 7) / 8;
     const uint32_t n = chunks <= 1024 ? (chunks + 31) / 32 * 32 : 1024;
-    auto go = [&](auto kernel, int rows) {
-        int per_sm = 0;
-        cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)n, 0);
-        if (e != cudaSuccess)
-            return e;
-        uint32_t grid = (uint32_t)(sm_count() * (per_sm > 0 ? per_sm : 1));
-        grid = grid < kMaxParts ? grid : kMaxParts;
+    auto blocks = [&](auto kernel, uint32_t rows, size_t smem) {
+        uint32_t fit = 0;
+        cudaError_t e = cudaSuccess;
+        if (smem)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e == cudaSuccess)
+            e = resident(kernel, n, smem, fit);
+        fit = fit < kMaxParts ? fit : kMaxParts;
         const uint32_t want = (a.rows + rows - 1) / rows;
-        parts = grid < want ? grid : want;
-        return launch_pdl(kernel, dim3(parts), dim3(n), 0, s, a);
+        parts = fit < want ? fit : want;
+        return e;
     };
+    auto go = [&](auto kernel, uint32_t rows) {
+        const cudaError_t e = blocks(kernel, rows, 0);
+        return e != cudaSuccess ? e : launch_pdl(kernel, dim3(parts), dim3(n), 0, s, a);
+    };
+    if constexpr (VEC) {
+        auto staged = [&](auto kernel, uint32_t rows) {
+            // a ring of up to 48 KB: two blocks and more to an SM
+            const uint32_t stage = 2 * rows * a.d * (uint32_t)sizeof(typename Elem<DT>::T);
+            uint32_t stages = 49152 / stage;
+            stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
+            const cudaError_t e = blocks(kernel, rows, (size_t)stages * stage);
+            return e != cudaSuccess ? e
+                                    : launch_pdl(kernel, dim3(parts), dim3(n), (size_t)stages * stage, s, a, stages);
+        };
+        if (chunks <= 256)
+            return staged(k_layernorm_backward_staged<DT, PT, 2, 256>, 2);
+        if (chunks <= 1024)
+            return staged(k_layernorm_backward_staged<DT, PT, 1, 1024>, 1);
+    }
     if (chunks > 1024)
-        return go(k_layernorm_backward<DT, PT, 2, 1, VEC>, 1);
-    return go(k_layernorm_backward<DT, PT, 1, R, VEC>, R);
+        return go(k_layernorm_backward<DT, PT, 2, 1, VEC, 1024>, 1);
+    if constexpr (!VEC) {
+        if (chunks <= 256)
+            return go(k_layernorm_backward<DT, PT, 1, 2, VEC, 256>, 2);
+        return go(k_layernorm_backward<DT, PT, 1, 1, VEC, 1024>, 1);
+    }
+    return cudaErrorInvalidValue;
 }
 
 /* Calls f with the types and the layout as template arguments. */
@@ -434,7 +718,7 @@ int zero_layernorm_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, con
     if (!dweight && !dbias)
         return ZERO_OK;
     const JoinArgs j{static_cast<const float*>(workspace), dweight, dbias, parts, dim, (uint32_t)grad_dtype, accumulate};
-    return rows_status(launch_pdl(k_layernorm_join, dim3((2 * dim + 31) / 32), dim3(256), 0, stream, j));
+    return rows_status(launch_pdl(k_layernorm_join, dim3((2 * dim + 31) / 32), dim3(1024), 0, stream, j));
 }
 
 }  // extern "C"

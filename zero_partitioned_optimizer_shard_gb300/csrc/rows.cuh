@@ -41,6 +41,34 @@ __device__ __forceinline__ float to_f32(typename Elem<DT>::T x)
         return one16<DT>(x);
 }
 
+/* A chunk as 4 pairs of neighbours, for the paired fp32 arithmetic. */
+template <zero_dtype_t DT>
+__device__ __forceinline__ void widen2(const typename Elem<DT>::Raw& r, uint64_t (&x)[4])
+{
+    if constexpr (DT == ZERO_F32) {
+        x[0] = f2(r.a.x, r.a.y), x[1] = f2(r.a.z, r.a.w), x[2] = f2(r.b.x, r.b.y), x[3] = f2(r.b.z, r.b.w);
+    } else {
+        const uint32_t w[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            x[q] = f2(lo16<DT>(w[q]), hi16<DT>(w[q]));
+    }
+}
+
+__device__ __forceinline__ void split4(const uint64_t (&p)[4], float (&x)[8])
+{
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        f2_split(p[q], x[2 * q], x[2 * q + 1]);
+}
+
+__device__ __forceinline__ float f2_sum(uint64_t p)
+{
+    float a, b;
+    f2_split(p, a, b);
+    return __fadd_rn(a, b);
+}
+
 /* Rounded to nearest even: the one rounding of an operator's 16-bit output. */
 template <zero_dtype_t DT>
 __device__ __forceinline__ typename Elem<DT>::T from_f32(float x)
