@@ -45,13 +45,13 @@ __device__ __forceinline__ float row_sum(float x, float* slots, uint32_t n)
     return warp_sum(lane < n / 32 ? slots[lane] : 0.0f);
 }
 
-/* One row of n threads from its chunks: the statistics, and y. */
-template <zero_dtype_t DT, zero_dtype_t PT, int NV, bool VEC>
+/* One row of n threads from its chunks: the statistics, and y.  params(i, w, b) gives chunk i's
+ * weights and biases. */
+template <zero_dtype_t DT, int NV, bool VEC, typename Params>
 __device__ __forceinline__ void norm_row(const ForwardArgs& a, uint32_t row, const typename Elem<DT>::Raw (&raw)[NV],
-                                         float (&slots)[2][32], uint32_t k, uint32_t n)
+                                         float (&slots)[2][32], uint32_t k, uint32_t n, Params params)
 {
     using T = typename Elem<DT>::T;
-    using P = typename Elem<PT>::T;
     const uint32_t d = a.d;
     uint64_t s = 0;  // a pair of zeros
 #pragma unroll
@@ -90,11 +90,9 @@ __device__ __forceinline__ void norm_row(const ForwardArgs& a, uint32_t row, con
     T* y = static_cast<T*>(a.y) + (uint64_t)row * a.y_stride;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        uint64_t v[4], w[4], b[4] = {0, 0, 0, 0};
+        uint64_t v[4], w[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
         widen2<DT>(raw[i], v);
-        widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), d, i, k, n), w);
-        if (a.bias)
-            widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), d, i, k, n), b);
+        params(i, w, b);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             v[q] = f2_fma(f2_mul(f2_sub(v[q], mean2), rstd2), w[q], b[q]);
@@ -109,6 +107,7 @@ template <zero_dtype_t DT, zero_dtype_t PT, int NV, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
 {
     using T = typename Elem<DT>::T;
+    using P = typename Elem<PT>::T;
     __shared__ float slots[2][32];
     grid_dependency_wait();
     const uint32_t n = blockDim.x, k = threadIdx.x, row = blockIdx.x * blockDim.y + threadIdx.y;
@@ -119,15 +118,33 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         raw[i] = load_chunk<DT, VEC>(x, a.d, i, k, n);
-    norm_row<DT, PT, NV, VEC>(a, row, raw, slots, k, n);
+    norm_row<DT, NV, VEC>(a, row, raw, slots, k, n, [&](int i, uint64_t(&w)[4], uint64_t(&b)[4]) {
+        widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), a.d, i, k, n), w);
+        if (a.bias)
+            widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), a.d, i, k, n), b);
+    });
+}
+
+/* A chunk from shared memory. */
+template <zero_dtype_t DT>
+__device__ __forceinline__ typename Elem<DT>::Raw shared_chunk(const uint4* row, uint32_t c)
+{
+    typename Elem<DT>::Raw r;
+    if constexpr (DT == ZERO_F32)
+        r.a = as_f4(row[2 * c]), r.b = as_f4(row[2 * c + 1]);
+    else
+        r.v = row[c];
+    return r;
 }
 
 /* A warp per row, many rows to a warp: lane 0 bulk-copies the warp's next rows into a ring of
- * its own, so that they are on their way while one is worked on. */
+ * its own, so that they are on their way while one is worked on.  The weights and biases lie in
+ * shared memory (read from global memory row after row they were what a warp waited for). */
 template <zero_dtype_t DT, zero_dtype_t PT, int NV>
-__global__ void __launch_bounds__(32 * kRingWarps) k_layernorm_staged(const ForwardArgs a, const uint32_t stages)
+__global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const ForwardArgs a, const uint32_t stages)
 {
     using T = typename Elem<DT>::T;
+    using P = typename Elem<PT>::T;
     extern __shared__ uint4 rings[];
     __shared__ uint64_t full[kRingWarps][kRing];
     __shared__ float slots[2][32];  // not used by single warps
@@ -139,7 +156,9 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_layernorm_staged(const Forw
     }
     __syncwarp();
     grid_dependency_wait();
-    const uint4* ring = rings + (uint64_t)warp * stages * row_bytes / 16;
+    const uint32_t param_words = d * sizeof(P) / 16;
+    uint4 *const weight = rings, *const bias = rings + param_words;
+    const uint4* ring = rings + 2 * param_words + (uint64_t)warp * stages * row_bytes / 16;
     const uint64_t first = blockIdx.x * kRingWarps + warp, step = gridDim.x * kRingWarps;
     auto fetch = [&](uint32_t turn) {
         const uint64_t row = first + turn * step;
@@ -152,6 +171,11 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_layernorm_staged(const Forw
     if (lane == 0)
         for (uint32_t q = 0; q < stages; ++q)
             fetch(q);
+    for (uint32_t i = threadIdx.x; i < param_words; i += blockDim.x) {
+        weight[i] = ld_v4(static_cast<const P*>(a.weight) + i * (16 / sizeof(P)));
+        bias[i] = a.bias ? ld_v4(static_cast<const P*>(a.bias) + i * (16 / sizeof(P))) : make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
     uint32_t turn = 0;
     for (uint64_t row = first; row < a.rows; row += step, ++turn) {
         const uint32_t q = turn % stages;
@@ -162,12 +186,8 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_layernorm_staged(const Forw
         for (int i = 0; i < NV; ++i) {
             const uint32_t c = i * 32 + lane;
             raw[i] = {};
-            if (c * 8 < d) {
-                if constexpr (DT == ZERO_F32)
-                    raw[i].a = as_f4(at[2 * c]), raw[i].b = as_f4(at[2 * c + 1]);
-                else
-                    raw[i].v = at[c];
-            }
+            if (c * 8 < d)
+                raw[i] = shared_chunk<DT>(at, c);
         }
         __syncwarp();  // the stage has been read
         if (!ok) {     // a copy did not arrive within 2 s: this row and the warp's later ones tell, as NaN
@@ -181,7 +201,13 @@ __global__ void __launch_bounds__(32 * kRingWarps) k_layernorm_staged(const Forw
         }
         if (lane == 0)
             fetch(turn + stages);
-        norm_row<DT, PT, NV, true>(a, (uint32_t)row, raw, slots, lane, 32);
+        norm_row<DT, NV, true>(a, (uint32_t)row, raw, slots, lane, 32, [&](int i, uint64_t(&w)[4], uint64_t(&b)[4]) {
+            const uint32_t c = i * 32 + lane;
+            if (c * 8 < d) {
+                widen2<PT>(shared_chunk<PT>(weight, c), w);
+                widen2<PT>(shared_chunk<PT>(bias, c), b);
+            }
+        });
     }
 }
 
@@ -236,6 +262,20 @@ struct Columns {
         }
     }
 
+    template <zero_dtype_t DT>
+    __device__ __forceinline__ void again(int i, const typename Elem<DT>::Raw& x, const typename Elem<DT>::Raw& dy,
+                                          float mean, float rstd, uint64_t (&xh)[4], uint64_t (&g)[4]) const
+    {
+        const uint64_t mean2 = f2(mean, mean), rstd2 = f2(rstd, rstd);
+        widen2<DT>(x, xh);
+        widen2<DT>(dy, g);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            xh[q] = f2_mul(f2_sub(xh[q], mean2), rstd2);
+            g[q] = f2_mul(g[q], w[i][q]);
+        }
+    }
+
     template <bool VEC>
     __device__ __forceinline__ void end(const BackwardArgs& a, uint32_t k, uint32_t n) const
     {
@@ -285,6 +325,30 @@ __device__ __forceinline__ void block_sums(float (&s)[N], float (&slots)[N][32],
 #pragma unroll
     for (int q = 0; q < N; ++q)
         s[q] = warp_sum(lane < n / 32 ? slots[q][lane] : 0.0f);
+}
+
+/* The same for 4 values over at most 8 warps: halves of the warp, then quarters, take over one
+ * value's sum each, which leaves 13 exchanges instead of 40. */
+__device__ __forceinline__ void block_sums4(float (&s)[4], float (&slots)[8][4], uint32_t n)
+{
+    const uint32_t all = 0xffffffffu, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool upper = lane & 16, odd = lane & 8;
+    const float a = __fadd_rn(upper ? s[2] : s[0], __shfl_xor_sync(all, upper ? s[0] : s[2], 16));
+    const float b = __fadd_rn(upper ? s[3] : s[1], __shfl_xor_sync(all, upper ? s[1] : s[3], 16));
+    float v = __fadd_rn(odd ? b : a, __shfl_xor_sync(all, odd ? a : b, 8));
+    v = __fadd_rn(v, __shfl_xor_sync(all, v, 4));
+    v = __fadd_rn(v, __shfl_xor_sync(all, v, 2));
+    v = __fadd_rn(v, __shfl_xor_sync(all, v, 1));
+    if ((lane & 7) == 0)
+        slots[warp][lane >> 3] = v;
+    __syncthreads();
+    v = (lane & 7) < n / 32 ? slots[lane & 7][lane >> 3] : 0.0f;
+    v = __fadd_rn(v, __shfl_xor_sync(all, v, 4));
+    v = __fadd_rn(v, __shfl_xor_sync(all, v, 2));
+    v = __fadd_rn(v, __shfl_xor_sync(all, v, 1));
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        s[q] = __shfl_sync(all, v, 8 * q);
 }
 
 /* R rows at a time per block, straight from global memory: rows that the bulk copies do not
@@ -342,11 +406,11 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs 
 /* The same through a ring of stages of R rows of x and dy, bulk-copied ahead by thread 0: the
  * rows of the next turns are on their way while one is worked on, without registers. */
 template <zero_dtype_t DT, zero_dtype_t PT, int R, int MAXT>
-__global__ void __launch_bounds__(MAXT) k_layernorm_backward_staged(const BackwardArgs a, const uint32_t stages)
+__global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const BackwardArgs a, const uint32_t stages)
 {
     using T = typename Elem<DT>::T;
     extern __shared__ uint4 ring[];
-    __shared__ float slots[2][2 * R][32];
+    __shared__ float slots[2][R == 2 ? 8 : 2 * R][R == 2 ? 4 : 32];
     __shared__ uint64_t full[kRing];
     const uint32_t n = blockDim.x, k = threadIdx.x, d = a.d, row_bytes = d * sizeof(T);
     if (k == 0) {
@@ -393,30 +457,25 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_backward_staged(const Backwa
         const uint32_t q = turn % stages;
         const bool ok = wait_parity_bounded(smem_addr(&full[q]), turn / stages & 1);
         const uint4* stage = ring + (uint64_t)q * 2 * R * row_bytes / 16;
-        uint64_t xh[R][4], g[R][4];
+        typename Elem<DT>::Raw x[R], dy[R];
         float s[2 * R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            typename Elem<DT>::Raw x = {}, dy = {};
+            x[r] = dy[r] = {};
             if (in && row0 + r < a.rows) {
                 const uint4 *px = stage + 2 * r * row_bytes / 16, *py = px + row_bytes / 16;
-                if constexpr (DT == ZERO_F32) {
-                    x.a = as_f4(px[2 * k]), x.b = as_f4(px[2 * k + 1]);
-                    dy.a = as_f4(py[2 * k]), dy.b = as_f4(py[2 * k + 1]);
-                } else {
-                    x.v = px[k];
-                    dy.v = py[k];
-                }
+                x[r] = shared_chunk<DT>(px, k);
+                dy[r] = shared_chunk<DT>(py, k);
             }
-            uint64_t sg = 0, sx = 0;
-            c.template add<DT>(0, x, dy, mean[r], rstd[r], xh[r], g[r], sg, sx);
+            uint64_t sg = 0, sx = 0, xh[4], g[4];
+            c.template add<DT>(0, x[r], dy[r], mean[r], rstd[r], xh, g, sg, sx);
             s[2 * r] = f2_sum(sg);
             s[2 * r + 1] = f2_sum(sx);
         }
-        float rs[R];
+        float m[R], rs[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            rs[r] = rstd[r];
+            m[r] = mean[r], rs[r] = rstd[r];
         statistics(row0 + (uint64_t)gridDim.x * R);  // of the next turn
         if (__syncthreads_or(!ok)) {                 // and: this stage has been read by everyone
             gave_up = true;
@@ -424,12 +483,18 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_backward_staged(const Backwa
         }
         if (k == 0)
             fetch(turn + stages);
-        block_sums(s, slots[turn & 1], n);
+        if constexpr (R == 2)
+            block_sums4(s, slots[turn & 1], n);
+        else
+            block_sums(s, slots[turn & 1], n);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row0 + r >= a.rows)
                 break;
-            put_dx<DT, true>(0, static_cast<T*>(a.dx) + (row0 + r) * a.dx_stride, d, k, n, xh[r], g[r], rs[r],
+            // x and dy are kept as they came and xh and g formed again: registers for a third block
+            uint64_t xh[4], g[4];
+            c.template again<DT>(0, x[r], dy[r], m[r], rs[r], xh, g);
+            put_dx<DT, true>(0, static_cast<T*>(a.dx) + (row0 + r) * a.dx_stride, d, k, n, xh, g, rs[r],
                              __fmul_rn(s[2 * r], inv_d), __fmul_rn(s[2 * r + 1], inv_d));
         }
     }
@@ -511,9 +576,11 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
     if constexpr (VEC) {
         if (n == 32) {
             const uint32_t row_bytes = a.d * (uint32_t)sizeof(typename Elem<DT>::T);
-            uint32_t stages = 16384 / row_bytes;
+            const uint32_t params = 2 * a.d * (uint32_t)sizeof(typename Elem<PT>::T);
+            // three blocks to an SM
+            uint32_t stages = (72 * 1024 - params) / (kRingWarps * row_bytes);
             stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
-            const size_t smem = (size_t)kRingWarps * stages * row_bytes;
+            const size_t smem = params + (size_t)kRingWarps * stages * row_bytes;
             auto staged = [&](auto kernel, bool& taken) {
                 uint32_t fit = 0;
                 cudaError_t e =
