@@ -336,12 +336,14 @@ def zero_step_static_workspace(layout: Layout, hp: HParams, dtype: int, replicas
 # lists of tensors
 # --------------------------------------------------------------------------------------
 _CODES = {}
+_ID_BYTES = {}
 
 
 def _dtype_codes() -> dict:
     """torch dtypes to zero_dtype_t; 16-bit integers to 0 (parameters' bit patterns)."""
     if not _CODES:
         import torch
+        _ID_BYTES.update({torch.int32: 4, torch.int64: 8})
         _CODES.update({torch.float16: ZERO_F16, torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32,
                        torch.uint8: ZERO_U8, torch.int16: 0, torch.uint16: 0})
     return _CODES
@@ -570,90 +572,101 @@ def zero_tensors_state8_write(to: TensorList, source: TensorList, stream=None) -
 _FLOATS = (ZERO_F16, ZERO_BF16, ZERO_F32)
 
 
-class _Operands:
-    """The tensors of one call, checked as they are named: CUDA tensors of one device, which is
-    the current one."""
+def _current() -> int:
+    """The current device."""
+    global _TORCH_C
+    if _TORCH_C is None:
+        import torch
+        torch.cuda.current_device()  # CUDA is initialised from here on
+        _TORCH_C = torch._C
+    if not _CODES:
+        _dtype_codes()
+    return _TORCH_C._cuda_getDevice()
 
-    def __init__(self):
-        self.device = None
 
-    def take(self, name: str, t, types=None) -> int:
-        """The tensor's type code."""
-        device = t.get_device()
-        if self.device is None:
-            import torch
-            if device < 0:
-                raise ValueError(f"{name} is not a CUDA tensor")
-            current = torch.cuda.current_device()
-            if device != current:
-                raise ValueError(f"{name} is on device {device}, the current device is {current}")
-            self.device = device
-        elif device != self.device:
-            raise ValueError(f"{name} is not on device {self.device}")
-        code = _dtype_codes().get(t.dtype, -1)
-        if types is not None and code not in types:
-            raise ValueError(f"{name} has type {t.dtype}")
-        return code
+def _here(stream, device: int) -> int | None:
+    return _TORCH_C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
-    def rows(self, name: str, t, dim: int, types) -> tuple:
-        """Type code, number of rows and their stride: the last dimension holds a row, the
-        others count rows at one distance from each other."""
-        code = self.take(name, t, types)
-        if t.dim() == 0 or t.shape[-1] != dim:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not rows of {dim}")
-        if t.is_contiguous():
-            return code, t.numel() // dim, dim
-        n, stride = 1, 0
-        if dim > 1 and t.stride(-1) != 1:
-            raise ValueError(f"{name}'s rows are not contiguous")
-        for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-            if size == 1:
-                continue
-            if stride and step != n * stride:
-                raise ValueError(f"{name}'s rows are not at one distance from each other")
-            stride = stride or step
-            n *= size
-        if stride < dim and n > 1:
-            raise ValueError(f"{name}'s rows overlap")
-        return code, n, stride or dim
 
-    def whole(self, name: str, t, shape: tuple, types) -> int:
-        """The type code of a contiguous tensor of the given shape."""
-        code = self.take(name, t, types)
-        if tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}" if tuple(t.shape) != shape
-                             else f"{name} is not contiguous")
-        return code
+def _type_of(name: str, t, device: int, types=None) -> int:
+    """The type code of a CUDA tensor of the current device."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} is not a CUDA tensor of the current device, {device}")
+    code = _CODES.get(t.dtype, -1)
+    if types is not None and code not in types:
+        raise ValueError(f"{name} has type {t.dtype}")
+    return code
 
-    def per_row(self, name: str, t, n: int) -> None:
-        """fp32, one number per row, in any shape."""
-        self.take(name, t, (ZERO_F32,))
-        if t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name} has {t.numel()} elements, not {n}" if t.numel() != n
-                             else f"{name} is not contiguous")
 
-    def ids(self, name: str, t, n: int | None = None) -> tuple:
-        """How many ids, and their bytes: int32 or int64."""
-        self.take(name, t)
-        size = {"torch.int32": 4, "torch.int64": 8}.get(str(t.dtype))
-        if size is None:
-            raise ValueError(f"{name} has type {t.dtype}, not int32 or int64")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} is not contiguous")
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{name} has {t.numel()} elements, not {n}")
-        return t.numel(), size
+def _rows(name: str, t, dim: int, device: int, types) -> tuple:
+    """Type code, number of rows and their stride: the last dimension holds a row, the others
+    count rows at one distance from each other."""
+    code = _type_of(name, t, device, types)
+    shape = t.shape
+    if not shape or shape[-1] != dim:
+        raise ValueError(f"{name} has shape {tuple(shape)}, not rows of {dim}")
+    if t.is_contiguous():
+        return code, t.numel() // dim, dim
+    n, stride = 1, 0
+    if dim > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s rows are not contiguous")
+    for size, step in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if n > 1 and step != n * stride:
+            raise ValueError(f"{name}'s rows are not at one distance from each other")
+        stride = stride if n > 1 else step
+        n *= size
+    if stride < dim and n > 1:
+        raise ValueError(f"{name}'s rows overlap")
+    return code, n, stride if n > 1 else dim
 
-    def work(self, fn: str, t, need: int) -> int:
-        """A workspace's address: a tensor that is smaller than needed is refused, the size
-        behind a plain address is the caller's word."""
-        if not isinstance(t, int):
-            self.take("workspace", t)
-            if not t.is_contiguous():
-                raise ValueError("workspace is not contiguous")
-            if t.nbytes < need:
-                raise ZeroError(fn, ZERO_ENOMEM)
-        return _ptr(t)
+
+def _whole(name: str, t, shape: tuple, device: int, types) -> int:
+    """The type code of a contiguous tensor of the given shape."""
+    code = _type_of(name, t, device, types)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return code
+
+
+def _per_row(name: str, t, n: int, device: int) -> int:
+    """The address of fp32 numbers, one per row, in any shape."""
+    _type_of(name, t, device, (ZERO_F32,))
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, not {n}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _ids(name: str, t, device: int, n: int | None = None) -> tuple:
+    """How many ids, and their bytes: int32 or int64."""
+    _type_of(name, t, device)
+    size = _ID_BYTES.get(t.dtype)
+    if size is None:
+        raise ValueError(f"{name} has type {t.dtype}, not int32 or int64")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    count = t.numel()
+    if n is not None and count != n:
+        raise ValueError(f"{name} has {count} elements, not {n}")
+    return count, size
+
+
+def _space(fn: str, t, need: int, device: int) -> int:
+    """A workspace's address: a tensor that is smaller than needed is refused, the size behind a
+    plain address is the caller's word."""
+    if isinstance(t, int):
+        return t
+    _type_of("workspace", t, device)
+    if not t.is_contiguous():
+        raise ValueError("workspace is not contiguous")
+    if t.nbytes < need:
+        raise ZeroError(fn, ZERO_ENOMEM)
+    return t.data_ptr()
 
 
 def zero_layernorm_workspace_bytes(rows: int, dim: int) -> int:
@@ -664,20 +677,20 @@ def zero_layernorm(x, weight, bias, y, mean=None, rstd=None, eps: float = 1e-5, 
     """y = (x - mean) * rstd * weight + bias over x's last dimension.  x, y: fp16, bf16 or fp32;
     weight, bias (or None): x's type or fp32; mean, rstd: fp32 per row, kept for the backward
     pass, or None."""
-    o, dim = _Operands(), weight.numel()
-    code, n, xs = o.rows("x", x, dim, _FLOATS)
-    param = o.whole("weight", weight, (dim,), (code, ZERO_F32))
+    device, dim = _current(), weight.numel()
+    code, n, xs = _rows("x", x, dim, device, _FLOATS)
+    param = _whole("weight", weight, (dim,), device, (code, ZERO_F32))
     if bias is not None:
-        o.whole("bias", bias, (dim,), (param,))
-    _, ny, ys = o.rows("y", y, dim, (code,))
+        _whole("bias", bias, (dim,), device, (param,))
+    _, ny, ys = _rows("y", y, dim, device, (code,))
     if ny != n:
         raise ValueError(f"x has {n} rows, y {ny}")
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            o.per_row(name, t, n)
-    _check("zero_layernorm", _lib().zero_layernorm(
-        code, n, dim, _ptr(x), xs, _ptr(weight), _ptr(bias), param, eps, _ptr(y), ys, _ptr(mean), _ptr(rstd),
-        _stream(stream)))
+    status = _lib().zero_layernorm(
+        code, n, dim, x.data_ptr(), xs, weight.data_ptr(), _ptr(bias), param, eps, y.data_ptr(), ys,
+        None if mean is None else _per_row("mean", mean, n, device),
+        None if rstd is None else _per_row("rstd", rstd, n, device), _here(stream, device))
+    if status:
+        _check("zero_layernorm", status)
 
 
 def zero_layernorm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, workspace, accumulate: bool = False,
@@ -685,44 +698,52 @@ def zero_layernorm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, works
     """The gradients of zero_layernorm.  dy, dx: x's type; dweight, dbias: x's type or fp32, either
     may be None; accumulate: they are added to.  workspace: of
     zero_layernorm_workspace_bytes(rows, dim) bytes."""
-    o, dim = _Operands(), weight.numel()
-    code, n, xs = o.rows("x", x, dim, _FLOATS)
-    param = o.whole("weight", weight, (dim,), (code, ZERO_F32))
-    _, nd, ds = o.rows("dy", dy, dim, (code,))
-    _, ng, gs = o.rows("dx", dx, dim, (code,))
+    device, dim, fn = _current(), weight.numel(), "zero_layernorm_backward"
+    code, n, xs = _rows("x", x, dim, device, _FLOATS)
+    param = _whole("weight", weight, (dim,), device, (code, ZERO_F32))
+    _, nd, ds = _rows("dy", dy, dim, device, (code,))
+    _, ng, gs = _rows("dx", dx, dim, device, (code,))
     if nd != n or ng != n:
         raise ValueError(f"x has {n} rows, dy {nd}, dx {ng}")
-    o.per_row("mean", mean, n)
-    o.per_row("rstd", rstd, n)
     grad = code
     if dweight is not None:
-        grad = o.whole("dweight", dweight, (dim,), (code, ZERO_F32))
+        grad = _whole("dweight", dweight, (dim,), device, (code, ZERO_F32))
     if dbias is not None:
-        grad = o.whole("dbias", dbias, (dim,), (code, ZERO_F32) if dweight is None else (grad,))
-    f, fn = _lib().zero_layernorm_backward, "zero_layernorm_backward"
-    _check(fn, f(code, n, dim, _ptr(x), xs, _ptr(weight), param, _ptr(mean), _ptr(rstd), _ptr(dy), ds, _ptr(dx), gs,
-                 _ptr(dweight), _ptr(dbias), grad, int(bool(accumulate)),
-                 o.work(fn, workspace, zero_layernorm_workspace_bytes(n, dim)), _stream(stream)))
+        grad = _whole("dbias", dbias, (dim,), device, (code, ZERO_F32) if dweight is None else (grad,))
+    f = _lib().zero_layernorm_backward
+    status = f(code, n, dim, x.data_ptr(), xs, weight.data_ptr(), param, _per_row("mean", mean, n, device),
+               _per_row("rstd", rstd, n, device), dy.data_ptr(), ds, dx.data_ptr(), gs, _ptr(dweight), _ptr(dbias), grad,
+               bool(accumulate), _space(fn, workspace, zero_layernorm_workspace_bytes(n, dim), device),
+               _here(stream, device))
+    if status:
+        _check(fn, status)
 
 
 def zero_embedding_workspace_bytes(n_tokens: int, dim: int, vocab: int) -> int:
     return _lib().zero_embedding_workspace_bytes(n_tokens, dim, vocab)
 
 
+def _table(name: str, t) -> tuple:
+    """(vocab, dim)."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} has shape {tuple(shape)}")
+    return shape
+
+
 def zero_embedding(tokens, table, out, scale: float = 1.0, stream=None) -> None:
     """out[t] = scale * table[tokens[t]], zeros for ids outside the table.  tokens: int32 or int64;
     table [vocab, dim] and out [..., dim]: fp16, bf16 or fp32, alike."""
-    o = _Operands()
-    n, size = o.ids("tokens", tokens)
-    if table.dim() != 2:
-        raise ValueError(f"table has shape {tuple(table.shape)}")
-    vocab, dim = table.shape
-    code = o.whole("table", table, (vocab, dim), _FLOATS)
-    _, no, stride = o.rows("out", out, dim, (code,))
+    device, (vocab, dim) = _current(), _table("table", table)
+    n, size = _ids("tokens", tokens, device)
+    code = _whole("table", table, (vocab, dim), device, _FLOATS)
+    _, no, stride = _rows("out", out, dim, device, (code,))
     if no != n:
         raise ValueError(f"{n} tokens, out has {no} rows")
-    _check("zero_embedding", _lib().zero_embedding(code, n, dim, vocab, _ptr(tokens), size, _ptr(table), scale, _ptr(out),
-                                                   stride, _stream(stream)))
+    status = _lib().zero_embedding(code, n, dim, vocab, tokens.data_ptr(), size, table.data_ptr(), scale, out.data_ptr(),
+                                   stride, _here(stream, device))
+    if status:
+        _check("zero_embedding", status)
 
 
 def zero_embedding_backward(tokens, dout, dtable, workspace, scale: float = 1.0, accumulate: bool = False,
@@ -731,47 +752,46 @@ def zero_embedding_backward(tokens, dout, dtable, workspace, scale: float = 1.0,
     dtable: dout's type or fp32; accumulate: it is added to (rows without a token are not
     touched), else all of it is written.  workspace: of
     zero_embedding_workspace_bytes(n_tokens, dim, vocab) bytes."""
-    o = _Operands()
-    n, size = o.ids("tokens", tokens)
-    if dtable.dim() != 2:
-        raise ValueError(f"dtable has shape {tuple(dtable.shape)}")
-    vocab, dim = dtable.shape
-    code, nd, stride = o.rows("dout", dout, dim, _FLOATS)
+    device, (vocab, dim), fn = _current(), _table("dtable", dtable), "zero_embedding_backward"
+    n, size = _ids("tokens", tokens, device)
+    code, nd, stride = _rows("dout", dout, dim, device, _FLOATS)
     if nd != n:
         raise ValueError(f"{n} tokens, dout has {nd} rows")
-    grad = o.whole("dtable", dtable, (vocab, dim), (code, ZERO_F32))
-    f, fn = _lib().zero_embedding_backward, "zero_embedding_backward"
-    _check(fn, f(code, n, dim, vocab, _ptr(tokens), size, _ptr(dout), stride, scale, _ptr(dtable), grad,
-                 int(bool(accumulate)), o.work(fn, workspace, zero_embedding_workspace_bytes(n, dim, vocab)),
-                 _stream(stream)))
+    grad = _whole("dtable", dtable, (vocab, dim), device, (code, ZERO_F32))
+    f = _lib().zero_embedding_backward
+    status = f(code, n, dim, vocab, tokens.data_ptr(), size, dout.data_ptr(), stride, scale, dtable.data_ptr(), grad,
+               bool(accumulate), _space(fn, workspace, zero_embedding_workspace_bytes(n, dim, vocab), device),
+               _here(stream, device))
+    if status:
+        _check(fn, status)
 
 
 def zero_head_workspace_bytes(rows: int, dim: int, vocab: int) -> int:
     return _lib().zero_head_workspace_bytes(rows, dim, vocab)
 
 
-def _head(o: _Operands, hidden, weight, targets) -> tuple:
+def _head(hidden, weight, targets, device: int) -> tuple:
     """What both of the head's calls check: (type code, rows, dim, vocab), row stride, bytes per
     target."""
-    if weight.dim() != 2:
-        raise ValueError(f"weight has shape {tuple(weight.shape)}")
-    vocab, dim = weight.shape
-    code, n, stride = o.rows("hidden", hidden, dim, (ZERO_F16, ZERO_BF16))
-    o.whole("weight", weight, (vocab, dim), (code,))
-    return (code, n, dim, vocab), stride, o.ids("targets", targets, n)[1]
+    vocab, dim = _table("weight", weight)
+    code, n, stride = _rows("hidden", hidden, dim, device, (ZERO_F16, ZERO_BF16))
+    _whole("weight", weight, (vocab, dim), device, (code,))
+    return (code, n, dim, vocab), stride, _ids("targets", targets, device, n)[1]
 
 
 def zero_head_loss(hidden, weight, targets, loss, lse, workspace, stream=None) -> None:
     """The cross entropy of every token and its logits' log-sum-exp, from hidden [..., dim] and
     weight [vocab, dim] (fp16 or bf16); the logits are never kept.  Tokens whose target lies outside
     [0, vocab) get 0.  workspace: of zero_head_workspace_bytes(rows, dim, vocab) bytes."""
-    o, fn = _Operands(), "zero_head_loss"
-    sizes, stride, width = _head(o, hidden, weight, targets)
-    o.per_row("loss", loss, sizes[1])
-    o.per_row("lse", lse, sizes[1])
-    _check(fn, _lib().zero_head_loss(*sizes, _ptr(hidden), stride, _ptr(weight), _ptr(targets), width, _ptr(loss),
-                                     _ptr(lse), o.work(fn, workspace, zero_head_workspace_bytes(*sizes[1:])),
-                                     _stream(stream)))
+    device, fn = _current(), "zero_head_loss"
+    sizes, stride, width = _head(hidden, weight, targets, device)
+    n = sizes[1]
+    status = _lib().zero_head_loss(*sizes, hidden.data_ptr(), stride, weight.data_ptr(), targets.data_ptr(), width,
+                                   _per_row("loss", loss, n, device), _per_row("lse", lse, n, device),
+                                   _space(fn, workspace, zero_head_workspace_bytes(*sizes[1:]), device),
+                                   _here(stream, device))
+    if status:
+        _check(fn, status)
 
 
 def zero_head_loss_backward(hidden, weight, targets, lse, dhidden, dweight, workspace, scale: float = 1.0,
@@ -779,25 +799,28 @@ def zero_head_loss_backward(hidden, weight, targets, lse, dhidden, dweight, work
     """The gradients of sum over tokens of scale * row_scale * loss, times the loss scale that the
     step state st holds (None: 1).  dhidden: hidden's type, or None; dweight: that or fp32, or
     None; accumulate: dweight is added to."""
-    o, fn = _Operands(), "zero_head_loss_backward"
-    sizes, stride, width = _head(o, hidden, weight, targets)
+    device, fn = _current(), "zero_head_loss_backward"
+    sizes, stride, width = _head(hidden, weight, targets, device)
     code, n, dim, vocab = sizes
-    o.per_row("lse", lse, n)
-    if row_scale is not None:
-        o.per_row("row_scale", row_scale, n)
+    row = None if row_scale is None else _per_row("row_scale", row_scale, n, device)
     hs, grad = dim, code
     if dhidden is not None:
-        _, nh, hs = o.rows("dhidden", dhidden, dim, (code,))
+        _, nh, hs = _rows("dhidden", dhidden, dim, device, (code,))
         if nh != n:
             raise ValueError(f"hidden has {n} rows, dhidden {nh}")
     if dweight is not None:
-        grad = o.whole("dweight", dweight, (vocab, dim), (code, ZERO_F32))
+        grad = _whole("dweight", dweight, (vocab, dim), device, (code, ZERO_F32))
     if st is not None and not isinstance(st, int):
-        o.take("st", st)
+        _type_of("st", st, device)
+        if st.nbytes < STATE_BYTES:
+            raise ValueError(f"st has {st.nbytes} bytes, not {STATE_BYTES}")
     f = _lib().zero_head_loss_backward
-    _check(fn, f(*sizes, _ptr(hidden), stride, _ptr(weight), _ptr(targets), width, _ptr(lse), scale, _ptr(row_scale),
-                 _ptr(st), _ptr(dhidden), hs, _ptr(dweight), grad, int(bool(accumulate)),
-                 o.work(fn, workspace, zero_head_workspace_bytes(*sizes[1:])), _stream(stream)))
+    status = f(*sizes, hidden.data_ptr(), stride, weight.data_ptr(), targets.data_ptr(), width,
+               _per_row("lse", lse, n, device), scale, row, _ptr(st), _ptr(dhidden), hs, _ptr(dweight), grad,
+               bool(accumulate), _space(fn, workspace, zero_head_workspace_bytes(*sizes[1:]), device),
+               _here(stream, device))
+    if status:
+        _check(fn, status)
 
 
 __all__ = [

@@ -534,7 +534,7 @@ cudaError_t fill_and_sort(const Tokens& tokens, uint32_t n, void* table, uint64_
     const unsigned fillers = bytes ? (unsigned)(want < cap ? (want ? want : 1) : cap) : 0;
     SortArgs a{tokens, nullptr, buf[0], hist, n, tiles, 0};
     if (tiles == 1) {
-        e = cudaFuncSetAttribute(k_sort_small, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SmallSmem));
+        e = allow_smem<k_sort_small>();
         sorted = buf[0];
         return e != cudaSuccess ? e
                                 : launch_pdl(k_sort_small, dim3(1 + fillers), dim3(kSortThreads), sizeof(SmallSmem), s, a,

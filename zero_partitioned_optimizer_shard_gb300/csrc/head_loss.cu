@@ -990,7 +990,7 @@ template <Mode MODE>
 cudaError_t product(const ProductArgs& a, bool f16, uint64_t tiles, cudaStream_t s)
 {
     auto* kernel = f16 ? k_head_product<MODE, true> : k_head_product<MODE, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    const cudaError_t e = f16 ? allow_smem<k_head_product<MODE, true>>() : allow_smem<k_head_product<MODE, false>>();
     if (e != cudaSuccess)
         return e;
     const uint64_t pairs = (uint64_t)sm_count() / 2;

@@ -10,8 +10,6 @@
  */
 #include "rows.cuh"
 
-#include <atomic>
-
 namespace zero {
 namespace {
 
@@ -554,14 +552,20 @@ __global__ void __launch_bounds__(1024) k_layernorm_join(const JoinArgs a)
     }
 }
 
-/* Blocks of a kernel that fit on the current device at once. */
-template <typename K>
-cudaError_t resident(K kernel, uint32_t threads, size_t smem, uint32_t& blocks)
+/* Rows by warps with rings, if there are several rows to a warp. */
+template <auto KERNEL>
+cudaError_t forward_staged(const ForwardArgs& a, size_t params, size_t row_bytes, bool& taken, cudaStream_t s)
 {
-    int per_sm = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, (int)threads, smem);
-    blocks = (uint32_t)(sm_count() * (per_sm > 0 ? per_sm : 1));
-    return e;
+    // three blocks to an SM
+    size_t stages = (72 * 1024 - params) / (kRingWarps * row_bytes);
+    stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
+    const size_t smem = params + kRingWarps * stages * row_bytes;
+    uint32_t fit = 0;
+    cudaError_t e = allow_smem<KERNEL>();
+    if (e == cudaSuccess)
+        e = resident<KERNEL>(32 * kRingWarps, smem, fit);
+    taken = e == cudaSuccess && a.rows > fit * kRingWarps;
+    return taken ? launch_pdl(KERNEL, dim3(fit), dim3(32 * kRingWarps), smem, s, a, (uint32_t)stages) : e;
 }
 
 template <zero_dtype_t DT, zero_dtype_t PT, bool VEC>
@@ -570,35 +574,21 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
     // a warp per row up to 2,048 elements (no barrier), then 128 and 512 threads
     const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 256 ? 32 : chunks <= 1024 ? 128 : 512;
     const uint32_t per = (chunks + n - 1) / n, rows = n == 32 ? 4 : 1;
-    auto go = [&](auto kernel) {
-        return launch_pdl(kernel, dim3((a.rows + rows - 1) / rows), dim3(n, rows), 0, s, a);
-    };
     if constexpr (VEC) {
         if (n == 32) {
-            const uint32_t row_bytes = a.d * (uint32_t)sizeof(typename Elem<DT>::T);
-            const uint32_t params = 2 * a.d * (uint32_t)sizeof(typename Elem<PT>::T);
-            // three blocks to an SM
-            uint32_t stages = (72 * 1024 - params) / (kRingWarps * row_bytes);
-            stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
-            const size_t smem = params + (size_t)kRingWarps * stages * row_bytes;
-            auto staged = [&](auto kernel, bool& taken) {
-                uint32_t fit = 0;
-                cudaError_t e =
-                    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                if (e == cudaSuccess)
-                    e = resident(kernel, 32 * kRingWarps, smem, fit);
-                taken = e == cudaSuccess && a.rows > fit * kRingWarps;  // several rows to a warp
-                return taken ? launch_pdl(kernel, dim3(fit), dim3(32 * kRingWarps), smem, s, a, stages) : e;
-            };
+            const size_t params = 2 * a.d * sizeof(typename Elem<PT>::T), row = a.d * sizeof(typename Elem<DT>::T);
             bool taken = false;
-            const cudaError_t e = per <= 1   ? staged(k_layernorm_staged<DT, PT, 1>, taken)
-                                  : per <= 2 ? staged(k_layernorm_staged<DT, PT, 2>, taken)
-                                  : per <= 4 ? staged(k_layernorm_staged<DT, PT, 4>, taken)
-                                             : staged(k_layernorm_staged<DT, PT, 8>, taken);
+            const cudaError_t e = per <= 1   ? forward_staged<k_layernorm_staged<DT, PT, 1>>(a, params, row, taken, s)
+                                  : per <= 2 ? forward_staged<k_layernorm_staged<DT, PT, 2>>(a, params, row, taken, s)
+                                  : per <= 4 ? forward_staged<k_layernorm_staged<DT, PT, 4>>(a, params, row, taken, s)
+                                             : forward_staged<k_layernorm_staged<DT, PT, 8>>(a, params, row, taken, s);
             if (taken || e != cudaSuccess)
                 return e;
         }
     }
+    auto go = [&](auto kernel) {
+        return launch_pdl(kernel, dim3((a.rows + rows - 1) / rows), dim3(n, rows), 0, s, a);
+    };
     if (n == 512)
         return per <= 2 ? go(k_layernorm<DT, PT, 2, VEC, 512>) : go(k_layernorm<DT, PT, 4, VEC, 512>);
     return per <= 1   ? go(k_layernorm<DT, PT, 1, VEC, 128>)
@@ -607,50 +597,42 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
                       : go(k_layernorm<DT, PT, 8, VEC, 128>);
 }
 
+/* As many blocks as fit at once, each with its share of the rows and its part of the sums. */
+template <auto KERNEL, typename... More>
+cudaError_t backward_blocks(const BackwardArgs& a, uint32_t threads, uint32_t rows, size_t smem, uint32_t& parts,
+                            cudaStream_t s, More... more)
+{
+    uint32_t fit = 0;
+    cudaError_t e = smem ? allow_smem<KERNEL>() : cudaSuccess;
+    if (e == cudaSuccess)
+        e = resident<KERNEL>(threads, smem, fit);
+    if (e != cudaSuccess)
+        return e;
+    const uint32_t want = (a.rows + rows - 1) / rows;
+    parts = fit < kMaxParts ? fit : kMaxParts;
+    parts = parts < want ? parts : want;
+    return launch_pdl(KERNEL, dim3(parts), dim3(threads), smem, s, a, more...);
+}
+
 template <zero_dtype_t DT, zero_dtype_t PT, bool VEC>
 cudaError_t backward(const BackwardArgs& a, uint32_t& parts, cudaStream_t s)
 {
-    const uint32_t chunks = (a.d + 7) / 8;
-    const uint32_t n = chunks <= 1024 ? (chunks + 31) / 32 * 32 : 1024;
-    auto blocks = [&](auto kernel, uint32_t rows, size_t smem) {
-        uint32_t fit = 0;
-        cudaError_t e = cudaSuccess;
-        if (smem)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e == cudaSuccess)
-            e = resident(kernel, n, smem, fit);
-        fit = fit < kMaxParts ? fit : kMaxParts;
-        const uint32_t want = (a.rows + rows - 1) / rows;
-        parts = fit < want ? fit : want;
-        return e;
-    };
-    auto go = [&](auto kernel, uint32_t rows) {
-        const cudaError_t e = blocks(kernel, rows, 0);
-        return e != cudaSuccess ? e : launch_pdl(kernel, dim3(parts), dim3(n), 0, s, a);
-    };
-    if constexpr (VEC) {
-        auto staged = [&](auto kernel, uint32_t rows) {
-            // a ring of up to 48 KB: two blocks and more to an SM
-            const uint32_t stage = 2 * rows * a.d * (uint32_t)sizeof(typename Elem<DT>::T);
-            uint32_t stages = 49152 / stage;
-            stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
-            const cudaError_t e = blocks(kernel, rows, (size_t)stages * stage);
-            return e != cudaSuccess ? e
-                                    : launch_pdl(kernel, dim3(parts), dim3(n), (size_t)stages * stage, s, a, stages);
-        };
-        if (chunks <= 256)
-            return staged(k_layernorm_backward_staged<DT, PT, 2, 256>, 2);
-        if (chunks <= 1024)
-            return staged(k_layernorm_backward_staged<DT, PT, 1, 1024>, 1);
-    }
+    const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 1024 ? (chunks + 31) / 32 * 32 : 1024;
     if (chunks > 1024)
-        return go(k_layernorm_backward<DT, PT, 2, 1, VEC, 1024>, 1);
-    if constexpr (!VEC) {
-        if (chunks <= 256)
-            return go(k_layernorm_backward<DT, PT, 1, 2, VEC, 256>, 2);
-        return go(k_layernorm_backward<DT, PT, 1, 1, VEC, 1024>, 1);
+        return backward_blocks<k_layernorm_backward<DT, PT, 2, 1, VEC, 1024>>(a, n, 1, 0, parts, s);
+    if constexpr (VEC) {
+        // a ring of up to 48 KB: two blocks and more to an SM
+        const uint32_t rows = chunks <= 256 ? 2 : 1, stage = 2 * rows * a.d * (uint32_t)sizeof(typename Elem<DT>::T);
+        uint32_t stages = 49152 / stage;
+        stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
+        const size_t smem = (size_t)stages * stage;
+        return chunks <= 256
+                   ? backward_blocks<k_layernorm_backward_staged<DT, PT, 2, 256>>(a, n, 2, smem, parts, s, stages)
+                   : backward_blocks<k_layernorm_backward_staged<DT, PT, 1, 1024>>(a, n, 1, smem, parts, s, stages);
+    } else {
+        return chunks <= 256 ? backward_blocks<k_layernorm_backward<DT, PT, 1, 2, VEC, 256>>(a, n, 2, 0, parts, s)
+                             : backward_blocks<k_layernorm_backward<DT, PT, 1, 1, VEC, 1024>>(a, n, 1, 0, parts, s);
     }
-    return cudaErrorInvalidValue;
 }
 
 /* Calls f with the types and the layout as template arguments. */

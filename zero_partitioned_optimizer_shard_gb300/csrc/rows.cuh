@@ -14,6 +14,8 @@
 #include "adamw_elem.cuh"
 #include "reduce_elem.cuh"
 
+#include <atomic>
+
 namespace zero {
 namespace {
 
@@ -219,6 +221,45 @@ inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb)
 {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+/* Lets a kernel take all of an SM's shared memory, once per kernel and device. */
+template <auto KERNEL>
+cudaError_t allow_smem()
+{
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit))
+        return e;
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, KERNEL);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448 - (int)at.sharedSizeBytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+/* Blocks of a kernel that fit on the current device at once; the last answer is kept. */
+template <auto KERNEL>
+cudaError_t resident(uint32_t threads, size_t smem, uint32_t& blocks)
+{
+    static std::atomic<uint64_t> last{0};  // device + 1, threads, 16-byte units of shared memory, blocks per SM
+    int dev = 0, per_sm = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t key = (uint64_t)(dev + 1) << 40 | (uint64_t)threads << 24 | (smem / 16) << 8;
+    const uint64_t have = last.load(std::memory_order_relaxed);
+    if (e == cudaSuccess && (have & ~255ull) == key) {
+        per_sm = (int)(have & 255);
+    } else if (e == cudaSuccess) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, (int)threads, smem);
+        if (e == cudaSuccess)
+            last.store(key | (uint64_t)per_sm, std::memory_order_relaxed);
+    }
+    blocks = (uint32_t)(sm_count() * (per_sm > 0 ? per_sm : 1));
+    return e;
 }
 
 inline int rows_status(cudaError_t e)
