@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(256) k_embedding(const LookupArgs a)
     using T = typename Elem<DT>::T;
     constexpr int W = 4;
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t lane = threadIdx.x & 31;
     const uint64_t total = (uint64_t)a.n * a.pieces;
     const uint64_t first = ((uint64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5)) * W;
@@ -97,19 +98,20 @@ struct RankSmem {
     uint32_t warp_total[8];
 };
 
-/* Each thread's kItems keys (a warp's are 32 * kItems neighbours, taken 32 at a time) get
+/* Each thread's ITEMS keys (a warp's are 32 * ITEMS neighbours, taken 32 at a time) get
  * their rank among the tile's keys of the same digit, in the keys' order; base[] becomes the
  * number of the tile's keys with a smaller digit and count the tile's keys of digit
  * threadIdx.x. */
-__device__ __forceinline__ void rank_tile(RankSmem& sm, const uint32_t (&key)[kItems], uint32_t shift,
-                                          uint32_t (&rank)[kItems], uint32_t& count)
+template <uint32_t ITEMS>
+__device__ __forceinline__ void rank_tile(RankSmem& sm, const uint32_t (&key)[ITEMS], uint32_t shift,
+                                          uint32_t (&rank)[ITEMS])
 {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (uint32_t b = lane; b < kBins; b += 32)
         sm.of_warp[warp][b] = 0;
     __syncwarp();
 #pragma unroll
-    for (uint32_t i = 0; i < kItems; ++i) {
+    for (uint32_t i = 0; i < ITEMS; ++i) {
         const uint32_t digit = key[i] >> shift & (kBins - 1);
         const uint32_t peers = __match_any_sync(0xffffffffu, digit);
         const uint32_t below = __popc(peers & ((1u << lane) - 1));
@@ -121,7 +123,7 @@ __device__ __forceinline__ void rank_tile(RankSmem& sm, const uint32_t (&key)[kI
         rank[i] = before + below;
     }
     __syncthreads();
-    count = 0;
+    uint32_t count = 0;
     if (threadIdx.x < kBins) {
 #pragma unroll 8
         for (uint32_t w = 0; w < kSortWarps; ++w) {
@@ -148,14 +150,15 @@ __device__ __forceinline__ void rank_tile(RankSmem& sm, const uint32_t (&key)[kI
     }
     __syncthreads();
 #pragma unroll
-    for (uint32_t i = 0; i < kItems; ++i)
+    for (uint32_t i = 0; i < ITEMS; ++i)
         rank[i] += sm.of_warp[warp][key[i] >> shift & (kBins - 1)];
 }
 
 /* The place in its tile of item i of the calling thread. */
+template <uint32_t ITEMS>
 __device__ __forceinline__ uint32_t item_at(uint32_t i)
 {
-    return (threadIdx.x >> 5) * 32 * kItems + i * 32 + (threadIdx.x & 31);
+    return (threadIdx.x >> 5) * 32 * ITEMS + i * 32 + (threadIdx.x & 31);
 }
 
 struct SortArgs {
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_count(const SortArgs a)
         count[threadIdx.x] = 0;
     __syncthreads();
     for (uint32_t i = 0; i < kItems; ++i) {
-        const uint32_t at = blockIdx.x * kTile + item_at(i);
+        const uint32_t at = blockIdx.x * kTile + item_at<kItems>(i);
         if (at < a.n)
             atomicAdd(&count[sort_item(a, at).x >> a.shift & (kBins - 1)], 1u);
     }
@@ -226,17 +229,17 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_scatter(const SortArgs a)
     extern __shared__ uint4 smem[];
     RankSmem& sm = *reinterpret_cast<RankSmem*>(smem);
     grid_dependency_wait();
-    uint32_t key[kItems], place[kItems], rank[kItems], count;
+    uint32_t key[kItems], place[kItems], rank[kItems];
 #pragma unroll
     for (uint32_t i = 0; i < kItems; ++i) {
-        const uint2 x = sort_item(a, blockIdx.x * kTile + item_at(i));
+        const uint2 x = sort_item(a, blockIdx.x * kTile + item_at<kItems>(i));
         key[i] = x.x;
         place[i] = x.y;
     }
-    rank_tile(sm, key, a.shift, rank, count);
+    rank_tile(sm, key, a.shift, rank);
 #pragma unroll
     for (uint32_t i = 0; i < kItems; ++i)
-        if (blockIdx.x * kTile + item_at(i) < a.n)
+        if (blockIdx.x * kTile + item_at<kItems>(i) < a.n)
             a.to[a.hist[(key[i] >> a.shift & (kBins - 1)) * a.tiles + blockIdx.x] + rank[i]] =
                 make_uint2(key[i], place[i]);
 }
@@ -267,41 +270,43 @@ struct SmallSmem {
     uint2 item[kTile];
 };
 
-/* All passes over at most one tile of tokens, by block 0, while the other blocks write the
+/* All passes over at most 1,024 * ITEMS tokens, by block 0, while the other blocks write the
  * table's zeros (sorting 8,192 tokens takes less time than 161 MB of zeros). */
+template <uint32_t ITEMS>
 __global__ void __launch_bounds__(kSortThreads) k_sort_small(const SortArgs a, const uint32_t bits, const Fill f)
 {
     extern __shared__ uint4 smem[];
     SmallSmem& sm = *reinterpret_cast<SmallSmem*>(smem);
     grid_dependency_wait();
+    grid_launch_dependents();
     if (blockIdx.x) {
         zero_fill(f, blockIdx.x - 1, gridDim.x - 1);
         return;
     }
-    uint32_t key[kItems], place[kItems], rank[kItems], count;
+    uint32_t key[ITEMS], place[ITEMS], rank[ITEMS];
 #pragma unroll
-    for (uint32_t i = 0; i < kItems; ++i) {
-        const uint2 x = sort_item(a, item_at(i));
+    for (uint32_t i = 0; i < ITEMS; ++i) {
+        const uint2 x = sort_item(a, item_at<ITEMS>(i));
         key[i] = x.x;
         place[i] = x.y;
     }
     for (uint32_t shift = 0; shift < bits; shift += 8) {
-        rank_tile(sm.rank, key, shift, rank, count);
+        rank_tile(sm.rank, key, shift, rank);
 #pragma unroll
-        for (uint32_t i = 0; i < kItems; ++i)
+        for (uint32_t i = 0; i < ITEMS; ++i)
             sm.item[sm.rank.base[key[i] >> shift & (kBins - 1)] + rank[i]] = make_uint2(key[i], place[i]);
         __syncthreads();
 #pragma unroll
-        for (uint32_t i = 0; i < kItems; ++i) {
-            const uint2 x = sm.item[item_at(i)];
+        for (uint32_t i = 0; i < ITEMS; ++i) {
+            const uint2 x = sm.item[item_at<ITEMS>(i)];
             key[i] = x.x;
             place[i] = x.y;
         }
     }
 #pragma unroll
-    for (uint32_t i = 0; i < kItems; ++i)
-        if (item_at(i) < a.n)
-            a.to[item_at(i)] = make_uint2(key[i], place[i]);
+    for (uint32_t i = 0; i < ITEMS; ++i)
+        if (item_at<ITEMS>(i) < a.n)
+            a.to[item_at<ITEMS>(i)] = make_uint2(key[i], place[i]);
 }
 
 /* ------------------------------------------------------------------------------------ */
@@ -342,6 +347,7 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
     using T = typename Elem<DT>::T;
     __shared__ uint2 item[kPlaces + 2];  // the chunk's, between its neighbours
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t chunk = blockIdx.x, lo = chunk * kPlaces;
     const uint32_t len = a.n - lo < kPlaces ? a.n - lo : kPlaces;
     if (threadIdx.x < kPlaces + 2) {
@@ -395,19 +401,20 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
 }
 
 /* Tokens over several chunks: their partial sums in the order of the chunks.  A block looks at
- * the last tokens of 8 chunks; for each that starts in its chunk and goes on, 8 warps sum a run
- * of the partials each, over 32 places of the row's piece. */
+ * the last tokens of `per` chunks (at most 8); for each that starts in its chunk and goes on, 8
+ * warps sum a run of the partials each, over 32 places of the row's piece. */
 template <zero_dtype_t GT, bool VEC>
-__global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a)
+__global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a, const uint32_t per)
 {
     __shared__ float part[8][8][33];
     __shared__ uint32_t owner[8];  // the token, or none
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5, piece = blockIdx.y;
     if (lane == 0) {
-        const uint32_t end = (blockIdx.x * 8 + run + 1) * kPlaces;
+        const uint32_t end = (blockIdx.x * per + run + 1) * kPlaces;
         uint32_t token = 0xffffffffu;
-        if (end < a.n) {
+        if (run < per && end < a.n) {
             const uint32_t before = end > kPlaces ? a.sorted[end - kPlaces - 1].x : 0xffffffffu;
             const uint32_t last = a.sorted[end - 1].x, next = a.sorted[end].x;
             token = last < a.vocab && next == last && before != last ? last : token;
@@ -415,8 +422,8 @@ __global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a)
         owner[run] = token;
     }
     __syncthreads();
-    for (uint32_t o = 0; o < 8; ++o) {
-        const uint32_t token = owner[o], chunk = blockIdx.x * 8 + o;
+    for (uint32_t o = 0; o < per; ++o) {
+        const uint32_t token = owner[o], chunk = blockIdx.x * per + o;
         if (token == 0xffffffffu)
             continue;
         const uint32_t chunks = a.last[token] / kPlaces - chunk;  // with a partial in head[]
@@ -499,7 +506,9 @@ cudaError_t sums(const GradArgs& a, cudaStream_t s)
                                dim3(threads), 0, s, a);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(k_embedding_join<GT, VEC>, dim3((chunks + 7) / 8, (eights + 31) / 32), dim3(256), 0, s, a);
+    // a wave of blocks or two, as few chunks to a block as that allows
+    const uint32_t pieces = (eights + 31) / 32, per = chunks * pieces <= 1216 ? 1 : chunks * pieces <= 4864 ? 4 : 8;
+    return launch_pdl(k_embedding_join<GT, VEC>, dim3((chunks + per - 1) / per, pieces), dim3(256), 0, s, a, per);
 }
 
 template <zero_dtype_t DT, zero_dtype_t GT>
@@ -512,6 +521,16 @@ Fill fill_of(void* p, uint64_t bytes)
 {
     const uint64_t n16 = aligned_to(p, 16) ? bytes / 16 : 0;
     return {static_cast<uint4*>(p), n16, static_cast<uint8_t*>(p) + n16 * 16, (uint32_t)(bytes - n16 * 16)};
+}
+
+template <uint32_t ITEMS>
+cudaError_t sort_small(const SortArgs& a, uint32_t bits, const Fill& f, unsigned fillers, cudaStream_t s)
+{
+    static_assert(ITEMS <= kItems, "the tile in shared memory");
+    const cudaError_t e = allow_smem<k_sort_small<ITEMS>>();
+    return e != cudaSuccess ? e
+                            : launch_pdl(k_sort_small<ITEMS>, dim3(1 + fillers), dim3(kSortThreads), sizeof(SmallSmem), s,
+                                         a, bits, f);
 }
 
 /* Zeros over the table's gradient (bytes of it, 0: none) and the tokens' places in order. */
@@ -534,11 +553,11 @@ cudaError_t fill_and_sort(const Tokens& tokens, uint32_t n, void* table, uint64_
     const unsigned fillers = bytes ? (unsigned)(want < cap ? (want ? want : 1) : cap) : 0;
     SortArgs a{tokens, nullptr, buf[0], hist, n, tiles, 0};
     if (tiles == 1) {
-        e = allow_smem<k_sort_small>();
         sorted = buf[0];
-        return e != cudaSuccess ? e
-                                : launch_pdl(k_sort_small, dim3(1 + fillers), dim3(kSortThreads), sizeof(SmallSmem), s, a,
-                                             bits, f);
+        return n <= kSortThreads       ? sort_small<1>(a, bits, f, fillers, s)
+               : n <= 2 * kSortThreads ? sort_small<2>(a, bits, f, fillers, s)
+               : n <= 4 * kSortThreads ? sort_small<4>(a, bits, f, fillers, s)
+                                       : sort_small<8>(a, bits, f, fillers, s);
     }
     if (fillers)
         e = launch_pdl(k_zero_fill, dim3(fillers * 2), dim3(512), 0, s, f);

@@ -69,7 +69,7 @@ struct ProductArgs {
     uint32_t rows_pad, dim, dim8, vocab;
     uint32_t v0, cols;      // the piece: columns [v0, v0 + cols) of the vocabulary
     uint32_t piece;
-    uint32_t splits;        // of the sum over the piece (dhidden) or the tokens (dweight)
+    uint32_t splits;        // dweight: of the sum over the tokens
     uint32_t group;         // row tiles that share a run through the columns
     uint32_t first_piece;   // sums start here
     uint32_t grad_dtype, accumulate, vec;
@@ -81,12 +81,20 @@ struct Tile {
     uint32_t split, nt;
 };
 
+/* Into how many parts the sum over k blocks of 64 is cut: few tiles leave SMs without work, and
+ * 8 blocks at least are worth a part. */
+__host__ __device__ inline uint32_t splits_of(uint32_t tiles, uint32_t k)
+{
+    const uint32_t want = tiles && tiles < kSms / 2 ? kSms / 2 / tiles : 1, most = k / 8;
+    return want < most ? want : most > 0 ? most : 1;
+}
+
 /* The extents of a launch's tiles, known once the number of tokens with a target is. */
 template <Mode MODE>
 struct Tiles {
     uint32_t mt, nt, units, blocks, splits, group, total;
 
-    __device__ Tiles(const ProductArgs& a, uint32_t valid)
+    __device__ __forceinline__ Tiles(const ProductArgs& a, uint32_t valid)
     {
         const uint32_t m = MODE == kDweight ? a.cols : valid;
         const uint32_t k = MODE == kDweight ? valid : MODE == kDhidden ? a.cols : a.dim;
@@ -95,7 +103,7 @@ struct Tiles {
         units = (n + 31) / 32;
         nt = (n + kTileN - 1) / kTileN;
         blocks = (k + kBlockK - 1) / kBlockK;
-        splits = MODE == kStats || MODE == kD ? 1 : a.splits;
+        splits = MODE == kDhidden ? splits_of(mt * nt, blocks) : MODE == kDweight ? a.splits : 1;
         group = a.group;
         total = mt * nt * splits;
     }
@@ -279,7 +287,7 @@ __device__ __forceinline__ void put_columns(typename Elem<GT>::T* row, uint32_t 
 /* Sums in fp32 (of a piece after the first: added in L2, one launch after another), or dweight's
  * rows of the piece. */
 template <Mode MODE, bool F16>
-__device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p)
+__device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t rows)
 {
     const float post = MODE == kDweight && a.splits == 1 ? a.head->post : 1.0f;
     const uint32_t row0 = p.row - p.lane;
@@ -301,7 +309,7 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
                                                         a.accumulate, a.vec, x);
             continue;
         }
-        if (row0 >= (MODE == kDhidden ? a.rows_pad : a.cols))
+        if (row0 >= rows)
             break;
 #pragma unroll
         for (uint32_t j = 0; j < 32; ++j)
@@ -322,7 +330,7 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
                                   __float_as_uint(x[4 * q + 3]));
             stage_row<128>(p.stage, p.lane, v);
         }
-        const uint32_t first = MODE == kDhidden ? t.split * a.rows_pad : a.splits == 1 ? a.v0 : t.split * a.piece;
+        const uint32_t first = MODE == kDhidden ? t.split * rows : a.splits == 1 ? a.v0 : t.split * a.piece;
         stage_send(p.stage, p.lane, &a.out, col, first + row0, MODE == kDhidden && !a.first_piece);
     }
 }
@@ -367,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
     const uint32_t tmem = sh.tmem;
     volatile uint32_t* gave_up = &sh.gave_up;
     grid_dependency_wait();
+    grid_launch_dependents();  // the next kernel's blocks get ready as this one's leave
     const uint32_t valid = *const_cast<const volatile uint32_t*>(&a.head->valid);
     const Tiles<MODE> tiles(a, valid);
     const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2;
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                 if constexpr (MODE == kD)
                     d_epilogue<F16>(a, t, p, valid);
                 else
-                    sum_epilogue<MODE, F16>(a, t, p);
+                    sum_epilogue<MODE, F16>(a, t, p, MODE == kDhidden ? tiles.mt * kTileM : a.cols);
                 if (!p.empty)
                     release();
             }
@@ -568,25 +577,68 @@ __device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_
     return v >= 0 && v < (int)vocab ? v : -1;
 }
 
-/* The tokens that have a target, in order, by one block: each warp counts its run of tokens,
- * then writes them behind the earlier warps'. */
-__global__ void __launch_bounds__(1024) k_head_list(const ListArgs a)
+/* 8 outputs of a padded row at once, from 8 neighbours of the dense one. */
+__device__ __forceinline__ void pad_chunk(const uint16_t* from, uint16_t* to, uint32_t c, uint32_t dim)
 {
+    uint32_t x[8];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j)
+        x[j] = 8 * c + j < dim ? *const_cast<const volatile uint16_t*>(from + 8 * c + j) : 0;
+    reinterpret_cast<uint4*>(to)[c] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+}
+
+struct PadArgs {
+    const uint16_t* from;
+    uint16_t* to;
+    uint32_t rows, dim, dim8;
+};
+
+/* Block 0: the tokens that have a target, in order.  Each warp counts its run of tokens, then
+ * writes them behind the earlier warps'; up to 8,192 tokens stay in registers in between.  The
+ * other blocks, if weight's rows are not of whole 16-byte groups: those rows at a pitch that the
+ * TMA takes. */
+__global__ void __launch_bounds__(1024) k_head_list(const ListArgs a, const PadArgs pad)
+{
+    constexpr uint32_t kHeld = 8;
     __shared__ uint32_t count[32];
     __shared__ float most[32];
     grid_dependency_wait();
+    grid_launch_dependents();
+    if (blockIdx.x) {
+        const uint32_t chunks = pad.dim8 / 8;
+        const uint64_t total = (uint64_t)pad.rows * chunks, step = (uint64_t)(gridDim.x - 1) * blockDim.x;
+        for (uint64_t i = (uint64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x; i < total; i += step) {
+            const uint64_t r = i / chunks;
+            pad_chunk(pad.from + r * pad.dim, pad.to + r * pad.dim8, (uint32_t)(i - r * chunks), pad.dim);
+        }
+        return;
+    }
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t each = (a.rows + 1023) / 1024 * 32, lo = warp * each;
     const uint32_t hi = lo + each < a.rows ? lo + each : a.rows;
     const float common = a.backward ? __fmul_rn(a.scale, a.st ? *const_cast<const volatile float*>(&a.st->loss_scale) : 1.0f) : 0.0f;
     uint32_t n = 0;
     float top = 0.0f;
-#pragma unroll 4
-    for (uint32_t t = lo + lane; t < hi; t += 32) {
-        const bool there = head_target(a.targets, a.wide, a.vocab, t) >= 0;
-        n += there;
-        if (a.f16 && a.backward && there)
-            top = fmaxf(top, fabsf(a.row_scale ? __fmul_rn(common, a.row_scale[t]) : common));
+    int target[kHeld];
+    float factor[kHeld];
+    auto load = [&](uint32_t from) {  // targets and factors of 8 times 32 tokens
+#pragma unroll
+        for (uint32_t i = 0; i < kHeld; ++i) {
+            const uint32_t t = from + i * 32 + lane;
+            target[i] = t < hi ? head_target(a.targets, a.wide, a.vocab, t) : -1;
+            factor[i] = common;
+            if (a.row_scale && t < hi)
+                factor[i] = __fmul_rn(common, *const_cast<const volatile float*>(a.row_scale + t));
+        }
+    };
+    for (uint32_t from = lo; from < hi; from += kHeld * 32) {
+        load(from);
+#pragma unroll
+        for (uint32_t i = 0; i < kHeld; ++i) {
+            n += target[i] >= 0;
+            if (target[i] >= 0)
+                top = fmaxf(top, fabsf(factor[i]));
+        }
     }
     n = __reduce_add_sync(0xffffffffu, n);
 #pragma unroll
@@ -597,12 +649,13 @@ __global__ void __launch_bounds__(1024) k_head_list(const ListArgs a)
         most[warp] = top;
     }
     __syncthreads();
-    uint32_t at = 0, all = 0;
-    for (uint32_t w = 0; w < 32; ++w) {
-        at += w < warp ? count[w] : 0;
-        all += count[w];
-        top = fmaxf(top, most[w]);
-    }
+    n = count[lane];
+    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
+    const uint32_t all = __reduce_add_sync(0xffffffffu, n);
+    top = most[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // 2^e with the largest |f| / 2^e in [2^14, 2^15); what is 0 or not finite stays as it is
     float post = 1.0f;
     if (a.f16 && a.backward && top > 0.0f && top <= 3.0e38f)
@@ -613,22 +666,29 @@ __global__ void __launch_bounds__(1024) k_head_list(const ListArgs a)
         a.head->error = 0;
         a.head->post = post;
     }
-#pragma unroll 2
-    for (uint32_t t = lo + lane; t - lane < hi; t += 32) {
-        const int target = t < hi ? head_target(a.targets, a.wide, a.vocab, t) : -1;
-        const uint32_t mask = __ballot_sync(0xffffffffu, target >= 0);
-        const uint32_t r = at + __popc(mask & ((1u << lane) - 1));
-        at += __popc(mask);
-        if (target >= 0) {
-            a.token[r] = t;
-            a.target[r] = target;
-            if (a.backward) {
-                a.lse_out[r] = a.lse_in[t];
-                a.factor[r] = __fmul_rn(a.row_scale ? __fmul_rn(common, a.row_scale[t]) : common, back);
+    for (uint32_t from = lo; from < hi; from += kHeld * 32) {
+        if (each > kHeld * 32)
+            load(from);
+        float lse[kHeld];
+#pragma unroll
+        for (uint32_t i = 0; i < kHeld; ++i)
+            lse[i] = a.backward && target[i] >= 0 ? *const_cast<const volatile float*>(a.lse_in + from + i * 32 + lane) : 0.0f;
+#pragma unroll
+        for (uint32_t i = 0; i < kHeld; ++i) {
+            const uint32_t t = from + i * 32 + lane, mask = __ballot_sync(0xffffffffu, target[i] >= 0);
+            const uint32_t r = at + __popc(mask & ((1u << lane) - 1));
+            at += __popc(mask);
+            if (target[i] >= 0) {
+                a.token[r] = t;
+                a.target[r] = target[i];
+                if (a.backward) {
+                    a.lse_out[r] = lse[i];
+                    a.factor[r] = __fmul_rn(factor[i], back);
+                }
+            } else if (t < hi && !a.backward) {
+                a.loss[t] = 0.0f;
+                a.lse[t] = 0.0f;
             }
-        } else if (t < hi && !a.backward) {
-            a.loss[t] = 0.0f;
-            a.lse[t] = 0.0f;
         }
     }
 }
@@ -645,11 +705,12 @@ struct GatherArgs {
     uint64_t dhidden_stride;
 };
 
-/* Rows of the tokens that have a target next to each other, then zeros up to a multiple of
- * 128 rows; nothing where every token has one and hidden can be used as it lies. */
+/* Rows of the tokens that have a target next to each other, then zeros up to a multiple of 256
+ * rows; nothing where every token has one and hidden can be used as it lies. */
 __global__ void __launch_bounds__(256) k_head_gather(const GatherArgs a)
 {
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t valid = a.head->valid, lane = threadIdx.x & 31;
     const uint32_t warps = gridDim.x * (blockDim.x / 32), first = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
     if (a.dhidden && valid != a.rows) {
@@ -668,25 +729,18 @@ __global__ void __launch_bounds__(256) k_head_gather(const GatherArgs a)
     for (uint32_t r = first; r < end; r += warps) {
         const uint16_t* from = a.hidden + (r < valid ? a.token[r] * a.hidden_stride : 0);
         uint16_t* to = a.gathered + (uint64_t)r * a.dim8;
-        if (vec) {
-            for (uint32_t c = lane; c < a.dim / 8; c += 32)
-                reinterpret_cast<uint4*>(to)[c] = r < valid ? ld_v4(from + c * 8) : make_uint4(0, 0, 0, 0);
+        if (r >= valid) {
+            for (uint32_t c = lane; c < a.dim8 / 8; c += 32)
+                reinterpret_cast<uint4*>(to)[c] = make_uint4(0, 0, 0, 0);
+        } else if (vec) {
+#pragma unroll 4
+            for (uint32_t c = lane; c < a.dim8 / 8; c += 32)
+                reinterpret_cast<uint4*>(to)[c] = ld_v4(from + c * 8);
         } else {
-            for (uint32_t c = lane; c < a.dim8; c += 32)
-                to[c] = r < valid && c < a.dim ? from[c] : (uint16_t)0;
+            for (uint32_t c = lane; c < a.dim8 / 8; c += 32)
+                pad_chunk(from, to, c, a.dim);
         }
     }
-}
-
-/* Rows of odd length at a pitch that the TMA takes. */
-__global__ void __launch_bounds__(256) k_head_pad(const uint16_t* from, uint16_t* to, uint32_t rows, uint32_t dim,
-                                                  uint32_t dim8)
-{
-    grid_dependency_wait();
-    const uint32_t lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
-    for (uint32_t r = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < rows; r += warps)
-        for (uint32_t c = lane; c < dim8; c += 32)
-            to[(uint64_t)r * dim8 + c] = c < dim ? from[(uint64_t)r * dim + c] : (uint16_t)0;
 }
 
 struct LossArgs {
@@ -703,6 +757,7 @@ struct LossArgs {
 __global__ void __launch_bounds__(256) k_head_loss(const LossArgs a)
 {
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t valid = a.head->valid, lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
     for (uint32_t r = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); r < valid; r += warps) {
         const float2* s = a.stats + (uint64_t)r * a.tiles;
@@ -740,6 +795,7 @@ struct JoinArgs {
     void* out;
     uint64_t out_stride, split_stride;
     uint32_t rows, v0, dim, dim8, splits, accumulate;
+    uint32_t k_blocks;      // dhidden: of the first piece's sum
 };
 
 /* The splits' sums in order, times the common factor, rounded once. */
@@ -748,9 +804,14 @@ __global__ void __launch_bounds__(256) k_head_join(const JoinArgs a)
 {
     using G = typename Elem<GT>::T;
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t rows = a.token ? a.head->valid : a.rows, lane = threadIdx.x & 31;
     const float post = a.head->post;
-    const uint32_t pieces = (a.dim + 255) / 256;
+    const uint32_t pieces = (a.dim + 255) / 256, mt = (rows + kTileM - 1) / kTileM;
+    // of dhidden: the splits and their distance that the products' blocks came to; a last, narrower
+    // piece of the vocabulary may have been cut into fewer, added to the first of these
+    const uint32_t splits = a.token ? splits_of(mt * ((a.dim + kTileN - 1) / kTileN), a.k_blocks) : a.splits;
+    const uint64_t split_stride = a.token ? (uint64_t)mt * kTileM * a.dim8 : a.split_stride;
     const uint64_t warps = (uint64_t)gridDim.x * (blockDim.x / 32), total = (uint64_t)rows * pieces;
     for (uint64_t u = (uint64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); u < total; u += warps) {
         const uint32_t r = (uint32_t)(u / pieces), piece = (uint32_t)(u - (uint64_t)r * pieces);
@@ -758,8 +819,8 @@ __global__ void __launch_bounds__(256) k_head_join(const JoinArgs a)
         const float* from = a.sums + (uint64_t)r * a.dim8;
         float s[8], v[8];
         widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(from, a.dim, piece, lane, 32), s);
-        for (uint32_t k = 1; k < a.splits; ++k) {
-            widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(from + k * a.split_stride, a.dim, piece, lane, 32), v);
+        for (uint32_t k = 1; k < splits; ++k) {
+            widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(from + k * split_stride, a.dim, piece, lane, 32), v);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 s[j] = __fadd_rn(s[j], v[j]);
@@ -819,7 +880,7 @@ uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
 /* How a call is cut, and where its parts lie in the workspace. */
 struct Plan {
-    uint32_t rows_pad, dim8, piece, splits_h, splits_w;
+    uint32_t rows_pad, dim8, piece, rows_h, splits_w;
     uint64_t token, target, factor, lse, logit, gathered, weight, stats, d, sums_h, sums_w, bytes;
 };
 
@@ -845,13 +906,10 @@ Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
         }
     }
     p.piece = (uint32_t)(width * kTileN);
-    // few tiles: the sum is split so that the SMs have work, 8 blocks of 64 at least to a split
-    auto splits = [](uint64_t tiles, uint64_t k) {
-        const uint64_t want = tiles >= kSms / 2 ? 1 : kSms / 2 / tiles, most = k / (8 * kBlockK);
-        return (uint32_t)(want < most ? want : most > 0 ? most : 1);
-    };
-    p.splits_h = splits((uint64_t)p.rows_pad / kTileM * nt, p.piece);
-    p.splits_w = splits((uint64_t)p.piece / kTileM * nt, p.rows_pad);
+    p.splits_w = splits_of((uint32_t)(width * nt), p.rows_pad / kBlockK);
+    // dhidden's sums: one of all rows, or as many parts of fewer rows as the SMs take
+    p.rows_h = kSms / 2 / (uint32_t)nt * kTileM;
+    p.rows_h = p.rows_h < p.rows_pad ? p.rows_pad : p.rows_h;
     uint64_t at = sizeof(Header);
     auto take = [&](uint64_t bytes) {
         const uint64_t q = at;
@@ -870,7 +928,7 @@ Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
     const uint64_t forward = at;
     at = shared;
     p.d = take(2ull * p.rows_pad * p.piece);
-    p.sums_h = take(4ull * p.splits_h * p.rows_pad * p.dim8);
+    p.sums_h = take(4ull * p.rows_h * p.dim8);
     p.sums_w = take(p.splits_w > 1 ? 4ull * p.splits_w * p.piece * p.dim8 : 0);
     p.bytes = at > forward ? at : forward;
     return p;
@@ -962,7 +1020,11 @@ int prologue(const Call& c, const Plan& p, ListArgs l, void* dhidden, uint64_t d
     // row tiles whose hidden rows (32 MB) stay in L2 while weight passes by
     const uint64_t group = (32ull << 20) / (kTileM * 2ull * p.dim8);
     a.group = (uint32_t)(group ? group : 1);
-    cudaError_t e = launch_pdl(k_head_list, dim3(1), dim3(1024), 0, c.stream, l);
+    const PadArgs pad{static_cast<const uint16_t*>(c.weight), reinterpret_cast<uint16_t*>(c.work + p.weight), c.vocab,
+                      c.dim, p.dim8};
+    const uint64_t padders = c.dim % 8 ? ((uint64_t)c.vocab * p.dim8 / 8 + 1023) / 1024 : 0, most = 2ull * sm_count() - 1;
+    cudaError_t e = launch_pdl(k_head_list, dim3((unsigned)(1 + (padders < most ? padders : most))), dim3(1024), 0, c.stream,
+                               l, pad);
     const GatherArgs g{c.targets,
                        l.wide,
                        l.rows,
@@ -979,10 +1041,6 @@ int prologue(const Call& c, const Plan& p, ListArgs l, void* dhidden, uint64_t d
                        dhidden_stride};
     if (e == cudaSuccess)
         e = launch_pdl(k_head_gather, dim3(warps_grid(p.rows_pad)), dim3(256), 0, c.stream, g);
-    if (e == cudaSuccess && c.dim % 8)
-        e = launch_pdl(k_head_pad, dim3(warps_grid(c.vocab)), dim3(256), 0, c.stream,
-                       static_cast<const uint16_t*>(c.weight), reinterpret_cast<uint16_t*>(c.work + p.weight), c.vocab,
-                       c.dim, p.dim8);
     return rows_status(e);
 }
 
@@ -1135,7 +1193,7 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     CUtensorMap out_d, out_h, out_w;
     float *sums_h = reinterpret_cast<float*>(c.work + p.sums_h), *sums_w = reinterpret_cast<float*>(c.work + p.sums_w);
     if (!tensor_map(&out_d, c.work + p.d, dtype, p.piece, p.rows_pad, p.piece, 64, 32) ||
-        !tensor_map(&out_h, sums_h, ZERO_F32, p.dim8, (uint64_t)p.splits_h * p.rows_pad, p.dim8, 32, 32) ||
+        !tensor_map(&out_h, sums_h, ZERO_F32, p.dim8, p.rows_h, p.dim8, 32, 32) ||
         (whole && !a.dweight && !tensor_map(&out_w, dweight, grad_dtype, dim, vocab, dim, 32, 32)) ||
         (dweight && !whole &&
          !tensor_map(&out_w, sums_w, ZERO_F32, p.dim8, (uint64_t)p.splits_w * p.piece, p.dim8, 32, 32)))
@@ -1149,9 +1207,8 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
         a.out = out_d;
         e = product<kD>(a, f16, mt * ((a.cols + kTileN - 1) / kTileN), stream);
         if (e == cudaSuccess && dhidden) {
-            a.splits = p.splits_h;
             a.out = out_h;
-            e = product<kDhidden>(a, f16, mt * nd_tiles * a.splits, stream);
+            e = product<kDhidden>(a, f16, kSms / 2, stream);  // with the tokens' number it finds its tiles
         }
         if (e == cudaSuccess && dweight) {
             a.splits = p.splits_w;
@@ -1159,7 +1216,7 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
             e = product<kDweight>(a, f16, (a.cols + kTileM - 1) / kTileM * nd_tiles * a.splits, stream);
             if (e == cudaSuccess && p.splits_w > 1) {
                 const JoinArgs j{a.head, sums_w, nullptr, dweight, dim, (uint64_t)p.piece * p.dim8, a.cols, v0, dim,
-                                 p.dim8, p.splits_w, accumulate};
+                                 p.dim8, p.splits_w, accumulate, 0};
                 e = join(j, a.cols, grad_dtype, a.vec, stream);
             }
         }
@@ -1170,13 +1227,14 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
                          reinterpret_cast<const uint32_t*>(c.work + p.token),
                          dhidden,
                          dhidden_stride,
-                         (uint64_t)p.rows_pad * p.dim8,
+                         0,
                          (uint32_t)rows,
                          0,
                          dim,
                          p.dim8,
-                         p.splits_h,
-                         0};
+                         0,
+                         0,
+                         ((vocab < p.piece ? vocab : p.piece) + kBlockK - 1) / kBlockK};
         e = join(j, rows, dtype, rows_vec(dhidden, dhidden_stride, dim, dtype), stream);
     }
     return rows_status(e);

@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
     using P = typename Elem<PT>::T;
     __shared__ float slots[2][32];
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t n = blockDim.x, k = threadIdx.x, row = blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= a.rows)
         return;
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const F
     }
     __syncwarp();
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t param_words = d * sizeof(P) / 16;
     uint4 *const weight = rings, *const bias = rings + param_words;
     const uint4* ring = rings + 2 * param_words + (uint64_t)warp * stages * row_bytes / 16;
@@ -520,6 +522,7 @@ __global__ void __launch_bounds__(1024) k_layernorm_join(const JoinArgs a)
 {
     __shared__ float part[32][33];
     grid_dependency_wait();
+    grid_launch_dependents();
     const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     uint32_t col = blockIdx.x * 32 + lane;
     const uint32_t n = 2 * a.d;
