@@ -49,14 +49,18 @@ struct Header {
 };
 static_assert(sizeof(Header) == 256, "the workspace's head");
 
-enum Mode { kStats, kD, kDhidden, kDweight };
+/* What a launch forms: the losses' statistics, a piece of D, or both gradients from it. */
+enum Mode { kStats, kD, kGrads };
+/* The products behind them. */
+enum Product { kLogits, kDhidden, kDweight };
 
 struct ProductArgs {
     CUtensorMap hidden;    // the caller's rows, or (where they cannot be used as they lie) the gathered ones
     CUtensorMap gathered;  // the rows of the tokens that have a target
     CUtensorMap weight;
     CUtensorMap d;         // D's piece
-    CUtensorMap out;       // what the launch writes: D's piece, or the sums, or dweight
+    CUtensorMap out;       // what the launch writes: D's piece, or dhidden's sums
+    CUtensorMap out_w;     // and dweight, or its sums
     Header* head;
     uint32_t* state_error;  // the step state's error word, or null
     const int* target;      // [valid]
@@ -72,6 +76,7 @@ struct ProductArgs {
     uint32_t splits;        // dweight: of the sum over the tokens
     uint32_t group;         // row tiles that share a run through the columns
     uint32_t first_piece;   // sums start here
+    uint32_t want_h, want_w;
     uint32_t grad_dtype, accumulate, vec;
 };
 
@@ -79,6 +84,7 @@ struct Tile {
     uint32_t m, n, width;  // first row and column, columns
     uint32_t k0, k1;       // blocks of 64 along the sum
     uint32_t split, nt;
+    Product product;
 };
 
 /* Into how many parts the sum over k blocks of 64 is cut: few tiles leave SMs without work, and
@@ -89,21 +95,21 @@ __host__ __device__ inline uint32_t splits_of(uint32_t tiles, uint32_t k)
     return want < most ? want : most > 0 ? most : 1;
 }
 
-/* The extents of a launch's tiles, known once the number of tokens with a target is. */
-template <Mode MODE>
+/* A product's tiles, known once the number of tokens with a target is. */
+template <Product P>
 struct Tiles {
     uint32_t mt, nt, units, blocks, splits, group, total;
 
     __device__ __forceinline__ Tiles(const ProductArgs& a, uint32_t valid)
     {
-        const uint32_t m = MODE == kDweight ? a.cols : valid;
-        const uint32_t k = MODE == kDweight ? valid : MODE == kDhidden ? a.cols : a.dim;
-        const uint32_t n = MODE == kStats || MODE == kD ? a.cols : a.dim;
+        const uint32_t m = P == kDweight ? a.cols : valid;
+        const uint32_t k = P == kDweight ? valid : P == kDhidden ? a.cols : a.dim;
+        const uint32_t n = P == kLogits ? a.cols : a.dim;
         mt = (m + kTileM - 1) / kTileM;
         units = (n + 31) / 32;
         nt = (n + kTileN - 1) / kTileN;
         blocks = (k + kBlockK - 1) / kBlockK;
-        splits = MODE == kDhidden ? splits_of(mt * nt, blocks) : MODE == kDweight ? a.splits : 1;
+        splits = P == kDhidden ? splits_of(mt * nt, blocks) : P == kDweight ? a.splits : 1;
         group = a.group;
         total = mt * nt * splits;
     }
@@ -112,9 +118,10 @@ struct Tiles {
     {
         Tile r;
         uint32_t m, n;
+        r.product = P;
         r.split = t / (mt * nt);
         t -= r.split * mt * nt;
-        if (MODE == kStats || MODE == kD) {
+        if (P == kLogits) {
             // a group's rows of hidden stay in L2 while the columns pass once
             const uint32_t g = t / (group * nt), first = g * group, in = mt - first < group ? mt - first : group;
             t -= g * group * nt;
@@ -125,7 +132,7 @@ struct Tiles {
             n = t - m * nt;
         }
         r.m = m * kTileM;
-        if (MODE == kStats || MODE == kD) {
+        if (P == kLogits) {
             r.n = n * kTileN;
             r.width = kTileN;
         } else {  // dim in equal tiles, to a multiple of 32
@@ -137,6 +144,26 @@ struct Tiles {
         r.k1 = (uint32_t)((uint64_t)blocks * (r.split + 1) / splits);
         return r;
     }
+};
+
+/* A launch's tiles. */
+template <Mode MODE>
+struct Work {
+    Tiles<kLogits> logits;
+    uint32_t total;
+    __device__ __forceinline__ Work(const ProductArgs& a, uint32_t valid) : logits(a, valid), total(logits.total) {}
+    __device__ __forceinline__ Tile at(uint32_t i) const { return logits.at(i); }
+};
+template <>
+struct Work<kGrads> {
+    Tiles<kDhidden> h;
+    Tiles<kDweight> w;
+    uint32_t first_w, total;
+    __device__ __forceinline__ Work(const ProductArgs& a, uint32_t valid)
+        : h(a, valid), w(a, valid), first_w(a.want_h ? h.total : 0), total(first_w + (a.want_w ? w.total : 0))
+    {
+    }
+    __device__ __forceinline__ Tile at(uint32_t i) const { return i < first_w ? h.at(i) : w.at(i - first_w); }
 };
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -286,10 +313,10 @@ __device__ __forceinline__ void put_columns(typename Elem<GT>::T* row, uint32_t 
 
 /* Sums in fp32 (of a piece after the first: added in L2, one launch after another), or dweight's
  * rows of the piece. */
-template <Mode MODE, bool F16>
+template <Product P, bool F16>
 __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t rows)
 {
-    const float post = MODE == kDweight && a.splits == 1 ? a.head->post : 1.0f;
+    const float post = P == kDweight && a.splits == 1 ? a.head->post : 1.0f;
     const uint32_t row0 = p.row - p.lane;
 #pragma unroll 1
     for (uint32_t c = 0; c < kTileN / 2; c += 32) {
@@ -298,7 +325,7 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
             break;  // the same for the whole warp
         float x[32];
         load_part(p, c, x);
-        if (MODE == kDweight && a.dweight) {
+        if (P == kDweight && a.dweight) {
             const uint64_t row = a.v0 + p.row;
             if (p.row >= a.cols)
                 continue;
@@ -315,7 +342,7 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
         for (uint32_t j = 0; j < 32; ++j)
             x[j] = __fmul_rn(x[j], post);
         stage_wait(p.lane);
-        if (MODE == kDweight && a.splits == 1 && a.grad_dtype != ZERO_F32) {
+        if (P == kDweight && a.splits == 1 && a.grad_dtype != ZERO_F32) {
             uint4 v[4];
 #pragma unroll
             for (uint32_t q = 0; q < 4; ++q)
@@ -330,12 +357,12 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
                                   __float_as_uint(x[4 * q + 3]));
             stage_row<128>(p.stage, p.lane, v);
         }
-        const uint32_t first = MODE == kDhidden ? t.split * rows : a.splits == 1 ? a.v0 : t.split * a.piece;
-        stage_send(p.stage, p.lane, &a.out, col, first + row0, MODE == kDhidden && !a.first_piece);
+        const uint32_t first = P == kDhidden ? t.split * rows : a.splits == 1 ? a.v0 : t.split * a.piece;
+        stage_send(p.stage, p.lane, P == kDhidden ? &a.out : &a.out_w, col, first + row0, P == kDhidden && !a.first_piece);
     }
 }
 
-/* One product over all its tiles: a pair of blocks on every two SMs takes tiles of 256 x 256 in
+/* A launch's products over all their tiles: a pair of blocks on every two SMs takes tiles of 256 x 256 in
  * turn.  Warp 0 copies operands in, warp 1 of the pair's first block issues the matrix
  * instructions (one elected lane each), warps 4 to 11 take finished accumulators out while the next
  * tile's are formed in the other half of tensor memory.
@@ -347,7 +374,6 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
 template <Mode MODE, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_constant__ ProductArgs a)
 {
-    constexpr bool kAmn = MODE == kDweight, kBmn = MODE == kDhidden || MODE == kDweight;
     constexpr uint32_t kPart = MODE == kStats ? kSumBlocks : ~0u;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
@@ -377,20 +403,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
     grid_dependency_wait();
     grid_launch_dependents();  // the next kernel's blocks get ready as this one's leave
     const uint32_t valid = *const_cast<const volatile uint32_t*>(&a.head->valid);
-    const Tiles<MODE> tiles(a, valid);
+    const Work<MODE> tiles(a, valid);
     const uint32_t first = blockIdx.x / 2, step = gridDim.x / 2;
 
     if (warp == 0) {
         // what earlier kernels wrote through the generic proxy, for the TMA's reads
         asm volatile("fence.proxy.async.global;" ::: "memory");
         const CUtensorMap* hidden = valid == a.rows ? &a.hidden : &a.gathered;
-        const CUtensorMap* ma = MODE == kStats || MODE == kD ? hidden : &a.d;
-        const CUtensorMap* mb = MODE == kDweight ? hidden : &a.weight;
-        const uint32_t b0 = MODE == kDweight ? 0 : a.v0;  // weight's rows of the piece
         uint32_t issued = 0;
         bool ok = true;
         for (uint32_t i = first; ok && i < tiles.total; i += step) {
             const Tile t = tiles.at(i);
+            const bool a_mn = t.product == kDweight, b_mn = t.product != kLogits;
+            const CUtensorMap *ma = b_mn ? &a.d : hidden, *mb = a_mn ? hidden : &a.weight;
+            const uint32_t b0 = a_mn ? 0 : a.v0;  // weight's rows of the piece
             const uint32_t m = t.m + rank * kRows, n = t.n + rank * (t.width / 2), boxes = (t.width / 2 + 63) / 64;
             for (uint32_t k = t.k0; k < t.k1; ++k, ++issued) {
                 const uint32_t s = issued % kRing, turn = issued / kRing;
@@ -405,11 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                         bar_expect(smem_addr(&sh.full[s]), 2 * (2 + boxes) * kBoxBytes);
                     for (uint32_t j = 0; j < 2; ++j) {
                         const uint32_t r = m + 64 * j;
-                        tma_box(to + j * kBoxBytes, ma, (int)(kAmn ? r : kk), (int)(kAmn ? kk : r), bar);
+                        tma_box(to + j * kBoxBytes, ma, (int)(a_mn ? r : kk), (int)(a_mn ? kk : r), bar);
                     }
                     for (uint32_t j = 0; j < boxes; ++j) {
                         const uint32_t r = n + 64 * j;
-                        tma_box(to + (2 + j) * kBoxBytes, mb, (int)(kBmn ? r : kk), (int)(kBmn ? b0 + kk : b0 + r), bar);
+                        tma_box(to + (2 + j) * kBoxBytes, mb, (int)(b_mn ? r : kk), (int)(b_mn ? b0 + kk : b0 + r), bar);
                     }
                 }
                 __syncwarp();
@@ -430,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
         bool ok = true;
         for (uint32_t i = first; ok && i < tiles.total; i += step) {
             const Tile t = tiles.at(i);
-            const uint32_t idesc = instr_desc(F16, kAmn, kBmn, kTileM, t.width);
+            const bool a_mn = t.product == kDweight, b_mn = t.product != kLogits;
+            const uint32_t idesc = instr_desc(F16, a_mn, b_mn, kTileM, t.width);
             for (uint32_t k = t.k0; ok && k < t.k1; ++buf) {
                 const uint32_t b = buf & 1, turn = buf >> 1, begin = k, end = t.k1 - k > kPart ? k + kPart : t.k1;
                 if (turn && !warp_wait(smem_addr(&sh.acc_empty[b]), (turn - 1) & 1, gave_up)) {
@@ -446,11 +473,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                     }
                     tmem_fence_after();
                     const uint32_t at = stages + s * kStageBytes;
-                    const uint64_t da = operand_desc(at, kAmn), db = operand_desc(at + 2 * kBoxBytes, kBmn);
+                    const uint64_t da = operand_desc(at, a_mn), db = operand_desc(at + 2 * kBoxBytes, b_mn);
                     if (elect_one()) {
 #pragma unroll
                         for (uint32_t q = 0; q < kBlockK / 16; ++q)
-                            mma_pair(tmem + b * kTileN, da + q * k_step(kAmn), db + q * k_step(kBmn), idesc,
+                            mma_pair(tmem + b * kTileN, da + q * k_step(a_mn), db + q * k_step(b_mn), idesc,
                                      k > begin || q > 0);
                         mma_commit(smem_addr(&sh.empty[s]));
                     }
@@ -524,8 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                 }
                 if constexpr (MODE == kD)
                     d_epilogue<F16>(a, t, p, valid);
+                else if (t.product == kDhidden)
+                    sum_epilogue<kDhidden, F16>(a, t, p, tiles.h.mt * kTileM);
                 else
-                    sum_epilogue<MODE, F16>(a, t, p, MODE == kDhidden ? tiles.mt * kTileM : a.cols);
+                    sum_epilogue<kDweight, F16>(a, t, p, a.cols);
                 if (!p.empty)
                     release();
             }
@@ -550,9 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
 /* ------------------------------------------------------------------------------------ */
 /* before and after the products                                                          */
 /* ------------------------------------------------------------------------------------ */
-struct ListArgs {
+struct TokenArgs {
     const void* targets;
-    uint32_t wide, rows, rows_pad, vocab;
+    uint32_t wide, rows, vocab, dim, dim8;
+    uint32_t direct;       // hidden can be used as it lies
+    uint32_t blocks, per;  // blocks with tokens, tokens of each (a multiple of 32)
     Header* head;
     uint32_t* token;       // [valid]: the token in its place
     int* target;           // [valid]
@@ -565,6 +596,14 @@ struct ListArgs {
     const zero_step_state_t* st;
     float scale;
     uint32_t backward, f16;
+    const uint16_t* hidden;
+    uint64_t hidden_stride;
+    uint16_t* gathered;    // [rows_pad][dim8]
+    uint16_t* dhidden;     // backward: rows of tokens without a target are written 0
+    uint64_t dhidden_stride;
+    // weight's rows at a pitch that the TMA takes, where they are not of whole 16-byte groups
+    const uint16_t* weight;
+    uint16_t* padded;
 };
 
 __device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_t vocab, uint32_t t)
@@ -587,160 +626,152 @@ __device__ __forceinline__ void pad_chunk(const uint16_t* from, uint16_t* to, ui
     reinterpret_cast<uint4*>(to)[c] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
 }
 
-struct PadArgs {
-    const uint16_t* from;
-    uint16_t* to;
-    uint32_t rows, dim, dim8;
-};
-
-/* Block 0: the tokens that have a target, in order.  Each warp counts its run of tokens, then
- * writes them behind the earlier warps'; up to 8,192 tokens stay in registers in between.  The
- * other blocks, if weight's rows are not of whole 16-byte groups: those rows at a pitch that the
- * TMA takes. */
-__global__ void __launch_bounds__(1024) k_head_list(const ListArgs a, const PadArgs pad)
+/* The tokens that have a target, in order: their places, targets, factors and lse; and unless
+ * that is all of them (or hidden cannot be used as it lies) their rows next to each other, with
+ * zeros behind them up to a multiple of 256 rows.  Every block counts the targets before its own
+ * tokens itself: with 8,192 of them that is 8 loads to a thread, less than a second launch.  The
+ * blocks past `blocks` pad weight's rows. */
+__global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
 {
-    constexpr uint32_t kHeld = 8;
-    __shared__ uint32_t count[32];
+    extern __shared__ uint32_t groups[];  // of 32 own tokens: which have a target; then the count before them
+    __shared__ uint32_t before[32], total[32];
     __shared__ float most[32];
     grid_dependency_wait();
     grid_launch_dependents();
-    if (blockIdx.x) {
-        const uint32_t chunks = pad.dim8 / 8;
-        const uint64_t total = (uint64_t)pad.rows * chunks, step = (uint64_t)(gridDim.x - 1) * blockDim.x;
-        for (uint64_t i = (uint64_t)(blockIdx.x - 1) * blockDim.x + threadIdx.x; i < total; i += step) {
+    if (blockIdx.x >= a.blocks) {
+        const uint32_t chunks = a.dim8 / 8;
+        const uint64_t all = (uint64_t)a.vocab * chunks, step = (uint64_t)(gridDim.x - a.blocks) * blockDim.x;
+        for (uint64_t i = (uint64_t)(blockIdx.x - a.blocks) * blockDim.x + threadIdx.x; i < all; i += step) {
             const uint64_t r = i / chunks;
-            pad_chunk(pad.from + r * pad.dim, pad.to + r * pad.dim8, (uint32_t)(i - r * chunks), pad.dim);
+            pad_chunk(a.weight + r * a.dim, a.padded + r * a.dim8, (uint32_t)(i - r * chunks), a.dim);
         }
         return;
     }
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t each = (a.rows + 1023) / 1024 * 32, lo = warp * each;
-    const uint32_t hi = lo + each < a.rows ? lo + each : a.rows;
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_groups = a.per / 32;
+    const uint32_t lo = blockIdx.x * a.per, hi = lo + a.per < a.rows ? lo + a.per : a.rows;
     const float common = a.backward ? __fmul_rn(a.scale, a.st ? *const_cast<const volatile float*>(&a.st->loss_scale) : 1.0f) : 0.0f;
-    uint32_t n = 0;
-    float top = 0.0f;
-    int target[kHeld];
-    float factor[kHeld];
-    auto load = [&](uint32_t from) {  // targets and factors of 8 times 32 tokens
-#pragma unroll
-        for (uint32_t i = 0; i < kHeld; ++i) {
-            const uint32_t t = from + i * 32 + lane;
-            target[i] = t < hi ? head_target(a.targets, a.wide, a.vocab, t) : -1;
-            factor[i] = common;
-            if (a.row_scale && t < hi)
-                factor[i] = __fmul_rn(common, *const_cast<const volatile float*>(a.row_scale + t));
-        }
+    auto target_of = [&](uint32_t t) { return t < a.rows ? head_target(a.targets, a.wide, a.vocab, t) : -1; };
+    auto factor_of = [&](uint32_t t) {
+        return a.row_scale ? __fmul_rn(common, *const_cast<const volatile float*>(a.row_scale + t)) : common;
     };
-    for (uint32_t from = lo; from < hi; from += kHeld * 32) {
-        load(from);
+    // all targets: how many there are, how many before this block's, and the largest |f|
+    const bool scaled = a.f16 && a.backward;
+    uint32_t earlier = 0, n = 0;
+    float top = 0.0f;
+    for (uint32_t from = threadIdx.x; from < a.rows; from += 8 * 1024) {
+        int target[8];
+        float f[8];
 #pragma unroll
-        for (uint32_t i = 0; i < kHeld; ++i) {
-            n += target[i] >= 0;
-            if (target[i] >= 0)
-                top = fmaxf(top, fabsf(factor[i]));
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint32_t t = from + i * 1024;
+            target[i] = target_of(t);
+            f[i] = scaled && t < a.rows ? factor_of(t) : 0.0f;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 8; ++i) {
+            const uint32_t there = target[i] >= 0;
+            n += there;
+            earlier += from + i * 1024 < lo ? there : 0;
+            if (there)
+                top = fmaxf(top, fabsf(f[i]));
         }
     }
-    n = __reduce_add_sync(0xffffffffu, n);
+    auto warp_max = [](float x) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int o = 16; o; o >>= 1)
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        return x;
+    };
+    earlier = __reduce_add_sync(0xffffffffu, earlier);
+    n = __reduce_add_sync(0xffffffffu, n);
+    top = warp_max(top);
     if (lane == 0) {
-        count[warp] = n;
+        before[warp] = earlier;
+        total[warp] = n;
         most[warp] = top;
     }
+    for (uint32_t g = warp; g < n_groups; g += 32) {
+        const uint32_t mask = __ballot_sync(0xffffffffu, target_of(lo + 32 * g + lane) >= 0 && lo + 32 * g + lane < hi);
+        if (lane == 0)
+            groups[g] = mask;
+    }
     __syncthreads();
-    n = count[lane];
-    uint32_t at = __reduce_add_sync(0xffffffffu, lane < warp ? n : 0);
-    const uint32_t all = __reduce_add_sync(0xffffffffu, n);
-    top = most[lane];
+    const uint32_t valid = __reduce_add_sync(0xffffffffu, total[lane]);
+    top = warp_max(most[lane]);
+    uint32_t* const counts = groups + n_groups;
+    if (warp == 0) {  // the groups' counts before each
+        uint32_t at = __reduce_add_sync(0xffffffffu, before[lane]);
+        for (uint32_t g = 0; g < n_groups; g += 32) {
+            const uint32_t c = g + lane < n_groups ? __popc(groups[g + lane]) : 0;
+            uint32_t sum = c;
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+                sum += lane >= (uint32_t)o ? up : 0;
+            }
+            if (g + lane < n_groups)
+                counts[g + lane] = at + sum - c;
+            at += __shfl_sync(0xffffffffu, sum, 31);
+        }
+    }
+    __syncthreads();
     // 2^e with the largest |f| / 2^e in [2^14, 2^15); what is 0 or not finite stays as it is
     float post = 1.0f;
-    if (a.f16 && a.backward && top > 0.0f && top <= 3.0e38f)
+    if (scaled && top > 0.0f && top <= 3.0e38f)
         post = scalbnf(1.0f, max(ilogbf(top) - 14, -126));
     const float back = __fdiv_rn(1.0f, post);
-    if (threadIdx.x == 0) {
-        a.head->valid = all;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        a.head->valid = valid;
         a.head->error = 0;
         a.head->post = post;
     }
-    for (uint32_t from = lo; from < hi; from += kHeld * 32) {
-        if (each > kHeld * 32)
-            load(from);
-        float lse[kHeld];
-#pragma unroll
-        for (uint32_t i = 0; i < kHeld; ++i)
-            lse[i] = a.backward && target[i] >= 0 ? *const_cast<const volatile float*>(a.lse_in + from + i * 32 + lane) : 0.0f;
-#pragma unroll
-        for (uint32_t i = 0; i < kHeld; ++i) {
-            const uint32_t t = from + i * 32 + lane, mask = __ballot_sync(0xffffffffu, target[i] >= 0);
-            const uint32_t r = at + __popc(mask & ((1u << lane) - 1));
-            at += __popc(mask);
-            if (target[i] >= 0) {
-                a.token[r] = t;
-                a.target[r] = target[i];
-                if (a.backward) {
-                    a.lse_out[r] = lse[i];
-                    a.factor[r] = __fmul_rn(factor[i], back);
-                }
-            } else if (t < hi && !a.backward) {
-                a.loss[t] = 0.0f;
-                a.lse[t] = 0.0f;
+    for (uint32_t g = warp; g < n_groups; g += 32) {
+        const uint32_t t = lo + 32 * g + lane, mask = groups[g], r = counts[g] + __popc(mask & ((1u << lane) - 1));
+        if (t >= hi)
+            continue;
+        if (mask >> lane & 1) {
+            a.token[r] = t;
+            a.target[r] = target_of(t);
+            if (a.backward) {
+                a.lse_out[r] = *const_cast<const volatile float*>(a.lse_in + t);
+                a.factor[r] = __fmul_rn(factor_of(t), back);
             }
+        } else if (!a.backward) {
+            a.loss[t] = 0.0f;
+            a.lse[t] = 0.0f;
         }
     }
-}
-
-struct GatherArgs {
-    const void* targets;
-    uint32_t wide, rows, vocab, dim, dim8, direct;  // direct: hidden can be used as it lies
-    const Header* head;
-    const uint32_t* token;
-    const uint16_t* hidden;
-    uint64_t hidden_stride;
-    uint16_t* gathered;   // [rows_pad][dim8]
-    uint16_t* dhidden;    // backward: rows of tokens without a target are written 0
-    uint64_t dhidden_stride;
-};
-
-/* Rows of the tokens that have a target next to each other, then zeros up to a multiple of 256
- * rows; nothing where every token has one and hidden can be used as it lies. */
-__global__ void __launch_bounds__(256) k_head_gather(const GatherArgs a)
-{
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const uint32_t valid = a.head->valid, lane = threadIdx.x & 31;
-    const uint32_t warps = gridDim.x * (blockDim.x / 32), first = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-    if (a.dhidden && valid != a.rows) {
-        for (uint32_t t = first; t < a.rows; t += warps) {
-            if (head_target(a.targets, a.wide, a.vocab, t) >= 0)
-                continue;
-            uint16_t* row = a.dhidden + t * a.dhidden_stride;
-            for (uint32_t c = lane; c < a.dim; c += 32)
-                row[c] = 0;
-        }
-    }
-    if (valid == a.rows && a.direct)
+    const bool gather = valid != a.rows || !a.direct;
+    if (!gather && !(a.dhidden && valid != a.rows))
         return;
     const bool vec = a.dim % 8 == 0 && a.hidden_stride % 8 == 0 && ((uintptr_t)a.hidden & 15) == 0;
-    const uint32_t end = (valid + kTileM - 1) / kTileM * kTileM;
-    for (uint32_t r = first; r < end; r += warps) {
-        const uint16_t* from = a.hidden + (r < valid ? a.token[r] * a.hidden_stride : 0);
+    const uint32_t chunks = a.dim8 / 8;
+    for (uint32_t t = lo + warp; t < hi; t += 32) {  // a row to a warp
+        const uint32_t g = (t - lo) / 32, bit = (t - lo) % 32, mask = groups[g];
+        if (!(mask >> bit & 1)) {
+            if (a.dhidden)
+                for (uint32_t c = lane; c < a.dim; c += 32)
+                    a.dhidden[t * a.dhidden_stride + c] = 0;
+            continue;
+        }
+        if (!gather)
+            continue;
+        const uint32_t r = counts[g] + __popc(mask & ((1u << bit) - 1));
+        const uint16_t* from = a.hidden + t * a.hidden_stride;
         uint16_t* to = a.gathered + (uint64_t)r * a.dim8;
-        if (r >= valid) {
-            for (uint32_t c = lane; c < a.dim8 / 8; c += 32)
-                reinterpret_cast<uint4*>(to)[c] = make_uint4(0, 0, 0, 0);
-        } else if (vec) {
+        if (vec) {
 #pragma unroll 4
-            for (uint32_t c = lane; c < a.dim8 / 8; c += 32)
+            for (uint32_t c = lane; c < chunks; c += 32)
                 reinterpret_cast<uint4*>(to)[c] = ld_v4(from + c * 8);
         } else {
-            for (uint32_t c = lane; c < a.dim8 / 8; c += 32)
+            for (uint32_t c = lane; c < chunks; c += 32)
                 pad_chunk(from, to, c, a.dim);
         }
     }
+    const uint32_t end = (valid + kTileM - 1) / kTileM * kTileM;
+    for (uint32_t r = valid + blockIdx.x * 32 + warp; gather && r < end; r += a.blocks * 32)
+        for (uint32_t c = lane; c < chunks; c += 32)
+            reinterpret_cast<uint4*>(a.gathered + (uint64_t)r * a.dim8)[c] = make_uint4(0, 0, 0, 0);
 }
 
 struct LossArgs {
@@ -936,7 +967,8 @@ Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
 
 bool sizes_ok(uint64_t rows, uint32_t dim, uint32_t vocab)
 {
-    return rows <= (1ull << 24) && dim >= 1 && dim <= 65536 && vocab >= 1 && vocab <= (1u << 24);
+    return rows <= (1ull << 24) && dim >= 1 && dim <= 65536 && vocab >= 1 && vocab <= (1u << 24) &&
+           (rows / kTileM + 1) * (vocab / kTileN + 1) <= 1ull << 30;  // tiles are counted in 32 bits
 }
 
 struct Call {
@@ -977,23 +1009,29 @@ unsigned warps_grid(uint64_t warps)
 
 /* Lists and gathers the tokens, pads weight's rows where they need it, and fills what the
  * products of the call share. */
-int prologue(const Call& c, const Plan& p, ListArgs l, void* dhidden, uint64_t dhidden_stride, ProductArgs& a)
+int prologue(const Call& c, const Plan& p, TokenArgs l, ProductArgs& a)
 {
-    const bool f16 = c.dtype == ZERO_F16;
     Header* head = reinterpret_cast<Header*>(c.work);
     l.targets = c.targets;
     l.wide = c.target_bytes == 8;
     l.rows = (uint32_t)c.rows;
-    l.rows_pad = p.rows_pad;
     l.vocab = c.vocab;
+    l.dim = c.dim;
+    l.dim8 = p.dim8;
     l.head = head;
     l.token = reinterpret_cast<uint32_t*>(c.work + p.token);
     l.target = reinterpret_cast<int*>(c.work + p.target);
     l.lse_out = reinterpret_cast<float*>(c.work + p.lse);
     l.factor = reinterpret_cast<float*>(c.work + p.factor);
-    l.f16 = f16;
+    l.f16 = c.dtype == ZERO_F16;
     const bool direct = c.dim % 8 == 0 && c.hidden_stride % 8 == 0 && aligned_to(c.hidden, 16);
+    l.direct = direct;
+    l.hidden = static_cast<const uint16_t*>(c.hidden);
+    l.hidden_stride = c.hidden_stride;
     uint16_t* gathered = reinterpret_cast<uint16_t*>(c.work + p.gathered);
+    l.gathered = gathered;
+    l.weight = static_cast<const uint16_t*>(c.weight);
+    l.padded = reinterpret_cast<uint16_t*>(c.work + p.weight);
     const void* weight = c.dim % 8 ? c.work + p.weight : c.weight;
     memset(&a, 0, sizeof a);
     const uint64_t stride = c.rows > 1 ? c.hidden_stride : p.dim8;
@@ -1020,27 +1058,15 @@ int prologue(const Call& c, const Plan& p, ListArgs l, void* dhidden, uint64_t d
     // row tiles whose hidden rows (32 MB) stay in L2 while weight passes by
     const uint64_t group = (32ull << 20) / (kTileM * 2ull * p.dim8);
     a.group = (uint32_t)(group ? group : 1);
-    const PadArgs pad{static_cast<const uint16_t*>(c.weight), reinterpret_cast<uint16_t*>(c.work + p.weight), c.vocab,
-                      c.dim, p.dim8};
-    const uint64_t padders = c.dim % 8 ? ((uint64_t)c.vocab * p.dim8 / 8 + 1023) / 1024 : 0, most = 2ull * sm_count() - 1;
-    cudaError_t e = launch_pdl(k_head_list, dim3((unsigned)(1 + (padders < most ? padders : most))), dim3(1024), 0, c.stream,
-                               l, pad);
-    const GatherArgs g{c.targets,
-                       l.wide,
-                       l.rows,
-                       c.vocab,
-                       c.dim,
-                       p.dim8,
-                       direct,
-                       head,
-                       l.token,
-                       static_cast<const uint16_t*>(c.hidden),
-                       c.hidden_stride,
-                       gathered,
-                       static_cast<uint16_t*>(dhidden),
-                       dhidden_stride};
+    // tokens to at most a block per SM, 32 at least to each; rows to pad on a second one
+    const uint64_t sms = (uint64_t)sm_count(), want = (c.rows + 31) / 32;
+    l.blocks = (uint32_t)(want < sms ? (want ? want : 1) : sms);
+    l.per = (uint32_t)up((c.rows + l.blocks - 1) / l.blocks, 32);
+    const uint64_t padders = c.dim % 8 ? ((uint64_t)c.vocab * p.dim8 / 8 + 1023) / 1024 : 0;
+    cudaError_t e = allow_smem<k_head_tokens>();
     if (e == cudaSuccess)
-        e = launch_pdl(k_head_gather, dim3(warps_grid(p.rows_pad)), dim3(256), 0, c.stream, g);
+        e = launch_pdl(k_head_tokens, dim3((unsigned)(l.blocks + (padders < sms ? padders : sms))), dim3(1024),
+                       (size_t)l.per / 32 * 8, c.stream, l);
     return rows_status(e);
 }
 
@@ -1118,11 +1144,11 @@ int zero_head_loss(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t voc
     if (rows == 0)
         return ZERO_OK;
     const Plan p = make_plan(rows, dim, vocab);
-    ListArgs l = {};
+    TokenArgs l = {};
     l.loss = loss;
     l.lse = lse;
     ProductArgs a;
-    rc = prologue(c, p, l, nullptr, 0, a);
+    rc = prologue(c, p, l, a);
     if (rc != ZERO_OK)
         return rc;
     a.cols = vocab;
@@ -1172,14 +1198,16 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
         return ZERO_OK;
     const bool f16 = dtype == ZERO_F16;
     const Plan p = make_plan(rows, dim, vocab);
-    ListArgs l = {};
+    TokenArgs l = {};
+    l.dhidden = static_cast<uint16_t*>(dhidden);
+    l.dhidden_stride = dhidden_stride;
     l.lse_in = lse;
     l.row_scale = row_scale;
     l.st = st;
     l.scale = scale;
     l.backward = 1;
     ProductArgs a;
-    rc = prologue(c, p, l, dhidden, dhidden_stride, a);
+    rc = prologue(c, p, l, a);
     if (rc != ZERO_OK)
         return rc;
     a.state_error = st ? &st->error : nullptr;
@@ -1190,15 +1218,18 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     const bool whole = p.splits_w == 1 && dweight;
     if (whole && (accumulate || !a.vec))
         a.dweight = dweight;
-    CUtensorMap out_d, out_h, out_w;
+    a.splits = p.splits_w;
+    a.want_h = dhidden != nullptr;
+    a.want_w = dweight != nullptr;
+    CUtensorMap out_d, out_h;
     float *sums_h = reinterpret_cast<float*>(c.work + p.sums_h), *sums_w = reinterpret_cast<float*>(c.work + p.sums_w);
     if (!tensor_map(&out_d, c.work + p.d, dtype, p.piece, p.rows_pad, p.piece, 64, 32) ||
         !tensor_map(&out_h, sums_h, ZERO_F32, p.dim8, p.rows_h, p.dim8, 32, 32) ||
-        (whole && !a.dweight && !tensor_map(&out_w, dweight, grad_dtype, dim, vocab, dim, 32, 32)) ||
+        (whole && !a.dweight && !tensor_map(&a.out_w, dweight, grad_dtype, dim, vocab, dim, 32, 32)) ||
         (dweight && !whole &&
-         !tensor_map(&out_w, sums_w, ZERO_F32, p.dim8, (uint64_t)p.splits_w * p.piece, p.dim8, 32, 32)))
+         !tensor_map(&a.out_w, sums_w, ZERO_F32, p.dim8, (uint64_t)p.splits_w * p.piece, p.dim8, 32, 32)))
         return map_refused();
-    const uint64_t mt = p.rows_pad / kTileM, nd_tiles = (dim + kTileN - 1) / kTileN;
+    const uint64_t mt = p.rows_pad / kTileM;
     cudaError_t e = cudaSuccess;
     for (uint32_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += p.piece) {
         a.v0 = v0;
@@ -1206,19 +1237,14 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
         a.first_piece = v0 == 0;
         a.out = out_d;
         e = product<kD>(a, f16, mt * ((a.cols + kTileN - 1) / kTileN), stream);
-        if (e == cudaSuccess && dhidden) {
-            a.out = out_h;
-            e = product<kDhidden>(a, f16, kSms / 2, stream);  // with the tokens' number it finds its tiles
-        }
-        if (e == cudaSuccess && dweight) {
-            a.splits = p.splits_w;
-            a.out = out_w;
-            e = product<kDweight>(a, f16, (a.cols + kTileM - 1) / kTileM * nd_tiles * a.splits, stream);
-            if (e == cudaSuccess && p.splits_w > 1) {
-                const JoinArgs j{a.head, sums_w, nullptr, dweight, dim, (uint64_t)p.piece * p.dim8, a.cols, v0, dim,
-                                 p.dim8, p.splits_w, accumulate, 0};
-                e = join(j, a.cols, grad_dtype, a.vec, stream);
-            }
+        if (e != cudaSuccess)
+            break;
+        a.out = out_h;
+        e = product<kGrads>(a, f16, kSms / 2, stream);  // with the tokens' number it finds its tiles
+        if (e == cudaSuccess && dweight && p.splits_w > 1) {
+            const JoinArgs j{a.head, sums_w, nullptr, dweight, dim, (uint64_t)p.piece * p.dim8, a.cols, v0, dim,
+                             p.dim8, p.splits_w, accumulate, 0};
+            e = join(j, a.cols, grad_dtype, a.vec, stream);
         }
     }
     if (e == cudaSuccess && dhidden && rows) {

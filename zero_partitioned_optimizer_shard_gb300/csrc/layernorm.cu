@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
     using P = typename Elem<PT>::T;
     __shared__ float slots[2][32];
     grid_dependency_wait();
-    grid_launch_dependents();
     const uint32_t n = blockDim.x, k = threadIdx.x, row = blockIdx.x * blockDim.y + threadIdx.y;
     if (row >= a.rows)
         return;
@@ -155,7 +154,6 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const F
     }
     __syncwarp();
     grid_dependency_wait();
-    grid_launch_dependents();
     const uint32_t param_words = d * sizeof(P) / 16;
     uint4 *const weight = rings, *const bias = rings + param_words;
     const uint4* ring = rings + 2 * param_words + (uint64_t)warp * stages * row_bytes / 16;
