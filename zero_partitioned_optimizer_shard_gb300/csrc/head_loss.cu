@@ -28,14 +28,14 @@
 namespace zero {
 namespace {
 
-constexpr uint32_t kTileM = 256, kTileN = 256, kBlockK = 64;
+constexpr uint32_t kTileM = 256, kTileN = 256;
 constexpr uint32_t kRows = kTileM / 2;  // of a block of the pair
-constexpr uint32_t kRing = 6;
-constexpr uint32_t kStageBytes = 4 * kBoxBytes;  // 128 rows of A and half of B's, by 64
+constexpr uint32_t kRingBytes = 192 * 1024;
+constexpr uint32_t kMaxRing = 6;
 constexpr uint32_t kSumBlocks = 16;     // logits: blocks of 64 that the matrix unit sums by itself
 constexpr uint32_t kEpilogueWarps = 8, kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kOutBytes = 4096;    // of an epilogue warp: 32 rows of 128 bytes
-constexpr uint32_t kSmem = kRing * kStageBytes + kEpilogueWarps * kOutBytes + 1024;  // and to a 1,024-byte boundary
+constexpr uint32_t kSmem = kRingBytes + kEpilogueWarps * kOutBytes + 1024;  // and to a 1,024-byte boundary
 static_assert(kSmem <= 226 * 1024, "beside the barriers, of 227 KB");
 constexpr uint32_t kSms = 152;  // of a GB300: sizes the workspace and the splits
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -53,6 +53,9 @@ static_assert(sizeof(Header) == 256, "the workspace's head");
 enum Mode { kStats, kD, kGrads };
 /* The products behind them. */
 enum Product { kLogits, kDhidden, kDweight };
+/* Along the sum a stage of the ring holds 64 of the logits' and 128 of the gradients' (whose
+ * MN-major boxes are 128 of it high): 6 stages of 32 KB, or 3 of 64. */
+constexpr uint32_t kLogitsK = 64, kGradsK = 128;
 
 struct ProductArgs {
     CUtensorMap hidden;    // the caller's rows, or (where they cannot be used as they lie) the gathered ones
@@ -82,16 +85,16 @@ struct ProductArgs {
 
 struct Tile {
     uint32_t m, n, width;  // first row and column, columns
-    uint32_t k0, k1;       // blocks of 64 along the sum
+    uint32_t k0, k1;       // blocks of kLogitsK or kGradsK along the sum
     uint32_t split, nt;
     Product product;
 };
 
-/* Into how many parts the sum over k blocks of 64 is cut: few tiles leave SMs without work, and
- * 8 blocks at least are worth a part. */
+/* Into how many parts a gradient's sum over k blocks of 128 is cut: few tiles leave SMs without
+ * work, and 4 blocks at least are worth a part. */
 __host__ __device__ inline uint32_t splits_of(uint32_t tiles, uint32_t k)
 {
-    const uint32_t want = tiles && tiles < kSms / 2 ? kSms / 2 / tiles : 1, most = k / 8;
+    const uint32_t want = tiles && tiles < kSms / 2 ? kSms / 2 / tiles : 1, most = k / 4;
     return want < most ? want : most > 0 ? most : 1;
 }
 
@@ -108,7 +111,7 @@ struct Tiles {
         mt = (m + kTileM - 1) / kTileM;
         units = (n + 31) / 32;
         nt = (n + kTileN - 1) / kTileN;
-        blocks = (k + kBlockK - 1) / kBlockK;
+        blocks = P == kLogits ? (k + kLogitsK - 1) / kLogitsK : (k + kGradsK - 1) / kGradsK;
         splits = P == kDhidden ? splits_of(mt * nt, blocks) : P == kDweight ? a.splits : 1;
         group = a.group;
         total = mt * nt * splits;
@@ -174,7 +177,7 @@ __device__ __forceinline__ float exp2_approx(float x)
 }
 
 struct Shared {
-    uint64_t full[kRing], empty[kRing], acc_full[2], acc_empty[2], drain;
+    uint64_t full[kMaxRing], empty[kMaxRing], acc_full[2], acc_empty[2], drain;
     uint32_t tmem, gave_up;
 };
 
@@ -375,6 +378,9 @@ template <Mode MODE, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_constant__ ProductArgs a)
 {
     constexpr uint32_t kPart = MODE == kStats ? kSumBlocks : ~0u;
+    constexpr uint32_t kK = MODE == kGrads ? kGradsK : kLogitsK, kHalf = kK / 64 * kBoxBytes, kStageBytes = 2 * kHalf;
+    constexpr uint32_t kRing = kRingBytes / kStageBytes;
+    static_assert(kRing <= kMaxRing, "barriers");
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = block_of_pair();
@@ -417,7 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
             const bool a_mn = t.product == kDweight, b_mn = t.product != kLogits;
             const CUtensorMap *ma = b_mn ? &a.d : hidden, *mb = a_mn ? hidden : &a.weight;
             const uint32_t b0 = a_mn ? 0 : a.v0;  // weight's rows of the piece
-            const uint32_t m = t.m + rank * kRows, n = t.n + rank * (t.width / 2), boxes = (t.width / 2 + 63) / 64;
+            const uint32_t m = t.m + rank * kRows, n = t.n + rank * (t.width / 2);
+            const uint32_t boxes = b_mn ? (t.width / 2 + 63) / 64 : 1;
             for (uint32_t k = t.k0; k < t.k1; ++k, ++issued) {
                 const uint32_t s = issued % kRing, turn = issued / kRing;
                 if (turn && !warp_wait(smem_addr(&sh.empty[s]), (turn - 1) & 1, gave_up)) {
@@ -425,18 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                     break;
                 }
                 // both blocks' copies count on the first one's barrier
-                const uint32_t bar = of_first(smem_addr(&sh.full[s])), to = stages + s * kStageBytes, kk = k * kBlockK;
+                const uint32_t bar = of_first(smem_addr(&sh.full[s])), to = stages + s * kStageBytes, kk = k * kK;
                 if (elect_one()) {
                     if (rank == 0)
-                        bar_expect(smem_addr(&sh.full[s]), 2 * (2 + boxes) * kBoxBytes);
-                    for (uint32_t j = 0; j < 2; ++j) {
-                        const uint32_t r = m + 64 * j;
-                        tma_box(to + j * kBoxBytes, ma, (int)(a_mn ? r : kk), (int)(a_mn ? kk : r), bar);
-                    }
-                    for (uint32_t j = 0; j < boxes; ++j) {
-                        const uint32_t r = n + 64 * j;
-                        tma_box(to + (2 + j) * kBoxBytes, mb, (int)(b_mn ? r : kk), (int)(b_mn ? b0 + kk : b0 + r), bar);
-                    }
+                        bar_expect(smem_addr(&sh.full[s]), 2 * (kK / 64 + boxes) * kBoxBytes);
+#pragma unroll
+                    for (uint32_t j = 0; j < kK / 64; ++j)
+                        tma_box(to + j * kBoxBytes, ma, (int)(a_mn ? m + 64 * j : kk + 64 * j), (int)(a_mn ? kk : m), bar);
+                    for (uint32_t j = 0; j < boxes; ++j)
+                        tma_box(to + kHalf + j * kBoxBytes, mb, (int)(b_mn ? n + 64 * j : kk), (int)(b_mn ? b0 + kk : b0 + n),
+                                bar);
                 }
                 __syncwarp();
             }
@@ -452,12 +457,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
             }
         }
     } else if (warp == 1 && rank == 0) {
-        uint32_t used = 0, buf = 0;
-        bool ok = true;
+        uint32_t s = 0, phase = 0, buf = 0;
+        bool ok = true, ready = false;
         for (uint32_t i = first; ok && i < tiles.total; i += step) {
             const Tile t = tiles.at(i);
             const bool a_mn = t.product == kDweight, b_mn = t.product != kLogits;
             const uint32_t idesc = instr_desc(F16, a_mn, b_mn, kTileM, t.width);
+            const uint64_t desc_a = operand_desc(stages, a_mn), desc_b = operand_desc(stages + kHalf, b_mn);
             for (uint32_t k = t.k0; ok && k < t.k1; ++buf) {
                 const uint32_t b = buf & 1, turn = buf >> 1, begin = k, end = t.k1 - k > kPart ? k + kPart : t.k1;
                 if (turn && !warp_wait(smem_addr(&sh.acc_empty[b]), (turn - 1) & 1, gave_up)) {
@@ -465,23 +471,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                     break;
                 }
                 tmem_fence_after();
-                for (; k < end; ++k, ++used) {
-                    const uint32_t s = used % kRing;
-                    if (!warp_wait(smem_addr(&sh.full[s]), (used / kRing) & 1, gave_up)) {
+                for (; k < end; ++k) {
+                    if (!ready && !warp_wait(smem_addr(&sh.full[s]), phase, gave_up)) {
                         ok = false;
                         break;
                     }
                     tmem_fence_after();
-                    const uint32_t at = stages + s * kStageBytes;
-                    const uint64_t da = operand_desc(at, a_mn), db = operand_desc(at + 2 * kBoxBytes, b_mn);
+                    const uint32_t at = s;
+                    s = s + 1 == kRing ? 0 : s + 1;
+                    phase ^= s == 0;
+                    const bool next = bar_test(smem_addr(&sh.full[s]), phase);
                     if (elect_one()) {
+                        const uint64_t da = desc_a + at * (kStageBytes / 16), db = desc_b + at * (kStageBytes / 16);
 #pragma unroll
-                        for (uint32_t q = 0; q < kBlockK / 16; ++q)
-                            mma_pair(tmem + b * kTileN, da + q * k_step(a_mn), db + q * k_step(b_mn), idesc,
+                        for (uint32_t q = 0; q < kK / 16; ++q)
+                            mma_pair(tmem + b * kTileN, da + k_step(a_mn, q), db + k_step(b_mn, q), idesc,
                                      k > begin || q > 0);
-                        mma_commit(smem_addr(&sh.empty[s]));
+                        mma_commit(smem_addr(&sh.empty[at]));
                     }
-                    __syncwarp();
+                    ready = __all_sync(0xffffffffu, next);
                 }
                 if (ok && elect_one())
                     mma_commit(smem_addr(&sh.acc_full[b]));
@@ -502,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
         Part p;
         p.half = (warp - 4) / 4;
         p.lane = lane;
-        p.stage = stages + kRing * kStageBytes + (warp - 4) * kOutBytes;
+        p.stage = stages + kRingBytes + (warp - 4) * kOutBytes;
         auto acquire = [&] {
             const uint32_t b = buf & 1;
             p.acc = tmem + (quarter * 32 << 16) + b * kTileN + p.half * (kTileN / 2);
@@ -937,7 +945,7 @@ Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
         }
     }
     p.piece = (uint32_t)(width * kTileN);
-    p.splits_w = splits_of((uint32_t)(width * nt), p.rows_pad / kBlockK);
+    p.splits_w = splits_of((uint32_t)(width * nt), p.rows_pad / kGradsK);
     // dhidden's sums: one of all rows, or as many parts of fewer rows as the SMs take
     p.rows_h = kSms / 2 / (uint32_t)nt * kTileM;
     p.rows_h = p.rows_h < p.rows_pad ? p.rows_pad : p.rows_h;
@@ -1035,10 +1043,10 @@ int prologue(const Call& c, const Plan& p, TokenArgs l, ProductArgs& a)
     const void* weight = c.dim % 8 ? c.work + p.weight : c.weight;
     memset(&a, 0, sizeof a);
     const uint64_t stride = c.rows > 1 ? c.hidden_stride : p.dim8;
-    if (!tensor_map(&a.gathered, gathered, c.dtype, c.dim, p.rows_pad, p.dim8, 64, 64) ||
-        !tensor_map(&a.weight, weight, c.dtype, c.dim, c.vocab, p.dim8, 64, 64) ||
-        (l.backward && !tensor_map(&a.d, c.work + p.d, c.dtype, p.piece, p.rows_pad, p.piece, 64, 64)) ||
-        (direct && c.rows && !tensor_map(&a.hidden, c.hidden, c.dtype, c.dim, c.rows, stride, 64, 64)))
+    if (!tensor_map(&a.gathered, gathered, c.dtype, c.dim, p.rows_pad, p.dim8, 64, kBoxRows) ||
+        !tensor_map(&a.weight, weight, c.dtype, c.dim, c.vocab, p.dim8, 64, kBoxRows) ||
+        (l.backward && !tensor_map(&a.d, c.work + p.d, c.dtype, p.piece, p.rows_pad, p.piece, 64, kBoxRows)) ||
+        (direct && c.rows && !tensor_map(&a.hidden, c.hidden, c.dtype, c.dim, c.rows, stride, 64, kBoxRows)))
         return map_refused();
     if (!direct || !c.rows)
         a.hidden = a.gathered;
@@ -1260,7 +1268,7 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
                          p.dim8,
                          0,
                          0,
-                         ((vocab < p.piece ? vocab : p.piece) + kBlockK - 1) / kBlockK};
+                         ((vocab < p.piece ? vocab : p.piece) + kGradsK - 1) / kGradsK};
         e = join(j, rows, dtype, rows_vec(dhidden, dhidden_stride, dim, dtype), stream);
     }
     return rows_status(e);

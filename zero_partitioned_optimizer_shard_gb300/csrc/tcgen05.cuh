@@ -3,11 +3,13 @@
  * works on one tile, shared-memory operand tiles brought in by TMA, accumulators in tensor
  * memory, mbarriers with bounded waits.
  *
- * Operands are 16-bit tiles under the 128-byte swizzle, cut into boxes of 64 rows of 128
- * bytes (8 KB, one TMA copy each):
- *   K-major   a box is 64 rows of the operand by 64 of K; 8-row groups lie 1,024 bytes apart,
- *             a step of 16 along K is 32 bytes
- *   MN-major  a box is 64 of K by 64 of the operand's rows: each K row holds 64 neighbours.
+ * Operands are 16-bit tiles under the 128-byte swizzle, cut into boxes of 128 rows of 128 bytes
+ * (16 KB, one TMA copy each; a copy takes the SM's TMA unit about 70 cycles and 1.36 a row, so
+ * that boxes of 64 rows, measured, bring in 53 bytes a cycle and of 128 rows 67, against the 64
+ * that the matrix unit uses up on tiles of 256 x 256):
+ *   K-major   a box is 128 rows of the operand by 64 of K; 8-row groups lie 1,024 bytes apart, a
+ *             step of 16 along K is 32 bytes, the next 64 of K are the next box
+ *   MN-major  a box is 128 of K by 64 of the operand's rows: each K row holds 64 neighbours.
  *             The next 64 lie a box further, the next 8 of K 1,024 bytes, a step of 16 along
  *             K 2,048 bytes
  */
@@ -20,7 +22,7 @@
 namespace zero {
 namespace {
 
-constexpr uint32_t kBoxBytes = 8192;
+constexpr uint32_t kBoxRows = 128, kBoxBytes = 128 * kBoxRows;
 
 __device__ __forceinline__ uint64_t operand_desc(uint32_t smem, bool mn_major)
 {
@@ -28,8 +30,11 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t smem, bool mn_major)
     return (uint64_t)((smem & 0x3ffff) >> 4) | lead << 16 | (uint64_t)(1024 / 16) << 32 | 1ull << 46 | 2ull << 61;
 }
 
-/* Bytes / 16 from one step of 16 along K to the next. */
-__host__ __device__ constexpr uint32_t k_step(bool mn_major) { return mn_major ? 128 : 2; }
+/* Bytes / 16 to step q of 16 along K. */
+__device__ __forceinline__ uint32_t k_step(bool mn_major, uint32_t q)
+{
+    return mn_major ? 128 * q : q / 4 * (kBoxBytes / 16) + q % 4 * 2;
+}
 
 /* fp32 accumulation of an M x N tile; A and B both bf16 or both fp16. */
 __device__ __forceinline__ uint32_t instr_desc(bool f16, bool a_mn, bool b_mn, uint32_t m, uint32_t n)
@@ -191,6 +196,17 @@ __device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok;
+}
+
+/* The same without waiting. */
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
                  : "=r"(ok)
                  : "r"(bar), "r"(parity)
                  : "memory");
