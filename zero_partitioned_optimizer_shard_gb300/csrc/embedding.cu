@@ -16,7 +16,7 @@ namespace zero {
 namespace {
 
 constexpr uint32_t kMaxDim = 65536;
-constexpr uint32_t kPlaces = 16;      // sorted places per chunk
+constexpr uint32_t kPlaces = 16;      // sorted places per chunk, at most
 constexpr uint32_t kSortThreads = 1024;
 constexpr uint32_t kItems = 8;        // per thread and tile of the sort
 constexpr uint32_t kTile = kSortThreads * kItems;
@@ -321,6 +321,7 @@ struct GradArgs {
     void* dtable;
     uint64_t dout_stride;
     uint32_t n, d, vocab;
+    uint32_t places;      // sorted places per chunk: 16, or 8 of few tokens
     uint32_t accumulate;
     float scale;
 };
@@ -348,9 +349,9 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
     __shared__ uint2 item[kPlaces + 2];  // the chunk's, between its neighbours
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint32_t chunk = blockIdx.x, lo = chunk * kPlaces;
-    const uint32_t len = a.n - lo < kPlaces ? a.n - lo : kPlaces;
-    if (threadIdx.x < kPlaces + 2) {
+    const uint32_t chunk = blockIdx.x, lo = chunk * a.places;
+    const uint32_t len = a.n - lo < a.places ? a.n - lo : a.places;
+    if (threadIdx.x < a.places + 2) {
         const uint32_t i = lo + threadIdx.x;  // of sorted place i - 1
         item[threadIdx.x] = i >= 1 && i <= a.n ? a.sorted[i - 1] : make_uint2(0xffffffffu, 0);
     }
@@ -412,10 +413,10 @@ __global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a, const 
     grid_launch_dependents();
     const uint32_t lane = threadIdx.x & 31, run = threadIdx.x >> 5, piece = blockIdx.y;
     if (lane == 0) {
-        const uint32_t end = (blockIdx.x * per + run + 1) * kPlaces;
+        const uint32_t end = (blockIdx.x * per + run + 1) * a.places;
         uint32_t token = 0xffffffffu;
         if (run < per && end < a.n) {
-            const uint32_t before = end > kPlaces ? a.sorted[end - kPlaces - 1].x : 0xffffffffu;
+            const uint32_t before = end > a.places ? a.sorted[end - a.places - 1].x : 0xffffffffu;
             const uint32_t last = a.sorted[end - 1].x, next = a.sorted[end].x;
             token = last < a.vocab && next == last && before != last ? last : token;
         }
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a, const 
         const uint32_t token = owner[o], chunk = blockIdx.x * per + o;
         if (token == 0xffffffffu)
             continue;
-        const uint32_t chunks = a.last[token] / kPlaces - chunk;  // with a partial in head[]
+        const uint32_t chunks = a.last[token] / a.places - chunk;  // with a partial in head[]
         float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (run == 0)
             widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(a.tail + (uint64_t)chunk * a.d, a.d, piece, lane, 32), s);
@@ -461,12 +462,15 @@ struct Workspace {
     uint64_t sorted[2], hist, last, head, tail, bytes;
 };
 
+/* Few tokens: twice as many blocks, of half the length. */
+uint32_t places_of(uint64_t n) { return n <= 4096 ? kPlaces / 2 : kPlaces; }
+
 uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
 
 Workspace layout(uint64_t n, uint32_t d, uint32_t vocab)
 {
     Workspace w;
-    const uint64_t tiles = (n + kTile - 1) / kTile, chunks = (n + kPlaces - 1) / kPlaces;
+    const uint64_t tiles = (n + kTile - 1) / kTile, places = places_of(n), chunks = (n + places - 1) / places;
     uint64_t at = 0;
     auto take = [&](uint64_t bytes) {
         const uint64_t p = at;
@@ -500,7 +504,7 @@ cudaError_t lookup(const LookupArgs& a, bool vec, cudaStream_t s)
 template <zero_dtype_t DT, zero_dtype_t GT, bool VEC>
 cudaError_t sums(const GradArgs& a, cudaStream_t s)
 {
-    const uint32_t chunks = (a.n + kPlaces - 1) / kPlaces, eights = (a.d + 7) / 8;
+    const uint32_t chunks = (a.n + a.places - 1) / a.places, eights = (a.d + 7) / 8;
     const uint32_t threads = eights < 256 ? (eights + 31) / 32 * 32 : 256;
     cudaError_t e = launch_pdl(k_embedding_sum<DT, GT, VEC>, dim3(chunks, (eights + threads - 1) / threads),
                                dim3(threads), 0, s, a);
@@ -652,6 +656,7 @@ int zero_embedding_backward(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim,
                      (uint32_t)n_tokens,
                      dim,
                      vocab,
+                     places_of(n_tokens),
                      accumulate,
                      scale};
     const bool vec = rows_vec(dout, dout_stride, dim, dtype) && rows_vec(dtable, dim, dim, grad_dtype);

@@ -624,14 +624,22 @@ __device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_
     return v >= 0 && v < (int)vocab ? v : -1;
 }
 
-/* 8 outputs of a padded row at once, from 8 neighbours of the dense one. */
+/* 8 outputs of a padded row at once, from 8 neighbours of the dense one: the 32-bit words that
+ * hold at least one of them, shifted where the row starts in the middle of a word. */
 __device__ __forceinline__ void pad_chunk(const uint16_t* from, uint16_t* to, uint32_t c, uint32_t dim)
 {
-    uint32_t x[8];
+    const uint32_t odd = (uintptr_t)from >> 1 & 1, left = dim - 8 * c < 8 ? dim - 8 * c : 8;
+    const volatile uint32_t* words = reinterpret_cast<const volatile uint32_t*>(from + 8 * c - odd);
+    uint32_t w[5];
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j)
-        x[j] = 8 * c + j < dim ? *const_cast<const volatile uint16_t*>(from + 8 * c + j) : 0;
-    reinterpret_cast<uint4*>(to)[c] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+    for (uint32_t j = 0; j < 5; ++j)
+        w[j] = 2 * j < left + odd ? words[j] : 0;
+#pragma unroll
+    for (uint32_t j = 0; j < 4; ++j) {
+        w[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+        w[j] = 2 * j + 1 < left ? w[j] : 2 * j < left ? w[j] & 0xffff : 0;
+    }
+    reinterpret_cast<uint4*>(to)[c] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 /* The tokens that have a target, in order: their places, targets, factors and lse; and unless
@@ -649,6 +657,7 @@ __global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
     if (blockIdx.x >= a.blocks) {
         const uint32_t chunks = a.dim8 / 8;
         const uint64_t all = (uint64_t)a.vocab * chunks, step = (uint64_t)(gridDim.x - a.blocks) * blockDim.x;
+#pragma unroll 2
         for (uint64_t i = (uint64_t)(blockIdx.x - a.blocks) * blockDim.x + threadIdx.x; i < all; i += step) {
             const uint64_t r = i / chunks;
             pad_chunk(a.weight + r * a.dim, a.padded + r * a.dim8, (uint32_t)(i - r * chunks), a.dim);

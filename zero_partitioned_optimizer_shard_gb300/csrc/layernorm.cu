@@ -135,6 +135,33 @@ __device__ __forceinline__ typename Elem<DT>::Raw shared_chunk(const uint4* row,
     return r;
 }
 
+__device__ __forceinline__ void ring_init(uint64_t& full, uint64_t& empty, uint32_t readers)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full)));
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(&empty)), "r"(readers));
+}
+
+__device__ __forceinline__ void ring_expect(uint64_t& full, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(&full)), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ void ring_release(uint64_t& empty)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&empty)) : "memory");
+}
+
+/* At most ~2 s (wait_parity_bounded), the first look without reading the clock. */
+__device__ __forceinline__ bool ring_wait(uint64_t& bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(ok)
+                 : "r"(smem_addr(&bar)), "r"(parity)
+                 : "memory");
+    return ok || wait_parity_bounded(smem_addr(&bar), parity);
+}
+
 /* A warp per row, many rows to a warp: lane 0 bulk-copies the warp's next rows into a ring of
  * its own, so that they are on their way while one is worked on.  The weights and biases lie in
  * shared memory (read from global memory row after row they were what a warp waited for). */
@@ -260,20 +287,6 @@ struct Columns {
         }
     }
 
-    template <zero_dtype_t DT>
-    __device__ __forceinline__ void again(int i, const typename Elem<DT>::Raw& x, const typename Elem<DT>::Raw& dy,
-                                          float mean, float rstd, uint64_t (&xh)[4], uint64_t (&g)[4]) const
-    {
-        const uint64_t mean2 = f2(mean, mean), rstd2 = f2(rstd, rstd);
-        widen2<DT>(x, xh);
-        widen2<DT>(dy, g);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            xh[q] = f2_mul(f2_sub(xh[q], mean2), rstd2);
-            g[q] = f2_mul(g[q], w[i][q]);
-        }
-    }
-
     template <bool VEC>
     __device__ __forceinline__ void end(const BackwardArgs& a, uint32_t k, uint32_t n) const
     {
@@ -304,7 +317,7 @@ __device__ __forceinline__ void put_dx(int i, typename Elem<DT>::T* dx, uint32_t
     store_chunk<DT, VEC>(dx, d, i, k, n, out);
 }
 
-/* Sums of N values over the block; slots are of this turn, so one barrier is enough. */
+/* Sums of N values over the first n threads; slots are of this turn, so one barrier is enough. */
 template <int N>
 __device__ __forceinline__ void block_sums(float (&s)[N], float (&slots)[N][32], uint32_t n)
 {
@@ -319,7 +332,7 @@ __device__ __forceinline__ void block_sums(float (&s)[N], float (&slots)[N][32],
         for (int q = 0; q < N; ++q)
             slots[q][warp] = s[q];
     }
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
 #pragma unroll
     for (int q = 0; q < N; ++q)
         s[q] = warp_sum(lane < n / 32 ? slots[q][lane] : 0.0f);
@@ -339,7 +352,7 @@ __device__ __forceinline__ void block_sums4(float (&s)[4], float (&slots)[8][4],
     v = __fadd_rn(v, __shfl_xor_sync(all, v, 1));
     if ((lane & 7) == 0)
         slots[warp][lane >> 3] = v;
-    __syncthreads();
+    asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
     v = (lane & 7) < n / 32 ? slots[lane & 7][lane >> 3] : 0.0f;
     v = __fadd_rn(v, __shfl_xor_sync(all, v, 4));
     v = __fadd_rn(v, __shfl_xor_sync(all, v, 2));
@@ -401,41 +414,55 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs 
     c.template end<VEC>(a, k, n);
 }
 
-/* The same through a ring of stages of R rows of x and dy, bulk-copied ahead by thread 0: the
- * rows of the next turns are on their way while one is worked on, without registers. */
+/* The same through a ring of stages of R rows of x and dy, bulk-copied ahead by one warp more:
+ * the rows of the next turns are on their way while one is worked on, without registers. */
 template <zero_dtype_t DT, zero_dtype_t PT, int R, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const BackwardArgs a, const uint32_t stages)
 {
     using T = typename Elem<DT>::T;
     extern __shared__ uint4 ring[];
     __shared__ float slots[2][R == 2 ? 8 : 2 * R][R == 2 ? 4 : 32];
-    __shared__ uint64_t full[kRing];
-    const uint32_t n = blockDim.x, k = threadIdx.x, d = a.d, row_bytes = d * sizeof(T);
+    __shared__ uint64_t full[kRing], empty[kRing];
+    __shared__ volatile uint32_t gave_up[2];  // in even turns, in odd ones
+    const uint32_t n = blockDim.x - 32, k = threadIdx.x, d = a.d, row_bytes = d * sizeof(T);
     if (k == 0) {
         for (uint32_t q = 0; q < stages; ++q)
-            asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&full[q])));
+            ring_init(full[q], empty[q], n / 32);
+        gave_up[0] = gave_up[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
-    auto fetch = [&](uint32_t turn) {
-        const uint64_t row0 = ((uint64_t)turn * gridDim.x + blockIdx.x) * R;
-        if (row0 >= a.rows)
-            return;
-        const uint32_t rows = a.rows - row0 < R ? (uint32_t)(a.rows - row0) : R, q = turn % stages;
-        const uint32_t bar = smem_addr(&full[q]), to = smem_addr(ring) + q * 2 * R * row_bytes;
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(2 * rows * row_bytes)
-                     : "memory");
-        for (uint32_t r = 0; r < rows; ++r) {
-            bulk_load<false>(to + 2 * r * row_bytes, static_cast<const T*>(a.x) + (row0 + r) * a.x_stride, row_bytes, bar);
-            bulk_load<false>(to + (2 * r + 1) * row_bytes, static_cast<const T*>(a.dy) + (row0 + r) * a.dy_stride,
-                             row_bytes, bar);
+    const uint64_t step = (uint64_t)gridDim.x * R;
+    if (k >= n) {
+        if (k == n) {
+            uint32_t q = 0, phase = 1, sent = 0;
+            bool ok = true;
+            for (uint64_t row0 = (uint64_t)blockIdx.x * R; row0 < a.rows; row0 += step, ++sent) {
+                if (sent >= stages && !ring_wait(empty[q], phase)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t rows = a.rows - row0 < R ? (uint32_t)(a.rows - row0) : R;
+                const uint32_t bar = smem_addr(&full[q]), to = smem_addr(ring) + q * 2 * R * row_bytes;
+                ring_expect(full[q], 2 * rows * row_bytes);
+                for (uint32_t r = 0; r < rows; ++r) {
+                    bulk_load<false>(to + 2 * r * row_bytes, static_cast<const T*>(a.x) + (row0 + r) * a.x_stride,
+                                     row_bytes, bar);
+                    bulk_load<false>(to + (2 * r + 1) * row_bytes, static_cast<const T*>(a.dy) + (row0 + r) * a.dy_stride,
+                                     row_bytes, bar);
+                }
+                q = q + 1 == stages ? 0 : q + 1;
+                phase ^= q == 0;
+            }
+            if (!ok)  // what is on its way lands before the block ends
+                for (uint32_t t = sent > stages ? sent - stages : 0; t < sent; ++t)
+                    wait_parity_bounded(smem_addr(&full[t % stages]), t / stages & 1);
         }
-    };
-    if (k == 0)
-        for (uint32_t q = 0; q < stages; ++q)
-            fetch(q);
+        __syncthreads();
+        return;
+    }
     Columns<1> c;
     c.template begin<PT, true>(a, k, n);
     const float inv_d = __fdiv_rn(1.0f, (float)d);
@@ -449,12 +476,12 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
         }
     };
     statistics((uint64_t)blockIdx.x * R);
-    bool gave_up = false;
-    uint32_t turn = 0;
-    for (uint64_t row0 = (uint64_t)blockIdx.x * R; row0 < a.rows; row0 += (uint64_t)gridDim.x * R, ++turn) {
-        const uint32_t q = turn % stages;
-        const bool ok = wait_parity_bounded(smem_addr(&full[q]), turn / stages & 1);
+    uint32_t q = 0, phase = 0, turn = 0;
+    for (uint64_t row0 = (uint64_t)blockIdx.x * R; row0 < a.rows; row0 += step, turn ^= 1) {
+        if (!ring_wait(full[q], phase))
+            gave_up[turn] = 1;
         const uint4* stage = ring + (uint64_t)q * 2 * R * row_bytes / 16;
+        uint64_t xh[R][4], g[R][4];
         typename Elem<DT>::Raw x[R], dy[R];
         float s[2 * R];
 #pragma unroll
@@ -465,46 +492,42 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
                 x[r] = shared_chunk<DT>(px, k);
                 dy[r] = shared_chunk<DT>(py, k);
             }
-            uint64_t sg = 0, sx = 0, xh[4], g[4];
-            c.template add<DT>(0, x[r], dy[r], mean[r], rstd[r], xh, g, sg, sx);
+        }
+        __syncwarp();
+        if ((k & 31) == 0)
+            ring_release(empty[q]);
+        q = q + 1 == stages ? 0 : q + 1;
+        phase ^= q == 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint64_t sg = 0, sx = 0;
+            c.template add<DT>(0, x[r], dy[r], mean[r], rstd[r], xh[r], g[r], sg, sx);
             s[2 * r] = f2_sum(sg);
             s[2 * r + 1] = f2_sum(sx);
         }
-        float m[R], rs[R];
+        float rs[R];
 #pragma unroll
         for (int r = 0; r < R; ++r)
-            m[r] = mean[r], rs[r] = rstd[r];
-        statistics(row0 + (uint64_t)gridDim.x * R);  // of the next turn
-        if (__syncthreads_or(!ok)) {                 // and: this stage has been read by everyone
-            gave_up = true;
-            break;
-        }
-        if (k == 0)
-            fetch(turn + stages);
+            rs[r] = rstd[r];
+        statistics(row0 + step);  // of the next turn
         if constexpr (R == 2)
-            block_sums4(s, slots[turn & 1], n);
+            block_sums4(s, slots[turn], n);
         else
-            block_sums(s, slots[turn & 1], n);
+            block_sums(s, slots[turn], n);
+        if (gave_up[turn])  // set before the sums' barrier: the same answer in every thread
+            break;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row0 + r >= a.rows)
                 break;
-            // x and dy are kept as they came and xh and g formed again: registers for a third block
-            uint64_t xh[4], g[4];
-            c.template again<DT>(0, x[r], dy[r], m[r], rs[r], xh, g);
-            put_dx<DT, true>(0, static_cast<T*>(a.dx) + (row0 + r) * a.dx_stride, d, k, n, xh, g, rs[r],
+            put_dx<DT, true>(0, static_cast<T*>(a.dx) + (row0 + r) * a.dx_stride, d, k, n, xh[r], g[r], rs[r],
                              __fmul_rn(s[2 * r], inv_d), __fmul_rn(s[2 * r + 1], inv_d));
         }
     }
-    if (gave_up) {  // a copy did not arrive within 2 s: the weights' gradients tell, as NaN
-        if (k == 0)
-            for (uint32_t t = turn; t < turn + stages; ++t)  // the others are let land
-                if (((uint64_t)t * gridDim.x + blockIdx.x) * R < a.rows)
-                    wait_parity_bounded(smem_addr(&full[t % stages]), t / stages & 1);
-        __syncthreads();
+    if (gave_up[0] | gave_up[1])  // a copy did not arrive within 2 s: the weights' gradients tell, as NaN
         c.dw[0][0] = c.db[0][0] = f2(__int_as_float(0x7fc00000), 0.0f);
-    }
     c.template end<true>(a, k, n);
+    __syncthreads();
 }
 
 struct JoinArgs {
@@ -618,8 +641,9 @@ cudaError_t backward_blocks(const BackwardArgs& a, uint32_t threads, uint32_t ro
 template <zero_dtype_t DT, zero_dtype_t PT, bool VEC>
 cudaError_t backward(const BackwardArgs& a, uint32_t& parts, cudaStream_t s)
 {
-    const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 1024 ? (chunks + 31) / 32 * 32 : 1024;
-    if (chunks > 1024)
+    // one warp more than the chunks need copies rows in
+    const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 992 ? (chunks + 31) / 32 * 32 : 1024;
+    if (chunks > 992)
         return backward_blocks<k_layernorm_backward<DT, PT, 2, 1, VEC, 1024>>(a, n, 1, 0, parts, s);
     if constexpr (VEC) {
         // a ring of up to 48 KB: two blocks and more to an SM
@@ -628,8 +652,8 @@ cudaError_t backward(const BackwardArgs& a, uint32_t& parts, cudaStream_t s)
         stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
         const size_t smem = (size_t)stages * stage;
         return chunks <= 256
-                   ? backward_blocks<k_layernorm_backward_staged<DT, PT, 2, 256>>(a, n, 2, smem, parts, s, stages)
-                   : backward_blocks<k_layernorm_backward_staged<DT, PT, 1, 1024>>(a, n, 1, smem, parts, s, stages);
+                   ? backward_blocks<k_layernorm_backward_staged<DT, PT, 2, 288>>(a, n + 32, 2, smem, parts, s, stages)
+                   : backward_blocks<k_layernorm_backward_staged<DT, PT, 1, 1024>>(a, n + 32, 1, smem, parts, s, stages);
     } else {
         return chunks <= 256 ? backward_blocks<k_layernorm_backward<DT, PT, 1, 2, VEC, 256>>(a, n, 2, 0, parts, s)
                              : backward_blocks<k_layernorm_backward<DT, PT, 1, 1, VEC, 1024>>(a, n, 1, 0, parts, s);
