@@ -18,8 +18,8 @@
  *
  * D's 16 bits: the products take operands of hidden's type.  bf16 has fp32's range; for fp16 D
  * is scaled by a power of two so that the largest |f_t| lies just below 2^15: softmax values
- * down to 2^-29 of it stay normal numbers.  Each D is rounded once, relative error 2^-9 (bf16)
- * or 2^-12, of the size of the one rounding of the 16-bit gradients themselves.
+ * down to 2^-28 of it stay normal numbers.  Each D is rounded once, by at most 2^-8 of its value
+ * (bf16) or 2^-11 (fp16): the size of the one rounding of the 16-bit gradients themselves.
  */
 #include "tcgen05.cuh"
 
@@ -365,6 +365,12 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
     }
 }
 
+#ifdef ZERO_TEST_HOOKS
+/* Test builds only (never the product library): the first block's stage whose copies of A are
+ * withheld, so that the waits on it run out without any fault. */
+__device__ unsigned long long zero_test_withheld_head_stage = ~0ull;
+#endif
+
 /* A launch's products over all their tiles: a pair of blocks on every two SMs takes tiles of 256 x 256 in
  * turn.  Warp 0 copies operands in, warp 1 of the pair's first block issues the matrix
  * instructions (one elected lane each), warps 4 to 11 take finished accumulators out while the next
@@ -436,6 +442,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                 if (elect_one()) {
                     if (rank == 0)
                         bar_expect(smem_addr(&sh.full[s]), 2 * (kK / 64 + boxes) * kBoxBytes);
+#ifdef ZERO_TEST_HOOKS
+                    if (blockIdx.x != 0 || issued != zero_test_withheld_head_stage)
+#endif
 #pragma unroll
                     for (uint32_t j = 0; j < kK / 64; ++j)
                         tma_box(to + j * kBoxBytes, ma, (int)(a_mn ? m + 64 * j : kk + 64 * j), (int)(a_mn ? kk : m), bar);
@@ -1132,6 +1141,13 @@ cudaError_t join(const JoinArgs& j, uint64_t rows, zero_dtype_t t, bool vec, cud
 using namespace zero;
 
 extern "C" {
+
+#ifdef ZERO_TEST_HOOKS
+int zero_test_withhold_head_stage(unsigned long long stage)
+{
+    return cudaMemcpyToSymbol(zero_test_withheld_head_stage, &stage, sizeof stage) == cudaSuccess ? 0 : -4;
+}
+#endif
 
 size_t zero_head_workspace_bytes(uint64_t rows, uint32_t dim, uint32_t vocab)
 {

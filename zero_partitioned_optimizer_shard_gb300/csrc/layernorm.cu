@@ -123,6 +123,15 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
     });
 }
 
+#ifdef ZERO_TEST_HOOKS
+/* Test builds only (never the product library): the turn of the first block's first ring whose
+ * copies are withheld, so that the waits on it run out without any fault. */
+__device__ unsigned long long zero_test_withheld_norm_turn = ~0ull;
+#define ZERO_WITHHELD(turn) (blockIdx.x == 0 && (turn) == zero_test_withheld_norm_turn)
+#else
+#define ZERO_WITHHELD(turn) false
+#endif
+
 /* A chunk from shared memory. */
 template <zero_dtype_t DT>
 __device__ __forceinline__ typename Elem<DT>::Raw shared_chunk(const uint4* row, uint32_t c)
@@ -191,7 +200,8 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const F
             return;
         const uint32_t q = turn % stages, bar = smem_addr(&full[warp][q]);
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(row_bytes) : "memory");
-        bulk_load<false>(smem_addr(ring) + q * row_bytes, static_cast<const T*>(a.x) + row * a.x_stride, row_bytes, bar);
+        if (!(warp == 0 && ZERO_WITHHELD(turn)))
+            bulk_load<false>(smem_addr(ring) + q * row_bytes, static_cast<const T*>(a.x) + row * a.x_stride, row_bytes, bar);
     };
     if (lane == 0)
         for (uint32_t q = 0; q < stages; ++q)
@@ -447,7 +457,7 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
                 const uint32_t rows = a.rows - row0 < R ? (uint32_t)(a.rows - row0) : R;
                 const uint32_t bar = smem_addr(&full[q]), to = smem_addr(ring) + q * 2 * R * row_bytes;
                 ring_expect(full[q], 2 * rows * row_bytes);
-                for (uint32_t r = 0; r < rows; ++r) {
+                for (uint32_t r = 0; r < rows && !ZERO_WITHHELD(sent); ++r) {
                     bulk_load<false>(to + 2 * r * row_bytes, static_cast<const T*>(a.x) + (row0 + r) * a.x_stride,
                                      row_bytes, bar);
                     bulk_load<false>(to + (2 * r + 1) * row_bytes, static_cast<const T*>(a.dy) + (row0 + r) * a.dy_stride,
@@ -709,6 +719,13 @@ bool weight_vec(const void* p, zero_dtype_t t) { return !p || (aligned_to(p, 16)
 using namespace zero;
 
 extern "C" {
+
+#ifdef ZERO_TEST_HOOKS
+int zero_test_withhold_norm_turn(unsigned long long turn)
+{
+    return cudaMemcpyToSymbol(zero_test_withheld_norm_turn, &turn, sizeof turn) == cudaSuccess ? 0 : -4;
+}
+#endif
 
 int zero_layernorm(zero_dtype_t dtype, uint64_t rows, uint32_t dim, const void* x, uint64_t x_stride,
                    const void* weight, const void* bias, zero_dtype_t param_dtype, float eps, void* y,
