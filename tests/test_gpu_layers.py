@@ -744,3 +744,46 @@ def test_waits_that_run_out_are_told(hooked):
     assert L.zero_test_withhold_head_stage(never) == 0
     # the context is still good
     head_check(h, w, t, dh, dw)
+
+
+# ------------------------------------------------------------------------------------------
+# the example's token model
+# ------------------------------------------------------------------------------------------
+@pytest.fixture(scope="module")
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_tensors.py")
+    spec = importlib.util.spec_from_file_location("train_tensors", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_example_runs_on_tokens(example):
+    losses, opt = example.train_tokens(8, 8, vocab=503, dim=64)
+    s = z.zero_step_state_read(opt.st)
+    assert len(losses) == 8 and all(math.isfinite(x) for x in losses)
+    assert s.t == 8 and s.skip == 0 and s.error == 0 and opt.bits == 8
+
+
+def test_example_gradients(example):
+    """The token model's gradients at a loss scale, against torch's in 64 bits."""
+    vocab, dim, scale = 503, 64, 256.0
+    model, opt = example.token_model(vocab, dim, loss_scale=scale)
+    tokens, targets = example.sequence(1, vocab)
+    n = int((targets >= 0).sum())
+    (model(tokens, targets, opt.st).sum() / n).backward()
+    ref = example.TokenModel(vocab, dim, 5).double().cuda()
+    ref.load_state_dict({k: p.double() for k, p in model.state_dict().items()})
+    x = ref.table[tokens] * dim ** 0.5
+    f, (a, b) = torch.nn.functional, ref.norms
+    x = x + ref.down(f.gelu(ref.up(f.layer_norm(x, (dim,), a.weight, a.bias))))
+    logits = f.layer_norm(x, (dim,), b.weight, b.bias) @ ref.table.T
+    loss = f.cross_entropy(logits.view(-1, vocab), targets.view(-1), reduction="sum", ignore_index=-100) / n
+    (loss * scale).backward()
+    # seven roundings to bf16 on the way to the logits (up to 8 in size), the gradients' seven on the
+    # way back; each at most half a step, 2^-8, of what it rounds
+    for (name, p), q in zip(model.named_parameters(), ref.parameters()):
+        off = float((p.grad.double() - q.grad).norm() / q.grad.norm())
+        assert off <= 14 * 2.0 ** -8, (name, off)
