@@ -406,6 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
     }
     if (warp == 2)
         tmem_alloc(smem_addr(&sh.tmem), 512);
+    if (threadIdx.x == 32) {
+        map_prefetch(&a.hidden);
+        map_prefetch(&a.weight);
+        if (MODE != kStats)
+            map_prefetch(&a.out);
+        if (MODE == kGrads)
+            map_prefetch(&a.d);
+    }
     tmem_fence_before();
     __syncthreads();
     pair_sync();
@@ -876,11 +884,20 @@ __global__ void __launch_bounds__(256) k_head_join(const JoinArgs a)
         const float* from = a.sums + (uint64_t)r * a.dim8;
         float s[8], v[8];
         widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(from, a.dim, piece, lane, 32), s);
-        for (uint32_t k = 1; k < splits; ++k) {
-            widen<ZERO_F32>(load_chunk<ZERO_F32, VEC>(from + k * split_stride, a.dim, piece, lane, 32), v);
+        for (uint32_t k = 1; k < splits; k += 4) {  // four splits' loads in flight
+            typename Elem<ZERO_F32>::Raw raw[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                s[j] = __fadd_rn(s[j], v[j]);
+            for (uint32_t q = 0; q < 4; ++q)
+                raw[q] = load_chunk<ZERO_F32, VEC>(from + (k + q) * split_stride, k + q < splits ? a.dim : 0, piece, lane, 32);
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) {
+                if (k + q >= splits)
+                    break;
+                widen<ZERO_F32>(raw[q], v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s[j] = __fadd_rn(s[j], v[j]);
+            }
         }
         if (a.accumulate)
             widen<GT>(load_chunk<GT, VEC>(row, a.dim, piece, lane, 32), v);

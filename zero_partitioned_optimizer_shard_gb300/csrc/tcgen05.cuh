@@ -106,6 +106,11 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
                  : "memory");
 }
 
+__device__ __forceinline__ void map_prefetch(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 /* A warp's finished columns on their way out: written row by row (thread l: row l) under the
  * swizzle of a tensor map whose box is 32 rows of kBytes, then one bulk copy, which what lies
  * outside the tensor is cut from.  The lane that issues it also waits before the next one. */
