@@ -322,7 +322,7 @@ def head_gradients(h, w, t, there, f, dtype):
     ed = HALF[dtype] * d.abs() + f.abs()[:, None] * p * (2 * el[:, None] + 2.0 ** -16)
     ed = torch.where(there[:, None], ed, 0.0)
     if dtype == F16:
-        ed += 2.0 ** -25 * f.abs().max() * 2.0 ** -14   # below fp16's normal numbers, D scaled to 2^14
+        ed += 2.0 ** -25 * f.abs().max() * 2.0 ** -14   # below fp16's normal numbers: D's unit is 2^14
     hh, ww = torch.where(there[:, None], h.double(), 0.0), w.double()
     n, v = d.shape
     eh = ed @ ww.abs() + (v / 16 + 8) * 2.0 ** -21 * (d.abs() @ ww.abs())

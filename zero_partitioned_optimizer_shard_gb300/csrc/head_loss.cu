@@ -16,10 +16,13 @@
  * that is all of them their hidden rows are gathered, so such a token costs nothing and
  * whatever its row holds reaches no sum.
  *
- * D's 16 bits: the products take operands of hidden's type.  bf16 has fp32's range; for fp16 D
- * is scaled by a power of two so that the largest |f_t| lies just below 2^15: softmax values
- * down to 2^-28 of it stay normal numbers.  Each D is rounded once, by at most 2^-8 of its value
- * (bf16) or 2^-11 (fp16): the size of the one rounding of the 16-bit gradients themselves.
+ * D's 16 bits: the products take operands of hidden's type.  f_t goes into D in units of the
+ * largest |f_t|, the unit into the products' results: where all f_t are equal D is the softmax
+ * less 1 at the target, and nothing of f is rounded (with f inside, f's own rounding would shift
+ * every target's share the same way: 2.9e-3 of dweight in one case, 1.7e-3 without).  bf16 has
+ * fp32's range; for fp16 the unit is 2^14, so that softmax values down to 2^-28 stay normal
+ * numbers.  Each D is rounded once, by at most 2^-8 of its value (bf16) or 2^-11 (fp16): the size
+ * of the one rounding of the 16-bit gradients themselves.
  */
 #include "tcgen05.cuh"
 
@@ -44,7 +47,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct Header {
     uint32_t valid;  // tokens that have a target
     uint32_t error;  // 1: a bounded wait gave up
-    float post;      // the gradients' factor beside D (fp16: a power of two; bf16: 1)
+    float post;      // the gradients' factor beside D
     uint32_t pad[61];
 };
 static_assert(sizeof(Header) == 256, "the workspace's head");
@@ -689,7 +692,6 @@ __global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
         return a.row_scale ? __fmul_rn(common, *const_cast<const volatile float*>(a.row_scale + t)) : common;
     };
     // all targets: how many there are, how many before this block's, and the largest |f|
-    const bool scaled = a.f16 && a.backward;
     uint32_t earlier = 0, n = 0;
     float top = 0.0f;
     for (uint32_t from = threadIdx.x; from < a.rows; from += 8 * 1024) {
@@ -699,7 +701,7 @@ __global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
         for (uint32_t i = 0; i < 8; ++i) {
             const uint32_t t = from + i * 1024;
             target[i] = target_of(t);
-            f[i] = scaled && t < a.rows ? factor_of(t) : 0.0f;
+            f[i] = a.backward && t < a.rows ? factor_of(t) : 0.0f;
         }
 #pragma unroll
         for (uint32_t i = 0; i < 8; ++i) {
@@ -749,11 +751,9 @@ __global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
         }
     }
     __syncthreads();
-    // 2^e with the largest |f| / 2^e in [2^14, 2^15); what is 0 or not finite stays as it is
-    float post = 1.0f;
-    if (scaled && top > 0.0f && top <= 3.0e38f)
-        post = scalbnf(1.0f, max(ilogbf(top) - 14, -126));
-    const float back = __fdiv_rn(1.0f, post);
+    // f in units of the largest |f| (fp16: of 2^-14 of it); what is 0 or not finite stays as it is
+    const bool scaled = top > 0.0f && top <= 3.0e38f;
+    const float most_units = a.f16 ? 16384.0f : 1.0f, post = scaled ? __fdiv_rn(top, most_units) : 1.0f;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.head->valid = valid;
         a.head->error = 0;
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
             a.target[r] = target_of(t);
             if (a.backward) {
                 a.lse_out[r] = *const_cast<const volatile float*>(a.lse_in + t);
-                a.factor[r] = __fmul_rn(factor_of(t), back);
+                a.factor[r] = scaled ? __fmul_rn(__fdiv_rn(factor_of(t), top), most_units) : factor_of(t);
             }
         } else if (!a.backward) {
             a.loss[t] = 0.0f;
