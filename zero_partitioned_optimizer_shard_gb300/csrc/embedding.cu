@@ -52,40 +52,51 @@ struct LookupArgs {
     float scale;
 };
 
-/* A warp takes a piece of a row; W pieces in flight at a time. */
+/* A warp takes W neighbouring pieces of rows, all in flight at a time.  A scale of 1 leaves the
+ * values as they are, without a detour over fp32. */
 template <zero_dtype_t DT, bool VEC>
 __global__ void __launch_bounds__(256) k_embedding(const LookupArgs a)
 {
     using T = typename Elem<DT>::T;
-    constexpr int W = 4;
+    constexpr uint32_t W = 4;
     grid_dependency_wait();
     grid_launch_dependents();
     const uint32_t lane = threadIdx.x & 31;
-    const uint64_t total = (uint64_t)a.n * a.pieces;
     const uint64_t first = ((uint64_t)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5)) * W;
     uint32_t row[W], at[W], id[W];
+    row[0] = first >> 32 ? (uint32_t)(first / a.pieces) : (uint32_t)first / a.pieces;
+    at[0] = (uint32_t)(first - (uint64_t)row[0] * a.pieces);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const uint64_t u = first + i;
-        row[i] = (uint32_t)(u / a.pieces);
-        at[i] = (uint32_t)(u - (uint64_t)row[i] * a.pieces);
-        id[i] = u < total ? a.tokens.at(row[i]) : 0xffffffffu;
+    for (uint32_t i = 1; i < W; ++i) {
+        const bool next = at[i - 1] + 1 == a.pieces;
+        row[i] = row[i - 1] + next;
+        at[i] = next ? 0 : at[i - 1] + 1;
     }
+#pragma unroll
+    for (uint32_t i = 0; i < W; ++i)
+        id[i] = row[i] < a.n ? a.tokens.at(row[i]) : 0xffffffffu;
     typename Elem<DT>::Raw x[W];
 #pragma unroll
-    for (int i = 0; i < W; ++i)
+    for (uint32_t i = 0; i < W; ++i)
         x[i] = load_chunk<DT, VEC>(static_cast<const T*>(a.table) + (uint64_t)id[i] * a.d,
                                    id[i] < a.tokens.vocab ? a.d : 0, at[i], lane, 32);
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (uint32_t i = 0; i < W; ++i) {
         if (id[i] == 0xffffffffu)
             return;
+        T* out = static_cast<T*>(a.out) + row[i] * a.out_stride;
+        if (VEC && a.scale == 1.0f) {
+            const uint32_t c = at[i] * 32 + lane;
+            if (c * 8 < a.d)
+                *reinterpret_cast<typename Elem<DT>::Raw*>(out + c * 8) = x[i];
+            continue;
+        }
         float v[8];
         widen<DT>(x[i], v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)  // rows without a token: 0, whatever the scale
             v[j] = id[i] < a.tokens.vocab ? __fmul_rn(v[j], a.scale) : 0.0f;
-        store_chunk<DT, VEC>(static_cast<T*>(a.out) + row[i] * a.out_stride, a.d, at[i], lane, 32, v);
+        store_chunk<DT, VEC>(out, a.d, at[i], lane, 32, v);
     }
 }
 
