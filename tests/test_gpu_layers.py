@@ -248,6 +248,24 @@ def test_embedding_backward(n, d, v, dtype):
         assert torch.equal(again.view(torch.uint8), dtable.view(torch.uint8))  # the same bits
 
 
+@pytest.mark.parametrize("n,d,v,gt", [(3000, 1600, 33000, BF16), (8192, 64, 400_000, F32), (9000, 1600, 33000, BF16),
+                                      (1, 4096, 40000, BF16)])
+def test_embedding_backward_of_large_tables(n, d, v, gt):
+    """Tables whose zeros are written in two parts, the second beside the sums: every row is
+    written, once."""
+    g = gen(n)
+    t = ids(g, n, v, torch.int64, 0.05)
+    t[:1] = v - 1
+    t[1:2] = 0
+    dout = normal(g, n, d, dtype=BF16)
+    dtable = torch.full((v, d), float("nan"), dtype=gt, device="cuda")
+    z.zero_embedding_backward(t, dout, dtable, work_bytes(z.zero_embedding_workspace_bytes(n, d, v)))
+    there = (t >= 0) & (t < v)
+    want = torch.zeros(v, d, dtype=torch.float64, device="cuda").index_add_(0, t[there], dout[there].double())
+    size = torch.zeros(v, d, dtype=torch.float64, device="cuda").index_add_(0, t[there], dout[there].double().abs())
+    check("dtable", dtable, want, (n + 4) * U * size)
+
+
 def test_embedding_backward_edges():
     d, v = 40, 9
     table = torch.full((v, d), 3.0, device="cuda")
