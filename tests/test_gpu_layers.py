@@ -562,6 +562,51 @@ def test_a_captured_step_follows_its_inputs_and_its_loss_scale():
             assert torch.equal(x, y)
 
 
+def test_a_capture_as_the_first_call_of_a_process():
+    """No call needs one before it: everything that is looked up once is allowed in a capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, zero_partitioned_optimizer_shard_gb300 as z
+from tests import test_gpu_layers as T
+m = T.Tied(); torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    m.step()
+graph.replay(); torch.cuda.synchronize()
+other = T.Tied(); other.step(); torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(m.master + m.grads + [m.loss], other.master + other.grads + [other.loss]))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0 and "same" in done.stdout, done.stderr[-2000:]
+
+
+def test_two_captured_graphs_share_a_workspace():
+    a, b = Tied(), Tied()
+    b.work = a.work
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        Tied().step()
+    torch.cuda.synchronize()
+    graphs = []
+    for m in (a, b):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            m.step()
+    alone = Tied()
+    for k in range(3):
+        for graph in graphs:        # one after another on one stream
+            graph.replay()
+        alone.step()
+    torch.cuda.synchronize()
+    for m in (a, b):
+        for x, y in zip(m.master + m.grads + [m.loss], alone.master + alone.grads + [alone.loss]):
+            assert torch.equal(x, y)
+
+
 def test_two_streams_with_a_workspace_each():
     a, b = Tied(n=700), Tied(n=700)
     alone = Tied(n=700)
@@ -640,6 +685,24 @@ def test_views_off_the_16_byte_grid():
         head_check(h, hw, t.long(), dh, normal(g, v * d + 1)[1:].view(v, d))
         hw = normal(g, v * (d - 1) + 1, sigma=0.2, dtype=dtype)[1:].view(v, d - 1)  # odd rows: anywhere
         head_check(h[:, :d - 1], hw, t.long(), dh[:, :d - 1], normal(g, v * (d - 1) + 1, dtype=dtype)[1:].view(v, d - 1))
+
+
+def test_columns_of_one_buffer():
+    """Inputs and outputs as columns of the same rows, side by side."""
+    g = gen(22)
+    buf = normal(g, 50, 256, dtype=BF16)
+    x, y, dx = buf[:, :64], buf[:, 64:128], buf[:, 192:]
+    w, b = normal(g, 64, dtype=BF16), normal(g, 64, dtype=BF16)
+    old, mean, rstd = buf.clone(), torch.empty(50, device="cuda"), torch.empty(50, device="cuda")
+    z.zero_layernorm(x, w, b, y, mean, rstd)
+    want, m64, r64 = norm_forward(old[:, :64], w, b, 1e-5)
+    check("y", y, want, norm_bounds(old[:, :64], w, m64, r64, want)[0])
+    z.zero_layernorm_backward(x, w, mean, rstd, y, dx, None, None, work_bytes(z.zero_layernorm_workspace_bytes(50, 64)))
+    rx, ex = norm_backward(x, w, mean, rstd, y)[:2]
+    check("dx", dx, rx, ex)
+    assert torch.equal(buf[:, :64], old[:, :64]) and torch.equal(buf[:, 128:192], old[:, 128:192])
+    with pytest.raises(z.ZeroError):
+        z.zero_layernorm(x, w, b, buf[:, 63:127])
 
 
 def head_check(h, w, t, dh, dw):

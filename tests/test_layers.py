@@ -106,6 +106,13 @@ def test_refusals(lib, name):
         assert call(lib, name, change) == z.ZERO_EALIGN, change
 
 
+def test_columns_of_one_buffer_that_overlap(lib):
+    """Rows of 64 in buffers of 256 a row: y one element into x's columns, from either side, at any
+    row, is refused (that y beside them is taken, the GPU tests show)."""
+    for y in (addr(0) + 126, addr(0) - 126, addr(0) + 7 * 512 + 2, addr(0) + 8 * 512 - 126, addr(0) + 99 * 512):
+        assert call(z.lib(), "zero_layernorm", dict(x_stride=256, y_stride=256, y=y)) == z.ZERO_EINVAL, y - addr(0)
+
+
 def test_calls_without_rows_do_nothing(lib):
     nothing = dict(x=None, y=None, weight=None)
     assert call(lib, "zero_layernorm", dict(rows=0, **nothing)) == z.ZERO_OK

@@ -613,8 +613,7 @@ int zero_embedding(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim, uint32_t
     const size_t e = dtype_size(dtype);
     if (!aligned_to(tokens, token_bytes) || !aligned_to(table, e) || !aligned_to(out, e))
         return ZERO_EALIGN;
-    const uint64_t no = span(n_tokens, out_stride, dim, dtype);
-    if (overlap(out, no, table, (uint64_t)vocab * dim * e) || overlap(out, no, tokens, n_tokens * token_bytes))
+    if (!apart({{out, n_tokens, out_stride, dim, dtype}}, {{table, (uint64_t)vocab * dim * e}, {tokens, n_tokens * token_bytes}}))
         return ZERO_EINVAL;
     const LookupArgs a{{tokens, token_bytes == 8, vocab}, table, out, out_stride, (uint32_t)n_tokens, dim,
                        (dim + 255) / 256, scale};
@@ -644,10 +643,9 @@ int zero_embedding_backward(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim,
         !aligned_to(dtable, dtype_size(grad_dtype)) || !aligned_to(workspace, 16))
         return ZERO_EALIGN;
     const Workspace w = layout(n_tokens, dim, vocab);
-    const uint64_t nt = (uint64_t)vocab * dim * dtype_size(grad_dtype), no = span(n_tokens, dout_stride, dim, dtype);
-    if (overlap(dtable, nt, dout, no) || overlap(dtable, nt, tokens, n_tokens * token_bytes) ||
-        overlap(workspace, w.bytes, dout, no) || overlap(workspace, w.bytes, tokens, n_tokens * token_bytes) ||
-        overlap(workspace, w.bytes, dtable, nt))
+    const uint64_t nt = (uint64_t)vocab * dim * dtype_size(grad_dtype);
+    if (!apart({{dtable, nt}, {workspace, w.bytes}},
+               {{dout, n_tokens, dout_stride, dim, dtype}, {tokens, n_tokens * token_bytes}}))
         return ZERO_EINVAL;
     char* base = static_cast<char*>(workspace);
     uint2* buf[2] = {reinterpret_cast<uint2*>(base + w.sorted[0]), reinterpret_cast<uint2*>(base + w.sorted[1])};

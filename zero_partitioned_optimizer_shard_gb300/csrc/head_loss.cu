@@ -26,8 +26,6 @@
  */
 #include "tcgen05.cuh"
 
-#include <mutex>
-
 namespace zero {
 namespace {
 
@@ -374,10 +372,16 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
 __device__ unsigned long long zero_test_withheld_head_stage = ~0ull;
 #endif
 
-/* A launch's products over all their tiles: a pair of blocks on every two SMs takes tiles of 256 x 256 in
- * turn.  Warp 0 copies operands in, warp 1 of the pair's first block issues the matrix
- * instructions (one elected lane each), warps 4 to 11 take finished accumulators out while the next
- * tile's are formed in the other half of tensor memory.
+/* A launch's products over all their tiles: a pair of blocks on every two SMs takes tiles of
+ * 256 x 256 in turn.  Warp 0 copies operands in, warp 1 of the pair's first block issues the
+ * matrix instructions (one elected lane each), warps 4 to 11 take finished accumulators out while
+ * the next tile's are formed in the other half of tensor memory.
+ *
+ * What bounds it: a tile's matrix instructions take 512 cycles per 64 of the sum (128 for each 16,
+ * measured alone), and in them shared memory gives 32 KB of operands and takes 32 KB of the next,
+ * 128 bytes a cycle, its limit; the TMA unit needs 486 for the copies.  A long launch of logits
+ * runs at 7% above the 512 (GPT-2 1.5B's 8,192 tokens: 612-640 us for 1.32 TFLOP, 2.1 PFLOP/s).
+ * A launch has about 8 us of its own: start, first copies, last epilogue.
  *
  * The matrix unit cuts its fp32 sums off instead of rounding them, always toward 0: 256 steps
  * for a logit of 4,096 terms left the loss 1.5e-5 too small.  The losses therefore take a
@@ -1027,7 +1031,7 @@ struct Call {
     cudaStream_t stream;
 };
 
-int check_call(const Call& c, uint64_t bytes)
+int check_call(const Call& c)
 {
     if ((c.dtype != ZERO_BF16 && c.dtype != ZERO_F16) || !sizes_ok(c.rows, c.dim, c.vocab) ||
         (c.target_bytes != 4 && c.target_bytes != 8) || !c.weight || !c.work)
@@ -1037,10 +1041,6 @@ int check_call(const Call& c, uint64_t bytes)
     if (!aligned_to(c.hidden, 2) || !aligned_to(c.weight, c.dim % 8 ? 2 : 16) ||
         !aligned_to(c.targets, c.target_bytes) || !aligned_to(c.work, 256))
         return ZERO_EALIGN;
-    if (overlap(c.work, bytes, c.hidden, span(c.rows, c.hidden_stride, c.dim, c.dtype)) ||
-        overlap(c.work, bytes, c.weight, 2ull * c.vocab * c.dim) ||
-        overlap(c.work, bytes, c.targets, c.rows * c.target_bytes))
-        return ZERO_EINVAL;
     return ZERO_OK;
 }
 
@@ -1179,17 +1179,13 @@ int zero_head_loss(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t voc
     const Call c{dtype,  rows,    dim,          vocab,  hidden, hidden_stride,
                  weight, targets, target_bytes, static_cast<char*>(workspace), stream};
     const uint64_t bytes = zero_head_workspace_bytes(rows, dim, vocab);
-    int rc = check_call(c, bytes);
+    int rc = check_call(c);
     if (rc == ZERO_EINVAL || (rows && (!loss || !lse)))
         return ZERO_EINVAL;
     if (rc != ZERO_OK || !aligned_to(loss, 4) || !aligned_to(lse, 4))
         return ZERO_EALIGN;
-    const uint64_t nh = span(rows, hidden_stride, dim, dtype), nv = 2ull * vocab * dim, nt = rows * target_bytes;
-    for (const float* out : {loss, lse})
-        if (overlap(out, rows * 4, hidden, nh) || overlap(out, rows * 4, weight, nv) ||
-            overlap(out, rows * 4, targets, nt) || overlap(out, rows * 4, workspace, bytes))
-            return ZERO_EINVAL;
-    if (overlap(loss, rows * 4, lse, rows * 4))
+    if (!apart({{loss, rows * 4}, {lse, rows * 4}, {workspace, bytes}},
+               {{hidden, rows, hidden_stride, dim, dtype}, {weight, 2ull * vocab * dim}, {targets, rows * target_bytes}}))
         return ZERO_EINVAL;
     if (rows == 0)
         return ZERO_OK;
@@ -1220,7 +1216,7 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     const Call c{dtype,  rows,    dim,          vocab,  hidden, hidden_stride,
                  weight, targets, target_bytes, static_cast<char*>(workspace), stream};
     const uint64_t bytes = zero_head_workspace_bytes(rows, dim, vocab);
-    int rc = check_call(c, bytes);
+    int rc = check_call(c);
     if (rc == ZERO_EINVAL || (rows && !lse) || (!dhidden && !dweight) || accumulate > 1 ||
         (dweight && grad_dtype != dtype && grad_dtype != ZERO_F32) || !(scale >= -3.0e38f && scale <= 3.0e38f) ||
         (dhidden && ((rows > 1 && dhidden_stride < dim) || dhidden_stride > (1ull << 32))))
@@ -1229,20 +1225,15 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     if (rc != ZERO_OK || !aligned_to(lse, 4) || !aligned_to(row_scale, 4) || !aligned_to(st, 16) ||
         !aligned_to(dhidden, 2) || !aligned_to(dweight, g))
         return ZERO_EALIGN;
-    const uint64_t nh = span(rows, hidden_stride, dim, dtype), nv = 2ull * vocab * dim, nt = rows * target_bytes,
-                   nd = span(rows, dhidden_stride, dim, dtype), nw = (uint64_t)vocab * dim * g;
-    const struct {
-        const void* p;
-        uint64_t n;
-    } in[] = {{hidden, nh}, {weight, nv}, {targets, nt}, {lse, rows * 4}, {row_scale, rows * 4}, {st, sizeof *st},
-              {workspace, bytes}},
-      out[] = {{dhidden, nd}, {dweight, nw}};
-    for (const auto& o : out)
-        for (const auto& i : in)
-            if (overlap(o.p, o.n, i.p, i.n))
-                return ZERO_EINVAL;
-    if (overlap(dhidden, nd, dweight, nw) || overlap(workspace, bytes, lse, rows * 4) ||
-        overlap(workspace, bytes, row_scale, rows * 4) || overlap(workspace, bytes, st, sizeof *st))
+    if (!apart({{dhidden, rows, dhidden_stride, dim, dtype},
+                {dweight, (uint64_t)vocab * dim * g},
+                {workspace, bytes}},
+               {{hidden, rows, hidden_stride, dim, dtype},
+                {weight, 2ull * vocab * dim},
+                {targets, rows * target_bytes},
+                {lse, rows * 4},
+                {row_scale, rows * 4},
+                {st, sizeof *st}}))
         return ZERO_EINVAL;
     if (rows == 0 && (!dweight || accumulate))
         return ZERO_OK;

@@ -711,8 +711,6 @@ bool sizes_ok(uint64_t rows, uint32_t dim)
     return rows <= (1ull << 30) && dim >= 1 && dim <= kMaxDim;
 }
 
-bool weight_vec(const void* p, zero_dtype_t t) { return !p || (aligned_to(p, 16) && float_dtype(t)); }
-
 }  // namespace
 }  // namespace zero
 
@@ -743,13 +741,12 @@ int zero_layernorm(zero_dtype_t dtype, uint64_t rows, uint32_t dim, const void* 
     if (!aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, p) || !aligned_to(bias, p) ||
         !aligned_to(mean, 4) || !aligned_to(rstd, 4))
         return ZERO_EALIGN;
-    const uint64_t ny = span(rows, y_stride, dim, dtype), nx = span(rows, x_stride, dim, dtype), np = dim * p;
-    if (overlap(y, ny, x, nx) || overlap(y, ny, weight, np) || overlap(y, ny, bias, np) ||
-        overlap(y, ny, mean, rows * 4) || overlap(y, ny, rstd, rows * 4) || overlap(mean, rows * 4, rstd, rows * 4))
+    if (!apart({{y, rows, y_stride, dim, dtype}, {mean, rows * 4}, {rstd, rows * 4}},
+               {{x, rows, x_stride, dim, dtype}, {weight, dim * p}, {bias, dim * p}}))
         return ZERO_EINVAL;
     const ForwardArgs a{x, weight, bias, y, mean, rstd, x_stride, y_stride, (uint32_t)rows, dim, eps};
     const bool vec = rows_vec(x, x_stride, dim, dtype) && rows_vec(y, y_stride, dim, dtype) &&
-                     weight_vec(weight, param_dtype) && weight_vec(bias, param_dtype);
+                     aligned_to(weight, 16) && aligned_to(bias, 16);
     return rows_status(with_types(dtype, param_dtype, vec, RunForward{a, stream}));
 }
 
@@ -780,28 +777,22 @@ int zero_layernorm_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, con
         !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dweight, g) || !aligned_to(dbias, g) ||
         !aligned_to(workspace, 16))
         return ZERO_EALIGN;
-    const uint64_t nx = span(rows, x_stride, dim, dtype), ny = span(rows, dy_stride, dim, dtype),
-                   nd = span(rows, dx_stride, dim, dtype), np = dim * dtype_size(param_dtype), ng = dim * g,
-                   nw = zero_layernorm_workspace_bytes(rows, dim);
-    const struct {
-        const void* p;
-        uint64_t n;
-    } in[] = {{x, nx}, {dy, ny}, {weight, np}, {mean, rows * 4}, {rstd, rows * 4}},
-      out[] = {{dx, nd}, {dweight, ng}, {dbias, ng}, {workspace, nw}};
-    for (int i = 0; i < 4; ++i) {
-        for (const auto& b : in)
-            if (overlap(out[i].p, out[i].n, b.p, b.n))
-                return ZERO_EINVAL;
-        for (int j = 0; j < i; ++j)
-            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
-                return ZERO_EINVAL;
-    }
+    if (!apart({{dx, rows, dx_stride, dim, dtype},
+                {dweight, dim * g},
+                {dbias, dim * g},
+                {workspace, zero_layernorm_workspace_bytes(rows, dim)}},
+               {{x, rows, x_stride, dim, dtype},
+                {dy, rows, dy_stride, dim, dtype},
+                {weight, dim * dtype_size(param_dtype)},
+                {mean, rows * 4},
+                {rstd, rows * 4}}))
+        return ZERO_EINVAL;
     uint32_t parts = 0;
     if (rows) {
         const BackwardArgs a{x,        weight,    mean,      rstd,           dy, dx, static_cast<float*>(workspace),
                              x_stride, dy_stride, dx_stride, (uint32_t)rows, dim};
         const bool vec = rows_vec(x, x_stride, dim, dtype) && rows_vec(dy, dy_stride, dim, dtype) &&
-                         rows_vec(dx, dx_stride, dim, dtype) && weight_vec(weight, param_dtype);
+                         rows_vec(dx, dx_stride, dim, dtype) && aligned_to(weight, 16);
         const int rc = rows_status(with_types(dtype, param_dtype, vec, RunBackward{a, parts, stream}));
         if (rc != ZERO_OK)
             return rc;

@@ -15,6 +15,8 @@
 #include "reduce_elem.cuh"
 
 #include <atomic>
+#include <initializer_list>
+#include <string.h>
 
 namespace zero {
 namespace {
@@ -211,16 +213,43 @@ inline bool rows_vec(const void* p, uint64_t stride, uint32_t dim, zero_dtype_t 
     return aligned_to(p, 16) && stride * dtype_size(t) % 16 == 0 && dim % 8 == 0;
 }
 
-/* Bytes that rows of a strided buffer span. */
-inline uint64_t span(uint64_t rows, uint64_t stride, uint64_t dim, zero_dtype_t t)
+/* Bytes of an argument: rows of `width` bytes, each `stride` after the one before. */
+struct Area {
+    const void* p;
+    uint64_t width, rows, stride;
+
+    Area(const void* p_, uint64_t bytes) : p(p_), width(bytes), rows(1), stride(0) {}
+    Area(const void* p_, uint64_t rows_, uint64_t stride_, uint64_t dim, zero_dtype_t t)
+        : p(p_), width(rows_ ? dim * dtype_size(t) : 0), rows(rows_), stride(stride_ * dtype_size(t))
+    {
+    }
+    uint64_t span() const { return rows ? (rows - 1) * stride + width : 0; }
+};
+
+inline bool clash(const Area& a, const Area& b)
 {
-    return rows ? ((rows - 1) * stride + dim) * dtype_size(t) : 0;
+    const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+    if (!a.p || !b.p || !a.width || !b.width || x >= y + b.span() || y >= x + a.span())
+        return false;
+    if (a.rows > 1 && b.rows > 1 && a.stride == b.stride) {  // columns of one buffer, side by side
+        const uint64_t at = y >= x ? (y - x) % a.stride : (a.stride - (x - y) % a.stride) % a.stride;  // of b in a's rows
+        return at < a.width || at + b.width > a.stride;
+    }
+    return true;
 }
 
-inline bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb)
+/* No output overlaps an input or another output. */
+inline bool apart(std::initializer_list<Area> out, std::initializer_list<Area> in)
 {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return a && b && na && nb && x < y + nb && y < x + na;
+    for (const Area* o = out.begin(); o != out.end(); ++o) {
+        for (const Area& i : in)
+            if (clash(*o, i))
+                return false;
+        for (const Area* q = out.begin(); q != o; ++q)
+            if (clash(*o, *q))
+                return false;
+    }
+    return true;
 }
 
 /* Lets a kernel take all of an SM's shared memory, once per kernel and device. */
