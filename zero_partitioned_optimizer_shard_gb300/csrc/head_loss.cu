@@ -72,7 +72,7 @@ struct ProductArgs {
     const float* lse;       // [valid]
     float* target_logit;    // [valid]
     float2* stats;          // [valid][2 * column tiles]
-    void* dweight;          // where it is added to, or lies as the TMA does not take it; else null
+    void* dweight;          // one split: where it lies as the TMA does not take it, or 16 bits are added to
     uint32_t rows;          // of the call, with or without a target
     uint32_t rows_pad, dim, dim8, vocab;
     uint32_t v0, cols;      // the piece: columns [v0, v0 + cols) of the vocabulary
@@ -81,7 +81,8 @@ struct ProductArgs {
     uint32_t group;         // row tiles that share a run through the columns
     uint32_t first_piece;   // sums start here
     uint32_t want_h, want_w;
-    uint32_t grad_dtype, accumulate, vec;
+    uint32_t grad_dtype, accumulate;
+    uint32_t bulk;          // dweight leaves by bulk copies
 };
 
 struct Tile {
@@ -285,38 +286,92 @@ __device__ __forceinline__ void d_epilogue(const ProductArgs& a, const Tile& t, 
     }
 }
 
-/* 32 columns of a row of the weight's gradient. */
+/* 32 columns of a warp's 32 rows of the weight's gradient where the TMA does not take its rows:
+ * through shared memory, so that a store is 32 neighbours of a row (a lane
+ * writing its own row took 8 times as long on rows of 2,223). */
 template <zero_dtype_t GT>
-__device__ __forceinline__ void put_columns(typename Elem<GT>::T* row, uint32_t col, uint32_t dim, float post,
-                                            bool accumulate, bool vec, const float (&x)[32])
+__device__ __forceinline__ void put_rows(uint32_t stage, uint32_t lane, typename Elem<GT>::T* to, uint32_t rows, uint32_t col,
+                                         uint32_t dim, float post, bool accumulate, const float (&x)[32])
 {
+    uint4 v[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const uint32_t c = col + 8 * q;
-        float v[8];
-        if (vec) {
-            if (c >= dim)
-                return;
-            if (accumulate)
-                widen<GT>(load_chunk<GT, true>(row + c, 8, 0, 0, 1), v);
+    for (uint32_t q = 0; q < 8; ++q)
+        v[q] = make_uint4(__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]), __float_as_uint(x[4 * q + 2]),
+                          __float_as_uint(x[4 * q + 3]));
+    stage_wait(lane);  // a bulk copy of an earlier tile may still read it
+    stage_row<128>(stage, lane, v);
+    __syncwarp();
+    if (col + lane >= dim)
+        return;
+    to += col + lane;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = accumulate ? __fmaf_rn(x[8 * q + j], post, v[j]) : __fmul_rn(x[8 * q + j], post);
-            store_chunk<GT, true>(row + c, 8, 0, 0, 1, v);
-        } else {
+    for (uint32_t r0 = 0; r0 < 32; r0 += 8) {
+        float y[8], old[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (c + j < dim) {
-                    const float y = x[8 * q + j];
-                    row[c + j] = from_f32<GT>(accumulate ? __fmaf_rn(y, post, to_f32<GT>(row[c + j])) : __fmul_rn(y, post));
-                }
-            }
+        for (uint32_t r = 0; r < 8; ++r) {
+            asm volatile("ld.shared.f32 %0, [%1];"
+                         : "=f"(y[r])
+                         : "r"(stage + (r0 + r) * 128 + ((lane / 4 ^ r) << 4) + lane % 4 * 4));
+            old[r] = accumulate && r0 + r < rows ? to_f32<GT>(to[(uint64_t)(r0 + r) * dim]) : 0.0f;
         }
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r)
+            if (r0 + r < rows)
+                to[(uint64_t)(r0 + r) * dim] = from_f32<GT>(accumulate ? __fmaf_rn(y[r], post, old[r]) : __fmul_rn(y[r], post));
+    }
+}
+
+/* 16-bit rows of dweight that are added to: what a lane's row holds now in the tile's 128 columns,
+ * asked for before the tile's sums are waited for (asked for afterwards, 32 columns at a time, it
+ * took 358 us instead of 75 to add 10 tokens' gradient to 74 MB). */
+struct OldRow {
+    uint4 v[16];
+
+    __device__ __forceinline__ void load(const ProductArgs& a, const Tile& t, const Part& p)
+    {
+        const uint32_t col = t.n + p.half * (kTileN / 2);
+        const uint16_t* row = static_cast<const uint16_t*>(a.dweight) + (uint64_t)(a.v0 + p.row) * a.dim + col;
+#pragma unroll
+        for (uint32_t q = 0; q < 16; ++q) {
+            const bool in = p.row < a.cols && p.half * (kTileN / 2) + 8 * q < t.width && col + 8 * q < a.dim;
+            v[q] = in ? ld_v4(row + 8 * q) : make_uint4(0, 0, 0, 0);
+        }
+    }
+};
+
+template <bool F16>
+__device__ __forceinline__ void add_epilogue(const ProductArgs& a, const Tile& t, const Part& p, const OldRow& old)
+{
+    constexpr zero_dtype_t GT = F16 ? ZERO_F16 : ZERO_BF16;
+    const float post = a.head->post;
+    const uint32_t row0 = p.row - p.lane;
+#pragma unroll
+    for (uint32_t c = 0; c < kTileN / 2; c += 32) {
+        const uint32_t at = p.half * (kTileN / 2) + c, col = t.n + at;
+        if (at >= t.width || col >= a.dim || row0 >= a.cols)
+            break;  // the same for the whole warp
+        float x[32];
+        load_part(p, c, x);
+        uint4 v[4];
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q) {
+            typename Elem<GT>::Raw raw;
+            float o[8];
+            raw.v = old.v[c / 8 + q];
+            widen<GT>(raw, o);
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j)
+                o[j] = __fmaf_rn(x[8 * q + j], post, o[j]);
+            v[q] = narrow<GT>(o).v;
+        }
+        stage_wait(p.lane);
+        stage_row<64>(p.stage, p.lane, v);
+        stage_send(p.stage, p.lane, &a.out_w, col, a.v0 + row0, false);
     }
 }
 
 /* Sums in fp32 (of a piece after the first: added in L2, one launch after another), or dweight's
- * rows of the piece. */
+ * rows of the piece (fp32 ones that are added to: in L2 too). */
 template <Product P, bool F16>
 __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t rows)
 {
@@ -329,19 +384,18 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
             break;  // the same for the whole warp
         float x[32];
         load_part(p, c, x);
-        if (P == kDweight && a.dweight) {
-            const uint64_t row = a.v0 + p.row;
-            if (p.row >= a.cols)
-                continue;
-            if (a.grad_dtype == ZERO_F32)
-                put_columns<ZERO_F32>(static_cast<float*>(a.dweight) + row * a.dim, col, a.dim, post, a.accumulate, a.vec, x);
-            else
-                put_columns<F16 ? ZERO_F16 : ZERO_BF16>(static_cast<uint16_t*>(a.dweight) + row * a.dim, col, a.dim, post,
-                                                        a.accumulate, a.vec, x);
-            continue;
-        }
         if (row0 >= rows)
             break;
+        if (P == kDweight && a.splits == 1 && !a.bulk) {
+            const uint64_t at_row = (uint64_t)(a.v0 + row0) * a.dim;
+            if (a.grad_dtype == ZERO_F32)
+                put_rows<ZERO_F32>(p.stage, p.lane, static_cast<float*>(a.dweight) + at_row, rows - row0, col, a.dim, post,
+                                   a.accumulate, x);
+            else
+                put_rows<F16 ? ZERO_F16 : ZERO_BF16>(p.stage, p.lane, static_cast<uint16_t*>(a.dweight) + at_row, rows - row0,
+                                                     col, a.dim, post, a.accumulate, x);
+            continue;
+        }
 #pragma unroll
         for (uint32_t j = 0; j < 32; ++j)
             x[j] = __fmul_rn(x[j], post);
@@ -362,7 +416,8 @@ __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t
             stage_row<128>(p.stage, p.lane, v);
         }
         const uint32_t first = P == kDhidden ? t.split * rows : a.splits == 1 ? a.v0 : t.split * a.piece;
-        stage_send(p.stage, p.lane, P == kDhidden ? &a.out : &a.out_w, col, first + row0, P == kDhidden && !a.first_piece);
+        stage_send(p.stage, p.lane, P == kDhidden ? &a.out : &a.out_w, col, first + row0,
+                   P == kDhidden ? !a.first_piece : a.splits == 1 && a.accumulate);
     }
 }
 
@@ -576,6 +631,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                     break;
                 stats_epilogue(a, t, p, valid, x);
             } else {
+                OldRow old;
+                const bool add16 = MODE == kGrads && t.product == kDweight && a.bulk && a.accumulate && a.grad_dtype != ZERO_F32;
+                if (add16)
+                    old.load(a, t, p);
                 if (!p.empty) {
                     acquire();
                     if (!ok)
@@ -585,6 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                     d_epilogue<F16>(a, t, p, valid);
                 else if (t.product == kDhidden)
                     sum_epilogue<kDhidden, F16>(a, t, p, tiles.h.mt * kTileM);
+                else if (add16)
+                    add_epilogue<F16>(a, t, p, old);
                 else
                     sum_epilogue<kDweight, F16>(a, t, p, a.cols);
                 if (!p.empty)
@@ -650,44 +711,41 @@ __device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_
 
 /* 8 outputs of a padded row at once, from 8 neighbours of the dense one: the 32-bit words that
  * hold at least one of them, shifted where the row starts in the middle of a word. */
-__device__ __forceinline__ void pad_chunk(const uint16_t* from, uint16_t* to, uint32_t c, uint32_t dim)
-{
-    const uint32_t odd = (uintptr_t)from >> 1 & 1, left = dim - 8 * c < 8 ? dim - 8 * c : 8;
-    const volatile uint32_t* words = reinterpret_cast<const volatile uint32_t*>(from + 8 * c - odd);
-    uint32_t w[5];
+struct PadChunk {
+    uint32_t w[5], odd, left;
+    uint4* to;
+
+    __device__ __forceinline__ void load(const uint16_t* from, uint16_t* to_, uint32_t c, uint32_t dim)
+    {
+        odd = (uintptr_t)from >> 1 & 1;
+        left = 8 * c + 8 <= dim ? 8 : 8 * c < dim ? dim - 8 * c : 0;
+        to = reinterpret_cast<uint4*>(to_) + c;
+        const volatile uint32_t* words = reinterpret_cast<const volatile uint32_t*>(from + 8 * c - odd);
 #pragma unroll
-    for (uint32_t j = 0; j < 5; ++j)
-        w[j] = 2 * j < left + odd ? words[j] : 0;
-#pragma unroll
-    for (uint32_t j = 0; j < 4; ++j) {
-        w[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
-        w[j] = 2 * j + 1 < left ? w[j] : 2 * j < left ? w[j] & 0xffff : 0;
+        for (uint32_t j = 0; j < 5; ++j)
+            w[j] = left && 2 * j < left + odd ? words[j] : 0;
     }
-    reinterpret_cast<uint4*>(to)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-}
+
+    __device__ __forceinline__ void store()
+    {
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) {
+            w[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
+            w[j] = 2 * j + 1 < left ? w[j] : 2 * j < left ? w[j] & 0xffff : 0;
+        }
+        *to = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
 
 /* The tokens that have a target, in order: their places, targets, factors and lse; and unless
  * that is all of them (or hidden cannot be used as it lies) their rows next to each other, with
  * zeros behind them up to a multiple of 256 rows.  Every block counts the targets before its own
- * tokens itself: with 8,192 of them that is 8 loads to a thread, less than a second launch.  The
- * blocks past `blocks` pad weight's rows. */
-__global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
+ * tokens itself: with 8,192 of them that is 8 loads to a thread, less than a second launch. */
+__device__ __forceinline__ void list_tokens(const TokenArgs& a, uint32_t* groups)
 {
-    extern __shared__ uint32_t groups[];  // of 32 own tokens: which have a target; then the count before them
+    // groups: of 32 own tokens: which have a target; then the count before them
     __shared__ uint32_t before[32], total[32];
     __shared__ float most[32];
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (blockIdx.x >= a.blocks) {
-        const uint32_t chunks = a.dim8 / 8;
-        const uint64_t all = (uint64_t)a.vocab * chunks, step = (uint64_t)(gridDim.x - a.blocks) * blockDim.x;
-#pragma unroll 2
-        for (uint64_t i = (uint64_t)(blockIdx.x - a.blocks) * blockDim.x + threadIdx.x; i < all; i += step) {
-            const uint64_t r = i / chunks;
-            pad_chunk(a.weight + r * a.dim, a.padded + r * a.dim8, (uint32_t)(i - r * chunks), a.dim);
-        }
-        return;
-    }
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n_groups = a.per / 32;
     const uint32_t lo = blockIdx.x * a.per, hi = lo + a.per < a.rows ? lo + a.per : a.rows;
     const float common = a.backward ? __fmul_rn(a.scale, a.st ? *const_cast<const volatile float*>(&a.st->loss_scale) : 1.0f) : 0.0f;
@@ -802,14 +860,56 @@ __global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
             for (uint32_t c = lane; c < chunks; c += 32)
                 reinterpret_cast<uint4*>(to)[c] = ld_v4(from + c * 8);
         } else {
-            for (uint32_t c = lane; c < chunks; c += 32)
-                pad_chunk(from, to, c, a.dim);
+            for (uint32_t c = lane; c < chunks; c += 32) {
+                PadChunk pad;
+                pad.load(from, to, c, a.dim);
+                pad.store();
+            }
         }
     }
     const uint32_t end = (valid + kTileM - 1) / kTileM * kTileM;
     for (uint32_t r = valid + blockIdx.x * 32 + warp; gather && r < end; r += a.blocks * 32)
         for (uint32_t c = lane; c < chunks; c += 32)
             reinterpret_cast<uint4*>(a.gathered + (uint64_t)r * a.dim8)[c] = make_uint4(0, 0, 0, 0);
+}
+
+/* Weight's rows at a pitch that the TMA takes, by all blocks: a thread's chunks lie a whole grid
+ * apart; row and place in it step along, without a division. */
+__device__ __forceinline__ void pad_rows(const TokenArgs& a)
+{
+    const uint32_t chunks = a.dim8 / 8, threads = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
+    const uint32_t rows_on = threads / chunks, on = threads % chunks;
+    uint32_t r = first / chunks, c = first % chunks;
+    while (r < a.vocab) {  // four in flight
+        PadChunk pad[4];
+        uint32_t n = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            if (r >= a.vocab)
+                break;
+            pad[i].load(a.weight + (uint64_t)r * a.dim, a.padded + (uint64_t)r * a.dim8, c, a.dim);
+            c += on;
+            const bool next = c >= chunks;
+            c -= next ? chunks : 0;
+            r += rows_on + next;
+            ++n;
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i)
+            if (i < n)
+                pad[i].store();
+    }
+}
+
+__global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
+{
+    extern __shared__ uint32_t groups[];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (blockIdx.x < a.blocks)
+        list_tokens(a, groups);
+    if (a.dim % 8)
+        pad_rows(a);
 }
 
 struct LossArgs {
@@ -1101,14 +1201,13 @@ int prologue(const Call& c, const Plan& p, TokenArgs l, ProductArgs& a)
     // row tiles whose hidden rows (32 MB) stay in L2 while weight passes by
     const uint64_t group = (32ull << 20) / (kTileM * 2ull * p.dim8);
     a.group = (uint32_t)(group ? group : 1);
-    // tokens to at most a block per SM, 32 at least to each; rows to pad on a second one
+    // tokens to at most a block per SM, 32 at least to each; rows to pad to all of them
     const uint64_t sms = (uint64_t)sm_count(), want = (c.rows + 31) / 32;
     l.blocks = (uint32_t)(want < sms ? (want ? want : 1) : sms);
     l.per = (uint32_t)up((c.rows + l.blocks - 1) / l.blocks, 32);
-    const uint64_t padders = c.dim % 8 ? ((uint64_t)c.vocab * p.dim8 / 8 + 1023) / 1024 : 0;
     cudaError_t e = allow_smem<k_head_tokens>();
     if (e == cudaSuccess)
-        e = launch_pdl(k_head_tokens, dim3((unsigned)(l.blocks + (padders < sms ? padders : sms))), dim3(1024),
+        e = launch_pdl(k_head_tokens, dim3(c.dim % 8 ? (unsigned)sms : l.blocks), dim3(1024),
                        (size_t)l.per / 32 * 8, c.stream, l);
     return rows_status(e);
 }
@@ -1254,11 +1353,9 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     a.state_error = st ? &st->error : nullptr;
     a.grad_dtype = (uint32_t)grad_dtype;
     a.accumulate = accumulate;
-    a.vec = dweight && rows_vec(dweight, dim, dim, grad_dtype);
-    // dweight leaves by bulk copies unless it is added to or its rows lie off the 16-byte grid
-    const bool whole = p.splits_w == 1 && dweight;
-    if (whole && (accumulate || !a.vec))
-        a.dweight = dweight;
+    const bool whole = p.splits_w == 1 && dweight, vec = dweight && rows_vec(dweight, dim, dim, grad_dtype);
+    a.dweight = dweight;
+    a.bulk = whole && vec;
     a.splits = p.splits_w;
     a.want_h = dhidden != nullptr;
     a.want_w = dweight != nullptr;
@@ -1266,7 +1363,7 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
     float *sums_h = reinterpret_cast<float*>(c.work + p.sums_h), *sums_w = reinterpret_cast<float*>(c.work + p.sums_w);
     if (!tensor_map(&out_d, c.work + p.d, dtype, p.piece, p.rows_pad, p.piece, 64, 32) ||
         !tensor_map(&out_h, sums_h, ZERO_F32, p.dim8, p.rows_h, p.dim8, 32, 32) ||
-        (whole && !a.dweight && !tensor_map(&a.out_w, dweight, grad_dtype, dim, vocab, dim, 32, 32)) ||
+        (a.bulk && !tensor_map(&a.out_w, dweight, grad_dtype, dim, vocab, dim, 32, 32)) ||
         (dweight && !whole &&
          !tensor_map(&a.out_w, sums_w, ZERO_F32, p.dim8, (uint64_t)p.splits_w * p.piece, p.dim8, 32, 32)))
         return map_refused();
@@ -1285,7 +1382,7 @@ int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uin
         if (e == cudaSuccess && dweight && p.splits_w > 1) {
             const JoinArgs j{a.head, sums_w, nullptr, dweight, dim, (uint64_t)p.piece * p.dim8, a.cols, v0, dim,
                              p.dim8, p.splits_w, accumulate, 0};
-            e = join(j, a.cols, grad_dtype, a.vec, stream);
+            e = join(j, a.cols, grad_dtype, vec, stream);
         }
     }
     if (e == cudaSuccess && dhidden && rows) {
