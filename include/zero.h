@@ -625,7 +625,8 @@ size_t zero_layernorm_workspace_bytes(uint64_t rows, uint32_t dim);
  *   mean, rstd      as zero_layernorm wrote them
  *   dweight, dbias  grad_dtype, dim elements; each may be NULL (not wanted)
  *   workspace       DEVICE, zero_layernorm_workspace_bytes(rows, dim), 16-byte aligned
- * Without rows dweight and dbias are 0 (or left as they are, accumulate). */
+ * Without rows dweight and dbias are 0 (or left as they are, accumulate).  Should a bounded wait
+ * inside give up, dweight, dbias and the rows that it reached not are NaN (as y's rows are). */
 int zero_layernorm_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, const void* x, uint64_t x_stride,
                             const void* weight, zero_dtype_t param_dtype, const float* mean, const float* rstd,
                             const void* dy, uint64_t dy_stride, void* dx, uint64_t dx_stride, void* dweight,
@@ -685,7 +686,8 @@ int zero_head_loss(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t voc
  *   scale       e.g. 1 / tokens, for the gradient of a mean
  *   row_scale   fp32 per token (what arrives at loss[t]), or NULL: 1
  *   st          the step state whose loss_scale the gradients get, or NULL: 1.  A bounded wait
- *               that gives up puts 1 into its error word (and the workspace's second word)
+ *               that gives up puts 1 into its error word (and the workspace's second word), and
+ *               dhidden is NaN
  *   dhidden     dtype, or NULL (not wanted);  dweight  grad_dtype, or NULL (not wanted) */
 int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t vocab, const void* hidden,
                             uint64_t hidden_stride, const void* weight, const void* targets, uint32_t target_bytes,

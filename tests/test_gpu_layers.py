@@ -150,6 +150,22 @@ def test_layernorm_backward(n, d, dtype, ptype):
         assert (dx[:, d:] == 7.0).all()
 
 
+@pytest.mark.parametrize("d", [24, 17, 1600, 8200, 12001])
+def test_layernorm_backward_of_a_large_constant_row(d):
+    """mean * rstd is more than fp32 holds, the row's own differences are 0: its gradient is finite."""
+    g = gen(d)
+    x, dy, w = normal(g, 9, d), normal(g, 9, d), normal(g, d)
+    x[4] = 2.0 ** 120
+    mean, rstd = x.mean(1), torch.full((9,), 2.0, device="cuda")
+    mean[4], rstd[4] = 2.0 ** 120, 2.0 ** 10
+    dx, dw, db = torch.empty_like(x), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    z.zero_layernorm_backward(x, w, mean, rstd, dy, dx, dw, db, work_bytes(z.zero_layernorm_workspace_bytes(9, d)))
+    wx, ex, ww, ew, wb, eb = norm_backward(x, w, mean, rstd, dy)
+    check("dx", dx, wx, ex)
+    check("dweight", dw, ww, ew)
+    check("dbias", db, wb, eb)
+
+
 def test_layernorm_backward_without_some_outputs_and_without_rows():
     g = gen(2)
     x, dy, w = normal(g, 50, 96), normal(g, 50, 96), normal(g, 96)
@@ -687,6 +703,32 @@ def test_views_off_the_16_byte_grid():
         head_check(h[:, :d - 1], hw, t.long(), dh[:, :d - 1], normal(g, v * (d - 1) + 1, dtype=dtype)[1:].view(v, d - 1))
 
 
+def test_a_captured_gradient_of_a_table_off_the_16_byte_grid():
+    g = gen(47)
+    n, d, v = 300, 24, 500
+    buf = torch.full((v * d + 3,), 7.0, dtype=BF16, device="cuda")
+    t, dout = ids(g, n, v, torch.int64), normal(g, n, d, dtype=BF16)
+    work = work_bytes(z.zero_embedding_workspace_bytes(n, d, v))
+    want = torch.empty(v, d, dtype=BF16, device="cuda")
+    z.zero_embedding_backward(t, dout, want, work)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        z.zero_embedding_backward(t, dout, buf[1:1 + v * d].view(v, d), work)
+    for _ in range(2):
+        buf.fill_(7.0)
+        graph.replay()
+        assert torch.equal(buf[1:1 + v * d].view(v, d), want)
+        assert (buf[:1] == 7.0).all() and (buf[1 + v * d:] == 7.0).all()
+
+
+def test_rows_of_no_elements_are_refused():
+    e = torch.empty(4, 0, device="cuda")
+    with pytest.raises(ValueError):
+        z.zero_layernorm(e, torch.empty(0, device="cuda"), None, e.clone())
+    with pytest.raises(ValueError):
+        z.zero_embedding(torch.zeros(4, dtype=torch.int64, device="cuda"), torch.empty(5, 0, device="cuda"), e)
+
+
 def test_columns_of_one_buffer():
     """Inputs and outputs as columns of the same rows, side by side."""
     g = gen(22)
@@ -807,6 +849,8 @@ def test_waits_that_run_out_are_told(hooked):
     timed(lambda: L.zero_layernorm_backward(z.ZERO_BF16, n, d, p(x), d, p(w), z.ZERO_BF16, p(mean), p(rstd), p(x), d, p(dx), d,
                                             p(dw), p(db), z.ZERO_F32, 0, p(work), s))
     assert torch.isnan(dw).any() and torch.isnan(db).any()
+    lost = torch.isnan(dx).all(1)
+    assert 0 < int(lost.sum()) < n and not torch.isnan(dx[~lost]).any()
     assert L.zero_test_withhold_norm_turn(never) == 0
     n, d, v = 600, 640, 5000
     h, w, t = normal(g, n, d, dtype=BF16), normal(g, v, d, sigma=0.05, dtype=BF16), torch.randint(0, v, (n,), device="cuda")
@@ -821,7 +865,7 @@ def test_waits_that_run_out_are_told(hooked):
     assert int(work[4:8].view(torch.int32)) == 1
     timed(lambda: L.zero_head_loss_backward(z.ZERO_BF16, n, d, v, p(h), d, p(w), p(t), 8, p(lse), 1.0, None, p(st), p(dh), d,
                                             p(dw), z.ZERO_BF16, 0, p(work), s))
-    assert z.zero_step_state_read(st).error == 1
+    assert z.zero_step_state_read(st).error == 1 and torch.isnan(dh).all()
     assert L.zero_test_withhold_head_stage(never) == 0
     # the context is still good
     head_check(h, w, t, dh, dw)

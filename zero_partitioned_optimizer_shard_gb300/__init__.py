@@ -603,7 +603,7 @@ def _rows(name: str, t, dim: int, device: int, types) -> tuple:
     count rows at one distance from each other."""
     code = _type_of(name, t, device, types)
     shape = t.shape
-    if not shape or shape[-1] != dim:
+    if not shape or not dim or shape[-1] != dim:
         raise ValueError(f"{name} has shape {tuple(shape)}, not rows of {dim}")
     if t.is_contiguous():
         return code, t.numel() // dim, dim

@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(256) k_head_join(const JoinArgs a)
     grid_dependency_wait();
     grid_launch_dependents();
     const uint32_t rows = a.token ? a.head->valid : a.rows, lane = threadIdx.x & 31;
-    const float post = a.head->post;
+    const float post = a.head->error ? __int_as_float(0x7fc00000) : a.head->post;  // a wait gave up: NaN
     const uint32_t pieces = (a.dim + 255) / 256, mt = (rows + kTileM - 1) / kTileM;
     // of dhidden: the splits and their distance that the products' blocks came to; a last, narrower
     // piece of the vocabulary may have been cut into fewer, added to the first of these

@@ -277,18 +277,27 @@ struct Columns {
     }
 
     /* A chunk of a row into the columns' sums and the row's two, of g and of g * xh, which stay.
-     * Past the row's end dy is 0; xh is finite there where the row's statistics are. */
-    template <zero_dtype_t DT>
+     * Past the row's end dy and xh are 0 (the latter too: mean * rstd may be more than fp32 holds
+     * where the row's own differences are 0). */
+    template <zero_dtype_t DT, bool VEC>
     __device__ __forceinline__ void add(int i, const typename Elem<DT>::Raw& x, const typename Elem<DT>::Raw& dy,
                                         float mean, float rstd, uint64_t (&xh)[4], uint64_t (&g)[4], uint64_t& sg,
-                                        uint64_t& sx)
+                                        uint64_t& sx, uint32_t d, uint32_t k, uint32_t n)
     {
+        if (VEC && elem_of<VEC>(i, 0, k, n) >= d)
+            mean = 0.0f;
         const uint64_t mean2 = f2(mean, mean), rstd2 = f2(rstd, rstd);
         widen2<DT>(x, xh);
         widen2<DT>(dy, g);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            xh[q] = f2_mul(f2_sub(xh[q], mean2), rstd2);
+            xh[q] = f2_sub(xh[q], mean2);
+            if constexpr (!VEC) {
+                float c0, c1;
+                f2_split(xh[q], c0, c1);
+                xh[q] = f2(elem_of<VEC>(i, 2 * q, k, n) < d ? c0 : 0.0f, elem_of<VEC>(i, 2 * q + 1, k, n) < d ? c1 : 0.0f);
+            }
+            xh[q] = f2_mul(xh[q], rstd2);
             dw[i][q] = f2_fma(g[q], xh[q], dw[i][q]);
             db[i][q] = f2_add(db[i][q], g[q]);
             g[q] = f2_mul(g[q], w[i][q]);
@@ -406,7 +415,7 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs 
             uint64_t sg = 0, sx = 0;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                c.template add<DT>(i, x[r][i], dy[r][i], mean[r], rstd[r], xh[r][i], g[r][i], sg, sx);
+                c.template add<DT, VEC>(i, x[r][i], dy[r][i], mean[r], rstd[r], xh[r][i], g[r][i], sg, sx, d, k, n);
             s[2 * r] = f2_sum(sg);
             s[2 * r + 1] = f2_sum(sx);
         }
@@ -487,7 +496,8 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
     };
     statistics((uint64_t)blockIdx.x * R);
     uint32_t q = 0, phase = 0, turn = 0;
-    for (uint64_t row0 = (uint64_t)blockIdx.x * R; row0 < a.rows; row0 += step, turn ^= 1) {
+    uint64_t row0 = (uint64_t)blockIdx.x * R;
+    for (; row0 < a.rows; row0 += step, turn ^= 1) {
         if (!ring_wait(full[q], phase))
             gave_up[turn] = 1;
         const uint4* stage = ring + (uint64_t)q * 2 * R * row_bytes / 16;
@@ -511,7 +521,7 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             uint64_t sg = 0, sx = 0;
-            c.template add<DT>(0, x[r], dy[r], mean[r], rstd[r], xh[r], g[r], sg, sx);
+            c.template add<DT, true>(0, x[r], dy[r], mean[r], rstd[r], xh[r], g[r], sg, sx, d, k, n);
             s[2 * r] = f2_sum(sg);
             s[2 * r + 1] = f2_sum(sx);
         }
@@ -534,8 +544,13 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
                              __fmul_rn(s[2 * r], inv_d), __fmul_rn(s[2 * r + 1], inv_d));
         }
     }
-    if (gave_up[0] | gave_up[1])  // a copy did not arrive within 2 s: the weights' gradients tell, as NaN
-        c.dw[0][0] = c.db[0][0] = f2(__int_as_float(0x7fc00000), 0.0f);
+    if (gave_up[0] | gave_up[1]) {  // a copy did not arrive within 2 s: the rows left and the weights' gradients tell, as NaN
+        const float nan = __int_as_float(0x7fc00000);
+        c.dw[0][0] = c.db[0][0] = f2(nan, 0.0f);
+        for (; row0 < a.rows; row0 += step)
+            for (uint32_t i = k; i < R * d && row0 + i / d < a.rows; i += n)
+                static_cast<T*>(a.dx)[(row0 + i / d) * a.dx_stride + i % d] = from_f32<DT>(nan);
+    }
     c.template end<true>(a, k, n);
     __syncthreads();
 }
