@@ -101,6 +101,25 @@ def test_layernorm(n, d, dtype, ptype):
         check("y", y[:, :d], want, ey)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,d", [(40000, 64), (20011, 128), (30001, 10), (30001, 34), (10007, 135), (10007, 256), (157, 200)])
+def test_short_rows(n, d, dtype):
+    """Heads' norms: many rows of at most 256 elements, several to a warp."""
+    g = gen(n + d)
+    x, dy = rows_of(g, n, d, dtype, 0 if d % 8 == 0 else 3), rows_of(g, n, d, dtype)
+    w, b = normal(g, d, dtype=dtype) + 1.0, normal(g, d, dtype=dtype)
+    y, mean, rstd = torch.empty(n, d, dtype=dtype, device="cuda"), torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    z.zero_layernorm(x, w, b, y, mean, rstd)
+    want, m64, r64 = norm_forward(x, w, b, 1e-5)
+    check("y", y, want, norm_bounds(x, w, m64, r64, want)[0])
+    dx, dw, db = torch.empty_like(y), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    z.zero_layernorm_backward(x, w, mean, rstd, dy, dx, dw, db, work_bytes(z.zero_layernorm_workspace_bytes(n, d)))
+    wx, ex, ww, ew, wb, eb = norm_backward(x, w, mean, rstd, dy)
+    check("dx", dx, wx, ex)
+    check("dweight", dw, ww, ew)
+    check("dbias", db, wb, eb)
+
+
 def test_layernorm_far_mean_constant_rows_and_nan():
     g = gen(5)
     x = normal(g, 64, 1600) + 4096.0
@@ -282,6 +301,23 @@ def test_embedding_backward_of_large_tables(n, d, v, gt):
     check("dtable", dtable, want, (n + 4) * U * size)
 
 
+@pytest.mark.parametrize("v", [200, 50257, 70000])
+@pytest.mark.parametrize("n", [1024, 1025, 2048, 2049, 8192, 8193, 16384, 16385, 32769, 65536, 65537])
+def test_embedding_backward_around_the_sorts_sizes(n, v):
+    """One block with 1 and 2 tokens to a thread, a cluster with 1, 2, 4 and 8 tokens to a thread, several launches; 1 to 3 passes.
+    Whole numbers: every sum is exact, whatever its order."""
+    g = gen(n + v)
+    d = 8
+    t = ids(g, n, v, torch.int64)
+    t[-3:] = v - 1
+    dout = torch.randint(-3, 4, (n, d), device="cuda", generator=g).to(F32)
+    dt = torch.full((v, d), 7.0, device="cuda")
+    z.zero_embedding_backward(t, dout, dt, work_bytes(z.zero_embedding_workspace_bytes(n, d, v)))
+    there = (t >= 0) & (t < v)
+    want = torch.zeros(v, d, device="cuda").index_add_(0, t[there], dout[there])
+    assert torch.equal(dt, want)
+
+
 def test_embedding_backward_edges():
     d, v = 40, 9
     table = torch.full((v, d), 3.0, device="cuda")
@@ -397,6 +433,28 @@ def test_head_loss_backward(n, d, v, dtype):
         only = torch.empty(n, d, dtype=dtype, device="cuda")
         z.zero_head_loss_backward(h, w, t, lse, only, None, work, scale=1.0 / n, row_scale=row, st=st)
         assert torch.equal(only, dh[:, :d])
+
+
+@pytest.mark.parametrize("n,d,v,gt,acc", [(2100, 200, 3000, BF16, False), (2100, 200, 3000, F32, True), (2100, 203, 3000, BF16, True),
+                                          (2048, 320, 2500, BF16, False), (300, 203, 3000, F32, True)])
+def test_head_rows_off_the_128_byte_grid(n, d, v, gt, acc):
+    """Calls of many rows move to 128-byte boundaries first; odd rows of the gradient are added to."""
+    g = gen(n + d + v)
+    for pad in (0, 8):
+        h, w, t, there = head_case(g, n, d, v, BF16, pad)
+        work = work_bytes(z.zero_head_workspace_bytes(n, d, v))
+        loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+        z.zero_head_loss(h, w, t, loss, lse, work)
+        _, rl, re, el, _ = head_reference(h, w, t, there)
+        e = el + 2.0 ** -17 + 16 * U * re.abs()   # as in test_head_loss
+        check("lse", lse, re, e)
+        check("loss", loss, rl, e + el)
+        dh, dw = torch.empty(n, d, dtype=BF16, device="cuda"), normal(g, v, d, sigma=0.1, dtype=gt)
+        old = dw.double() if acc else 0.0
+        z.zero_head_loss_backward(h, w, t, re.float(), dh, dw, work, scale=1.0 / n, accumulate=acc)
+        rh, eh, rw, ew = head_gradients(h, w, t, there, torch.full((n,), 1.0 / n, dtype=torch.float64, device="cuda"), BF16)
+        check("dhidden", dh, rh, eh)
+        check("dweight", dw, rw + old, ew + (2 * U * old.abs() if acc else 0.0))
 
 
 @pytest.mark.parametrize("n,d,v", [(8200, 64, 20000), (16500, 24, 9000)])

@@ -30,11 +30,21 @@ struct ForwardArgs {
     float eps;
 };
 
-/* A sum over the block (of one warp: over the warp), the same in every thread. */
+/* A sum over the n threads of a row, the same in each of them: n lanes of a warp (a power of
+ * two), or the whole block. */
+__device__ __forceinline__ float lanes_sum(float x, uint32_t n)
+{
+#pragma unroll
+    for (uint32_t o = 16; o; o >>= 1)
+        if (o < n)
+            x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
 __device__ __forceinline__ float row_sum(float x, float* slots, uint32_t n)
 {
-    x = warp_sum(x);
-    if (n == 32)
+    x = lanes_sum(x, n);
+    if (n <= 32)
         return x;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
@@ -43,11 +53,11 @@ __device__ __forceinline__ float row_sum(float x, float* slots, uint32_t n)
     return warp_sum(lane < n / 32 ? slots[lane] : 0.0f);
 }
 
-/* One row of n threads from its chunks: the statistics, and y.  params(i, w, b) gives chunk i's
- * weights and biases. */
+/* One row of n threads from its chunks: the statistics, and y (nothing is written of a row behind
+ * the last).  params(i, w, b) gives chunk i's weights and biases. */
 template <zero_dtype_t DT, int NV, bool VEC, typename Params>
 __device__ __forceinline__ void norm_row(const ForwardArgs& a, uint32_t row, const typename Elem<DT>::Raw (&raw)[NV],
-                                         float (&slots)[2][32], uint32_t k, uint32_t n, Params params)
+                                         float (&slots)[2][32], uint32_t k, uint32_t n, Params params, bool there = true)
 {
     using T = typename Elem<DT>::T;
     const uint32_t d = a.d;
@@ -80,6 +90,8 @@ __device__ __forceinline__ void norm_row(const ForwardArgs& a, uint32_t row, con
     }
     const float var = __fdiv_rn(row_sum(f2_sum(s), slots[1], n), (float)d);
     const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+    if (!there)
+        return;
     if (k == 0 && a.mean)
         a.mean[row] = mean;
     if (k == 0 && a.rstd)
@@ -100,7 +112,9 @@ __device__ __forceinline__ void norm_row(const ForwardArgs& a, uint32_t row, con
     }
 }
 
-/* One row per n threads: a warp (blockDim.y rows per block) or the whole block. */
+/* One row per n threads: a warp (blockDim.y rows per block) or the whole block.  Calls of few rows,
+ * where the launch counts, long rows, and rows off the 16-byte grid; of the last a warp would have
+ * its 2-byte loads one after another (403 rows of 1,400: 19 us, 13 with 128 threads to a row). */
 template <zero_dtype_t DT, zero_dtype_t PT, int NV, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
 {
@@ -121,6 +135,43 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
         if (a.bias)
             widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), a.d, i, k, n), b);
     });
+}
+
+/* Rows of at most 256 elements (heads' norms): n = 4 to 32 lanes to a row, U rows of each such
+ * group in flight, and the weights of a lane's columns in registers.  What bounds it is how many
+ * loads are in flight: 204,800 rows of 64 bf16 take 19 us (7.7 for their bytes), a warp to a row
+ * took 68; of 20,909 rows of 135, off the 16-byte grid, 33 us instead of 52. */
+constexpr uint32_t kShortWarps = 8;
+
+template <zero_dtype_t DT, zero_dtype_t PT, int U, bool VEC>
+__global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_short(const ForwardArgs a, const uint32_t n)
+{
+    using T = typename Elem<DT>::T;
+    using P = typename Elem<PT>::T;
+    __shared__ float slots[2][32];  // not used by single warps
+    grid_dependency_wait();
+    const uint32_t lane = threadIdx.x & 31, k = lane & (n - 1), rows = 32 / n;
+    const uint32_t first = (blockIdx.x * kShortWarps + (threadIdx.x >> 5)) * U * rows + lane / n;
+    typename Elem<DT>::Raw raw[U][1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t row = first + u * rows;
+        raw[u][0] = load_chunk<DT, VEC>(static_cast<const T*>(a.x) + (uint64_t)row * a.x_stride, row < a.rows ? a.d : 0, 0, k, n);
+    }
+    uint64_t wk[4], bk[4] = {0, 0, 0, 0};
+    widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), a.d, 0, k, n), wk);
+    if (a.bias)
+        widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), a.d, 0, k, n), bk);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        norm_row<DT, 1, VEC>(
+            a, first + u * rows, raw[u], slots, k, n,
+            [&](int, uint64_t(&w)[4], uint64_t(&b)[4]) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    w[q] = wk[q], b[q] = bk[q];
+            },
+            first + u * rows < a.rows);
 }
 
 #ifdef ZERO_TEST_HOOKS
@@ -173,7 +224,11 @@ __device__ __forceinline__ bool ring_wait(uint64_t& bar, uint32_t parity)
 
 /* A warp per row, many rows to a warp: lane 0 bulk-copies the warp's next rows into a ring of
  * its own, so that they are on their way while one is worked on.  The weights and biases lie in
- * shared memory (read from global memory row after row they were what a warp waited for). */
+ * shared memory (read from global memory row after row they were what a warp waited for).
+ * 8,192 rows of 1,600 bf16: 12.8 us a call, its 52 MB 7.7 at the copy's rate; the first, one row to
+ * a warp straight from global memory, took 17.7.  What is left is the launch (about 3 us) and
+ * issue slots: 32 lanes' conversions and paired arithmetic took 58% of them.  Rows kept ahead in
+ * registers (21.5 us) and one copying warp for all rings (15.8) were slower. */
 template <zero_dtype_t DT, zero_dtype_t PT, int NV>
 __global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const ForwardArgs a, const uint32_t stages)
 {
@@ -382,7 +437,8 @@ __device__ __forceinline__ void block_sums4(float (&s)[4], float (&slots)[8][4],
 }
 
 /* R rows at a time per block, straight from global memory: rows that the bulk copies do not
- * take, and the longest. */
+ * take, and the longest.  Bound by the latency of a turn's loads and its barrier: 4,099 rows of
+ * 641 fp16 take 18 us with the join (2.3 for the bytes). */
 template <zero_dtype_t DT, zero_dtype_t PT, int NV, int R, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs a)
 {
@@ -434,7 +490,11 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs 
 }
 
 /* The same through a ring of stages of R rows of x and dy, bulk-copied ahead by one warp more:
- * the rows of the next turns are on their way while one is worked on, without registers. */
+ * the rows of the next turns are on their way while one is worked on, without registers.
+ * 8,192 rows of 1,600 bf16: 21.7 us a call with the join, 11.6 for its 79 MB at the copy's rate;
+ * 38.8 straight from global memory with two barriers a turn.  Left are two launches and, in a
+ * turn, the sums' 13 exchanges and barrier.  Blocks of two groups that take turns (27.8 us) and three
+ * blocks to an SM, whose registers spill (27.7), were slower. */
 template <zero_dtype_t DT, zero_dtype_t PT, int R, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const BackwardArgs a, const uint32_t stages)
 {
@@ -555,6 +615,69 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
     __syncthreads();
 }
 
+/* Rows of at most 256 elements: n = 4 to 32 lanes to a row as in the forward pass, R rows of each
+ * group in flight; at the end the groups' sums of a column are joined, those of a warp over its
+ * lanes, then the warps' in order.  204,800 rows of 64 bf16: 28 us with the join (11.6 for the
+ * bytes), 142 with a block to two rows; 20,909 rows of 135: 48 us instead of 64. */
+template <zero_dtype_t DT, zero_dtype_t PT, int R, bool VEC>
+__global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_backward_short(const BackwardArgs a, const uint32_t n)
+{
+    using T = typename Elem<DT>::T;
+    __shared__ float sums[kShortWarps][2][8][33];  // [warp][of dweight, dbias][element of the chunk][lane]
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = lane & (n - 1), groups = 32 / n, d = a.d;
+    Columns<1> c;
+    c.template begin<PT, VEC>(a, k, n);
+    const float inv_d = __fdiv_rn(1.0f, (float)d);
+    const uint32_t step = gridDim.x * kShortWarps * R * groups;
+    for (uint32_t row0 = (blockIdx.x * kShortWarps + warp) * R * groups; row0 < a.rows; row0 += step) {
+        typename Elem<DT>::Raw x[R], dy[R];
+        float mean[R], rstd[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t row = row0 + r * groups + lane / n, len = row < a.rows ? d : 0;
+            x[r] = load_chunk<DT, VEC>(static_cast<const T*>(a.x) + (uint64_t)row * a.x_stride, len, 0, k, n);
+            dy[r] = load_chunk<DT, VEC>(static_cast<const T*>(a.dy) + (uint64_t)row * a.dy_stride, len, 0, k, n);
+            mean[r] = len ? a.mean[row] : 0.0f;
+            rstd[r] = len ? a.rstd[row] : 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t row = row0 + r * groups + lane / n;
+            uint64_t xh[4], g[4], sg = 0, sx = 0;
+            c.template add<DT, VEC>(0, x[r], dy[r], mean[r], rstd[r], xh, g, sg, sx, d, k, n);
+            const float s = lanes_sum(f2_sum(sg), n), t = lanes_sum(f2_sum(sx), n);
+            if (row < a.rows)
+                put_dx<DT, VEC>(0, static_cast<T*>(a.dx) + (uint64_t)row * a.dx_stride, d, k, n, xh, g, rstd[r],
+                                __fmul_rn(s, inv_d), __fmul_rn(t, inv_d));
+        }
+    }
+    float v[2][8];
+    split4(c.dw[0], v[0]);
+    split4(c.db[0], v[1]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            for (uint32_t o = 16; o >= n; o >>= 1)
+                v[q][j] = __fadd_rn(v[q][j], __shfl_xor_sync(0xffffffffu, v[q][j], o));
+            sums[warp][q][j][lane] = v[q][j];
+        }
+    __syncthreads();
+    if (warp >= 2 || lane >= n)
+        return;
+    float s[8];  // the first warp joins dweight's, the second dbias's
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        s[j] = sums[0][warp][j][lane];
+#pragma unroll
+        for (uint32_t w = 1; w < kShortWarps; ++w)
+            s[j] = __fadd_rn(s[j], sums[w][warp][j][lane]);
+    }
+    store_chunk<ZERO_F32, VEC>(a.parts + ((uint64_t)blockIdx.x * 2 + warp) * d, d, 0, k, n, s);
+}
+
 struct JoinArgs {
     const float* parts;
     void* dweight;
@@ -617,11 +740,22 @@ cudaError_t forward_staged(const ForwardArgs& a, size_t params, size_t row_bytes
     return taken ? launch_pdl(KERNEL, dim3(fit), dim3(32 * kRingWarps), smem, s, a, (uint32_t)stages) : e;
 }
 
+/* Lanes to a row of at most 256 elements. */
+uint32_t short_lanes(uint32_t chunks) { return chunks <= 4 ? 4 : chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32; }
+
 template <zero_dtype_t DT, zero_dtype_t PT, bool VEC>
 cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
 {
-    // a warp per row up to 2,048 elements (no barrier), then 128 and 512 threads
-    const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 256 ? 32 : chunks <= 1024 ? 128 : 512;
+    const uint32_t chunks = (a.d + 7) / 8;
+    if (chunks <= 32) {
+        const uint32_t lanes = short_lanes(chunks), rows = kShortWarps * (32 / lanes);
+        const bool many = a.rows > 4 * rows * (uint32_t)sm_count();  // a block on each SM, with 4 rows to a group
+        const dim3 grid(many ? (a.rows + 4 * rows - 1) / (4 * rows) : (a.rows + rows - 1) / rows);
+        return many ? launch_pdl(k_layernorm_short<DT, PT, 4, VEC>, grid, dim3(32 * kShortWarps), 0, s, a, lanes)
+                    : launch_pdl(k_layernorm_short<DT, PT, 1, VEC>, grid, dim3(32 * kShortWarps), 0, s, a, lanes);
+    }
+    // a warp per row up to 2,048 elements (no barrier) in 128-bit accesses, then 128 and 512 threads
+    const uint32_t n = VEC && chunks <= 256 ? 32 : chunks <= 1024 ? 128 : 512;
     const uint32_t per = (chunks + n - 1) / n, rows = n == 32 ? 4 : 1;
     if constexpr (VEC) {
         if (n == 32) {
@@ -630,7 +764,6 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
             cudaError_t e = cudaSuccess;
             // exactly the chunks that a lane holds: an eighth for 1,600 elements (7) cost 10%
             switch (per) {
-            case 1: e = forward_staged<k_layernorm_staged<DT, PT, 1>>(a, params, row, taken, s); break;
             case 2: e = forward_staged<k_layernorm_staged<DT, PT, 2>>(a, params, row, taken, s); break;
             case 3: e = forward_staged<k_layernorm_staged<DT, PT, 3>>(a, params, row, taken, s); break;
             case 4: e = forward_staged<k_layernorm_staged<DT, PT, 4>>(a, params, row, taken, s); break;
@@ -648,8 +781,11 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
     };
     if (n == 512)
         return per <= 2 ? go(k_layernorm<DT, PT, 2, VEC, 512>) : go(k_layernorm<DT, PT, 4, VEC, 512>);
-    return per <= 1   ? go(k_layernorm<DT, PT, 1, VEC, 128>)
-           : per <= 2 ? go(k_layernorm<DT, PT, 2, VEC, 128>)
+    if constexpr (!VEC) {
+        if (per <= 1)
+            return go(k_layernorm<DT, PT, 1, VEC, 128>);
+    }
+    return per <= 2   ? go(k_layernorm<DT, PT, 2, VEC, 128>)
            : per <= 4 ? go(k_layernorm<DT, PT, 4, VEC, 128>)
                       : go(k_layernorm<DT, PT, 8, VEC, 128>);
 }
@@ -676,6 +812,12 @@ cudaError_t backward(const BackwardArgs& a, uint32_t& parts, cudaStream_t s)
 {
     // one warp more than the chunks need copies rows in
     const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 992 ? (chunks + 31) / 32 * 32 : 1024;
+    if (chunks <= 32) {
+        const uint32_t lanes = short_lanes(chunks), rows = kShortWarps * (32 / lanes);
+        return a.rows > 4 * rows * (uint32_t)sm_count()
+                   ? backward_blocks<k_layernorm_backward_short<DT, PT, 4, VEC>>(a, 32 * kShortWarps, 4 * rows, 0, parts, s, lanes)
+                   : backward_blocks<k_layernorm_backward_short<DT, PT, 1, VEC>>(a, 32 * kShortWarps, rows, 0, parts, s, lanes);
+    }
     if (chunks > 992)
         return backward_blocks<k_layernorm_backward<DT, PT, 2, 1, VEC, 1024>>(a, n, 1, 0, parts, s);
     if constexpr (VEC) {
