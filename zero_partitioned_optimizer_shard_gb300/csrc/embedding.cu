@@ -53,7 +53,10 @@ struct LookupArgs {
 };
 
 /* A warp takes W neighbouring pieces of rows, all in flight at a time.  A scale of 1 leaves the
- * values as they are, without a detour over fp32. */
+ * values as they are, without a detour over fp32.  Bound by memory: 16,384 tokens of 4,096 bf16 from
+ * a table of 32,000 take 29.8 us a call, 39.6 for reading each row that occurs once and writing
+ * the output at the copy's rate (its writes stay in L2 in part).  With a warp to a piece, W = 1,
+ * it was issue-bound (70% of the slots, 34.5 us). */
 template <zero_dtype_t DT, bool VEC>
 __global__ void __launch_bounds__(256) k_embedding(const LookupArgs a)
 {
@@ -105,17 +108,39 @@ __global__ void __launch_bounds__(256) k_embedding(const LookupArgs a)
 /* ------------------------------------------------------------------------------------ */
 struct RankSmem {
     uint32_t of_warp[kSortWarps][kBins];  // counts, then offsets, of each warp's keys
-    uint32_t base[kBins];                 // keys of the tile below each digit
+    uint32_t base[kBins];                 // where a digit's keys begin
     uint32_t warp_total[8];
 };
 
+/* base[digit threadIdx.x] = first + the sum of `count` over the digits below. */
+__device__ __forceinline__ void digit_base(RankSmem& sm, uint32_t count, uint32_t first)
+{
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t sum = count;
+    if (threadIdx.x < kBins) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
+            sum += lane >= (uint32_t)o ? up : 0;
+        }
+        if (lane == 31)
+            sm.warp_total[warp] = sum;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBins) {
+        for (uint32_t w = 0; w < warp; ++w)
+            first += sm.warp_total[w];
+        sm.base[threadIdx.x] = first + sum - count;
+    }
+    __syncthreads();
+}
+
 /* Each thread's ITEMS keys (a warp's are 32 * ITEMS neighbours, taken 32 at a time) get
- * their rank among the tile's keys of the same digit, in the keys' order; base[] becomes the
- * number of the tile's keys with a smaller digit and count the tile's keys of digit
- * threadIdx.x. */
+ * their rank among the tile's keys of the same digit, in the keys' order.  The answer is the
+ * number of the tile's keys of digit threadIdx.x. */
 template <uint32_t ITEMS>
-__device__ __forceinline__ void rank_tile(RankSmem& sm, const uint32_t (&key)[ITEMS], uint32_t shift,
-                                          uint32_t (&rank)[ITEMS])
+__device__ __forceinline__ uint32_t rank_tile(RankSmem& sm, const uint32_t (&key)[ITEMS], uint32_t shift,
+                                              uint32_t (&rank)[ITEMS])
 {
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (uint32_t b = lane; b < kBins; b += 32)
@@ -142,27 +167,28 @@ __device__ __forceinline__ void rank_tile(RankSmem& sm, const uint32_t (&key)[IT
             sm.of_warp[w][threadIdx.x] = count;
             count += c;
         }
-        uint32_t sum = count;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t up = __shfl_up_sync(0xffffffffu, sum, o);
-            sum += lane >= (uint32_t)o ? up : 0;
-        }
-        if (lane == 31)
-            sm.warp_total[warp] = sum;
-        sm.base[threadIdx.x] = sum - count;
-    }
-    __syncthreads();
-    if (threadIdx.x < kBins) {
-        uint32_t more = 0;
-        for (uint32_t w = 0; w < warp; ++w)
-            more += sm.warp_total[w];
-        sm.base[threadIdx.x] += more;
     }
     __syncthreads();
 #pragma unroll
     for (uint32_t i = 0; i < ITEMS; ++i)
         rank[i] += sm.of_warp[warp][key[i] >> shift & (kBins - 1)];
+    return count;
+}
+
+/* A barrier over the cluster; what its blocks wrote before is seen behind it. */
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n"
+                 "barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+/* This address in shared memory as block b of the cluster has it. */
+__device__ __forceinline__ uint32_t of_block(const uint32_t* p, uint32_t b)
+{
+    uint32_t at, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(b));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
 /* The place in its tile of item i of the calling thread. */
@@ -278,11 +304,11 @@ __global__ void __launch_bounds__(512) k_zero_fill(const Fill f)
 
 struct SmallSmem {
     RankSmem rank;
-    uint2 item[kTile];
+    uint2 item[2 * kSortThreads];
 };
 
 /* All passes over at most 1,024 * ITEMS tokens, by block 0, while the other blocks write the
- * table's zeros (sorting 8,192 tokens takes less time than 161 MB of zeros). */
+ * table's zeros. */
 template <uint32_t ITEMS>
 __global__ void __launch_bounds__(kSortThreads) k_sort_small(const SortArgs a, const uint32_t bits, const Fill f)
 {
@@ -302,7 +328,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_small(const SortArgs a, c
         place[i] = x.y;
     }
     for (uint32_t shift = 0; shift < bits; shift += 8) {
-        rank_tile(sm.rank, key, shift, rank);
+        digit_base(sm.rank, rank_tile(sm.rank, key, shift, rank), 0);
 #pragma unroll
         for (uint32_t i = 0; i < ITEMS; ++i)
             sm.item[sm.rank.base[key[i] >> shift & (kBins - 1)] + rank[i]] = make_uint2(key[i], place[i]);
@@ -318,6 +344,64 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_small(const SortArgs a, c
     for (uint32_t i = 0; i < ITEMS; ++i)
         if (item_at<ITEMS>(i) < a.n)
             a.to[item_at<ITEMS>(i)] = make_uint2(key[i], place[i]);
+}
+
+/* All passes over at most 8 * 1,024 * ITEMS tokens, by the first cluster: each of its 8 blocks
+ * ranks a tile, the blocks read each other's counts of a digit, and the items change places
+ * through memory, to[] and other[] in turn.  The other clusters write the table's zeros meanwhile
+ * (161 MB of them take 26 us, the sort of 8,192 tokens less).  A pass is bound by its steps one
+ * after another: three barriers of the block, two of the cluster.  By one block 8,192 tokens took 11 us
+ * more; 16,384 in launches of their own, with the zeros before them, 40 more (97 -> 57 us for the whole gradient
+ * of a 50,257 x 1,600 table). */
+constexpr uint32_t kCluster = 8;
+
+template <uint32_t ITEMS>
+__global__ void __launch_bounds__(kSortThreads) k_sort_cluster(const SortArgs a, uint2* const other, const uint32_t bits,
+                                                               const Fill f)
+{
+    extern __shared__ uint4 smem[];
+    RankSmem& sm = *reinterpret_cast<RankSmem*>(smem);
+    __shared__ uint32_t count[kBins];  // of the tile, for the cluster
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (blockIdx.x >= kCluster) {
+        zero_fill(f, blockIdx.x - kCluster, gridDim.x - kCluster);
+        return;
+    }
+    const uint32_t first = blockIdx.x * kSortThreads * ITEMS;
+    uint2* to = a.to;
+    for (uint32_t shift = 0; shift < bits; shift += 8) {
+        uint32_t key[ITEMS], place[ITEMS], rank[ITEMS];
+#pragma unroll
+        for (uint32_t i = 0; i < ITEMS; ++i) {
+            const uint32_t at = first + item_at<ITEMS>(i);
+            uint2 x = make_uint2(0xffffffffu, 0);
+            if (at < a.n)
+                x = shift ? __ldcg((to == a.to ? other : a.to) + at) : make_uint2(a.tokens.at(at), at);
+            key[i] = x.x;
+            place[i] = x.y;
+        }
+        const uint32_t mine = rank_tile(sm, key, shift, rank);
+        if (threadIdx.x < kBins)
+            count[threadIdx.x] = mine;
+        cluster_sync();
+        uint32_t before = 0, all = 0;
+        if (threadIdx.x < kBins) {
+#pragma unroll
+            for (uint32_t b = 0; b < kCluster; ++b) {
+                const uint32_t c = of_block(&count[threadIdx.x], b);
+                before += b < blockIdx.x ? c : 0;
+                all += c;
+            }
+        }
+        digit_base(sm, all, before);
+#pragma unroll
+        for (uint32_t i = 0; i < ITEMS; ++i)
+            if (first + item_at<ITEMS>(i) < a.n)
+                to[sm.base[key[i] >> shift & (kBins - 1)] + rank[i]] = make_uint2(key[i], place[i]);
+        cluster_sync();
+        to = to == a.to ? other : a.to;
+    }
 }
 
 /* ------------------------------------------------------------------------------------ */
@@ -353,6 +437,10 @@ __device__ __forceinline__ void put_grad(const GradArgs& a, uint32_t token, uint
     store_chunk<GT, VEC>(row, a.d, i, k, n, v);
 }
 
+/* A block per chunk of sorted places and (rows beyond 2,048 elements) piece of the row, 8 rows in
+ * flight to a thread.  Bound by memory and by the chunk's latency: 8,192 rows of 1,600 bf16 take 10
+ * us, 26 MB at 2.6 TB/s.  A chunk is 16 places, so that few tokens reach over two of them and
+ * a block still has two turns of loads; of few tokens 8, for twice the blocks. */
 template <zero_dtype_t DT, zero_dtype_t GT, bool VEC>
 __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
 {
@@ -414,7 +502,9 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
 
 /* Tokens over several chunks: their partial sums in the order of the chunks.  A block looks at
  * the last tokens of `per` chunks (at most 8); for each that starts in its chunk and goes on, 8
- * warps sum a run of the partials each, over 32 places of the row's piece. */
+ * warps sum a run of the partials each, over 32 places of the row's piece.  7 us, nearly all of it
+ * launch and one round trip; a token in half of a million places takes a block thousands of turns (a
+ * padding id belongs outside the table, where it costs nothing). */
 template <zero_dtype_t GT, bool VEC>
 __global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a, const uint32_t per)
 {
@@ -541,11 +631,30 @@ Fill fill_of(void* p, uint64_t bytes)
 template <uint32_t ITEMS>
 cudaError_t sort_small(const SortArgs& a, uint32_t bits, const Fill& f, unsigned fillers, cudaStream_t s)
 {
-    static_assert(ITEMS <= kItems, "the tile in shared memory");
     const cudaError_t e = allow_smem<k_sort_small<ITEMS>>();
     return e != cudaSuccess ? e
                             : launch_pdl(k_sort_small<ITEMS>, dim3(1 + fillers), dim3(kSortThreads), sizeof(SmallSmem), s,
                                          a, bits, f);
+}
+
+/* The first cluster sorts, the others fill. */
+template <uint32_t ITEMS>
+cudaError_t sort_cluster(const SortArgs& a, uint2* other, uint32_t bits, const Fill& f, unsigned fillers, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster + (fillers + kCluster - 1) / kCluster * kCluster);
+    cfg.blockDim = dim3(kSortThreads);
+    cfg.dynamicSmemBytes = sizeof(RankSmem);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kCluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_sort_cluster<ITEMS>, a, other, bits, f);
 }
 
 /* Zeros over the table's gradient (bytes of it, 0: none) and the tokens' places in order. */
@@ -567,17 +676,22 @@ cudaError_t fill_and_sort(const Tokens& tokens, uint32_t n, void* table, uint64_
     const uint64_t want = (f.n16 + 4095) / 4096, cap = (uint64_t)sm_count() * 2 - 1;
     const unsigned fillers = bytes ? (unsigned)(want < cap ? (want ? want : 1) : cap) : 0;
     SortArgs a{tokens, nullptr, buf[0], hist, n, tiles, 0};
-    if (tiles == 1) {
+    // one block up to 2,048 tokens (14.9 us for a whole call there, a cluster 17.0), a cluster up to
+    // 65,536 (of 8,192 tokens: 32.4 us, one block 43.6; of 65,536: 67, launches of a step each 80)
+    if (n && n <= 2 * kSortThreads) {
         sorted = buf[0];
-        return n <= kSortThreads       ? sort_small<1>(a, bits, f, fillers, s)
-               : n <= 2 * kSortThreads ? sort_small<2>(a, bits, f, fillers, s)
-               : n <= 4 * kSortThreads ? sort_small<4>(a, bits, f, fillers, s)
-                                       : sort_small<8>(a, bits, f, fillers, s);
+        return n <= kSortThreads ? sort_small<1>(a, bits, f, fillers, s) : sort_small<2>(a, bits, f, fillers, s);
+    }
+    if (n && n <= kCluster * kTile) {
+        const uint32_t each = (n + kCluster * kSortThreads - 1) / (kCluster * kSortThreads);
+        sorted = buf[(bits + 7) / 8 & 1 ? 0 : 1];
+        return each <= 1   ? sort_cluster<1>(a, buf[1], bits, f, fillers, s)
+               : each <= 2 ? sort_cluster<2>(a, buf[1], bits, f, fillers, s)
+               : each <= 4 ? sort_cluster<4>(a, buf[1], bits, f, fillers, s)
+                           : sort_cluster<8>(a, buf[1], bits, f, fillers, s);
     }
     if (fillers)
         e = launch_pdl(k_zero_fill, dim3(fillers * 2), dim3(512), 0, s, f);
-    if (tiles && e == cudaSuccess)
-        e = cudaFuncSetAttribute(k_sort_scatter, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(RankSmem));
     for (uint32_t turn = 0; tiles && a.shift < bits && e == cudaSuccess; a.shift += 8, ++turn) {
         a.to = buf[turn & 1];
         e = launch_pdl(k_sort_count, dim3(tiles), dim3(kSortThreads), 0, s, a);
