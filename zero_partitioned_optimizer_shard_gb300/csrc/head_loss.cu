@@ -287,12 +287,15 @@ __device__ __forceinline__ void d_epilogue(const ProductArgs& a, const Tile& t, 
 }
 
 /* 32 columns of a warp's 32 rows of the weight's gradient where the TMA does not take its rows:
- * through shared memory, so that a store is 32 neighbours of a row (a lane
- * writing its own row took 8 times as long on rows of 2,223). */
+ * through shared memory, so that a store is 32 neighbours of a row (a lane writing its own row
+ * took 8 times as long on rows of 2,223). */
 template <zero_dtype_t GT>
 __device__ __forceinline__ void put_rows(uint32_t stage, uint32_t lane, typename Elem<GT>::T* to, uint32_t rows, uint32_t col,
                                          uint32_t dim, float post, bool accumulate, const float (&x)[32])
 {
+    using G = typename Elem<GT>::T;
+    to += col + lane;
+    const bool in = col + lane < dim;
     uint4 v[8];
 #pragma unroll
     for (uint32_t q = 0; q < 8; ++q)
@@ -301,23 +304,32 @@ __device__ __forceinline__ void put_rows(uint32_t stage, uint32_t lane, typename
     stage_wait(lane);  // a bulk copy of an earlier tile may still read it
     stage_row<128>(stage, lane, v);
     __syncwarp();
-    if (col + lane >= dim)
+    if (!in)
         return;
-    to += col + lane;
+    auto batch = [&](uint32_t r0, const G* old) {  // 8 rows; what they held, or null
+        float y[8];
 #pragma unroll
-    for (uint32_t r0 = 0; r0 < 32; r0 += 8) {
-        float y[8], old[8];
-#pragma unroll
-        for (uint32_t r = 0; r < 8; ++r) {
+        for (uint32_t r = 0; r < 8; ++r)
             asm volatile("ld.shared.f32 %0, [%1];"
                          : "=f"(y[r])
                          : "r"(stage + (r0 + r) * 128 + ((lane / 4 ^ r) << 4) + lane % 4 * 4));
-            old[r] = accumulate && r0 + r < rows ? to_f32<GT>(to[(uint64_t)(r0 + r) * dim]) : 0.0f;
-        }
 #pragma unroll
         for (uint32_t r = 0; r < 8; ++r)
             if (r0 + r < rows)
-                to[(uint64_t)(r0 + r) * dim] = from_f32<GT>(accumulate ? __fmaf_rn(y[r], post, old[r]) : __fmul_rn(y[r], post));
+                to[(uint64_t)(r0 + r) * dim] = from_f32<GT>(old ? __fmaf_rn(y[r], post, to_f32<GT>(old[r])) : __fmul_rn(y[r], post));
+    };
+    if (accumulate) {  // all 32 asked for at once (8 at a time: 439 us for 100 x 2970 x 16881, not 306)
+        G old[32];
+#pragma unroll
+        for (uint32_t r = 0; r < 32; ++r)
+            old[r] = r < rows ? *const_cast<const volatile G*>(to + (uint64_t)r * dim) : G(0);
+#pragma unroll
+        for (uint32_t r0 = 0; r0 < 32; r0 += 8)
+            batch(r0, old + r0);
+    } else {
+#pragma unroll
+        for (uint32_t r0 = 0; r0 < 32; r0 += 8)
+            batch(r0, nullptr);
     }
 }
 
@@ -674,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
 /* ------------------------------------------------------------------------------------ */
 struct TokenArgs {
     const void* targets;
-    uint32_t wide, rows, vocab, dim, dim8;
+    uint32_t wide, rows, vocab, dim, pitch;
     uint32_t direct;       // hidden can be used as it lies
     uint32_t blocks, per;  // blocks with tokens, tokens of each (a multiple of 32)
     Header* head;
@@ -691,12 +703,11 @@ struct TokenArgs {
     uint32_t backward, f16;
     const uint16_t* hidden;
     uint64_t hidden_stride;
-    uint16_t* gathered;    // [rows_pad][dim8]
+    uint16_t* gathered;    // [rows_pad][pitch]
     uint16_t* dhidden;     // backward: rows of tokens without a target are written 0
     uint64_t dhidden_stride;
-    // weight's rows at a pitch that the TMA takes, where they are not of whole 16-byte groups
     const uint16_t* weight;
-    uint16_t* padded;
+    uint16_t* padded;      // [vocab][pitch], or null: weight is used as it lies
 };
 
 __device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_t vocab, uint32_t t)
@@ -709,27 +720,35 @@ __device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_
     return v >= 0 && v < (int)vocab ? v : -1;
 }
 
-/* 8 outputs of a padded row at once, from 8 neighbours of the dense one: the 32-bit words that
- * hold at least one of them, shifted where the row starts in the middle of a word. */
+/* 8 outputs of a padded row at once, from 8 neighbours of the dense one: one 128-bit load, or the
+ * 32-bit words that hold at least one of them, shifted where the row starts in the middle of a
+ * word. */
 struct PadChunk {
     uint32_t w[5], odd, left;
     uint4* to;
 
+    template <bool VEC>
     __device__ __forceinline__ void load(const uint16_t* from, uint16_t* to_, uint32_t c, uint32_t dim)
     {
+        to = reinterpret_cast<uint4*>(to_) + c;
+        if constexpr (VEC) {
+            const uint4 v = 8 * c < dim ? ld_v4(from + 8 * c) : make_uint4(0, 0, 0, 0);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            return;
+        }
         odd = (uintptr_t)from >> 1 & 1;
         left = 8 * c + 8 <= dim ? 8 : 8 * c < dim ? dim - 8 * c : 0;
-        to = reinterpret_cast<uint4*>(to_) + c;
         const volatile uint32_t* words = reinterpret_cast<const volatile uint32_t*>(from + 8 * c - odd);
 #pragma unroll
         for (uint32_t j = 0; j < 5; ++j)
             w[j] = left && 2 * j < left + odd ? words[j] : 0;
     }
 
+    template <bool VEC>
     __device__ __forceinline__ void store()
     {
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
+        for (uint32_t j = 0; j < 4 && !VEC; ++j) {
             w[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
             w[j] = 2 * j + 1 < left ? w[j] : 2 * j < left ? w[j] & 0xffff : 0;
         }
@@ -841,7 +860,7 @@ __device__ __forceinline__ void list_tokens(const TokenArgs& a, uint32_t* groups
     if (!gather && !(a.dhidden && valid != a.rows))
         return;
     const bool vec = a.dim % 8 == 0 && a.hidden_stride % 8 == 0 && ((uintptr_t)a.hidden & 15) == 0;
-    const uint32_t chunks = a.dim8 / 8;
+    const uint32_t chunks = a.pitch / 8;
     for (uint32_t t = lo + warp; t < hi; t += 32) {  // a row to a warp
         const uint32_t g = (t - lo) / 32, bit = (t - lo) % 32, mask = groups[g];
         if (!(mask >> bit & 1)) {
@@ -854,30 +873,31 @@ __device__ __forceinline__ void list_tokens(const TokenArgs& a, uint32_t* groups
             continue;
         const uint32_t r = counts[g] + __popc(mask & ((1u << bit) - 1));
         const uint16_t* from = a.hidden + t * a.hidden_stride;
-        uint16_t* to = a.gathered + (uint64_t)r * a.dim8;
+        uint16_t* to = a.gathered + (uint64_t)r * a.pitch;
         if (vec) {
 #pragma unroll 4
             for (uint32_t c = lane; c < chunks; c += 32)
-                reinterpret_cast<uint4*>(to)[c] = ld_v4(from + c * 8);
+                reinterpret_cast<uint4*>(to)[c] = c * 8 < a.dim ? ld_v4(from + c * 8) : make_uint4(0, 0, 0, 0);
         } else {
             for (uint32_t c = lane; c < chunks; c += 32) {
                 PadChunk pad;
-                pad.load(from, to, c, a.dim);
-                pad.store();
+                pad.load<false>(from, to, c, a.dim);
+                pad.store<false>();
             }
         }
     }
     const uint32_t end = (valid + kTileM - 1) / kTileM * kTileM;
     for (uint32_t r = valid + blockIdx.x * 32 + warp; gather && r < end; r += a.blocks * 32)
         for (uint32_t c = lane; c < chunks; c += 32)
-            reinterpret_cast<uint4*>(a.gathered + (uint64_t)r * a.dim8)[c] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(a.gathered + (uint64_t)r * a.pitch)[c] = make_uint4(0, 0, 0, 0);
 }
 
-/* Weight's rows at a pitch that the TMA takes, by all blocks: a thread's chunks lie a whole grid
- * apart; row and place in it step along, without a division. */
+/* Weight's rows at another pitch, by all blocks: a thread's chunks lie a whole grid apart; row and
+ * place in it step along, without a division. */
+template <bool VEC>
 __device__ __forceinline__ void pad_rows(const TokenArgs& a)
 {
-    const uint32_t chunks = a.dim8 / 8, threads = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
+    const uint32_t chunks = a.pitch / 8, threads = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + threadIdx.x;
     const uint32_t rows_on = threads / chunks, on = threads % chunks;
     uint32_t r = first / chunks, c = first % chunks;
     while (r < a.vocab) {  // four in flight
@@ -887,7 +907,7 @@ __device__ __forceinline__ void pad_rows(const TokenArgs& a)
         for (uint32_t i = 0; i < 4; ++i) {
             if (r >= a.vocab)
                 break;
-            pad[i].load(a.weight + (uint64_t)r * a.dim, a.padded + (uint64_t)r * a.dim8, c, a.dim);
+            pad[i].load<VEC>(a.weight + (uint64_t)r * a.dim, a.padded + (uint64_t)r * a.pitch, c, a.dim);
             c += on;
             const bool next = c >= chunks;
             c -= next ? chunks : 0;
@@ -897,7 +917,7 @@ __device__ __forceinline__ void pad_rows(const TokenArgs& a)
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i)
             if (i < n)
-                pad[i].store();
+                pad[i].store<VEC>();
     }
 }
 
@@ -908,8 +928,10 @@ __global__ void __launch_bounds__(1024, 1) k_head_tokens(const TokenArgs a)
     grid_launch_dependents();
     if (blockIdx.x < a.blocks)
         list_tokens(a, groups);
-    if (a.dim % 8)
-        pad_rows(a);
+    if (a.padded && a.dim % 8)
+        pad_rows<false>(a);
+    else if (a.padded)
+        pad_rows<true>(a);
 }
 
 struct LossArgs {
@@ -1056,9 +1078,16 @@ int map_refused()
 
 uint64_t up(uint64_t x, uint64_t to) { return (x + to - 1) / to * to; }
 
+/* A 128-byte row of a TMA box that does not start on 128 bytes touches two lines: rows of 840
+ * instead of 832 or 896 slow the products by a fifth.  Calls of so many rows copy hidden and weight
+ * to 128-byte boundaries first (840 by 33,140, forward and backward: 8,192 rows 325 + 1,077 us, so 281 + 979;
+ * 2,048 rows 102 + 308, 100 + 299; 1,024 rows the same either way). */
+constexpr uint32_t kAlignRows = 2048;
+
 /* How a call is cut, and where its parts lie in the workspace. */
 struct Plan {
-    uint32_t rows_pad, dim8, piece, rows_h, splits_w;
+    uint32_t rows_pad, dim8, pitch, piece, rows_h, splits_w;
+    bool pad;  // weight's rows are copied to another pitch
     uint64_t token, target, factor, lse, logit, gathered, weight, stats, d, sums_h, sums_w, bytes;
 };
 
@@ -1067,6 +1096,8 @@ Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
     Plan p;
     p.rows_pad = (uint32_t)up(rows ? rows : 1, kTileM);
     p.dim8 = (uint32_t)up(dim, 8);
+    p.pitch = (uint32_t)up(dim, 64);
+    p.pad = dim % 8 || (dim % 64 && rows >= kAlignRows);
     const uint64_t vp = up(vocab, kTileN), tiles = vp / kTileN, nt = (dim + kTileN - 1) / kTileN;
     // D of a piece: 64 million elements (128 MB, about the L2) or 8,192 columns, whichever is more.
     // Within a factor of two above that, the width whose dweight tiles leave the fewest SMs idle
@@ -1099,8 +1130,8 @@ Plan make_plan(uint64_t rows, uint32_t dim, uint32_t vocab)
     p.factor = take(4ull * p.rows_pad);
     p.lse = take(4ull * p.rows_pad);
     p.logit = take(4ull * p.rows_pad);
-    p.gathered = take(2ull * p.rows_pad * p.dim8);
-    p.weight = take(dim % 8 ? 2ull * vocab * p.dim8 : 0);
+    p.gathered = take(2ull * p.rows_pad * p.pitch);
+    p.weight = take(p.pad ? 2ull * vocab * p.pitch : 0);
     const uint64_t shared = at;
     p.stats = take(8ull * p.rows_pad * (vp / 128));
     const uint64_t forward = at;
@@ -1160,26 +1191,27 @@ int prologue(const Call& c, const Plan& p, TokenArgs l, ProductArgs& a)
     l.rows = (uint32_t)c.rows;
     l.vocab = c.vocab;
     l.dim = c.dim;
-    l.dim8 = p.dim8;
+    l.pitch = p.pitch;
     l.head = head;
     l.token = reinterpret_cast<uint32_t*>(c.work + p.token);
     l.target = reinterpret_cast<int*>(c.work + p.target);
     l.lse_out = reinterpret_cast<float*>(c.work + p.lse);
     l.factor = reinterpret_cast<float*>(c.work + p.factor);
     l.f16 = c.dtype == ZERO_F16;
-    const bool direct = c.dim % 8 == 0 && c.hidden_stride % 8 == 0 && aligned_to(c.hidden, 16);
+    const bool direct = c.rows < kAlignRows ? c.dim % 8 == 0 && c.hidden_stride % 8 == 0 && aligned_to(c.hidden, 16)
+                                            : c.dim % 8 == 0 && c.hidden_stride % 64 == 0 && aligned_to(c.hidden, 128);
     l.direct = direct;
     l.hidden = static_cast<const uint16_t*>(c.hidden);
     l.hidden_stride = c.hidden_stride;
     uint16_t* gathered = reinterpret_cast<uint16_t*>(c.work + p.gathered);
     l.gathered = gathered;
     l.weight = static_cast<const uint16_t*>(c.weight);
-    l.padded = reinterpret_cast<uint16_t*>(c.work + p.weight);
-    const void* weight = c.dim % 8 ? c.work + p.weight : c.weight;
+    l.padded = p.pad ? reinterpret_cast<uint16_t*>(c.work + p.weight) : nullptr;
+    const void* weight = p.pad ? l.padded : c.weight;
     memset(&a, 0, sizeof a);
-    const uint64_t stride = c.rows > 1 ? c.hidden_stride : p.dim8;
-    if (!tensor_map(&a.gathered, gathered, c.dtype, c.dim, p.rows_pad, p.dim8, 64, kBoxRows) ||
-        !tensor_map(&a.weight, weight, c.dtype, c.dim, c.vocab, p.dim8, 64, kBoxRows) ||
+    const uint64_t stride = c.rows > 1 ? c.hidden_stride : p.dim8, pitch_w = p.pad ? p.pitch : c.dim;
+    if (!tensor_map(&a.gathered, gathered, c.dtype, c.dim, p.rows_pad, p.pitch, 64, kBoxRows) ||
+        !tensor_map(&a.weight, weight, c.dtype, c.dim, c.vocab, pitch_w, 64, kBoxRows) ||
         (l.backward && !tensor_map(&a.d, c.work + p.d, c.dtype, p.piece, p.rows_pad, p.piece, 64, kBoxRows)) ||
         (direct && c.rows && !tensor_map(&a.hidden, c.hidden, c.dtype, c.dim, c.rows, stride, 64, kBoxRows)))
         return map_refused();
@@ -1199,7 +1231,7 @@ int prologue(const Call& c, const Plan& p, TokenArgs l, ProductArgs& a)
     a.piece = p.piece;
     a.splits = 1;
     // row tiles whose hidden rows (32 MB) stay in L2 while weight passes by
-    const uint64_t group = (32ull << 20) / (kTileM * 2ull * p.dim8);
+    const uint64_t group = (32ull << 20) / (kTileM * 2ull * p.pitch);
     a.group = (uint32_t)(group ? group : 1);
     // tokens to at most a block per SM, 32 at least to each; rows to pad to all of them
     const uint64_t sms = (uint64_t)sm_count(), want = (c.rows + 31) / 32;
@@ -1207,7 +1239,7 @@ int prologue(const Call& c, const Plan& p, TokenArgs l, ProductArgs& a)
     l.per = (uint32_t)up((c.rows + l.blocks - 1) / l.blocks, 32);
     cudaError_t e = allow_smem<k_head_tokens>();
     if (e == cudaSuccess)
-        e = launch_pdl(k_head_tokens, dim3(c.dim % 8 ? (unsigned)sms : l.blocks), dim3(1024),
+        e = launch_pdl(k_head_tokens, dim3(p.pad ? (unsigned)sms : l.blocks), dim3(1024),
                        (size_t)l.per / 32 * 8, c.stream, l);
     return rows_status(e);
 }
