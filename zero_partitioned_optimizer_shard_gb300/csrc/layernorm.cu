@@ -30,85 +30,110 @@ struct ForwardArgs {
     float eps;
 };
 
-/* A sum over the n threads of a row, the same in each of them: n lanes of a warp (a power of
- * two), or the whole block. */
-__device__ __forceinline__ float lanes_sum(float x, uint32_t n)
+/* Sums of U values over n lanes of a warp (a power of two), the same in each of them; step by
+ * step for all U, whose exchanges then wait together. */
+template <int U>
+__device__ __forceinline__ void lanes_sums(float (&x)[U], uint32_t n)
 {
 #pragma unroll
     for (uint32_t o = 16; o; o >>= 1)
-        if (o < n)
-            x = __fadd_rn(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+        if (o < n) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x[u] = __fadd_rn(x[u], __shfl_xor_sync(0xffffffffu, x[u], o));
+        }
 }
 
-__device__ __forceinline__ float row_sum(float x, float* slots, uint32_t n)
+/* The same over the n threads of U rows: lanes of a warp, or (one row) the whole block. */
+template <int U>
+__device__ __forceinline__ void row_sums(float (&x)[U], float* slots, uint32_t n)
 {
-    x = lanes_sum(x, n);
-    if (n <= 32)
-        return x;
+    lanes_sums(x, n);
+    if (U > 1 || n <= 32)
+        return;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0)
-        slots[warp] = x;
+        slots[warp] = x[0];
     __syncthreads();
-    return warp_sum(lane < n / 32 ? slots[lane] : 0.0f);
+    x[0] = warp_sum(lane < n / 32 ? slots[lane] : 0.0f);
 }
 
-/* One row of n threads from its chunks: the statistics, and y (nothing is written of a row behind
- * the last).  params(i, w, b) gives chunk i's weights and biases. */
-template <zero_dtype_t DT, int NV, bool VEC, typename Params>
-__device__ __forceinline__ void norm_row(const ForwardArgs& a, uint32_t row, const typename Elem<DT>::Raw (&raw)[NV],
-                                         float (&slots)[2][32], uint32_t k, uint32_t n, Params params, bool there = true)
+/* U rows, `apart` from each other, of n threads each from their chunks: the statistics, and y
+ * (nothing is written of rows behind the last).  params(i, w, b) gives chunk i's weights and
+ * biases. */
+template <zero_dtype_t DT, int U, int NV, bool VEC, typename Params>
+__device__ __forceinline__ void norm_rows(const ForwardArgs& a, uint32_t row, uint32_t apart,
+                                          const typename Elem<DT>::Raw (&raw)[U][NV], float (&slots)[2][32], uint32_t k,
+                                          uint32_t n, Params params)
 {
     using T = typename Elem<DT>::T;
     const uint32_t d = a.d;
-    uint64_t s = 0;  // a pair of zeros
+    float mean[U], rstd[U];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        uint64_t v[4];
-        widen2<DT>(raw[i], v);
-        s = f2_add(s, f2_add(f2_add(v[0], v[1]), f2_add(v[2], v[3])));
-    }
-    const float mean = __fdiv_rn(row_sum(f2_sum(s), slots[0], n), (float)d);
-    const uint64_t mean2 = f2(mean, mean);
-    s = 0;
+    for (int u = 0; u < U; ++u) {
+        uint64_t s = 0;  // a pair of zeros
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        uint64_t v[4];
-        widen2<DT>(raw[i], v);
-        if (VEC && elem_of<VEC>(i, 0, k, n) >= d)
-            continue;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint64_t c = f2_sub(v[q], mean2);
-            if constexpr (!VEC) {
-                float c0, c1;
-                f2_split(c, c0, c1);
-                c = f2(elem_of<VEC>(i, 2 * q, k, n) < d ? c0 : 0.0f, elem_of<VEC>(i, 2 * q + 1, k, n) < d ? c1 : 0.0f);
-            }
-            s = f2_fma(c, c, s);
+        for (int i = 0; i < NV; ++i) {
+            uint64_t v[4];
+            widen2<DT>(raw[u][i], v);
+            s = f2_add(s, f2_add(f2_add(v[0], v[1]), f2_add(v[2], v[3])));
         }
+        mean[u] = f2_sum(s);
     }
-    const float var = __fdiv_rn(row_sum(f2_sum(s), slots[1], n), (float)d);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
-    if (!there)
-        return;
-    if (k == 0 && a.mean)
-        a.mean[row] = mean;
-    if (k == 0 && a.rstd)
-        a.rstd[row] = rstd;
-    const uint64_t rstd2 = f2(rstd, rstd);
-    T* y = static_cast<T*>(a.y) + (uint64_t)row * a.y_stride;
+    row_sums(mean, slots[0], n);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        uint64_t v[4], w[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
-        widen2<DT>(raw[i], v);
-        params(i, w, b);
+    for (int u = 0; u < U; ++u) {
+        mean[u] = __fdiv_rn(mean[u], (float)d);
+        const uint64_t mean2 = f2(mean[u], mean[u]);
+        uint64_t s = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            v[q] = f2_fma(f2_mul(f2_sub(v[q], mean2), rstd2), w[q], b[q]);
-        float out[8];
-        split4(v, out);
-        store_chunk<DT, VEC>(y, d, i, k, n, out);
+        for (int i = 0; i < NV; ++i) {
+            uint64_t v[4];
+            widen2<DT>(raw[u][i], v);
+            if (VEC && elem_of<VEC>(i, 0, k, n) >= d)
+                continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint64_t c = f2_sub(v[q], mean2);
+                if constexpr (!VEC) {
+                    float c0, c1;
+                    f2_split(c, c0, c1);
+                    c = f2(elem_of<VEC>(i, 2 * q, k, n) < d ? c0 : 0.0f, elem_of<VEC>(i, 2 * q + 1, k, n) < d ? c1 : 0.0f);
+                }
+                s = f2_fma(c, c, s);
+            }
+        }
+        rstd[u] = f2_sum(s);
+    }
+    row_sums(rstd, slots[1], n);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const float var = __fdiv_rn(rstd[u], (float)d);
+        rstd[u] = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(var, a.eps)));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t at = row + u * apart;
+        if (at >= a.rows)
+            break;
+        if (k == 0 && a.mean)
+            a.mean[at] = mean[u];
+        if (k == 0 && a.rstd)
+            a.rstd[at] = rstd[u];
+        const uint64_t mean2 = f2(mean[u], mean[u]), rstd2 = f2(rstd[u], rstd[u]);
+        T* y = static_cast<T*>(a.y) + (uint64_t)at * a.y_stride;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            uint64_t v[4], w[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+            widen2<DT>(raw[u][i], v);
+            params(i, w, b);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] = f2_fma(f2_mul(f2_sub(v[q], mean2), rstd2), w[q], b[q]);
+            float out[8];
+            split4(v, out);
+            store_chunk<DT, VEC>(y, d, i, k, n, out);
+        }
     }
 }
 
@@ -126,11 +151,11 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
     if (row >= a.rows)
         return;
     const T* x = static_cast<const T*>(a.x) + (uint64_t)row * a.x_stride;
-    typename Elem<DT>::Raw raw[NV];
+    typename Elem<DT>::Raw raw[1][NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        raw[i] = load_chunk<DT, VEC>(x, a.d, i, k, n);
-    norm_row<DT, NV, VEC>(a, row, raw, slots, k, n, [&](int i, uint64_t(&w)[4], uint64_t(&b)[4]) {
+        raw[0][i] = load_chunk<DT, VEC>(x, a.d, i, k, n);
+    norm_rows<DT, 1, NV, VEC>(a, row, 0, raw, slots, k, n, [&](int i, uint64_t(&w)[4], uint64_t(&b)[4]) {
         widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), a.d, i, k, n), w);
         if (a.bias)
             widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), a.d, i, k, n), b);
@@ -140,7 +165,8 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
 /* Rows of at most 256 elements (heads' norms): n = 4 to 32 lanes to a row, U rows of each such
  * group in flight, and the weights of a lane's columns in registers.  What bounds it is how many
  * loads are in flight: 204,800 rows of 64 bf16 take 19 us (7.7 for their bytes), a warp to a row
- * took 68; of 20,909 rows of 135, off the 16-byte grid, 33 us instead of 52. */
+ * took 68; of 20,909 rows of 135, off the 16-byte grid, 33 us instead of 52.  As many blocks as fit, over
+ * the rows in turns: 21 us and 29. */
 constexpr uint32_t kShortWarps = 8;
 
 template <zero_dtype_t DT, zero_dtype_t PT, int U, bool VEC>
@@ -162,16 +188,11 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_short(const Forw
     widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), a.d, 0, k, n), wk);
     if (a.bias)
         widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), a.d, 0, k, n), bk);
+    norm_rows<DT, U, 1, VEC>(a, first, rows, raw, slots, k, n, [&](int, uint64_t(&w)[4], uint64_t(&b)[4]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        norm_row<DT, 1, VEC>(
-            a, first + u * rows, raw[u], slots, k, n,
-            [&](int, uint64_t(&w)[4], uint64_t(&b)[4]) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    w[q] = wk[q], b[q] = bk[q];
-            },
-            first + u * rows < a.rows);
+        for (int q = 0; q < 4; ++q)
+            w[q] = wk[q], b[q] = bk[q];
+    });
 }
 
 #ifdef ZERO_TEST_HOOKS
@@ -271,13 +292,13 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const F
         const uint32_t q = turn % stages;
         const bool ok = __all_sync(0xffffffffu, wait_parity_bounded(smem_addr(&full[warp][q]), turn / stages & 1));
         const uint4* at = ring + q * row_bytes / 16;
-        typename Elem<DT>::Raw raw[NV];
+        typename Elem<DT>::Raw raw[1][NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const uint32_t c = i * 32 + lane;
-            raw[i] = {};
+            raw[0][i] = {};
             if (c * 8 < d)
-                raw[i] = shared_chunk<DT>(at, c);
+                raw[0][i] = shared_chunk<DT>(at, c);
         }
         __syncwarp();  // the stage has been read
         if (!ok) {     // a copy did not arrive within 2 s: this row and the warp's later ones tell, as NaN
@@ -291,7 +312,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const F
         }
         if (lane == 0)
             fetch(turn + stages);
-        norm_row<DT, NV, true>(a, (uint32_t)row, raw, slots, lane, 32, [&](int i, uint64_t(&w)[4], uint64_t(&b)[4]) {
+        norm_rows<DT, 1, NV, true>(a, (uint32_t)row, 0, raw, slots, lane, 32, [&](int i, uint64_t(&w)[4], uint64_t(&b)[4]) {
             const uint32_t c = i * 32 + lane;
             if (c * 8 < d) {
                 widen2<PT>(shared_chunk<PT>(weight, c), w);
@@ -617,8 +638,8 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
 
 /* Rows of at most 256 elements: n = 4 to 32 lanes to a row as in the forward pass, R rows of each
  * group in flight; at the end the groups' sums of a column are joined, those of a warp over its
- * lanes, then the warps' in order.  204,800 rows of 64 bf16: 28 us with the join (11.6 for the
- * bytes), 142 with a block to two rows; 20,909 rows of 135: 48 us instead of 64. */
+ * lanes, then the warps' in order.  204,800 rows of 64 bf16: 26 us with the join (11.6 for the
+ * bytes), 142 with a block to two rows; 20,909 rows of 135: 29 us instead of 64. */
 template <zero_dtype_t DT, zero_dtype_t PT, int R, bool VEC>
 __global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_backward_short(const BackwardArgs a, const uint32_t n)
 {
@@ -642,15 +663,22 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_backward_short(c
             mean[r] = len ? a.mean[row] : 0.0f;
             rstd[r] = len ? a.rstd[row] : 0.0f;
         }
+        uint64_t xh[R][4], g[R][4];
+        float s[2 * R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint64_t sg = 0, sx = 0;
+            c.template add<DT, VEC>(0, x[r], dy[r], mean[r], rstd[r], xh[r], g[r], sg, sx, d, k, n);
+            s[2 * r] = f2_sum(sg);
+            s[2 * r + 1] = f2_sum(sx);
+        }
+        lanes_sums(s, n);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const uint32_t row = row0 + r * groups + lane / n;
-            uint64_t xh[4], g[4], sg = 0, sx = 0;
-            c.template add<DT, VEC>(0, x[r], dy[r], mean[r], rstd[r], xh, g, sg, sx, d, k, n);
-            const float s = lanes_sum(f2_sum(sg), n), t = lanes_sum(f2_sum(sx), n);
             if (row < a.rows)
-                put_dx<DT, VEC>(0, static_cast<T*>(a.dx) + (uint64_t)row * a.dx_stride, d, k, n, xh, g, rstd[r],
-                                __fmul_rn(s, inv_d), __fmul_rn(t, inv_d));
+                put_dx<DT, VEC>(0, static_cast<T*>(a.dx) + (uint64_t)row * a.dx_stride, d, k, n, xh[r], g[r], rstd[r],
+                                __fmul_rn(s[2 * r], inv_d), __fmul_rn(s[2 * r + 1], inv_d));
         }
     }
     float v[2][8];
@@ -814,8 +842,9 @@ cudaError_t backward(const BackwardArgs& a, uint32_t& parts, cudaStream_t s)
     const uint32_t chunks = (a.d + 7) / 8, n = chunks <= 992 ? (chunks + 31) / 32 * 32 : 1024;
     if (chunks <= 32) {
         const uint32_t lanes = short_lanes(chunks), rows = kShortWarps * (32 / lanes);
-        return a.rows > 4 * rows * (uint32_t)sm_count()
-                   ? backward_blocks<k_layernorm_backward_short<DT, PT, 4, VEC>>(a, 32 * kShortWarps, 4 * rows, 0, parts, s, lanes)
+        constexpr uint32_t R = VEC ? 4 : 2;  // element by element 4 take 147 registers: 48 us instead of 34
+        return a.rows > R * rows * (uint32_t)sm_count()
+                   ? backward_blocks<k_layernorm_backward_short<DT, PT, R, VEC>>(a, 32 * kShortWarps, R * rows, 0, parts, s, lanes)
                    : backward_blocks<k_layernorm_backward_short<DT, PT, 1, VEC>>(a, 32 * kShortWarps, rows, 0, parts, s, lanes);
     }
     if (chunks > 992)
