@@ -637,23 +637,43 @@ cudaError_t sort_small(const SortArgs& a, uint32_t bits, const Fill& f, unsigned
                                          a, bits, f);
 }
 
-/* The first cluster sorts, the others fill. */
+/* The first cluster sorts, the others fill: as many as fit at once (35 with it; a second wave of
+ * three more cost 2 us of 40). */
 template <uint32_t ITEMS>
-cudaError_t sort_cluster(const SortArgs& a, uint2* other, uint32_t bits, const Fill& f, unsigned fillers, cudaStream_t s)
+cudaError_t sort_cluster(const SortArgs& a, uint2* other, uint32_t bits, const Fill& f, cudaStream_t s)
 {
+    static std::atomic<uint64_t> last{0};  // device + 1, clusters
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCluster + (fillers + kCluster - 1) / kCluster * kCluster);
+    cfg.gridDim = dim3(kCluster);
     cfg.blockDim = dim3(kSortThreads);
     cfg.dynamicSmemBytes = sizeof(RankSmem);
     cfg.stream = s;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = kCluster;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
+    if (f.n16 || f.tail_bytes) {
+        int dev = 0, fit = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        const uint64_t have = last.load(std::memory_order_relaxed);
+        if (e == cudaSuccess && have >> 32 == (uint64_t)dev + 1) {
+            fit = (int)(uint32_t)have;
+        } else if (e == cudaSuccess) {
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&fit, k_sort_cluster<ITEMS>, &cfg);
+            cfg.numAttrs = 2;
+            if (e == cudaSuccess)
+                last.store((uint64_t)(dev + 1) << 32 | (uint32_t)fit, std::memory_order_relaxed);
+        }
+        if (e != cudaSuccess)
+            return e;
+        const uint64_t want = (f.n16 + 4096 * kCluster - 1) / (4096 * kCluster), most = fit > 2 ? fit - 1 : 1;
+        cfg.gridDim = dim3((unsigned)(kCluster * (1 + (want < most ? (want ? want : 1) : most))));
+    }
     return cudaLaunchKernelEx(&cfg, k_sort_cluster<ITEMS>, a, other, bits, f);
 }
 
@@ -685,10 +705,10 @@ cudaError_t fill_and_sort(const Tokens& tokens, uint32_t n, void* table, uint64_
     if (n && n <= kCluster * kTile) {
         const uint32_t each = (n + kCluster * kSortThreads - 1) / (kCluster * kSortThreads);
         sorted = buf[(bits + 7) / 8 & 1 ? 0 : 1];
-        return each <= 1   ? sort_cluster<1>(a, buf[1], bits, f, fillers, s)
-               : each <= 2 ? sort_cluster<2>(a, buf[1], bits, f, fillers, s)
-               : each <= 4 ? sort_cluster<4>(a, buf[1], bits, f, fillers, s)
-                           : sort_cluster<8>(a, buf[1], bits, f, fillers, s);
+        return each <= 1   ? sort_cluster<1>(a, buf[1], bits, f, s)
+               : each <= 2 ? sort_cluster<2>(a, buf[1], bits, f, s)
+               : each <= 4 ? sort_cluster<4>(a, buf[1], bits, f, s)
+                           : sort_cluster<8>(a, buf[1], bits, f, s);
     }
     if (fillers)
         e = launch_pdl(k_zero_fill, dim3(fillers * 2), dim3(512), 0, s, f);
