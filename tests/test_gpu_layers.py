@@ -658,6 +658,58 @@ print("same")
     assert done.returncode == 0 and "same" in done.stdout, done.stderr[-2000:]
 
 
+def every_shape():
+    """One call of each of the operators' shapes that a small model does not reach: short and long rows of
+    layer norm, a cluster's sort and the one beyond it, rows of the head off the 128-byte grid."""
+    g = gen(7)
+    out = []
+    for n, d in ((20000, 64), (20000, 1600), (300, 5000), (40, 9000)):
+        x, w = normal(g, n, d, dtype=BF16), normal(g, d, dtype=BF16)
+        out.append([x, w, torch.empty_like(x), torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty_like(x),
+                    torch.empty(d, device="cuda"), torch.empty(d, device="cuda"),
+                    work_bytes(z.zero_layernorm_workspace_bytes(n, d))])
+    for n, d, v in ((3000, 64, 40000), (20000, 16, 70000), (66000, 8, 300)):
+        out.append([ids(g, n, v, torch.int64), normal(g, n, d), torch.empty(v, d, device="cuda"),
+                    work_bytes(z.zero_embedding_workspace_bytes(n, d, v))])
+    n, d, v = 2100, 200, 3000
+    out.append([normal(g, n, d, dtype=BF16), normal(g, v, d, sigma=0.1, dtype=BF16), ids(g, n, v, torch.int64),
+                torch.empty(n, device="cuda"), torch.empty(n, device="cuda"), torch.empty(n, d, dtype=BF16, device="cuda"),
+                torch.empty(v, d, dtype=BF16, device="cuda"), work_bytes(z.zero_head_workspace_bytes(n, d, v))])
+
+    def run():
+        for x, w, y, mean, rstd, dx, dw, db, work in out[:4]:
+            z.zero_layernorm(x, w, w, y, mean, rstd)
+            z.zero_layernorm_backward(x, w, mean, rstd, y, dx, dw, db, work)
+        for t, dout, dt, work in out[4:7]:
+            z.zero_embedding_backward(t, dout, dt, work)
+        h, w, t, loss, lse, dh, dw, work = out[7]
+        z.zero_head_loss(h, w, t, loss, lse, work)
+        z.zero_head_loss_backward(h, w, t, lse, dh, dw, work)
+
+    return run, [t for part in out for t in part[:-1]]
+
+
+def test_every_shape_captured_as_the_first_call_of_a_process():
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from tests import test_gpu_layers as T
+run, tensors = T.every_shape(); torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+graph.replay(); graph.replay(); torch.cuda.synchronize()
+other, others = T.every_shape(); other(); torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(tensors, others))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert done.returncode == 0 and "same" in done.stdout, done.stderr[-2000:]
+
+
 def test_two_captured_graphs_share_a_workspace():
     a, b = Tied(), Tied()
     b.work = a.work
