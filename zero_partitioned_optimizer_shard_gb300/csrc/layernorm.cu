@@ -139,7 +139,7 @@ __device__ __forceinline__ void norm_rows(const ForwardArgs& a, uint32_t row, ui
 
 /* One row per n threads: a warp (blockDim.y rows per block) or the whole block.  Calls of few rows,
  * where the launch counts, long rows, and rows off the 16-byte grid; of the last a warp would have
- * its 2-byte loads one after another (403 rows of 1,400: 19 us, 13 with 128 threads to a row). */
+ * its 2-byte loads one after another (403 rows of 1,400: 19 us, 9 with 256 threads to a row). */
 template <zero_dtype_t DT, zero_dtype_t PT, int NV, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
 {
@@ -782,8 +782,10 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
         return many ? launch_pdl(k_layernorm_short<DT, PT, 4, VEC>, grid, dim3(32 * kShortWarps), 0, s, a, lanes)
                     : launch_pdl(k_layernorm_short<DT, PT, 1, VEC>, grid, dim3(32 * kShortWarps), 0, s, a, lanes);
     }
-    // a warp per row up to 2,048 elements (no barrier) in 128-bit accesses, then 128 and 512 threads
-    const uint32_t n = VEC && chunks <= 256 ? 32 : chunks <= 1024 ? 128 : 512;
+    // in 128-bit accesses a warp per row up to 2,048 elements (no barrier), then 128 and 512 threads;
+    // element by element a chunk or two to a thread (4,096 rows of 1,601: 37 us with 128 threads, 29
+    // with 256, 53 with 512; 1,957 of 3,235: 42, 35, 31; 403 of 1,400: 13, 9, 13)
+    const uint32_t n = VEC ? (chunks <= 256 ? 32 : chunks <= 1024 ? 128 : 512) : chunks <= 128 ? 128 : chunks <= 1024 ? 256 : 512;
     const uint32_t per = (chunks + n - 1) / n, rows = n == 32 ? 4 : 1;
     if constexpr (VEC) {
         if (n == 32) {
@@ -809,13 +811,14 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
     };
     if (n == 512)
         return per <= 2 ? go(k_layernorm<DT, PT, 2, VEC, 512>) : go(k_layernorm<DT, PT, 4, VEC, 512>);
-    if constexpr (!VEC) {
-        if (per <= 1)
-            return go(k_layernorm<DT, PT, 1, VEC, 128>);
-    }
-    return per <= 2   ? go(k_layernorm<DT, PT, 2, VEC, 128>)
-           : per <= 4 ? go(k_layernorm<DT, PT, 4, VEC, 128>)
-                      : go(k_layernorm<DT, PT, 8, VEC, 128>);
+    if constexpr (VEC)
+        return per <= 2   ? go(k_layernorm<DT, PT, 2, VEC, 128>)
+               : per <= 4 ? go(k_layernorm<DT, PT, 4, VEC, 128>)
+                          : go(k_layernorm<DT, PT, 8, VEC, 128>);
+    else
+        return per <= 1   ? go(k_layernorm<DT, PT, 1, VEC, 256>)
+               : per <= 2 ? go(k_layernorm<DT, PT, 2, VEC, 256>)
+                          : go(k_layernorm<DT, PT, 4, VEC, 256>);
 }
 
 /* As many blocks as fit at once, each with its share of the rows and its part of the sums. */
