@@ -118,6 +118,21 @@ __device__ __forceinline__ uint4 ld_v4(const void* p)
     return v;
 }
 
+/* (A load through a volatile pointer would pass L1 by.) */
+__device__ __forceinline__ uint16_t ld_one(const uint16_t* p)
+{
+    uint16_t v;
+    asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float ld_one(const float* p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 __device__ __forceinline__ float4 as_f4(const uint4& v)
 {
     return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
@@ -146,7 +161,7 @@ __device__ __forceinline__ typename Elem<DT>::Raw load_chunk(const typename Elem
 #pragma unroll
         for (uint32_t j = 0; j < 8; ++j) {
             const uint32_t e = (i * 8 + j) * n + k;
-            x[j] = e < d ? *const_cast<const volatile typename Elem<DT>::T*>(row + e) : typename Elem<DT>::T(0);
+            x[j] = e < d ? ld_one(row + e) : typename Elem<DT>::T(0);
         }
         if constexpr (DT == ZERO_F32) {
             r.a = make_float4(x[0], x[1], x[2], x[3]);
