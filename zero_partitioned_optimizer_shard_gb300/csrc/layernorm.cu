@@ -14,7 +14,7 @@ namespace zero {
 namespace {
 
 constexpr uint32_t kMaxDim = 16384;
-constexpr uint32_t kMaxParts = 608;  // blocks of the backward pass: 4 on each of 152 SMs
+constexpr uint32_t kMaxParts = 912;  // blocks of the backward pass: 6 on each of 152 SMs
 constexpr uint32_t kRing = 4;        // stages of a ring, at most
 constexpr uint32_t kRingWarps = 8;   // forward: warps per block, each with a ring of its own
 
@@ -419,8 +419,6 @@ __device__ __forceinline__ void block_sums(float (&s)[N], float (&slots)[N][32],
 #pragma unroll
     for (int q = 0; q < N; ++q)
         s[q] = warp_sum(s[q]);
-    if (n == 32)
-        return;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) {
 #pragma unroll
@@ -458,13 +456,14 @@ __device__ __forceinline__ void block_sums4(float (&s)[4], float (&slots)[8][4],
 }
 
 /* R rows at a time per block, straight from global memory: rows that the bulk copies do not
- * take, and the longest.  Bound by the latency of a turn's loads and its barrier: 4,099 rows of
- * 641 fp16 take 18 us with the join (2.3 for the bytes). */
+ * take, and the longest.  Bound by the latency of a turn's loads and of its exchanges: 4,099 rows
+ * of 641 fp16 take 13.4 us with the join (2.3 for the bytes), 15.4 by at most 4 blocks to an SM
+ * instead of 6, 17 with 40 exchanges a turn instead of 13. */
 template <zero_dtype_t DT, zero_dtype_t PT, int NV, int R, bool VEC, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs a)
 {
     using T = typename Elem<DT>::T;
-    __shared__ float slots[2][2 * R][32];
+    __shared__ float slots[2][R == 2 ? 8 : 2 * R][R == 2 ? 4 : 32];
     grid_dependency_wait();
     grid_launch_dependents();
     const uint32_t n = blockDim.x, k = threadIdx.x, d = a.d;
@@ -496,7 +495,10 @@ __global__ void __launch_bounds__(MAXT) k_layernorm_backward(const BackwardArgs 
             s[2 * r] = f2_sum(sg);
             s[2 * r + 1] = f2_sum(sx);
         }
-        block_sums(s, slots[turn], n);
+        if constexpr (R == 2)
+            block_sums4(s, slots[turn], n);
+        else
+            block_sums(s, slots[turn], n);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row0 + r >= a.rows)
