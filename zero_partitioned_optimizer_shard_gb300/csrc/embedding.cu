@@ -421,27 +421,32 @@ struct GradArgs {
     float scale;
 };
 
-/* One row's piece of the gradient, with the scale, added to what is there if so asked. */
-template <zero_dtype_t GT, bool VEC>
-__device__ __forceinline__ void put_grad(const GradArgs& a, uint32_t token, uint32_t i, uint32_t k, uint32_t n,
-                                         const float (&s)[8])
+template <zero_dtype_t GT>
+__device__ __forceinline__ typename Elem<GT>::T* grad_row(const GradArgs& a, uint32_t token)
 {
-    using G = typename Elem<GT>::T;
-    G* row = static_cast<G*>(a.dtable) + (uint64_t)token * a.d;
-    float v[8];
-    if (a.accumulate)
-        widen<GT>(load_chunk<GT, VEC>(row, a.d, i, k, n), v);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = a.accumulate ? __fmaf_rn(s[j], a.scale, v[j]) : __fmul_rn(s[j], a.scale);
-    store_chunk<GT, VEC>(row, a.d, i, k, n, v);
+    return static_cast<typename Elem<GT>::T*>(a.dtable) + (uint64_t)token * a.d;
 }
 
-/* A block per chunk of sorted places and (rows beyond 2,048 elements) piece of the row, 8 rows in
+/* One row's piece of the gradient, with the scale, added to what was there (add). */
+template <zero_dtype_t GT, bool VEC>
+__device__ __forceinline__ void put_grad(const GradArgs& a, uint32_t token, uint32_t i, uint32_t k, uint32_t n,
+                                         const float (&s)[8], bool add, const typename Elem<GT>::Raw& old)
+{
+    float v[8];
+    widen<GT>(old, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = add ? __fmaf_rn(s[j], a.scale, v[j]) : __fmul_rn(s[j], a.scale);
+    store_chunk<GT, VEC>(grad_row<GT>(a, token), a.d, i, k, n, v);
+}
+
+/* A block per chunk of sorted places and (rows beyond 2,048 elements) piece of the row, Q rows in
  * flight to a thread.  Bound by memory and by the chunk's latency: 8,192 rows of 1,600 bf16 take 10
  * us, 26 MB at 2.6 TB/s.  A chunk is 16 places, so that few tokens reach over two of them and
- * a block still has two turns of loads; of few tokens 8, for twice the blocks. */
-template <zero_dtype_t DT, zero_dtype_t GT, bool VEC>
+ * a block still has two turns of loads; of few tokens 8, for twice the blocks.  What rows are added
+ * to (ADD) is loaded with the places that end them: row after row it was a round trip each (the whole call on 8,192
+ * rows of 1,600 33.6 us, so 31.5). */
+template <zero_dtype_t DT, zero_dtype_t GT, bool VEC, bool ADD>
 __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
 {
     using T = typename Elem<DT>::T;
@@ -463,16 +468,24 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
     const uint32_t n = blockDim.x, piece = blockIdx.y, k = threadIdx.x;
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     bool from_before = item[0].x == item[1].x;
-    for (uint32_t at = 0; at < len; at += 8) {
-        typename Elem<DT>::Raw x[8];
+    // places in flight; element by element 8 take 168 registers (8,192 rows of 1,001: 66 us a call, 53 with 4)
+    constexpr uint32_t Q = VEC ? 8 : 4;
+    for (uint32_t at = 0; at < len; at += Q) {
+        typename Elem<DT>::Raw x[Q];
+        typename Elem<GT>::Raw old[Q];
 #pragma unroll
-        for (uint32_t q = 0; q < 8; ++q) {
+        for (uint32_t q = 0; q < Q; ++q) {
             const uint2 it = item[1 + (at + q < len ? at + q : 0)];
             x[q] = load_chunk<DT, VEC>(static_cast<const T*>(a.dout) + it.y * a.dout_stride,
                                        at + q < len && it.x < a.vocab ? a.d : 0, piece, k, n);
+            old[q] = {};
+            if constexpr (ADD) {
+                const bool here = at + q < len && it.x < a.vocab && it.x != item[0].x && it.x != item[2 + at + q].x;
+                old[q] = load_chunk<GT, VEC>(grad_row<GT>(a, here ? it.x : 0), here ? a.d : 0, piece, k, n);
+            }
         }
 #pragma unroll
-        for (uint32_t q = 0; q < 8; ++q) {
+        for (uint32_t q = 0; q < Q; ++q) {
             if (at + q >= len)
                 break;
             const uint32_t token = item[1 + at + q].x;
@@ -489,7 +502,7 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
             if (from_before)
                 store_chunk<ZERO_F32, VEC>(a.head + (uint64_t)chunk * a.d, a.d, piece, k, n, s);
             else if (ends)
-                put_grad<GT, VEC>(a, token, piece, k, n, s);
+                put_grad<GT, VEC>(a, token, piece, k, n, s, ADD, old[q]);
             else
                 store_chunk<ZERO_F32, VEC>(a.tail + (uint64_t)chunk * a.d, a.d, piece, k, n, s);
             from_before = false;
@@ -550,7 +563,8 @@ __global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a, const 
 #pragma unroll
                 for (int r = 1; r < 8; ++r)
                     s[j] = __fadd_rn(s[j], part[r][j][lane]);
-            put_grad<GT, VEC>(a, token, piece, lane, 32, s);
+            put_grad<GT, VEC>(a, token, piece, lane, 32, s, a.accumulate,
+                              load_chunk<GT, VEC>(grad_row<GT>(a, token), a.accumulate ? a.d : 0, piece, lane, 32));
         }
         __syncthreads();
     }
@@ -605,9 +619,10 @@ cudaError_t lookup(const LookupArgs& a, bool vec, cudaStream_t s)
 template <zero_dtype_t DT, zero_dtype_t GT, bool VEC>
 cudaError_t sums(const GradArgs& a, cudaStream_t s)
 {
+    auto* kernel = a.accumulate ? k_embedding_sum<DT, GT, VEC, true> : k_embedding_sum<DT, GT, VEC, false>;
     const uint32_t chunks = (a.n + a.places - 1) / a.places, eights = (a.d + 7) / 8;
     const uint32_t threads = eights < 256 ? (eights + 31) / 32 * 32 : 256;
-    cudaError_t e = launch_pdl(k_embedding_sum<DT, GT, VEC>, dim3(chunks, (eights + threads - 1) / threads),
+    cudaError_t e = launch_pdl(kernel, dim3(chunks, (eights + threads - 1) / threads),
                                dim3(threads), 0, s, a);
     if (e != cudaSuccess)
         return e;
