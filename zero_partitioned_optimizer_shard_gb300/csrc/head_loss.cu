@@ -39,7 +39,7 @@ constexpr uint32_t kOutBytes = 4096;    // of an epilogue warp: 32 rows of 128 b
 constexpr uint32_t kSmem = kRingBytes + kEpilogueWarps * kOutBytes + 1024;  // and to a 1,024-byte boundary
 static_assert(kSmem <= 226 * 1024, "beside the barriers, of 227 KB");
 constexpr uint32_t kSms = 152;  // of a GB300: sizes the workspace and the splits
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 /* Head of the workspace. */
 struct Header {
@@ -178,6 +178,13 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+/* What a row's exponentials are taken relative to, its maximum; of a row of -inf anything will do,
+ * exp gives 0.  It is subtracted before log2(e) goes in: near the maximum that is exact, whatever the
+ * logits' size, and the maximum's own exponential is 1, so that a sum is 1 at least and its logarithm
+ * not negative.  (x * log2(e) - round(maximum * log2(e)) in one instruction has the rounding of a number
+ * of the logits' size in every exponent: lse off by 5.7e-5 at logits of 110, and losses below 0.) */
+__device__ __forceinline__ float reference(float top) { return top == __int_as_float(0xff800000) ? 0.0f : top; }
+
 struct Shared {
     uint64_t full[kMaxRing], empty[kMaxRing], acc_full[2], acc_empty[2], drain;
     uint32_t tmem, gave_up;
@@ -234,13 +241,16 @@ __device__ __forceinline__ void stats_epilogue(const ProductArgs& a, const Tile&
         for (uint32_t j = 0; j < 32; ++j)
             top[j & 3] = fmaxf(top[j & 3], x[q][j]);
     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    // a row of -inf: any reference will do, exp gives 0
-    const float ref = m == none ? 0.0f : __fmul_rn(m, kLog2e);
+    const uint64_t ref = f2(reference(m), reference(m));
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q)
 #pragma unroll
-        for (uint32_t j = 0; j < 32; ++j)
-            s[j & 3] = __fadd_rn(s[j & 3], exp2_approx(__fmaf_rn(x[q][j], kLog2e, -ref)));
+        for (uint32_t j = 0; j < 32; j += 2) {
+            float e0, e1;
+            f2_split(f2_mul(f2_sub(f2(x[q][j], x[q][j + 1]), ref), f2(kLog2e, kLog2e)), e0, e1);
+            s[j & 3] = __fadd_rn(s[j & 3], exp2_approx(e0));
+            s[(j + 1) & 3] = __fadd_rn(s[(j + 1) & 3], exp2_approx(e1));
+        }
     if (p.row < valid) {
         const uint32_t tiles = 2 * ((a.cols + kTileN - 1) / kTileN);
         a.stats[(uint64_t)p.row * tiles + 2 * t.nt + p.half] =
@@ -945,6 +955,12 @@ struct LossArgs {
     uint32_t tiles;
 };
 
+/* A sum of exponentials relative to top, relative to m instead. */
+__device__ __forceinline__ float below(float sum, float top, float m)
+{
+    return __fmul_rn(sum, exp2f(__fmul_rn(__fsub_rn(top, reference(m)), kLog2e)));
+}
+
 /* The tiles' statistics of a token, a warp per token: 7 us for 8,192 tokens of 50,257 logits, whose 26
  * MB come out of L2. */
 __global__ void __launch_bounds__(256) k_head_loss(const LossArgs a)
@@ -957,26 +973,23 @@ __global__ void __launch_bounds__(256) k_head_loss(const LossArgs a)
         float top = __int_as_float(0xff800000), sum = 0.0f;
         for (uint32_t i = lane; i < a.tiles; i += 32) {
             const float2 x = s[i];
-            const float m = fmaxf(top, x.x), ref = m == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(m, kLog2e);
-            sum = __fadd_rn(__fmul_rn(sum, exp2f(__fmaf_rn(top, kLog2e, -ref))),
-                            __fmul_rn(x.y, exp2f(__fmaf_rn(x.x, kLog2e, -ref))));
+            const float m = fmaxf(top, x.x);
+            sum = __fadd_rn(below(sum, top, m), below(x.y, x.x, m));
             top = m;
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             const float ot = __shfl_xor_sync(0xffffffffu, top, o), os = __shfl_xor_sync(0xffffffffu, sum, o);
-            const float m = fmaxf(top, ot), ref = m == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(m, kLog2e);
-            sum = __fadd_rn(__fmul_rn(sum, exp2f(__fmaf_rn(top, kLog2e, -ref))),
-                            __fmul_rn(os, exp2f(__fmaf_rn(ot, kLog2e, -ref))));
+            const float m = fmaxf(top, ot);
+            sum = __fadd_rn(below(sum, top, m), below(os, ot, m));
             top = m;
         }
         if (lane == 0) {
-            // sum is relative to 2^(top * log2e): the same product as in the exponents
-            const float ref = top == __int_as_float(0xff800000) ? 0.0f : __fmul_rn(top, kLog2e);
-            const float lse = a.head->error ? __int_as_float(0x7fc00000)
-                                            : __fmul_rn(__fadd_rn(log2f(sum), ref), kLn2);
-            a.lse[a.token[r]] = lse;
-            a.loss[a.token[r]] = __fsub_rn(lse, a.target_logit[r]);
+            // the maximum is taken off the target's logit before the logarithm comes in: a confident
+            // token's loss keeps its own digits, and is not negative
+            const float more = a.head->error ? __int_as_float(0x7fc00000) : logf(sum);
+            a.lse[a.token[r]] = __fadd_rn(top, more);
+            a.loss[a.token[r]] = __fadd_rn(__fsub_rn(top, a.target_logit[r]), more);
         }
     }
 }
