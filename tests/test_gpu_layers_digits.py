@@ -1,10 +1,10 @@
 """Digits that the operators beside the matrix products keep where a looser bound would hide a loss:
-confident tokens, logits far from 0.  Definitions in 64 bits."""
+confident tokens, logits far from 0, sums of many terms of one sign.  Definitions in 64 bits."""
 import pytest
 import torch
 
 import zero_partitioned_optimizer_shard_gb300 as z
-from tests.test_gpu_layers import BF16, F16, U, check, gen, work_bytes
+from tests.test_gpu_layers import BF16, F16, HALF, U, check, gen, normal, work_bytes
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,67 @@ def test_logits_far_from_0_over_a_large_vocabulary():
     check("lse", lse, want, torch.full_like(want, err))
     rows = torch.arange(n, device="cuda")
     check("loss", loss, want - l[rows, t], torch.full_like(want, err))
+
+
+def one_sign(n, d, v, seed):
+    """Tokens and weights whose logits' terms have one sign each: around +8 at row 0, -8 elsewhere."""
+    g = gen(seed)
+    h = (normal(g, n, d).abs() + 0.25).bfloat16()
+    w = normal(g, v, d).abs() + 0.25
+    w = w * (8.0 / (h.float().mean() * w.mean() * d))
+    w[1:].neg_()
+    return h, w.bfloat16()
+
+
+# A sum of d terms of one sign by the matrix unit: d/16 steps, each cut off by less than one unit
+# (2^-23) of what the sum is then.  In parts of 1,024 terms, 64 steps, whose sums grow evenly up to
+# a part of the logit, that is less than 2^-23 * 33 of the logit; in one part of 4,096 terms 4 times that.
+CUT = 33 * 2.0 ** -23
+
+
+def test_logits_of_many_terms_of_one_sign():
+    n, d, v = 512, 4096, 64
+    h, w = one_sign(n, d, v, 5)
+    _, lse = head_loss(h, w, torch.zeros(n, dtype=torch.int64, device="cuda"))
+    want = torch.logsumexp(h.double() @ w.double().T, 1)
+    assert float((lse.double() - want).mean().abs()) <= CUT * float(want.abs().mean())
+
+
+# ------------------------------------------------------------------------------------------
+# the loss's gradients
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [640, 4096])
+def test_gradients_of_confident_tokens(d, dtype):
+    """Targets that take all but 1e-4 of the softmax: D there is the small difference of two numbers
+    near 1, of which the logit in the backward pass and the lse of the forward pass must agree."""
+    n, v = 256, 1000
+    h, w = (x.to(dtype) for x in one_sign(n, d, v, 7))
+    t = torch.zeros(n, dtype=torch.int64, device="cuda")
+    _, lse = head_loss(h, w, t)
+    dh, dw = torch.empty_like(h), torch.empty(v, d, device="cuda")
+    z.zero_head_loss_backward(h, w, t, lse, dh, dw, work_bytes(z.zero_head_workspace_bytes(n, d, v)))
+    h64, w64 = h.double(), w.double()
+    l = h64 @ w64.T
+    lse64 = torch.logsumexp(l, 1)
+    p = torch.exp(l - lse64[:, None])
+    less = p[:, 1:].sum(1)              # 1 - p at the target, without cancellation
+    assert 1e-6 < float(less.min()) and float(less.max()) < 1e-2
+    D = p.clone()
+    D[:, 0] = -less
+    # logits off by CUT of their size (the same in both passes) change p by its own share of that.
+    # p - 1 takes in ex2's 2^-22 and what lse is off: half a unit of its own, and the roundings of its
+    # sum, which is 1 and a little.  The additions to a partial sum that holds the target's 1 round by
+    # half a unit of [1, 2), 2^-24, each: 31 in its chain of 32 columns, 2 where 4 chains join, then
+    # 1 turn over the 8 half tiles and 5 exchanges of k_head_loss: 64 at most.  Then D's rounding
+    el = CUT * (l.abs() + l[:, :1].abs())
+    ed = p * (el + 2.0 ** -21)
+    ed[:, 0] = less * el.amax(1) + 2.0 ** -24 * lse64.abs() + 2.0 ** -21 + 64 * 2.0 ** -24
+    ed += HALF[dtype] * D.abs() + (2.0 ** -39 if dtype == F16 else 0.0)
+    eh = ed @ w64.abs() + (v / 16 + 8) * 2.0 ** -21 * (D.abs() @ w64.abs())
+    ew = ed.T @ h64.abs() + (n / 16 + 8) * 2.0 ** -21 * (D.T.abs() @ h64.abs())
+    check("dhidden", dh, D @ w64, eh)
+    check("dweight", dw, D.T @ h64, ew)
+    # the target's row as a whole: nearly all of its bound is one-sided errors' room
+    want = (D.T @ h64)[0]
+    assert float((dw[0].double() - want).norm() / want.norm()) <= HALF[dtype] + float((ed[:, 0] / less).mean())

@@ -22,7 +22,10 @@
  * every target's share the same way: 2.9e-3 of dweight in one case, 1.7e-3 without).  bf16 has
  * fp32's range; for fp16 the unit is 2^14, so that softmax values down to 2^-28 stay normal
  * numbers.  Each D is rounded once, by at most 2^-8 of its value (bf16) or 2^-11 (fp16): the size
- * of the one rounding of the 16-bit gradients themselves.
+ * of the one rounding of the 16-bit gradients themselves.  Before that it is good to fp32's digits of
+ * the softmax, but for the target's: a difference from 1, it is off by what lse is (half a unit, and
+ * the roundings of a sum of 1 and a little) and by 2^-22 as well: one or two per cent of it where the
+ * target has all but 1e-4 of the softmax.
  */
 #include "tcgen05.cuh"
 
@@ -258,41 +261,41 @@ __device__ __forceinline__ void stats_epilogue(const ProductArgs& a, const Tile&
     }
 }
 
+/* x: the row's 128 logits of the tile, summed as the forward pass sums them, less lse before log2(e)
+ * goes in: at the target of a confident token D is a small difference from 1, of which a logit that
+ * differs from the one in lse by 1e-5, or an exponent rounded at lse's size, would leave little. */
 template <bool F16>
-__device__ __forceinline__ void d_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid)
+__device__ __forceinline__ void d_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t valid,
+                                           const float (&x)[4][32])
 {
     const bool in = p.row < valid;
     const int target = in ? a.target[p.row] - (int)a.v0 : -1;
     const float f = in ? a.factor[p.row] : 0.0f;
-    const float lse = in ? __fmul_rn(a.lse[p.row], kLog2e) : 0.0f;
-#pragma unroll 1
-    for (uint32_t c = 0; c < kTileN / 2; c += 64) {
-        const uint32_t col = t.n + p.half * (kTileN / 2) + c, off = (uint32_t)target - col;
-        uint4 v[8];
+    const float lse = in ? a.lse[p.row] : 0.0f;
+    const uint32_t col = t.n + p.half * (kTileN / 2), off = (uint32_t)target - col;
 #pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-            float x[32];
-            tmem_load32(p.acc + c + 32 * h, x);
+    for (uint32_t q = 0; q < 4; ++q) {  // 32 columns at a time: registers
+        uint32_t v[16];
 #pragma unroll
-            for (uint32_t j = 0; j < 32; ++j) {
-                float e = exp2_approx(__fmaf_rn(x[j], kLog2e, -lse));
-                if (off == 32 * h + j)
-                    e = __fsub_rn(e, 1.0f);
-                x[j] = in ? __fmul_rn(f, e) : 0.0f;
+        for (uint32_t j = 0; j < 32; j += 2) {
+            float e[2];
+            f2_split(f2_mul(f2_sub(f2(x[q][j], x[q][j + 1]), f2(lse, lse)), f2(kLog2e, kLog2e)), e[0], e[1]);
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i) {
+                e[i] = exp2_approx(e[i]);
+                e[i] = off == 32 * q + j + i ? __fsub_rn(e[i], 1.0f) : e[i];
+                e[i] = in && col + 32 * q + j + i < a.cols ? __fmul_rn(f, e[i]) : 0.0f;  // 0 behind the vocabulary
             }
-            if (col + 64 > a.cols) {  // behind the vocabulary
-#pragma unroll
-                for (uint32_t j = 0; j < 32; ++j)
-                    x[j] = col + 32 * h + j < a.cols ? x[j] : 0.0f;
-            }
-#pragma unroll
-            for (uint32_t q = 0; q < 4; ++q)
-                v[4 * h + q] = make_uint4(pack2<F16>(x[8 * q], x[8 * q + 1]), pack2<F16>(x[8 * q + 2], x[8 * q + 3]),
-                                          pack2<F16>(x[8 * q + 4], x[8 * q + 5]), pack2<F16>(x[8 * q + 6], x[8 * q + 7]));
+            v[j / 2] = pack2<F16>(e[0], e[1]);
         }
-        stage_wait(p.lane);
-        stage_row<128>(p.stage, p.lane, v);
-        stage_send(p.stage, p.lane, &a.out, col, p.row - p.lane, false);
+        if (q % 2 == 0)
+            stage_wait(p.lane);
+        stage_row<128>(p.stage, p.lane,
+                       {make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7]),
+                        make_uint4(v[8], v[9], v[10], v[11]), make_uint4(v[12], v[13], v[14], v[15])},
+                       q % 2 * 4);
+        if (q % 2)
+            stage_send(p.stage, p.lane, &a.out, col + 32 * (q - 1), p.row - p.lane, false);
     }
 }
 
@@ -461,13 +464,16 @@ __device__ unsigned long long zero_test_withheld_head_stage = ~0ull;
  * A launch has about 8 us of its own: start, first copies, last epilogue.
  *
  * The matrix unit cuts its fp32 sums off instead of rounding them, always toward 0: 256 steps
- * for a logit of 4,096 terms left the loss 1.5e-5 too small.  The losses therefore take a
- * logit in parts of 1,024 terms, added up in registers (measured: 4e-6 there, at no cost in
- * time).  The gradients' sums end in 16 bits and go without. */
+ * for a logit of 4,096 terms left the loss 1.5e-5 too small.  The logits are therefore taken
+ * in parts of 1,024 terms, added up in registers (measured: 4e-6 there, at no cost in time), by
+ * the losses and by D alike: D's logit and the one in lse have the same bits.  (D from logits in one
+ * part: of a target with all but 1e-4 of the softmax, over 4,096 terms of one sign, it was off by 80%.)
+ * The gradients' sums take operands of 16 bits, whose roundings pass what is cut off (2^-23 of the
+ * sum so far in each of its steps of 16 terms), and go without. */
 template <Mode MODE, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_constant__ ProductArgs a)
 {
-    constexpr uint32_t kPart = MODE == kStats ? kSumBlocks : ~0u;
+    constexpr uint32_t kPart = MODE == kGrads ? ~0u : kSumBlocks;
     constexpr uint32_t kK = MODE == kGrads ? kGradsK : kLogitsK, kHalf = kK / 64 * kBoxBytes, kStageBytes = 2 * kHalf;
     constexpr uint32_t kRing = kRingBytes / kStageBytes;
     static_assert(kRing <= kMaxRing, "barriers");
@@ -629,32 +635,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
             const Tile t = tiles.at(i);
             p.row = t.m + rank * kRows + quarter * 32 + lane;
             p.empty = t.k0 >= t.k1;
-            if constexpr (MODE == kStats) {
+            if constexpr (MODE != kGrads) {
+                // the first part's sums, then the others' added 16 columns at a time (both in one loop, 32 at
+                // a time, D's epilogue spilled 110 registers)
                 float x[4][32];
-                for (uint32_t k = t.k0; k < t.k1; k += kPart) {
+                acquire();
+                if (!ok)
+                    break;
+#pragma unroll
+                for (uint32_t q = 0; q < 4; ++q)
+                    tmem_load32(p.acc + 32 * q, x[q]);
+                release();
+#pragma unroll 1
+                for (uint32_t k = t.k0 + kPart; k < t.k1; k += kPart) {
                     acquire();
                     if (!ok)
                         break;
 #pragma unroll
-                    for (uint32_t q = 0; q < 4; ++q) {
-                        if (k == t.k0) {
-                            tmem_load32(p.acc + 32 * q, x[q]);
-                        } else {
-                            float y[32];
-                            tmem_load32(p.acc + 32 * q, y);
+                    for (uint32_t q = 0; q < 8; ++q) {
+                        float y[16];
+                        tmem_load16(p.acc + 16 * q, y);
 #pragma unroll
-                            for (uint32_t j = 0; j < 32; ++j)
-                                x[q][j] = __fadd_rn(x[q][j], y[j]);
-                        }
+                        for (uint32_t j = 0; j < 16; ++j)
+                            x[q / 2][q % 2 * 16 + j] = __fadd_rn(x[q / 2][q % 2 * 16 + j], y[j]);
                     }
                     release();
                 }
                 if (!ok)
                     break;
-                stats_epilogue(a, t, p, valid, x);
+                if constexpr (MODE == kStats)
+                    stats_epilogue(a, t, p, valid, x);
+                else
+                    d_epilogue<F16>(a, t, p, valid, x);
             } else {
                 OldRow old;
-                const bool add16 = MODE == kGrads && t.product == kDweight && a.bulk && a.accumulate && a.grad_dtype != ZERO_F32;
+                const bool add16 = t.product == kDweight && a.bulk && a.accumulate && a.grad_dtype != ZERO_F32;
                 if (add16)
                     old.load(a, t, p);
                 if (!p.empty) {
@@ -662,9 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                     if (!ok)
                         break;
                 }
-                if constexpr (MODE == kD)
-                    d_epilogue<F16>(a, t, p, valid);
-                else if (t.product == kDhidden)
+                if (t.product == kDhidden)
                     sum_epilogue<kDhidden, F16>(a, t, p, tiles.h.mt * kTileM);
                 else if (add16)
                     add_epilogue<F16>(a, t, p, old);

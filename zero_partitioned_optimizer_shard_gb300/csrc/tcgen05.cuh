@@ -97,6 +97,21 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32])
         v[i] = __uint_as_float(r[i]);
 }
 
+/* The same of 16 columns. */
+__device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+
 /* One box at (x: the contiguous dimension, y: the rows); what lies outside the tensor is 0.
  * x is a multiple of 8 elements.  bar: of either block of the pair. */
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
@@ -113,15 +128,16 @@ __device__ __forceinline__ void map_prefetch(const CUtensorMap* map)
 
 /* A warp's finished columns on their way out: written row by row (thread l: row l) under the
  * swizzle of a tensor map whose box is 32 rows of kBytes, then one bulk copy, which what lies
- * outside the tensor is cut from.  The lane that issues it also waits before the next one. */
-template <uint32_t kBytes>
-__device__ __forceinline__ void stage_row(uint32_t smem, uint32_t lane, const uint4 (&v)[kBytes / 16])
+ * outside the tensor is cut from.  The lane that issues it also waits before the next one.  v: the
+ * row's N pieces of 16 bytes from `first` on. */
+template <uint32_t kBytes, uint32_t N>
+__device__ __forceinline__ void stage_row(uint32_t smem, uint32_t lane, const uint4 (&v)[N], uint32_t first = 0)
 {
     static_assert(kBytes == 128 || kBytes == 64, "the swizzle of 128 or of 64 bytes");
     const uint32_t turn = kBytes == 128 ? lane & 7 : lane >> 1 & 3;
 #pragma unroll
-    for (uint32_t q = 0; q < kBytes / 16; ++q)
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(smem + lane * kBytes + ((q ^ turn) << 4)),
+    for (uint32_t q = 0; q < N; ++q)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(smem + lane * kBytes + (((first + q) ^ turn) << 4)),
                      "r"(v[q].x), "r"(v[q].y), "r"(v[q].z), "r"(v[q].w)
                      : "memory");
 }
