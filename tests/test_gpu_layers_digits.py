@@ -1,10 +1,13 @@
 """Digits that the operators beside the matrix products keep where a looser bound would hide a loss:
-confident tokens, logits far from 0, sums of many terms of one sign.  Definitions in 64 bits."""
+confident tokens, logits far from 0, sums of many terms of one sign, weights' gradients over many
+rows; and that the same call gives the same bits.  Definitions in 64 bits."""
+import math
+
 import pytest
 import torch
 
 import zero_partitioned_optimizer_shard_gb300 as z
-from tests.test_gpu_layers import BF16, F16, HALF, U, check, gen, normal, work_bytes
+from tests.test_gpu_layers import BF16, F16, F32, HALF, U, check, gen, ids, normal, work_bytes
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +133,43 @@ def test_gradients_of_confident_tokens(d, dtype):
     # the target's row as a whole: nearly all of its bound is one-sided errors' room
     want = (D.T @ h64)[0]
     assert float((dw[0].double() - want).norm() / want.norm()) <= HALF[dtype] + float((ed[:, 0] / less).mean())
+
+
+def test_the_heads_calls_repeat_their_bits():
+    """Pieces of the vocabulary, sums cut into splits, and tokens without a target: the same bits."""
+    for n, d, v, dtype, gt, acc in ((8192, 320, 20000, BF16, BF16, False), (1024, 640, 32000, F16, F32, True),
+                                    (40, 96, 700, BF16, F32, False), (500, 203, 3000, F16, F16, True)):
+        g = gen(n + v)
+        h, w, t = normal(g, n, d, dtype=dtype), normal(g, v, d, sigma=2.0 / math.sqrt(d), dtype=dtype), ids(g, n, v, torch.int64)
+        row, old, first = torch.rand(n, device="cuda", generator=g), normal(g, v, d, dtype=gt), None
+        for fill in (0xA5, 0x00, 0x5A, 0xFF):
+            work = work_bytes(z.zero_head_workspace_bytes(n, d, v)).fill_(fill)
+            loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+            dh, dw = torch.empty_like(h), old.clone()
+            z.zero_head_loss(h, w, t, loss, lse, work)
+            z.zero_head_loss_backward(h, w, t, lse, dh, dw, work, scale=1.0 / n, row_scale=row, accumulate=acc)
+            out = (loss, lse, dh, dw)
+            first = first or out
+            assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(out, first))
+
+
+# ------------------------------------------------------------------------------------------
+# layer norm's sums over rows
+# ------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("n,d,dtype", [(1_100_000, 2048, BF16), (300_000, 641, F16), (900_000, 64, BF16)])
+def test_the_weights_gradients_take_in_every_row(n, d, dtype):
+    """Sums over so many rows, as exact as their additions allow: in fp32 whole numbers below 2^24
+    add exactly, so a row left out or taken twice shows."""
+    g = gen(n)
+    x = torch.randint(0, 2, (n, d), device="cuda", generator=g, dtype=torch.int8).to(dtype)
+    dy = torch.empty_like(x)
+    for part in dy.split(1 << 18):
+        part.copy_(torch.randint(-2, 3, part.shape, device="cuda", generator=g, dtype=torch.int8))
+    w, mean, rstd = torch.ones(d, dtype=dtype, device="cuda"), torch.full((n,), -1.0, device="cuda"), torch.full((n,), 2.0, device="cuda")
+    dx, dw, db = torch.empty_like(x), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    z.zero_layernorm_backward(x, w, mean, rstd, dy, dx, dw, db, work_bytes(z.zero_layernorm_workspace_bytes(n, d)))
+    ww, wb = (torch.zeros(d, dtype=torch.float64, device="cuda") for _ in range(2))
+    for px, pd in zip(x.split(1 << 16), dy.split(1 << 16)):
+        ww += (pd.double() * (px.double() + 1.0) * 2.0).sum(0)
+        wb += pd.double().sum(0)
+    assert torch.equal(dw.double(), ww) and torch.equal(db.double(), wb)
