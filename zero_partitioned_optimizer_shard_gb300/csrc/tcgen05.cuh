@@ -78,10 +78,13 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns));
 }
 
-/* 32 columns of the warp's 32 accumulator rows: thread l gets row l. */
+/* 32 columns of the warp's 32 accumulator rows: thread l gets row l.  The whole warp executes the
+ * load together (.aligned), so it is brought together first: what comes before may have taken lanes
+ * apart (a row's end, the lane that sends a bulk copy). */
 __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32])
 {
     uint32_t r[32];
+    __syncwarp();
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
                  "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
@@ -101,6 +104,7 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32])
 __device__ __forceinline__ void tmem_load16(uint32_t at, float (&v)[16])
 {
     uint32_t r[16];
+    __syncwarp();
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
