@@ -15,7 +15,7 @@ SOURCES = ["partition.cu", "reduce.cu", "finalize.cu", "adamw.cu", "adamw_varian
            "embedding.cu", "head_loss.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("zero_internal.h", "adamw_elem.cuh", "reduce_elem.cuh",
                                            "step_scalars.cuh", "state8.cuh", "tensors.cuh", "rows.cuh",
-                                           "tcgen05.cuh")]
+                                           "tcgen05.cuh", "pad.h")]
 HEADERS.append(os.path.join(ROOT, "include", "zero.h"))
 
 ARCH = os.environ.get("ZERO_CUDA_ARCH", "103a")

@@ -27,6 +27,7 @@
  * the roundings of a sum of 1 and a little) and by 2^-22 as well: one or two per cent of it where the
  * target has all but 1e-4 of the softmax.
  */
+#include "pad.h"
 #include "tcgen05.cuh"
 
 namespace zero {
@@ -744,15 +745,16 @@ __device__ __forceinline__ int head_target(const void* p, uint32_t wide, uint32_
 }
 
 /* 8 outputs of a padded row at once, from 8 neighbours of the dense one: one 128-bit load, or the
- * 32-bit words that hold at least one of them, shifted where the row starts in the middle of a
- * word. */
+ * 32-bit words that hold at least one of them (pad.h). */
 struct PadChunk {
-    uint32_t w[5], odd, left;
+    uint32_t w[5], c, dim, odd;
     uint4* to;
 
     template <bool VEC>
-    __device__ __forceinline__ void load(const uint16_t* from, uint16_t* to_, uint32_t c, uint32_t dim)
+    __device__ __forceinline__ void load(const uint16_t* from, uint16_t* to_, uint32_t c_, uint32_t dim_)
     {
+        c = c_;
+        dim = dim_;
         to = reinterpret_cast<uint4*>(to_) + c;
         if constexpr (VEC) {
             const uint4 v = 8 * c < dim ? ld_v4(from + 8 * c) : make_uint4(0, 0, 0, 0);
@@ -760,21 +762,15 @@ struct PadChunk {
             return;
         }
         odd = (uintptr_t)from >> 1 & 1;
-        left = 8 * c + 8 <= dim ? 8 : 8 * c < dim ? dim - 8 * c : 0;
-        const volatile uint32_t* words = reinterpret_cast<const volatile uint32_t*>(from + 8 * c - odd);
-#pragma unroll
-        for (uint32_t j = 0; j < 5; ++j)
-            w[j] = left && 2 * j < left + odd ? words[j] : 0;
+        pad_load(w, c, dim, odd, [&](int64_t e) { return *reinterpret_cast<const volatile uint32_t*>(from + e); },
+                 [&](int64_t e) { return ld_one(from + e); });
     }
 
     template <bool VEC>
     __device__ __forceinline__ void store()
     {
-#pragma unroll
-        for (uint32_t j = 0; j < 4 && !VEC; ++j) {
-            w[j] = odd ? __funnelshift_r(w[j], w[j + 1], 16) : w[j];
-            w[j] = 2 * j + 1 < left ? w[j] : 2 * j < left ? w[j] & 0xffff : 0;
-        }
+        if constexpr (!VEC)
+            pad_shift(w, c, dim, odd);
         *to = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
