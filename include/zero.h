@@ -686,8 +686,8 @@ int zero_head_loss(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t voc
  *   scale       e.g. 1 / tokens, for the gradient of a mean
  *   row_scale   fp32 per token (what arrives at loss[t]), or NULL: 1
  *   st          the step state whose loss_scale the gradients get, or NULL: 1.  A bounded wait
- *               that gives up puts 1 into its error word (and the workspace's second word), and
- *               dhidden is NaN
+ *               that gives up puts 1 into its error word (and the workspace's second word);
+ *               dhidden is NaN then, and so is what was not formed of dweight
  *   dhidden     dtype, or NULL (not wanted);  dweight  grad_dtype, or NULL (not wanted) */
 int zero_head_loss_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t vocab, const void* hidden,
                             uint64_t hidden_stride, const void* weight, const void* targets, uint32_t target_bytes,

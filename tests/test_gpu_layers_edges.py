@@ -1,5 +1,5 @@
 """Edges of the operators beside the matrix products: rows that end inside a warp's columns with
-further tiles behind them.  Definitions in 64 bits."""
+further tiles behind them, and what waits that run out leave.  Definitions in 64 bits."""
 import math
 
 import pytest
@@ -35,3 +35,57 @@ def test_tiles_behind_a_rows_end(d, gt, acc):
     rh, eh, rw, ew = head_gradients(h, w, t, there, torch.full((n,), 1.0 / n, dtype=torch.float64, device="cuda"), BF16)
     check("dhidden", dh, rh, eh)
     check("dweight", dw, rw + old, ew + (2 * U * old.abs() if acc else 0.0))
+
+
+# ------------------------------------------------------------------------------------------
+# waits that run out
+# ------------------------------------------------------------------------------------------
+def prototypes(L):
+    import ctypes as C
+    ref = z.lib()
+    for name in ("zero_layernorm", "zero_layernorm_backward", "zero_head_loss", "zero_head_loss_backward"):
+        getattr(L, name).argtypes, getattr(L, name).restype = getattr(ref, name).argtypes, C.c_int
+    for name in ("zero_test_withhold_head_stage", "zero_test_withhold_norm_turn"):
+        getattr(L, name).argtypes, getattr(L, name).restype = [C.c_ulonglong], C.c_int
+    return L
+
+
+NEVER = 0xFFFFFFFFFFFFFFFF
+
+
+@pytest.mark.parametrize("d,gt,acc", [(64, BF16, False), (64, BF16, True), (64, F32, True), (63, BF16, False), (63, F32, True)])
+def test_weights_gradients_that_a_wait_left_undone_are_nan(hooked, d, gt, acc):
+    """dweight alone, without a step state.  79 tiles of 256 rows over 76 pairs of SMs: the first pair has
+    tiles 0 and 76.  A copy of D's launch that never comes leaves nothing of dweight; one of the
+    second tile (stages 5 to 9 of the gradients' launch; D's has 4) that tile's rows."""
+    L, g = prototypes(hooked), gen(d)
+    n, v, s = 600, 20000, torch.cuda.current_stream().cuda_stream
+    h, w, t = normal(g, n, d, dtype=BF16), normal(g, v, d, sigma=0.1, dtype=BF16), torch.randint(0, v, (n,), device="cuda", generator=g)
+    lse = torch.logsumexp(h.double() @ w.double().T, 1).float()
+    work = work_bytes(z.zero_head_workspace_bytes(n, d, v))
+    old = normal(g, v, d, sigma=0.1, dtype=gt)
+    code = z.ZERO_F32 if gt == F32 else z.ZERO_BF16
+
+    def run(stage):
+        dw = old.clone()
+        assert L.zero_test_withhold_head_stage(stage) == 0
+        assert L.zero_head_loss_backward(z.ZERO_BF16, n, d, v, h.data_ptr(), d, w.data_ptr(), t.data_ptr(), 8, lse.data_ptr(), 1.0,
+                                         None, None, None, 0, dw.data_ptr(), code, acc, work.data_ptr(), s) == 0
+        torch.cuda.synchronize()
+        assert L.zero_test_withhold_head_stage(NEVER) == 0
+        return dw, int(work[4:8].view(torch.int32))
+
+    good, error = run(NEVER)
+    assert error == 0 and torch.isfinite(good).all()
+    lost, error = run(2)
+    assert error == 1 and torch.isnan(lost).all()
+    lost, error = run(5)
+    assert error == 1
+    undone = slice(76 * 256, 77 * 256)
+    assert torch.isnan(lost[undone]).all()
+    rest = torch.cat([lost[:undone.start], lost[undone.stop:]])
+    want = torch.cat([good[:undone.start], good[undone.stop:]])
+    told = torch.isnan(rest)            # a tile that ended after the wait gave up may be NaN as well
+    assert torch.equal(rest[~told], want[~told]) and not told.all()
+    again, error = run(NEVER)
+    assert error == 0 and torch.equal(again, good)

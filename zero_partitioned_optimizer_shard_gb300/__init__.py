@@ -798,7 +798,8 @@ def zero_head_loss_backward(hidden, weight, targets, lse, dhidden, dweight, work
                             row_scale=None, st=None, accumulate: bool = False, stream=None) -> None:
     """The gradients of sum over tokens of scale * row_scale * loss, times the loss scale that the
     step state st holds (None: 1).  dhidden: hidden's type, or None; dweight: that or fp32, or
-    None; accumulate: dweight is added to."""
+    None; accumulate: dweight is added to.  Should a bounded wait inside give up, dhidden and what was
+    not formed of dweight are NaN, and st's error word is 1."""
     device, fn = _current(), "zero_head_loss_backward"
     sizes, stride, width = _head(hidden, weight, targets, device)
     code, n, dim, vocab = sizes

@@ -76,7 +76,7 @@ struct ProductArgs {
     const float* lse;       // [valid]
     float* target_logit;    // [valid]
     float2* stats;          // [valid][2 * column tiles]
-    void* dweight;          // one split: where it lies as the TMA does not take it, or 16 bits are added to
+    void* dweight;
     uint32_t rows;          // of the call, with or without a target
     uint32_t rows_pad, dim, dim8, vocab;
     uint32_t v0, cols;      // the piece: columns [v0, v0 + cols) of the vocabulary
@@ -366,10 +366,27 @@ struct OldRow {
 };
 
 template <bool F16>
+__device__ __forceinline__ void put_nan(const ProductArgs& a, uint64_t at)
+{
+    const float nan = __int_as_float(0x7fc00000);
+    if (a.grad_dtype == ZERO_F32)
+        static_cast<float*>(a.dweight)[at] = nan;
+    else
+        static_cast<uint16_t*>(a.dweight)[at] = from_f32<F16 ? ZERO_F16 : ZERO_BF16>(nan);
+}
+
+/* The weight gradient's factor beside D: NaN once a wait has given up, in an earlier launch of the
+ * call or in this one. */
+__device__ __forceinline__ float weight_factor(const ProductArgs& a)
+{
+    return *const_cast<const volatile uint32_t*>(&a.head->error) ? __int_as_float(0x7fc00000) : a.head->post;
+}
+
+template <bool F16>
 __device__ __forceinline__ void add_epilogue(const ProductArgs& a, const Tile& t, const Part& p, const OldRow& old)
 {
     constexpr zero_dtype_t GT = F16 ? ZERO_F16 : ZERO_BF16;
-    const float post = a.head->post;
+    const float post = weight_factor(a);
     const uint32_t row0 = p.row - p.lane;
 #pragma unroll
     for (uint32_t c = 0; c < kTileN / 2; c += 32) {
@@ -401,7 +418,7 @@ __device__ __forceinline__ void add_epilogue(const ProductArgs& a, const Tile& t
 template <Product P, bool F16>
 __device__ __forceinline__ void sum_epilogue(const ProductArgs& a, const Tile& t, const Part& p, uint32_t rows)
 {
-    const float post = P == kDweight && a.splits == 1 ? a.head->post : 1.0f;
+    const float post = P == kDweight && a.splits == 1 ? weight_factor(a) : 1.0f;
     const uint32_t row0 = p.row - p.lane;
 #pragma unroll 1
     for (uint32_t c = 0; c < kTileN / 2; c += 32) {
@@ -632,7 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
                 bar_arrive(of_first(smem_addr(&sh.acc_empty[buf & 1])));
             ++buf;
         };
-        for (uint32_t i = first; i < tiles.total; i += step) {
+        uint32_t i = first;
+        for (; i < tiles.total; i += step) {
             const Tile t = tiles.at(i);
             p.row = t.m + rank * kRows + quarter * 32 + lane;
             p.empty = t.k0 >= t.k1;
@@ -690,6 +708,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_head_product(const __grid_const
         }
         if (lane == 0)  // what is on its way out has left shared memory, and is written
             asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if constexpr (MODE == kGrads) {  // a wait gave up: the tiles of dweight left undone tell, as NaN
+            __syncwarp();
+            for (; i < tiles.total && a.splits == 1; i += step) {
+                const Tile t = tiles.at(i);
+                if (t.product != kDweight)
+                    continue;
+                const uint32_t row = t.m + rank * kRows + quarter * 32 + lane, at = p.half * (kTileN / 2);
+                const uint32_t end = t.width < at + kTileN / 2 ? t.width : at + kTileN / 2;
+                if (row < a.cols)
+                    for (uint32_t c = at; c < end && t.n + c < a.dim; ++c)
+                        put_nan<F16>(a, (uint64_t)(a.v0 + row) * a.dim + t.n + c);
+            }
+        }
     }
     __syncwarp();
     tmem_fence_before();
