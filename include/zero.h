@@ -626,7 +626,8 @@ size_t zero_layernorm_workspace_bytes(uint64_t rows, uint32_t dim);
  *   dweight, dbias  grad_dtype, dim elements; each may be NULL (not wanted)
  *   workspace       DEVICE, zero_layernorm_workspace_bytes(rows, dim), 16-byte aligned
  * Without rows dweight and dbias are 0 (or left as they are, accumulate).  Should a bounded wait
- * inside give up, dweight, dbias and the rows of dx left undone are NaN; of zero_layernorm, y's. */
+ * inside give up, dweight, dbias and the rows of dx left undone are NaN; of zero_layernorm, the rows of
+ * y left undone with their mean and rstd. */
 int zero_layernorm_backward(zero_dtype_t dtype, uint64_t rows, uint32_t dim, const void* x, uint64_t x_stride,
                             const void* weight, zero_dtype_t param_dtype, const float* mean, const float* rstd,
                             const void* dy, uint64_t dy_stride, void* dx, uint64_t dx_stride, void* dweight,

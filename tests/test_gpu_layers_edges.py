@@ -89,3 +89,18 @@ def test_weights_gradients_that_a_wait_left_undone_are_nan(hooked, d, gt, acc):
     assert torch.equal(rest[~told], want[~told]) and not told.all()
     again, error = run(NEVER)
     assert error == 0 and torch.equal(again, good)
+
+
+def test_rows_that_a_wait_left_undone_have_no_statistics(hooked):
+    L, g = prototypes(hooked), gen(4)
+    n, d, s = 20000, 1600, torch.cuda.current_stream().cuda_stream
+    x, w = normal(g, n, d, dtype=BF16), normal(g, d, dtype=BF16)
+    y, mean, rstd = torch.zeros_like(x), torch.full((n,), 7.0, device="cuda"), torch.full((n,), 7.0, device="cuda")
+    assert L.zero_test_withhold_norm_turn(1) == 0
+    assert L.zero_layernorm(z.ZERO_BF16, n, d, x.data_ptr(), d, w.data_ptr(), w.data_ptr(), z.ZERO_BF16, 1e-5, y.data_ptr(), d,
+                            mean.data_ptr(), rstd.data_ptr(), s) == 0
+    torch.cuda.synchronize()
+    assert L.zero_test_withhold_norm_turn(NEVER) == 0
+    lost = torch.isnan(y).all(1)
+    assert 0 < int(lost.sum()) < n
+    assert torch.equal(torch.isnan(mean), lost) and torch.equal(torch.isnan(rstd), lost)

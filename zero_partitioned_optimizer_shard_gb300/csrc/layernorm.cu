@@ -305,9 +305,15 @@ __global__ void __launch_bounds__(32 * kRingWarps, 3) k_layernorm_staged(const F
             if (lane == 0)
                 for (uint32_t t = turn; t < turn + stages && first + t * step < a.rows; ++t)
                     wait_parity_bounded(smem_addr(&full[warp][t % stages]), t / stages & 1);
-            for (; row < a.rows; row += step)
+            const float nan = __int_as_float(0x7fc00000);
+            for (; row < a.rows; row += step) {
                 for (uint32_t c = lane; c < d; c += 32)
-                    static_cast<T*>(a.y)[row * a.y_stride + c] = from_f32<DT>(__int_as_float(0x7fc00000));
+                    static_cast<T*>(a.y)[row * a.y_stride + c] = from_f32<DT>(nan);
+                if (lane == 0 && a.mean)
+                    a.mean[row] = nan;
+                if (lane == 0 && a.rstd)
+                    a.rstd[row] = nan;
+            }
             return;
         }
         if (lane == 0)
