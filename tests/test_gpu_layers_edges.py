@@ -1,12 +1,12 @@
 """Edges of the operators beside the matrix products: rows that end inside a warp's columns with
-further tiles behind them, and what waits that run out leave.  Definitions in 64 bits."""
+further tiles behind them, short rows in turns, and what waits that run out leave.  Definitions in 64 bits."""
 import math
 
 import pytest
 import torch
 
 import zero_partitioned_optimizer_shard_gb300 as z
-from tests.test_gpu_layers import BF16, F32, U, check, gen, head_gradients, normal, work_bytes
+from tests.test_gpu_layers import BF16, F16, F32, U, check, gen, head_gradients, norm_bounds, norm_forward, normal, work_bytes
 
 pytestmark = pytest.mark.gpu
 
@@ -35,6 +35,21 @@ def test_tiles_behind_a_rows_end(d, gt, acc):
     rh, eh, rw, ew = head_gradients(h, w, t, there, torch.full((n,), 1.0 / n, dtype=torch.float64, device="cuda"), BF16)
     check("dhidden", dh, rh, eh)
     check("dweight", dw, rw + old, ew + (2 * U * old.abs() if acc else 0.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("n,d,pad", [(200_003, 33, 0), (100_001, 65, 3), (60_007, 255, 0), (300_000, 9, 1), (150_001, 64, 1)])
+def test_many_short_rows_off_the_16_byte_grid(n, d, pad, dtype):
+    """More rows than as many blocks as fit take at a time: 16-bit ones go on in turns."""
+    g = gen(n + d)
+    x = normal(g, n, d + pad, dtype=dtype)[:, :d]
+    w, b = normal(g, d, dtype=dtype) + 1.0, normal(g, d, dtype=dtype)
+    y, mean, rstd = torch.full((n, d + 2), 7.0, dtype=dtype, device="cuda"), torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    z.zero_layernorm(x, w, b, y[:, :d], mean, rstd)
+    want, m64, r64 = norm_forward(x, w, b, 1e-5)
+    check("y", y[:, :d], want, norm_bounds(x, w, m64, r64, want)[0])
+    check("mean", mean, m64, norm_bounds(x, w, m64, r64, want)[1])
+    assert (y[:, d:] == 7.0).all()
 
 
 # ------------------------------------------------------------------------------------------

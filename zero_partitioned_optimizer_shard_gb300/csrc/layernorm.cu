@@ -164,10 +164,16 @@ __global__ void __launch_bounds__(MAXT) k_layernorm(const ForwardArgs a)
 
 /* Rows of at most 256 elements (heads' norms): n = 4 to 32 lanes to a row, U rows of each such
  * group in flight, and the weights of a lane's columns in registers.  What bounds it is how many
- * loads are in flight: 204,800 rows of 64 bf16 take 19 us (7.7 for their bytes), a warp to a row
- * took 68; of 20,909 rows of 135, off the 16-byte grid, 33 us instead of 52.  As many blocks as fit, over
- * the rows in turns: 21 us and 29. */
+ * loads are in flight: 204,800 rows of 64 bf16 take 18.5 us (7.7 for their bytes), a warp to a row
+ * took 68.  16-bit rows off the 16-byte grid, whose every access is 2 bytes wide, by as many blocks as
+ * fit, over the rows in turns: their weights' 16 narrow loads come once, not with every 4 rows (20,909
+ * rows of 135 bf16 25.0 us with a block to every 4 rows of its groups, so 23.2; 100,000 of 65 41.3, so 34.5;
+ * 200,000 of 33 fp16 28.9, so 26.3; 50,000 of 255 the same).  All others with a block to its rows (in turns: 204,800 of 64 bf16 18.5, 20.3;
+ * of 64 fp32 23.0, 24.3; 20,909 of 135 fp32, whose accesses are twice as wide, 18.8, 20.2). */
 constexpr uint32_t kShortWarps = 8;
+
+template <zero_dtype_t DT, int U, bool VEC>
+constexpr bool kShortTurns = !VEC && DT != ZERO_F32 && U > 1;
 
 template <zero_dtype_t DT, zero_dtype_t PT, int U, bool VEC>
 __global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_short(const ForwardArgs a, const uint32_t n)
@@ -177,22 +183,41 @@ __global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_short(const Forw
     __shared__ float slots[2][32];  // not used by single warps
     grid_dependency_wait();
     const uint32_t lane = threadIdx.x & 31, k = lane & (n - 1), rows = 32 / n;
-    const uint32_t first = (blockIdx.x * kShortWarps + (threadIdx.x >> 5)) * U * rows + lane / n;
+    uint32_t first = (blockIdx.x * kShortWarps + (threadIdx.x >> 5)) * U * rows + lane / n;
     typename Elem<DT>::Raw raw[U][1];
+    auto load = [&] {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const uint32_t row = first + u * rows;
-        raw[u][0] = load_chunk<DT, VEC>(static_cast<const T*>(a.x) + (uint64_t)row * a.x_stride, row < a.rows ? a.d : 0, 0, k, n);
-    }
+        for (int u = 0; u < U; ++u) {
+            const uint32_t row = first + u * rows;
+            raw[u][0] =
+                load_chunk<DT, VEC>(static_cast<const T*>(a.x) + (uint64_t)row * a.x_stride, row < a.rows ? a.d : 0, 0, k, n);
+        }
+    };
     uint64_t wk[4], bk[4] = {0, 0, 0, 0};
-    widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), a.d, 0, k, n), wk);
-    if (a.bias)
-        widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), a.d, 0, k, n), bk);
-    norm_rows<DT, U, 1, VEC>(a, first, rows, raw, slots, k, n, [&](int, uint64_t(&w)[4], uint64_t(&b)[4]) {
+    auto weights = [&] {
+        widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.weight), a.d, 0, k, n), wk);
+        if (a.bias)
+            widen2<PT>(load_chunk<PT, VEC>(static_cast<const P*>(a.bias), a.d, 0, k, n), bk);
+    };
+    auto norm = [&] {
+        norm_rows<DT, U, 1, VEC>(a, first, rows, raw, slots, k, n, [&](int, uint64_t(&w)[4], uint64_t(&b)[4]) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            w[q] = wk[q], b[q] = bk[q];
-    });
+            for (int q = 0; q < 4; ++q)
+                w[q] = wk[q], b[q] = bk[q];
+        });
+    };
+    if constexpr (kShortTurns<DT, U, VEC>) {
+        weights();
+        const uint32_t step = gridDim.x * kShortWarps * U * rows;
+        for (; first - lane / n < a.rows; first += step) {  // the same for the whole warp
+            load();
+            norm();
+        }
+    } else {
+        load();
+        weights();
+        norm();
+    }
 }
 
 #ifdef ZERO_TEST_HOOKS
@@ -786,7 +811,15 @@ cudaError_t forward(const ForwardArgs& a, cudaStream_t s)
     if (chunks <= 32) {
         const uint32_t lanes = short_lanes(chunks), rows = kShortWarps * (32 / lanes);
         const bool many = a.rows > 4 * rows * (uint32_t)sm_count();  // a block on each SM, with 4 rows to a group
-        const dim3 grid(many ? (a.rows + 4 * rows - 1) / (4 * rows) : (a.rows + rows - 1) / rows);
+        uint32_t blocks = many ? (a.rows + 4 * rows - 1) / (4 * rows) : (a.rows + rows - 1) / rows;
+        if (kShortTurns<DT, 4, VEC> && many) {
+            uint32_t fit = 0;
+            const cudaError_t e = resident<k_layernorm_short<DT, PT, 4, VEC>>(32 * kShortWarps, 0, fit);
+            if (e != cudaSuccess)
+                return e;
+            blocks = blocks < fit ? blocks : fit;
+        }
+        const dim3 grid(blocks);
         return many ? launch_pdl(k_layernorm_short<DT, PT, 4, VEC>, grid, dim3(32 * kShortWarps), 0, s, a, lanes)
                     : launch_pdl(k_layernorm_short<DT, PT, 1, VEC>, grid, dim3(32 * kShortWarps), 0, s, a, lanes);
     }
