@@ -111,7 +111,7 @@ def space(bytes_: int, like: torch.Tensor) -> torch.Tensor:
 
 
 class Embed(torch.autograd.Function):
-    """Rows of the table; their gradient is added to what the head left in table.grad."""
+    """Rows of the table; their gradient is added to table.grad, where the head's went."""
 
     @staticmethod
     def forward(ctx, table, tokens, scale):
@@ -149,7 +149,8 @@ class Norm(torch.autograd.Function):
 
 class HeadLoss(torch.autograd.Function):
     """Each token's cross entropy against the table's rows, without the logits.  The backward pass
-    multiplies by the step state's loss scale and overwrites table.grad."""
+    multiplies by the step state's loss scale and adds to table.grad (zeros before the first
+    micro-batch of a step)."""
 
     @staticmethod
     def forward(ctx, hidden, table, targets, st):
@@ -165,7 +166,7 @@ class HeadLoss(torch.autograd.Function):
         hidden, targets, lse, work = ctx.saved_tensors
         dhidden = torch.empty_like(hidden)
         z.zero_head_loss_backward(hidden, ctx.table, targets, lse, dhidden, ctx.table.grad, work,
-                                  row_scale=dloss.contiguous(), st=ctx.st)
+                                  row_scale=dloss.contiguous(), st=ctx.st, accumulate=True)
         return dhidden, None, None, None
 
 
