@@ -110,6 +110,14 @@ def space(bytes_: int, like: torch.Tensor) -> torch.Tensor:
     return torch.empty(bytes_, dtype=torch.uint8, device=like.device)
 
 
+def gradient(table: torch.Tensor) -> torch.Tensor:
+    """table.grad, zeros where there is none yet (zero_grad lets gradients go; the list then takes the
+    new ones by set_grad)."""
+    if table.grad is None:
+        table.grad = torch.zeros_like(table)
+    return table.grad
+
+
 class Embed(torch.autograd.Function):
     """Rows of the table; their gradient is added to table.grad, where the head's went."""
 
@@ -125,7 +133,7 @@ class Embed(torch.autograd.Function):
     def backward(ctx, dout):
         (tokens,), (vocab, dim) = ctx.saved_tensors, ctx.table.shape
         work = space(z.zero_embedding_workspace_bytes(tokens.numel(), dim, vocab), dout)
-        z.zero_embedding_backward(tokens, dout.contiguous(), ctx.table.grad, work, scale=ctx.scale, accumulate=True)
+        z.zero_embedding_backward(tokens, dout.contiguous(), gradient(ctx.table), work, scale=ctx.scale, accumulate=True)
         return None, None, None
 
 
@@ -165,7 +173,7 @@ class HeadLoss(torch.autograd.Function):
     def backward(ctx, dloss):
         hidden, targets, lse, work = ctx.saved_tensors
         dhidden = torch.empty_like(hidden)
-        z.zero_head_loss_backward(hidden, ctx.table, targets, lse, dhidden, ctx.table.grad, work,
+        z.zero_head_loss_backward(hidden, ctx.table, targets, lse, dhidden, gradient(ctx.table), work,
                                   row_scale=dloss.contiguous(), st=ctx.st, accumulate=True)
         return dhidden, None, None, None
 

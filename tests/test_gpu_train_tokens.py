@@ -1,4 +1,5 @@
-"""The example's token model as programs use it around its backward pass: micro-batches."""
+"""The example's token model as programs use it around its backward pass: micro-batches,
+gradients let go between steps."""
 import importlib.util
 import os
 
@@ -47,3 +48,19 @@ def test_micro_batches_add_up(example):
     for name, got in gradients(model).items():
         a, b = alone[0][name], alone[1][name]
         assert float((got - a - b).norm()) <= 6 * 2.0 ** -8 * float(a.norm() + b.norm()), name
+
+
+def test_gradients_that_were_let_go_come_back(example):
+    model, opt = example.token_model(VOCAB, DIM)
+    backward(example, model, opt, 1)
+    want = gradients(model)
+    model.zero_grad(set_to_none=True)
+    backward(example, model, opt, 1)
+    got = gradients(model)
+    assert set(got) == set(want)
+    for name in want:                   # the sums that torch makes may vary in their last bits
+        assert float((got[name] - want[name]).norm()) <= 2.0 ** -8 * float(want[name].norm()), name
+    opt.list.set_grad(opt.grads())
+    before = [x.clone() for x in opt.master]
+    opt.step()
+    assert all(not torch.equal(a, b) for a, b in zip(before, opt.master))
