@@ -679,7 +679,7 @@ int zero_head_loss(zero_dtype_t dtype, uint64_t rows, uint32_t dim, uint32_t voc
 /* Its gradients.  With f[t] = scale * row_scale[t] * st->loss_scale:
  *   D[t][v]   = f[t] * (exp(l[t][v] - lse[t]) - (v == targets[t]))
  *   dhidden   = D . weight  (0 for tokens without a target);  dweight (+)= D^T . hidden
- * D is formed a piece of the vocabulary at a time, in units of the largest |f| (fp16: of 2^-14
+ * D is formed a piece of the vocabulary at a time, in units of the largest finite |f| (fp16: of 2^-14
  * of it), and rounded to dtype before the two products; also for an fp32 dweight, whose rows are
  * thus good to dtype's digits.  fp16: tokens whose |f| is less than 2^-14 of the largest lose
  * digits.

@@ -1,5 +1,6 @@
 """Edges of the operators beside the matrix products: rows that end inside a warp's columns with
-further tiles behind them, short rows in turns, and what waits that run out leave.  Definitions in 64 bits."""
+further tiles behind them, short rows in turns, factors that are not finite, and what waits that run
+out leave.  Definitions in 64 bits."""
 import math
 
 import pytest
@@ -50,6 +51,29 @@ def test_many_short_rows_off_the_16_byte_grid(n, d, pad, dtype):
     check("y", y[:, :d], want, norm_bounds(x, w, m64, r64, want)[0])
     check("mean", mean, m64, norm_bounds(x, w, m64, r64, want)[1])
     assert (y[:, d:] == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_a_factor_that_is_not_finite_is_its_own_tokens(value, dtype):
+    """What arrives at one token's loss is not finite (a weight, an overflow): the other tokens'
+    gradients keep their digits, small as their factors are."""
+    n, d, v, bad = 200, 64, 3000, 77
+    g = gen(8)
+    h, w = normal(g, n, d, dtype=dtype), normal(g, v, d, sigma=0.25, dtype=dtype)
+    t = torch.randint(0, v, (n,), device="cuda", generator=g)
+    lse = torch.logsumexp(h.double() @ w.double().T, 1).float()
+    row = torch.rand(n, device="cuda", generator=g) + 0.5
+    row[0], row[bad] = 2.0, 1.0         # the largest is another's
+    out = []
+    for x in (1.0, value):
+        row[bad] = x
+        dh = torch.empty_like(h)
+        z.zero_head_loss_backward(h, w, t, lse, dh, None, work_bytes(z.zero_head_workspace_bytes(n, d, v)), scale=2.0 ** -6, row_scale=row)
+        out.append(dh)
+    others = torch.arange(n, device="cuda") != bad
+    assert not torch.isfinite(out[1][bad]).any()
+    assert torch.equal(out[0][others], out[1][others])
 
 
 # ------------------------------------------------------------------------------------------

@@ -43,7 +43,7 @@ constexpr uint32_t kOutBytes = 4096;    // of an epilogue warp: 32 rows of 128 b
 constexpr uint32_t kSmem = kRingBytes + kEpilogueWarps * kOutBytes + 1024;  // and to a 1,024-byte boundary
 static_assert(kSmem <= 226 * 1024, "beside the barriers, of 227 KB");
 constexpr uint32_t kSms = 152;  // of a GB300: sizes the workspace and the splits
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kMaxFloat = 3.402823466e38f;
 
 /* Head of the workspace. */
 struct Header {
@@ -840,7 +840,7 @@ __device__ __forceinline__ void list_tokens(const TokenArgs& a, uint32_t* groups
             const uint32_t there = target[i] >= 0;
             n += there;
             earlier += from + i * 1024 < lo ? there : 0;
-            if (there)
+            if (there && fabsf(f[i]) <= kMaxFloat)  // one that is not finite says nothing of the others' size
                 top = fmaxf(top, fabsf(f[i]));
         }
     }
@@ -883,8 +883,8 @@ __device__ __forceinline__ void list_tokens(const TokenArgs& a, uint32_t* groups
         }
     }
     __syncthreads();
-    // f in units of the largest |f| (fp16: of 2^-14 of it); what is 0 or not finite stays as it is
-    const bool scaled = top > 0.0f && top <= 3.0e38f;
+    // f in units of the largest finite |f| (fp16: of 2^-14 of it); without one it stays as it is
+    const bool scaled = top > 0.0f;
     const float most_units = a.f16 ? 16384.0f : 1.0f, post = scaled ? __fdiv_rn(top, most_units) : 1.0f;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         a.head->valid = valid;
