@@ -648,7 +648,7 @@ int zero_embedding(zero_dtype_t dtype, uint64_t n_tokens, uint32_t dim, uint32_t
 size_t zero_embedding_workspace_bytes(uint64_t n_tokens, uint32_t dim, uint32_t vocab);
 
 /* Its gradient: dtable[v] (+)= scale * (sum over the places t with tokens[t] = v of dout[t]),
- * in the order of the places.  Ids outside [0, vocab) have none.  With accumulate the rows of
+ * in an order that the tokens alone give.  Ids outside [0, vocab) have none.  With accumulate the rows of
  * tokens that do not occur are not touched; without, they are written 0.
  *   dtable      grad_dtype, [vocab][dim]
  *   workspace   DEVICE, zero_embedding_workspace_bytes(...), 16-byte aligned */

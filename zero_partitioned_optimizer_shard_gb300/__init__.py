@@ -782,7 +782,8 @@ def _head(hidden, weight, targets, device: int) -> tuple:
 def zero_head_loss(hidden, weight, targets, loss, lse, workspace, stream=None) -> None:
     """The cross entropy of every token and its logits' log-sum-exp, from hidden [..., dim] and
     weight [vocab, dim] (fp16 or bf16); the logits are never kept.  Tokens whose target lies outside
-    [0, vocab) get 0.  workspace: of zero_head_workspace_bytes(rows, dim, vocab) bytes."""
+    [0, vocab) get 0.  workspace: of zero_head_workspace_bytes(rows, dim, vocab) bytes.  Should a bounded
+    wait inside give up, the losses are NaN."""
     device, fn = _current(), "zero_head_loss"
     sizes, stride, width = _head(hidden, weight, targets, device)
     n = sizes[1]

@@ -3,11 +3,11 @@
  * over the tokens in a fixed order.
  *
  * Forward: out[t] = scale * table[token[t]].
- * Backward: dtable[v] (+)= scale * (sum over the places t with token[t] = v, ascending, of
- * dout[t]).  The places are sorted by token (stable), cut into chunks of a fixed number of
- * sorted places, and each chunk's tokens are summed in fp32 by one block; a token whose
- * places lie in several chunks leaves one partial sum per chunk, which a second kernel adds
- * in the order of the chunks.  No atomics on values: the same call gives the same bits.
+ * Backward: dtable[v] (+)= scale * (sum over the places t with token[t] = v of dout[t]).  The
+ * places are sorted by token (stable), cut into chunks of a fixed number of sorted places, and each
+ * chunk's tokens are summed in fp32 by one block, in the order of the places; a token whose places
+ * lie in several chunks leaves one partial sum per chunk, which a second kernel adds in an order
+ * that the chunks alone give.  No atomics on values: the same call gives the same bits.
  * Ids outside [0, vocab) sort behind all others and are dropped.
  */
 #include "rows.cuh"
@@ -513,11 +513,12 @@ __global__ void __launch_bounds__(256) k_embedding_sum(const GradArgs a)
     }
 }
 
-/* Tokens over several chunks: their partial sums in the order of the chunks.  A block looks at
- * the last tokens of `per` chunks (at most 8); for each that starts in its chunk and goes on, 8
- * warps sum a run of the partials each, over 32 places of the row's piece.  7 us, nearly all of it
- * launch and one round trip; a token in half of a million places takes a block thousands of turns (a
- * padding id belongs outside the table, where it costs nothing). */
+/* Tokens over several chunks: their partial sums.  A block looks at the last tokens of `per` chunks
+ * (at most 8); for each that starts in its chunk and goes on, 8 warps sum every eighth of the partials
+ * each, over 32 places of the row's piece, then the 8 results are added: always in that order.  7 us,
+ * nearly all of it launch and one round trip; a token in half of a million places takes a block
+ * thousands of turns (524,288 places of 256 elements, L2 flushed: 2.1 ms where all hold one token, 1.1 where
+ * half do; a padding id belongs outside the table, where it costs nothing). */
 template <zero_dtype_t GT, bool VEC>
 __global__ void __launch_bounds__(256) k_embedding_join(const GradArgs a, const uint32_t per)
 {

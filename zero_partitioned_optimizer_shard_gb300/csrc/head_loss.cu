@@ -482,8 +482,8 @@ __device__ unsigned long long zero_test_withheld_head_stage = ~0ull;
  * A launch has about 8 us of its own: start, first copies, last epilogue.
  *
  * The matrix unit cuts its fp32 sums off instead of rounding them, always toward 0: 256 steps
- * for a logit of 4,096 terms left the loss 1.5e-5 too small.  The logits are therefore taken
- * in parts of 1,024 terms, added up in registers (measured: 4e-6 there, at no cost in time), by
+ * for a logit of 4,096 terms left the losses 1.5e-5 too small on the average.  The logits are
+ * therefore taken in parts of 1,024 terms, added up in registers (4e-6 there, at no cost in time), by
  * the losses and by D alike: D's logit and the one in lse have the same bits.  (D from logits in one
  * part: of a target with all but 1e-4 of the softmax, over 4,096 terms of one sign, it was off by 80%.)
  * The gradients' sums take operands of 16 bits, whose roundings pass what is cut off (2^-23 of the

@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(MAXT, 1) k_layernorm_backward_staged(const Bac
 /* Rows of at most 256 elements: n = 4 to 32 lanes to a row as in the forward pass, R rows of each
  * group in flight; at the end the groups' sums of a column are joined, those of a warp over its
  * lanes, then the warps' in order.  204,800 rows of 64 bf16: 26 us with the join (11.6 for the
- * bytes), 142 with a block to two rows; 20,909 rows of 135: 29 us instead of 64. */
+ * bytes), 142 with a block to two rows; 20,909 rows of 135: 25 us instead of 64. */
 template <zero_dtype_t DT, zero_dtype_t PT, int R, bool VEC>
 __global__ void __launch_bounds__(32 * kShortWarps) k_layernorm_backward_short(const BackwardArgs a, const uint32_t n)
 {
@@ -789,7 +789,10 @@ __global__ void __launch_bounds__(1024) k_layernorm_join(const JoinArgs a)
 template <auto KERNEL>
 cudaError_t forward_staged(const ForwardArgs& a, size_t params, size_t row_bytes, bool& taken, cudaStream_t s)
 {
-    // three blocks to an SM
+    // three blocks to an SM; two stages of the longest fp32 rows leave room for two of them (from 1,280
+    // elements up) or one (from 1,600), still not slower than a row to a warp straight from global memory:
+    // 8,192 rows of fp32, L2 flushed, 1,024 elements 20.1 us (20.9 without rings), 1,280 22.9 (25.0),
+    // 1,600 27.1 (28.9), 2,048 32.4 (32.6); of 640 16.8 (15.9), where the rings cost 6%
     size_t stages = (72 * 1024 - params) / (kRingWarps * row_bytes);
     stages = stages < 2 ? 2 : stages > kRing ? kRing : stages;
     const size_t smem = params + kRingWarps * stages * row_bytes;
